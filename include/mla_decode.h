@@ -27,8 +27,9 @@
  * kernel parameters.  Every call is asynchronous on `stream` and never
  * synchronises the host, except mla_device_status().
  *
- * CUDA graphs: mla_decode_metadata, mla_decode, mla_kv_insert and
- * mla_query_absorb can be captured into a CUDA graph on `stream` once the
+ * CUDA graphs: mla_decode_metadata, mla_decode, mla_kv_insert,
+ * mla_kv_insert_rope, mla_query_absorb, mla_kv_expand, mla_prefill and
+ * mla_value_project can be captured into a CUDA graph on `stream` once the
  * calling thread has made the same kind of call outside capture (the first
  * call does one-time host set-up).  A replay uses the buffers seen at
  * capture and reads their contents at replay time; the split-KV schedule is
@@ -69,6 +70,7 @@ extern "C" {
 #define MLA_STATUS_BAD_TOPK 2u      /* top-k index >= s_k or < -1               */
 #define MLA_STATUS_BAD_SEQLEN 4u    /* negative s_k, or more pages than max_pages */
 #define MLA_STATUS_WAIT_TIMEOUT 8u  /* a bounded device wait gave up            */
+#define MLA_STATUS_BAD_POSITION 32u /* position outside [0, max_pos), not -1    */
 #define MLA_STATUS_SMEM_ALIGN 16u   /* dynamic shared memory not 1024-byte aligned:
                                        the decode kernel did nothing */
 
@@ -329,6 +331,123 @@ size_t mla_query_absorb_workspace_bytes(int N, int H);
 int mla_query_absorb(const void *q_a, int ld_qa, const void *w_qa, float eps, const void *w_qb,
                      const void *w_uk, int N, int H, void *q, void *workspace, size_t workspace_bytes,
                      mla_stream_t stream);
+
+/*
+ * KV insert with rotation: mla_kv_insert for keys that have not been rotated
+ * yet, and the rotation of the same tokens' query rows, in one launch.  For
+ * token j at position pos = positions[j], with c_i = cos_sin[pos][i] and
+ * s_i = cos_sin[pos][32 + i], the 32 pairs (a, b) = (x[2i], x[2i + 1])
+ * (interleaved = 1) or (x[i], x[i + 32]) (interleaved = 0) of a row of 64
+ * become
+ *   a' = bf16(fp32(fp32(a c_i) - fp32(b s_i)))
+ *   b' = bf16(fp32(fp32(a s_i) + fp32(b c_i)))
+ * The cache row is the one mla_kv_insert writes, bit for bit, for the rotated
+ * key; q_out[j][h] is the rotated q_pe[j][h] for every head h < H.
+ *
+ *   slots      as in mla_kv_insert; -1 = no cache row (the queries of the
+ *              token are still rotated)
+ *   positions  device int64 [N]; -1 = a token that is skipped (no cache row,
+ *              its q_out left as it was).  Any other position outside
+ *              [0, max_pos) is skipped too and sets MLA_STATUS_BAD_POSITION.
+ *   cos_sin    device fp32 [max_pos][64], 16-byte aligned
+ *   q_pe       device bf16 rows of 64 values: row (j, h) at q_pe + j * q_tok +
+ *              h * q_head (elements, multiples of 8, at least 64; 16-byte
+ *              aligned), e.g. the last 64 columns of [N][H][576] or
+ *              [N][H][192] queries; NULL (with q_out NULL): keys alone
+ *   q_out      as q_pe with strides o_tok, o_head: q_pe itself (in place, the
+ *              same strides) or memory that does not overlap it.  Distinct
+ *              rows must not overlap.
+ * The other arguments, the errors and the streams are mla_kv_insert's.
+ */
+int mla_kv_insert_rope(const void *kv_c, int ld_kv, const void *k_pe, int ld_pe, const void *w_kva, float eps,
+                       const int64_t *slots, const int64_t *positions, const float *cos_sin, int max_pos,
+                       int interleaved, int N, void *kv_cache, int kv_format, int num_pages, int page_size,
+                       float *kv_scales, const float *k_scale_inv, const void *q_pe, int64_t q_tok, int64_t q_head,
+                       void *q_out, int64_t o_tok, int64_t o_head, int H, mla_stream_t stream);
+
+/*
+ * KV expansion: cached latent rows to per-head keys and values, the input of
+ * mla_prefill.  The tokens of B sequences are packed one after the other:
+ * output row r with cu_seqlens[b] <= r < cu_seqlens[b + 1] is token
+ * pos = r - cu_seqlens[b] of sequence b, cached at page block_table[b][pos / 64],
+ * slot pos % 64.  With c its 512 latent values,
+ *   kv[r][h][i]       = bf16(sum_l w_uk[h][i][l] c_l)     i < 128  (no-PE key)
+ *   kv[r][h][128 + i] = bf16(sum_l w_uv[h][i][l] c_l)     i < 128  (value)
+ *   k_pe[r]           = its 64 rotated key values, bf16
+ * Sums are fp32.  c_l is the row's bf16 value (MLA_KV_BF16),
+ * bf16(e4m3 * scale) (MLA_KV_FP8_E4M3), or e4m3 with the one scale applied to
+ * the sum (MLA_KV_FP8_E4M3_TENSOR; k_pe is bf16(e4m3 * scale)).
+ *
+ *   kv_cache, kv_format, num_pages, page_size, kv_scales   as in mla_decode
+ *   block_table  device int32 [B][max_pages]
+ *   cu_seqlens   device int32 [B + 1], 0 <= cu_seqlens[b] <= cu_seqlens[b + 1]
+ *                <= total
+ *   total        rows of kv and k_pe; rows of no sequence are left as they were
+ *   w_uk, w_uv   device bf16: row i of head h at w + h * *_head + i * *_row
+ *                (elements, multiples of 8, at least 512; 16-byte aligned):
+ *                two [H][128][512] tensors, or the halves of one [H][256][512]
+ *   kv           device bf16 [total][H][256], k_pe device bf16 [total][64],
+ *                written (16-byte aligned)
+ * A page outside the pool sets MLA_STATUS_BAD_PAGE, a sequence longer than
+ * 64 * max_pages or a bad cu_seqlens MLA_STATUS_BAD_SEQLEN; rows that cannot
+ * be read are written as zeros.  A wait that gives up sets
+ * MLA_STATUS_WAIT_TIMEOUT.  Asynchronous on `stream`; can be captured in a
+ * CUDA graph as the other calls can.  Returns MLA_OK or a negative code.
+ */
+int mla_kv_expand(const void *kv_cache, int kv_format, int num_pages, int page_size, const int32_t *block_table,
+                  int max_pages, const int32_t *cu_seqlens, int B, int total, const float *kv_scales,
+                  const void *w_uk, int64_t uk_row, int64_t uk_head, const void *w_uv, int64_t uv_row,
+                  int64_t uv_head, int H, void *kv, void *k_pe, mla_stream_t stream);
+
+/*
+ * Prefill attention: the queries of B sequences (whole prompts, or chunks of
+ * new tokens behind a cached context) over their expanded keys and values.
+ * With query row i of n_q and keys j < n_k of a sequence,
+ *   s_j = softmax_scale * (q[i][h][0:128] . k_nope[j][h] + q[i][h][128:192] . k_pe[j])
+ *   lse[h][i] = ln sum_j exp(s_j),  out[i][h] = sum_j exp(s_j - lse) v[j][h]
+ * over all n_k keys (causal = 0) or j < n_k - n_q + i + 1 (causal = 1: the
+ * last query sees every key).  A row that sees no key gets out = 0 and
+ * lse = -inf.  Keys and values that a row does not see do not reach it,
+ * whatever they hold (inf and nan too).
+ *
+ *   q            device bf16 rows of 192: (i, h) at q + i * q_tok + h * q_head
+ *   k_nope, v    device bf16 rows of 128, likewise (e.g. the halves of
+ *                mla_kv_expand's kv: tok stride H * 256, head stride 256)
+ *   k_pe         device bf16 rows of 64 at k_pe + j * pe_tok, shared by the heads
+ *                (strides in elements, multiples of 8 and at least a row's
+ *                width; pointers 16-byte aligned)
+ *   cu_seqlens_q, cu_seqlens_k   device int32 [B + 1]: a sequence's rows among
+ *                the Nq packed query rows and the Nk packed key rows.  Values
+ *                outside these or out of order are clamped and set
+ *                MLA_STATUS_BAD_SEQLEN.
+ *   out          device bf16 [Nq][H][128], lse device fp32 [H][Nq], written;
+ *                rows of no sequence are left as they were
+ * Probabilities are rounded to bf16 before they multiply v; scores, sums and
+ * outputs are accumulated in fp32.  A wait that gives up sets
+ * MLA_STATUS_WAIT_TIMEOUT.  Asynchronous on `stream`; can be captured in a
+ * CUDA graph.  Returns MLA_OK or a negative code.
+ */
+int mla_prefill(const void *q, int64_t q_tok, int64_t q_head, const void *k_nope, int64_t k_tok, int64_t k_head,
+                const void *k_pe, int64_t pe_tok, const void *v, int64_t v_tok, int64_t v_head,
+                const int32_t *cu_seqlens_q, const int32_t *cu_seqlens_k, int B, int H, int Nq, int Nk,
+                float softmax_scale, int causal, void *out, float *lse, mla_stream_t stream);
+
+/*
+ * Value projection: the decode's latent output rows to the 128 values a head
+ * hands to the output projection,
+ *   out[n][h][i] = bf16(sum_{l<512} attn[n][h][l] * w_uv[h][i][l])     i < 128
+ * (fp32 sums).
+ *
+ *   attn   device bf16 rows of 512: (n, h) at attn + n * ld_token + h * ld_head
+ *          (mla_decode's out: H * 512 and 512)
+ *   w_uv   device bf16: row i of head h at w_uv + h * w_head + i * w_row
+ *          (strides in elements, multiples of 8, at least 512; 16-byte aligned)
+ *   out    device bf16 [N][H][128], written (16-byte aligned)
+ * Asynchronous on `stream`; can be captured in a CUDA graph.  A wait that
+ * gives up sets MLA_STATUS_WAIT_TIMEOUT.  Returns MLA_OK or a negative code.
+ */
+int mla_value_project(const void *attn, int64_t ld_token, int64_t ld_head, const void *w_uv, int64_t w_row,
+                      int64_t w_head, int N, int H, void *out, mla_stream_t stream);
 
 /* Text of the calling thread's last error ("" if none). */
 const char *mla_last_error_string(void);

@@ -14,6 +14,10 @@ every call raises.
                           tile_md=tile_md, num_splits=num_splits)
     mla.kv_insert(kv_c, k_pe, w_kva, slots, kv_cache, eps=1e-6,
                   kv_scales=kv_scales)   # the cache producer
+
+A decode step from the projections' output: query_absorb, kv_insert_rope
+(rotates the queries in place and appends the rotated keys), metadata, decode,
+value_project.  A prompt or a chunk of one: kv_insert_rope, kv_expand, prefill.
 """
 from __future__ import annotations
 
@@ -39,6 +43,7 @@ STATUS_BAD_TOPK = 2
 STATUS_BAD_SEQLEN = 4
 STATUS_WAIT_TIMEOUT = 8
 STATUS_SMEM_ALIGN = 16
+STATUS_BAD_POSITION = 32
 
 _lock = threading.Lock()
 _lib = None
@@ -72,6 +77,13 @@ def lib():
             L.mla_decode_noalloc.argtypes = [P, P, i, i, i, P, i, P, P, i, P, ctypes.c_float, i,
                                              P, P, i, i, i, P]
             L.mla_kv_insert.argtypes = [P, i, P, i, P, ctypes.c_float, P, i, P, i, i, i, P, P, P]
+            i64 = ctypes.c_int64
+            L.mla_kv_insert_rope.argtypes = [P, i, P, i, P, ctypes.c_float, P, P, P, i, i, i, P, i, i, i, P, P,
+                                             P, i64, i64, P, i64, i64, i, P]
+            L.mla_kv_expand.argtypes = [P, i, i, i, P, i, P, i, i, P, P, i64, i64, P, i64, i64, i, P, P, P]
+            L.mla_prefill.argtypes = [P, i64, i64, P, i64, i64, P, i64, P, i64, i64, P, P, i, i, i, i,
+                                      ctypes.c_float, i, P, P, P]
+            L.mla_value_project.argtypes = [P, i64, i64, P, i64, i64, i, i, P, P]
             L.mla_query_absorb_workspace_bytes.argtypes = [i, i]
             L.mla_query_absorb_workspace_bytes.restype = sz
             L.mla_query_absorb.argtypes = [P, i, P, ctypes.c_float, P, P, i, i, P, P, sz, P]
@@ -311,18 +323,9 @@ def _rows_view(t: torch.Tensor, name: str, width: int):
     return t, t.stride(0) if t.shape[0] > 1 else max(t.shape[1], width)
 
 
-def kv_insert(kv_c: torch.Tensor, k_pe: torch.Tensor, w_kva: torch.Tensor, slots: torch.Tensor,
-              kv_cache: torch.Tensor, *, eps: float, kv_scales: Optional[torch.Tensor] = None,
-              k_scale_inv: Optional[torch.Tensor] = None, fp8_per_tensor: bool = False):
-    """RMSNorm the new tokens' latent rows and write them, with k_pe, into
-    their cache slots, on the current stream (mla_kv_insert).
-
-    kv_c bf16 [N, >=512] (columns 0..511 are read; rows may be a strided
-    column slice); k_pe bf16 [N, >=64]; w_kva bf16 [512]; slots int64 [N]
-    (-1 = skip).  kv_cache: bf16 [P, page, 576] (bf16 rows), uint8
-    [P, page, 640] with kv_scales fp32 [P, page, 4] (the decode's FP8 rows),
-    or uint8 [P, page, 576] with fp8_per_tensor=True and k_scale_inv fp32 [1].
-    Returns kv_cache."""
+def _insert_args(kv_c, k_pe, w_kva, slots, kv_cache, kv_scales, k_scale_inv, fp8_per_tensor):
+    """Checks of the inserts' common arguments -> (kv_c, its row stride, k_pe,
+    its row stride, device, N, cache format)."""
     kv_c, ld_kv = _rows_view(kv_c, "kv_c", D_V)
     k_pe, ld_pe = _rows_view(k_pe, "k_pe", 64)
     dev = kv_c.device
@@ -348,6 +351,23 @@ def kv_insert(kv_c: torch.Tensor, k_pe: torch.Tensor, w_kva: torch.Tensor, slots
             raise ValueError("kv_scales must be [P, page, 4]")
     if fmt == KV_FP8_E4M3_TENSOR:
         _need(k_scale_inv, "k_scale_inv", torch.float32, dev)
+    return kv_c, ld_kv, k_pe, ld_pe, dev, N, fmt
+
+
+def kv_insert(kv_c: torch.Tensor, k_pe: torch.Tensor, w_kva: torch.Tensor, slots: torch.Tensor,
+              kv_cache: torch.Tensor, *, eps: float, kv_scales: Optional[torch.Tensor] = None,
+              k_scale_inv: Optional[torch.Tensor] = None, fp8_per_tensor: bool = False):
+    """RMSNorm the new tokens' latent rows and write them, with k_pe, into
+    their cache slots, on the current stream (mla_kv_insert).
+
+    kv_c bf16 [N, >=512] (columns 0..511 are read; rows may be a strided
+    column slice); k_pe bf16 [N, >=64]; w_kva bf16 [512]; slots int64 [N]
+    (-1 = skip).  kv_cache: bf16 [P, page, 576] (bf16 rows), uint8
+    [P, page, 640] with kv_scales fp32 [P, page, 4] (the decode's FP8 rows),
+    or uint8 [P, page, 576] with fp8_per_tensor=True and k_scale_inv fp32 [1].
+    Returns kv_cache."""
+    kv_c, ld_kv, k_pe, ld_pe, dev, N, fmt = _insert_args(kv_c, k_pe, w_kva, slots, kv_cache, kv_scales, k_scale_inv,
+                                                         fp8_per_tensor)
     with torch.cuda.device(dev):
         _check(lib().mla_kv_insert(
             _ptr(kv_c), ld_kv, _ptr(k_pe), ld_pe, _ptr(w_kva), float(eps), _ptr(slots), N,
@@ -355,6 +375,218 @@ def kv_insert(kv_c: torch.Tensor, k_pe: torch.Tensor, w_kva: torch.Tensor, slots
             _ptr(kv_scales) if fmt == KV_FP8_E4M3 else None,
             _ptr(k_scale_inv) if fmt == KV_FP8_E4M3_TENSOR else None, _stream(dev)))
     return kv_cache
+
+
+def _strided(t, name, shape, dev, dtype=torch.bfloat16):
+    """A bf16 CUDA tensor of this shape (None: any size) whose last axis is
+    contiguous and whose other strides are multiples of 8 elements."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != len(shape) or any(n is not None and m != n for m, n in zip(t.shape, shape)):
+        raise ValueError(f"{name} must be {['*' if n is None else n for n in shape]}, got {list(t.shape)}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on a CUDA device")
+    if dev is not None and t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    if t.numel() and (t.stride(-1) != 1 or any(t.stride(k) % 8 for k in range(t.dim() - 1) if t.shape[k] > 1)):
+        raise ValueError(f"{name} must have unit stride in its last axis and strides that are multiples of 8")
+
+
+def _ld(t, k):
+    """Stride of axis k as the C ABI wants it: that of an axis of one entry is
+    never used, and torch may give it any value."""
+    return t.stride(k) if t.shape[k] > 1 else t.shape[-1]
+
+
+def kv_insert_rope(kv_c: torch.Tensor, k_pe: torch.Tensor, w_kva: torch.Tensor, slots: torch.Tensor,
+                   kv_cache: torch.Tensor, *, eps: float, positions: torch.Tensor, cos_sin: torch.Tensor,
+                   interleaved: bool = True, q_pe: Optional[torch.Tensor] = None,
+                   q_out: Optional[torch.Tensor] = None, kv_scales: Optional[torch.Tensor] = None,
+                   k_scale_inv: Optional[torch.Tensor] = None, fp8_per_tensor: bool = False):
+    """kv_insert() for keys that are not rotated yet, and the rotation of the
+    same tokens' queries, in one launch (mla_kv_insert_rope) -> (kv_cache,
+    rotated queries or None).
+
+    positions int64 [N] (-1 = a token that is skipped); cos_sin fp32
+    [max_pos, 64], 32 cosines then 32 sines a position; interleaved: pairs
+    (2i, 2i+1), else (i, i+32).  q_pe bf16 [N, H, 64], rows may be strided
+    (q[..., -64:] of [N, H, 576] or [N, H, 192] queries); q_out as q_pe, default
+    q_pe itself: the queries are rotated in place.  It must be q_pe or not
+    overlap it.  The other arguments are kv_insert()'s."""
+    kv_c, ld_kv, k_pe, ld_pe, dev, N, fmt = _insert_args(kv_c, k_pe, w_kva, slots, kv_cache, kv_scales, k_scale_inv,
+                                                         fp8_per_tensor)
+    _need(positions, "positions", torch.int64, dev, 1)
+    _need(cos_sin, "cos_sin", torch.float32, dev, 2)
+    if positions.shape[0] != N or cos_sin.shape[1] != 64 or cos_sin.shape[0] < 1:
+        raise ValueError("positions must be [N], cos_sin [max_pos, 64]")
+    H, strides = 0, (0, 0, 0, 0)
+    if q_pe is None and q_out is not None:
+        raise ValueError("q_out needs q_pe")
+    if q_pe is not None:
+        _strided(q_pe, "q_pe", (N, None, 64), dev)
+        H = q_pe.shape[1]
+        if q_out is None:
+            q_out = q_pe
+        else:
+            _strided(q_out, "q_out", (N, H, 64), dev)
+        check_rows_apart(q_out.shape, q_out.stride(), "q_out")
+        strides = (_ld(q_pe, 0), _ld(q_pe, 1), _ld(q_out, 0), _ld(q_out, 1))
+        if q_out.data_ptr() == q_pe.data_ptr() and N and strides[:2] != strides[2:]:
+            raise ValueError("q_out in q_pe's place must have its strides")
+    with torch.cuda.device(dev):
+        _check(lib().mla_kv_insert_rope(
+            _ptr(kv_c), ld_kv, _ptr(k_pe), ld_pe, _ptr(w_kva), float(eps), _ptr(slots), _ptr(positions),
+            _ptr(cos_sin), cos_sin.shape[0], int(bool(interleaved)), N,
+            _ptr(kv_cache), fmt, kv_cache.shape[0], kv_cache.shape[1],
+            _ptr(kv_scales) if fmt == KV_FP8_E4M3 else None,
+            _ptr(k_scale_inv) if fmt == KV_FP8_E4M3_TENSOR else None,
+            _ptr(q_pe), strides[0], strides[1], _ptr(q_out), strides[2], strides[3], H, _stream(dev)))
+    return kv_cache, q_out
+
+
+def check_rows_apart(shape, stride, name: str) -> None:
+    """Raises ValueError where two rows of a written [N, H, W] tensor overlap
+    (an expanded tensor, or strides below a row's width)."""
+    n, h, w = shape
+    axes = sorted((s, k) for s, k in ((stride[0], n), (stride[1], h)) if k > 1)
+    span = w
+    for s, k in axes:
+        if s < span:
+            raise ValueError(f"{name}: rows overlap")
+        span = s * (k - 1) + span
+
+
+def kv_expand(kv_cache: torch.Tensor, block_table: torch.Tensor, cu_seqlens: torch.Tensor, w_uk: torch.Tensor,
+              w_uv: torch.Tensor, *, total: Optional[int] = None, kv_scales: Optional[torch.Tensor] = None,
+              kv: Optional[torch.Tensor] = None, k_pe: Optional[torch.Tensor] = None):
+    """Cached latent rows -> per-head keys and values for prefill(), on the
+    current stream (mla_kv_expand) -> (kv bf16 [total, H, 256], k_pe bf16
+    [total, 64]); kv[..., :128] are the no-PE keys, kv[..., 128:] the values.
+
+    kv_cache and kv_scales as in decode(); block_table int32 [B, max_pages];
+    cu_seqlens int32 [B+1]: sequence b's tokens 0.. become rows
+    cu_seqlens[b]..cu_seqlens[b+1]-1; w_uk, w_uv bf16 [H, 128, 512] (views of one
+    [H, 256, 512] tensor will do).  total: rows of the outputs, at least
+    cu_seqlens[B] (a host number: this call does not wait for the device);
+    taken from kv or k_pe where one is given.  Rows of no sequence are left as
+    they were."""
+    if not isinstance(kv_cache, torch.Tensor):
+        raise TypeError("kv_cache must be a torch.Tensor")
+    fmt = _cache_format(kv_cache, kv_scales)
+    dev = kv_cache.device
+    _need(kv_cache, "kv_cache", kv_cache.dtype, dev, 3)
+    _need(block_table, "block_table", torch.int32, dev, 2)
+    _need(cu_seqlens, "cu_seqlens", torch.int32, dev, 1)
+    B = block_table.shape[0]
+    if cu_seqlens.shape[0] != B + 1:
+        raise ValueError("cu_seqlens must be [B + 1] for a block_table of B rows")
+    _strided(w_uk, "w_uk", (None, 128, D_V), dev)
+    H = w_uk.shape[0]
+    _strided(w_uv, "w_uv", (H, 128, D_V), dev)
+    if fmt == KV_FP8_E4M3 and tuple(kv_scales.shape) != (kv_cache.shape[0], kv_cache.shape[1], 4):
+        raise ValueError("kv_scales must be [P, 64, 4]")
+    if total is None:
+        if kv is None and k_pe is None:
+            raise ValueError("total (the outputs' rows) is needed where no output is given")
+        total = (kv if kv is not None else k_pe).shape[0]
+    total = int(total)
+    if kv is None:
+        kv = torch.empty((total, H, 256), dtype=torch.bfloat16, device=dev)
+    if k_pe is None:
+        k_pe = torch.empty((total, 64), dtype=torch.bfloat16, device=dev)
+    _need(kv, "kv", torch.bfloat16, dev, 3)
+    _need(k_pe, "k_pe", torch.bfloat16, dev, 2)
+    if tuple(kv.shape) != (total, H, 256) or tuple(k_pe.shape) != (total, 64):
+        raise ValueError(f"kv must be [{total}, {H}, 256], k_pe [{total}, 64]")
+    with torch.cuda.device(dev):
+        _check(lib().mla_kv_expand(
+            _ptr(kv_cache), fmt, kv_cache.shape[0], kv_cache.shape[1], _ptr(block_table), block_table.shape[1],
+            _ptr(cu_seqlens), B, total, _ptr(kv_scales) if fmt != KV_BF16 else None,
+            _ptr(w_uk), w_uk.stride(1), _ld(w_uk, 0), _ptr(w_uv), w_uv.stride(1), _ld(w_uv, 0), H,
+            _ptr(kv), _ptr(k_pe), _stream(dev)))
+    return kv, k_pe
+
+
+def _cache_format(kv_cache, kv_scales) -> int:
+    """The format of a cache by its type and row width."""
+    if kv_cache.dtype == torch.bfloat16:
+        if kv_cache.dim() != 3 or kv_cache.shape[2] != D_QK:
+            raise ValueError("bf16 kv_cache must be [P, 64, 576]")
+        return KV_BF16
+    if kv_cache.dtype != torch.uint8:
+        raise TypeError("kv_cache must be bfloat16 or uint8 (fp8 rows)")
+    if kv_cache.dim() != 3 or kv_cache.shape[2] not in (FP8_ROW_BYTES, D_QK):
+        raise ValueError("fp8 kv_cache must be uint8 [P, 64, 640] (per-128 scales) or [P, 64, 576] (per-tensor)")
+    if kv_cache.shape[2] == FP8_ROW_BYTES:
+        _need(kv_scales, "kv_scales", torch.float32, kv_cache.device, 3)
+        return KV_FP8_E4M3
+    _need(kv_scales, "kv_scales", torch.float32, kv_cache.device)
+    if kv_scales.numel() != 1:
+        raise ValueError("a per-tensor fp8 cache takes kv_scales with one fp32 scale")
+    return KV_FP8_E4M3_TENSOR
+
+
+def prefill(q: torch.Tensor, k_nope: torch.Tensor, k_pe: torch.Tensor, v: torch.Tensor, cu_seqlens_q: torch.Tensor,
+            cu_seqlens_k: torch.Tensor, *, softmax_scale: float, causal: bool = True,
+            out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None):
+    """Attention of prompts, or of chunks of new tokens, over expanded keys and
+    values, on the current stream (mla_prefill) -> (out bf16 [Nq, H, 128], lse
+    fp32 [H, Nq]).
+
+    q bf16 [Nq, H, 192] (128 no-PE, then 64 rotated values); k_nope, v bf16
+    [Nk, H, 128] and k_pe bf16 [Nk, 64] (as kv_expand() gives them; rows may be
+    strided); cu_seqlens_q, cu_seqlens_k int32 [B+1]: the rows of each sequence.
+    causal: the last query of a sequence sees all its keys, each one before it
+    one less.  A row that sees no key gets 0 and -inf.  Rows of no sequence
+    are left as they were."""
+    _strided(q, "q", (None, None, 192), None)
+    dev, (Nq, H) = q.device, q.shape[:2]
+    _strided(k_nope, "k_nope", (None, H, 128), dev)
+    Nk = k_nope.shape[0]
+    _strided(k_pe, "k_pe", (Nk, 64), dev)
+    _strided(v, "v", (Nk, H, 128), dev)
+    _need(cu_seqlens_q, "cu_seqlens_q", torch.int32, dev, 1)
+    _need(cu_seqlens_k, "cu_seqlens_k", torch.int32, dev, 1)
+    B = cu_seqlens_q.shape[0] - 1
+    if B < 0 or cu_seqlens_k.shape[0] != B + 1:
+        raise ValueError("cu_seqlens_q and cu_seqlens_k must be [B + 1]")
+    if out is None:
+        out = torch.empty((Nq, H, 128), dtype=torch.bfloat16, device=dev)
+    if lse is None:
+        lse = torch.empty((H, Nq), dtype=torch.float32, device=dev)
+    _need(out, "out", torch.bfloat16, dev, 3)
+    _need(lse, "lse", torch.float32, dev, 2)
+    if tuple(out.shape) != (Nq, H, 128) or tuple(lse.shape) != (H, Nq):
+        raise ValueError(f"out must be [{Nq}, {H}, 128], lse [{H}, {Nq}]")
+    with torch.cuda.device(dev):
+        _check(lib().mla_prefill(
+            _ptr(q), _ld(q, 0), _ld(q, 1), _ptr(k_nope), _ld(k_nope, 0), _ld(k_nope, 1), _ptr(k_pe), _ld(k_pe, 0),
+            _ptr(v), _ld(v, 0), _ld(v, 1), _ptr(cu_seqlens_q), _ptr(cu_seqlens_k), B, H, Nq, Nk,
+            float(softmax_scale), int(bool(causal)), _ptr(out), _ptr(lse), _stream(dev)))
+    return out, lse
+
+
+def value_project(attn: torch.Tensor, w_uv: torch.Tensor, *, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The decode's output rows through each head's W_UV, on the current
+    stream (mla_value_project) -> bf16 [N, H, 128].
+
+    attn bf16 [N, H, 512] (decode()'s out with B and T flattened; rows may be
+    strided); w_uv bf16 [H, 128, 512] (a view of a [H, 256, 512] tensor will
+    do)."""
+    _strided(attn, "attn", (None, None, D_V), None)
+    dev, (N, H) = attn.device, attn.shape[:2]
+    _strided(w_uv, "w_uv", (H, 128, D_V), dev)
+    if out is None:
+        out = torch.empty((N, H, 128), dtype=torch.bfloat16, device=dev)
+    _need(out, "out", torch.bfloat16, dev, 3)
+    if tuple(out.shape) != (N, H, 128):
+        raise ValueError(f"out must be [{N}, {H}, 128], got {list(out.shape)}")
+    with torch.cuda.device(dev):
+        _check(lib().mla_value_project(_ptr(attn), _ld(attn, 0), _ld(attn, 1), _ptr(w_uv), w_uv.stride(1),
+                                       _ld(w_uv, 0), N, H, _ptr(out), _stream(dev)))
+    return out
 
 
 D_QA = 1536

@@ -249,9 +249,12 @@ int mla_decode(const void *q, const void *kv_cache, int kv_format,
   return ok();
 }
 
-int mla_kv_insert(const void *kv_c, int ld_kv, const void *k_pe, int ld_pe, const void *w_kva, float eps,
+namespace {
+// The checks and parameters that both inserts share.  N == 0: nothing to do
+// (p.N stays 0).
+int insert_params(const void *kv_c, int ld_kv, const void *k_pe, int ld_pe, const void *w_kva, float eps,
                   const int64_t *slots, int N, void *kv_cache, int kv_format, int num_pages, int page_size,
-                  float *kv_scales, const float *k_scale_inv, mla_stream_t stream) {
+                  float *kv_scales, const float *k_scale_inv, mla::KvInsertParams &p) {
   if (N < 0) return fail(MLA_ERR_INVALID_ARG, "N = %d must be >= 0", N);
   if (kv_format != MLA_KV_BF16 && kv_format != MLA_KV_FP8_E4M3 && kv_format != MLA_KV_FP8_E4M3_TENSOR)
     return fail(MLA_ERR_INVALID_ARG, "kv_format %d unknown", kv_format);
@@ -261,7 +264,7 @@ int mla_kv_insert(const void *kv_c, int ld_kv, const void *k_pe, int ld_pe, cons
   if (ld_pe < mla::D_ROPE || ld_pe % 8)
     return fail(MLA_ERR_INVALID_ARG, "ld_pe = %d: need >= 64, multiple of 8", ld_pe);
   if (!(eps >= 0.f) || !std::isfinite(eps)) return fail(MLA_ERR_INVALID_ARG, "eps must be finite and >= 0");
-  if (N == 0) return ok();
+  if (N == 0) return MLA_OK;
   if (!kv_c || !k_pe || !w_kva || !slots || !kv_cache) return fail(MLA_ERR_INVALID_ARG, "null pointer");
   if (!aligned(kv_c, 16) || !aligned(k_pe, 16) || !aligned(w_kva, 16) || !aligned(kv_cache, 16) ||
       !aligned(slots, 8))
@@ -273,7 +276,6 @@ int mla_kv_insert(const void *kv_c, int ld_kv, const void *k_pe, int ld_pe, cons
   unsigned int *st = nullptr;
   int rc;
   if ((rc = status_ptr(&st)) != MLA_OK) return rc;
-  mla::KvInsertParams p{};
   p.kv_c = static_cast<const __nv_bfloat16 *>(kv_c);
   p.k_pe = static_cast<const __nv_bfloat16 *>(k_pe);
   p.w_kva = static_cast<const __nv_bfloat16 *>(w_kva);
@@ -288,7 +290,61 @@ int mla_kv_insert(const void *kv_c, int ld_kv, const void *k_pe, int ld_pe, cons
   p.N = N;
   p.kv_format = kv_format;
   p.eps = eps;
+  return MLA_OK;
+}
+}  // namespace
+
+int mla_kv_insert(const void *kv_c, int ld_kv, const void *k_pe, int ld_pe, const void *w_kva, float eps,
+                  const int64_t *slots, int N, void *kv_cache, int kv_format, int num_pages, int page_size,
+                  float *kv_scales, const float *k_scale_inv, mla_stream_t stream) {
+  mla::KvInsertParams p{};
+  const int rc = insert_params(kv_c, ld_kv, k_pe, ld_pe, w_kva, eps, slots, N, kv_cache, kv_format, num_pages,
+                               page_size, kv_scales, k_scale_inv, p);
+  if (rc != MLA_OK) return rc;
+  if (N == 0) return ok();
   cudaError_t e = mla::launch_kv_insert(p, (cudaStream_t)stream);
+  if (e != cudaSuccess) return fail(MLA_ERR_CUDA, "kv insert launch: %s", cudaGetErrorString(e));
+  return ok();
+}
+
+int mla_kv_insert_rope(const void *kv_c, int ld_kv, const void *k_pe, int ld_pe, const void *w_kva, float eps,
+                       const int64_t *slots, const int64_t *positions, const float *cos_sin, int max_pos,
+                       int interleaved, int N, void *kv_cache, int kv_format, int num_pages, int page_size,
+                       float *kv_scales, const float *k_scale_inv, const void *q_pe, int64_t q_tok, int64_t q_head,
+                       void *q_out, int64_t o_tok, int64_t o_head, int H, mla_stream_t stream) {
+  if (max_pos < 1) return fail(MLA_ERR_INVALID_ARG, "max_pos = %d must be >= 1", max_pos);
+  if (interleaved != 0 && interleaved != 1) return fail(MLA_ERR_INVALID_ARG, "interleaved must be 0 or 1");
+  if ((q_pe == nullptr) != (q_out == nullptr)) return fail(MLA_ERR_INVALID_ARG, "q_pe and q_out go together");
+  if (q_pe) {
+    if (H < 1 || H > MLA_MAX_HEADS) return fail(MLA_ERR_INVALID_ARG, "H = %d not in [1, %d]", H, MLA_MAX_HEADS);
+    if (q_tok % 8 || q_head % 8 || o_tok % 8 || o_head % 8)
+      return fail(MLA_ERR_INVALID_ARG, "query strides must be multiples of 8 elements");
+    if ((N > 1 && (q_tok < mla::D_ROPE || o_tok < mla::D_ROPE)) || (H > 1 && (q_head < mla::D_ROPE || o_head < mla::D_ROPE)))
+      return fail(MLA_ERR_INVALID_ARG, "query strides must be at least 64 elements");
+    if (!aligned(q_pe, 16) || !aligned(q_out, 16))
+      return fail(MLA_ERR_INVALID_ARG, "q_pe and q_out must be 16-byte aligned");
+  }
+  if (N > 0 && (!positions || !cos_sin)) return fail(MLA_ERR_INVALID_ARG, "null pointer");
+  if (!aligned(positions, 8) || !aligned(cos_sin, 16))
+    return fail(MLA_ERR_INVALID_ARG, "positions must be 8-byte aligned, cos_sin 16");
+  mla::KvInsertParams p{};
+  const int rc = insert_params(kv_c, ld_kv, k_pe, ld_pe, w_kva, eps, slots, N, kv_cache, kv_format, num_pages,
+                               page_size, kv_scales, k_scale_inv, p);
+  if (rc != MLA_OK) return rc;
+  if (N == 0) return ok();
+  mla::RopeParams r{};
+  r.positions = positions;
+  r.cos_sin = cos_sin;
+  r.q_pe = static_cast<const __nv_bfloat16 *>(q_pe);
+  r.q_out = static_cast<__nv_bfloat16 *>(q_out);
+  r.q_tok = q_tok;
+  r.q_head = q_head;
+  r.o_tok = o_tok;
+  r.o_head = o_head;
+  r.max_pos = max_pos;
+  r.interleaved = interleaved;
+  r.H = H;
+  cudaError_t e = mla::launch_kv_insert_rope(p, r, (cudaStream_t)stream);
   if (e != cudaSuccess) return fail(MLA_ERR_CUDA, "kv insert launch: %s", cudaGetErrorString(e));
   return ok();
 }

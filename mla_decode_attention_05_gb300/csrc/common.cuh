@@ -176,6 +176,20 @@ struct KvInsertParams {
   float eps;
 };
 cudaError_t launch_kv_insert(const KvInsertParams &p, cudaStream_t stream);
+
+// What mla_kv_insert_rope adds to an insert: the angle table, the tokens'
+// positions and the query rows that are rotated with the keys.
+struct RopeParams {
+  const int64_t *positions;
+  const float *cos_sin;  // [max_pos][64]: 32 cosines, 32 sines
+  const __nv_bfloat16 *q_pe;  // rows of 64 values, null without queries
+  __nv_bfloat16 *q_out;
+  long long q_tok, q_head, o_tok, o_head;  // element strides
+  int max_pos;
+  int interleaved;
+  int H;
+};
+cudaError_t launch_kv_insert_rope(const KvInsertParams &p, const RopeParams &r, cudaStream_t stream);
 void set_last_error(const char *msg);
 int status_word(unsigned int **out);
 }  // namespace mla

@@ -1,0 +1,391 @@
+// KV expansion: cached latent rows to the keys and values of every head, for
+// the attention of prompts (mla_prefill).  Packed output row r belongs to
+// sequence b with cu[b] <= r < cu[b + 1] and holds token pos = r - cu[b],
+// found at page block_table[b][pos / 64], slot pos % 64:
+//   kv[r][h][0:128]   = bf16(W_UK[h] . c)       (128 no-PE key values)
+//   kv[r][h][128:256] = bf16(W_UV[h] . c)       (128 values)
+//   k_pe[r]           = the row's 64 rotated key values
+// with c the row's 512 latent values.
+//
+// As one GEMM with gathered rows: M = 128 rows of the packed output, N = 256
+// (one head: its W_UK rows, then its W_UV rows), K = 512.  2 * 512 flops per
+// 2-byte output value are above the ridge, so with many rows it is bound by
+// the tensor cores, with the output's write close behind; with few rows by
+// the read of the weights.
+//
+// Roundings: bf16 rows are used as they are.  A row with per-128 scales is
+// dequantised to bf16 (one rounding, the one the decode makes too: the MMA's
+// operands have one type, and the four scales of a row cannot leave its sum).
+// The codes of a one-scale cache are exact in bf16, so there the scale
+// multiplies the fp32 sum.  Sums are fp32 in tensor memory, rounded once.
+#include <cuda_fp8.h>
+
+#include "common.cuh"
+#include "ptx.cuh"
+#include "tma_map.cuh"
+
+namespace mla {
+namespace {
+
+using namespace ptx;
+
+struct ExpandParams {
+  const uint8_t *cache;
+  const float *scales;
+  const int32_t *block_table;
+  const int32_t *cu;
+  __nv_bfloat16 *kv;    // [total][H][256]
+  __nv_bfloat16 *k_pe;  // [total][64]
+  unsigned int *status;
+  int format, num_pages, max_pages, B, H, total;
+  int store_v8;  // kv is 32-byte aligned
+};
+
+// Warps 0-3 gather the rows (A) and drain D, warp 4 loads the weights, warp 5
+// issues the MMAs.  A CTA walks over (row block, head) units, heads innermost,
+// so A (128 rows x 512, 128 KB) stays in shared memory for all heads of a
+// block while W_UK[h] and W_UV[h] stream through a ring; D is double buffered
+// in tensor memory, so a unit is drained while the next one is computed.
+constexpr int kThreads = 192;
+constexpr int kM = 128;
+constexpr int kKBlocks = 8;
+constexpr uint32_t kABlock = kM * 128;        // 64 latent values x 128 rows
+constexpr uint32_t kWStage = 256 * 128;       // 64 latent values x 256 weight rows
+constexpr int kWStages = 3;
+constexpr uint32_t OFF_W = kKBlocks * kABlock;
+constexpr uint32_t OFF_BARS = OFF_W + kWStages * kWStage;
+constexpr uint32_t IDESC = idesc_bf16_f32(128, 256, false, false);
+
+struct Bars {
+  uint64_t w_full[kWStages], w_empty[kWStages];
+  uint64_t a_full;
+  uint64_t d_full[2], d_empty[2];
+  uint32_t tmem_base;
+  int abort;
+};
+constexpr uint32_t kSmem = OFF_BARS + sizeof(Bars) + 1024;
+static_assert(kSmem <= 232448, "shared memory budget");
+
+__device__ __forceinline__ bool wait_ok(Bars *b, uint64_t *bar, uint32_t parity, unsigned int *status) {
+  if (mbar_wait<false>(smem_u32(bar), parity, &b->abort, kDefaultWaitNs)) return true;
+  atomicOr(status, MLA_STATUS_WAIT_TIMEOUT);
+  *(volatile int *)&b->abort = 1;
+  return false;
+}
+
+// The cache row of packed row r: its index in the pool, -1 for a row that
+// cannot be read (written as zeros) and -2 for one that belongs to no
+// sequence (left as it was).
+__device__ long long row_source(const ExpandParams &p, int r) {
+  if (r >= p.total) return -2;
+  int lo = 0, hi = p.B;  // the last b with cu[b] <= r
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (__ldg(p.cu + mid) <= r) lo = mid; else hi = mid;
+  }
+  const int start = __ldg(p.cu + lo), end = __ldg(p.cu + lo + 1);
+  if (start < 0 || end > p.total) atomicOr(p.status, MLA_STATUS_BAD_SEQLEN);
+  if (start < 0 || r < start || r >= end) return -2;
+  const int pos = r - start;
+  if (pos / PAGE >= p.max_pages) {
+    atomicOr(p.status, MLA_STATUS_BAD_SEQLEN);
+    return -1;
+  }
+  const int page = __ldg(p.block_table + (size_t)lo * p.max_pages + pos / PAGE);
+  if (page < 0 || page >= p.num_pages) {
+    atomicOr(p.status, MLA_STATUS_BAD_PAGE);
+    return -1;
+  }
+  return (long long)page * PAGE + pos % PAGE;
+}
+
+// 16 e4m3 codes times sc -> 16 bf16 (the products rounded once).
+__device__ __forceinline__ void dequant(const uint4 &v, float sc, uint32_t (&o)[8]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 8; i++) {
+    const uint16_t two = (uint16_t)(w[i >> 1] >> (16 * (i & 1)));
+    const __half2 h2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3));
+    const float2 f = __half22float2(h2);
+    __nv_bfloat162 b = __floats2bfloat162_rn(f.x * sc, f.y * sc);
+    o[i] = *reinterpret_cast<uint32_t *>(&b);
+  }
+}
+
+// Byte offset of 16-byte piece c (0..63) of row r in the swizzled A blocks.
+__device__ __forceinline__ uint32_t a_off(int r, int c) {
+  return (uint32_t)(c >> 3) * kABlock + (uint32_t)r * 128 + (uint32_t)(((c & 7) ^ (r & 7)) << 4);
+}
+
+// Warp w fetches rows 32w .. 32w + 31 of the block at row0 into A; src: the
+// lane's own row.  With `pe` it also writes the rows' k_pe.
+__device__ void gather_rows(const ExpandParams &p, uint8_t *a, int row0, int warp, int lane, long long src, bool pe) {
+  const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+  if (p.format == MLA_KV_BF16) {
+    constexpr int kBatch = 4;
+    for (int i = 0; i < 32; i += kBatch) {
+      uint4 v[kBatch][2], q[kBatch];
+#pragma unroll
+      for (int j = 0; j < kBatch; j++) {
+        const long long s = __shfl_sync(0xffffffffu, src, i + j);
+        const uint4 *row = reinterpret_cast<const uint4 *>(p.cache + (size_t)(s < 0 ? 0 : s) * (D_QK * 2));
+        v[j][0] = s < 0 ? zero : __ldg(row + lane);
+        v[j][1] = s < 0 ? zero : __ldg(row + 32 + lane);
+        q[j] = (s < 0 || !pe || lane >= 8) ? zero : __ldg(row + 64 + lane);
+      }
+#pragma unroll
+      for (int j = 0; j < kBatch; j++) {
+        const int r = warp * 32 + i + j;
+        *reinterpret_cast<uint4 *>(a + a_off(r, lane)) = v[j][0];
+        *reinterpret_cast<uint4 *>(a + a_off(r, 32 + lane)) = v[j][1];
+        const long long s = __shfl_sync(0xffffffffu, src, i + j);
+        if (pe && s != -2 && lane < 8)
+          reinterpret_cast<uint4 *>(p.k_pe + (size_t)(row0 + r) * D_ROPE)[lane] = q[j];
+      }
+    }
+    return;
+  }
+  const bool tile = p.format == MLA_KV_FP8_E4M3;
+  const int row_bytes = tile ? FP8_ROW : D_QK;
+  const float one = tile ? 0.f : __ldg(p.scales);
+  constexpr int kBatch = 4;
+  for (int i = 0; i < 32; i += kBatch) {
+    uint4 v[kBatch], q[kBatch];
+    float sc[kBatch];
+#pragma unroll
+    for (int j = 0; j < kBatch; j++) {
+      const long long s = __shfl_sync(0xffffffffu, src, i + j);
+      const uint8_t *row = p.cache + (size_t)(s < 0 ? 0 : s) * row_bytes;
+      v[j] = s < 0 ? zero : __ldg(reinterpret_cast<const uint4 *>(row) + lane);
+      sc[j] = (tile && s >= 0) ? __ldg(p.scales + s * 4 + (lane >> 3)) : 1.f;
+      // k_pe: 8 pieces of 16 bytes, or 4 pieces of 16 codes
+      q[j] = (s < 0 || !pe || lane >= (tile ? 8 : 4)) ? zero : __ldg(reinterpret_cast<const uint4 *>(row + D_V) + lane);
+    }
+#pragma unroll
+    for (int j = 0; j < kBatch; j++) {
+      const int r = warp * 32 + i + j;
+      uint32_t o[8];
+      dequant(v[j], sc[j], o);
+      *reinterpret_cast<uint4 *>(a + a_off(r, 2 * lane)) = make_uint4(o[0], o[1], o[2], o[3]);
+      *reinterpret_cast<uint4 *>(a + a_off(r, 2 * lane + 1)) = make_uint4(o[4], o[5], o[6], o[7]);
+      const long long s = __shfl_sync(0xffffffffu, src, i + j);
+      if (pe && s != -2) {
+        uint4 *dst = reinterpret_cast<uint4 *>(p.k_pe + (size_t)(row0 + r) * D_ROPE);
+        if (tile) {
+          if (lane < 8) dst[lane] = q[j];
+        } else if (lane < 4) {
+          dequant(q[j], one, o);
+          dst[2 * lane] = make_uint4(o[0], o[1], o[2], o[3]);
+          dst[2 * lane + 1] = make_uint4(o[4], o[5], o[6], o[7]);
+        }
+      }
+    }
+  }
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+    expand_kernel(const __grid_constant__ CUtensorMap uk_map, const __grid_constant__ CUtensorMap uv_map,
+                  ExpandParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *base = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  Bars *br = reinterpret_cast<Bars *>(base + OFF_BARS);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const long long units = (long long)ceil_div(p.total, kM) * p.H;
+  const int u0 = (int)(units * blockIdx.x / gridDim.x), u1 = (int)(units * (blockIdx.x + 1) / gridDim.x);
+  if (warp == 0) {
+    tmem_alloc(smem_u32(&br->tmem_base), 512);
+    tmem_relinquish();
+  }
+  if (threadIdx.x == 32) {
+    for (int s = 0; s < kWStages; s++) {
+      mbar_init(smem_u32(&br->w_full[s]), 1);
+      mbar_init(smem_u32(&br->w_empty[s]), 1);
+    }
+    mbar_init(smem_u32(&br->a_full), 4);
+    for (int s = 0; s < 2; s++) {
+      mbar_init(smem_u32(&br->d_full[s]), 1);
+      mbar_init(smem_u32(&br->d_empty[s]), 4);
+    }
+    br->abort = 0;
+    fence_mbar_init_cluster();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = br->tmem_base;
+  const uint32_t sa = smem_u32(base), sw = sa + OFF_W;
+
+  if (warp < 4) {
+    const float out_scale = p.format == MLA_KV_FP8_E4M3_TENSOR ? __ldg(p.scales) : 1.f;
+    const uint32_t lane_base = tmem + ((uint32_t)(warp * 32) << 16);
+    long long src = -2;
+    // this block's rows
+    auto gather = [&](int u) {
+      const int row0 = u / p.H * kM;
+      src = row_source(p, row0 + warp * 32 + lane);
+      gather_rows(p, base, row0, warp, lane, src, u % p.H == 0);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&br->a_full));
+    };
+    if (u0 < u1) gather(u0);
+    for (int u = u0; u < u1; u++) {
+      const int i = u - u0, buf = i & 1;
+      const bool ok = __all_sync(0xffffffffu, wait_ok(br, &br->d_full[buf], (i >> 1) & 1, p.status));
+      if (!ok) break;
+      tc_fence_after();
+      const long long mine = src;
+      const int row = u / p.H * kM + warp * 32 + lane, h = u % p.H;
+      // the next unit's rows first: every MMA that reads A has completed
+      if (u + 1 < u1 && h + 1 == p.H) gather(u + 1);
+      uint8_t *dst = reinterpret_cast<uint8_t *>(p.kv + ((size_t)row * p.H + h) * 256);
+#pragma unroll 2
+      for (int c = 0; c < 8; c++) {
+        uint32_t v[32];
+        tmem_ld32(lane_base + buf * 256 + 32 * c, v);
+        tmem_wait_ld();
+        if (mine == -2) continue;
+        uint32_t w[16];
+#pragma unroll
+        for (int j = 0; j < 16; j++) {
+          __nv_bfloat162 b2 = __floats2bfloat162_rn(__uint_as_float(v[2 * j]) * out_scale,
+                                                    __uint_as_float(v[2 * j + 1]) * out_scale);
+          w[j] = *reinterpret_cast<uint32_t *>(&b2);
+        }
+        if (p.store_v8) {
+          const uint32_t a8[8] = {w[0], w[1], w[2], w[3], w[4], w[5], w[6], w[7]};
+          const uint32_t b8[8] = {w[8], w[9], w[10], w[11], w[12], w[13], w[14], w[15]};
+          st_global_v8(dst + 64 * c, a8);
+          st_global_v8(dst + 64 * c + 32, b8);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; j++)
+            reinterpret_cast<uint4 *>(dst + 64 * c)[j] = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&br->d_empty[buf]));
+    }
+  } else if (warp == 4) {
+    if (lane == 0) {
+      const uint64_t pol = policy_evict_normal();
+      uint32_t k = 0;
+      bool ok = true;
+      for (int u = u0; u < u1 && ok; u++) {
+        const int h = u % p.H;
+        for (int kb = 0; kb < kKBlocks; kb++, k++) {
+          const uint32_t s = k % kWStages;
+          ok = wait_ok(br, &br->w_empty[s], ((k / kWStages) & 1) ^ 1, p.status);
+          if (!ok) break;
+          mbar_arrive_expect_tx(smem_u32(&br->w_full[s]), kWStage);
+          tma_load_3d(sw + s * kWStage, &uk_map, smem_u32(&br->w_full[s]), 64 * kb, 0, h, pol);
+          tma_load_3d(sw + s * kWStage + kWStage / 2, &uv_map, smem_u32(&br->w_full[s]), 64 * kb, 0, h, pol);
+        }
+      }
+    }
+  } else if (lane == 0) {
+    uint32_t k = 0, na = 0;
+    bool ok = true;
+    for (int u = u0; u < u1 && ok; u++) {
+      const int i = u - u0, buf = i & 1;
+      if (i == 0 || u % p.H == 0) ok = wait_ok(br, &br->a_full, na++ & 1, p.status);
+      if (ok) ok = wait_ok(br, &br->d_empty[buf], ((i >> 1) & 1) ^ 1, p.status);
+      if (!ok) break;
+      tc_fence_after();
+      for (int kb = 0; kb < kKBlocks; kb++, k++) {
+        const uint32_t s = k % kWStages;
+        ok = wait_ok(br, &br->w_full[s], (k / kWStages) & 1, p.status);
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll
+        for (int kk = 0; kk < 4; kk++)
+          mma_ss(tmem + buf * 256, smem_desc_sw128(sa + kb * kABlock + kk * 32, 16, 1024),
+                 smem_desc_sw128(sw + s * kWStage + kk * 32, 16, 1024), IDESC, (kb | kk) ? 1u : 0u);
+        mma_commit(smem_u32(&br->w_empty[s]));
+      }
+      if (ok) mma_commit(smem_u32(&br->d_full[buf]));
+    }
+  }
+  __syncthreads();
+  if (*(volatile int *)&br->abort) {  // a wait gave up: let copies or MMAs still in flight land before the CTA exits
+    const uint64_t t0 = globaltimer();
+    while (globaltimer() - t0 < 2000000ull) {
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+int fail(int code, const char *msg) {
+  set_last_error(msg);
+  return code;
+}
+
+}  // namespace
+}  // namespace mla
+
+int mla_kv_expand(const void *kv_cache, int kv_format, int num_pages, int page_size, const int32_t *block_table,
+                  int max_pages, const int32_t *cu_seqlens, int B, int total, const float *kv_scales,
+                  const void *w_uk, int64_t uk_row, int64_t uk_head, const void *w_uv, int64_t uv_row,
+                  int64_t uv_head, int H, void *kv, void *k_pe, mla_stream_t stream) {
+  using namespace mla;
+  if (B < 0 || total < 0) return fail(MLA_ERR_INVALID_ARG, "B and total must be >= 0");
+  if (total > (1 << 30)) return fail(MLA_ERR_UNSUPPORTED, "total must be at most 2^30 rows");
+  if (H < 1 || H > MLA_MAX_HEADS) return fail(MLA_ERR_INVALID_ARG, "H must be in [1, 128]");
+  if (kv_format != MLA_KV_BF16 && kv_format != MLA_KV_FP8_E4M3 && kv_format != MLA_KV_FP8_E4M3_TENSOR)
+    return fail(MLA_ERR_INVALID_ARG, "kv_format unknown");
+  if (page_size != MLA_PAGE_SIZE) return fail(MLA_ERR_UNSUPPORTED, "page_size must be 64");
+  if (num_pages < 1 || max_pages < 1) return fail(MLA_ERR_INVALID_ARG, "num_pages and max_pages must be >= 1");
+  if (uk_row % 8 || uk_head % 8 || uv_row % 8 || uv_head % 8)
+    return fail(MLA_ERR_INVALID_ARG, "weight strides must be multiples of 8 elements");
+  if (uk_row < D_V || uv_row < D_V || (H > 1 && (uk_head < D_V || uv_head < D_V)))
+    return fail(MLA_ERR_INVALID_ARG, "weight strides must be at least 512 elements");
+  if (B == 0 || total == 0) {
+    set_last_error("");
+    return MLA_OK;
+  }
+  if (!kv_cache || !block_table || !cu_seqlens || !w_uk || !w_uv || !kv || !k_pe)
+    return fail(MLA_ERR_INVALID_ARG, "null pointer");
+  auto al = [](const void *p, unsigned a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; };
+  if (!al(kv_cache, 16) || !al(w_uk, 16) || !al(w_uv, 16) || !al(kv, 16) || !al(k_pe, 16))
+    return fail(MLA_ERR_INVALID_ARG, "kv_cache, w_uk, w_uv, kv and k_pe must be 16-byte aligned");
+  if (!al(block_table, 4) || !al(cu_seqlens, 4))
+    return fail(MLA_ERR_INVALID_ARG, "int32 arrays must be 4-byte aligned");
+  if (kv_format != MLA_KV_BF16 && (!kv_scales || !al(kv_scales, 4)))
+    return fail(MLA_ERR_INVALID_ARG, "an FP8 cache needs kv_scales (4-byte aligned)");
+  CUtensorMap uk_map, uv_map;
+  if (!make_map_3d(&uk_map, w_uk, D_V, 128, H, uk_row, uk_head, 128, 1) ||
+      !make_map_3d(&uv_map, w_uv, D_V, 128, H, uv_row, uv_head, 128, 1))
+    return fail(MLA_ERR_CUDA, "cuTensorMapEncodeTiled failed");
+  ExpandParams p;
+  p.cache = static_cast<const uint8_t *>(kv_cache);
+  p.scales = kv_scales;
+  p.block_table = block_table;
+  p.cu = cu_seqlens;
+  p.kv = static_cast<__nv_bfloat16 *>(kv);
+  p.k_pe = static_cast<__nv_bfloat16 *>(k_pe);
+  if (status_word(&p.status) != MLA_OK) return MLA_ERR_CUDA;
+  p.format = kv_format;
+  p.num_pages = num_pages;
+  p.max_pages = max_pages;
+  p.B = B;
+  p.H = H;
+  p.total = total;
+  p.store_v8 = al(kv, 32) ? 1 : 0;
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(expand_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+  if (e != cudaSuccess) return fail(MLA_ERR_CUDA, cudaGetErrorString(e));
+  const long long units = (long long)ceil_div(total, kM) * H;
+  expand_kernel<<<(int)(units < sms ? units : sms), kThreads, kSmem, (cudaStream_t)stream>>>(uk_map, uv_map, p);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return fail(MLA_ERR_CUDA, cudaGetErrorString(e));
+  set_last_error("");
+  return MLA_OK;
+}

@@ -21,6 +21,18 @@
 // Lane l holds latent values 16l .. 16l + 15, so the 8 lanes 8t .. 8t+7 hold
 // FP8 scale tile t (values 128t .. 128t + 127) and every lane stores one
 // 16-byte piece of the latent part of the row.
+//
+// With rotation (mla_kv_insert_rope) the pair (a, b) of a key or query row
+// and its angle's cosine c and sine s at the token's position become
+//   a' = bf16(fp32(fp32(a c) - fp32(b s)))
+//   b' = bf16(fp32(fp32(a s) + fp32(b c)))
+// from a table of fp32 cosines and sines (angles of far positions need more
+// than 32 bits, so they are the caller's, taken once).  The key is rotated in
+// the lanes that hold it before the row is written, so a row is bit for bit
+// what the plain insert writes for the rotated bf16 key.  The query rows are
+// rotated by further blocks of the same launch: rows of 128 bytes, eight
+// lanes a row, so a warp moves four rows at a time; that part is bound by HBM
+// (256 bytes a row) and shares nothing with the insert but the launch.
 #include <cuda_fp8.h>
 
 #include "common.cuh"
@@ -69,8 +81,11 @@ __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_gr
 
 // Start the copies of token j into a stage (nothing past the last token);
 // every call commits one group, so the group count per stage stays fixed.
-__device__ __forceinline__ void issue_token(const KvInsertParams &p, int j, int lane, uint32_t stage) {
+template <bool kRope>
+__device__ __forceinline__ void issue_token(const KvInsertParams &p, const int64_t *positions, int j, int lane,
+                                            uint32_t stage) {
   if (j < p.N) {
+    if (kRope && lane == 1) cp_async8(stage + 1160, positions + j);
     const uint8_t *x = reinterpret_cast<const uint8_t *>(p.kv_c + (size_t)j * p.ld_kv) + 32 * lane;
     cp_async16(stage + 32 * lane, x);
     cp_async16(stage + 32 * lane + 16, x + 16);
@@ -186,7 +201,92 @@ __device__ __forceinline__ void insert_token(const KvInsertParams &p, const Toke
   }
 }
 
-__global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm) kv_insert_kernel(KvInsertParams p) {
+// The rotation of one 16-byte piece (values 8 * sub .. 8 * sub + 7) of a row
+// of 64, held by eight neighbouring lanes.  cs: the position's 32 cosines and
+// 32 sines.  Pairs are (2i, 2i + 1), within a piece, or (i, i + 32), whose
+// halves are four lanes apart; every lane of the warp takes part.
+__device__ __forceinline__ uint4 rotate8(uint4 x, int sub, const float *cs, int interleaved) {
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+  uint32_t o[4];
+  if (interleaved) {
+    const float4 c = __ldg(reinterpret_cast<const float4 *>(cs) + sub);
+    const float4 s = __ldg(reinterpret_cast<const float4 *>(cs) + 8 + sub);
+    const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+    for (int k = 0; k < 4; k++) {
+      const float a = __uint_as_float(w[k] << 16), b = __uint_as_float(w[k] & 0xFFFF0000u);
+      __nv_bfloat162 r = __floats2bfloat162_rn(__fsub_rn(__fmul_rn(a, cc[k]), __fmul_rn(b, ss[k])),
+                                               __fadd_rn(__fmul_rn(a, ss[k]), __fmul_rn(b, cc[k])));
+      o[k] = *reinterpret_cast<uint32_t *>(&r);
+    }
+  } else {
+    const float4 *cp = reinterpret_cast<const float4 *>(cs) + 2 * (sub & 3);
+    const float4 c0 = __ldg(cp), c1 = __ldg(cp + 1), s0 = __ldg(cp + 8), s1 = __ldg(cp + 9);
+    const float cc[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
+    const float ss[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
+#pragma unroll
+    for (int k = 0; k < 4; k++) {
+      const uint32_t u = __shfl_xor_sync(0xffffffffu, w[k], 4);  // the other half of each pair
+      float r[2];
+#pragma unroll
+      for (int e = 0; e < 2; e++) {
+        const float own = __uint_as_float(e ? w[k] & 0xFFFF0000u : w[k] << 16);
+        const float far = __uint_as_float(e ? u & 0xFFFF0000u : u << 16);
+        const float c = cc[2 * k + e], s = ss[2 * k + e];
+        r[e] = sub < 4 ? __fsub_rn(__fmul_rn(own, c), __fmul_rn(far, s))
+                       : __fadd_rn(__fmul_rn(far, s), __fmul_rn(own, c));
+      }
+      __nv_bfloat162 r2 = __floats2bfloat162_rn(r[0], r[1]);
+      o[k] = *reinterpret_cast<uint32_t *>(&r2);
+    }
+  }
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+// A token's position: false for a token that is skipped (-1), and for one
+// outside the table, which also sets the status bit.
+__device__ __forceinline__ bool position_ok(long long pos, int max_pos, unsigned int *status, bool tell) {
+  if (pos >= 0 && pos < max_pos) return true;
+  if (pos != -1 && tell) atomicOr(status, MLA_STATUS_BAD_POSITION);
+  return false;
+}
+
+// Query rows: each warp takes eight heads of one token at a time, as two
+// groups of four rows.
+constexpr int kQHeads = 8;
+__device__ void rotate_queries(const KvInsertParams &p, const RopeParams &r, int unit, int stride) {
+  const int lane = threadIdx.x & 31, sub = lane & 7;
+  const int groups = (r.H + kQHeads - 1) / kQHeads;
+  const long long units = (long long)p.N * groups;
+  for (long long u = unit; u < units; u += stride) {
+    const int n = (int)(u / groups), h0 = (int)(u % groups) * kQHeads;
+    const long long pos = __ldg(reinterpret_cast<const long long *>(r.positions) + n);
+    if (!position_ok(pos, r.max_pos, p.status, lane == 0)) continue;
+    const float *cs = r.cos_sin + pos * 64;
+    uint4 x[2];
+#pragma unroll
+    for (int i = 0; i < 2; i++) {
+      const int h = h0 + 4 * i + (lane >> 3);
+      x[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (h < r.H) x[i] = *reinterpret_cast<const uint4 *>(r.q_pe + n * r.q_tok + h * r.q_head + 8 * sub);
+    }
+#pragma unroll
+    for (int i = 0; i < 2; i++) {
+      const int h = h0 + 4 * i + (lane >> 3);
+      const uint4 y = rotate8(x[i], sub, cs, r.interleaved);
+      if (h < r.H) *reinterpret_cast<uint4 *>(r.q_out + n * r.o_tok + h * r.o_head + 8 * sub) = y;
+    }
+  }
+}
+
+template <bool kRope>
+__global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm)
+    kv_insert_kernel(KvInsertParams p, RopeParams r, int insert_blocks) {
+  if (kRope && (int)blockIdx.x >= insert_blocks) {
+    rotate_queries(p, r, ((int)blockIdx.x - insert_blocks) * kWarps + ((int)threadIdx.x >> 5),
+                   ((int)gridDim.x - insert_blocks) * kWarps);
+    return;
+  }
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ uint32_t sc_tab[256], inv_tab[256];  // fp32(m / 448), fp32(1 / that), m = 0..255
   static_assert(kWarps * 32 == 256, "one table entry per thread");
@@ -198,7 +298,7 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm) kv_insert_kernel(Kv
   __syncthreads();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int first = blockIdx.x * kWarps + warp;
-  const int stride = gridDim.x * kWarps;
+  const int stride = insert_blocks * kWarps;
   if (first >= p.N) return;
   uint8_t *ring = smem + warp * kStages * kStageBytes;
   const uint32_t ring_s = (uint32_t)__cvta_generic_to_shared(ring);
@@ -207,11 +307,11 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm) kv_insert_kernel(Kv
   unpack8(__ldg(wr), w, 0);
   unpack8(__ldg(wr + 1), w, 8);
 #pragma unroll
-  for (int s = 0; s < kStages - 1; s++) issue_token(p, first + s * stride, lane, ring_s + s * kStageBytes);
+  for (int s = 0; s < kStages - 1; s++) issue_token<kRope>(p, r.positions, first + s * stride, lane, ring_s + s * kStageBytes);
   int st = 0;
   for (int j = first; j < p.N; j += stride) {
     const int ahead = st == 0 ? kStages - 1 : st - 1;  // the stage freed last iteration
-    issue_token(p, j + (kStages - 1) * stride, lane, ring_s + ahead * kStageBytes);
+    issue_token<kRope>(p, r.positions, j + (kStages - 1) * stride, lane, ring_s + ahead * kStageBytes);
     cp_async_wait<kStages - 1>();  // this token's group has landed (for this lane's copies)
     __syncwarp();                  // ... and lane 0's slot copy is visible to all lanes
     const uint8_t *cur = ring + st * kStageBytes;
@@ -220,7 +320,17 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm) kv_insert_kernel(Kv
     tk.xb = *reinterpret_cast<const uint4 *>(cur + 32 * lane + 16);
     tk.pe = lane < 8 ? *reinterpret_cast<const uint4 *>(cur + 1024 + 16 * lane) : make_uint4(0u, 0u, 0u, 0u);
     tk.slot = *reinterpret_cast<const long long *>(cur + 1152);
-    __syncwarp();  // every lane has read the stage before it is refilled
+    if (kRope) {
+      const long long pos = *reinterpret_cast<const long long *>(cur + 1160);
+      __syncwarp();  // every lane has read the stage before it is refilled
+      if (!position_ok(pos, r.max_pos, p.status, lane == 0)) {
+        st = st + 1 == kStages ? 0 : st + 1;
+        continue;
+      }
+      tk.pe = rotate8(tk.pe, lane & 7, r.cos_sin + pos * 64, r.interleaved);  // (lanes 8.. rotate zeros)
+    } else {
+      __syncwarp();  // every lane has read the stage before it is refilled
+    }
     insert_token(p, tk, w, lane, sc_tab, inv_tab);
     st = st + 1 == kStages ? 0 : st + 1;
   }
@@ -237,7 +347,22 @@ cudaError_t launch_kv_insert(const KvInsertParams &p, cudaStream_t stream) {
   const int need = (p.N + kWarps - 1) / kWarps;
   const int blocks = need < sms * kBlocksPerSm ? need : sms * kBlocksPerSm;
   static_assert(kSmemBytes <= 48 * 1024, "dynamic shared memory above the default limit");
-  kv_insert_kernel<<<blocks, kWarps * 32, kSmemBytes, stream>>>(p);
+  kv_insert_kernel<false><<<blocks, kWarps * 32, kSmemBytes, stream>>>(p, RopeParams{}, blocks);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_kv_insert_rope(const KvInsertParams &p, const RopeParams &r, cudaStream_t stream) {
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  const long long most = (long long)sms * kBlocksPerSm;
+  const long long need = ((long long)p.N + kWarps - 1) / kWarps;
+  const long long q_units = r.q_pe ? (long long)p.N * ((r.H + kQHeads - 1) / kQHeads) : 0;
+  const long long q_need = (q_units + kWarps - 1) / kWarps;
+  const int blocks = (int)(need < most ? need : most);
+  const int q_blocks = (int)(q_need < 2 * most ? q_need : 2 * most);
+  kv_insert_kernel<true><<<blocks + q_blocks, kWarps * 32, kSmemBytes, stream>>>(p, r, blocks);
   return cudaGetLastError();
 }
 

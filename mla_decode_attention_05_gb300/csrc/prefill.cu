@@ -1,0 +1,612 @@
+// Prefill attention: the queries of prompts, or of chunks of new tokens, over
+// the expanded keys and values of their sequences.  For query row i of a
+// sequence with n_q queries and n_k keys, and head h,
+//   s_j = scale * (q[i][h][0:128] . k_nope[j][h] + q[i][h][128:192] . k_pe[j])
+//   lse = ln sum_j exp(s_j),  out = sum_j exp(s_j - lse) v[j][h]
+// over j < n_k, causal: j < n_k - n_q + i + 1 (the last query sees every key).
+// A row without keys gets out = 0 and lse = -inf.
+//
+// 640 flops a pair and head against one exponential, so the tensor cores
+// bound it; softmax has to stay in their shadow.  One pass over the keys with
+// a running reference m and sum l per row:
+//   p_j = 2^(s_j c - m c),  l += p_j,  O += p_j v_j        (c = scale log2 e)
+// m is the row's maximum when it was last moved.  It moves, and O and l are
+// scaled down, only when the maximum has grown by more than 8 in the exponent:
+// until then p stays below 2^8, which costs fp32 sums and bf16 probabilities
+// no precision (a rounding is relative), and O is rarely touched.
+//
+// Roundings: p to bf16 (the MMA's operand; l sums the fp32 values), out to
+// bf16 once.  Scores, m, l and O are fp32.
+//
+// Values that a row does not see must not reach it, whatever they hold: 0 * inf
+// and 0 * nan in P V would.  In the tiles where some row sees only a part of
+// the keys, a warp looks through the values in shared memory, replaces what is
+// not finite by zero before the MMA reads it and notes the key; rows that do
+// see such a key add its non-finite values at the end.  (A weight is positive,
+// so inf and nan reach the row's output as they are.)
+#include "common.cuh"
+#include "ptx.cuh"
+#include "tma_map.cuh"
+
+namespace mla {
+namespace {
+
+using namespace ptx;
+
+constexpr int kNope = 128;
+constexpr int kHead = 192;
+constexpr int kDv = 128;
+constexpr int kRows = 128;     // query rows of one tile; a CTA has two
+constexpr int kKeys = 128;     // keys of one step
+constexpr int kCtaRows = 2 * kRows;
+
+// Warps 0-3 and 4-7: softmax and output of tile 0 and 1 (one row a thread);
+// warp 8 issues the MMAs, warp 9 the loads, warp 10 looks through values.
+constexpr int kThreads = 352;
+
+// Shared memory: Q of both tiles as 2 x 3 blocks of 128 rows x 64 values; a
+// ring of 16 KB units for keys (128 keys x 64 values: no-PE low, no-PE high,
+// PE) and values (64 keys x 128 values, as two boxes of 64 values).
+constexpr uint32_t kUnit = 16384;
+constexpr int kUnits = 8;
+constexpr int kUnitsPerStep = 5;
+constexpr uint32_t OFF_RING = 6 * kUnit;
+constexpr uint32_t OFF_BARS = OFF_RING + kUnits * kUnit;
+
+// Tensor memory: S of both tiles (P, as bf16, over the S it came from), O of both.
+constexpr uint32_t TM_S = 0;
+constexpr uint32_t TM_O = 256;
+constexpr uint32_t IDESC_QK = idesc_bf16_f32(128, 128, false, false);
+constexpr uint32_t IDESC_PV = idesc_bf16_f32(128, 128, false, true);
+constexpr float kMoveAt = 8.f;
+
+struct Bars {
+  uint64_t full[kUnits], empty[kUnits];
+  uint64_t q_full[2];
+  uint64_t s_full[2];   // scores of a tile are in tensor memory
+  uint64_t p_full[2];   // its probabilities are
+  uint64_t o_done[2];   // its P V has been added
+  uint64_t v_look;      // the values of a masked step are there (told by the MMA warp: the ring's barriers
+                        // can be a phase further than a warp that does not follow every unit)
+  uint64_t v_ok;        // they have been looked through
+  uint32_t bad_keys[16];  // keys with a non-finite value, from the first masked step on
+  uint32_t tmem_base;
+  int abort;
+};
+constexpr uint32_t kSmem = OFF_BARS + sizeof(Bars) + 1024;
+static_assert(kSmem <= 232448, "shared memory budget");
+
+struct PrefillParams {
+  const int32_t *cu_q, *cu_k;
+  const __nv_bfloat16 *v;
+  __nv_bfloat16 *out;  // [Nq][H][128]
+  float *lse;          // [H][Nq]
+  unsigned int *status;
+  long long v_tok, v_head;
+  int B, H, Nq, Nk, tiles;
+  int causal;
+  int out_v8;
+  float scale, scale_log2;
+};
+
+// A CTA's work: 256 query rows of one sequence, one head.
+struct Work {
+  int q0, nq;  // first row in the packed queries, rows of this CTA (<= 256); nq = 0: nothing
+  int k0, nk;  // first key, keys of the sequence
+  int diff;    // row i of the CTA sees min(nk, max(0, diff + i + 1)) keys
+  int h;
+};
+
+__device__ __forceinline__ int visible(const Work &w, int i) { return min(w.nk, max(0, w.diff + i + 1)); }
+
+// Tiles are numbered through the sequences; the whole warp looks for tile t.
+__device__ Work find_work(const PrefillParams &p, int t, int h, int lane) {
+  Work w;
+  w.nq = 0;
+  w.h = h;
+  int before = 0;
+  for (int b0 = 0; b0 < p.B; b0 += 32) {
+    const int b = b0 + lane;
+    int s = 0, e = 0;
+    if (b < p.B) {
+      const int cs = __ldg(p.cu_q + b), ce = __ldg(p.cu_q + b + 1);
+      s = min(max(cs, 0), p.Nq);
+      e = min(max(ce, s), p.Nq);
+      if (s != cs || e != ce) atomicOr(p.status, MLA_STATUS_BAD_SEQLEN);
+    }
+    const int mine = ceil_div(e - s, kCtaRows);
+    int upto = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += v;
+    }
+    const int total = __shfl_sync(0xffffffffu, upto, 31);
+    if (t < before + total) {
+      const unsigned hit = __ballot_sync(0xffffffffu, t < before + upto);
+      const int who = __ffs(hit) - 1;
+      const int part = t - before - __shfl_sync(0xffffffffu, upto - mine, who);
+      s = __shfl_sync(0xffffffffu, s, who);
+      e = __shfl_sync(0xffffffffu, e, who);
+      const int ck = __ldg(p.cu_k + b0 + who), cke = __ldg(p.cu_k + b0 + who + 1);
+      w.k0 = min(max(ck, 0), p.Nk);
+      w.nk = min(max(cke, w.k0), p.Nk) - w.k0;
+      if (lane == 0 && (w.k0 != ck || w.k0 + w.nk != cke)) atomicOr(p.status, MLA_STATUS_BAD_SEQLEN);
+      w.q0 = s + part * kCtaRows;
+      w.nq = min(kCtaRows, e - w.q0);
+      w.diff = p.causal ? w.nk - (e - s) + part * kCtaRows : p.Nk;
+      return w;
+    }
+    before += total;
+  }
+  return w;
+}
+
+// Steps over the keys: n[t] of tile t, of which those from `masked` on hold
+// keys that some row of a tile does not see.
+struct Steps {
+  int n[2], most, masked;
+};
+
+__device__ __forceinline__ Steps steps_of(const Work &w) {
+  Steps s;
+  s.masked = 1 << 30;
+#pragma unroll
+  for (int t = 0; t < 2; t++) {
+    const int first = t * kRows, last = min(w.nq, first + kRows) - 1;
+    s.n[t] = last < first ? 0 : ceil_div(visible(w, last), kKeys);
+    const int whole = visible(w, first) / kKeys;  // steps that every row of the tile sees whole
+    if (whole < s.n[t]) s.masked = min(s.masked, whole);
+  }
+  s.most = max(s.n[0], s.n[1]);
+  return s;
+}
+
+__device__ __forceinline__ bool wait_ok(Bars *b, uint64_t *bar, uint32_t parity, unsigned int *status) {
+  if (mbar_wait<false>(smem_u32(bar), parity, &b->abort, kDefaultWaitNs)) return true;
+  atomicOr(status, MLA_STATUS_WAIT_TIMEOUT);
+  *(volatile int *)&b->abort = 1;
+  return false;
+}
+
+__device__ __forceinline__ bool warp_wait_ok(Bars *b, uint64_t *bar, uint32_t parity, unsigned int *status) {
+  return __all_sync(0xffffffffu, wait_ok(b, bar, parity, status));
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Pairs of fp32 in one 64-bit register (fma and add of two at a time).
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float &a, float &b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+__device__ __forceinline__ void issue_loads(const CUtensorMap *q_map, const CUtensorMap *kn_map,
+                                            const CUtensorMap *kp_map, const CUtensorMap *v_map, Bars *br,
+                                            uint32_t smem, const Work &w, const Steps &st, unsigned int *status) {
+  const uint64_t pol = policy_evict_normal(), first = policy_evict_first();
+#pragma unroll
+  for (int t = 0; t < 2; t++) {
+    if (st.n[t] == 0) continue;
+    mbar_arrive_expect_tx(smem_u32(&br->q_full[t]), 3 * kUnit);
+    for (int c = 0; c < 3; c++)
+      tma_load_3d(smem + (3 * t + c) * kUnit, q_map, smem_u32(&br->q_full[t]), 64 * c, w.h, w.q0 + t * kRows, first);
+  }
+  uint32_t u = 0;
+  for (int j = 0; j < st.most; j++) {
+    const int key = w.k0 + j * kKeys;
+#pragma unroll 1
+    for (int c = 0; c < kUnitsPerStep; c++, u++) {
+      const uint32_t s = u % kUnits, full = smem_u32(&br->full[s]), dst = smem + OFF_RING + s * kUnit;
+      if (!wait_ok(br, &br->empty[s], ((u / kUnits) & 1) ^ 1, status)) return;
+      mbar_arrive_expect_tx(full, kUnit);
+      if (c < 2) {
+        tma_load_3d(dst, kn_map, full, 64 * c, w.h, key, pol);
+      } else if (c == 2) {
+        tma_load_3d(dst, kp_map, full, 0, 0, key, pol);
+      } else {
+        tma_load_3d(dst, v_map, full, 0, w.h, key + 64 * (c - 3), pol);
+        tma_load_3d(dst + kUnit / 2, v_map, full, 64, w.h, key + 64 * (c - 3), pol);
+      }
+    }
+  }
+}
+
+__device__ __forceinline__ void issue_mmas(Bars *br, uint32_t smem, uint32_t tmem, const Steps &st,
+                                           unsigned int *status) {
+  const uint32_t ring = smem + OFF_RING;
+  // scores of tile t for step j: its three key units are units 5j .. 5j + 2
+  auto qk = [&](int t, int j, bool wait) {
+    for (int c = 0; c < 3; c++) {
+      const uint32_t u = (uint32_t)j * kUnitsPerStep + c, s = u % kUnits;
+      if (wait && !wait_ok(br, &br->full[s], (u / kUnits) & 1, status)) return false;
+      tc_fence_after();
+      const uint32_t a = smem + (3 * t + c) * kUnit, b = ring + s * kUnit;
+#pragma unroll
+      for (int k = 0; k < 4; k++)
+        mma_ss(tmem + TM_S + t * 128, smem_desc_sw128(a + k * 32, 16, 1024), smem_desc_sw128(b + k * 32, 16, 1024),
+               IDESC_QK, (c | k) ? 1u : 0u);
+    }
+    mma_commit(smem_u32(&br->s_full[t]));
+    return true;
+  };
+  auto pv = [&](int t, int j, bool wait) {
+    const uint32_t u = (uint32_t)j * kUnitsPerStep + 3, sa = u % kUnits, sb = (u + 1) % kUnits;
+    const bool look = wait && j >= st.masked;
+    if (wait && (!wait_ok(br, &br->full[sa], (u / kUnits) & 1, status) ||
+                 !wait_ok(br, &br->full[sb], ((u + 1) / kUnits) & 1, status)))
+      return false;
+    if (look) mbar_arrive(smem_u32(&br->v_look));
+    if (!wait_ok(br, &br->p_full[t], j & 1, status)) return false;
+    if (look && !wait_ok(br, &br->v_ok, (j - st.masked) & 1, status)) return false;
+    tc_fence_after();
+#pragma unroll
+    for (int k = 0; k < 8; k++)
+      mma_ts(tmem + TM_O + t * 128, tmem + TM_S + t * 128 + k * 8,
+             smem_desc_sw128(ring + (k < 4 ? sa : sb) * kUnit + (k & 3) * 2048, kUnit / 2, 1024), IDESC_PV,
+             (j | k) ? 1u : 0u);
+    mma_commit(smem_u32(&br->o_done[t]));
+    return true;
+  };
+  auto release = [&](int j, int from, int to) {
+    for (int c = from; c < to; c++) mma_commit(smem_u32(&br->empty[((uint32_t)j * kUnitsPerStep + c) % kUnits]));
+  };
+  const int n0 = st.n[0], n1 = st.n[1];
+  if (st.most == 0) return;
+  if (n0 > 0 && (!wait_ok(br, &br->q_full[0], 0, status) || !qk(0, 0, true))) return;
+  if (n1 > 0 && (!wait_ok(br, &br->q_full[1], 0, status) || !qk(1, 0, n0 == 0))) return;
+  release(0, 0, 3);
+  // While a tile's softmax runs, the tensor cores work on the other tile: its
+  // P V, then its next scores.  A unit goes back to the loads after the last
+  // tile that reads it.
+  for (int j = 0; j < st.most; j++) {
+    const bool v0 = j < n0, v1 = j < n1, s0 = j + 1 < n0, s1 = j + 1 < n1;
+    if (v0 && !pv(0, j, true)) return;
+    if (!v1) release(j, 3, 5);
+    if (s0 && !qk(0, j + 1, true)) return;
+    if (s0 && !s1) release(j + 1, 0, 3);
+    if (v1) {
+      if (!pv(1, j, !v0)) return;
+      release(j, 3, 5);
+    }
+    if (s1) {
+      if (!qk(1, j + 1, !s0)) return;
+      release(j + 1, 0, 3);
+    }
+  }
+}
+
+// The whole warp looks through the values of every masked step.
+__device__ void check_values(Bars *br, uint8_t *ring, const Steps &st, int lane, unsigned int *status) {
+  for (int j = st.masked; j < st.most; j++) {
+    if (!warp_wait_ok(br, &br->v_look, (j - st.masked) & 1, status)) return;
+    bool patched = false;
+    for (int c = 0; c < 2; c++) {
+      const uint32_t u = (uint32_t)j * kUnitsPerStep + 3 + c, s = u % kUnits;
+      if (!warp_wait_ok(br, &br->full[s], (u / kUnits) & 1, status)) return;
+      uint8_t *unit = ring + s * kUnit;
+#pragma unroll 8
+      for (int i = lane; i < (int)(kUnit / 16); i += 32) {
+        uint4 v = *reinterpret_cast<const uint4 *>(unit + i * 16);
+        // a bf16 is not finite when its eight exponent bits are all set
+        auto bad = [](uint32_t x) { return (x & 0x7F80u) == 0x7F80u || (x & 0x7F800000u) == 0x7F800000u; };
+        if (bad(v.x) || bad(v.y) || bad(v.z) || bad(v.w)) {
+          auto clean = [](uint32_t x) {
+            if ((x & 0x7F80u) == 0x7F80u) x &= 0xFFFF0000u;
+            if ((x & 0x7F800000u) == 0x7F800000u) x &= 0x0000FFFFu;
+            return x;
+          };
+          *reinterpret_cast<uint4 *>(unit + i * 16) = make_uint4(clean(v.x), clean(v.y), clean(v.z), clean(v.w));
+          const int key = (j - st.masked) * kKeys + c * 64 + ((i * 16) % (int)(kUnit / 2)) / 128;
+          if (key < 512) atomicOr(&br->bad_keys[key >> 5], 1u << (key & 31));
+          patched = true;
+        }
+      }
+    }
+    if (patched) fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&br->v_ok));
+  }
+}
+
+// One row a thread: the softmax of tile t over its steps, then its output.
+__device__ void softmax_rows(const PrefillParams &p, Bars *br, uint32_t tmem, const Work &w, const Steps &st, int t) {
+  const int warp = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
+  const int i = t * kRows + warp * 32 + lane;  // the CTA's row
+  const int seen = visible(w, i);
+  const uint32_t lanes = (uint32_t)(warp * 32) << 16;
+  const uint32_t ts = tmem + TM_S + t * 128 + lanes, to = tmem + TM_O + t * 128 + lanes;
+  const int n = t == 0 ? st.n[0] : st.n[1];
+  float m = -INFINITY;  // reference, in score units
+  uint64_t l0 = 0, l1 = 0;
+  const uint64_t c2 = pack2(p.scale_log2, p.scale_log2);
+  for (int j = 0; j < n; j++) {
+    if (!warp_wait_ok(br, &br->s_full[t], j & 1, p.status)) return;
+    tc_fence_after();
+    uint32_t s[4][32];
+#pragma unroll
+    for (int c = 0; c < 4; c++) tmem_ld32(ts + 32 * c, s[c]);
+    tmem_wait_ld();
+    const int here = seen - j * kKeys;  // keys of this step that the row sees
+    if (j >= st.masked && here < kKeys) {
+#pragma unroll
+      for (int c = 0; c < 4; c++)
+#pragma unroll
+        for (int e = 0; e < 32; e++)
+          if (32 * c + e >= here) s[c][e] = 0xFF800000u;
+    }
+    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+    for (int c = 0; c < 4; c++)
+#pragma unroll
+      for (int e = 0; e < 32; e += 2)
+        mx[c] = fmaxf(fmaxf(mx[c], __uint_as_float(s[c][e])), __uint_as_float(s[c][e + 1]));
+    const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+    const bool move = (top - m) * p.scale_log2 > kMoveAt;  // (-inf - -inf is nan: no move)
+    if (__any_sync(0xffffffffu, move)) {
+      const float alpha = move ? ex2((m - top) * p.scale_log2) : 1.f;
+      if (move) m = top;
+      if (j > 0) {
+        if (!warp_wait_ok(br, &br->o_done[t], (j - 1) & 1, p.status)) return;
+        tc_fence_after();
+        const uint64_t a2 = pack2(alpha, alpha);
+        asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(l0) : "l"(a2));
+        asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(l1) : "l"(a2));
+#pragma unroll 1
+        for (int c = 0; c < 8; c++) {
+          uint32_t o[16];
+          asm volatile(
+              "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
+              "%14, %15}, [%16];"
+              : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3]), "=r"(o[4]), "=r"(o[5]), "=r"(o[6]), "=r"(o[7]),
+                "=r"(o[8]), "=r"(o[9]), "=r"(o[10]), "=r"(o[11]), "=r"(o[12]), "=r"(o[13]), "=r"(o[14]), "=r"(o[15])
+              : "r"(to + 16 * c)
+              : "memory");
+          tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 16; e++) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+          asm volatile(
+              "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
+              "%14, %15, %16};" ::"r"(to + 16 * c),
+              "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3]), "r"(o[4]), "r"(o[5]), "r"(o[6]), "r"(o[7]), "r"(o[8]),
+              "r"(o[9]), "r"(o[10]), "r"(o[11]), "r"(o[12]), "r"(o[13]), "r"(o[14]), "r"(o[15])
+              : "memory");
+        }
+      }
+    }
+    const float mc = m == -INFINITY ? 0.f : m * p.scale_log2;
+    const uint64_t nm2 = pack2(-mc, -mc);
+#pragma unroll
+    for (int half = 0; half < 2; half++) {
+      uint32_t pw[32];
+#pragma unroll
+      for (int e = 0; e < 32; e++) {
+        const int c = 2 * half + (e >> 4), x = 2 * (e & 15);
+        const uint64_t y = fma2(pack2(__uint_as_float(s[c][x]), __uint_as_float(s[c][x + 1])), c2, nm2);
+        float a, b;
+        unpack2(y, a, b);
+        a = ex2(a);
+        b = ex2(b);
+        if (e & 1) l1 = add2(l1, pack2(a, b)); else l0 = add2(l0, pack2(a, b));
+        __nv_bfloat162 h2 = __floats2bfloat162_rn(a, b);
+        pw[e] = *reinterpret_cast<uint32_t *>(&h2);
+      }
+      tmem_st32(ts + 32 * half, pw);
+    }
+    tmem_wait_st();
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&br->p_full[t]));
+  }
+
+  float la, lb, lc, ld;
+  unpack2(l0, la, lb);
+  unpack2(l1, lc, ld);
+  const float l = (la + lb) + (lc + ld);
+  const bool live = i < w.nq;
+  if (n > 0) {
+    if (!warp_wait_ok(br, &br->o_done[t], (n - 1) & 1, p.status)) return;
+    tc_fence_after();
+  }
+  const bool none = live && seen == 0;
+  const float inv = l != 0.f ? 1.f / l : 0.f;
+  // do masked steps hold non-finite values?
+  bool bad = false;
+  if (n > 0 && st.masked < st.most)
+    for (int k = 0; k < 16; k++) bad |= *(volatile uint32_t *)&br->bad_keys[k] != 0;
+  __nv_bfloat16 *dst = p.out + ((size_t)(w.q0 + i) * p.H + w.h) * kDv;
+#pragma unroll 1
+  for (int c = 0; c < 4; c++) {
+    uint32_t o[32];
+    if (n > 0) {
+      tmem_ld32(to + 32 * c, o);
+      tmem_wait_ld();
+    }
+    if (!live) continue;
+    uint32_t r[16];
+#pragma unroll
+    for (int e = 0; e < 32; e += 2) {
+      float a = none ? 0.f : __uint_as_float(o[e]) * inv, b = none ? 0.f : __uint_as_float(o[e + 1]) * inv;
+      __nv_bfloat162 h2 = __floats2bfloat162_rn(a, b);
+      r[e >> 1] = *reinterpret_cast<uint32_t *>(&h2);
+    }
+    if (p.out_v8) {
+      const uint32_t a8[8] = {r[0], r[1], r[2], r[3], r[4], r[5], r[6], r[7]};
+      const uint32_t b8[8] = {r[8], r[9], r[10], r[11], r[12], r[13], r[14], r[15]};
+      st_global_v8(dst + 32 * c, a8);
+      st_global_v8(dst + 32 * c + 16, b8);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; k++)
+        reinterpret_cast<uint4 *>(dst + 32 * c)[k] = make_uint4(r[4 * k], r[4 * k + 1], r[4 * k + 2], r[4 * k + 3]);
+    }
+  }
+  if (live && bad) {  // rare: add the non-finite values of the keys that this row sees
+    for (int k = 0; k < 512; k++) {
+      if (!((*(volatile uint32_t *)&br->bad_keys[k >> 5] >> (k & 31)) & 1u)) continue;
+      const int key = st.masked * kKeys + k;
+      if (key >= seen) continue;
+      const __nv_bfloat16 *vr = p.v + (size_t)(w.k0 + key) * p.v_tok + (size_t)w.h * p.v_head;
+      for (int d = 0; d < kDv; d++) {
+        const float x = __bfloat162float(vr[d]);
+        if (!(fabsf(x) < INFINITY)) dst[d] = __float2bfloat16_rn(__bfloat162float(dst[d]) + x);
+      }
+    }
+  }
+  if (live) p.lse[(size_t)w.h * p.Nq + w.q0 + i] = none ? -INFINITY : m * p.scale + logf(l);
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+    prefill_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap kn_map,
+                   const __grid_constant__ CUtensorMap kp_map, const __grid_constant__ CUtensorMap v_map,
+                   PrefillParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *base = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  Bars *br = reinterpret_cast<Bars *>(base + OFF_BARS);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // the last tiles of a sequence see the most keys: they go first
+  const int tile = p.tiles - 1 - (int)(blockIdx.x % (unsigned)p.tiles);
+  const Work w = find_work(p, tile, (int)(blockIdx.x / (unsigned)p.tiles), lane);
+  if (w.nq == 0) return;  // (the same for every thread of the CTA)
+  const Steps st = steps_of(w);
+  if (warp == 0) {
+    tmem_alloc(smem_u32(&br->tmem_base), 512);
+    tmem_relinquish();
+  }
+  if (threadIdx.x == 32) {
+    for (int s = 0; s < kUnits; s++) {
+      mbar_init(smem_u32(&br->full[s]), 1);
+      mbar_init(smem_u32(&br->empty[s]), 1);
+    }
+    for (int t = 0; t < 2; t++) {
+      mbar_init(smem_u32(&br->q_full[t]), 1);
+      mbar_init(smem_u32(&br->s_full[t]), 1);
+      mbar_init(smem_u32(&br->p_full[t]), 4);
+      mbar_init(smem_u32(&br->o_done[t]), 1);
+    }
+    mbar_init(smem_u32(&br->v_look), 1);
+    mbar_init(smem_u32(&br->v_ok), 1);
+    for (int k = 0; k < 16; k++) br->bad_keys[k] = 0;
+    br->abort = 0;
+    fence_mbar_init_cluster();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = br->tmem_base, smem = smem_u32(base);
+  if (warp < 8) {
+    softmax_rows(p, br, tmem, w, st, warp >> 2);
+  } else if (warp == 8) {
+    if (lane == 0) issue_mmas(br, smem, tmem, st, p.status);
+  } else if (warp == 9) {
+    if (lane == 0) issue_loads(&q_map, &kn_map, &kp_map, &v_map, br, smem, w, st, p.status);
+  } else {
+    check_values(br, base + OFF_RING, st, lane, p.status);
+  }
+  __syncthreads();
+  if (*(volatile int *)&br->abort) {  // a wait gave up: let copies or MMAs still in flight land before the CTA exits
+    const uint64_t t0 = globaltimer();
+    while (globaltimer() - t0 < 2000000ull) {
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+int fail(int code, const char *msg) {
+  set_last_error(msg);
+  return code;
+}
+
+}  // namespace
+}  // namespace mla
+
+int mla_prefill(const void *q, int64_t q_tok, int64_t q_head, const void *k_nope, int64_t k_tok, int64_t k_head,
+                const void *k_pe, int64_t pe_tok, const void *v, int64_t v_tok, int64_t v_head,
+                const int32_t *cu_seqlens_q, const int32_t *cu_seqlens_k, int B, int H, int Nq, int Nk,
+                float softmax_scale, int causal, void *out, float *lse, mla_stream_t stream) {
+  using namespace mla;
+  if (B < 0 || Nq < 0 || Nk < 0) return fail(MLA_ERR_INVALID_ARG, "B, Nq and Nk must be >= 0");
+  if (B > (1 << 20) || Nq > (1 << 30) || Nk > (1 << 30))
+    return fail(MLA_ERR_UNSUPPORTED, "B must be at most 2^20, Nq and Nk at most 2^30");
+  if (H < 1 || H > MLA_MAX_HEADS) return fail(MLA_ERR_INVALID_ARG, "H must be in [1, 128]");
+  if (causal != 0 && causal != 1) return fail(MLA_ERR_INVALID_ARG, "causal must be 0 or 1");
+  if (!(softmax_scale > 0.f) || softmax_scale > 3.0e38f)
+    return fail(MLA_ERR_INVALID_ARG, "softmax_scale must be finite and > 0");
+  for (int64_t s : {q_tok, q_head, k_tok, k_head, pe_tok, v_tok, v_head})
+    if (s % 8) return fail(MLA_ERR_INVALID_ARG, "strides must be multiples of 8 elements");
+  if ((Nq > 1 && q_tok < kHead) || (H > 1 && q_head < kHead) || (Nk > 1 && (k_tok < kNope || v_tok < kDv || pe_tok < 64)) ||
+      (H > 1 && (k_head < kNope || v_head < kDv)))
+    return fail(MLA_ERR_INVALID_ARG, "strides must be at least a row's width");
+  if (B == 0 || Nq == 0) {
+    set_last_error("");
+    return MLA_OK;
+  }
+  if (!q || !cu_seqlens_q || !cu_seqlens_k || !out || !lse || (Nk > 0 && (!k_nope || !k_pe || !v)))
+    return fail(MLA_ERR_INVALID_ARG, "null pointer");
+  auto al = [](const void *p, unsigned a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; };
+  if (!al(q, 16) || !al(k_nope, 16) || !al(k_pe, 16) || !al(v, 16) || !al(out, 16))
+    return fail(MLA_ERR_INVALID_ARG, "q, k_nope, k_pe, v and out must be 16-byte aligned");
+  if (!al(cu_seqlens_q, 4) || !al(cu_seqlens_k, 4) || !al(lse, 4))
+    return fail(MLA_ERR_INVALID_ARG, "int32 and fp32 arrays must be 4-byte aligned");
+  // 256 rows a tile: at most one tile that is not full for each sequence
+  const long long tiles = Nq < B ? Nq : (Nq - B) / kCtaRows + (long long)B;
+  if (tiles * H > 0x7FFFFFFFll) return fail(MLA_ERR_UNSUPPORTED, "too many query tiles");
+  CUtensorMap q_map, kn_map, kp_map, v_map;
+  bool ok = make_map_3d(&q_map, q, kHead, H, Nq, q_head, q_tok, 1, kRows);
+  if (Nk > 0) {
+    ok = ok && make_map_3d(&kn_map, k_nope, kNope, H, Nk, k_head, k_tok, 1, kKeys) &&
+         make_map_3d(&kp_map, k_pe, 64, 1, Nk, 64, pe_tok, 1, kKeys) &&
+         make_map_3d(&v_map, v, kDv, H, Nk, v_head, v_tok, 1, kKeys / 2);
+  } else {
+    kn_map = kp_map = v_map = q_map;  // no step reads them
+  }
+  if (!ok) return fail(MLA_ERR_CUDA, "cuTensorMapEncodeTiled failed");
+  PrefillParams p;
+  p.cu_q = cu_seqlens_q;
+  p.cu_k = cu_seqlens_k;
+  p.v = static_cast<const __nv_bfloat16 *>(v);
+  p.out = static_cast<__nv_bfloat16 *>(out);
+  p.lse = lse;
+  if (status_word(&p.status) != MLA_OK) return MLA_ERR_CUDA;
+  p.v_tok = v_tok;
+  p.v_head = v_head;
+  p.B = B;
+  p.H = H;
+  p.Nq = Nq;
+  p.Nk = Nk;
+  p.tiles = (int)tiles;
+  p.causal = causal;
+  p.out_v8 = al(out, 32) ? 1 : 0;
+  p.scale = softmax_scale;
+  p.scale_log2 = softmax_scale * LOG2E;
+  cudaError_t e = cudaFuncSetAttribute(prefill_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+  if (e != cudaSuccess) return fail(MLA_ERR_CUDA, cudaGetErrorString(e));
+  prefill_kernel<<<(unsigned)(tiles * H), kThreads, kSmem, (cudaStream_t)stream>>>(q_map, kn_map, kp_map, v_map, p);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return fail(MLA_ERR_CUDA, cudaGetErrorString(e));
+  set_last_error("");
+  return MLA_OK;
+}
