@@ -24,6 +24,8 @@
 // not finite by zero before the MMA reads it and notes the key; rows that do
 // see such a key add its non-finite values at the end.  (A weight is positive,
 // so inf and nan reach the row's output as they are.)
+#include <type_traits>
+
 #include "common.cuh"
 #include "ptx.cuh"
 #include "tma_map.cuh"
@@ -41,8 +43,11 @@ constexpr int kKeys = 128;     // keys of one step
 constexpr int kCtaRows = 2 * kRows;
 
 // Warps 0-3 and 4-7: softmax and output of tile 0 and 1 (one row a thread);
-// warp 8 issues the MMAs, warp 9 the loads, warp 10 looks through values.
-constexpr int kThreads = 352;
+// warp 8 issues the MMAs, warp 9 the loads, warp 10 looks through values,
+// warp 11 waits for warp 8.  Registers move between the three warpgroups, from
+// 168 a thread at launch to 208 for the softmax and 88 for
+// the rest (2 * 208 + 88 = 3 * 168).
+constexpr int kThreads = 384;
 
 // Shared memory: Q of both tiles as 2 x 3 blocks of 128 rows x 64 values; a
 // ring of 16 KB units for keys (128 keys x 64 values: no-PE low, no-PE high,
@@ -64,9 +69,9 @@ struct Bars {
   uint64_t full[kUnits], empty[kUnits];
   uint64_t q_full[2];
   uint64_t s_full[2];   // scores of a tile are in tensor memory
-  uint64_t p_full[2];   // its probabilities are
+  uint64_t p_full[2][2];  // its probabilities are: of the first and the last 64 keys
   uint64_t o_done[2];   // its P V has been added
-  uint64_t v_look;      // the values of a masked step are there (told by the MMA warp: the ring's barriers
+  uint64_t v_look;      // the values of a masked step are there (told by the waiting warp: the ring's barriers
                         // can be a phase further than a warp that does not follow every unit)
   uint64_t v_ok;        // they have been looked through
   uint32_t bad_keys[16];  // keys with a non-finite value, from the first masked step on
@@ -230,66 +235,102 @@ __device__ __forceinline__ void issue_loads(const CUtensorMap *q_map, const CUte
   }
 }
 
-__device__ __forceinline__ void issue_mmas(Bars *br, uint32_t smem, uint32_t tmem, const Steps &st,
-                                           unsigned int *status) {
+// The MMA warp's order of work, gone through by two warps.  A wait on an
+// mbarrier by the warp that issues MMAs returns only when its MMAs in flight
+// are done (measured: about 130 cycles of idle tensor cores a wait, 4100
+// instead of 2560 cycles a step of two tiles); a named barrier does not.  So
+// warp 11 (kWaiter) makes the waits, meeting the MMA warp at a named barrier
+// before each group of MMAs; the barrier also tells of a wait that gave up.
+constexpr uint32_t kMmaBar = 1;
+
+template <bool kWaiter>
+__device__ __forceinline__ void mma_sequence(Bars *br, uint32_t smem, uint32_t tmem, const Steps &st,
+                                             unsigned int *status) {
   const uint32_t ring = smem + OFF_RING;
-  // scores of tile t for step j: its three key units are units 5j .. 5j + 2
-  auto qk = [&](int t, int j, bool wait) {
-    for (int c = 0; c < 3; c++) {
-      const uint32_t u = (uint32_t)j * kUnitsPerStep + c, s = u % kUnits;
-      if (wait && !wait_ok(br, &br->full[s], (u / kUnits) & 1, status)) return false;
-      tc_fence_after();
-      const uint32_t a = smem + (3 * t + c) * kUnit, b = ring + s * kUnit;
+  const int n0 = st.n[0], n1 = st.n[1];
+  bool ok = true;
+  auto landed = [&](uint32_t u) {
+    if (kWaiter) ok = ok && warp_wait_ok(br, &br->full[u % kUnits], (u / kUnits) & 1, status);
+  };
+  auto arrived = [&](uint64_t *bar, uint32_t parity) {
+    if (kWaiter) ok = ok && warp_wait_ok(br, bar, parity, status);
+  };
+  auto meet = [&]() { return !bar_red_or(kMmaBar, 64, !ok); };
+  // Scores of tile t for step j (units 5j .. 5j + 2).  A unit goes back to the
+  // loads after the MMAs of the last tile that reads it.
+  auto qk = [&](int t, int j, bool last) {
+    if (kWaiter) return;
+    tc_fence_after();
+    if (elect_one()) {
+#pragma unroll
+      for (int c = 0; c < 3; c++) {
+        const uint32_t u = (uint32_t)j * kUnitsPerStep + c;
+        const uint32_t a = smem + (3 * t + c) * kUnit, b = ring + u % kUnits * kUnit;
+#pragma unroll
+        for (int k = 0; k < 4; k++)
+          mma_ss(tmem + TM_S + t * 128, smem_desc_sw128(a + k * 32, 16, 1024), smem_desc_sw128(b + k * 32, 16, 1024),
+                 IDESC_QK, (c | k) ? 1u : 0u);
+        if (c == 2) mma_commit(smem_u32(&br->s_full[t]));
+        if (last) mma_commit(smem_u32(&br->empty[u % kUnits]));
+      }
+    }
+    __syncwarp();
+  };
+  // Half c of P V of tile t for step j (unit 5j + 3 + c: 64 keys).
+  auto pv = [&](int t, int j, int c, bool last) {
+    if (kWaiter) return;
+    const uint32_t u = (uint32_t)j * kUnitsPerStep + 3 + c;
+    tc_fence_after();
+    if (elect_one()) {
 #pragma unroll
       for (int k = 0; k < 4; k++)
-        mma_ss(tmem + TM_S + t * 128, smem_desc_sw128(a + k * 32, 16, 1024), smem_desc_sw128(b + k * 32, 16, 1024),
-               IDESC_QK, (c | k) ? 1u : 0u);
+        mma_ts(tmem + TM_O + t * 128, tmem + TM_S + t * 128 + c * 32 + k * 8,
+               smem_desc_sw128(ring + u % kUnits * kUnit + k * 2048, kUnit / 2, 1024), IDESC_PV,
+               (j | c | k) ? 1u : 0u);
+      if (c == 1) mma_commit(smem_u32(&br->o_done[t]));
+      if (last) mma_commit(smem_u32(&br->empty[u % kUnits]));
     }
-    mma_commit(smem_u32(&br->s_full[t]));
-    return true;
+    __syncwarp();
   };
-  auto pv = [&](int t, int j, bool wait) {
-    const uint32_t u = (uint32_t)j * kUnitsPerStep + 3, sa = u % kUnits, sb = (u + 1) % kUnits;
-    const bool look = wait && j >= st.masked;
-    if (wait && (!wait_ok(br, &br->full[sa], (u / kUnits) & 1, status) ||
-                 !wait_ok(br, &br->full[sb], ((u + 1) / kUnits) & 1, status)))
-      return false;
-    if (look) mbar_arrive(smem_u32(&br->v_look));
-    if (!wait_ok(br, &br->p_full[t], j & 1, status)) return false;
-    if (look && !wait_ok(br, &br->v_ok, (j - st.masked) & 1, status)) return false;
-    tc_fence_after();
-#pragma unroll
-    for (int k = 0; k < 8; k++)
-      mma_ts(tmem + TM_O + t * 128, tmem + TM_S + t * 128 + k * 8,
-             smem_desc_sw128(ring + (k < 4 ? sa : sb) * kUnit + (k & 3) * 2048, kUnit / 2, 1024), IDESC_PV,
-             (j | k) ? 1u : 0u);
-    mma_commit(smem_u32(&br->o_done[t]));
-    return true;
-  };
-  auto release = [&](int j, int from, int to) {
-    for (int c = from; c < to; c++) mma_commit(smem_u32(&br->empty[((uint32_t)j * kUnitsPerStep + c) % kUnits]));
-  };
-  const int n0 = st.n[0], n1 = st.n[1];
   if (st.most == 0) return;
-  if (n0 > 0 && (!wait_ok(br, &br->q_full[0], 0, status) || !qk(0, 0, true))) return;
-  if (n1 > 0 && (!wait_ok(br, &br->q_full[1], 0, status) || !qk(1, 0, n0 == 0))) return;
-  release(0, 0, 3);
+  for (uint32_t u = 0; u < 3; u++) landed(u);
+  if (n0 > 0) {
+    arrived(&br->q_full[0], 0);
+    if (!meet()) return;
+    qk(0, 0, n1 == 0);
+  }
+  if (n1 > 0) {
+    arrived(&br->q_full[1], 0);
+    if (!meet()) return;
+    qk(1, 0, true);
+  }
   // While a tile's softmax runs, the tensor cores work on the other tile: its
-  // P V, then its next scores.  A unit goes back to the loads after the last
-  // tile that reads it.
+  // P V, then its next scores.
   for (int j = 0; j < st.most; j++) {
-    const bool v0 = j < n0, v1 = j < n1, s0 = j + 1 < n0, s1 = j + 1 < n1;
-    if (v0 && !pv(0, j, true)) return;
-    if (!v1) release(j, 3, 5);
-    if (s0 && !qk(0, j + 1, true)) return;
-    if (s0 && !s1) release(j + 1, 0, 3);
-    if (v1) {
-      if (!pv(1, j, !v0)) return;
-      release(j, 3, 5);
+    landed((uint32_t)j * kUnitsPerStep + 3);
+    landed((uint32_t)j * kUnitsPerStep + 4);
+    if (kWaiter && ok && j >= st.masked) {
+      if (elect_one()) mbar_arrive(smem_u32(&br->v_look));
+      arrived(&br->v_ok, (j - st.masked) & 1);
     }
-    if (s1) {
-      if (!qk(1, j + 1, !s0)) return;
-      release(j + 1, 0, 3);
+#pragma unroll
+    for (int t = 0; t < 2; t++) {
+      const int n = t == 0 ? n0 : n1, other = t == 0 ? n1 : n0;
+      if (j >= n) continue;
+      const bool last_v = t == 1 || j >= other, last_k = t == 1 || j + 1 >= other;
+      arrived(&br->p_full[t][0], j & 1);
+      if (!meet()) return;
+      pv(t, j, 0, last_v);
+      arrived(&br->p_full[t][1], j & 1);
+      if (!meet()) return;
+      pv(t, j, 1, last_v);
+      if (j + 1 < n) {
+        if (t == 0 || j + 1 >= other) {  // the tile that reads the keys first
+          for (uint32_t c = 0; c < 3; c++) landed((uint32_t)(j + 1) * kUnitsPerStep + c);
+          if (!meet()) return;
+        }
+        qk(t, j + 1, last_k);
+      }
     }
   }
 }
@@ -338,15 +379,19 @@ __device__ void softmax_rows(const PrefillParams &p, Bars *br, uint32_t tmem, co
   float m = -INFINITY;  // reference, in score units
   uint64_t l0 = 0, l1 = 0;
   const uint64_t c2 = pack2(p.scale_log2, p.scale_log2);
-  for (int j = 0; j < n; j++) {
-    if (!warp_wait_ok(br, &br->s_full[t], j & 1, p.status)) return;
+  // A step; kMasked: a row may see only a part of its keys.  Two copies, since
+  // the compiler turns the comparisons of one copy into selects that every
+  // step pays.
+  auto step = [&](int j, auto masked) -> bool {
+    constexpr bool kMasked = decltype(masked)::value;
+    if (!warp_wait_ok(br, &br->s_full[t], j & 1, p.status)) return false;
     tc_fence_after();
     uint32_t s[4][32];
 #pragma unroll
     for (int c = 0; c < 4; c++) tmem_ld32(ts + 32 * c, s[c]);
     tmem_wait_ld();
-    const int here = seen - j * kKeys;  // keys of this step that the row sees
-    if (j >= st.masked && here < kKeys) {
+    if (kMasked) {
+      const int here = seen - j * kKeys;  // keys of this step that the row sees
 #pragma unroll
       for (int c = 0; c < 4; c++)
 #pragma unroll
@@ -365,7 +410,7 @@ __device__ void softmax_rows(const PrefillParams &p, Bars *br, uint32_t tmem, co
       const float alpha = move ? ex2((m - top) * p.scale_log2) : 1.f;
       if (move) m = top;
       if (j > 0) {
-        if (!warp_wait_ok(br, &br->o_done[t], (j - 1) & 1, p.status)) return;
+        if (!warp_wait_ok(br, &br->o_done[t], (j - 1) & 1, p.status)) return false;
         tc_fence_after();
         const uint64_t a2 = pack2(alpha, alpha);
         asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(l0) : "l"(a2));
@@ -410,12 +455,18 @@ __device__ void softmax_rows(const PrefillParams &p, Bars *br, uint32_t tmem, co
         pw[e] = *reinterpret_cast<uint32_t *>(&h2);
       }
       tmem_st32(ts + 32 * half, pw);
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&br->p_full[t][half]));
     }
-    tmem_wait_st();
-    tc_fence_before();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(smem_u32(&br->p_full[t]));
-  }
+    return true;
+  };
+  const int whole = min(n, st.masked);
+  for (int j = 0; j < whole; j++)
+    if (!step(j, std::false_type{})) return;
+  for (int j = whole; j < n; j++)
+    if (!step(j, std::true_type{})) return;
 
   float la, lb, lc, ld;
   unpack2(l0, la, lb);
@@ -499,7 +550,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int t = 0; t < 2; t++) {
       mbar_init(smem_u32(&br->q_full[t]), 1);
       mbar_init(smem_u32(&br->s_full[t]), 1);
-      mbar_init(smem_u32(&br->p_full[t]), 4);
+      mbar_init(smem_u32(&br->p_full[t][0]), 4);
+      mbar_init(smem_u32(&br->p_full[t][1]), 4);
       mbar_init(smem_u32(&br->o_done[t]), 1);
     }
     mbar_init(smem_u32(&br->v_look), 1);
@@ -513,13 +565,19 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = br->tmem_base, smem = smem_u32(base);
   if (warp < 8) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     softmax_rows(p, br, tmem, w, st, warp >> 2);
-  } else if (warp == 8) {
-    if (lane == 0) issue_mmas(br, smem, tmem, st, p.status);
-  } else if (warp == 9) {
-    if (lane == 0) issue_loads(&q_map, &kn_map, &kp_map, &v_map, br, smem, w, st, p.status);
   } else {
-    check_values(br, base + OFF_RING, st, lane, p.status);
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    if (warp == 8) {
+      mma_sequence<false>(br, smem, tmem, st, p.status);
+    } else if (warp == 9) {
+      if (lane == 0) issue_loads(&q_map, &kn_map, &kp_map, &v_map, br, smem, w, st, p.status);
+    } else if (warp == 10) {
+      check_values(br, base + OFF_RING, st, lane, p.status);
+    } else {
+      mma_sequence<true>(br, smem, tmem, st, p.status);
+    }
   }
   __syncthreads();
   if (*(volatile int *)&br->abort) {  // a wait gave up: let copies or MMAs still in flight land before the CTA exits
