@@ -58,6 +58,8 @@ class MlaError(RuntimeError):
 def lib():
     """The loaded C library (raises if it was never built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -110,7 +112,34 @@ def _stream(device) -> ctypes.c_void_p:
     return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
 
 
+def _call(name, dev, *args):
+    """Calls the library's function `name` with these arguments and the current
+    stream of `dev`, with that device current (entered only where it is not:
+    small calls cost what the host spends on them)."""
+    f = getattr(lib(), name)
+    if torch.cuda.current_device() == dev.index:
+        rc = f(*args, _raw_stream(dev.index))
+    else:
+        with torch.cuda.device(dev):
+            rc = f(*args, _raw_stream(dev.index))
+    if rc < 0:
+        _check(rc)
+
+
+# The current stream's handle without the Stream object around it (2 us a call).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _at(t) -> Optional[int]:
+    """A tensor's address for a pointer argument (None: NULL)."""
+    return None if t is None else t.data_ptr()
+
+
 def _need(t, name, dtype, device=None, ndim=None):
+    if (type(t) is torch.Tensor and t.dtype is dtype and t.is_cuda and t.is_contiguous()
+            and (ndim is None or t.dim() == ndim) and (device is None or t.get_device() == device.index)):
+        return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype != dtype:
@@ -379,7 +408,15 @@ def kv_insert(kv_c: torch.Tensor, k_pe: torch.Tensor, w_kva: torch.Tensor, slots
 
 def _strided(t, name, shape, dev, dtype=torch.bfloat16):
     """A bf16 CUDA tensor of this shape (None: any size) whose last axis is
-    contiguous and whose other strides are multiples of 8 elements."""
+    contiguous and whose other strides are multiples of 8 elements.  Every
+    caller's last axis is a multiple of 8."""
+    if (type(t) is torch.Tensor and t.dtype is dtype and t.is_cuda and t.is_contiguous()
+            and (dev is None or t.get_device() == dev.index) and t.dim() == len(shape)):
+        for m, n in zip(t.shape, shape):
+            if n is not None and m != n:
+                break
+        else:
+            return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype != dtype:
@@ -435,14 +472,11 @@ def kv_insert_rope(kv_c: torch.Tensor, k_pe: torch.Tensor, w_kva: torch.Tensor, 
         strides = (_ld(q_pe, 0), _ld(q_pe, 1), _ld(q_out, 0), _ld(q_out, 1))
         if q_out.data_ptr() == q_pe.data_ptr() and N and strides[:2] != strides[2:]:
             raise ValueError("q_out in q_pe's place must have its strides")
-    with torch.cuda.device(dev):
-        _check(lib().mla_kv_insert_rope(
-            _ptr(kv_c), ld_kv, _ptr(k_pe), ld_pe, _ptr(w_kva), float(eps), _ptr(slots), _ptr(positions),
-            _ptr(cos_sin), cos_sin.shape[0], int(bool(interleaved)), N,
-            _ptr(kv_cache), fmt, kv_cache.shape[0], kv_cache.shape[1],
-            _ptr(kv_scales) if fmt == KV_FP8_E4M3 else None,
-            _ptr(k_scale_inv) if fmt == KV_FP8_E4M3_TENSOR else None,
-            _ptr(q_pe), strides[0], strides[1], _ptr(q_out), strides[2], strides[3], H, _stream(dev)))
+    _call("mla_kv_insert_rope", dev, _at(kv_c), ld_kv, _at(k_pe), ld_pe, _at(w_kva), float(eps), _at(slots),
+          _at(positions), _at(cos_sin), cos_sin.shape[0], int(bool(interleaved)), N,
+          _at(kv_cache), fmt, kv_cache.shape[0], kv_cache.shape[1],
+          _at(kv_scales) if fmt == KV_FP8_E4M3 else None, _at(k_scale_inv) if fmt == KV_FP8_E4M3_TENSOR else None,
+          _at(q_pe), strides[0], strides[1], _at(q_out), strides[2], strides[3], H)
     return kv_cache, q_out
 
 
@@ -500,12 +534,9 @@ def kv_expand(kv_cache: torch.Tensor, block_table: torch.Tensor, cu_seqlens: tor
     _need(k_pe, "k_pe", torch.bfloat16, dev, 2)
     if tuple(kv.shape) != (total, H, 256) or tuple(k_pe.shape) != (total, 64):
         raise ValueError(f"kv must be [{total}, {H}, 256], k_pe [{total}, 64]")
-    with torch.cuda.device(dev):
-        _check(lib().mla_kv_expand(
-            _ptr(kv_cache), fmt, kv_cache.shape[0], kv_cache.shape[1], _ptr(block_table), block_table.shape[1],
-            _ptr(cu_seqlens), B, total, _ptr(kv_scales) if fmt != KV_BF16 else None,
-            _ptr(w_uk), w_uk.stride(1), _ld(w_uk, 0), _ptr(w_uv), w_uv.stride(1), _ld(w_uv, 0), H,
-            _ptr(kv), _ptr(k_pe), _stream(dev)))
+    _call("mla_kv_expand", dev, _at(kv_cache), fmt, kv_cache.shape[0], kv_cache.shape[1], _at(block_table),
+          block_table.shape[1], _at(cu_seqlens), B, total, _at(kv_scales) if fmt != KV_BF16 else None,
+          _at(w_uk), w_uk.stride(1), _ld(w_uk, 0), _at(w_uv), w_uv.stride(1), _ld(w_uv, 0), H, _at(kv), _at(k_pe))
     return kv, k_pe
 
 
@@ -560,11 +591,9 @@ def prefill(q: torch.Tensor, k_nope: torch.Tensor, k_pe: torch.Tensor, v: torch.
     _need(lse, "lse", torch.float32, dev, 2)
     if tuple(out.shape) != (Nq, H, 128) or tuple(lse.shape) != (H, Nq):
         raise ValueError(f"out must be [{Nq}, {H}, 128], lse [{H}, {Nq}]")
-    with torch.cuda.device(dev):
-        _check(lib().mla_prefill(
-            _ptr(q), _ld(q, 0), _ld(q, 1), _ptr(k_nope), _ld(k_nope, 0), _ld(k_nope, 1), _ptr(k_pe), _ld(k_pe, 0),
-            _ptr(v), _ld(v, 0), _ld(v, 1), _ptr(cu_seqlens_q), _ptr(cu_seqlens_k), B, H, Nq, Nk,
-            float(softmax_scale), int(bool(causal)), _ptr(out), _ptr(lse), _stream(dev)))
+    _call("mla_prefill", dev, _at(q), _ld(q, 0), _ld(q, 1), _at(k_nope), _ld(k_nope, 0), _ld(k_nope, 1), _at(k_pe),
+          _ld(k_pe, 0), _at(v), _ld(v, 0), _ld(v, 1), _at(cu_seqlens_q), _at(cu_seqlens_k), B, H, Nq, Nk,
+          float(softmax_scale), int(bool(causal)), _at(out), _at(lse))
     return out, lse
 
 
@@ -583,9 +612,8 @@ def value_project(attn: torch.Tensor, w_uv: torch.Tensor, *, out: Optional[torch
     _need(out, "out", torch.bfloat16, dev, 3)
     if tuple(out.shape) != (N, H, 128):
         raise ValueError(f"out must be [{N}, {H}, 128], got {list(out.shape)}")
-    with torch.cuda.device(dev):
-        _check(lib().mla_value_project(_ptr(attn), _ld(attn, 0), _ld(attn, 1), _ptr(w_uv), w_uv.stride(1),
-                                       _ld(w_uv, 0), N, H, _ptr(out), _stream(dev)))
+    _call("mla_value_project", dev, _at(attn), _ld(attn, 0), _ld(attn, 1), _at(w_uv), w_uv.stride(1),
+          _ld(w_uv, 0), N, H, _at(out))
     return out
 
 
