@@ -410,13 +410,14 @@ def _strided(t, name, shape, dev, dtype=torch.bfloat16):
     """A bf16 CUDA tensor of this shape (None: any size) whose last axis is
     contiguous and whose other strides are multiples of 8 elements.  Every
     caller's last axis is a multiple of 8."""
-    if (type(t) is torch.Tensor and t.dtype is dtype and t.is_cuda and t.is_contiguous()
-            and (dev is None or t.get_device() == dev.index) and t.dim() == len(shape)):
-        for m, n in zip(t.shape, shape):
-            if n is not None and m != n:
-                break
-        else:
-            return
+    if type(t) is torch.Tensor and t.dtype is dtype and t.is_cuda and (dev is None or t.get_device() == dev.index):
+        size, stride = t.shape, t.stride()
+        if len(size) == len(shape) and stride[-1] == 1 and size[-1] == shape[-1]:
+            for m, n, k in zip(size[:-1], shape, stride):
+                if (n is not None and m != n) or (k & 7 and m > 1):
+                    break
+            else:
+                return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype != dtype:

@@ -249,11 +249,19 @@ __device__ __forceinline__ void mma_sequence(Bars *br, uint32_t smem, uint32_t t
   const uint32_t ring = smem + OFF_RING;
   const int n0 = st.n[0], n1 = st.n[1];
   bool ok = true;
-  auto landed = [&](uint32_t u) {
-    if (kWaiter) ok = ok && warp_wait_ok(br, &br->full[u % kUnits], (u / kUnits) & 1, status);
-  };
-  auto arrived = [&](uint64_t *bar, uint32_t parity) {
-    if (kWaiter) ok = ok && warp_wait_ok(br, bar, parity, status);
+  const int lane = threadIdx.x & 31;
+  // up to `units` units from u on, and one barrier more, each waited for by a
+  // lane of its own (one after the other, the waits cost 60 cycles each)
+  auto wait_for = [&](uint32_t u, int units, uint64_t *bar, uint32_t parity) {
+    if (!kWaiter) return;
+    uint64_t *mine = nullptr;
+    if (lane < units) {
+      mine = &br->full[(u + lane) % kUnits];
+      parity = ((u + lane) / kUnits) & 1;
+    } else if (lane == units) {
+      mine = bar;
+    }
+    ok = __all_sync(0xffffffffu, ok && (mine == nullptr || wait_ok(br, mine, parity, status)));
   };
   auto meet = [&]() { return !bar_red_or(kMmaBar, 64, !ok); };
   // Scores of tile t for step j (units 5j .. 5j + 2).  A unit goes back to the
@@ -293,40 +301,39 @@ __device__ __forceinline__ void mma_sequence(Bars *br, uint32_t smem, uint32_t t
     __syncwarp();
   };
   if (st.most == 0) return;
-  for (uint32_t u = 0; u < 3; u++) landed(u);
   if (n0 > 0) {
-    arrived(&br->q_full[0], 0);
+    wait_for(0, 3, &br->q_full[0], 0);
     if (!meet()) return;
     qk(0, 0, n1 == 0);
   }
   if (n1 > 0) {
-    arrived(&br->q_full[1], 0);
+    wait_for(0, 3, &br->q_full[1], 0);
     if (!meet()) return;
     qk(1, 0, true);
   }
   // While a tile's softmax runs, the tensor cores work on the other tile: its
   // P V, then its next scores.
   for (int j = 0; j < st.most; j++) {
-    landed((uint32_t)j * kUnitsPerStep + 3);
-    landed((uint32_t)j * kUnitsPerStep + 4);
-    if (kWaiter && ok && j >= st.masked) {
-      if (elect_one()) mbar_arrive(smem_u32(&br->v_look));
-      arrived(&br->v_ok, (j - st.masked) & 1);
+    const uint32_t uv = (uint32_t)j * kUnitsPerStep + 3;
+    if (kWaiter && j >= st.masked) {
+      wait_for(uv, 2, nullptr, 0);
+      if (ok && elect_one()) mbar_arrive(smem_u32(&br->v_look));
+      wait_for(uv, 0, &br->v_ok, (j - st.masked) & 1);
     }
 #pragma unroll
     for (int t = 0; t < 2; t++) {
       const int n = t == 0 ? n0 : n1, other = t == 0 ? n1 : n0;
       if (j >= n) continue;
       const bool last_v = t == 1 || j >= other, last_k = t == 1 || j + 1 >= other;
-      arrived(&br->p_full[t][0], j & 1);
+      wait_for(uv, 2, &br->p_full[t][0], j & 1);
       if (!meet()) return;
       pv(t, j, 0, last_v);
-      arrived(&br->p_full[t][1], j & 1);
+      wait_for(uv, 0, &br->p_full[t][1], j & 1);
       if (!meet()) return;
       pv(t, j, 1, last_v);
       if (j + 1 < n) {
         if (t == 0 || j + 1 >= other) {  // the tile that reads the keys first
-          for (uint32_t c = 0; c < 3; c++) landed((uint32_t)(j + 1) * kUnitsPerStep + c);
+          wait_for((uint32_t)(j + 1) * kUnitsPerStep, 3, nullptr, 0);
           if (!meet()) return;
         }
         qk(t, j + 1, last_k);
