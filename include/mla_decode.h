@@ -420,6 +420,11 @@ int mla_kv_expand(const void *kv_cache, int kv_format, int num_pages, int page_s
  *                the Nq packed query rows and the Nk packed key rows.  Values
  *                outside these or out of order are clamped and set
  *                MLA_STATUS_BAD_SEQLEN.
+ *   workspace    device, >= mla_prefill_workspace_bytes(B, H, Nq, Nk) bytes,
+ *                256-byte aligned (NULL where that is 0): few queries over
+ *                many keys are split over the keys, and the parts' outputs
+ *                (fp32) meet there.  No initialisation; calls that overlap on
+ *                the GPU need separate ones.
  *   out          device bf16 [Nq][H][128], lse device fp32 [H][Nq], written;
  *                rows of no sequence are left as they were
  * Probabilities are rounded to bf16 before they multiply v; scores, sums and
@@ -427,10 +432,12 @@ int mla_kv_expand(const void *kv_cache, int kv_format, int num_pages, int page_s
  * MLA_STATUS_WAIT_TIMEOUT.  Asynchronous on `stream`; can be captured in a
  * CUDA graph.  Returns MLA_OK or a negative code.
  */
+size_t mla_prefill_workspace_bytes(int B, int H, int Nq, int Nk);
 int mla_prefill(const void *q, int64_t q_tok, int64_t q_head, const void *k_nope, int64_t k_tok, int64_t k_head,
                 const void *k_pe, int64_t pe_tok, const void *v, int64_t v_tok, int64_t v_head,
                 const int32_t *cu_seqlens_q, const int32_t *cu_seqlens_k, int B, int H, int Nq, int Nk,
-                float softmax_scale, int causal, void *out, float *lse, mla_stream_t stream);
+                float softmax_scale, int causal, void *workspace, size_t workspace_bytes, void *out, float *lse,
+                mla_stream_t stream);
 
 /*
  * Value projection: the decode's latent output rows to the 128 values a head

@@ -84,7 +84,9 @@ def lib():
                                              P, i64, i64, P, i64, i64, i, P]
             L.mla_kv_expand.argtypes = [P, i, i, i, P, i, P, i, i, P, P, i64, i64, P, i64, i64, i, P, P, P]
             L.mla_prefill.argtypes = [P, i64, i64, P, i64, i64, P, i64, P, i64, i64, P, P, i, i, i, i,
-                                      ctypes.c_float, i, P, P, P]
+                                      ctypes.c_float, i, P, sz, P, P, P]
+            L.mla_prefill_workspace_bytes.argtypes = [i, i, i, i]
+            L.mla_prefill_workspace_bytes.restype = sz
             L.mla_value_project.argtypes = [P, i64, i64, P, i64, i64, i, i, P, P]
             L.mla_query_absorb_workspace_bytes.argtypes = [i, i]
             L.mla_query_absorb_workspace_bytes.restype = sz
@@ -562,7 +564,8 @@ def _cache_format(kv_cache, kv_scales) -> int:
 
 def prefill(q: torch.Tensor, k_nope: torch.Tensor, k_pe: torch.Tensor, v: torch.Tensor, cu_seqlens_q: torch.Tensor,
             cu_seqlens_k: torch.Tensor, *, softmax_scale: float, causal: bool = True,
-            out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None):
+            workspace: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+            lse: Optional[torch.Tensor] = None):
     """Attention of prompts, or of chunks of new tokens, over expanded keys and
     values, on the current stream (mla_prefill) -> (out bf16 [Nq, H, 128], lse
     fp32 [H, Nq]).
@@ -572,7 +575,8 @@ def prefill(q: torch.Tensor, k_nope: torch.Tensor, k_pe: torch.Tensor, v: torch.
     strided); cu_seqlens_q, cu_seqlens_k int32 [B+1]: the rows of each sequence.
     causal: the last query of a sequence sees all its keys, each one before it
     one less.  A row that sees no key gets 0 and -inf.  Rows of no sequence
-    are left as they were."""
+    are left as they were.  workspace: at least prefill_workspace_bytes() bytes
+    (allocated here where it is needed and not given)."""
     _strided(q, "q", (None, None, 192), None)
     dev, (Nq, H) = q.device, q.shape[:2]
     _strided(k_nope, "k_nope", (None, H, 128), dev)
@@ -592,10 +596,23 @@ def prefill(q: torch.Tensor, k_nope: torch.Tensor, k_pe: torch.Tensor, v: torch.
     _need(lse, "lse", torch.float32, dev, 2)
     if tuple(out.shape) != (Nq, H, 128) or tuple(lse.shape) != (H, Nq):
         raise ValueError(f"out must be [{Nq}, {H}, 128], lse [{H}, {Nq}]")
+    room = prefill_workspace_bytes(B, H, Nq, Nk)
+    if workspace is None:
+        if room:
+            workspace = torch.empty(room, dtype=torch.uint8, device=dev)
+    else:
+        _need(workspace, "workspace", workspace.dtype, dev)
+        room = workspace.numel() * workspace.element_size()
     _call("mla_prefill", dev, _at(q), _ld(q, 0), _ld(q, 1), _at(k_nope), _ld(k_nope, 0), _ld(k_nope, 1), _at(k_pe),
           _ld(k_pe, 0), _at(v), _ld(v, 0), _ld(v, 1), _at(cu_seqlens_q), _at(cu_seqlens_k), B, H, Nq, Nk,
-          float(softmax_scale), int(bool(causal)), _at(out), _at(lse))
+          float(softmax_scale), int(bool(causal)), _at(workspace), room, _at(out), _at(lse))
     return out, lse
+
+
+def prefill_workspace_bytes(B: int, H: int, Nq: int, Nk: int) -> int:
+    """Workspace of prefill() for B sequences, H heads and these packed rows
+    (0: none)."""
+    return int(lib().mla_prefill_workspace_bytes(B, H, Nq, Nk))
 
 
 def value_project(attn: torch.Tensor, w_uv: torch.Tensor, *, out: Optional[torch.Tensor] = None) -> torch.Tensor:

@@ -24,6 +24,7 @@
 // not finite by zero before the MMA reads it and notes the key; rows that do
 // see such a key add its non-finite values at the end.  (A weight is positive,
 // so inf and nan reach the row's output as they are.)
+#include <cstddef>
 #include <type_traits>
 
 #include "common.cuh"
@@ -65,42 +66,58 @@ constexpr uint32_t IDESC_QK = idesc_bf16_f32(128, 128, false, false);
 constexpr uint32_t IDESC_PV = idesc_bf16_f32(128, 128, false, true);
 constexpr float kMoveAt = 8.f;
 
-struct Bars {
-  uint64_t full[kUnits], empty[kUnits];
-  uint64_t q_full[2];
-  uint64_t s_full[2];   // scores of a tile are in tensor memory
-  uint64_t p_full[2][2];  // its probabilities are: of the first and the last 64 keys
-  uint64_t o_done[2];   // its P V has been added
-  uint64_t v_look;      // the values of a masked step are there (told by the waiting warp: the ring's barriers
-                        // can be a phase further than a warp that does not follow every unit)
-  uint64_t v_ok;        // they have been looked through
-  uint32_t bad_keys[16];  // keys with a non-finite value, from the first masked step on
-  uint32_t tmem_base;
-  int abort;
-};
-constexpr uint32_t kSmem = OFF_BARS + sizeof(Bars) + 1024;
-static_assert(kSmem <= 232448, "shared memory budget");
-
 struct PrefillParams {
   const int32_t *cu_q, *cu_k;
   const __nv_bfloat16 *v;
   __nv_bfloat16 *out;  // [Nq][H][128]
   float *lse;          // [H][Nq]
+  float *part_o;       // splits > 1: [splits][Nq][H][128], normalised
+  float *part_lse;     // splits > 1: [splits][H][Nq]
   unsigned int *status;
   long long v_tok, v_head;
-  int B, H, Nq, Nk, tiles;
+  int B, H, Nq, Nk, tiles, splits;
   int causal;
   int out_v8;
   float scale, scale_log2;
 };
 
-// A CTA's work: 256 query rows of one sequence, one head.
+// A CTA's unit of work: up to 256 query rows of one sequence, one head, a
+// range of its keys.
 struct Work {
-  int q0, nq;  // first row in the packed queries, rows of this CTA (<= 256); nq = 0: nothing
-  int k0, nk;  // first key, keys of the sequence
-  int diff;    // row i of the CTA sees min(nk, max(0, diff + i + 1)) keys
-  int h;
+  int q0, nq;  // first row in the packed queries, rows (<= 256); 0: no more work
+  int k0, nk;  // first key, keys
+  int diff;    // row i sees min(nk, max(0, diff + i + 1)) of them
+  int h, split;
 };
+
+// Steps over its keys: n[t] of tile t, of which those from `masked` on hold
+// keys that some row of a tile does not see.
+struct Steps {
+  int n[2], most, masked;
+};
+
+struct Bars {
+  uint64_t full[kUnits], empty[kUnits];
+  uint64_t work_full[2], work_empty[2];
+  uint64_t q_full[2], q_empty[2];
+  uint64_t s_full[2];   // scores of a tile are in tensor memory
+  uint64_t p_full[2][2];  // its probabilities are: of the first and the last 64 keys
+  uint64_t o_done[2];   // its P V has been added
+  uint64_t o_free[2];   // its output has been read
+  uint64_t v_look;      // the values of a masked step are there (told by the waiting warp: the ring's barriers
+                        // can be a phase further than a warp that does not follow every unit)
+  uint64_t v_ok;        // they have been looked through
+  uint64_t next_full;   // the answer to a request for the next unit of work
+  uint4 next;           // (16 bytes, 16-byte aligned)
+  Work work[2];
+  Steps steps[2];
+  uint32_t bad_keys[2][16];  // keys with a non-finite value, from the first masked step on
+  uint32_t tmem_base;
+  int abort;
+};
+constexpr uint32_t kSmem = OFF_BARS + sizeof(Bars) + 1024;
+static_assert(kSmem <= 232448, "shared memory budget");
+static_assert(OFF_BARS % 16 == 0 && offsetof(Bars, next) % 16 == 0, "the answer is 16 bytes");
 
 __device__ __forceinline__ int visible(const Work &w, int i) { return min(w.nk, max(0, w.diff + i + 1)); }
 
@@ -109,6 +126,7 @@ __device__ Work find_work(const PrefillParams &p, int t, int h, int lane) {
   Work w;
   w.nq = 0;
   w.h = h;
+  w.split = 0;
   int before = 0;
   for (int b0 = 0; b0 < p.B; b0 += 32) {
     const int b = b0 + lane;
@@ -147,12 +165,6 @@ __device__ Work find_work(const PrefillParams &p, int t, int h, int lane) {
   return w;
 }
 
-// Steps over the keys: n[t] of tile t, of which those from `masked` on hold
-// keys that some row of a tile does not see.
-struct Steps {
-  int n[2], most, masked;
-};
-
 __device__ __forceinline__ Steps steps_of(const Work &w) {
   Steps s;
   s.masked = 1 << 30;
@@ -165,6 +177,16 @@ __device__ __forceinline__ Steps steps_of(const Work &w) {
   }
   s.most = max(s.n[0], s.n[1]);
   return s;
+}
+
+// The part of a work unit's steps that falls to split `i` of `splits`.
+__device__ __forceinline__ void take_split(Work &w, int i, int splits) {
+  const int most = steps_of(w).most;
+  const int from = (int)((long long)most * i / splits), to = (int)((long long)most * (i + 1) / splits);
+  w.split = i;
+  w.k0 += from * kKeys;
+  w.nk = max(0, min(w.nk - from * kKeys, (to - from) * kKeys));
+  w.diff -= from * kKeys;
 }
 
 __device__ __forceinline__ bool wait_ok(Bars *b, uint64_t *bar, uint32_t parity, unsigned int *status) {
@@ -204,34 +226,110 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   return r;
 }
 
-__device__ __forceinline__ void issue_loads(const CUtensorMap *q_map, const CUtensorMap *kn_map,
-                                            const CUtensorMap *kp_map, const CUtensorMap *v_map, Bars *br,
-                                            uint32_t smem, const Work &w, const Steps &st, unsigned int *status) {
-  const uint64_t pol = policy_evict_normal(), first = policy_evict_first();
+// Asks the hardware for a block of the grid that has not been launched yet:
+// this CTA takes over its work.  The answer arrives at `next_full`.
+__device__ __forceinline__ void ask_next(Bars *br) {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the last answer has been read
+  mbar_arrive_expect_tx(smem_u32(&br->next_full), 16);
+  asm volatile(
+      "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+          smem_u32(&br->next)),
+      "r"(smem_u32(&br->next_full))
+      : "memory");
+}
+
+// The block that was taken over, or -1 if there was none.
+__device__ __forceinline__ int next_block(Bars *br) {
+  int got, x;
+  asm volatile(
+      "{\n\t.reg .b128 h;\n\t.reg .pred p;\n\t.reg .b32 y, z, w;\n\t"
+      "ld.shared.b128 h, [%2];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\t"
+      "selp.s32 %0, 1, 0, p;\n\t"
+      "mov.s32 %1, 0;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%1, y, z, w}, h;\n\t}"
+      : "=r"(got), "=r"(x)
+      : "r"(smem_u32(&br->next))
+      : "memory");
+  return got ? x : -1;
+}
+
+// Block -> work.  Heads go in groups of eight, so that the keys and values in
+// use at a time stay in L2; within a group the last tiles, which see the most
+// keys, go first.
+constexpr int kHeadGroup = 8;
+__device__ __forceinline__ Work block_work(const PrefillParams &p, int block, int lane) {
+  const int split = block % p.splits;
+  const int i = block / p.splits;
+  const int g = i / (p.tiles * kHeadGroup), in = i % (p.tiles * kHeadGroup);
+  const int heads = min(kHeadGroup, p.H - g * kHeadGroup);
+  Work w = find_work(p, p.tiles - 1 - in / heads, g * kHeadGroup + in % heads, lane);
+  if (p.splits > 1 && w.nq > 0) take_split(w, split, p.splits);
+  return w;
+}
+
+// The load warp: finds the work, tells the others, and fetches it.
+__device__ __forceinline__ void load_work(const CUtensorMap *q_map, const CUtensorMap *kn_map,
+                                          const CUtensorMap *kp_map, const CUtensorMap *v_map, Bars *br,
+                                          uint32_t smem, const PrefillParams &p, int lane) {
+  const uint64_t pol = policy_evict_normal(), once = policy_evict_first();
+  int block = blockIdx.x;
+  uint32_t u = 0, asked = 0, count = 0, tile_count[2] = {0, 0};
+  bool ok = true;
+  auto tell = [&](const Work &w, const Steps &st) {
+    const uint32_t slot = count & 1;
+    ok = wait_ok(br, &br->work_empty[slot], ((count >> 1) & 1) ^ 1, p.status);
+    if (!ok) return;
+    br->work[slot] = w;
+    br->steps[slot] = st;
+    mbar_arrive(smem_u32(&br->work_full[slot]));
+    count++;
+  };
+  for (;;) {
+    if (lane == 0) ask_next(br);
+    const Work w = block_work(p, block, lane);
+    if (w.nq > 0 && lane == 0) {
+      const Steps st = steps_of(w);
+      tell(w, st);
 #pragma unroll
-  for (int t = 0; t < 2; t++) {
-    if (st.n[t] == 0) continue;
-    mbar_arrive_expect_tx(smem_u32(&br->q_full[t]), 3 * kUnit);
-    for (int c = 0; c < 3; c++)
-      tma_load_3d(smem + (3 * t + c) * kUnit, q_map, smem_u32(&br->q_full[t]), 64 * c, w.h, w.q0 + t * kRows, first);
-  }
-  uint32_t u = 0;
-  for (int j = 0; j < st.most; j++) {
-    const int key = w.k0 + j * kKeys;
+      for (int t = 0; t < 2; t++) {
+        if (st.n[t] == 0 || !ok) continue;
+        ok = wait_ok(br, &br->q_empty[t], (tile_count[t]++ & 1) ^ 1, p.status);
+        if (!ok) continue;
+        mbar_arrive_expect_tx(smem_u32(&br->q_full[t]), 3 * kUnit);
+        for (int c = 0; c < 3; c++)
+          tma_load_3d(smem + (3 * t + c) * kUnit, q_map, smem_u32(&br->q_full[t]), 64 * c, w.h, w.q0 + t * kRows, once);
+      }
+      for (int j = 0; j < st.most && ok; j++) {
+        const int key = w.k0 + j * kKeys;
 #pragma unroll 1
-    for (int c = 0; c < kUnitsPerStep; c++, u++) {
-      const uint32_t s = u % kUnits, full = smem_u32(&br->full[s]), dst = smem + OFF_RING + s * kUnit;
-      if (!wait_ok(br, &br->empty[s], ((u / kUnits) & 1) ^ 1, status)) return;
-      mbar_arrive_expect_tx(full, kUnit);
-      if (c < 2) {
-        tma_load_3d(dst, kn_map, full, 64 * c, w.h, key, pol);
-      } else if (c == 2) {
-        tma_load_3d(dst, kp_map, full, 0, 0, key, pol);
-      } else {
-        tma_load_3d(dst, v_map, full, 0, w.h, key + 64 * (c - 3), pol);
-        tma_load_3d(dst + kUnit / 2, v_map, full, 64, w.h, key + 64 * (c - 3), pol);
+        for (int c = 0; c < kUnitsPerStep; c++, u++) {
+          const uint32_t s = u % kUnits, full = smem_u32(&br->full[s]), dst = smem + OFF_RING + s * kUnit;
+          ok = wait_ok(br, &br->empty[s], ((u / kUnits) & 1) ^ 1, p.status);
+          if (!ok) break;
+          mbar_arrive_expect_tx(full, kUnit);
+          if (c < 2) {
+            tma_load_3d(dst, kn_map, full, 64 * c, w.h, key, pol);
+          } else if (c == 2) {
+            tma_load_3d(dst, kp_map, full, 0, 0, key, pol);
+          } else {
+            tma_load_3d(dst, v_map, full, 0, w.h, key + 64 * (c - 3), pol);
+            tma_load_3d(dst + kUnit / 2, v_map, full, 64, w.h, key + 64 * (c - 3), pol);
+          }
+        }
       }
     }
+    // (also after a wait that gave up: the answer has to land before the CTA ends)
+    const bool told = warp_wait_ok(br, &br->next_full, asked++ & 1, p.status);
+    ok = __shfl_sync(0xffffffffu, (int)ok, 0) && told;
+    block = told ? next_block(br) : -1;
+    __syncwarp();
+    if (!ok || block < 0) break;
+  }
+  if (ok && lane == 0) {
+    Work none;
+    none.nq = 0;
+    tell(none, Steps());
   }
 }
 
@@ -244,15 +342,15 @@ __device__ __forceinline__ void issue_loads(const CUtensorMap *q_map, const CUte
 constexpr uint32_t kMmaBar = 1;
 
 template <bool kWaiter>
-__device__ __forceinline__ void mma_sequence(Bars *br, uint32_t smem, uint32_t tmem, const Steps &st,
-                                             unsigned int *status) {
-  const uint32_t ring = smem + OFF_RING;
-  const int n0 = st.n[0], n1 = st.n[1];
-  bool ok = true;
+__device__ __forceinline__ void mma_sequence(Bars *br, uint32_t smem, uint32_t tmem, unsigned int *status) {
   const int lane = threadIdx.x & 31;
-  // up to `units` units from u on, and one barrier more, each waited for by a
+  const uint64_t q_desc = smem_desc_sw128(smem, 16, 1024), k_desc = smem_desc_sw128(smem + OFF_RING, 16, 1024);
+  const uint64_t v_desc = smem_desc_sw128(smem + OFF_RING, kUnit / 2, 1024);
+  bool ok = true;
+  uint32_t base = 0, masked = 0, steps[2] = {0, 0}, works[2] = {0, 0};  // units, masked steps, steps, works so far
+  // up to `units` units from u on, and two barriers more, each waited for by a
   // lane of its own (one after the other, the waits cost 60 cycles each)
-  auto wait_for = [&](uint32_t u, int units, uint64_t *bar, uint32_t parity) {
+  auto wait_for = [&](uint32_t u, int units, uint64_t *bar, uint32_t parity, uint64_t *bar2, uint32_t parity2) {
     if (!kWaiter) return;
     uint64_t *mine = nullptr;
     if (lane < units) {
@@ -260,123 +358,159 @@ __device__ __forceinline__ void mma_sequence(Bars *br, uint32_t smem, uint32_t t
       parity = ((u + lane) / kUnits) & 1;
     } else if (lane == units) {
       mine = bar;
+    } else if (lane == units + 1) {
+      mine = bar2;
+      parity = parity2;
     }
     ok = __all_sync(0xffffffffu, ok && (mine == nullptr || wait_ok(br, mine, parity, status)));
   };
-  auto meet = [&]() { return !bar_red_or(kMmaBar, 64, !ok); };
+  auto meet = [&](bool stop = false) { return !bar_red_or(kMmaBar, 64, !ok || stop); };
   // Scores of tile t for step j (units 5j .. 5j + 2).  A unit goes back to the
-  // loads after the MMAs of the last tile that reads it.
-  auto qk = [&](int t, int j, bool last) {
+  // loads after the MMAs of the last tile that reads it, Q after the last step.
+  auto qk = [&](int t, int j, bool last, bool last_q) {
     if (kWaiter) return;
     tc_fence_after();
     if (elect_one()) {
 #pragma unroll
       for (int c = 0; c < 3; c++) {
-        const uint32_t u = (uint32_t)j * kUnitsPerStep + c;
-        const uint32_t a = smem + (3 * t + c) * kUnit, b = ring + u % kUnits * kUnit;
+        const uint32_t s = (base + (uint32_t)j * kUnitsPerStep + c) % kUnits;
+        const uint64_t a = q_desc + (((3 * t + c) * kUnit) >> 4), b = k_desc + s * (kUnit >> 4);
 #pragma unroll
         for (int k = 0; k < 4; k++)
-          mma_ss(tmem + TM_S + t * 128, smem_desc_sw128(a + k * 32, 16, 1024), smem_desc_sw128(b + k * 32, 16, 1024),
-                 IDESC_QK, (c | k) ? 1u : 0u);
+          mma_ss(tmem + TM_S + t * 128, a + 2 * k, b + 2 * k, IDESC_QK, (c | k) ? 1u : 0u);
         if (c == 2) mma_commit(smem_u32(&br->s_full[t]));
-        if (last) mma_commit(smem_u32(&br->empty[u % kUnits]));
+        if (last) mma_commit(smem_u32(&br->empty[s]));
       }
+      if (last_q) mma_commit(smem_u32(&br->q_empty[t]));
     }
     __syncwarp();
   };
   // Half c of P V of tile t for step j (unit 5j + 3 + c: 64 keys).
   auto pv = [&](int t, int j, int c, bool last) {
     if (kWaiter) return;
-    const uint32_t u = (uint32_t)j * kUnitsPerStep + 3 + c;
     tc_fence_after();
     if (elect_one()) {
+      const uint32_t s = (base + (uint32_t)j * kUnitsPerStep + 3 + c) % kUnits;
+      const uint64_t b = v_desc + s * (kUnit >> 4);
 #pragma unroll
       for (int k = 0; k < 4; k++)
-        mma_ts(tmem + TM_O + t * 128, tmem + TM_S + t * 128 + c * 32 + k * 8,
-               smem_desc_sw128(ring + u % kUnits * kUnit + k * 2048, kUnit / 2, 1024), IDESC_PV,
+        mma_ts(tmem + TM_O + t * 128, tmem + TM_S + t * 128 + c * 32 + k * 8, b + k * (2048 >> 4), IDESC_PV,
                (j | c | k) ? 1u : 0u);
       if (c == 1) mma_commit(smem_u32(&br->o_done[t]));
-      if (last) mma_commit(smem_u32(&br->empty[u % kUnits]));
+      if (last) mma_commit(smem_u32(&br->empty[s]));
     }
     __syncwarp();
   };
-  if (st.most == 0) return;
-  if (n0 > 0) {
-    wait_for(0, 3, &br->q_full[0], 0);
-    if (!meet()) return;
-    qk(0, 0, n1 == 0);
-  }
-  if (n1 > 0) {
-    wait_for(0, 3, &br->q_full[1], 0);
-    if (!meet()) return;
-    qk(1, 0, true);
-  }
-  // While a tile's softmax runs, the tensor cores work on the other tile: its
-  // P V, then its next scores.
-  for (int j = 0; j < st.most; j++) {
-    const uint32_t uv = (uint32_t)j * kUnitsPerStep + 3;
-    if (kWaiter && j >= st.masked) {
-      wait_for(uv, 2, nullptr, 0);
-      if (ok && elect_one()) mbar_arrive(smem_u32(&br->v_look));
-      wait_for(uv, 0, &br->v_ok, (j - st.masked) & 1);
+  for (uint32_t count = 0;; count++) {
+    const uint32_t slot = count & 1;
+    wait_for(0, 0, &br->work_full[slot], (count >> 1) & 1, nullptr, 0);
+    const bool stop = kWaiter && ok && br->work[slot].nq == 0;
+    if (!meet(stop)) return;
+    const Steps st = br->steps[slot];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&br->work_empty[slot]));
+    const int n0 = st.n[0], n1 = st.n[1];
+    if (n0 > 0) {
+      wait_for(base, 3, &br->q_full[0], works[0] & 1, nullptr, 0);
+      if (!meet()) return;
+      qk(0, 0, n1 == 0, n0 == 1);
     }
-#pragma unroll
-    for (int t = 0; t < 2; t++) {
-      const int n = t == 0 ? n0 : n1, other = t == 0 ? n1 : n0;
-      if (j >= n) continue;
-      const bool last_v = t == 1 || j >= other, last_k = t == 1 || j + 1 >= other;
-      wait_for(uv, 2, &br->p_full[t][0], j & 1);
+    if (n1 > 0) {
+      wait_for(base, 3, &br->q_full[1], works[1] & 1, nullptr, 0);
       if (!meet()) return;
-      pv(t, j, 0, last_v);
-      wait_for(uv, 0, &br->p_full[t][1], j & 1);
-      if (!meet()) return;
-      pv(t, j, 1, last_v);
-      if (j + 1 < n) {
-        if (t == 0 || j + 1 >= other) {  // the tile that reads the keys first
-          wait_for((uint32_t)(j + 1) * kUnitsPerStep, 3, nullptr, 0);
-          if (!meet()) return;
+      qk(1, 0, true, n1 == 1);
+    }
+    // While a tile's softmax runs, the tensor cores work on the other tile:
+    // its P V, then its next scores.
+    for (int j = 0; j < st.most; j++) {
+      const uint32_t uv = base + (uint32_t)j * kUnitsPerStep + 3;
+      if (j >= st.masked) {
+        if (kWaiter) {
+          wait_for(uv, 2, nullptr, 0, nullptr, 0);
+          if (ok && elect_one()) mbar_arrive(smem_u32(&br->v_look));
+          wait_for(uv, 0, &br->v_ok, masked & 1, nullptr, 0);
         }
-        qk(t, j + 1, last_k);
+        masked++;
       }
+#pragma unroll
+      for (int t = 0; t < 2; t++) {
+        const int n = t == 0 ? n0 : n1, other = t == 0 ? n1 : n0;
+        if (j >= n) continue;
+        const bool last_v = t == 1 || j >= other, last_k = t == 1 || j + 1 >= other;
+        // the first P V of a unit of work overwrites the output of the one before
+        wait_for(uv, 2, &br->p_full[t][0], (steps[t] + j) & 1, j == 0 ? &br->o_free[t] : nullptr, (works[t] & 1) ^ 1);
+        if (!meet()) return;
+        pv(t, j, 0, last_v);
+        wait_for(uv, 0, &br->p_full[t][1], (steps[t] + j) & 1, nullptr, 0);
+        if (!meet()) return;
+        pv(t, j, 1, last_v);
+        if (j + 1 < n) {
+          if (t == 0 || j + 1 >= other) {  // the tile that reads the keys first
+            wait_for(uv + 2, 3, nullptr, 0, nullptr, 0);
+            if (!meet()) return;
+          }
+          qk(t, j + 1, last_k, j + 2 == n);
+        }
+      }
+    }
+    base += (uint32_t)st.most * kUnitsPerStep;
+    for (int t = 0; t < 2; t++) {
+      steps[t] += st.n[t];
+      works[t] += st.n[t] > 0 ? 1 : 0;
     }
   }
 }
 
 // The whole warp looks through the values of every masked step.
-__device__ void check_values(Bars *br, uint8_t *ring, const Steps &st, int lane, unsigned int *status) {
-  for (int j = st.masked; j < st.most; j++) {
-    if (!warp_wait_ok(br, &br->v_look, (j - st.masked) & 1, status)) return;
-    bool patched = false;
-    for (int c = 0; c < 2; c++) {
-      const uint32_t u = (uint32_t)j * kUnitsPerStep + 3 + c, s = u % kUnits;
-      if (!warp_wait_ok(br, &br->full[s], (u / kUnits) & 1, status)) return;
-      uint8_t *unit = ring + s * kUnit;
+__device__ __forceinline__ void check_values(Bars *br, uint8_t *ring, int lane, unsigned int *status) {
+  uint32_t base = 0, looks = 0;
+  for (uint32_t count = 0;; count++) {
+    const uint32_t slot = count & 1;
+    if (!warp_wait_ok(br, &br->work_full[slot], (count >> 1) & 1, status)) return;
+    const Steps st = br->steps[slot];
+    if (br->work[slot].nq == 0) return;
+    // (no row reads this slot's keys any more: the slot was given back after its output)
+    if (lane < 16) br->bad_keys[slot][lane] = 0;
+    __syncwarp();
+    for (int j = st.masked; j < st.most; j++) {
+      if (!warp_wait_ok(br, &br->v_look, looks++ & 1, status)) return;
+      bool patched = false;
+      for (int c = 0; c < 2; c++) {
+        const uint32_t u = base + (uint32_t)j * kUnitsPerStep + 3 + c, s = u % kUnits;
+        if (!warp_wait_ok(br, &br->full[s], (u / kUnits) & 1, status)) return;
+        uint8_t *unit = ring + s * kUnit;
 #pragma unroll 8
-      for (int i = lane; i < (int)(kUnit / 16); i += 32) {
-        uint4 v = *reinterpret_cast<const uint4 *>(unit + i * 16);
-        // a bf16 is not finite when its eight exponent bits are all set
-        auto bad = [](uint32_t x) { return (x & 0x7F80u) == 0x7F80u || (x & 0x7F800000u) == 0x7F800000u; };
-        if (bad(v.x) || bad(v.y) || bad(v.z) || bad(v.w)) {
-          auto clean = [](uint32_t x) {
-            if ((x & 0x7F80u) == 0x7F80u) x &= 0xFFFF0000u;
-            if ((x & 0x7F800000u) == 0x7F800000u) x &= 0x0000FFFFu;
-            return x;
-          };
-          *reinterpret_cast<uint4 *>(unit + i * 16) = make_uint4(clean(v.x), clean(v.y), clean(v.z), clean(v.w));
-          const int key = (j - st.masked) * kKeys + c * 64 + ((i * 16) % (int)(kUnit / 2)) / 128;
-          if (key < 512) atomicOr(&br->bad_keys[key >> 5], 1u << (key & 31));
-          patched = true;
+        for (int i = lane; i < (int)(kUnit / 16); i += 32) {
+          const uint4 v = *reinterpret_cast<const uint4 *>(unit + i * 16);
+          // a bf16 is not finite when its eight exponent bits are all set
+          auto bad = [](uint32_t x) { return (x & 0x7F80u) == 0x7F80u || (x & 0x7F800000u) == 0x7F800000u; };
+          if (bad(v.x) || bad(v.y) || bad(v.z) || bad(v.w)) {
+            auto clean = [](uint32_t x) {
+              if ((x & 0x7F80u) == 0x7F80u) x &= 0xFFFF0000u;
+              if ((x & 0x7F800000u) == 0x7F800000u) x &= 0x0000FFFFu;
+              return x;
+            };
+            *reinterpret_cast<uint4 *>(unit + i * 16) = make_uint4(clean(v.x), clean(v.y), clean(v.z), clean(v.w));
+            const int key = (j - st.masked) * kKeys + c * 64 + ((i * 16) % (int)(kUnit / 2)) / 128;
+            if (key < 512) atomicOr(&br->bad_keys[slot][key >> 5], 1u << (key & 31));
+            patched = true;
+          }
         }
       }
+      if (patched) fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&br->v_ok));
     }
-    if (patched) fence_proxy_async_smem();
+    base += (uint32_t)st.most * kUnitsPerStep;
     __syncwarp();
-    if (lane == 0) mbar_arrive(smem_u32(&br->v_ok));
+    if (lane == 0) mbar_arrive(smem_u32(&br->work_empty[slot]));
   }
 }
 
-// One row a thread: the softmax of tile t over its steps, then its output.
-__device__ void softmax_rows(const PrefillParams &p, Bars *br, uint32_t tmem, const Work &w, const Steps &st, int t) {
+// One row a thread: the softmax of tile t over the steps of one unit of work,
+// then its output.  done: the tile's steps before this unit.
+__device__ __forceinline__ bool softmax_work(const PrefillParams &p, Bars *br, uint32_t tmem, const Work &w,
+                                             const Steps &st, const uint32_t *bad_keys, int t, uint32_t done) {
   const int warp = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
   const int i = t * kRows + warp * 32 + lane;  // the CTA's row
   const int seen = visible(w, i);
@@ -391,7 +525,7 @@ __device__ void softmax_rows(const PrefillParams &p, Bars *br, uint32_t tmem, co
   // step pays.
   auto step = [&](int j, auto masked) -> bool {
     constexpr bool kMasked = decltype(masked)::value;
-    if (!warp_wait_ok(br, &br->s_full[t], j & 1, p.status)) return false;
+    if (!warp_wait_ok(br, &br->s_full[t], (done + j) & 1, p.status)) return false;
     tc_fence_after();
     uint32_t s[4][32];
 #pragma unroll
@@ -417,7 +551,7 @@ __device__ void softmax_rows(const PrefillParams &p, Bars *br, uint32_t tmem, co
       const float alpha = move ? ex2((m - top) * p.scale_log2) : 1.f;
       if (move) m = top;
       if (j > 0) {
-        if (!warp_wait_ok(br, &br->o_done[t], (j - 1) & 1, p.status)) return false;
+        if (!warp_wait_ok(br, &br->o_done[t], (done + j - 1) & 1, p.status)) return false;
         tc_fence_after();
         const uint64_t a2 = pack2(alpha, alpha);
         asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(l0) : "l"(a2));
@@ -471,26 +605,27 @@ __device__ void softmax_rows(const PrefillParams &p, Bars *br, uint32_t tmem, co
   };
   const int whole = min(n, st.masked);
   for (int j = 0; j < whole; j++)
-    if (!step(j, std::false_type{})) return;
+    if (!step(j, std::false_type{})) return false;
   for (int j = whole; j < n; j++)
-    if (!step(j, std::true_type{})) return;
+    if (!step(j, std::true_type{})) return false;
 
   float la, lb, lc, ld;
   unpack2(l0, la, lb);
   unpack2(l1, lc, ld);
   const float l = (la + lb) + (lc + ld);
-  const bool live = i < w.nq;
+  const bool live = i < w.nq, none = seen == 0;
   if (n > 0) {
-    if (!warp_wait_ok(br, &br->o_done[t], (n - 1) & 1, p.status)) return;
+    if (!warp_wait_ok(br, &br->o_done[t], (done + n - 1) & 1, p.status)) return false;
     tc_fence_after();
   }
-  const bool none = live && seen == 0;
   const float inv = l != 0.f ? 1.f / l : 0.f;
   // do masked steps hold non-finite values?
   bool bad = false;
   if (n > 0 && st.masked < st.most)
-    for (int k = 0; k < 16; k++) bad |= *(volatile uint32_t *)&br->bad_keys[k] != 0;
-  __nv_bfloat16 *dst = p.out + ((size_t)(w.q0 + i) * p.H + w.h) * kDv;
+    for (int k = 0; k < 16; k++) bad |= *(volatile const uint32_t *)&bad_keys[k] != 0;
+  const size_t row = w.q0 + i;
+  __nv_bfloat16 *dst = p.out + (row * p.H + w.h) * kDv;
+  float *part = p.part_o + ((w.split * (size_t)p.Nq + row) * p.H + w.h) * kDv;
 #pragma unroll 1
   for (int c = 0; c < 4; c++) {
     uint32_t o[32];
@@ -499,12 +634,22 @@ __device__ void softmax_rows(const PrefillParams &p, Bars *br, uint32_t tmem, co
       tmem_wait_ld();
     }
     if (!live) continue;
+#pragma unroll
+    for (int e = 0; e < 32; e++) o[e] = none ? 0u : __float_as_uint(__uint_as_float(o[e]) * inv);
+    if (p.splits > 1) {
+#pragma unroll
+      for (int k = 0; k < 4; k++) {
+        const uint32_t a8[8] = {o[8 * k],     o[8 * k + 1], o[8 * k + 2], o[8 * k + 3],
+                                o[8 * k + 4], o[8 * k + 5], o[8 * k + 6], o[8 * k + 7]};
+        st_global_v8(part + 32 * c + 8 * k, a8);
+      }
+      continue;
+    }
     uint32_t r[16];
 #pragma unroll
-    for (int e = 0; e < 32; e += 2) {
-      float a = none ? 0.f : __uint_as_float(o[e]) * inv, b = none ? 0.f : __uint_as_float(o[e + 1]) * inv;
-      __nv_bfloat162 h2 = __floats2bfloat162_rn(a, b);
-      r[e >> 1] = *reinterpret_cast<uint32_t *>(&h2);
+    for (int e = 0; e < 16; e++) {
+      __nv_bfloat162 h2 = __floats2bfloat162_rn(__uint_as_float(o[2 * e]), __uint_as_float(o[2 * e + 1]));
+      r[e] = *reinterpret_cast<uint32_t *>(&h2);
     }
     if (p.out_v8) {
       const uint32_t a8[8] = {r[0], r[1], r[2], r[3], r[4], r[5], r[6], r[7]};
@@ -517,19 +662,85 @@ __device__ void softmax_rows(const PrefillParams &p, Bars *br, uint32_t tmem, co
         reinterpret_cast<uint4 *>(dst + 32 * c)[k] = make_uint4(r[4 * k], r[4 * k + 1], r[4 * k + 2], r[4 * k + 3]);
     }
   }
+  if (n > 0) {  // the MMA warp may start the next unit's output
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&br->o_free[t]));
+  }
   if (live && bad) {  // rare: add the non-finite values of the keys that this row sees
     for (int k = 0; k < 512; k++) {
-      if (!((*(volatile uint32_t *)&br->bad_keys[k >> 5] >> (k & 31)) & 1u)) continue;
+      if (!((*(volatile const uint32_t *)&bad_keys[k >> 5] >> (k & 31)) & 1u)) continue;
       const int key = st.masked * kKeys + k;
       if (key >= seen) continue;
       const __nv_bfloat16 *vr = p.v + (size_t)(w.k0 + key) * p.v_tok + (size_t)w.h * p.v_head;
       for (int d = 0; d < kDv; d++) {
         const float x = __bfloat162float(vr[d]);
-        if (!(fabsf(x) < INFINITY)) dst[d] = __float2bfloat16_rn(__bfloat162float(dst[d]) + x);
+        if (fabsf(x) < INFINITY) continue;
+        if (p.splits > 1) part[d] += x;
+        else dst[d] = __float2bfloat16_rn(__bfloat162float(dst[d]) + x);
       }
     }
   }
-  if (live) p.lse[(size_t)w.h * p.Nq + w.q0 + i] = none ? -INFINITY : m * p.scale + logf(l);
+  if (live) {
+    const float lse = none ? -INFINITY : m * p.scale + logf(l);
+    if (p.splits > 1) p.part_lse[((size_t)w.split * p.H + w.h) * p.Nq + row] = lse;
+    else p.lse[(size_t)w.h * p.Nq + row] = lse;
+  }
+  return true;
+}
+
+__device__ __forceinline__ void softmax_rows(const PrefillParams &p, Bars *br, uint32_t tmem, int t) {
+  uint32_t done = 0;
+  for (uint32_t count = 0;; count++) {
+    const uint32_t slot = count & 1;
+    if (!warp_wait_ok(br, &br->work_full[slot], (count >> 1) & 1, p.status)) return;
+    const Work w = br->work[slot];
+    if (w.nq == 0) return;
+    const Steps st = br->steps[slot];
+    if (!softmax_work(p, br, tmem, w, st, br->bad_keys[slot], t, done)) return;
+    done += t == 0 ? st.n[0] : st.n[1];
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(smem_u32(&br->work_empty[slot]));
+  }
+}
+
+// Splits joined: one warp a row and head, four values a lane.
+__global__ void __launch_bounds__(256) prefill_join_kernel(PrefillParams p) {
+  const int lane = threadIdx.x & 31;
+  const long long i = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+  if (i >= (long long)p.Nq * p.H) return;
+  const int row = (int)(i / p.H), h = (int)(i % p.H);
+  int lo = 0, hi = p.B;  // the last sequence that starts at or before the row
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (__ldg(p.cu_q + mid) <= row) lo = mid; else hi = mid;
+  }
+  if (row < __ldg(p.cu_q + lo) || row >= __ldg(p.cu_q + lo + 1)) return;  // of no sequence
+  const float mine = lane < p.splits ? p.part_lse[((size_t)lane * p.H + h) * p.Nq + row] : -INFINITY;
+  // (a nan among them has to stay one: not through fmaxf alone)
+  float m = mine;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  const float weight = mine == -INFINITY ? 0.f : expf(mine - m);
+  float sum = weight;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int s = 0; s < p.splits; s++) {
+    if (__shfl_sync(0xffffffffu, mine, s) == -INFINITY) continue;  // no keys
+    const float ws = __shfl_sync(0xffffffffu, weight, s);
+    const float4 v = *reinterpret_cast<const float4 *>(p.part_o + ((s * (size_t)p.Nq + row) * p.H + h) * kDv + 4 * lane);
+    acc.x += ws * v.x;
+    acc.y += ws * v.y;
+    acc.z += ws * v.z;
+    acc.w += ws * v.w;
+  }
+  const bool none = sum == 0.f;
+  const float inv = none ? 0.f : 1.f / sum;
+  __nv_bfloat162 a = __floats2bfloat162_rn(acc.x * inv, acc.y * inv), b = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
+  uint2 r = make_uint2(*reinterpret_cast<uint32_t *>(&a), *reinterpret_cast<uint32_t *>(&b));
+  *reinterpret_cast<uint2 *>(p.out + (size_t)i * kDv + 4 * lane) = r;
+  if (lane == 0) p.lse[(size_t)h * p.Nq + row] = none ? -INFINITY : m + logf(sum);
 }
 
 __global__ void __launch_bounds__(kThreads, 1)
@@ -540,11 +751,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t *base = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   Bars *br = reinterpret_cast<Bars *>(base + OFF_BARS);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  // the last tiles of a sequence see the most keys: they go first
-  const int tile = p.tiles - 1 - (int)(blockIdx.x % (unsigned)p.tiles);
-  const Work w = find_work(p, tile, (int)(blockIdx.x / (unsigned)p.tiles), lane);
-  if (w.nq == 0) return;  // (the same for every thread of the CTA)
-  const Steps st = steps_of(w);
   if (warp == 0) {
     tmem_alloc(smem_u32(&br->tmem_base), 512);
     tmem_relinquish();
@@ -555,15 +761,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(smem_u32(&br->empty[s]), 1);
     }
     for (int t = 0; t < 2; t++) {
+      mbar_init(smem_u32(&br->work_full[t]), 1);
+      mbar_init(smem_u32(&br->work_empty[t]), 11);  // softmax warps, MMA warp and its waiter, value check
       mbar_init(smem_u32(&br->q_full[t]), 1);
+      mbar_init(smem_u32(&br->q_empty[t]), 1);
       mbar_init(smem_u32(&br->s_full[t]), 1);
       mbar_init(smem_u32(&br->p_full[t][0]), 4);
       mbar_init(smem_u32(&br->p_full[t][1]), 4);
       mbar_init(smem_u32(&br->o_done[t]), 1);
+      mbar_init(smem_u32(&br->o_free[t]), 4);
     }
     mbar_init(smem_u32(&br->v_look), 1);
     mbar_init(smem_u32(&br->v_ok), 1);
-    for (int k = 0; k < 16; k++) br->bad_keys[k] = 0;
+    mbar_init(smem_u32(&br->next_full), 1);
     br->abort = 0;
     fence_mbar_init_cluster();
   }
@@ -573,17 +783,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = br->tmem_base, smem = smem_u32(base);
   if (warp < 8) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
-    softmax_rows(p, br, tmem, w, st, warp >> 2);
+    softmax_rows(p, br, tmem, warp >> 2);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     if (warp == 8) {
-      mma_sequence<false>(br, smem, tmem, st, p.status);
+      mma_sequence<false>(br, smem, tmem, p.status);
     } else if (warp == 9) {
-      if (lane == 0) issue_loads(&q_map, &kn_map, &kp_map, &v_map, br, smem, w, st, p.status);
+      load_work(&q_map, &kn_map, &kp_map, &v_map, br, smem, p, lane);
     } else if (warp == 10) {
-      check_values(br, base + OFF_RING, st, lane, p.status);
+      check_values(br, base + OFF_RING, lane, p.status);
     } else {
-      mma_sequence<true>(br, smem, tmem, st, p.status);
+      mma_sequence<true>(br, smem, tmem, p.status);
     }
   }
   __syncthreads();
@@ -608,10 +818,45 @@ int fail(int code, const char *msg) {
 }  // namespace
 }  // namespace mla
 
+namespace mla {
+namespace {
+
+// 256 rows a tile: at most one tile that is not full for each sequence.
+long long tiles_of(int B, int Nq) { return Nq < B ? Nq : (Nq - B) / kCtaRows + (long long)B; }
+
+// Few tiles over long keys: each tile's keys are split, as far as that fills
+// the 152 SMs and leaves every part at least four steps of 128 keys (of a
+// sequence of average length).  8 heads, 200 queries on 12200 keys: 8 parts of
+// 96 steps or 152 of 5.
+constexpr int kSms = 152;
+constexpr int kMaxSplits = 32;  // a lane each in the join
+int splits_of(int B, int H, int Nq, int Nk) {
+  const long long works = tiles_of(B, Nq) * H;
+  if (B < 1 || works < 1 || 2 * works > kSms) return 1;
+  const long long parts = (long long)Nk / B / (4 * kKeys);
+  long long s = kSms / works;
+  if (s > parts) s = parts;
+  if (s > kMaxSplits) s = kMaxSplits;
+  return s < 2 ? 1 : (int)s;
+}
+
+size_t lse_bytes(int splits, int H, int Nq) { return ((size_t)splits * H * Nq * 4 + 255) / 256 * 256; }
+
+}  // namespace
+}  // namespace mla
+
+size_t mla_prefill_workspace_bytes(int B, int H, int Nq, int Nk) {
+  using namespace mla;
+  if (B < 0 || H < 1 || H > MLA_MAX_HEADS || Nq < 0 || Nk < 0) return 0;
+  const int s = splits_of(B, H, Nq, Nk);
+  return s == 1 ? 0 : lse_bytes(s, H, Nq) + (size_t)s * Nq * H * kDv * 4;
+}
+
 int mla_prefill(const void *q, int64_t q_tok, int64_t q_head, const void *k_nope, int64_t k_tok, int64_t k_head,
                 const void *k_pe, int64_t pe_tok, const void *v, int64_t v_tok, int64_t v_head,
                 const int32_t *cu_seqlens_q, const int32_t *cu_seqlens_k, int B, int H, int Nq, int Nk,
-                float softmax_scale, int causal, void *out, float *lse, mla_stream_t stream) {
+                float softmax_scale, int causal, void *workspace, size_t workspace_bytes, void *out, float *lse,
+                mla_stream_t stream) {
   using namespace mla;
   if (B < 0 || Nq < 0 || Nk < 0) return fail(MLA_ERR_INVALID_ARG, "B, Nq and Nk must be >= 0");
   if (B > (1 << 20) || Nq > (1 << 30) || Nk > (1 << 30))
@@ -636,9 +881,13 @@ int mla_prefill(const void *q, int64_t q_tok, int64_t q_head, const void *k_nope
     return fail(MLA_ERR_INVALID_ARG, "q, k_nope, k_pe, v and out must be 16-byte aligned");
   if (!al(cu_seqlens_q, 4) || !al(cu_seqlens_k, 4) || !al(lse, 4))
     return fail(MLA_ERR_INVALID_ARG, "int32 and fp32 arrays must be 4-byte aligned");
-  // 256 rows a tile: at most one tile that is not full for each sequence
-  const long long tiles = Nq < B ? Nq : (Nq - B) / kCtaRows + (long long)B;
-  if (tiles * H > 0x7FFFFFFFll) return fail(MLA_ERR_UNSUPPORTED, "too many query tiles");
+  const size_t need = mla_prefill_workspace_bytes(B, H, Nq, Nk);
+  if (need > 0 && (!workspace || workspace_bytes < need))
+    return fail(MLA_ERR_WORKSPACE, "workspace smaller than mla_prefill_workspace_bytes(B, H, Nq, Nk)");
+  if (need > 0 && !al(workspace, 256)) return fail(MLA_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+  const long long tiles = tiles_of(B, Nq);
+  const int splits = splits_of(B, H, Nq, Nk);
+  if (tiles * H * splits > 0x7FFFFFFFll) return fail(MLA_ERR_UNSUPPORTED, "too many query tiles");
   CUtensorMap q_map, kn_map, kp_map, v_map;
   bool ok = make_map_3d(&q_map, q, kHead, H, Nq, q_head, q_tok, 1, kRows);
   if (Nk > 0) {
@@ -663,13 +912,19 @@ int mla_prefill(const void *q, int64_t q_tok, int64_t q_head, const void *k_nope
   p.Nq = Nq;
   p.Nk = Nk;
   p.tiles = (int)tiles;
+  p.splits = splits;
+  p.part_lse = static_cast<float *>(workspace);
+  p.part_o = splits > 1 ? p.part_lse + lse_bytes(splits, H, Nq) / 4 : nullptr;
   p.causal = causal;
   p.out_v8 = al(out, 32) ? 1 : 0;
   p.scale = softmax_scale;
   p.scale_log2 = softmax_scale * LOG2E;
   cudaError_t e = cudaFuncSetAttribute(prefill_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
   if (e != cudaSuccess) return fail(MLA_ERR_CUDA, cudaGetErrorString(e));
-  prefill_kernel<<<(unsigned)(tiles * H), kThreads, kSmem, (cudaStream_t)stream>>>(q_map, kn_map, kp_map, v_map, p);
+  prefill_kernel<<<(unsigned)(tiles * H * splits), kThreads, kSmem, (cudaStream_t)stream>>>(q_map, kn_map, kp_map,
+                                                                                              v_map, p);
+  if (splits > 1)
+    prefill_join_kernel<<<(unsigned)(((long long)Nq * H + 7) / 8), 256, 0, (cudaStream_t)stream>>>(p);
   e = cudaGetLastError();
   if (e != cudaSuccess) return fail(MLA_ERR_CUDA, cudaGetErrorString(e));
   set_last_error("");

@@ -40,6 +40,55 @@ def test_prefill(nq, nk, H, causal):
     assert mla.device_status() == 0
 
 
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("nq,nk,H", [([200], [2200], 2), ([1], [5000], 1), ([3, 130], [40, 4100], 2), ([260], [4099], 1),
+                                     ([300, 5], [100, 6000], 3), ([9, 0, 2], [1, 2, 9000], 1)])
+def test_few_queries_over_long_keys(nq, nk, H, causal):
+    """These are split over the keys; parts without keys of a row among them."""
+    import mla_decode_attention_05_gb300 as mla
+    assert mla.prefill_workspace_bytes(len(nq), H, sum(nq), sum(nk)) > 0
+    ins = _inputs(nq, nk, H, 300 + sum(nq) + sum(nk))
+    mla.device_status()
+    out, lse = mla.prefill(*ins, cu(nq), cu(nk), softmax_scale=SCALE, causal=causal)
+    _check(out, lse, ins, nq, nk, causal)
+    assert mla.device_status() == 0
+    # values that are not finite, in and behind what rows see; rows of no sequence
+    ins[3][-2, 0, 5] = float("inf")
+    ins[3][3, 0, 7] = float("nan")
+    o2 = torch.full((sum(nq) + 3, H, 128), 9.0, dtype=torch.bfloat16, device="cuda")
+    l2 = torch.full((H, sum(nq) + 3), 9.0, device="cuda")
+    q2 = torch.cat([ins[0], ins[0].new_ones((3, H, 192))])
+    mla.prefill(q2, *ins[1:], cu(nq), cu(nk), softmax_scale=SCALE, causal=causal, out=o2, lse=l2)
+    assert bool((o2[sum(nq):] == 9).all()) and bool((l2[:, sum(nq):] == 9).all())
+    assert torch.equal(l2[:, :sum(nq)], lse)
+    hit = torch.zeros_like(out, dtype=torch.bool)
+    at, kt = np.cumsum([0] + nq), np.cumsum([0] + nk)
+    for key, d in ((sum(nk) - 2, 5), (3, 7)):
+        b = int(np.searchsorted(kt, key, side="right")) - 1
+        first = max(0, key - int(kt[b]) - nk[b] + nq[b]) if causal else 0
+        hit[at[b] + first:at[b + 1], 0, d] = True
+    assert not bool(o2[:sum(nq)][hit].isfinite().any()) and torch.equal(o2[:sum(nq)][~hit], out[~hit])
+
+
+def test_many_units_of_work():
+    """More tiles than SMs, so that a block takes over the work of others; a
+    given workspace."""
+    import mla_decode_attention_05_gb300 as mla
+    nq, nk, H = [513, 40, 0, 300, 257, 1, 700] * 3, [513, 100, 5, 290, 600, 1, 900] * 3, 12
+    ins = _inputs(nq, nk, H, 18, 1.0)
+    mla.device_status()
+    out, lse = mla.prefill(*ins, cu(nq), cu(nk), softmax_scale=SCALE, workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))
+    assert mla.device_status() == 0
+    at, kt = np.cumsum([0] + nq), np.cumsum([0] + nk)
+    for b, heads in ((0, (0, 11)), (8, (5,)), (10, (7,)), (20, (3, 8)), (18, (9,)), (19, (0,))):
+        s, k = slice(at[b], at[b + 1]), slice(kt[b], kt[b + 1])
+        h = list(heads)
+        part = [ins[0][s, h], ins[1][k, h], ins[2][k], ins[3][k, h]]
+        _check(out[s, h], lse[h, s], part, [nq[b]], [nk[b]], True)
+    again = mla.prefill(*ins, cu(nq), cu(nk), softmax_scale=SCALE)
+    assert torch.equal(again[0], out) and torch.equal(again[1], lse)
+
+
 @pytest.mark.parametrize("q_std,scale", [(0.01, SCALE), (30.0, SCALE), (1.0, 1.5)])
 def test_flat_and_sharp_scores(q_std, scale):
     """Scores that grow along the keys move the reference many times."""

@@ -69,16 +69,29 @@ def test_expand_arguments(L, args, code):
     (dict(v_head=132), -1), (dict(pe_tok=32), -1), (dict(q=None), -1), (dict(q=264), -1), (dict(out=8), -1),
     (dict(lse=2), -1), (dict(cq=None), -1), (dict(ck=257), -1), (dict(kn=None), -1), (dict(vv=264), -1),
     (dict(Nq=0, q=None, out=None, lse=None), 0), (dict(B=0), 0),
+    (dict(B=1, Nk=9000, ws=None), -3), (dict(B=1, Nk=9000, ws_bytes=1000), -3), (dict(B=1, Nk=9000, ws=128), -1),
 ])
 def test_prefill_arguments(L, args, code):
     a = dict(q=256, q_tok=768, q_head=192, kn=256, k_tok=1024, k_head=256, pe=256, pe_tok=64, vv=256, v_tok=1024,
-             v_head=256, cq=256, ck=256, B=2, H=4, Nq=10, Nk=20, scale=0.07, causal=1, out=256, lse=256)
+             v_head=256, cq=256, ck=256, B=2, H=4, Nq=10, Nk=20, scale=0.07, causal=1, out=256, lse=256, ws=256,
+             ws_bytes=1 << 30)
     a.update(args)
     rc = L.mla_prefill(v(a["q"]), a["q_tok"], a["q_head"], v(a["kn"]), a["k_tok"], a["k_head"], v(a["pe"]), a["pe_tok"],
                        v(a["vv"]), a["v_tok"], a["v_head"], v(a["cq"]), v(a["ck"]), a["B"], a["H"], a["Nq"], a["Nk"],
-                       a["scale"], a["causal"], v(a["out"]), v(a["lse"]), None)
+                       a["scale"], a["causal"], v(a["ws"]), a["ws_bytes"], v(a["out"]), v(a["lse"]), None)
     assert rc == code
     assert bool(L.mla_last_error_string()) == (code != 0)
+
+
+def test_prefill_workspace(L):
+    """Few query tiles over long keys are split over the keys, others not."""
+    import mla_decode_attention_05_gb300 as m
+    assert m.prefill_workspace_bytes(1, 128, 256, 100000) == 0      # 128 tiles
+    assert m.prefill_workspace_bytes(1, 8, 200, 500) == 0           # short keys
+    n = m.prefill_workspace_bytes(1, 8, 200, 12200)
+    assert n == 19 * 200 * 8 * 129 * 4 + (-(19 * 200 * 8 * 4) % 256)
+    assert m.prefill_workspace_bytes(1, 1, 1, 1 << 30) == 32 * 128 * 4 + 256
+    assert m.prefill_workspace_bytes(0, 8, 0, 0) == 0 and m.prefill_workspace_bytes(1, 0, 5, 5) == 0
 
 
 @pytest.mark.parametrize("args,code", [
