@@ -479,22 +479,46 @@ __device__ __forceinline__ void check_values(Bars *br, uint8_t *ring, int lane, 
         const uint32_t u = base + (uint32_t)j * kUnitsPerStep + 3 + c, s = u % kUnits;
         if (!warp_wait_ok(br, &br->full[s], (u / kUnits) & 1, status)) return;
         uint8_t *unit = ring + s * kUnit;
-#pragma unroll 8
-        for (int i = lane; i < (int)(kUnit / 16); i += 32) {
-          const uint4 v = *reinterpret_cast<const uint4 *>(unit + i * 16);
-          // a bf16 is not finite when its eight exponent bits are all set
-          auto bad = [](uint32_t x) { return (x & 0x7F80u) == 0x7F80u || (x & 0x7F800000u) == 0x7F800000u; };
-          if (bad(v.x) || bad(v.y) || bad(v.z) || bad(v.w)) {
-            auto clean = [](uint32_t x) {
-              if ((x & 0x7F80u) == 0x7F80u) x &= 0xFFFF0000u;
-              if ((x & 0x7F800000u) == 0x7F800000u) x &= 0x0000FFFFu;
-              return x;
-            };
-            *reinterpret_cast<uint4 *>(unit + i * 16) = make_uint4(clean(v.x), clean(v.y), clean(v.z), clean(v.w));
-            const int key = (j - st.masked) * kKeys + c * 64 + ((i * 16) % (int)(kUnit / 2)) / 128;
-            if (key < 512) atomicOr(&br->bad_keys[slot][key >> 5], 1u << (key & 31));
-            patched = true;
+        // x * 0 summed up stays 0, unless some x is not finite: then it is nan
+        uint32_t sum[4] = {0u, 0u, 0u, 0u};
+#pragma unroll 1
+        for (int i = lane; i < (int)(kUnit / 16); i += 32 * 8) {
+          uint4 v[8];
+#pragma unroll
+          for (int k = 0; k < 8; k++) v[k] = *reinterpret_cast<const uint4 *>(unit + (i + 32 * k) * 16);
+#pragma unroll
+          for (int k = 0; k < 8; k++) {
+            const uint32_t x[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+#pragma unroll
+            for (int e = 0; e < 4; e++) asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(sum[e]) : "r"(x[e]), "r"(0u));
           }
+        }
+        bool some = false;
+#pragma unroll
+        for (int e = 0; e < 4; e++) some |= (sum[e] & 0x7FFF7FFFu) != 0;
+        if (!some) continue;
+#pragma unroll 1
+        for (int i = lane; i < (int)(kUnit / 16); i += 32) {  // (this lane's part again)
+          uint32_t x[4];
+          bool bad = false;
+#pragma unroll
+          for (int e = 0; e < 4; e++) {
+            x[e] = reinterpret_cast<const uint32_t *>(unit + i * 16)[e];
+            // a bf16 is not finite when its eight exponent bits are all set
+            if ((x[e] & 0x7F80u) == 0x7F80u) {
+              x[e] &= 0xFFFF0000u;
+              bad = true;
+            }
+            if ((x[e] & 0x7F800000u) == 0x7F800000u) {
+              x[e] &= 0x0000FFFFu;
+              bad = true;
+            }
+          }
+          if (!bad) continue;
+          *reinterpret_cast<uint4 *>(unit + i * 16) = make_uint4(x[0], x[1], x[2], x[3]);
+          const int key = (j - st.masked) * kKeys + c * 64 + ((i * 16) % (int)(kUnit / 2)) / 128;
+          if (key < 512) atomicOr(&br->bad_keys[slot][key >> 5], 1u << (key & 31));
+          patched = true;
         }
       }
       if (patched) fence_proxy_async_smem();
