@@ -25,7 +25,6 @@
 // see such a key add its non-finite values at the end.  (A weight is positive,
 // so inf and nan reach the row's output as they are.)
 #include <cstddef>
-#include <type_traits>
 
 #include "common.cuh"
 #include "ptx.cuh"
@@ -544,24 +543,25 @@ __device__ __forceinline__ bool softmax_work(const PrefillParams &p, Bars *br, u
   float m = -INFINITY;  // reference, in score units
   uint64_t l0 = 0, l1 = 0;
   const uint64_t c2 = pack2(p.scale_log2, p.scale_log2);
-  // A step; kMasked: a row may see only a part of its keys.  Two copies, since
-  // the compiler turns the comparisons of one copy into selects that every
-  // step pays.
-  auto step = [&](int j, auto masked) -> bool {
-    constexpr bool kMasked = decltype(masked)::value;
+  const int low = __shfl_sync(0xffffffffu, seen, 0);  // the fewest keys of the warp's rows
+  for (int j = 0; j < n; j++) {
     if (!warp_wait_ok(br, &br->s_full[t], (done + j) & 1, p.status)) return false;
     tc_fence_after();
     uint32_t s[4][32];
 #pragma unroll
     for (int c = 0; c < 4; c++) tmem_ld32(ts + 32 * c, s[c]);
     tmem_wait_ld();
-    if (kMasked) {
-      const int here = seen - j * kKeys;  // keys of this step that the row sees
+    if (low < (j + 1) * kKeys) {  // some row sees only a part of these keys
 #pragma unroll
-      for (int c = 0; c < 4; c++)
+      for (int c = 0; c < 4; c++) {
+        const int here = seen - j * kKeys - 32 * c;
+        if (low - j * kKeys - 32 * c < 32) {  // (the same for the whole warp)
+          const uint32_t keep = here <= 0 ? 0u : here >= 32 ? 0xFFFFFFFFu : (1u << here) - 1u;
 #pragma unroll
-        for (int e = 0; e < 32; e++)
-          if (32 * c + e >= here) s[c][e] = 0xFF800000u;
+          for (int e = 0; e < 32; e++)
+            if (!((keep >> e) & 1u)) s[c][e] = 0xFF800000u;
+        }
+      }
     }
     float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
@@ -625,13 +625,7 @@ __device__ __forceinline__ bool softmax_work(const PrefillParams &p, Bars *br, u
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&br->p_full[t][half]));
     }
-    return true;
-  };
-  const int whole = min(n, st.masked);
-  for (int j = 0; j < whole; j++)
-    if (!step(j, std::false_type{})) return false;
-  for (int j = whole; j < n; j++)
-    if (!step(j, std::true_type{})) return false;
+  }
 
   float la, lb, lc, ld;
   unpack2(l0, la, lb);
