@@ -273,7 +273,7 @@ __device__ __forceinline__ void load_work(const CUtensorMap *q_map, const CUtens
                                           uint32_t smem, const PrefillParams &p, int lane) {
   const uint64_t pol = policy_evict_normal(), once = policy_evict_first();
   int block = blockIdx.x;
-  uint32_t u = 0, asked = 0, count = 0, tile_count[2] = {0, 0};
+  uint32_t u = 0, asked = 0, count = 0, tiles0 = 0, tiles1 = 0;
   bool ok = true;
   auto tell = [&](const Work &w, const Steps &st) {
     const uint32_t slot = count & 1;
@@ -293,7 +293,7 @@ __device__ __forceinline__ void load_work(const CUtensorMap *q_map, const CUtens
 #pragma unroll
       for (int t = 0; t < 2; t++) {
         if (st.n[t] == 0 || !ok) continue;
-        ok = wait_ok(br, &br->q_empty[t], (tile_count[t]++ & 1) ^ 1, p.status);
+        ok = wait_ok(br, &br->q_empty[t], ((t == 0 ? tiles0++ : tiles1++) & 1) ^ 1, p.status);
         if (!ok) continue;
         mbar_arrive_expect_tx(smem_u32(&br->q_full[t]), 3 * kUnit);
         for (int c = 0; c < 3; c++)
@@ -346,7 +346,7 @@ __device__ __forceinline__ void mma_sequence(Bars *br, uint32_t smem, uint32_t t
   const uint64_t q_desc = smem_desc_sw128(smem, 16, 1024), k_desc = smem_desc_sw128(smem + OFF_RING, 16, 1024);
   const uint64_t v_desc = smem_desc_sw128(smem + OFF_RING, kUnit / 2, 1024);
   bool ok = true;
-  uint32_t base = 0, masked = 0, steps[2] = {0, 0}, works[2] = {0, 0};  // units, masked steps, steps, works so far
+  uint32_t base = 0, masked = 0, steps0 = 0, steps1 = 0, works0 = 0, works1 = 0;  // units, masked steps, steps, works so far
   // up to `units` units from u on, and two barriers more, each waited for by a
   // lane of its own (one after the other, the waits cost 60 cycles each)
   auto wait_for = [&](uint32_t u, int units, uint64_t *bar, uint32_t parity, uint64_t *bar2, uint32_t parity2) {
@@ -373,7 +373,7 @@ __device__ __forceinline__ void mma_sequence(Bars *br, uint32_t smem, uint32_t t
 #pragma unroll
       for (int c = 0; c < 3; c++) {
         const uint32_t s = (base + (uint32_t)j * kUnitsPerStep + c) % kUnits;
-        const uint64_t a = q_desc + (((3 * t + c) * kUnit) >> 4), b = k_desc + s * (kUnit >> 4);
+        const uint64_t a = q_desc + (uint32_t)(3 * t + c) * (kUnit >> 4), b = k_desc + s * (kUnit >> 4);
 #pragma unroll
         for (int k = 0; k < 4; k++)
           mma_ss(tmem + TM_S + t * 128, a + 2 * k, b + 2 * k, IDESC_QK, (c | k) ? 1u : 0u);
@@ -409,20 +409,12 @@ __device__ __forceinline__ void mma_sequence(Bars *br, uint32_t smem, uint32_t t
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_u32(&br->work_empty[slot]));
     const int n0 = st.n[0], n1 = st.n[1];
-    if (n0 > 0) {
-      wait_for(base, 3, &br->q_full[0], works[0] & 1, nullptr, 0);
-      if (!meet()) return;
-      qk(0, 0, n1 == 0, n0 == 1);
-    }
-    if (n1 > 0) {
-      wait_for(base, 3, &br->q_full[1], works[1] & 1, nullptr, 0);
-      if (!meet()) return;
-      qk(1, 0, true, n1 == 1);
-    }
     // While a tile's softmax runs, the tensor cores work on the other tile:
-    // its P V, then its next scores.
-    for (int j = 0; j < st.most; j++) {
-      const uint32_t uv = base + (uint32_t)j * kUnitsPerStep + 3;
+    // its P V, then its next scores (j = -1: the first ones).  The loops stay
+    // loops: the code of all roles has to stay in the instruction cache.
+#pragma unroll 1
+    for (int j = -1; j < st.most; j++) {
+      const uint32_t uv = base + (uint32_t)(j * kUnitsPerStep + 3);
       if (j >= st.masked) {
         if (kWaiter) {
           wait_for(uv, 2, nullptr, 0, nullptr, 0);
@@ -431,32 +423,34 @@ __device__ __forceinline__ void mma_sequence(Bars *br, uint32_t smem, uint32_t t
         }
         masked++;
       }
-#pragma unroll
+#pragma unroll 1
       for (int t = 0; t < 2; t++) {
         const int n = t == 0 ? n0 : n1, other = t == 0 ? n1 : n0;
         if (j >= n) continue;
-        const bool last_v = t == 1 || j >= other, last_k = t == 1 || j + 1 >= other;
-        // the first P V of a unit of work overwrites the output of the one before
-        wait_for(uv, 2, &br->p_full[t][0], (steps[t] + j) & 1, j == 0 ? &br->o_free[t] : nullptr, (works[t] & 1) ^ 1);
-        if (!meet()) return;
-        pv(t, j, 0, last_v);
-        wait_for(uv, 0, &br->p_full[t][1], (steps[t] + j) & 1, nullptr, 0);
-        if (!meet()) return;
-        pv(t, j, 1, last_v);
+        const uint32_t work_parity = (t == 0 ? works0 : works1) & 1, step = (t == 0 ? steps0 : steps1) + j;
+        if (j >= 0) {
+#pragma unroll
+          for (int c = 0; c < 2; c++) {
+            // (the first P V of a unit of work overwrites the output of the one before)
+            wait_for(uv, c == 0 ? 2 : 0, &br->p_full[t][c], step & 1, c + j == 0 ? &br->o_free[t] : nullptr, work_parity ^ 1);
+            if (!meet()) return;
+            pv(t, j, c, t == 1 || j >= other);
+          }
+        }
         if (j + 1 < n) {
-          if (t == 0 || j + 1 >= other) {  // the tile that reads the keys first
-            wait_for(uv + 2, 3, nullptr, 0, nullptr, 0);
+          if (j < 0 || t == 0 || j + 1 >= other) {  // the tile that reads the keys first, or Q
+            wait_for(uv + 2, 3, j < 0 ? &br->q_full[t] : nullptr, work_parity, nullptr, 0);
             if (!meet()) return;
           }
-          qk(t, j + 1, last_k, j + 2 == n);
+          qk(t, j + 1, t == 1 || j + 1 >= other, j + 2 == n);
         }
       }
     }
     base += (uint32_t)st.most * kUnitsPerStep;
-    for (int t = 0; t < 2; t++) {
-      steps[t] += st.n[t];
-      works[t] += st.n[t] > 0 ? 1 : 0;
-    }
+    steps0 += n0;
+    steps1 += n1;
+    works0 += n0 > 0 ? 1 : 0;
+    works1 += n1 > 0 ? 1 : 0;
   }
 }
 
@@ -686,11 +680,13 @@ __device__ __forceinline__ bool softmax_work(const PrefillParams &p, Bars *br, u
     if (lane == 0) mbar_arrive(smem_u32(&br->o_free[t]));
   }
   if (live && bad) {  // rare: add the non-finite values of the keys that this row sees
+#pragma unroll 1
     for (int k = 0; k < 512; k++) {
       if (!((*(volatile const uint32_t *)&bad_keys[k >> 5] >> (k & 31)) & 1u)) continue;
       const int key = st.masked * kKeys + k;
       if (key >= seen) continue;
       const __nv_bfloat16 *vr = p.v + (size_t)(w.k0 + key) * p.v_tok + (size_t)w.h * p.v_head;
+#pragma unroll 1
       for (int d = 0; d < kDv; d++) {
         const float x = __bfloat162float(vr[d]);
         if (fabsf(x) < INFINITY) continue;
