@@ -205,6 +205,12 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float y;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
+
 // Pairs of fp32 in one 64-bit register (fma and add of two at a time).
 __device__ __forceinline__ uint64_t pack2(float a, float b) {
   uint64_t r;
@@ -431,15 +437,20 @@ __device__ __forceinline__ void mma_sequence(Bars *br, uint32_t smem, uint32_t t
         if (j >= 0) {
 #pragma unroll
           for (int c = 0; c < 2; c++) {
-            // (the first P V of a unit of work overwrites the output of the one before)
-            wait_for(uv, c == 0 ? 2 : 0, &br->p_full[t][c], step & 1, c + j == 0 ? &br->o_free[t] : nullptr, work_parity ^ 1);
+            // first half: the values, and for the first P V of a unit of work the output of the one before; second
+            // half: the next keys, if this tile reads them first
+            if (c == 0) {
+              wait_for(uv, 2, &br->p_full[t][0], step & 1, j == 0 ? &br->o_free[t] : nullptr, work_parity ^ 1);
+            } else {
+              wait_for(uv + 2, j + 1 < n && (t == 0 || j + 1 >= other) ? 3 : 0, &br->p_full[t][1], step & 1, nullptr, 0);
+            }
             if (!meet()) return;
             pv(t, j, c, t == 1 || j >= other);
           }
         }
         if (j + 1 < n) {
-          if (j < 0 || t == 0 || j + 1 >= other) {  // the tile that reads the keys first, or Q
-            wait_for(uv + 2, 3, j < 0 ? &br->q_full[t] : nullptr, work_parity, nullptr, 0);
+          if (j < 0) {
+            wait_for(uv + 2, 3, &br->q_full[t], work_parity, nullptr, 0);
             if (!meet()) return;
           }
           qk(t, j + 1, t == 1 || j + 1 >= other, j + 2 == n);
@@ -557,13 +568,15 @@ __device__ __forceinline__ bool softmax_work(const PrefillParams &p, Bars *br, u
         }
       }
     }
-    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+    float mx[4];
 #pragma unroll
-    for (int c = 0; c < 4; c++)
+    for (int c = 0; c < 4; c++) {
+      mx[c] = __uint_as_float(s[c][0]);
 #pragma unroll
-      for (int e = 0; e < 32; e += 2)
-        mx[c] = fmaxf(fmaxf(mx[c], __uint_as_float(s[c][e])), __uint_as_float(s[c][e + 1]));
-    const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+      for (int e = 1; e < 31; e += 2) mx[c] = max3(mx[c], __uint_as_float(s[c][e]), __uint_as_float(s[c][e + 1]));
+      mx[c] = fmaxf(mx[c], __uint_as_float(s[c][31]));
+    }
+    const float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
     const bool move = (top - m) * p.scale_log2 > kMoveAt;  // (-inf - -inf is nan: no move)
     if (__any_sync(0xffffffffu, move)) {
       const float alpha = move ? ex2((m - top) * p.scale_log2) : 1.f;
