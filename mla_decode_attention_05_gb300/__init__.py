@@ -408,22 +408,29 @@ def kv_insert(kv_c: torch.Tensor, k_pe: torch.Tensor, w_kva: torch.Tensor, slots
     return kv_cache
 
 
-def _strided(t, name, shape, dev, dtype=torch.bfloat16):
-    """A bf16 CUDA tensor of this shape (None: any size) whose last axis is
-    contiguous and whose other strides are multiples of 8 elements.  Every
-    caller's last axis is a multiple of 8."""
-    if type(t) is torch.Tensor and t.dtype is dtype and t.is_cuda and (dev is None or t.get_device() == dev.index):
+def _strided(t, name, shape, dev):
+    """Checks for a bf16 CUDA tensor of this shape (None: any size) whose last
+    axis (of a multiple of 8) is contiguous and whose other strides are
+    multiples of 8 elements -> the other axes' strides as the C ABI wants them:
+    that of an axis of one entry is never used and torch may give it any value,
+    so it is the row's width there."""
+    if type(t) is torch.Tensor and t.dtype is torch.bfloat16 and t.is_cuda and (
+            dev is None or t.get_device() == dev.index):
         size, stride = t.shape, t.stride()
-        if len(size) == len(shape) and stride[-1] == 1 and size[-1] == shape[-1]:
-            for m, n, k in zip(size[:-1], shape, stride):
-                if (n is not None and m != n) or (k & 7 and m > 1):
-                    break
-            else:
-                return
+        w = shape[-1]
+        if len(size) == len(shape) and size[-1] == w and stride[-1] == 1:
+            if len(shape) == 3:
+                n, h, _ = size
+                a, b, _ = stride
+                if ((shape[0] is None or shape[0] == n) and (shape[1] is None or shape[1] == h)
+                        and not (a & 7 and n > 1) and not (b & 7 and h > 1)):
+                    return a if n > 1 else w, b if h > 1 else w
+            elif (shape[0] is None or shape[0] == size[0]) and not (stride[0] & 7 and size[0] > 1):
+                return (stride[0] if size[0] > 1 else w,)
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
     if t.dim() != len(shape) or any(n is not None and m != n for m, n in zip(t.shape, shape)):
         raise ValueError(f"{name} must be {['*' if n is None else n for n in shape]}, got {list(t.shape)}")
     if not t.is_cuda:
@@ -432,12 +439,7 @@ def _strided(t, name, shape, dev, dtype=torch.bfloat16):
         raise ValueError(f"{name} is on {t.device}, expected {dev}")
     if t.numel() and (t.stride(-1) != 1 or any(t.stride(k) % 8 for k in range(t.dim() - 1) if t.shape[k] > 1)):
         raise ValueError(f"{name} must have unit stride in its last axis and strides that are multiples of 8")
-
-
-def _ld(t, k):
-    """Stride of axis k as the C ABI wants it: that of an axis of one entry is
-    never used, and torch may give it any value."""
-    return t.stride(k) if t.shape[k] > 1 else t.shape[-1]
+    return tuple(t.stride(k) if t.shape[k] > 1 else t.shape[-1] for k in range(t.dim() - 1))
 
 
 def kv_insert_rope(kv_c: torch.Tensor, k_pe: torch.Tensor, w_kva: torch.Tensor, slots: torch.Tensor,
@@ -457,6 +459,8 @@ def kv_insert_rope(kv_c: torch.Tensor, k_pe: torch.Tensor, w_kva: torch.Tensor, 
     overlap it.  The other arguments are kv_insert()'s."""
     kv_c, ld_kv, k_pe, ld_pe, dev, N, fmt = _insert_args(kv_c, k_pe, w_kva, slots, kv_cache, kv_scales, k_scale_inv,
                                                          fp8_per_tensor)
+    if k_pe.get_device() != dev.index:
+        raise ValueError(f"k_pe is on {k_pe.device}, expected {dev}")
     _need(positions, "positions", torch.int64, dev, 1)
     _need(cos_sin, "cos_sin", torch.float32, dev, 2)
     if positions.shape[0] != N or cos_sin.shape[1] != 64 or cos_sin.shape[0] < 1:
@@ -465,21 +469,22 @@ def kv_insert_rope(kv_c: torch.Tensor, k_pe: torch.Tensor, w_kva: torch.Tensor, 
     if q_pe is None and q_out is not None:
         raise ValueError("q_out needs q_pe")
     if q_pe is not None:
-        _strided(q_pe, "q_pe", (N, None, 64), dev)
+        strides = _strided(q_pe, "q_pe", (N, None, 64), dev)
         H = q_pe.shape[1]
         if q_out is None:
-            q_out = q_pe
+            q_out, out_strides = q_pe, strides
         else:
-            _strided(q_out, "q_out", (N, H, 64), dev)
-        check_rows_apart(q_out.shape, q_out.stride(), "q_out")
-        strides = (_ld(q_pe, 0), _ld(q_pe, 1), _ld(q_out, 0), _ld(q_out, 1))
+            out_strides = _strided(q_out, "q_out", (N, H, 64), dev)
+        if not q_out.is_contiguous():
+            check_rows_apart(q_out.shape, out_strides + (1,), "q_out")
+        strides += out_strides
         if q_out.data_ptr() == q_pe.data_ptr() and N and strides[:2] != strides[2:]:
             raise ValueError("q_out in q_pe's place must have its strides")
     _call("mla_kv_insert_rope", dev, _at(kv_c), ld_kv, _at(k_pe), ld_pe, _at(w_kva), float(eps), _at(slots),
           _at(positions), _at(cos_sin), cos_sin.shape[0], int(bool(interleaved)), N,
           _at(kv_cache), fmt, kv_cache.shape[0], kv_cache.shape[1],
           _at(kv_scales) if fmt == KV_FP8_E4M3 else None, _at(k_scale_inv) if fmt == KV_FP8_E4M3_TENSOR else None,
-          _at(q_pe), strides[0], strides[1], _at(q_out), strides[2], strides[3], H)
+          _at(q_pe), *strides[:2], _at(q_out), *strides[2:], H)
     return kv_cache, q_out
 
 
@@ -519,9 +524,9 @@ def kv_expand(kv_cache: torch.Tensor, block_table: torch.Tensor, cu_seqlens: tor
     B = block_table.shape[0]
     if cu_seqlens.shape[0] != B + 1:
         raise ValueError("cu_seqlens must be [B + 1] for a block_table of B rows")
-    _strided(w_uk, "w_uk", (None, 128, D_V), dev)
+    uk_head, uk_row = _strided(w_uk, "w_uk", (None, 128, D_V), dev)
     H = w_uk.shape[0]
-    _strided(w_uv, "w_uv", (H, 128, D_V), dev)
+    uv_head, uv_row = _strided(w_uv, "w_uv", (H, 128, D_V), dev)
     if fmt == KV_FP8_E4M3 and tuple(kv_scales.shape) != (kv_cache.shape[0], kv_cache.shape[1], 4):
         raise ValueError("kv_scales must be [P, 64, 4]")
     if total is None:
@@ -529,17 +534,23 @@ def kv_expand(kv_cache: torch.Tensor, block_table: torch.Tensor, cu_seqlens: tor
             raise ValueError("total (the outputs' rows) is needed where no output is given")
         total = (kv if kv is not None else k_pe).shape[0]
     total = int(total)
+    if total < 0:
+        raise ValueError("total must be >= 0")
     if kv is None:
         kv = torch.empty((total, H, 256), dtype=torch.bfloat16, device=dev)
+    else:
+        _need(kv, "kv", torch.bfloat16, dev, 3)
+        if tuple(kv.shape) != (total, H, 256):
+            raise ValueError(f"kv must be [{total}, {H}, 256], got {list(kv.shape)}")
     if k_pe is None:
         k_pe = torch.empty((total, 64), dtype=torch.bfloat16, device=dev)
-    _need(kv, "kv", torch.bfloat16, dev, 3)
-    _need(k_pe, "k_pe", torch.bfloat16, dev, 2)
-    if tuple(kv.shape) != (total, H, 256) or tuple(k_pe.shape) != (total, 64):
-        raise ValueError(f"kv must be [{total}, {H}, 256], k_pe [{total}, 64]")
+    else:
+        _need(k_pe, "k_pe", torch.bfloat16, dev, 2)
+        if tuple(k_pe.shape) != (total, 64):
+            raise ValueError(f"k_pe must be [{total}, 64], got {list(k_pe.shape)}")
     _call("mla_kv_expand", dev, _at(kv_cache), fmt, kv_cache.shape[0], kv_cache.shape[1], _at(block_table),
           block_table.shape[1], _at(cu_seqlens), B, total, _at(kv_scales) if fmt != KV_BF16 else None,
-          _at(w_uk), w_uk.stride(1), _ld(w_uk, 0), _at(w_uv), w_uv.stride(1), _ld(w_uv, 0), H, _at(kv), _at(k_pe))
+          w_uk.data_ptr(), uk_row, uk_head, w_uv.data_ptr(), uv_row, uv_head, H, kv.data_ptr(), k_pe.data_ptr())
     return kv, k_pe
 
 
@@ -577,12 +588,12 @@ def prefill(q: torch.Tensor, k_nope: torch.Tensor, k_pe: torch.Tensor, v: torch.
     one less.  A row that sees no key gets 0 and -inf.  Rows of no sequence
     are left as they were.  workspace: at least prefill_workspace_bytes() bytes
     (allocated here where it is needed and not given)."""
-    _strided(q, "q", (None, None, 192), None)
-    dev, (Nq, H) = q.device, q.shape[:2]
-    _strided(k_nope, "k_nope", (None, H, 128), dev)
+    q_strides = _strided(q, "q", (None, None, 192), None)
+    dev, (Nq, H, _) = q.device, q.shape
+    k_strides = _strided(k_nope, "k_nope", (None, H, 128), dev)
     Nk = k_nope.shape[0]
-    _strided(k_pe, "k_pe", (Nk, 64), dev)
-    _strided(v, "v", (Nk, H, 128), dev)
+    pe_strides = _strided(k_pe, "k_pe", (Nk, 64), dev)
+    v_strides = _strided(v, "v", (Nk, H, 128), dev)
     _need(cu_seqlens_q, "cu_seqlens_q", torch.int32, dev, 1)
     _need(cu_seqlens_k, "cu_seqlens_k", torch.int32, dev, 1)
     B = cu_seqlens_q.shape[0] - 1
@@ -590,12 +601,16 @@ def prefill(q: torch.Tensor, k_nope: torch.Tensor, k_pe: torch.Tensor, v: torch.
         raise ValueError("cu_seqlens_q and cu_seqlens_k must be [B + 1]")
     if out is None:
         out = torch.empty((Nq, H, 128), dtype=torch.bfloat16, device=dev)
+    else:
+        _need(out, "out", torch.bfloat16, dev, 3)
+        if tuple(out.shape) != (Nq, H, 128):
+            raise ValueError(f"out must be [{Nq}, {H}, 128], got {list(out.shape)}")
     if lse is None:
         lse = torch.empty((H, Nq), dtype=torch.float32, device=dev)
-    _need(out, "out", torch.bfloat16, dev, 3)
-    _need(lse, "lse", torch.float32, dev, 2)
-    if tuple(out.shape) != (Nq, H, 128) or tuple(lse.shape) != (H, Nq):
-        raise ValueError(f"out must be [{Nq}, {H}, 128], lse [{H}, {Nq}]")
+    else:
+        _need(lse, "lse", torch.float32, dev, 2)
+        if tuple(lse.shape) != (H, Nq):
+            raise ValueError(f"lse must be [{H}, {Nq}], got {list(lse.shape)}")
     room = prefill_workspace_bytes(B, H, Nq, Nk)
     if workspace is None:
         if room:
@@ -603,9 +618,9 @@ def prefill(q: torch.Tensor, k_nope: torch.Tensor, k_pe: torch.Tensor, v: torch.
     else:
         _need(workspace, "workspace", workspace.dtype, dev)
         room = workspace.numel() * workspace.element_size()
-    _call("mla_prefill", dev, _at(q), _ld(q, 0), _ld(q, 1), _at(k_nope), _ld(k_nope, 0), _ld(k_nope, 1), _at(k_pe),
-          _ld(k_pe, 0), _at(v), _ld(v, 0), _ld(v, 1), _at(cu_seqlens_q), _at(cu_seqlens_k), B, H, Nq, Nk,
-          float(softmax_scale), int(bool(causal)), _at(workspace), room, _at(out), _at(lse))
+    _call("mla_prefill", dev, q.data_ptr(), *q_strides, k_nope.data_ptr(), *k_strides, k_pe.data_ptr(), *pe_strides,
+          v.data_ptr(), *v_strides, cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(), B, H, Nq, Nk,
+          float(softmax_scale), int(bool(causal)), _at(workspace), room, out.data_ptr(), lse.data_ptr())
     return out, lse
 
 
@@ -622,16 +637,16 @@ def value_project(attn: torch.Tensor, w_uv: torch.Tensor, *, out: Optional[torch
     attn bf16 [N, H, 512] (decode()'s out with B and T flattened; rows may be
     strided); w_uv bf16 [H, 128, 512] (a view of a [H, 256, 512] tensor will
     do)."""
-    _strided(attn, "attn", (None, None, D_V), None)
-    dev, (N, H) = attn.device, attn.shape[:2]
-    _strided(w_uv, "w_uv", (H, 128, D_V), dev)
+    strides = _strided(attn, "attn", (None, None, D_V), None)
+    dev, (N, H, _) = attn.device, attn.shape
+    w_head, w_row = _strided(w_uv, "w_uv", (H, 128, D_V), dev)
     if out is None:
         out = torch.empty((N, H, 128), dtype=torch.bfloat16, device=dev)
-    _need(out, "out", torch.bfloat16, dev, 3)
-    if tuple(out.shape) != (N, H, 128):
-        raise ValueError(f"out must be [{N}, {H}, 128], got {list(out.shape)}")
-    _call("mla_value_project", dev, _at(attn), _ld(attn, 0), _ld(attn, 1), _at(w_uv), w_uv.stride(1),
-          _ld(w_uv, 0), N, H, _at(out))
+    else:
+        _need(out, "out", torch.bfloat16, dev, 3)
+        if tuple(out.shape) != (N, H, 128):
+            raise ValueError(f"out must be [{N}, {H}, 128], got {list(out.shape)}")
+    _call("mla_value_project", dev, attn.data_ptr(), *strides, w_uv.data_ptr(), w_row, w_head, N, H, out.data_ptr())
     return out
 
 

@@ -15,100 +15,178 @@ namespace {
 
 using namespace ptx;
 
-// One CTA per (block of up to 64 tokens, head).  D[v][n] is computed with the
-// 128 weight rows as the MMA's M and the tokens as its N, so that a decode
-// batch of any size fills M.
-constexpr int kThreads = 128;
+// D[v][n] is computed with the 128 weight rows as the MMA's M and up to 64
+// tokens as its N, so that a decode batch of any size fills M.  A persistent
+// CTA takes an equal share of the (head, token tile) items, heads outermost:
+// W_UV[h] (128 KB) stays in shared memory for all its tiles of a head while
+// the tokens' rows stream through a ring.  D is double buffered in tensor
+// memory; four warps drain it through shared memory, from where TMA stores
+// whole lines (and clips the tokens behind the last).
+//
+// Warps 0-3 drain D, warp 4 loads, warp 5 issues the MMAs.
+constexpr int kThreads = 192;
 constexpr int kDv = 128;
 constexpr int kKBlocks = D_V / 64;            // 8 blocks of 64 latent values
 constexpr uint32_t kWBytes = 128 * 128;       // one block of 128 weight rows
 constexpr int kMaxTile = 64;
-constexpr uint32_t kSmem = kKBlocks * (kWBytes + kMaxTile * 128) + 256 + 1024;
+constexpr uint32_t kUnit = 2 * kMaxTile * 128;  // 128 latent values of a tile's tokens, as two boxes of 64
+constexpr int kUnits = 5;
+constexpr uint32_t OFF_RING = kKBlocks * kWBytes;
+constexpr uint32_t OFF_OUT = OFF_RING + kUnits * kUnit;
+constexpr uint32_t OFF_BARS = OFF_OUT + kMaxTile * kDv * 2;
+
+struct Bars {
+  uint64_t w_full[kKBlocks / 2], w_empty;
+  uint64_t full[kUnits], empty[kUnits];
+  uint64_t d_full[2], d_empty[2];
+  uint32_t tmem_base;
+  int abort;
+};
+constexpr uint32_t kSmem = OFF_BARS + sizeof(Bars) + 1024;
+static_assert(kSmem <= 232448, "shared memory budget");
+
+__device__ __forceinline__ bool wait_ok(Bars *b, uint64_t *bar, uint32_t parity, unsigned int *status) {
+  if (mbar_wait<false>(smem_u32(bar), parity, &b->abort, kDefaultWaitNs)) return true;
+  atomicOr(status, MLA_STATUS_WAIT_TIMEOUT);
+  *(volatile int *)&b->abort = 1;
+  return false;
+}
 
 __global__ void __launch_bounds__(kThreads, 1)
     value_kernel(const __grid_constant__ CUtensorMap w_map, const __grid_constant__ CUtensorMap x_map,
-                 __nv_bfloat16 *out, int N, int H, int ntile, unsigned int *status) {
+                 const __grid_constant__ CUtensorMap o_map, int tiles, int items, int ntile, unsigned int *status) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t *base = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  uint64_t *full = reinterpret_cast<uint64_t *>(base + kKBlocks * (kWBytes + kMaxTile * 128));
-  uint64_t *done = full + kKBlocks;
-  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(done + 1);
+  Bars *br = reinterpret_cast<Bars *>(base + OFF_BARS);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int h = blockIdx.y, n0 = blockIdx.x * ntile;
-  int abort_flag = 0;  // the waits below give up only on their time limit
+  const int i0 = (int)((long long)items * blockIdx.x / gridDim.x);
+  const int i1 = (int)((long long)items * (blockIdx.x + 1) / gridDim.x);
   if (warp == 0) {
-    tmem_alloc(smem_u32(tmem_slot), 64);
+    tmem_alloc(smem_u32(&br->tmem_base), 128);
     tmem_relinquish();
   }
   if (threadIdx.x == 32) {
-    for (int k = 0; k < kKBlocks; k++) mbar_init(smem_u32(&full[k]), 1);
-    mbar_init(smem_u32(done), 1);
+    for (int k = 0; k < kKBlocks / 2; k++) mbar_init(smem_u32(&br->w_full[k]), 1);
+    mbar_init(smem_u32(&br->w_empty), 1);
+    for (int s = 0; s < kUnits; s++) {
+      mbar_init(smem_u32(&br->full[s]), 1);
+      mbar_init(smem_u32(&br->empty[s]), 1);
+    }
+    for (int s = 0; s < 2; s++) {
+      mbar_init(smem_u32(&br->d_full[s]), 1);
+      mbar_init(smem_u32(&br->d_empty[s]), 4);
+    }
+    br->abort = 0;
     fence_mbar_init_cluster();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
-  const uint32_t sw = smem_u32(base), sx = sw + kKBlocks * kWBytes;
-  if (threadIdx.x == 0) {
-    const uint64_t pol_w = policy_evict_normal(), pol_x = policy_evict_first();
-    for (int k = 0; k < kKBlocks; k++) {
-      mbar_arrive_expect_tx(smem_u32(&full[k]), kWBytes + ntile * 128);
-      tma_load_3d(sw + k * kWBytes, &w_map, smem_u32(&full[k]), 64 * k, 0, h, pol_w);
-      tma_load_3d(sx + k * (uint32_t)ntile * 128, &x_map, smem_u32(&full[k]), 64 * k, h, n0, pol_x);
+  const uint32_t tmem = br->tmem_base, smem = smem_u32(base);
+  const uint32_t box = (uint32_t)ntile * 128;
+
+  if (warp == 4) {
+    if (lane == 0) {
+      const uint64_t pol_w = policy_evict_normal(), pol_x = policy_evict_first();
+      uint32_t u = 0, heads = 0;
+      bool ok = true;
+      for (int i = i0; i < i1 && ok; i++) {
+        const int h = i / tiles, n0 = i % tiles * ntile;
+        const bool new_head = i == i0 || n0 == 0;
+        if (new_head) ok = wait_ok(br, &br->w_empty, (heads++ & 1) ^ 1, status);
+        for (int k = 0; k < kKBlocks / 2 && ok; k++, u++) {
+          if (new_head) {
+            mbar_arrive_expect_tx(smem_u32(&br->w_full[k]), 2 * kWBytes);
+            tma_load_3d(smem + 2 * k * kWBytes, &w_map, smem_u32(&br->w_full[k]), 128 * k, 0, h, pol_w);
+            tma_load_3d(smem + (2 * k + 1) * kWBytes, &w_map, smem_u32(&br->w_full[k]), 128 * k + 64, 0, h, pol_w);
+          }
+          const uint32_t s = u % kUnits, dst = smem + OFF_RING + s * kUnit;
+          ok = wait_ok(br, &br->empty[s], ((u / kUnits) & 1) ^ 1, status);
+          if (!ok) break;
+          mbar_arrive_expect_tx(smem_u32(&br->full[s]), 2 * box);
+          tma_load_3d(dst, &x_map, smem_u32(&br->full[s]), 128 * k, h, n0, pol_x);
+          tma_load_3d(dst + box, &x_map, smem_u32(&br->full[s]), 128 * k + 64, h, n0, pol_x);
+        }
+      }
     }
-    const uint32_t idesc = idesc_bf16_f32(128, ntile, false, false);
-    bool ok = true;
-    for (int k = 0; k < kKBlocks && ok; k++) {
-      ok = mbar_wait<false>(smem_u32(&full[k]), 0, &abort_flag, kDefaultWaitNs);
-      if (!ok) break;
-      tc_fence_after();
+  } else if (warp == 5) {
+    if (lane == 0) {
+      const uint32_t idesc = idesc_bf16_f32(128, ntile, false, false);
+      uint32_t u = 0, heads = 0;
+      bool ok = true;
+      for (int i = i0; i < i1 && ok; i++) {
+        const int j = i - i0, buf = j & 1;
+        const bool new_head = i == i0 || i % tiles == 0;
+        heads += new_head ? 1 : 0;
+        ok = wait_ok(br, &br->d_empty[buf], ((j >> 1) & 1) ^ 1, status);
+        for (int k = 0; k < kKBlocks / 2 && ok; k++, u++) {
+          const uint32_t s = u % kUnits;
+          if (new_head) ok = wait_ok(br, &br->w_full[k], (heads - 1) & 1, status);
+          ok = ok && wait_ok(br, &br->full[s], (u / kUnits) & 1, status);
+          if (!ok) break;
+          tc_fence_after();
 #pragma unroll
-      for (int kk = 0; kk < 4; kk++)
-        mma_ss(tmem, smem_desc_sw128(sw + k * kWBytes + kk * 32, 16, 1024),
-               smem_desc_sw128(sx + k * (uint32_t)ntile * 128 + kk * 32, 16, 1024), idesc, (k | kk) ? 1u : 0u);
+          for (int kk = 0; kk < 8; kk++)
+            mma_ss(tmem + buf * 64, smem_desc_sw128(smem + (2 * k + (kk >> 2)) * kWBytes + (kk & 3) * 32, 16, 1024),
+                   smem_desc_sw128(smem + OFF_RING + s * kUnit + (kk >> 2) * box + (kk & 3) * 32, 16, 1024), idesc,
+                   (k | kk) ? 1u : 0u);
+          mma_commit(smem_u32(&br->empty[s]));
+        }
+        if (!ok) break;
+        mma_commit(smem_u32(&br->d_full[buf]));
+        if (i + 1 == i1 || (i + 1) % tiles == 0) mma_commit(smem_u32(&br->w_empty));
+      }
     }
-    if (ok) {
-      mma_commit(smem_u32(done));
-    } else {
-      atomicOr(status, MLA_STATUS_WAIT_TIMEOUT);
-    }
-  }
-  const bool ok = __syncthreads_and(mbar_wait<false>(smem_u32(done), 0, &abort_flag, kDefaultWaitNs));
-  if (ok) {
-    tc_fence_after();
-    // D (lane = value row, column = token) -> bf16 [token][128] in the
-    // weights' place, which every MMA has finished reading
+  } else {
+    uint8_t *out = base + OFF_OUT;
     const int r = warp * 32 + lane;
-    for (int c = 0; c < ntile; c += 32) {
-      uint32_t v[32];
-      tmem_ld32(tmem + ((uint32_t)(warp * 32) << 16) + c, v);
-      tmem_wait_ld();
+    for (int i = i0; i < i1; i++) {
+      const int j = i - i0, buf = j & 1;
+      // a wait that gives up lets all four warps go on to the barriers below, which they pass together
+      const bool ok = __all_sync(0xffffffffu, wait_ok(br, &br->d_full[buf], (j >> 1) & 1, status));
+      tc_fence_after();
+      if (threadIdx.x == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // the tile before is out
+      named_bar_sync(1, 128);
+      if (ok) {
+        // D (lane = value row, column = token) -> bf16 [token][128]
+        for (int c = 0; c < ntile; c += 32) {
+          uint32_t v[32];
+          tmem_ld32(tmem + ((uint32_t)(warp * 32) << 16) + buf * 64 + c, v);
+          tmem_wait_ld();
 #pragma unroll
-      for (int j = 0; j < 32; j++)
-        if (c + j < ntile)
-          *reinterpret_cast<__nv_bfloat16 *>(base + (c + j) * 256 + r * 2) =
-              __float2bfloat16_rn(__uint_as_float(v[j]));
+          for (int e = 0; e < 32; e++)
+            if (c + e < ntile)
+              *reinterpret_cast<__nv_bfloat16 *>(out + (c + e) * 256 + r * 2) =
+                  __float2bfloat16_rn(__uint_as_float(v[e]));
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&br->d_empty[buf]));
+      fence_proxy_async_smem();
+      named_bar_sync(1, 128);
+      if (*(volatile int *)&br->abort) break;  // (set before the barrier by whoever gave up: nothing of this tile is stored)
+      if (threadIdx.x == 0) {
+        asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+                         reinterpret_cast<uint64_t>(&o_map)),
+                     "r"(smem + OFF_OUT), "r"(0), "r"(i / tiles), "r"(i % tiles * ntile)
+                     : "memory");
+        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+      }
     }
-  } else {  // a wait gave up: let copies or MMAs still in flight land before the CTA exits
-    if (lane == 0) atomicOr(status, MLA_STATUS_WAIT_TIMEOUT);
+    if (threadIdx.x == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+  }
+  __syncthreads();
+  if (*(volatile int *)&br->abort) {  // a wait gave up: let copies or MMAs still in flight land before the CTA exits
     const uint64_t t0 = globaltimer();
     while (globaltimer() - t0 < 2000000ull) {
     }
   }
   tc_fence_before();
   __syncthreads();
-  if (ok) {
-    const int rows = min(ntile, N - n0);
-    for (int i = threadIdx.x; i < rows * 16; i += kThreads) {
-      const int n = i >> 4, c = i & 15;
-      reinterpret_cast<uint4 *>(out + ((size_t)(n0 + n) * H + h) * kDv)[c] =
-          *reinterpret_cast<const uint4 *>(base + n * 256 + c * 16);
-    }
-  }
   if (warp == 0) {
     tc_fence_after();
-    tmem_dealloc(tmem, 64);
+    tmem_dealloc(tmem, 128);
   }
 }
 
@@ -138,16 +216,23 @@ int mla_value_project(const void *attn, int64_t ld_token, int64_t ld_head, const
   if (!a16(attn) || !a16(w_uv) || !a16(out))
     return fail(MLA_ERR_INVALID_ARG, "attn, w_uv and out must be 16-byte aligned");
   const int ntile = N >= kMaxTile ? kMaxTile : (N + 15) / 16 * 16;
-  CUtensorMap w_map, x_map;
+  CUtensorMap w_map, x_map, o_map;
   if (!make_map_3d(&w_map, w_uv, D_V, kDv, H, w_row, w_head, 128, 1) ||
-      !make_map_3d(&x_map, attn, D_V, H, N, ld_head, ld_token, 1, ntile))
+      !make_map_3d(&x_map, attn, D_V, H, N, ld_head, ld_token, 1, ntile) ||
+      !make_map_3d(&o_map, out, kDv, H, N, kDv, (int64_t)H * kDv, 1, ntile, kDv, false))
     return fail(MLA_ERR_CUDA, "cuTensorMapEncodeTiled failed");
+  const int tiles = (N + ntile - 1) / ntile;
+  if ((long long)tiles * H > 0x7FFFFFFFll) return fail(MLA_ERR_UNSUPPORTED, "too many tokens");
   unsigned int *st = nullptr;
   if (status_word(&st) != MLA_OK) return MLA_ERR_CUDA;
-  cudaError_t e = cudaFuncSetAttribute(value_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(value_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
   if (e != cudaSuccess) return fail(MLA_ERR_CUDA, cudaGetErrorString(e));
-  value_kernel<<<dim3((N + ntile - 1) / ntile, H), kThreads, kSmem, (cudaStream_t)stream>>>(
-      w_map, x_map, static_cast<__nv_bfloat16 *>(out), N, H, ntile, st);
+  const int items = tiles * H;
+  value_kernel<<<items < sms ? items : sms, kThreads, kSmem, (cudaStream_t)stream>>>(w_map, x_map, o_map, tiles, items,
+                                                                                     ntile, st);
   e = cudaGetLastError();
   if (e != cudaSuccess) return fail(MLA_ERR_CUDA, cudaGetErrorString(e));
   set_last_error("");
