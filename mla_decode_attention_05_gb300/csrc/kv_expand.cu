@@ -7,8 +7,8 @@
 //   k_pe[r]           = the row's 64 rotated key values
 // with c the row's 512 latent values.
 //
-// As one GEMM with gathered rows: M = 128 rows of the packed output, N = 256
-// (one head: its W_UK rows, then its W_UV rows), K = 512.  2 * 512 flops per
+// As one GEMM with gathered rows: M = rows of the packed output, N = 256 (one
+// head: its W_UK rows, then its W_UV rows), K = 512.  2 * 512 flops per
 // 2-byte output value are above the ridge, so with many rows it is bound by
 // the tensor cores, with the output's write close behind; with few rows by
 // the read of the weights.
@@ -41,25 +41,36 @@ struct ExpandParams {
   int store_v8;  // kv is 32-byte aligned
 };
 
+// A cluster of two CTAs works as one: M = 256 rows, 128 gathered by each CTA;
+// of the N = 256 weight rows of a head rank 0 fetches W_UK[h] and rank 1
+// W_UV[h], and each MMA reads both.  One CTA alone would take 32 KB of weights
+// from L2 for every 64 latent values (64 bytes a cycle and SM at the tensor
+// cores' pace, more than L2 gives); a pair takes half of that.
+//
 // Warps 0-3 gather the rows (A) and drain D, warp 4 loads the weights, warp 5
-// issues the MMAs.  A CTA walks over (row block, head) units, heads innermost,
-// so A (128 rows x 512, 128 KB) stays in shared memory for all heads of a
-// block while W_UK[h] and W_UV[h] stream through a ring; D is double buffered
-// in tensor memory, so a unit is drained while the next one is computed.
+// of rank 0 issues the MMAs.  A pair walks over (row block, head) units, heads
+// innermost, so A (128 rows x 512, 128 KB) stays in shared memory for all heads
+// of a block while the weights stream through a ring; D is double buffered in
+// tensor memory, so a unit is drained while the next one is computed.
 constexpr int kThreads = 192;
-constexpr int kM = 128;
+constexpr int kM = 128;                       // rows of a CTA
+constexpr int kPairRows = 2 * kM;
 constexpr int kKBlocks = 8;
 constexpr uint32_t kABlock = kM * 128;        // 64 latent values x 128 rows
-constexpr uint32_t kWStage = 256 * 128;       // 64 latent values x 256 weight rows
+constexpr uint32_t kWBlock = 128 * 128;       // 64 latent values x this CTA's 128 weight rows
+constexpr uint32_t kWStage = 2 * kWBlock;     // 128 latent values
+constexpr int kSteps = kKBlocks / 2;          // stages of a unit
 constexpr int kWStages = 3;
 constexpr uint32_t OFF_W = kKBlocks * kABlock;
 constexpr uint32_t OFF_BARS = OFF_W + kWStages * kWStage;
-constexpr uint32_t IDESC = idesc_bf16_f32(128, 256, false, false);
+constexpr uint32_t IDESC = idesc_bf16_f32(256, 256, false, false);
 
 struct Bars {
-  uint64_t w_full[kWStages], w_empty[kWStages];
-  uint64_t a_full;
-  uint64_t d_full[2], d_empty[2];
+  uint64_t w_full[kWStages];   // rank 0: the stage of both CTAs
+  uint64_t w_empty[kWStages];
+  uint64_t a_full;             // rank 0: the rows of both CTAs
+  uint64_t d_full[2];
+  uint64_t d_empty[2];         // rank 0: drained by both CTAs
   uint32_t tmem_base;
   int abort;
 };
@@ -67,7 +78,7 @@ constexpr uint32_t kSmem = OFF_BARS + sizeof(Bars) + 1024;
 static_assert(kSmem <= 232448, "shared memory budget");
 
 __device__ __forceinline__ bool wait_ok(Bars *b, uint64_t *bar, uint32_t parity, unsigned int *status) {
-  if (mbar_wait<false>(smem_u32(bar), parity, &b->abort, kDefaultWaitNs)) return true;
+  if (mbar_wait<true>(smem_u32(bar), parity, &b->abort, kDefaultWaitNs)) return true;
   atomicOr(status, MLA_STATUS_WAIT_TIMEOUT);
   *(volatile int *)&b->abort = 1;
   return false;
@@ -183,34 +194,37 @@ __device__ void gather_rows(const ExpandParams &p, uint8_t *a, int row0, int war
   }
 }
 
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     expand_kernel(const __grid_constant__ CUtensorMap uk_map, const __grid_constant__ CUtensorMap uv_map,
                   ExpandParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t *base = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   Bars *br = reinterpret_cast<Bars *>(base + OFF_BARS);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const long long units = (long long)ceil_div(p.total, kM) * p.H;
-  const int u0 = (int)(units * blockIdx.x / gridDim.x), u1 = (int)(units * (blockIdx.x + 1) / gridDim.x);
+  const uint32_t rank = cluster_ctarank();
+  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  const long long units = (long long)ceil_div(p.total, kPairRows) * p.H;
+  const int u0 = (int)(units * pair / pairs), u1 = (int)(units * (pair + 1) / pairs);
   if (warp == 0) {
-    tmem_alloc(smem_u32(&br->tmem_base), 512);
-    tmem_relinquish();
+    tmem_alloc_pair(smem_u32(&br->tmem_base), 512);
+    tmem_relinquish_pair();
   }
   if (threadIdx.x == 32) {
     for (int s = 0; s < kWStages; s++) {
       mbar_init(smem_u32(&br->w_full[s]), 1);
       mbar_init(smem_u32(&br->w_empty[s]), 1);
     }
-    mbar_init(smem_u32(&br->a_full), 4);
+    mbar_init(smem_u32(&br->a_full), 8);
     for (int s = 0; s < 2; s++) {
       mbar_init(smem_u32(&br->d_full[s]), 1);
-      mbar_init(smem_u32(&br->d_empty[s]), 4);
+      mbar_init(smem_u32(&br->d_empty[s]), 8);
     }
     br->abort = 0;
     fence_mbar_init_cluster();
   }
   tc_fence_before();
   __syncthreads();
+  cluster_sync();  // both CTAs' barriers are there
   tc_fence_after();
   const uint32_t tmem = br->tmem_base;
   const uint32_t sa = smem_u32(base), sw = sa + OFF_W;
@@ -221,12 +235,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     long long src = -2;
     // this block's rows
     auto gather = [&](int u) {
-      const int row0 = u / p.H * kM;
+      const int row0 = u / p.H * kPairRows + (int)rank * kM;
       src = row_source(p, row0 + warp * 32 + lane);
       gather_rows(p, base, row0, warp, lane, src, u % p.H == 0);
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&br->a_full));
+      if (lane == 0) mbar_arrive_remote(mapa(smem_u32(&br->a_full), 0));
     };
     if (u0 < u1) gather(u0);
     for (int u = u0; u < u1; u++) {
@@ -235,7 +249,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
       tc_fence_after();
       const long long mine = src;
-      const int row = u / p.H * kM + warp * 32 + lane, h = u % p.H;
+      const int row = u / p.H * kPairRows + (int)rank * kM + warp * 32 + lane, h = u % p.H;
       // the next unit's rows first: every MMA that reads A has completed
       if (u + 1 < u1 && h + 1 == p.H) gather(u + 1);
       uint8_t *dst = reinterpret_cast<uint8_t *>(p.kv + ((size_t)row * p.H + h) * 256);
@@ -265,26 +279,28 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&br->d_empty[buf]));
+      if (lane == 0) mbar_arrive_remote(mapa(smem_u32(&br->d_empty[buf]), 0));
     }
   } else if (warp == 4) {
     if (lane == 0) {
       const uint64_t pol = policy_evict_normal();
+      const CUtensorMap *map = rank == 0 ? &uk_map : &uv_map;
       uint32_t k = 0;
       bool ok = true;
       for (int u = u0; u < u1 && ok; u++) {
         const int h = u % p.H;
-        for (int kb = 0; kb < kKBlocks; kb++, k++) {
-          const uint32_t s = k % kWStages;
+        for (int kb = 0; kb < kSteps; kb++, k++) {
+          const uint32_t s = k % kWStages, dst = sw + s * kWStage;
           ok = wait_ok(br, &br->w_empty[s], ((k / kWStages) & 1) ^ 1, p.status);
           if (!ok) break;
-          mbar_arrive_expect_tx(smem_u32(&br->w_full[s]), kWStage);
-          tma_load_3d(sw + s * kWStage, &uk_map, smem_u32(&br->w_full[s]), 64 * kb, 0, h, pol);
-          tma_load_3d(sw + s * kWStage + kWStage / 2, &uv_map, smem_u32(&br->w_full[s]), 64 * kb, 0, h, pol);
+          if (rank == 0) mbar_arrive_expect_tx(smem_u32(&br->w_full[s]), 2 * kWStage);
+          const uint32_t full = mapa(smem_u32(&br->w_full[s]), 0);
+          tma_load_3d_pair(dst, map, full, 128 * kb, 0, h, pol);
+          tma_load_3d_pair(dst + kWBlock, map, full, 128 * kb + 64, 0, h, pol);
         }
       }
     }
-  } else if (lane == 0) {
+  } else if (rank == 0 && lane == 0) {
     uint32_t k = 0, na = 0;
     bool ok = true;
     for (int u = u0; u < u1 && ok; u++) {
@@ -293,18 +309,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (ok) ok = wait_ok(br, &br->d_empty[buf], ((i >> 1) & 1) ^ 1, p.status);
       if (!ok) break;
       tc_fence_after();
-      for (int kb = 0; kb < kKBlocks; kb++, k++) {
+      for (int kb = 0; kb < kSteps; kb++, k++) {
         const uint32_t s = k % kWStages;
         ok = wait_ok(br, &br->w_full[s], (k / kWStages) & 1, p.status);
         if (!ok) break;
         tc_fence_after();
 #pragma unroll
-        for (int kk = 0; kk < 4; kk++)
-          mma_ss(tmem + buf * 256, smem_desc_sw128(sa + kb * kABlock + kk * 32, 16, 1024),
-                 smem_desc_sw128(sw + s * kWStage + kk * 32, 16, 1024), IDESC, (kb | kk) ? 1u : 0u);
-        mma_commit(smem_u32(&br->w_empty[s]));
+        for (int kk = 0; kk < 8; kk++)
+          mma_pair_ss(tmem + buf * 256,
+                      smem_desc_sw128(sa + (2 * kb + (kk >> 2)) * kABlock + (kk & 3) * 32, 16, 1024),
+                      smem_desc_sw128(sw + s * kWStage + (kk >> 2) * kWBlock + (kk & 3) * 32, 16, 1024), IDESC,
+                      (kb | kk) ? 1u : 0u);
+        mma_commit_pair(smem_u32(&br->w_empty[s]));
       }
-      if (ok) mma_commit(smem_u32(&br->d_full[buf]));
+      if (ok) mma_commit_pair(smem_u32(&br->d_full[buf]));
     }
   }
   __syncthreads();
@@ -315,9 +333,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
+  cluster_sync();  // neither CTA's memory is used by the other any more
   if (warp == 0) {
     tc_fence_after();
-    tmem_dealloc(tmem, 512);
+    tmem_dealloc_pair(tmem, 512);
   }
 }
 
@@ -382,8 +401,9 @@ int mla_kv_expand(const void *kv_cache, int kv_format, int num_pages, int page_s
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e == cudaSuccess) e = cudaFuncSetAttribute(expand_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
   if (e != cudaSuccess) return fail(MLA_ERR_CUDA, cudaGetErrorString(e));
-  const long long units = (long long)ceil_div(total, kM) * H;
-  expand_kernel<<<(int)(units < sms ? units : sms), kThreads, kSmem, (cudaStream_t)stream>>>(uk_map, uv_map, p);
+  const long long units = (long long)ceil_div(total, kPairRows) * H;
+  const int pairs = (int)(units < sms / 2 ? units : sms / 2);
+  expand_kernel<<<2 * pairs, kThreads, kSmem, (cudaStream_t)stream>>>(uk_map, uv_map, p);
   e = cudaGetLastError();
   if (e != cudaSuccess) return fail(MLA_ERR_CUDA, cudaGetErrorString(e));
   set_last_error("");
