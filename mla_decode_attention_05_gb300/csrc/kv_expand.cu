@@ -38,7 +38,6 @@ struct ExpandParams {
   __nv_bfloat16 *k_pe;  // [total][64]
   unsigned int *status;
   int format, num_pages, max_pages, B, H, total;
-  int store_v8;  // kv is 32-byte aligned
 };
 
 // A cluster of two CTAs works as one: M = 256 rows, 128 gathered by each CTA;
@@ -57,12 +56,12 @@ constexpr int kM = 128;                       // rows of a CTA
 constexpr int kPairRows = 2 * kM;
 constexpr int kKBlocks = 8;
 constexpr uint32_t kABlock = kM * 128;        // 64 latent values x 128 rows
-constexpr uint32_t kWBlock = 128 * 128;       // 64 latent values x this CTA's 128 weight rows
-constexpr uint32_t kWStage = 2 * kWBlock;     // 128 latent values
-constexpr int kSteps = kKBlocks / 2;          // stages of a unit
-constexpr int kWStages = 3;
+constexpr uint32_t kWStage = 128 * 128;       // 64 latent values x this CTA's 128 weight rows
+constexpr int kWStages = 4;
+constexpr uint32_t kOutBytes = 32 * 128;      // 32 rows x 64 columns of the output, on their way out
 constexpr uint32_t OFF_W = kKBlocks * kABlock;
-constexpr uint32_t OFF_BARS = OFF_W + kWStages * kWStage;
+constexpr uint32_t OFF_OUT = OFF_W + kWStages * kWStage;  // two for each draining warp
+constexpr uint32_t OFF_BARS = OFF_OUT + 8 * kOutBytes;
 constexpr uint32_t IDESC = idesc_bf16_f32(256, 256, false, false);
 
 struct Bars {
@@ -196,7 +195,7 @@ __device__ void gather_rows(const ExpandParams &p, uint8_t *a, int row0, int war
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     expand_kernel(const __grid_constant__ CUtensorMap uk_map, const __grid_constant__ CUtensorMap uv_map,
-                  ExpandParams p) {
+                  const __grid_constant__ CUtensorMap o_map, ExpandParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t *base = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   Bars *br = reinterpret_cast<Bars *>(base + OFF_BARS);
@@ -252,35 +251,58 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const int row = u / p.H * kPairRows + (int)rank * kM + warp * 32 + lane, h = u % p.H;
       // the next unit's rows first: every MMA that reads A has completed
       if (u + 1 < u1 && h + 1 == p.H) gather(u + 1);
+      // Rows go out as boxes of 32 rows x 64 columns through shared memory, by
+      // TMA (rows behind the last of the output are clipped): stores of a
+      // lane's own row, 32 bytes at a time, took 6600 cycles a unit, longer
+      // than its MMAs.  Where a row belongs to no sequence each lane stores its own.
+      const bool whole = __all_sync(0xffffffffu, mine != -2 || row >= p.total);
       uint8_t *dst = reinterpret_cast<uint8_t *>(p.kv + ((size_t)row * p.H + h) * 256);
-#pragma unroll 2
-      for (int c = 0; c < 8; c++) {
-        uint32_t v[32];
-        tmem_ld32(lane_base + buf * 256 + 32 * c, v);
+#pragma unroll 1
+      for (int c = 0; c < 4; c++) {
+        uint32_t v[2][32];
+        tmem_ld32(lane_base + buf * 256 + 64 * c, v[0]);
+        tmem_ld32(lane_base + buf * 256 + 64 * c + 32, v[1]);
+        uint8_t *out = base + OFF_OUT + (2 * warp + (c & 1)) * kOutBytes;
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");  // the box before the last is out
         tmem_wait_ld();
-        if (mine == -2) continue;
-        uint32_t w[16];
+        __syncwarp();
 #pragma unroll
-        for (int j = 0; j < 16; j++) {
-          __nv_bfloat162 b2 = __floats2bfloat162_rn(__uint_as_float(v[2 * j]) * out_scale,
-                                                    __uint_as_float(v[2 * j + 1]) * out_scale);
-          w[j] = *reinterpret_cast<uint32_t *>(&b2);
+        for (int k = 0; k < 8; k++) {
+          uint32_t w[4];
+#pragma unroll
+          for (int j = 0; j < 4; j++) {
+            const uint32_t *x = &v[k >> 2][8 * (k & 3) + 2 * j];
+            __nv_bfloat162 b2 = __floats2bfloat162_rn(__uint_as_float(x[0]) * out_scale, __uint_as_float(x[1]) * out_scale);
+            w[j] = *reinterpret_cast<uint32_t *>(&b2);
+          }
+          const uint4 piece = make_uint4(w[0], w[1], w[2], w[3]);
+          if (whole) {
+            *reinterpret_cast<uint4 *>(out + lane * 128 + ((k ^ (lane & 7)) << 4)) = piece;
+          } else if (mine != -2) {
+            *reinterpret_cast<uint4 *>(dst + 128 * c + 16 * k) = piece;
+          }
         }
-        if (p.store_v8) {
-          const uint32_t a8[8] = {w[0], w[1], w[2], w[3], w[4], w[5], w[6], w[7]};
-          const uint32_t b8[8] = {w[8], w[9], w[10], w[11], w[12], w[13], w[14], w[15]};
-          st_global_v8(dst + 64 * c, a8);
-          st_global_v8(dst + 64 * c + 32, b8);
-        } else {
-#pragma unroll
-          for (int j = 0; j < 4; j++)
-            reinterpret_cast<uint4 *>(dst + 64 * c)[j] = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+        if (whole) {
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            const int first = row;  // lane 0's
+            if (first < p.total)
+              asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+                               reinterpret_cast<uint64_t>(&o_map)),
+                           "r"(smem_u32(out)), "r"(64 * c), "r"(h), "r"(first)
+                           : "memory");
+            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+          }
         }
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_remote(mapa(smem_u32(&br->d_empty[buf]), 0));
+      // relaxed: nothing but tensor memory has been read, and the releasing
+      // form would wait for the output's way to memory (3700 cycles a unit)
+      if (lane == 0) mbar_arrive_remote_relaxed(mapa(smem_u32(&br->d_empty[buf]), 0));
     }
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
   } else if (warp == 4) {
     if (lane == 0) {
       const uint64_t pol = policy_evict_normal();
@@ -289,14 +311,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       bool ok = true;
       for (int u = u0; u < u1 && ok; u++) {
         const int h = u % p.H;
-        for (int kb = 0; kb < kSteps; kb++, k++) {
+        for (int kb = 0; kb < kKBlocks; kb++, k++) {
           const uint32_t s = k % kWStages, dst = sw + s * kWStage;
           ok = wait_ok(br, &br->w_empty[s], ((k / kWStages) & 1) ^ 1, p.status);
           if (!ok) break;
           if (rank == 0) mbar_arrive_expect_tx(smem_u32(&br->w_full[s]), 2 * kWStage);
           const uint32_t full = mapa(smem_u32(&br->w_full[s]), 0);
-          tma_load_3d_pair(dst, map, full, 128 * kb, 0, h, pol);
-          tma_load_3d_pair(dst + kWBlock, map, full, 128 * kb + 64, 0, h, pol);
+          tma_load_3d_pair(dst, map, full, 64 * kb, 0, h, pol);
         }
       }
     }
@@ -309,17 +330,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (ok) ok = wait_ok(br, &br->d_empty[buf], ((i >> 1) & 1) ^ 1, p.status);
       if (!ok) break;
       tc_fence_after();
-      for (int kb = 0; kb < kSteps; kb++, k++) {
+      for (int kb = 0; kb < kKBlocks; kb++, k++) {
         const uint32_t s = k % kWStages;
         ok = wait_ok(br, &br->w_full[s], (k / kWStages) & 1, p.status);
         if (!ok) break;
         tc_fence_after();
 #pragma unroll
-        for (int kk = 0; kk < 8; kk++)
-          mma_pair_ss(tmem + buf * 256,
-                      smem_desc_sw128(sa + (2 * kb + (kk >> 2)) * kABlock + (kk & 3) * 32, 16, 1024),
-                      smem_desc_sw128(sw + s * kWStage + (kk >> 2) * kWBlock + (kk & 3) * 32, 16, 1024), IDESC,
-                      (kb | kk) ? 1u : 0u);
+        for (int kk = 0; kk < 4; kk++)
+          mma_pair_ss(tmem + buf * 256, smem_desc_sw128(sa + kb * kABlock + kk * 32, 16, 1024),
+                      smem_desc_sw128(sw + s * kWStage + kk * 32, 16, 1024), IDESC, (kb | kk) ? 1u : 0u);
         mma_commit_pair(smem_u32(&br->w_empty[s]));
       }
       if (ok) mma_commit_pair(smem_u32(&br->d_full[buf]));
@@ -377,9 +396,10 @@ int mla_kv_expand(const void *kv_cache, int kv_format, int num_pages, int page_s
     return fail(MLA_ERR_INVALID_ARG, "int32 arrays must be 4-byte aligned");
   if (kv_format != MLA_KV_BF16 && (!kv_scales || !al(kv_scales, 4)))
     return fail(MLA_ERR_INVALID_ARG, "an FP8 cache needs kv_scales (4-byte aligned)");
-  CUtensorMap uk_map, uv_map;
+  CUtensorMap uk_map, uv_map, o_map;
   if (!make_map_3d(&uk_map, w_uk, D_V, 128, H, uk_row, uk_head, 128, 1) ||
-      !make_map_3d(&uv_map, w_uv, D_V, 128, H, uv_row, uv_head, 128, 1))
+      !make_map_3d(&uv_map, w_uv, D_V, 128, H, uv_row, uv_head, 128, 1) ||
+      !make_map_3d(&o_map, kv, 256, H, total, 256, (int64_t)H * 256, 1, 32))
     return fail(MLA_ERR_CUDA, "cuTensorMapEncodeTiled failed");
   ExpandParams p;
   p.cache = static_cast<const uint8_t *>(kv_cache);
@@ -395,7 +415,6 @@ int mla_kv_expand(const void *kv_cache, int kv_format, int num_pages, int page_s
   p.B = B;
   p.H = H;
   p.total = total;
-  p.store_v8 = al(kv, 32) ? 1 : 0;
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
@@ -403,7 +422,7 @@ int mla_kv_expand(const void *kv_cache, int kv_format, int num_pages, int page_s
   if (e != cudaSuccess) return fail(MLA_ERR_CUDA, cudaGetErrorString(e));
   const long long units = (long long)ceil_div(total, kPairRows) * H;
   const int pairs = (int)(units < sms / 2 ? units : sms / 2);
-  expand_kernel<<<2 * pairs, kThreads, kSmem, (cudaStream_t)stream>>>(uk_map, uv_map, p);
+  expand_kernel<<<2 * pairs, kThreads, kSmem, (cudaStream_t)stream>>>(uk_map, uv_map, o_map, p);
   e = cudaGetLastError();
   if (e != cudaSuccess) return fail(MLA_ERR_CUDA, cudaGetErrorString(e));
   set_last_error("");
