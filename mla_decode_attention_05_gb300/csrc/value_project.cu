@@ -110,31 +110,37 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else if (warp == 5) {
-    if (lane == 0) {
-      const uint32_t idesc = idesc_bf16_f32(128, ntile, false, false);
-      uint32_t u = 0, heads = 0;
-      bool ok = true;
-      for (int i = i0; i < i1 && ok; i++) {
-        const int j = i - i0, buf = j & 1;
-        const bool new_head = i == i0 || i % tiles == 0;
-        heads += new_head ? 1 : 0;
-        ok = wait_ok(br, &br->d_empty[buf], ((j >> 1) & 1) ^ 1, status);
-        for (int k = 0; k < kKBlocks / 2 && ok; k++, u++) {
-          const uint32_t s = u % kUnits;
-          if (new_head) ok = wait_ok(br, &br->w_full[k], (heads - 1) & 1, status);
-          ok = ok && wait_ok(br, &br->full[s], (u / kUnits) & 1, status);
-          if (!ok) break;
-          tc_fence_after();
+    // the whole warp waits, one elected lane issues
+    const uint32_t idesc = idesc_bf16_f32(128, ntile, false, false);
+    uint32_t u = 0, heads = 0;
+    bool ok = true;
+    auto wait = [&](uint64_t *bar, uint32_t parity) {
+      ok = ok && __all_sync(0xffffffffu, wait_ok(br, bar, parity, status));
+    };
+    for (int i = i0; i < i1 && ok; i++) {
+      const int j = i - i0, buf = j & 1;
+      const bool new_head = i == i0 || i % tiles == 0;
+      heads += new_head ? 1 : 0;
+      wait(&br->d_empty[buf], ((j >> 1) & 1) ^ 1);
+      for (int k = 0; k < kKBlocks / 2; k++, u++) {
+        const uint32_t s = u % kUnits;
+        if (new_head) wait(&br->w_full[k], (heads - 1) & 1);
+        wait(&br->full[s], (u / kUnits) & 1);
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < 8; kk++)
             mma_ss(tmem + buf * 64, smem_desc_sw128(smem + (2 * k + (kk >> 2)) * kWBytes + (kk & 3) * 32, 16, 1024),
                    smem_desc_sw128(smem + OFF_RING + s * kUnit + (kk >> 2) * box + (kk & 3) * 32, 16, 1024), idesc,
                    (k | kk) ? 1u : 0u);
           mma_commit(smem_u32(&br->empty[s]));
+          if (k == kKBlocks / 2 - 1) {
+            mma_commit(smem_u32(&br->d_full[buf]));
+            if (i + 1 == i1 || (i + 1) % tiles == 0) mma_commit(smem_u32(&br->w_empty));
+          }
         }
-        if (!ok) break;
-        mma_commit(smem_u32(&br->d_full[buf]));
-        if (i + 1 == i1 || (i + 1) % tiles == 0) mma_commit(smem_u32(&br->w_empty));
+        __syncwarp();
       }
     }
   } else {
