@@ -107,7 +107,7 @@ struct Order {
 // The cache rows of the 32 packed rows from r0 on, one a lane: the row's index
 // in the pool, -1 for one that cannot be read (written as zeros) and -2 for one
 // that belongs to no sequence (left as it was).
-__device__ long long row_source(const ExpandParams &p, int r0, int lane) {
+__device__ int row_source(const ExpandParams &p, int r0, int lane) {
   const int r = r0 + lane;
   // the last sequence that starts at or before r0, by 32 probes at a time ...
   int lo = 0, hi = p.B;
@@ -139,7 +139,7 @@ __device__ long long row_source(const ExpandParams &p, int r0, int lane) {
     atomicOr(p.status, MLA_STATUS_BAD_PAGE);
     return -1;
   }
-  return (long long)page * PAGE + pos % PAGE;
+  return page * PAGE + pos % PAGE;  // (the host has checked that the pool's rows fit)
 }
 
 // 16 e4m3 codes times sc -> 16 bf16 (the products rounded once).
@@ -160,69 +160,83 @@ __device__ __forceinline__ uint32_t a_off(int r, int c) {
   return (uint32_t)(c >> 3) * kABlock + (uint32_t)r * 128 + (uint32_t)(((c & 7) ^ (r & 7)) << 4);
 }
 
+// 16 bytes, or 16 zero bytes where `bytes` is 0 (nothing is read then).
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(src)),
+               "r"(bytes)
+               : "memory");
+}
+
 // Warp w fetches rows 32w .. 32w + 31 of the block at row0 into A; src: the
-// lane's own row.  With `pe` it also writes the rows' k_pe.
-__device__ void gather_rows(const ExpandParams &p, uint8_t *a, int row0, int warp, int lane, long long src, bool pe) {
-  const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-  if (p.format == MLA_KV_BF16) {
-    constexpr int kBatch = 8;
-    for (int i = 0; i < 32; i += kBatch) {
-      uint4 v[kBatch][2], q[kBatch];
-#pragma unroll
-      for (int j = 0; j < kBatch; j++) {
-        const long long s = __shfl_sync(0xffffffffu, src, i + j);
-        const uint4 *row = reinterpret_cast<const uint4 *>(p.cache + (size_t)(s < 0 ? 0 : s) * (D_QK * 2));
-        v[j][0] = s < 0 ? zero : __ldg(row + lane);
-        v[j][1] = s < 0 ? zero : __ldg(row + 32 + lane);
-        q[j] = (s < 0 || !pe || lane >= 8) ? zero : __ldg(row + 64 + lane);
-      }
-#pragma unroll
-      for (int j = 0; j < kBatch; j++) {
-        const int r = warp * 32 + i + j;
-        *reinterpret_cast<uint4 *>(a + a_off(r, lane)) = v[j][0];
-        *reinterpret_cast<uint4 *>(a + a_off(r, 32 + lane)) = v[j][1];
-        const long long s = __shfl_sync(0xffffffffu, src, i + j);
-        if (pe && s != -2 && lane < 8)
-          reinterpret_cast<uint4 *>(p.k_pe + (size_t)(row0 + r) * D_ROPE)[lane] = q[j];
-      }
-    }
-    return;
+// lane's own row.  With `pe` it also writes the rows' k_pe.  All of the warp's
+// rows are on their way at once (16 to 32 KB): fetched eight rows at a time a
+// block took 16000 cycles, four memory latencies under load.
+__device__ void gather_rows(const ExpandParams &p, uint8_t *a, int row0, int warp, int lane, int src, bool pe) {
+  const uint32_t sa = smem_u32(a);
+  const bool bf16 = p.format == MLA_KV_BF16, tile = p.format == MLA_KV_FP8_E4M3;
+  const int row_bytes = bf16 ? 2 * D_QK : tile ? FP8_ROW : D_QK;
+  // Latent values: bf16 rows straight to their place, codes into the upper
+  // half of it (pieces 32..63), from where they are expanded below, and the
+  // four scales of a row into its first piece.
+#pragma unroll 4
+  for (int i = 0; i < 32; i++) {  // (no branches: the addresses of four rows at a time)
+    const int s = __shfl_sync(0xffffffffu, src, i);
+    const int r = warp * 32 + i;
+    const uint8_t *row = p.cache + (size_t)(s < 0 ? 0 : s) * row_bytes + lane * 16;
+    const uint32_t bytes = s < 0 ? 0u : 16u;
+    cp_async16(sa + a_off(r, 32 + lane), row + (bf16 ? 512 : 0), bytes);
+    if (bf16) cp_async16(sa + a_off(r, lane), row, bytes);
+    if (tile && lane == 0) cp_async16(sa + a_off(r, 0), p.scales + (size_t)(s < 0 ? 0 : s) * 4, bytes);
   }
-  const bool tile = p.format == MLA_KV_FP8_E4M3;
-  const int row_bytes = tile ? FP8_ROW : D_QK;
-  const float one = tile ? 0.f : __ldg(p.scales);
-  constexpr int kBatch = 8;
-  for (int i = 0; i < 32; i += kBatch) {
-    uint4 v[kBatch], q[kBatch];
-    float sc[kBatch];
+  if (pe) {  // four rows at a time, eight lanes each
+    const int sub = lane & 7;
+    const float one = p.format == MLA_KV_FP8_E4M3_TENSOR ? __ldg(p.scales) : 1.f;
+    uint4 q[8];
 #pragma unroll
-    for (int j = 0; j < kBatch; j++) {
-      const long long s = __shfl_sync(0xffffffffu, src, i + j);
-      const uint8_t *row = p.cache + (size_t)(s < 0 ? 0 : s) * row_bytes;
-      v[j] = s < 0 ? zero : __ldg(reinterpret_cast<const uint4 *>(row) + lane);
-      sc[j] = (tile && s >= 0) ? __ldg(p.scales + s * 4 + (lane >> 3)) : 1.f;
-      // k_pe: 8 pieces of 16 bytes, or 4 pieces of 16 codes
-      q[j] = (s < 0 || !pe || lane >= (tile ? 8 : 4)) ? zero : __ldg(reinterpret_cast<const uint4 *>(row + D_V) + lane);
-    }
-#pragma unroll
-    for (int j = 0; j < kBatch; j++) {
-      const int r = warp * 32 + i + j;
-      uint32_t o[8];
-      dequant(v[j], sc[j], o);
-      *reinterpret_cast<uint4 *>(a + a_off(r, 2 * lane)) = make_uint4(o[0], o[1], o[2], o[3]);
-      *reinterpret_cast<uint4 *>(a + a_off(r, 2 * lane + 1)) = make_uint4(o[4], o[5], o[6], o[7]);
-      const long long s = __shfl_sync(0xffffffffu, src, i + j);
-      if (pe && s != -2) {
-        uint4 *dst = reinterpret_cast<uint4 *>(p.k_pe + (size_t)(row0 + r) * D_ROPE);
-        if (tile) {
-          if (lane < 8) dst[lane] = q[j];
-        } else if (lane < 4) {
-          dequant(q[j], one, o);
-          dst[2 * lane] = make_uint4(o[0], o[1], o[2], o[3]);
-          dst[2 * lane + 1] = make_uint4(o[4], o[5], o[6], o[7]);
+    for (int i = 0; i < 8; i++) {
+      const int s = __shfl_sync(0xffffffffu, src, 4 * i + (lane >> 3));
+      const uint8_t *at = p.cache + (size_t)(s < 0 ? 0 : s) * row_bytes + (bf16 ? 2 * D_V : D_V);
+      q[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (s >= 0) {
+        if (bf16 || tile) {
+          q[i] = __ldg(reinterpret_cast<const uint4 *>(at) + sub);
+        } else {  // eight codes a lane
+          const uint2 v = __ldg(reinterpret_cast<const uint2 *>(at) + sub);
+          uint32_t o[8];
+          dequant(make_uint4(v.x, v.y, 0u, 0u), one, o);
+          q[i] = make_uint4(o[0], o[1], o[2], o[3]);
         }
       }
     }
+#pragma unroll
+    for (int i = 0; i < 8; i++) {
+      const int s = __shfl_sync(0xffffffffu, src, 4 * i + (lane >> 3));
+      if (s != -2)
+        reinterpret_cast<uint4 *>(p.k_pe + (size_t)(row0 + warp * 32 + 4 * i + (lane >> 3)) * D_ROPE)[sub] = q[i];
+    }
+  }
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  __syncwarp();
+  if (bf16) return;
+  // (little code: it runs once or twice a launch, and unrolled further it costs
+  // more in instruction fetches than it hides)
+  const int t = lane >> 3;
+  uint4 next = *reinterpret_cast<const uint4 *>(a + a_off(warp * 32, 32 + lane));
+  float next_scale = tile ? *reinterpret_cast<const float *>(a + a_off(warp * 32, 0) + 4 * t) : 1.f;
+#pragma unroll 2
+  for (int i = 0; i < 32; i++) {
+    const int r = warp * 32 + i;
+    const uint4 v = next;
+    const float scale = next_scale;
+    if (i < 31) {
+      next = *reinterpret_cast<const uint4 *>(a + a_off(r + 1, 32 + lane));
+      if (tile) next_scale = *reinterpret_cast<const float *>(a + a_off(r + 1, 0) + 4 * t);
+    }
+    uint32_t o[8];
+    dequant(v, scale, o);
+    __syncwarp();  // the row's codes are all read before its values are written
+    *reinterpret_cast<uint4 *>(a + a_off(r, 2 * lane)) = make_uint4(o[0], o[1], o[2], o[3]);
+    *reinterpret_cast<uint4 *>(a + a_off(r, 2 * lane + 1)) = make_uint4(o[4], o[5], o[6], o[7]);
   }
 }
 
@@ -266,7 +280,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const float out_scale = p.format == MLA_KV_FP8_E4M3_TENSOR ? __ldg(p.scales) : 1.f;
     const uint32_t lane_base = tmem + ((uint32_t)(warp * 32) << 16);
     const uint64_t pol_out = policy_evict_first();
-    long long src = -2;
+    int src = -2;
     // this block's rows
     auto gather = [&](int u) {
       const int row0 = u / p.H * kPairRows + (int)rank * kM;
@@ -282,7 +296,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const bool ok = __all_sync(0xffffffffu, wait_ok(br, &br->d_full[buf], (i >> 1) & 1, p.status));
       if (!ok) break;
       tc_fence_after();
-      const long long mine = src;
+      const int mine = src;
       const int row = u / p.H * kPairRows + (int)rank * kM + warp * 32 + lane, h = u % p.H;
       // the next unit's rows first: every MMA that reads A has completed
       if (i + 1 < n && order.new_rows(i + 1)) gather(order.unit(i + 1));
@@ -421,6 +435,7 @@ int mla_kv_expand(const void *kv_cache, int kv_format, int num_pages, int page_s
     return fail(MLA_ERR_INVALID_ARG, "kv_format unknown");
   if (page_size != MLA_PAGE_SIZE) return fail(MLA_ERR_UNSUPPORTED, "page_size must be 64");
   if (num_pages < 1 || max_pages < 1) return fail(MLA_ERR_INVALID_ARG, "num_pages and max_pages must be >= 1");
+  if (num_pages > 0x7FFFFFFF / MLA_PAGE_SIZE) return fail(MLA_ERR_UNSUPPORTED, "num_pages must be below 2^25");
   if (uk_row % 8 || uk_head % 8 || uv_row % 8 || uv_head % 8)
     return fail(MLA_ERR_INVALID_ARG, "weight strides must be multiples of 8 elements");
   if (uk_row < D_V || uv_row < D_V || (H > 1 && (uk_head < D_V || uv_head < D_V)))
@@ -436,8 +451,8 @@ int mla_kv_expand(const void *kv_cache, int kv_format, int num_pages, int page_s
     return fail(MLA_ERR_INVALID_ARG, "kv_cache, w_uk, w_uv, kv and k_pe must be 16-byte aligned");
   if (!al(block_table, 4) || !al(cu_seqlens, 4))
     return fail(MLA_ERR_INVALID_ARG, "int32 arrays must be 4-byte aligned");
-  if (kv_format != MLA_KV_BF16 && (!kv_scales || !al(kv_scales, 4)))
-    return fail(MLA_ERR_INVALID_ARG, "an FP8 cache needs kv_scales (4-byte aligned)");
+  if (kv_format != MLA_KV_BF16 && (!kv_scales || !al(kv_scales, kv_format == MLA_KV_FP8_E4M3 ? 16 : 4)))
+    return fail(MLA_ERR_INVALID_ARG, "an FP8 cache needs kv_scales (16-byte aligned per row, 4 for one scale)");
   CUtensorMap uk_map, uv_map, o_map;
   if (!make_map_3d(&uk_map, w_uk, D_V, 128, H, uk_row, uk_head, 128, 1) ||
       !make_map_3d(&uv_map, w_uv, D_V, 128, H, uv_row, uv_head, 128, 1) ||

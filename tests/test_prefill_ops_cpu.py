@@ -48,7 +48,7 @@ def test_insert_rope_arguments(L, args, code):
     (dict(fmt=3), -1), (dict(page=32), -2), (dict(pages=0), -1), (dict(max_pages=0), -1), (dict(uk_row=500), -1),
     (dict(uk_row=516), -1), (dict(uv_head=60), -1), (dict(uv_row=8), -1), (dict(kv=None), -1), (dict(kv=8), -1),
     (dict(uk=None), -1), (dict(uv=264), -1), (dict(pe=264), -1), (dict(bt=258), -1), (dict(cu=257), -1),
-    (dict(fmt=1, sc=None), -1), (dict(fmt=2, sc=258), -1), (dict(cache=264), -1),
+    (dict(fmt=1, sc=None), -1), (dict(fmt=1, sc=264), -1), (dict(fmt=2, sc=258), -1), (dict(pages=1 << 25), -2), (dict(cache=264), -1),
     (dict(total=0, kv=None, pe=None), 0), (dict(B=0), 0),
 ])
 def test_expand_arguments(L, args, code):
