@@ -19,11 +19,13 @@
 // bf16 once.  Scores, m, l and O are fp32.
 //
 // Values that a row does not see must not reach it, whatever they hold: 0 * inf
-// and 0 * nan in P V would.  In the tiles where some row sees only a part of
-// the keys, a warp looks through the values in shared memory, replaces what is
-// not finite by zero before the MMA reads it and notes the key; rows that do
-// see such a key add its non-finite values at the end.  (A weight is positive,
-// so inf and nan reach the row's output as they are.)
+// and 0 * nan in P V would.  Such a row comes out as nan.  So a unit of work in
+// which some row sees only a part of its keys, and some output is not finite, is
+// done again: then a warp looks through the values of those steps in shared
+// memory, replaces what is not finite by zero before the MMA reads it and notes
+// the key, and rows that do see such a key add its non-finite values at the
+// end.  (A weight is positive, so inf and nan reach the row's output as they
+// are.)  Looking through all values the first time cost ragged prompts a third.
 #include <cstddef>
 
 #include "common.cuh"
@@ -87,13 +89,17 @@ struct Work {
   int k0, nk;  // first key, keys
   int diff;    // row i sees min(nk, max(0, diff + i + 1)) of them
   int h, split;
+  int block;   // the block of the grid that it is
 };
 
 // Steps over its keys: n[t] of tile t, of which those from `masked` on hold
-// keys that some row of a tile does not see.
+// keys that some row of a tile does not see.  The values of the steps from
+// `look` on are looked through.
 struct Steps {
-  int n[2], most, masked;
+  int n[2], most, masked, look;
 };
+constexpr int kNever = 1 << 30;
+constexpr int kRedo = 64;
 
 struct Bars {
   uint64_t full[kUnits], empty[kUnits];
@@ -103,14 +109,17 @@ struct Bars {
   uint64_t p_full[2][2];  // its probabilities are: of the first and the last 64 keys
   uint64_t o_done[2];   // its P V has been added
   uint64_t o_free[2];   // its output has been read
-  uint64_t v_look;      // the values of a masked step are there (told by the waiting warp: the ring's barriers
+  uint64_t v_look;      // the values of a step are there (told by the waiting warp: the ring's barriers
                         // can be a phase further than a warp that does not follow every unit)
   uint64_t v_ok;        // they have been looked through
   uint64_t next_full;   // the answer to a request for the next unit of work
   uint4 next;           // (16 bytes, 16-byte aligned)
   Work work[2];
   Steps steps[2];
-  uint32_t bad_keys[2][16];  // keys with a non-finite value, from the first masked step on
+  uint32_t bad_keys[2][16];  // keys with a non-finite value, from step `look` on
+  uint32_t odd[2];           // the work's output is not finite
+  uint32_t redo_count;       // works to be done again, so far
+  int redo[kRedo];           // their blocks (a ring)
   uint32_t tmem_base;
   int abort;
 };
@@ -166,7 +175,8 @@ __device__ Work find_work(const PrefillParams &p, int t, int h, int lane) {
 
 __device__ __forceinline__ Steps steps_of(const Work &w) {
   Steps s;
-  s.masked = 1 << 30;
+  s.masked = kNever;
+  s.look = kNever;
 #pragma unroll
   for (int t = 0; t < 2; t++) {
     const int first = t * kRows, last = min(w.nq, first + kRows) - 1;
@@ -278,58 +288,88 @@ __device__ __forceinline__ void load_work(const CUtensorMap *q_map, const CUtens
                                           const CUtensorMap *kp_map, const CUtensorMap *v_map, Bars *br,
                                           uint32_t smem, const PrefillParams &p, int lane) {
   const uint64_t pol = policy_evict_normal(), once = policy_evict_first();
-  int block = blockIdx.x;
-  uint32_t u = 0, asked = 0, count = 0, tiles0 = 0, tiles1 = 0;
+  uint32_t u = 0, asked = 0, count = 0, redone = 0, tiles0 = 0, tiles1 = 0;
   bool ok = true;
+  // the slot that unit of work number n gets is free
+  auto slot_free = [&](uint32_t n) {
+    ok = ok && wait_ok(br, &br->work_empty[n & 1], ((n >> 1) & 1) ^ 1, p.status);
+  };
   auto tell = [&](const Work &w, const Steps &st) {
     const uint32_t slot = count & 1;
-    ok = wait_ok(br, &br->work_empty[slot], ((count >> 1) & 1) ^ 1, p.status);
+    slot_free(count);
     if (!ok) return;
     br->work[slot] = w;
     br->steps[slot] = st;
+    br->odd[slot] = 0;
     mbar_arrive(smem_u32(&br->work_full[slot]));
     count++;
   };
-  for (;;) {
-    if (lane == 0) ask_next(br);
-    const Work w = block_work(p, block, lane);
-    if (w.nq > 0 && lane == 0) {
-      const Steps st = steps_of(w);
-      tell(w, st);
+  auto process = [&](int block, bool look) {
+    Work w = block_work(p, block, lane);
+    w.block = block;
+    if (w.nq == 0 || lane != 0) return;
+    Steps st = steps_of(w);
+    if (look) st.look = st.masked;
+    tell(w, st);
 #pragma unroll
-      for (int t = 0; t < 2; t++) {
-        if (st.n[t] == 0 || !ok) continue;
-        ok = wait_ok(br, &br->q_empty[t], ((t == 0 ? tiles0++ : tiles1++) & 1) ^ 1, p.status);
-        if (!ok) continue;
-        mbar_arrive_expect_tx(smem_u32(&br->q_full[t]), 3 * kUnit);
-        for (int c = 0; c < 3; c++)
-          tma_load_3d(smem + (3 * t + c) * kUnit, q_map, smem_u32(&br->q_full[t]), 64 * c, w.h, w.q0 + t * kRows, once);
-      }
-      for (int j = 0; j < st.most && ok; j++) {
-        const int key = w.k0 + j * kKeys;
+    for (int t = 0; t < 2; t++) {
+      if (st.n[t] == 0 || !ok) continue;
+      ok = wait_ok(br, &br->q_empty[t], ((t == 0 ? tiles0++ : tiles1++) & 1) ^ 1, p.status);
+      if (!ok) continue;
+      mbar_arrive_expect_tx(smem_u32(&br->q_full[t]), 3 * kUnit);
+      for (int c = 0; c < 3; c++)
+        tma_load_3d(smem + (3 * t + c) * kUnit, q_map, smem_u32(&br->q_full[t]), 64 * c, w.h, w.q0 + t * kRows, once);
+    }
+    for (int j = 0; j < st.most && ok; j++) {
+      const int key = w.k0 + j * kKeys;
 #pragma unroll 1
-        for (int c = 0; c < kUnitsPerStep; c++, u++) {
-          const uint32_t s = u % kUnits, full = smem_u32(&br->full[s]), dst = smem + OFF_RING + s * kUnit;
-          ok = wait_ok(br, &br->empty[s], ((u / kUnits) & 1) ^ 1, p.status);
-          if (!ok) break;
-          mbar_arrive_expect_tx(full, kUnit);
-          if (c < 2) {
-            tma_load_3d(dst, kn_map, full, 64 * c, w.h, key, pol);
-          } else if (c == 2) {
-            tma_load_3d(dst, kp_map, full, 0, 0, key, pol);
-          } else {
-            tma_load_3d(dst, v_map, full, 0, w.h, key + 64 * (c - 3), pol);
-            tma_load_3d(dst + kUnit / 2, v_map, full, 64, w.h, key + 64 * (c - 3), pol);
-          }
+      for (int c = 0; c < kUnitsPerStep; c++, u++) {
+        const uint32_t s = u % kUnits, full = smem_u32(&br->full[s]), dst = smem + OFF_RING + s * kUnit;
+        ok = wait_ok(br, &br->empty[s], ((u / kUnits) & 1) ^ 1, p.status);
+        if (!ok) break;
+        mbar_arrive_expect_tx(full, kUnit);
+        if (c < 2) {
+          tma_load_3d(dst, kn_map, full, 64 * c, w.h, key, pol);
+        } else if (c == 2) {
+          tma_load_3d(dst, kp_map, full, 0, 0, key, pol);
+        } else {
+          tma_load_3d(dst, v_map, full, 0, w.h, key + 64 * (c - 3), pol);
+          tma_load_3d(dst + kUnit / 2, v_map, full, 64, w.h, key + 64 * (c - 3), pol);
         }
       }
     }
-    // (also after a wait that gave up: the answer has to land before the CTA ends)
-    const bool told = warp_wait_ok(br, &br->next_full, asked++ & 1, p.status);
-    ok = __shfl_sync(0xffffffffu, (int)ok, 0) && told;
-    block = told ? next_block(br) : -1;
+  };
+  // Blocks of the grid one after the other.  When there are no more, or many
+  // units of work wait to be done again (never more than the ring holds: two are
+  // under way beside this), all that is under way is let finish, and they are.
+  int block = blockIdx.x;
+  for (;;) {
+    const uint32_t waiting = __shfl_sync(0xffffffffu, *(volatile uint32_t *)&br->redo_count, 0) - redone;
+    const bool redo = block < 0 || waiting >= kRedo / 2;
+    int now = block;
+    if (redo) {
+      if (lane == 0) {
+        slot_free(count);
+        slot_free(count + 1);
+      }
+      ok = __shfl_sync(0xffffffffu, (int)ok, 0);
+      __syncwarp();
+      if (!ok || *(volatile uint32_t *)&br->redo_count == redone) break;
+      now = *(volatile int *)&br->redo[redone++ % kRedo];
+    } else if (lane == 0) {
+      ask_next(br);
+    }
     __syncwarp();
-    if (!ok || block < 0) break;
+    process(now, redo);
+    if (!redo) {
+      // (also after a wait that gave up: the answer has to land before the CTA ends)
+      const bool told = warp_wait_ok(br, &br->next_full, asked++ & 1, p.status);
+      ok = ok && told;
+      block = told ? next_block(br) : -1;
+    }
+    ok = __shfl_sync(0xffffffffu, (int)ok, 0);
+    __syncwarp();
+    if (!ok) break;
   }
   if (ok && lane == 0) {
     Work none;
@@ -421,7 +461,7 @@ __device__ __forceinline__ void mma_sequence(Bars *br, uint32_t smem, uint32_t t
 #pragma unroll 1
     for (int j = -1; j < st.most; j++) {
       const uint32_t uv = base + (uint32_t)(j * kUnitsPerStep + 3);
-      if (j >= st.masked) {
+      if (j >= st.look) {
         if (kWaiter) {
           wait_for(uv, 2, nullptr, 0, nullptr, 0);
           if (ok && elect_one()) mbar_arrive(smem_u32(&br->v_look));
@@ -465,7 +505,7 @@ __device__ __forceinline__ void mma_sequence(Bars *br, uint32_t smem, uint32_t t
   }
 }
 
-// The whole warp looks through the values of every masked step.
+// The whole warp looks through the values of the steps from `look` on.
 __device__ __forceinline__ void check_values(Bars *br, uint8_t *ring, int lane, unsigned int *status) {
   uint32_t base = 0, looks = 0;
   for (uint32_t count = 0;; count++) {
@@ -476,7 +516,7 @@ __device__ __forceinline__ void check_values(Bars *br, uint8_t *ring, int lane, 
     // (no row reads this slot's keys any more: the slot was given back after its output)
     if (lane < 16) br->bad_keys[slot][lane] = 0;
     __syncwarp();
-    for (int j = st.masked; j < st.most; j++) {
+    for (int j = st.look; j < st.most; j++) {
       if (!warp_wait_ok(br, &br->v_look, looks++ & 1, status)) return;
       bool patched = false;
       for (int c = 0; c < 2; c++) {
@@ -520,7 +560,7 @@ __device__ __forceinline__ void check_values(Bars *br, uint8_t *ring, int lane, 
           }
           if (!bad) continue;
           *reinterpret_cast<uint4 *>(unit + i * 16) = make_uint4(x[0], x[1], x[2], x[3]);
-          const int key = (j - st.masked) * kKeys + c * 64 + ((i * 16) % (int)(kUnit / 2)) / 128;
+          const int key = (j - st.look) * kKeys + c * 64 + ((i * 16) % (int)(kUnit / 2)) / 128;
           if (key < 512) atomicOr(&br->bad_keys[slot][key >> 5], 1u << (key & 31));
           patched = true;
         }
@@ -538,7 +578,7 @@ __device__ __forceinline__ void check_values(Bars *br, uint8_t *ring, int lane, 
 // One row a thread: the softmax of tile t over the steps of one unit of work,
 // then its output.  done: the tile's steps before this unit.
 __device__ __forceinline__ bool softmax_work(const PrefillParams &p, Bars *br, uint32_t tmem, const Work &w,
-                                             const Steps &st, const uint32_t *bad_keys, int t, uint32_t done) {
+                                             const Steps &st, int slot, int t, uint32_t done) {
   const int warp = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
   const int i = t * kRows + warp * 32 + lane;  // the CTA's row
   const int seen = visible(w, i);
@@ -644,10 +684,12 @@ __device__ __forceinline__ bool softmax_work(const PrefillParams &p, Bars *br, u
     tc_fence_after();
   }
   const float inv = l != 0.f ? 1.f / l : 0.f;
-  // do masked steps hold non-finite values?
+  // have the steps that were looked through non-finite values?
+  const uint32_t *bad_keys = br->bad_keys[slot];
   bool bad = false;
-  if (n > 0 && st.masked < st.most)
+  if (n > 0 && st.look < st.most)
     for (int k = 0; k < 16; k++) bad |= *(volatile const uint32_t *)&bad_keys[k] != 0;
+  float zero = 0.f;  // becomes nan if an output is not finite
   const size_t row = w.q0 + i;
   __nv_bfloat16 *dst = p.out + (row * p.H + w.h) * kDv;
   float *part = p.part_o + ((w.split * (size_t)p.Nq + row) * p.H + w.h) * kDv;
@@ -660,7 +702,10 @@ __device__ __forceinline__ bool softmax_work(const PrefillParams &p, Bars *br, u
     }
     if (!live) continue;
 #pragma unroll
-    for (int e = 0; e < 32; e++) o[e] = none ? 0u : __float_as_uint(__uint_as_float(o[e]) * inv);
+    for (int e = 0; e < 32; e++) {
+      zero = fmaf(__uint_as_float(o[e]), 0.f, zero);
+      o[e] = none ? 0u : __float_as_uint(__uint_as_float(o[e]) * inv);
+    }
     if (p.splits > 1) {
 #pragma unroll
       for (int k = 0; k < 4; k++) {
@@ -692,11 +737,15 @@ __device__ __forceinline__ bool softmax_work(const PrefillParams &p, Bars *br, u
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_u32(&br->o_free[t]));
   }
+  // once more, with a look at the values
+  if (st.masked < st.most && st.look == kNever && __any_sync(0xffffffffu, n > 0 && live && !none && zero != 0.f)) {
+    if (lane == 0 && atomicExch(&br->odd[slot], 1u) == 0) br->redo[atomicAdd(&br->redo_count, 1u) % kRedo] = w.block;
+  }
   if (live && bad) {  // rare: add the non-finite values of the keys that this row sees
 #pragma unroll 1
     for (int k = 0; k < 512; k++) {
       if (!((*(volatile const uint32_t *)&bad_keys[k >> 5] >> (k & 31)) & 1u)) continue;
-      const int key = st.masked * kKeys + k;
+      const int key = st.look * kKeys + k;
       if (key >= seen) continue;
       const __nv_bfloat16 *vr = p.v + (size_t)(w.k0 + key) * p.v_tok + (size_t)w.h * p.v_head;
 #pragma unroll 1
@@ -724,7 +773,7 @@ __device__ __forceinline__ void softmax_rows(const PrefillParams &p, Bars *br, u
     const Work w = br->work[slot];
     if (w.nq == 0) return;
     const Steps st = br->steps[slot];
-    if (!softmax_work(p, br, tmem, w, st, br->bad_keys[slot], t, done)) return;
+    if (!softmax_work(p, br, tmem, w, st, (int)slot, t, done)) return;
     done += t == 0 ? st.n[0] : st.n[1];
     __syncwarp();
     if ((threadIdx.x & 31) == 0) mbar_arrive(smem_u32(&br->work_empty[slot]));
@@ -801,6 +850,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(smem_u32(&br->v_look), 1);
     mbar_init(smem_u32(&br->v_ok), 1);
     mbar_init(smem_u32(&br->next_full), 1);
+    br->redo_count = 0;
     br->abort = 0;
     fence_mbar_init_cluster();
   }

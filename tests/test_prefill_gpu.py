@@ -179,6 +179,21 @@ def test_a_value_that_is_not_finite_reaches_the_rows_that_see_it(bad):
     assert torch.equal(out[~hit], want[~hit]) and torch.equal(lse, wl)
 
 
+def test_many_units_of_work_are_done_again():
+    """Every unit of work holds a value that its earlier rows do not see and
+    that is not finite: more than wait to be done again at a time."""
+    import mla_decode_attention_05_gb300 as mla
+    B, H = 60, 128
+    nq = [3] * B
+    ins = _inputs(nq, nq, H, 19)
+    base, bl = mla.prefill(*ins, cu(nq), cu(nq), softmax_scale=SCALE)
+    ins[3][2::3] = float("nan")
+    out, lse = mla.prefill(*ins, cu(nq), cu(nq), softmax_scale=SCALE)
+    last = torch.arange(3 * B, device="cuda") % 3 == 2
+    assert torch.equal(out[~last], base[~last]) and torch.equal(lse, bl)
+    assert bool(out[last].isnan().all()) and mla.device_status() == 0
+
+
 def test_lengths_out_of_order_are_clamped():
     """cu_seqlens that leave the rows there are, or go back: a status bit, no
     access outside, and the sequences before them as they are."""
