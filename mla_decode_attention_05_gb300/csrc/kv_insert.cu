@@ -251,9 +251,9 @@ __device__ __forceinline__ bool position_ok(long long pos, int max_pos, unsigned
   return false;
 }
 
-// Query rows: each warp takes eight heads of one token at a time, as two
-// groups of four rows.
-constexpr int kQHeads = 8;
+// Query rows: each warp takes sixteen heads of one token at a time, as groups
+// of four rows (2 KB on their way for each warp).
+constexpr int kQHeads = 16;
 __device__ void rotate_queries(const KvInsertParams &p, const RopeParams &r, int unit, int stride) {
   const int lane = threadIdx.x & 31, sub = lane & 7;
   const int groups = (r.H + kQHeads - 1) / kQHeads;
@@ -263,16 +263,17 @@ __device__ void rotate_queries(const KvInsertParams &p, const RopeParams &r, int
     const long long pos = __ldg(reinterpret_cast<const long long *>(r.positions) + n);
     if (!position_ok(pos, r.max_pos, p.status, lane == 0)) continue;
     const float *cs = r.cos_sin + pos * 64;
-    uint4 x[2];
+    uint4 x[kQHeads / 4];
 #pragma unroll
-    for (int i = 0; i < 2; i++) {
+    for (int i = 0; i < kQHeads / 4; i++) {
       const int h = h0 + 4 * i + (lane >> 3);
       x[i] = make_uint4(0u, 0u, 0u, 0u);
       if (h < r.H) x[i] = *reinterpret_cast<const uint4 *>(r.q_pe + n * r.q_tok + h * r.q_head + 8 * sub);
     }
 #pragma unroll
-    for (int i = 0; i < 2; i++) {
+    for (int i = 0; i < kQHeads / 4; i++) {
       const int h = h0 + 4 * i + (lane >> 3);
+      if (h0 + 4 * i >= r.H) break;  // (the same for the whole warp)
       const uint4 y = rotate8(x[i], sub, cs, r.interleaved);
       if (h < r.H) *reinterpret_cast<uint4 *>(r.q_out + n * r.o_tok + h * r.o_head + 8 * sub) = y;
     }
@@ -282,10 +283,16 @@ __device__ void rotate_queries(const KvInsertParams &p, const RopeParams &r, int
 template <bool kRope>
 __global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm)
     kv_insert_kernel(KvInsertParams p, RopeParams r, int insert_blocks) {
-  if (kRope && (int)blockIdx.x >= insert_blocks) {
-    rotate_queries(p, r, ((int)blockIdx.x - insert_blocks) * kWarps + ((int)threadIdx.x >> 5),
-                   ((int)gridDim.x - insert_blocks) * kWarps);
-    return;
+  // Blocks of both kinds are spread evenly over the grid, so that the queries'
+  // stream runs beside the inserts' arithmetic on every SM.
+  int block = blockIdx.x;
+  if (kRope) {
+    const int grid = gridDim.x, before = (int)((long long)block * insert_blocks / grid);
+    if ((int)((long long)(block + 1) * insert_blocks / grid) == before) {
+      rotate_queries(p, r, (block - before) * kWarps + ((int)threadIdx.x >> 5), (grid - insert_blocks) * kWarps);
+      return;
+    }
+    block = before;
   }
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ uint32_t sc_tab[256], inv_tab[256];  // fp32(m / 448), fp32(1 / that), m = 0..255
@@ -297,7 +304,7 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm)
   }
   __syncthreads();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int first = blockIdx.x * kWarps + warp;
+  const int first = block * kWarps + warp;
   const int stride = insert_blocks * kWarps;
   if (first >= p.N) return;
   uint8_t *ring = smem + warp * kStages * kStageBytes;
@@ -360,8 +367,11 @@ cudaError_t launch_kv_insert_rope(const KvInsertParams &p, const RopeParams &r, 
   const long long need = ((long long)p.N + kWarps - 1) / kWarps;
   const long long q_units = r.q_pe ? (long long)p.N * ((r.H + kQHeads - 1) / kQHeads) : 0;
   const long long q_need = (q_units + kWarps - 1) / kWarps;
-  const int blocks = (int)(need < most ? need : most);
-  const int q_blocks = (int)(q_need < 2 * most ? q_need : 2 * most);
+  // All blocks run at once.  With queries, which are most of the bytes, the
+  // inserts get what those leave, at least a block (8 tokens at a time) on each SM.
+  const long long rest = q_need + sms < most ? most - q_need : sms;
+  const int blocks = (int)(need < rest ? need : rest);
+  const int q_blocks = (int)(q_need < most - blocks ? q_need : most - blocks);
   kv_insert_kernel<true><<<blocks + q_blocks, kWarps * 32, kSmemBytes, stream>>>(p, r, blocks);
   return cudaGetLastError();
 }
