@@ -427,6 +427,8 @@ int mla_kv_expand(const void *kv_cache, int kv_format, int num_pages, int page_s
  *                the GPU need separate ones.
  *   out          device bf16 [Nq][H][128], lse device fp32 [H][Nq], written;
  *                rows of no sequence are left as they were
+ * At most 2^20 sequences, 2^30 query rows and 2^26 key rows
+ * (MLA_ERR_UNSUPPORTED above).
  * Probabilities are rounded to bf16 before they multiply v; scores, sums and
  * outputs are accumulated in fp32.  A wait that gives up sets
  * MLA_STATUS_WAIT_TIMEOUT.  Asynchronous on `stream`; can be captured in a

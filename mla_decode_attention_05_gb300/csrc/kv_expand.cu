@@ -119,12 +119,14 @@ __device__ int row_source(const ExpandParams &p, int r0, int lane) {
   }
   // ... and from there each lane's own
   int start = __ldg(p.cu + lo), end = __ldg(p.cu + lo + 1);
-  while (__any_sync(0xffffffffu, lo + 1 < p.B && end <= r)) {
-    if (lo + 1 < p.B && end <= r) {
-      lo++;
-      start = end;
-      end = __ldg(p.cu + lo + 1);
+  if (lo + 1 < p.B && end <= r) {
+    int top = p.B;
+    while (top - lo > 1) {
+      const int mid = (lo + top) >> 1;
+      if (__ldg(p.cu + mid) <= r) lo = mid; else top = mid;
     }
+    start = __ldg(p.cu + lo);
+    end = __ldg(p.cu + lo + 1);
   }
   if (r >= p.total) return -2;
   if (start < 0 || end > p.total || end < start) atomicOr(p.status, MLA_STATUS_BAD_SEQLEN);

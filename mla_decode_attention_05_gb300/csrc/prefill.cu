@@ -129,15 +129,22 @@ static_assert(OFF_BARS % 16 == 0 && offsetof(Bars, next) % 16 == 0, "the answer 
 
 __device__ __forceinline__ int visible(const Work &w, int i) { return min(w.nk, max(0, w.diff + i + 1)); }
 
-// Tiles are numbered through the sequences; the whole warp looks for tile t.
-__device__ Work find_work(const PrefillParams &p, int t, int h, int lane) {
+// Where the last search ended: sequences b0 .. b0 + 31, the first of whose
+// tiles is number `before`.
+struct Place {
+  int b0, before;
+};
+
+// Tiles are numbered through the sequences; the whole warp looks for tile t,
+// from the last place on (units of work come in nearly falling order).
+__device__ Work find_work(const PrefillParams &p, int t, int h, int lane, Place &at) {
   Work w;
   w.nq = 0;
   w.h = h;
   w.split = 0;
-  int before = 0;
-  for (int b0 = 0; b0 < p.B; b0 += 32) {
-    const int b = b0 + lane;
+  bool back = false;
+  for (;;) {
+    const int b = at.b0 + lane;
     int s = 0, e = 0;
     if (b < p.B) {
       const int cs = __ldg(p.cu_q + b), ce = __ldg(p.cu_q + b + 1);
@@ -153,24 +160,33 @@ __device__ Work find_work(const PrefillParams &p, int t, int h, int lane) {
       if (lane >= o) upto += v;
     }
     const int total = __shfl_sync(0xffffffffu, upto, 31);
-    if (t < before + total) {
-      const unsigned hit = __ballot_sync(0xffffffffu, t < before + upto);
-      const int who = __ffs(hit) - 1;
-      const int part = t - before - __shfl_sync(0xffffffffu, upto - mine, who);
-      s = __shfl_sync(0xffffffffu, s, who);
-      e = __shfl_sync(0xffffffffu, e, who);
-      const int ck = __ldg(p.cu_k + b0 + who), cke = __ldg(p.cu_k + b0 + who + 1);
-      w.k0 = min(max(ck, 0), p.Nk);
-      w.nk = min(max(cke, w.k0), p.Nk) - w.k0;
-      if (lane == 0 && (w.k0 != ck || w.k0 + w.nk != cke)) atomicOr(p.status, MLA_STATUS_BAD_SEQLEN);
-      w.q0 = s + part * kCtaRows;
-      w.nq = min(kCtaRows, e - w.q0);
-      w.diff = p.causal ? w.nk - (e - s) + part * kCtaRows : p.Nk;
-      return w;
+    if (back) at.before -= total;
+    if (t < at.before) {  // (before > 0, so there are sequences before b0)
+      at.b0 -= 32;
+      back = true;
+      continue;
     }
-    before += total;
+    if (t >= at.before + total) {
+      if (at.b0 + 32 >= p.B) return w;
+      at.b0 += 32;
+      at.before += total;
+      back = false;
+      continue;
+    }
+    const unsigned hit = __ballot_sync(0xffffffffu, t < at.before + upto);
+    const int who = __ffs(hit) - 1;
+    const int part = t - at.before - __shfl_sync(0xffffffffu, upto - mine, who);
+    s = __shfl_sync(0xffffffffu, s, who);
+    e = __shfl_sync(0xffffffffu, e, who);
+    const int ck = __ldg(p.cu_k + at.b0 + who), cke = __ldg(p.cu_k + at.b0 + who + 1);
+    w.k0 = min(max(ck, 0), p.Nk);
+    w.nk = min(max(cke, w.k0), p.Nk) - w.k0;
+    if (lane == 0 && (w.k0 != ck || w.k0 + w.nk != cke)) atomicOr(p.status, MLA_STATUS_BAD_SEQLEN);
+    w.q0 = s + part * kCtaRows;
+    w.nq = min(kCtaRows, e - w.q0);
+    w.diff = p.causal ? w.nk - (e - s) + part * kCtaRows : p.Nk;
+    return w;
   }
-  return w;
 }
 
 __device__ __forceinline__ Steps steps_of(const Work &w) {
@@ -273,12 +289,12 @@ __device__ __forceinline__ int next_block(Bars *br) {
 // use at a time stay in L2; within a group the last tiles, which see the most
 // keys, go first.
 constexpr int kHeadGroup = 8;
-__device__ __forceinline__ Work block_work(const PrefillParams &p, int block, int lane) {
+__device__ __forceinline__ Work block_work(const PrefillParams &p, int block, int lane, Place &at) {
   const int split = block % p.splits;
   const int i = block / p.splits;
   const int g = i / (p.tiles * kHeadGroup), in = i % (p.tiles * kHeadGroup);
   const int heads = min(kHeadGroup, p.H - g * kHeadGroup);
-  Work w = find_work(p, p.tiles - 1 - in / heads, g * kHeadGroup + in % heads, lane);
+  Work w = find_work(p, p.tiles - 1 - in / heads, g * kHeadGroup + in % heads, lane, at);
   if (p.splits > 1 && w.nq > 0) take_split(w, split, p.splits);
   return w;
 }
@@ -289,6 +305,7 @@ __device__ __forceinline__ void load_work(const CUtensorMap *q_map, const CUtens
                                           uint32_t smem, const PrefillParams &p, int lane) {
   const uint64_t pol = policy_evict_normal(), once = policy_evict_first();
   uint32_t u = 0, asked = 0, count = 0, redone = 0, tiles0 = 0, tiles1 = 0;
+  Place place = {0, 0};
   bool ok = true;
   // the slot that unit of work number n gets is free
   auto slot_free = [&](uint32_t n) {
@@ -305,7 +322,7 @@ __device__ __forceinline__ void load_work(const CUtensorMap *q_map, const CUtens
     count++;
   };
   auto process = [&](int block, bool look) {
-    Work w = block_work(p, block, lane);
+    Work w = block_work(p, block, lane, place);
     w.block = block;
     if (w.nq == 0 || lane != 0) return;
     Steps st = steps_of(w);
@@ -936,8 +953,9 @@ int mla_prefill(const void *q, int64_t q_tok, int64_t q_head, const void *k_nope
                 mla_stream_t stream) {
   using namespace mla;
   if (B < 0 || Nq < 0 || Nk < 0) return fail(MLA_ERR_INVALID_ARG, "B, Nq and Nk must be >= 0");
-  if (B > (1 << 20) || Nq > (1 << 30) || Nk > (1 << 30))
-    return fail(MLA_ERR_UNSUPPORTED, "B must be at most 2^20, Nq and Nk at most 2^30");
+  // (2^26 keys are a second's work for one tile, under the limit of its waits)
+  if (B > (1 << 20) || Nq > (1 << 30) || Nk > (1 << 26))
+    return fail(MLA_ERR_UNSUPPORTED, "B must be at most 2^20, Nq at most 2^30, Nk at most 2^26");
   if (H < 1 || H > MLA_MAX_HEADS) return fail(MLA_ERR_INVALID_ARG, "H must be in [1, 128]");
   if (causal != 0 && causal != 1) return fail(MLA_ERR_INVALID_ARG, "causal must be 0 or 1");
   if (!(softmax_scale > 0.f) || softmax_scale > 3.0e38f)

@@ -120,6 +120,42 @@ def test_pages_and_lengths_that_cannot_be_read(fmt):
     assert torch.equal(kv, good[:200])
 
 
+def test_many_short_sequences():
+    import mla_decode_attention_05_gb300 as mla
+    lens, H = [int(x) for x in np.random.default_rng(11).integers(0, 4, 1500)], 2
+    lens[700] = 400
+    w = _cache(lens, "fp8", 12)
+    rng = np.random.default_rng(13)
+    w_uk, w_uv = bf16(rng, (H, 128, 512), 0.05).cuda(), bf16(rng, (H, 128, 512), 0.05).cuda()
+    cache, bt, sc = _dev(w, "fp8")
+    mla.device_status()
+    kv, pe = mla.kv_expand(cache, bt, cu(lens), w_uk, w_uv, total=sum(lens), kv_scales=sc)
+    _check(kv, pe, w, "fp8", w_uk, w_uv)
+    assert mla.device_status() == 0
+
+
+def test_more_row_blocks_than_pairs():
+    """Pairs of CTAs that come by several blocks of rows: the same rows as in
+    calls of their own, bit for bit."""
+    import mla_decode_attention_05_gb300 as mla
+    lens, H = [9000, 70, 11000], 7
+    w = _cache(lens, "bf16", 14)
+    rng = np.random.default_rng(15)
+    w_uk, w_uv = bf16(rng, (H, 128, 512), 0.05).cuda(), bf16(rng, (H, 128, 512), 0.05).cuda()
+    cache, bt, _ = _dev(w, "bf16")
+    mla.device_status()
+    kv, pe = mla.kv_expand(cache, bt, cu(lens), w_uk, w_uv, total=sum(lens))
+    at = np.cumsum([0] + lens)
+    for b in range(3):
+        k, e = mla.kv_expand(cache, bt[b:b + 1].contiguous(), cu(lens[b:b + 1]), w_uk, w_uv, total=lens[b])
+        assert torch.equal(kv[at[b]:at[b + 1]], k) and torch.equal(pe[at[b]:at[b + 1]], e)
+    lat, _, _ = _rows(w, "bf16")
+    some = rng.integers(0, sum(lens), 200)
+    want, mag = O.expand(lat[some], f64(w_uk), f64(w_uv))
+    check_sum(kv[torch.from_numpy(some).cuda()], want, mag, 513)
+    assert mla.device_status() == 0
+
+
 def test_a_row_that_is_not_finite_stays_alone():
     import mla_decode_attention_05_gb300 as mla
     lens, H = [140], 3

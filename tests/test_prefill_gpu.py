@@ -179,6 +179,29 @@ def test_a_value_that_is_not_finite_reaches_the_rows_that_see_it(bad):
     assert torch.equal(out[~hit], want[~hit]) and torch.equal(lse, wl)
 
 
+def test_many_short_sequences():
+    """Thousands of sequences, empty ones among them, some of several tiles."""
+    import mla_decode_attention_05_gb300 as mla
+    rng = np.random.default_rng(23)
+    nq = [int(x) for x in rng.integers(0, 5, 3000)]
+    for b in (0, 700, 1500, 2999):
+        nq[b] = 300
+    nk = [q + int(c) for q, c in zip(nq, rng.integers(0, 4, 3000))]
+    ins = _inputs(nq, nk, 2, 24)
+    mla.device_status()
+    out, lse = mla.prefill(*ins, cu(nq), cu(nk), softmax_scale=SCALE)
+    assert mla.device_status() == 0
+    at, kt = np.cumsum([0] + nq), np.cumsum([0] + nk)
+    for b in [0, 1, 2, 31, 32, 33, 699, 700, 701, 1024, 1499, 1500, 2000, 2998, 2999]:
+        s, k = slice(at[b], at[b + 1]), slice(kt[b], kt[b + 1])
+        _check(out[s], lse[:, s], [ins[0][s], ins[1][k], ins[2][k], ins[3][k]], [nq[b]], [nk[b]], True)
+    # a row's result does not depend on the sequences around its own
+    for a, z in ((0, 40), (1480, 1530), (2950, 3000)):
+        s, k = slice(at[a], at[z]), slice(kt[a], kt[z])
+        o, l = mla.prefill(ins[0][s], ins[1][k], ins[2][k], ins[3][k], cu(nq[a:z]), cu(nk[a:z]), softmax_scale=SCALE)
+        assert torch.equal(o, out[s]) and torch.equal(l, lse[:, s])
+
+
 def test_many_units_of_work_are_done_again():
     """Every unit of work holds a value that its earlier rows do not see and
     that is not finite: more than wait to be done again at a time."""

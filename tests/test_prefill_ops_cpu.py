@@ -64,6 +64,7 @@ def test_expand_arguments(L, args, code):
 
 @pytest.mark.parametrize("args,code", [
     (dict(B=-1), -1), (dict(B=(1 << 20) + 1), -2), (dict(Nq=-1), -1), (dict(Nk=-1), -1), (dict(Nq=(1 << 30) + 1), -2),
+    (dict(Nk=(1 << 26) + 1), -2),
     (dict(H=0), -1), (dict(H=129), -1), (dict(causal=2), -1), (dict(scale=0.0), -1), (dict(scale=float("nan")), -1),
     (dict(scale=float("inf")), -1), (dict(q_tok=100), -1), (dict(q_head=188), -1), (dict(k_tok=64), -1),
     (dict(v_head=132), -1), (dict(pe_tok=32), -1), (dict(q=None), -1), (dict(q=264), -1), (dict(out=8), -1),
@@ -90,7 +91,7 @@ def test_prefill_workspace(L):
     assert m.prefill_workspace_bytes(1, 8, 200, 500) == 0           # short keys
     n = m.prefill_workspace_bytes(1, 8, 200, 12200)
     assert n == 19 * 200 * 8 * 129 * 4 + (-(19 * 200 * 8 * 4) % 256)
-    assert m.prefill_workspace_bytes(1, 1, 1, 1 << 30) == 32 * 128 * 4 + 256
+    assert m.prefill_workspace_bytes(1, 1, 1, 1 << 26) == 32 * 128 * 4 + 256
     assert m.prefill_workspace_bytes(0, 8, 0, 0) == 0 and m.prefill_workspace_bytes(1, 0, 5, 5) == 0
 
 
