@@ -45,10 +45,10 @@ constexpr int kKeys = 128;     // keys of one step
 constexpr int kCtaRows = 2 * kRows;
 
 // Warps 0-3 and 4-7: softmax and output of tile 0 and 1 (one row a thread);
-// warp 8 issues the MMAs, warp 9 the loads, warp 10 looks through values,
-// warp 11 waits for warp 8.  Registers move between the three warpgroups, from
-// 168 a thread at launch to 208 for the softmax and 88 for
-// the rest (2 * 208 + 88 = 3 * 168).
+// warp 8 issues the MMAs, warp 9 the loads, warp 10 hands out the work, warp 11
+// waits for warp 8.  Registers move between the three warpgroups, from 168 a
+// thread at launch to 208 for the softmax and 88 for the rest (2 * 208 + 88 =
+// 3 * 168).
 constexpr int kThreads = 384;
 
 // Shared memory: Q of both tiles as 2 x 3 blocks of 128 rows x 64 values; a
@@ -104,6 +104,7 @@ constexpr int kRedo = 64;
 struct Bars {
   uint64_t full[kUnits], empty[kUnits];
   uint64_t work_full[2], work_empty[2];
+  uint64_t taken;       // the load warp has begun with a unit of work
   uint64_t q_full[2], q_empty[2];
   uint64_t s_full[2];   // scores of a tile are in tensor memory
   uint64_t p_full[2][2];  // its probabilities are: of the first and the last 64 keys
@@ -138,10 +139,8 @@ struct Place {
 // Tiles are numbered through the sequences; the whole warp looks for tile t,
 // from the last place on (units of work come in nearly falling order).
 __device__ Work find_work(const PrefillParams &p, int t, int h, int lane, Place &at) {
-  Work w;
-  w.nq = 0;
+  Work w = {};
   w.h = h;
-  w.split = 0;
   bool back = false;
   for (;;) {
     const int b = at.b0 + lane;
@@ -299,99 +298,57 @@ __device__ __forceinline__ Work block_work(const PrefillParams &p, int block, in
   return w;
 }
 
-// The load warp: finds the work, tells the others, and fetches it.
-__device__ __forceinline__ void load_work(const CUtensorMap *q_map, const CUtensorMap *kn_map,
+// The load warp.  One lane asks for the units in their order, each as soon as
+// its place in the ring is free (a lane for each unit of a step would make the
+// first ones wait for the last one's place: 8192 tokens 563 us).
+__device__ __forceinline__ void load_rows(const CUtensorMap *q_map, const CUtensorMap *kn_map,
                                           const CUtensorMap *kp_map, const CUtensorMap *v_map, Bars *br,
-                                          uint32_t smem, const PrefillParams &p, int lane) {
+                                          uint32_t smem, unsigned int *status, int lane) {
   const uint64_t pol = policy_evict_normal(), once = policy_evict_first();
-  uint32_t u = 0, asked = 0, count = 0, redone = 0, tiles0 = 0, tiles1 = 0;
-  Place place = {0, 0};
-  bool ok = true;
-  // the slot that unit of work number n gets is free
-  auto slot_free = [&](uint32_t n) {
-    ok = ok && wait_ok(br, &br->work_empty[n & 1], ((n >> 1) & 1) ^ 1, p.status);
-  };
-  auto tell = [&](const Work &w, const Steps &st) {
+  uint32_t u = 0, tiles0 = 0, tiles1 = 0;  // units, tiles so far
+  for (uint32_t count = 0;; count++) {
     const uint32_t slot = count & 1;
-    slot_free(count);
-    if (!ok) return;
-    br->work[slot] = w;
-    br->steps[slot] = st;
-    br->odd[slot] = 0;
-    mbar_arrive(smem_u32(&br->work_full[slot]));
-    count++;
-  };
-  auto process = [&](int block, bool look) {
-    Work w = block_work(p, block, lane, place);
-    w.block = block;
-    if (w.nq == 0 || lane != 0) return;
-    Steps st = steps_of(w);
-    if (look) st.look = st.masked;
-    tell(w, st);
-#pragma unroll
-    for (int t = 0; t < 2; t++) {
-      if (st.n[t] == 0 || !ok) continue;
-      ok = wait_ok(br, &br->q_empty[t], ((t == 0 ? tiles0++ : tiles1++) & 1) ^ 1, p.status);
-      if (!ok) continue;
-      mbar_arrive_expect_tx(smem_u32(&br->q_full[t]), 3 * kUnit);
-      for (int c = 0; c < 3; c++)
-        tma_load_3d(smem + (3 * t + c) * kUnit, q_map, smem_u32(&br->q_full[t]), 64 * c, w.h, w.q0 + t * kRows, once);
+    if (!warp_wait_ok(br, &br->work_full[slot], (count >> 1) & 1, status)) return;
+    const Work w = br->work[slot];
+    const Steps st = br->steps[slot];
+    __syncwarp();
+    if (w.nq == 0) return;
+    if (lane == 0) {
+      mbar_arrive(smem_u32(&br->work_empty[slot]));
+      mbar_arrive(smem_u32(&br->taken));
     }
-    for (int j = 0; j < st.most && ok; j++) {
-      const int key = w.k0 + j * kKeys;
+    bool ok = true;
+    if (lane == 0) {
 #pragma unroll 1
-      for (int c = 0; c < kUnitsPerStep; c++, u++) {
-        const uint32_t s = u % kUnits, full = smem_u32(&br->full[s]), dst = smem + OFF_RING + s * kUnit;
-        ok = wait_ok(br, &br->empty[s], ((u / kUnits) & 1) ^ 1, p.status);
+      for (int t = 0; t < 2 && ok; t++) {
+        if ((t == 0 ? st.n[0] : st.n[1]) == 0) continue;
+        const uint32_t full = smem_u32(&br->q_full[t]);
+        ok = wait_ok(br, &br->q_empty[t], ((t == 0 ? tiles0++ : tiles1++) & 1) ^ 1, status);
         if (!ok) break;
-        mbar_arrive_expect_tx(full, kUnit);
-        if (c < 2) {
-          tma_load_3d(dst, kn_map, full, 64 * c, w.h, key, pol);
-        } else if (c == 2) {
-          tma_load_3d(dst, kp_map, full, 0, 0, key, pol);
-        } else {
-          tma_load_3d(dst, v_map, full, 0, w.h, key + 64 * (c - 3), pol);
-          tma_load_3d(dst + kUnit / 2, v_map, full, 64, w.h, key + 64 * (c - 3), pol);
+        mbar_arrive_expect_tx(full, 3 * kUnit);
+#pragma unroll 1
+        for (int c = 0; c < 3; c++)
+          tma_load_3d(smem + (3 * t + c) * kUnit, q_map, full, 64 * c, w.h, w.q0 + t * kRows, once);
+      }
+#pragma unroll 1
+      for (int j = 0; j < st.most && ok; j++) {
+        const int key = w.k0 + j * kKeys;
+#pragma unroll 1
+        for (int c = 0; c < kUnitsPerStep; c++, u++) {
+          const uint32_t s = u % kUnits, full = smem_u32(&br->full[s]), dst = smem + OFF_RING + s * kUnit;
+          ok = wait_ok(br, &br->empty[s], ((u / kUnits) & 1) ^ 1, status);
+          if (!ok) break;
+          mbar_arrive_expect_tx(full, kUnit);
+          if (c < 3) {
+            tma_load_3d(dst, c < 2 ? kn_map : kp_map, full, c < 2 ? 64 * c : 0, c < 2 ? w.h : 0, key, pol);
+          } else {
+            tma_load_3d(dst, v_map, full, 0, w.h, key + 64 * (c - 3), pol);
+            tma_load_3d(dst + kUnit / 2, v_map, full, 64, w.h, key + 64 * (c - 3), pol);
+          }
         }
       }
     }
-  };
-  // Blocks of the grid one after the other.  When there are no more, or many
-  // units of work wait to be done again (never more than the ring holds: two are
-  // under way beside this), all that is under way is let finish, and they are.
-  int block = blockIdx.x;
-  for (;;) {
-    const uint32_t waiting = __shfl_sync(0xffffffffu, *(volatile uint32_t *)&br->redo_count, 0) - redone;
-    const bool redo = block < 0 || waiting >= kRedo / 2;
-    int now = block;
-    if (redo) {
-      if (lane == 0) {
-        slot_free(count);
-        slot_free(count + 1);
-      }
-      ok = __shfl_sync(0xffffffffu, (int)ok, 0);
-      __syncwarp();
-      if (!ok || *(volatile uint32_t *)&br->redo_count == redone) break;
-      now = *(volatile int *)&br->redo[redone++ % kRedo];
-    } else if (lane == 0) {
-      ask_next(br);
-    }
-    __syncwarp();
-    process(now, redo);
-    if (!redo) {
-      // (also after a wait that gave up: the answer has to land before the CTA ends)
-      const bool told = warp_wait_ok(br, &br->next_full, asked++ & 1, p.status);
-      ok = ok && told;
-      block = told ? next_block(br) : -1;
-    }
-    ok = __shfl_sync(0xffffffffu, (int)ok, 0);
-    __syncwarp();
-    if (!ok) break;
-  }
-  if (ok && lane == 0) {
-    Work none;
-    none.nq = 0;
-    tell(none, Steps());
+    if (!__all_sync(0xffffffffu, ok)) return;
   }
 }
 
@@ -522,74 +479,128 @@ __device__ __forceinline__ void mma_sequence(Bars *br, uint32_t smem, uint32_t t
   }
 }
 
-// The whole warp looks through the values of the steps from `look` on.
-__device__ __forceinline__ void check_values(Bars *br, uint8_t *ring, int lane, unsigned int *status) {
-  uint32_t base = 0, looks = 0;
-  for (uint32_t count = 0;; count++) {
-    const uint32_t slot = count & 1;
-    if (!warp_wait_ok(br, &br->work_full[slot], (count >> 1) & 1, status)) return;
-    const Steps st = br->steps[slot];
-    if (br->work[slot].nq == 0) return;
-    // (no row reads this slot's keys any more: the slot was given back after its output)
-    if (lane < 16) br->bad_keys[slot][lane] = 0;
-    __syncwarp();
-    for (int j = st.look; j < st.most; j++) {
-      if (!warp_wait_ok(br, &br->v_look, looks++ & 1, status)) return;
-      bool patched = false;
-      for (int c = 0; c < 2; c++) {
-        const uint32_t u = base + (uint32_t)j * kUnitsPerStep + 3 + c, s = u % kUnits;
-        if (!warp_wait_ok(br, &br->full[s], (u / kUnits) & 1, status)) return;
-        uint8_t *unit = ring + s * kUnit;
-        // x * 0 summed up stays 0, unless some x is not finite: then it is nan
-        uint32_t sum[4] = {0u, 0u, 0u, 0u};
+// The whole warp looks through the values of one unit of work, from step `look`
+// on; base: the unit of the ring that its first step begins with.
+__device__ __forceinline__ bool check_values(Bars *br, uint8_t *ring, const Steps &st, uint32_t slot, uint32_t base,
+                                             uint32_t &looks, int lane, unsigned int *status) {
+  for (int j = st.look; j < st.most; j++) {
+    if (!warp_wait_ok(br, &br->v_look, looks++ & 1, status)) return false;
+    bool patched = false;
+    for (int c = 0; c < 2; c++) {
+      const uint32_t u = base + (uint32_t)j * kUnitsPerStep + 3 + c, s = u % kUnits;
+      if (!warp_wait_ok(br, &br->full[s], (u / kUnits) & 1, status)) return false;
+      uint8_t *unit = ring + s * kUnit;
+      // x * 0 summed up stays 0, unless some x is not finite: then it is nan
+      uint32_t sum[4] = {0u, 0u, 0u, 0u};
 #pragma unroll 1
-        for (int i = lane; i < (int)(kUnit / 16); i += 32 * 8) {
-          uint4 v[8];
+      for (int i = lane; i < (int)(kUnit / 16); i += 32 * 8) {
+        uint4 v[8];
 #pragma unroll
-          for (int k = 0; k < 8; k++) v[k] = *reinterpret_cast<const uint4 *>(unit + (i + 32 * k) * 16);
+        for (int k = 0; k < 8; k++) v[k] = *reinterpret_cast<const uint4 *>(unit + (i + 32 * k) * 16);
 #pragma unroll
-          for (int k = 0; k < 8; k++) {
-            const uint32_t x[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+        for (int k = 0; k < 8; k++) {
+          const uint32_t x[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
 #pragma unroll
-            for (int e = 0; e < 4; e++) asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(sum[e]) : "r"(x[e]), "r"(0u));
-          }
-        }
-        bool some = false;
-#pragma unroll
-        for (int e = 0; e < 4; e++) some |= (sum[e] & 0x7FFF7FFFu) != 0;
-        if (!some) continue;
-#pragma unroll 1
-        for (int i = lane; i < (int)(kUnit / 16); i += 32) {  // (this lane's part again)
-          uint32_t x[4];
-          bool bad = false;
-#pragma unroll
-          for (int e = 0; e < 4; e++) {
-            x[e] = reinterpret_cast<const uint32_t *>(unit + i * 16)[e];
-            // a bf16 is not finite when its eight exponent bits are all set
-            if ((x[e] & 0x7F80u) == 0x7F80u) {
-              x[e] &= 0xFFFF0000u;
-              bad = true;
-            }
-            if ((x[e] & 0x7F800000u) == 0x7F800000u) {
-              x[e] &= 0x0000FFFFu;
-              bad = true;
-            }
-          }
-          if (!bad) continue;
-          *reinterpret_cast<uint4 *>(unit + i * 16) = make_uint4(x[0], x[1], x[2], x[3]);
-          const int key = (j - st.look) * kKeys + c * 64 + ((i * 16) % (int)(kUnit / 2)) / 128;
-          if (key < 512) atomicOr(&br->bad_keys[slot][key >> 5], 1u << (key & 31));
-          patched = true;
+          for (int e = 0; e < 4; e++) asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(sum[e]) : "r"(x[e]), "r"(0u));
         }
       }
-      if (patched) fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&br->v_ok));
+      bool some = false;
+#pragma unroll
+      for (int e = 0; e < 4; e++) some |= (sum[e] & 0x7FFF7FFFu) != 0;
+      if (!some) continue;
+#pragma unroll 1
+      for (int i = lane; i < (int)(kUnit / 16); i += 32) {  // (this lane's part again)
+        uint32_t x[4];
+        bool bad = false;
+#pragma unroll
+        for (int e = 0; e < 4; e++) {
+          x[e] = reinterpret_cast<const uint32_t *>(unit + i * 16)[e];
+          // a bf16 is not finite when its eight exponent bits are all set
+          if ((x[e] & 0x7F80u) == 0x7F80u) {
+            x[e] &= 0xFFFF0000u;
+            bad = true;
+          }
+          if ((x[e] & 0x7F800000u) == 0x7F800000u) {
+            x[e] &= 0x0000FFFFu;
+            bad = true;
+          }
+        }
+        if (!bad) continue;
+        *reinterpret_cast<uint4 *>(unit + i * 16) = make_uint4(x[0], x[1], x[2], x[3]);
+        const int key = (j - st.look) * kKeys + c * 64 + ((i * 16) % (int)(kUnit / 2)) / 128;
+        if (key < 512) atomicOr(&br->bad_keys[slot][key >> 5], 1u << (key & 31));
+        patched = true;
+      }
     }
-    base += (uint32_t)st.most * kUnitsPerStep;
+    if (patched) fence_proxy_async_smem();
     __syncwarp();
-    if (lane == 0) mbar_arrive(smem_u32(&br->work_empty[slot]));
+    if (lane == 0) mbar_arrive(smem_u32(&br->v_ok));
   }
+  return true;
+}
+
+// The scheduling warp: hands out the units of work.  Blocks of the grid come one
+// after the other.  When there are no more, or many units wait to be done again
+// (never more than their ring holds: two are under way beside this), all that
+// is under way is let finish, and they are, with this warp looking through their
+// values.
+__device__ __forceinline__ void schedule(const PrefillParams &p, Bars *br, uint8_t *ring, int lane) {
+  uint32_t asked = 0, count = 0, redone = 0, base = 0, looks = 0;
+  Place place = {0, 0};
+  // the slot that unit of work number n gets is free
+  auto slot_free = [&](uint32_t n) {
+    return warp_wait_ok(br, &br->work_empty[n & 1], ((n >> 1) & 1) ^ 1, p.status);
+  };
+  auto tell = [&](const Work &w, const Steps &st) {
+    const uint32_t slot = count & 1;
+    if (!slot_free(count)) return false;
+    if (lane < 16) br->bad_keys[slot][lane] = 0;
+    if (lane == 0) {
+      br->work[slot] = w;
+      br->steps[slot] = st;
+      br->odd[slot] = 0;
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&br->work_full[slot]));
+    count++;
+    return true;
+  };
+  int block = blockIdx.x;
+  for (;;) {
+    const uint32_t waiting = __shfl_sync(0xffffffffu, *(volatile uint32_t *)&br->redo_count, 0) - redone;
+    const bool redo = block < 0 || waiting >= kRedo / 2;
+    int now = block;
+    if (redo) {
+      if (!slot_free(count) || !slot_free(count + 1)) return;
+      if (*(volatile uint32_t *)&br->redo_count == redone) break;
+      now = *(volatile int *)&br->redo[redone++ % kRedo];
+    }
+    __syncwarp();
+    Work w = block_work(p, now, lane, place);
+    w.block = now;
+    bool ok = true;
+    if (w.nq > 0) {
+      Steps st = steps_of(w);
+      if (redo) st.look = st.masked;
+      const uint32_t slot = count & 1;
+      ok = tell(w, st);
+      if (ok && redo) ok = check_values(br, ring, st, slot, base, looks, lane, p.status);
+      base += (uint32_t)st.most * kUnitsPerStep;
+      // The next block is taken over when this one's loads begin: taken earlier,
+      // blocks are shared out unevenly (8192 tokens 545 us instead of 472).
+      ok = ok && warp_wait_ok(br, &br->taken, (count - 1) & 1, p.status);
+    }
+    if (!redo && ok) {
+      if (lane == 0) ask_next(br);
+      // (also after a wait that gave up: the answer has to land before the CTA ends)
+      const bool told = warp_wait_ok(br, &br->next_full, asked++ & 1, p.status);
+      ok = ok && told;
+      block = told ? next_block(br) : -1;
+      __syncwarp();
+    }
+    if (!ok) return;
+  }
+  tell(Work{}, Steps{});
 }
 
 // One row a thread: the softmax of tile t over the steps of one unit of work,
@@ -855,7 +866,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int t = 0; t < 2; t++) {
       mbar_init(smem_u32(&br->work_full[t]), 1);
-      mbar_init(smem_u32(&br->work_empty[t]), 11);  // softmax warps, MMA warp and its waiter, value check
+      mbar_init(smem_u32(&br->work_empty[t]), 11);  // softmax, MMA, waiting and load warps
       mbar_init(smem_u32(&br->q_full[t]), 1);
       mbar_init(smem_u32(&br->q_empty[t]), 1);
       mbar_init(smem_u32(&br->s_full[t]), 1);
@@ -867,6 +878,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(smem_u32(&br->v_look), 1);
     mbar_init(smem_u32(&br->v_ok), 1);
     mbar_init(smem_u32(&br->next_full), 1);
+    mbar_init(smem_u32(&br->taken), 1);
     br->redo_count = 0;
     br->abort = 0;
     fence_mbar_init_cluster();
@@ -883,9 +895,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 8) {
       mma_sequence<false>(br, smem, tmem, p.status);
     } else if (warp == 9) {
-      load_work(&q_map, &kn_map, &kp_map, &v_map, br, smem, p, lane);
+      load_rows(&q_map, &kn_map, &kp_map, &v_map, br, smem, p.status, lane);
     } else if (warp == 10) {
-      check_values(br, base + OFF_RING, lane, p.status);
+      schedule(p, br, base + OFF_RING, lane);
     } else {
       mma_sequence<true>(br, smem, tmem, p.status);
     }
