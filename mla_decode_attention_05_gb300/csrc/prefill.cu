@@ -104,7 +104,7 @@ constexpr int kRedo = 64;
 struct Bars {
   uint64_t full[kUnits], empty[kUnits];
   uint64_t work_full[2], work_empty[2];
-  uint64_t taken;       // the load warp has begun with a unit of work
+  uint64_t taken;       // the load warp is about to end a unit of work
   uint64_t q_full[2], q_empty[2];
   uint64_t s_full[2];   // scores of a tile are in tensor memory
   uint64_t p_full[2][2];  // its probabilities are: of the first and the last 64 keys
@@ -284,9 +284,10 @@ __device__ __forceinline__ int next_block(Bars *br) {
   return got ? x : -1;
 }
 
-// Block -> work.  Heads go in groups of eight, so that the keys and values in
-// use at a time stay in L2; within a group the last tiles, which see the most
-// keys, go first.
+// Block -> work.  Heads go in groups of eight, so that several CTAs come by the
+// same keys and values together (groups of 4, 8, 16, 32: 443, 431, 439 and
+// 438 us for 8192 tokens and 32 heads); within a group the last tiles, which see
+// the most keys, go first, so that the small ones fill the end.
 constexpr int kHeadGroup = 8;
 __device__ __forceinline__ Work block_work(const PrefillParams &p, int block, int lane, Place &at) {
   const int split = block % p.splits;
@@ -313,10 +314,7 @@ __device__ __forceinline__ void load_rows(const CUtensorMap *q_map, const CUtens
     const Steps st = br->steps[slot];
     __syncwarp();
     if (w.nq == 0) return;
-    if (lane == 0) {
-      mbar_arrive(smem_u32(&br->work_empty[slot]));
-      mbar_arrive(smem_u32(&br->taken));
-    }
+    if (lane == 0) mbar_arrive(smem_u32(&br->work_empty[slot]));
     bool ok = true;
     if (lane == 0) {
 #pragma unroll 1
@@ -330,8 +328,10 @@ __device__ __forceinline__ void load_rows(const CUtensorMap *q_map, const CUtens
         for (int c = 0; c < 3; c++)
           tma_load_3d(smem + (3 * t + c) * kUnit, q_map, full, 64 * c, w.h, w.q0 + t * kRows, once);
       }
+      if (st.most == 0) mbar_arrive(smem_u32(&br->taken));
 #pragma unroll 1
       for (int j = 0; j < st.most && ok; j++) {
+        if (j == max(0, st.most - 3)) mbar_arrive(smem_u32(&br->taken));
         const int key = w.k0 + j * kKeys;
 #pragma unroll 1
         for (int c = 0; c < kUnitsPerStep; c++, u++) {
@@ -586,8 +586,9 @@ __device__ __forceinline__ void schedule(const PrefillParams &p, Bars *br, uint8
       ok = tell(w, st);
       if (ok && redo) ok = check_values(br, ring, st, slot, base, looks, lane, p.status);
       base += (uint32_t)st.most * kUnitsPerStep;
-      // The next block is taken over when this one's loads begin: taken earlier,
-      // blocks are shared out unevenly (8192 tokens 545 us instead of 472).
+      // The next block is taken over when this one's last loads begin: taken
+      // earlier, blocks are shared out unevenly (8192 tokens, two units ahead:
+      // 545 us).
       ok = ok && warp_wait_ok(br, &br->taken, (count - 1) & 1, p.status);
     }
     if (!redo && ok) {
