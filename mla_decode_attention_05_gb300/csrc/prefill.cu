@@ -811,6 +811,7 @@ __device__ __forceinline__ void softmax_rows(const PrefillParams &p, Bars *br, u
 
 // Splits joined: one warp a row and head, four values a lane.
 __global__ void __launch_bounds__(256) prefill_join_kernel(PrefillParams p) {
+  grid_dep_wait();  // (a programmatic dependent of the kernel above)
   const int lane = threadIdx.x & 31;
   const long long i = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
   if (i >= (long long)p.Nq * p.H) return;
@@ -831,14 +832,26 @@ __global__ void __launch_bounds__(256) prefill_join_kernel(PrefillParams p) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int s = 0; s < p.splits; s++) {
-    if (__shfl_sync(0xffffffffu, mine, s) == -INFINITY) continue;  // no keys
-    const float ws = __shfl_sync(0xffffffffu, weight, s);
-    const float4 v = *reinterpret_cast<const float4 *>(p.part_o + ((s * (size_t)p.Nq + row) * p.H + h) * kDv + 4 * lane);
-    acc.x += ws * v.x;
-    acc.y += ws * v.y;
-    acc.z += ws * v.z;
-    acc.w += ws * v.w;
+  const float *part = p.part_o + (size_t)i * kDv + 4 * lane;
+  const size_t next = (size_t)p.Nq * p.H * kDv;
+  constexpr int kBatch = 8;  // parts on their way at a time
+  for (int s0 = 0; s0 < p.splits; s0 += kBatch) {
+    float4 v[kBatch];
+#pragma unroll
+    for (int k = 0; k < kBatch; k++) {
+      // (a part without keys has weight 0 and finite values)
+      v[k] = s0 + k < p.splits ? __ldcs(reinterpret_cast<const float4 *>(part + (s0 + k) * next))
+                               : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+#pragma unroll
+    for (int k = 0; k < kBatch; k++) {
+      const float ws = __shfl_sync(0xffffffffu, weight, (s0 + k) & 31);
+      if (s0 + k >= p.splits) continue;
+      acc.x += ws * v[k].x;
+      acc.y += ws * v[k].y;
+      acc.z += ws * v[k].z;
+      acc.w += ws * v[k].w;
+    }
   }
   const bool none = sum == 0.f;
   const float inv = none ? 0.f : 1.f / sum;
@@ -852,6 +865,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     prefill_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap kn_map,
                    const __grid_constant__ CUtensorMap kp_map, const __grid_constant__ CUtensorMap v_map,
                    PrefillParams p) {
+  grid_dep_trigger();  // the join's blocks may come in as these leave
   extern __shared__ uint8_t smem_raw[];
   uint8_t *base = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   Bars *br = reinterpret_cast<Bars *>(base + OFF_BARS);
@@ -1031,9 +1045,19 @@ int mla_prefill(const void *q, int64_t q_tok, int64_t q_head, const void *k_nope
   if (e != cudaSuccess) return fail(MLA_ERR_CUDA, cudaGetErrorString(e));
   prefill_kernel<<<(unsigned)(tiles * H * splits), kThreads, kSmem, (cudaStream_t)stream>>>(q_map, kn_map, kp_map,
                                                                                               v_map, p);
-  if (splits > 1)
-    prefill_join_kernel<<<(unsigned)(((long long)Nq * H + 7) / 8), 256, 0, (cudaStream_t)stream>>>(p);
   e = cudaGetLastError();
+  if (e == cudaSuccess && splits > 1) {
+    cudaLaunchAttribute pdl[1];
+    pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    pdl[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(((long long)Nq * H + 7) / 8));
+    cfg.blockDim = dim3(256);
+    cfg.stream = (cudaStream_t)stream;
+    cfg.attrs = pdl;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, prefill_join_kernel, p);
+  }
   if (e != cudaSuccess) return fail(MLA_ERR_CUDA, cudaGetErrorString(e));
   set_last_error("");
   return MLA_OK;
