@@ -30,6 +30,7 @@ import torch
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "_lib", "libmla_decode.so")
+FAST_PATH = os.path.join(_HERE, "_lib", "fastcall.so")
 
 KV_BF16 = 0
 KV_FP8_E4M3 = 1
@@ -47,6 +48,7 @@ STATUS_BAD_POSITION = 32
 
 _lock = threading.Lock()
 _lib = None
+_fast = None  # the short way of csrc_host/fastcall.cpp, once the library is loaded; None: not built
 
 
 class MlaError(RuntimeError):
@@ -97,7 +99,27 @@ def lib():
             L.mla_set_wait_limit_ns.argtypes = [ctypes.c_uint64]
             L.mla_set_dual_gemm.argtypes = [ctypes.c_int]
             _lib = L
+            _load_fast(L)
     return _lib
+
+
+def _load_fast(L) -> None:
+    """Loads fastcall.so, if it was built for this interpreter and PyTorch, and
+    gives it the library's functions."""
+    global _fast
+    if _fast is not None or not os.path.exists(FAST_PATH):
+        return
+    import importlib.machinery
+    import importlib.util
+    try:
+        loader = importlib.machinery.ExtensionFileLoader("fastcall", FAST_PATH)
+        m = importlib.util.module_from_spec(importlib.util.spec_from_loader("fastcall", loader))
+        loader.exec_module(m)
+    except ImportError:
+        return
+    m.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
+        L.mla_kv_insert_rope, L.mla_kv_expand, L.mla_prefill, L.mla_prefill_workspace_bytes, L.mla_value_project)))
+    _fast = m
 
 
 def _check(rc: int):
@@ -457,6 +479,13 @@ def kv_insert_rope(kv_c: torch.Tensor, k_pe: torch.Tensor, w_kva: torch.Tensor, 
     (q[..., -64:] of [N, H, 576] or [N, H, 192] queries); q_out as q_pe, default
     q_pe itself: the queries are rotated in place.  It must be q_pe or not
     overlap it.  The other arguments are kv_insert()'s."""
+    if _fast is not None:
+        r = _fast.kv_insert_rope(kv_c, k_pe, w_kva, slots, kv_cache, eps, positions, cos_sin, interleaved, q_pe, q_out,
+                                 kv_scales, k_scale_inv, fp8_per_tensor)
+        if r is not None:
+            if r is not True:
+                _check(r)
+            return kv_cache, q_pe if q_out is None else q_out
     kv_c, ld_kv, k_pe, ld_pe, dev, N, fmt = _insert_args(kv_c, k_pe, w_kva, slots, kv_cache, kv_scales, k_scale_inv,
                                                          fp8_per_tensor)
     if k_pe.get_device() != dev.index:
@@ -514,6 +543,14 @@ def kv_expand(kv_cache: torch.Tensor, block_table: torch.Tensor, cu_seqlens: tor
     cu_seqlens[B] (a host number: this call does not wait for the device);
     taken from kv or k_pe where one is given.  Rows of no sequence are left as
     they were."""
+    if total is None:
+        if kv is None and k_pe is None:
+            raise ValueError("total (the outputs' rows) is needed where no output is given")
+        total = (kv if kv is not None else k_pe).shape[0]
+    if _fast is not None:
+        r = _fast.kv_expand(kv_cache, block_table, cu_seqlens, w_uk, w_uv, total, kv_scales, kv, k_pe)
+        if r is not None:
+            return r if type(r) is tuple else _check(r)
     if not isinstance(kv_cache, torch.Tensor):
         raise TypeError("kv_cache must be a torch.Tensor")
     fmt = _cache_format(kv_cache, kv_scales)
@@ -529,10 +566,6 @@ def kv_expand(kv_cache: torch.Tensor, block_table: torch.Tensor, cu_seqlens: tor
     uv_head, uv_row = _strided(w_uv, "w_uv", (H, 128, D_V), dev)
     if fmt == KV_FP8_E4M3 and tuple(kv_scales.shape) != (kv_cache.shape[0], kv_cache.shape[1], 4):
         raise ValueError("kv_scales must be [P, 64, 4]")
-    if total is None:
-        if kv is None and k_pe is None:
-            raise ValueError("total (the outputs' rows) is needed where no output is given")
-        total = (kv if kv is not None else k_pe).shape[0]
     total = int(total)
     if total < 0:
         raise ValueError("total must be >= 0")
@@ -588,6 +621,10 @@ def prefill(q: torch.Tensor, k_nope: torch.Tensor, k_pe: torch.Tensor, v: torch.
     one less.  A row that sees no key gets 0 and -inf.  Rows of no sequence
     are left as they were.  workspace: at least prefill_workspace_bytes() bytes
     (allocated here where it is needed and not given)."""
+    if _fast is not None:
+        r = _fast.prefill(q, k_nope, k_pe, v, cu_seqlens_q, cu_seqlens_k, softmax_scale, causal, workspace, out, lse)
+        if r is not None:
+            return r if type(r) is tuple else _check(r)
     q_strides = _strided(q, "q", (None, None, 192), None)
     dev, (Nq, H, _) = q.device, q.shape
     k_strides = _strided(k_nope, "k_nope", (None, H, 128), dev)
@@ -637,6 +674,10 @@ def value_project(attn: torch.Tensor, w_uv: torch.Tensor, *, out: Optional[torch
     attn bf16 [N, H, 512] (decode()'s out with B and T flattened; rows may be
     strided); w_uv bf16 [H, 128, 512] (a view of a [H, 256, 512] tensor will
     do)."""
+    if _fast is not None:
+        r = _fast.value_project(attn, w_uv, out)
+        if r is not None:
+            return _check(r) if type(r) is int else r
     strides = _strided(attn, "attn", (None, None, D_V), None)
     dev, (N, H, _) = attn.device, attn.shape
     w_head, w_row = _strided(w_uv, "w_uv", (H, 128, D_V), dev)

@@ -5,6 +5,9 @@
 Each translation unit of csrc/ is compiled by its own nvcc process (in
 parallel), then linked into _lib/libmla_decode.so with the CUDA runtime
 linked statically, so the library loads on a machine without a GPU driver.
+Beside it the host compiler makes _lib/fastcall.so, the binding's short way past
+the interpreter (csrc_host/), against the installed PyTorch.  The binding does
+without it where it cannot be built: it only saves a call's time on the host.
 """
 from __future__ import annotations
 
@@ -22,6 +25,8 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB_DIR = os.path.join(HERE, "_lib")
 OBJ_DIR = os.path.join(LIB_DIR, "obj")
 SO = os.path.join(LIB_DIR, "libmla_decode.so")
+FAST_SRC = os.path.join(HERE, "csrc_host", "fastcall.cpp")
+FAST = os.path.join(LIB_DIR, "fastcall.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -46,10 +51,53 @@ def up_to_date() -> bool:
     return all(os.path.getmtime(d) <= t for d in deps) and os.path.getmtime(__file__) <= t
 
 
+def _start_fast(force: bool):
+    """Starts the host compiler on fastcall.cpp if it has to run -> (process,
+    its output file) or None."""
+    deps = [FAST_SRC, os.path.join(INCLUDE, "mla_decode.h"), __file__]
+    if not force and os.path.exists(FAST) and all(os.path.getmtime(d) <= os.path.getmtime(FAST) for d in deps):
+        return None
+    import sysconfig
+
+    import torch
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(_nvcc()))
+    tmp = FAST + f".tmp{os.getpid()}"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE,
+           "-I", os.path.join(root, "include"), "-I", os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           "-I", sysconfig.get_paths()["include"], "-I", os.path.join(cuda, "include"), FAST_SRC, "-o", tmp,
+           "-L", os.path.join(root, "lib"), "-ltorch_python", "-ltorch_cpu", "-ltorch", "-lc10", "-lc10_cuda"]
+    try:
+        return subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT), tmp
+    except OSError as e:
+        sys.stderr.write(f"fastcall.so not built: {e}\n")
+        return None
+
+
+def _finish_fast(started) -> None:
+    if started is None:
+        return
+    pr, tmp = started
+    text = pr.communicate()[0].decode(errors="replace")
+    if pr.returncode == 0:
+        os.replace(tmp, FAST)
+    else:
+        sys.stderr.write("fastcall.so not built (calls take longer on the host):\n" + text[-4000:])
+
+
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:
+    os.makedirs(OBJ_DIR, exist_ok=True)
+    fast = _start_fast(force)
+    try:
+        return _build_library(force, verbose_ptxas)
+    finally:
+        _finish_fast(fast)
+
+
+def _build_library(force: bool, verbose_ptxas: bool) -> str:
     if not force and up_to_date():
         return SO
-    os.makedirs(OBJ_DIR, exist_ok=True)
     nvcc = _nvcc()
     srcs, _ = _inputs()
     flags = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
