@@ -271,10 +271,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     br->abort = 0;
     fence_mbar_init_cluster();
   }
+  grid_dep_trigger();
   tc_fence_before();
   __syncthreads();
   cluster_sync();  // both CTAs' barriers are there
   tc_fence_after();
+  grid_dep_wait();  // nothing of the caller's is read or written before the kernel in front has ended
   const uint32_t tmem = br->tmem_base;
   const uint32_t sa = smem_u32(base), sw = sa + OFF_W;
 
@@ -481,8 +483,7 @@ int mla_kv_expand(const void *kv_cache, int kv_format, int num_pages, int page_s
   if (e != cudaSuccess) return fail(MLA_ERR_CUDA, cudaGetErrorString(e));
   const long long units = (long long)ceil_div(total, kPairRows) * H;
   const int pairs = (int)(units < sms / 2 ? units : sms / 2);
-  expand_kernel<<<2 * pairs, kThreads, kSmem, (cudaStream_t)stream>>>(uk_map, uv_map, o_map, p);
-  e = cudaGetLastError();
+  e = launch_dependent(expand_kernel, 2 * pairs, kThreads, kSmem, (cudaStream_t)stream, uk_map, uv_map, o_map, p);
   if (e != cudaSuccess) return fail(MLA_ERR_CUDA, cudaGetErrorString(e));
   set_last_error("");
   return MLA_OK;

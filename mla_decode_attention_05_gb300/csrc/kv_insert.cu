@@ -283,6 +283,10 @@ __device__ void rotate_queries(const KvInsertParams &p, const RopeParams &r, int
 template <bool kRope>
 __global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm)
     kv_insert_kernel(KvInsertParams p, RopeParams r, int insert_blocks) {
+  if (kRope) {
+    grid_dep_trigger();
+    grid_dep_wait();  // nothing of the caller's is read or written before the kernel in front has ended
+  }
   // Blocks of both kinds are spread evenly over the grid, so that the queries'
   // stream runs beside the inserts' arithmetic on every SM.
   int block = blockIdx.x;
@@ -372,8 +376,7 @@ cudaError_t launch_kv_insert_rope(const KvInsertParams &p, const RopeParams &r, 
   const long long rest = q_need + sms < most ? most - q_need : sms;
   const int blocks = (int)(need < rest ? need : rest);
   const int q_blocks = (int)(q_need < most - blocks ? q_need : most - blocks);
-  kv_insert_kernel<true><<<blocks + q_blocks, kWarps * 32, kSmemBytes, stream>>>(p, r, blocks);
-  return cudaGetLastError();
+  return launch_dependent(kv_insert_kernel<true>, blocks + q_blocks, kWarps * 32, kSmemBytes, stream, p, r, blocks);
 }
 
 }  // namespace mla

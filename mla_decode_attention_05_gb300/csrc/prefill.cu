@@ -865,7 +865,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     prefill_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap kn_map,
                    const __grid_constant__ CUtensorMap kp_map, const __grid_constant__ CUtensorMap v_map,
                    PrefillParams p) {
-  grid_dep_trigger();  // the join's blocks may come in as these leave
+  grid_dep_trigger();
   extern __shared__ uint8_t smem_raw[];
   uint8_t *base = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   Bars *br = reinterpret_cast<Bars *>(base + OFF_BARS);
@@ -901,6 +901,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  grid_dep_wait();  // nothing of the caller's is read or written before the kernel in front has ended
   const uint32_t tmem = br->tmem_base, smem = smem_u32(base);
   if (warp < 8) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
@@ -1043,21 +1044,10 @@ int mla_prefill(const void *q, int64_t q_tok, int64_t q_head, const void *k_nope
   p.scale_log2 = softmax_scale * LOG2E;
   cudaError_t e = cudaFuncSetAttribute(prefill_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
   if (e != cudaSuccess) return fail(MLA_ERR_CUDA, cudaGetErrorString(e));
-  prefill_kernel<<<(unsigned)(tiles * H * splits), kThreads, kSmem, (cudaStream_t)stream>>>(q_map, kn_map, kp_map,
-                                                                                              v_map, p);
-  e = cudaGetLastError();
-  if (e == cudaSuccess && splits > 1) {
-    cudaLaunchAttribute pdl[1];
-    pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    pdl[0].val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(((long long)Nq * H + 7) / 8));
-    cfg.blockDim = dim3(256);
-    cfg.stream = (cudaStream_t)stream;
-    cfg.attrs = pdl;
-    cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, prefill_join_kernel, p);
-  }
+  e = launch_dependent(prefill_kernel, (unsigned)(tiles * H * splits), kThreads, kSmem, (cudaStream_t)stream, q_map,
+                       kn_map, kp_map, v_map, p);
+  if (e == cudaSuccess && splits > 1)
+    e = launch_dependent(prefill_join_kernel, (unsigned)(((long long)Nq * H + 7) / 8), 256, 0, (cudaStream_t)stream, p);
   if (e != cudaSuccess) return fail(MLA_ERR_CUDA, cudaGetErrorString(e));
   set_last_error("");
   return MLA_OK;

@@ -79,9 +79,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     br->abort = 0;
     fence_mbar_init_cluster();
   }
+  grid_dep_trigger();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  grid_dep_wait();  // nothing of the caller's is read or written before the kernel in front has ended
   const uint32_t tmem = br->tmem_base, smem = smem_u32(base);
   const uint32_t box = (uint32_t)ntile * 128;
 
@@ -237,9 +239,8 @@ int mla_value_project(const void *attn, int64_t ld_token, int64_t ld_head, const
   if (e == cudaSuccess) e = cudaFuncSetAttribute(value_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
   if (e != cudaSuccess) return fail(MLA_ERR_CUDA, cudaGetErrorString(e));
   const int items = tiles * H;
-  value_kernel<<<items < sms ? items : sms, kThreads, kSmem, (cudaStream_t)stream>>>(w_map, x_map, o_map, tiles, items,
-                                                                                     ntile, st);
-  e = cudaGetLastError();
+  e = launch_dependent(value_kernel, items < sms ? items : sms, kThreads, kSmem, (cudaStream_t)stream, w_map, x_map,
+                       o_map, tiles, items, ntile, st);
   if (e != cudaSuccess) return fail(MLA_ERR_CUDA, cudaGetErrorString(e));
   set_last_error("");
   return MLA_OK;
