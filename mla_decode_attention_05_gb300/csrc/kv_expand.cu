@@ -271,6 +271,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     br->abort = 0;
     fence_mbar_init_cluster();
   }
+  if (threadIdx.x == 4 * 32) {
+    prefetch_tensormap(rank == 0 ? &uk_map : &uv_map);
+    prefetch_tensormap(&o_map);
+  }
   grid_dep_trigger();
   tc_fence_before();
   __syncthreads();

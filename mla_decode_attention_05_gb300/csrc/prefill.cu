@@ -144,9 +144,11 @@ __device__ Work find_work(const PrefillParams &p, int t, int h, int lane, Place 
   bool back = false;
   for (;;) {
     const int b = at.b0 + lane;
-    int s = 0, e = 0;
+    int s = 0, e = 0, ck = 0, cke = 0;
     if (b < p.B) {
       const int cs = __ldg(p.cu_q + b), ce = __ldg(p.cu_q + b + 1);
+      ck = __ldg(p.cu_k + b);
+      cke = __ldg(p.cu_k + b + 1);
       s = min(max(cs, 0), p.Nq);
       e = min(max(ce, s), p.Nq);
       if (s != cs || e != ce) atomicOr(p.status, MLA_STATUS_BAD_SEQLEN);
@@ -177,7 +179,8 @@ __device__ Work find_work(const PrefillParams &p, int t, int h, int lane, Place 
     const int part = t - at.before - __shfl_sync(0xffffffffu, upto - mine, who);
     s = __shfl_sync(0xffffffffu, s, who);
     e = __shfl_sync(0xffffffffu, e, who);
-    const int ck = __ldg(p.cu_k + at.b0 + who), cke = __ldg(p.cu_k + at.b0 + who + 1);
+    ck = __shfl_sync(0xffffffffu, ck, who);
+    cke = __shfl_sync(0xffffffffu, cke, who);
     w.k0 = min(max(ck, 0), p.Nk);
     w.nk = min(max(cke, w.k0), p.Nk) - w.k0;
     if (lane == 0 && (w.k0 != ck || w.k0 + w.nk != cke)) atomicOr(p.status, MLA_STATUS_BAD_SEQLEN);
@@ -897,6 +900,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     br->redo_count = 0;
     br->abort = 0;
     fence_mbar_init_cluster();
+  }
+  if (threadIdx.x == 9 * 32) {
+    prefetch_tensormap(&q_map);
+    prefetch_tensormap(&kn_map);
+    prefetch_tensormap(&kp_map);
+    prefetch_tensormap(&v_map);
   }
   tc_fence_before();
   __syncthreads();

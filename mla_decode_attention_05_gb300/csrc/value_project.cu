@@ -79,6 +79,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     br->abort = 0;
     fence_mbar_init_cluster();
   }
+  if (threadIdx.x == 4 * 32) {
+    prefetch_tensormap(&w_map);
+    prefetch_tensormap(&x_map);
+    prefetch_tensormap(&o_map);
+  }
   grid_dep_trigger();
   tc_fence_before();
   __syncthreads();
