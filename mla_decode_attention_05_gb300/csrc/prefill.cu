@@ -66,6 +66,7 @@ constexpr uint32_t TM_O = 256;
 constexpr uint32_t IDESC_QK = idesc_bf16_f32(128, 128, false, false);
 constexpr uint32_t IDESC_PV = idesc_bf16_f32(128, 128, false, true);
 constexpr float kMoveAt = 8.f;
+constexpr int kMaxSplits = 32;  // parts of a unit's keys, a lane each in the join
 
 struct PrefillParams {
   const int32_t *cu_q, *cu_k;
@@ -812,20 +813,33 @@ __device__ __forceinline__ void softmax_rows(const PrefillParams &p, Bars *br, u
   }
 }
 
-// Splits joined: one warp a row and head, four values a lane.
-__global__ void __launch_bounds__(256) prefill_join_kernel(PrefillParams p) {
-  grid_dep_wait();  // (a programmatic dependent of the kernel above)
-  const int lane = threadIdx.x & 31;
-  const long long i = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (i >= (long long)p.Nq * p.H) return;
+// Splits joined: four warps a row and head, every fourth part each, four values
+// a lane.  All loads go out at once (a warp that took eight parts at a time after
+// it had found its row needed 11 us for 1600 rows of 19 parts).
+constexpr int kJoinWarps = 4;
+__global__ void __launch_bounds__(32 * kJoinWarps) prefill_join_kernel(PrefillParams p) {
+  __shared__ float4 sums[kJoinWarps][32];
+  grid_dep_trigger();
+  grid_dep_wait();  // (a programmatic dependent of the kernel below)
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const long long i = blockIdx.x;
   const int row = (int)(i / p.H), h = (int)(i % p.H);
+  const float *part = p.part_o + (size_t)i * kDv + 4 * lane;
+  const size_t next = (size_t)p.Nq * p.H * kDv;
+  float4 v[kMaxSplits / kJoinWarps];
+#pragma unroll
+  for (int k = 0; k < kMaxSplits / kJoinWarps; k++) {
+    const int s = warp + kJoinWarps * k;
+    v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (s < p.splits) v[k] = *reinterpret_cast<const float4 *>(part + s * next);
+  }
+  const float mine = lane < p.splits ? p.part_lse[((size_t)lane * p.H + h) * p.Nq + row] : -INFINITY;
   int lo = 0, hi = p.B;  // the last sequence that starts at or before the row
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
     if (__ldg(p.cu_q + mid) <= row) lo = mid; else hi = mid;
   }
-  if (row < __ldg(p.cu_q + lo) || row >= __ldg(p.cu_q + lo + 1)) return;  // of no sequence
-  const float mine = lane < p.splits ? p.part_lse[((size_t)lane * p.H + h) * p.Nq + row] : -INFINITY;
+  const bool live = row >= __ldg(p.cu_q + lo) && row < __ldg(p.cu_q + lo + 1);  // else: of no sequence
   // (a nan among them has to stay one: not through fmaxf alone)
   float m = mine;
 #pragma unroll
@@ -835,26 +849,26 @@ __global__ void __launch_bounds__(256) prefill_join_kernel(PrefillParams p) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  const float *part = p.part_o + (size_t)i * kDv + 4 * lane;
-  const size_t next = (size_t)p.Nq * p.H * kDv;
-  constexpr int kBatch = 8;  // parts on their way at a time
-  for (int s0 = 0; s0 < p.splits; s0 += kBatch) {
-    float4 v[kBatch];
 #pragma unroll
-    for (int k = 0; k < kBatch; k++) {
-      // (a part without keys has weight 0 and finite values)
-      v[k] = s0 + k < p.splits ? __ldcs(reinterpret_cast<const float4 *>(part + (s0 + k) * next))
-                               : make_float4(0.f, 0.f, 0.f, 0.f);
-    }
+  for (int k = 0; k < kMaxSplits / kJoinWarps; k++) {
+    const int s = warp + kJoinWarps * k;
+    const float ws = __shfl_sync(0xffffffffu, weight, s);
+    if (s >= p.splits) continue;
+    acc.x += ws * v[k].x;  // (a part without keys has weight 0 and finite values)
+    acc.y += ws * v[k].y;
+    acc.z += ws * v[k].z;
+    acc.w += ws * v[k].w;
+  }
+  sums[warp][lane] = acc;
+  __syncthreads();
+  if (warp != 0 || !live) return;
 #pragma unroll
-    for (int k = 0; k < kBatch; k++) {
-      const float ws = __shfl_sync(0xffffffffu, weight, (s0 + k) & 31);
-      if (s0 + k >= p.splits) continue;
-      acc.x += ws * v[k].x;
-      acc.y += ws * v[k].y;
-      acc.z += ws * v[k].z;
-      acc.w += ws * v[k].w;
-    }
+  for (int k = 1; k < kJoinWarps; k++) {
+    const float4 o = sums[k][lane];
+    acc.x += o.x;
+    acc.y += o.y;
+    acc.z += o.z;
+    acc.w += o.w;
   }
   const bool none = sum == 0.f;
   const float inv = none ? 0.f : 1.f / sum;
@@ -960,7 +974,6 @@ long long tiles_of(int B, int Nq) { return Nq < B ? Nq : (Nq - B) / kCtaRows + (
 // sequence of average length).  8 heads, 200 queries on 12200 keys: 8 parts of
 // 96 steps or 152 of 5.
 constexpr int kSms = 152;
-constexpr int kMaxSplits = 32;  // a lane each in the join
 int splits_of(int B, int H, int Nq, int Nk) {
   const long long works = tiles_of(B, Nq) * H;
   if (B < 1 || works < 1 || 2 * works > kSms) return 1;
@@ -1056,7 +1069,7 @@ int mla_prefill(const void *q, int64_t q_tok, int64_t q_head, const void *k_nope
   e = launch_dependent(prefill_kernel, (unsigned)(tiles * H * splits), kThreads, kSmem, (cudaStream_t)stream, q_map,
                        kn_map, kp_map, v_map, p);
   if (e == cudaSuccess && splits > 1)
-    e = launch_dependent(prefill_join_kernel, (unsigned)(((long long)Nq * H + 7) / 8), 256, 0, (cudaStream_t)stream, p);
+    e = launch_dependent(prefill_join_kernel, (unsigned)((long long)Nq * H), 32 * kJoinWarps, 0, (cudaStream_t)stream, p);
   if (e != cudaSuccess) return fail(MLA_ERR_CUDA, cudaGetErrorString(e));
   set_last_error("");
   return MLA_OK;
