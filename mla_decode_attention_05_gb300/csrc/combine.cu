@@ -56,8 +56,10 @@ combine_kernel(DecodeParams p) {
   const int i = blockIdx.x;
   const int base = p.num_splits[i];
   const int ns = p.num_splits[i + 1] - base;
+  // The decode kernel's partials are complete.  (Every block waits: a programmatic
+  // dependent of this kernel waits for it alone, and reads what the decode wrote.)
+  grid_dep_wait();
   if (ns <= 1) return;
-  grid_dep_wait();  // the decode kernel's partials are complete
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int b, row0, rows;
   if (p.topk_len > 0) {

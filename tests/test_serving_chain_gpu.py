@@ -142,3 +142,44 @@ def test_runs_give_the_same_bits():
     first = [t.clone() for t in _chunk(s)]
     for _ in range(5):
         assert all(torch.equal(x, y) for x, y in zip(_chunk(s), first))
+
+
+@pytest.mark.parametrize("H,lens", [(16, [40] * 64), (128, [500, 64, 3000])])
+def test_a_projection_right_behind_its_decode(H, lens):
+    """Sequences of one part and of several: the projection starts while the
+    decode's last kernel ends, and reads what the decode itself wrote.  Eager and
+    replayed without a pause, the bits of calls that wait for one another."""
+    import mla_decode_attention_05_gb300 as mla
+    rng = np.random.default_rng(41)
+    B = len(lens)
+    per = [-(-m // 64) for m in lens]
+    bt = torch.zeros((B, max(per)), dtype=torch.int32)
+    for b, m in enumerate(per):
+        bt[b, :m] = torch.arange(sum(per[:b]), sum(per[:b + 1]))
+    bt, sk = bt.cuda(), torch.tensor(lens, dtype=torch.int32, device="cuda")
+    cache = bf16(rng, (sum(per), 64, 576)).cuda()
+    w_uv = bf16(rng, (H, 128, 512), 512 ** -0.5).cuda()
+    qs = [bf16(rng, (B, 1, H, 576), 0.3).cuda() for _ in range(4)]
+    q = torch.empty_like(qs[0])
+
+    def step(x, wait=False):
+        q.copy_(x)
+        o, _ = mla.decode(q, cache, bt, sk, softmax_scale=SCALE)
+        if wait:
+            torch.cuda.synchronize()
+        return mla.value_project(o.view(B, H, 512), w_uv)
+    mla.device_status()
+    want = [step(x, True).clone() for x in qs]
+    for _ in range(5):
+        got = [step(x) for x in qs]
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = [step(x) for x in qs]
+    for _ in range(5):
+        for t in got:
+            t.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert mla.device_status() == 0
