@@ -273,7 +273,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     mbar_init(smem_u32(&br->a_full), 2 * kRowWarps);
     for (int s = 0; s < 2; s++) {
       mbar_init(smem_u32(&br->d_full[s]), 1);
-      mbar_init(smem_u32(&br->d_empty[s]), few ? 2 * kRowWarps : kRowWarps);
+      mbar_init(smem_u32(&br->d_empty[s]), 2 * kRowWarps);
     }
     br->abort = 0;
     fence_mbar_init_cluster();
@@ -372,7 +372,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       __syncwarp();
       // relaxed: nothing but tensor memory has been read, and the releasing
       // form would wait for the output's way to memory (3700 cycles a unit)
-      if (lane == 0 && c1 > 0) mbar_arrive_remote_relaxed(mapa(smem_u32(&br->d_empty[buf]), 0));
+      // (also from a warp that drains nothing: d_full must not run a phase ahead of it)
+      if (lane == 0) mbar_arrive_remote_relaxed(mapa(smem_u32(&br->d_empty[buf]), 0));
     }
     if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
   } else if (warp == kRowWarps) {
