@@ -177,8 +177,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&br->d_empty[buf]));
       fence_proxy_async_smem();
-      named_bar_sync(1, 128);
-      if (*(volatile int *)&br->abort) break;  // (set before the barrier by whoever gave up: nothing of this tile is stored)
+      // all four warps stop together, at the barrier (abort alone may be set
+      // by another role between their looks at it); nothing of this tile is stored then
+      if (bar_red_or(1, 128, !ok || *(volatile int *)&br->abort)) break;
       if (threadIdx.x == 0) {
         asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
                          reinterpret_cast<uint64_t>(&o_map)),
