@@ -407,6 +407,7 @@ int mla_kv_expand(const void *kv_cache, int kv_format, int num_pages, int page_s
  *   lse[h][i] = ln sum_j exp(s_j),  out[i][h] = sum_j exp(s_j - lse) v[j][h]
  * over all n_k keys (causal = 0) or j < n_k - n_q + i + 1 (causal = 1: the
  * last query sees every key).  A row that sees no key gets out = 0 and
+ * lse = -inf; one whose scores are all -inf gets out = nan (0 / 0) and
  * lse = -inf.  Keys and values that a row does not see do not reach it,
  * whatever they hold (inf and nan too).
  *

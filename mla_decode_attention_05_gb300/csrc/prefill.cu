@@ -716,7 +716,8 @@ __device__ __forceinline__ bool softmax_work(const PrefillParams &p, Bars *br, u
     if (!warp_wait_ok(br, &br->o_done[t], (done + n - 1) & 1, p.status)) return false;
     tc_fence_after();
   }
-  const float inv = l != 0.f ? 1.f / l : 0.f;
+  // l = 0: every score of the row is -inf (0 / 0: nan, unless another part of its keys has weight)
+  const float inv = l != 0.f || p.splits == 1 ? 1.f / l : 0.f;
   // have the steps that were looked through non-finite values?
   const uint32_t *bad_keys = br->bad_keys[slot];
   bool bad = false;
@@ -871,7 +872,12 @@ __global__ void __launch_bounds__(32 * kJoinWarps) prefill_join_kernel(PrefillPa
     acc.w += o.w;
   }
   const bool none = sum == 0.f;
-  const float inv = none ? 0.f : 1.f / sum;
+  float inv = none ? 0.f : 1.f / sum;
+  if (none) {  // no key, or all scores -inf?
+    const int s = min(max(__ldg(p.cu_q + lo), 0), p.Nq), e = min(max(__ldg(p.cu_q + lo + 1), s), p.Nq);
+    const int k0 = min(max(__ldg(p.cu_k + lo), 0), p.Nk), nk = min(max(__ldg(p.cu_k + lo + 1), k0), p.Nk) - k0;
+    if ((p.causal ? min(nk, nk - (e - s) + row - s + 1) : nk) > 0) inv = INFINITY;  // 0 / 0
+  }
   __nv_bfloat162 a = __floats2bfloat162_rn(acc.x * inv, acc.y * inv), b = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
   uint2 r = make_uint2(*reinterpret_cast<uint32_t *>(&a), *reinterpret_cast<uint32_t *>(&b));
   *reinterpret_cast<uint2 *>(p.out + (size_t)i * kDv + 4 * lane) = r;
@@ -1008,8 +1014,8 @@ int mla_prefill(const void *q, int64_t q_tok, int64_t q_head, const void *k_nope
     return fail(MLA_ERR_UNSUPPORTED, "B must be at most 2^20, Nq at most 2^30, Nk at most 2^26");
   if (H < 1 || H > MLA_MAX_HEADS) return fail(MLA_ERR_INVALID_ARG, "H must be in [1, 128]");
   if (causal != 0 && causal != 1) return fail(MLA_ERR_INVALID_ARG, "causal must be 0 or 1");
-  if (!(softmax_scale > 0.f) || softmax_scale > 3.0e38f)
-    return fail(MLA_ERR_INVALID_ARG, "softmax_scale must be finite and > 0");
+  if (!(softmax_scale > 0.f) || softmax_scale > 2.0e38f)  // (log2 e times it is finite too)
+    return fail(MLA_ERR_INVALID_ARG, "softmax_scale must be > 0 and at most 2e38");
   for (int64_t s : {q_tok, q_head, k_tok, k_head, pe_tok, v_tok, v_head})
     if (s % 8) return fail(MLA_ERR_INVALID_ARG, "strides must be multiples of 8 elements");
   if ((Nq > 1 && q_tok < kHead) || (H > 1 && q_head < kHead) || (Nk > 1 && (k_tok < kNope || v_tok < kDv || pe_tok < 64)) ||

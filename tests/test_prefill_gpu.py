@@ -179,6 +179,27 @@ def test_a_value_that_is_not_finite_reaches_the_rows_that_see_it(bad):
     assert torch.equal(out[~hit], want[~hit]) and torch.equal(lse, wl)
 
 
+@pytest.mark.parametrize("nq,nk", [([70], [200]), ([3], [4000])])
+def test_scores_of_minus_infinity(nq, nk):
+    """Keys whose scores are -inf: of weight 0 beside others, as if they
+    were not there, and 0 / 0 where a row sees no
+    other key.  In one part and in several."""
+    import mla_decode_attention_05_gb300 as mla
+    H = 2
+    q, kn, kp, v = _inputs(nq, nk, H, 31)
+    q[:, :, 128] = 1.0
+    gone = kp.clone()
+    gone[:, 0] = -float("inf")
+    out, lse = mla.prefill(q, kn, gone, v, cu(nq), cu(nk), softmax_scale=SCALE)
+    assert bool(out.isnan().all()) and bool(lse.isneginf().all())
+    some = gone.clone()
+    keep = [5, 130, nk[0] - 100]
+    some[keep] = kp[keep]
+    out, lse = mla.prefill(q, kn, some, v, cu(nq), cu(nk), softmax_scale=SCALE, causal=False)
+    few = (q, kn[keep], kp[keep], v[keep])
+    _check(out, lse, few, nq, [3], False)
+
+
 def test_many_short_sequences():
     """Thousands of sequences, empty ones among them, some of several tiles."""
     import mla_decode_attention_05_gb300 as mla

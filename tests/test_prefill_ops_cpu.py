@@ -66,7 +66,7 @@ def test_expand_arguments(L, args, code):
     (dict(B=-1), -1), (dict(B=(1 << 20) + 1), -2), (dict(Nq=-1), -1), (dict(Nk=-1), -1), (dict(Nq=(1 << 30) + 1), -2),
     (dict(Nk=(1 << 26) + 1), -2),
     (dict(H=0), -1), (dict(H=129), -1), (dict(causal=2), -1), (dict(scale=0.0), -1), (dict(scale=float("nan")), -1),
-    (dict(scale=float("inf")), -1), (dict(q_tok=100), -1), (dict(q_head=188), -1), (dict(k_tok=64), -1),
+    (dict(scale=float("inf")), -1), (dict(scale=2.5e38), -1), (dict(q_tok=100), -1), (dict(q_head=188), -1), (dict(k_tok=64), -1),
     (dict(v_head=132), -1), (dict(pe_tok=32), -1), (dict(q=None), -1), (dict(q=264), -1), (dict(out=8), -1),
     (dict(lse=2), -1), (dict(cq=None), -1), (dict(ck=257), -1), (dict(kn=None), -1), (dict(vv=264), -1),
     (dict(Nq=0, q=None, out=None, lse=None), 0), (dict(B=0), 0),
