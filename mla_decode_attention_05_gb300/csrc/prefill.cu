@@ -103,13 +103,14 @@ constexpr int kNever = 1 << 30;
 constexpr int kRedo = 64;
 
 struct Bars {
-  uint64_t full[kUnits], empty[kUnits];
+  uint64_t k_full[2], v_full[2];  // the keys (values) of every second step have landed
+  uint64_t empty[kUnits];         // all products with this part of the ring are done
   uint64_t work_full[2], work_empty[2];
   uint64_t taken;       // the load warp is about to end a unit of work
   uint64_t q_full[2], q_empty[2];
   uint64_t s_full[2];   // scores of a tile are in tensor memory
   uint64_t p_full[2][2];  // its probabilities are: of the first and the last 64 keys
-  uint64_t o_done[2];   // its P V has been added
+  uint64_t o_done[2];   // its last P V of a unit of work has been added
   uint64_t o_free[2];   // its output has been read
   uint64_t v_look;      // the values of a step are there (told by the waiting warp: the ring's barriers
                         // can be a phase further than a warp that does not follow every unit)
@@ -217,15 +218,14 @@ __device__ __forceinline__ void take_split(Work &w, int i, int splits) {
   w.diff -= from * kKeys;
 }
 
-__device__ __forceinline__ bool wait_ok(Bars *b, uint64_t *bar, uint32_t parity, unsigned int *status) {
-  if (mbar_wait<false>(smem_u32(bar), parity, &b->abort, kDefaultWaitNs)) return true;
-  atomicOr(status, MLA_STATUS_WAIT_TIMEOUT);
-  *(volatile int *)&b->abort = 1;
-  return false;
+// A bounded wait; the kernel tells of one that gave up at its end.  (With the
+// longer form of a wait in its twenty places: ragged prompts 304 us, not 296.)
+__device__ __forceinline__ bool wait_ok(Bars *b, uint64_t *bar, uint32_t parity) {
+  return mbar_wait_small<false>(smem_u32(bar), parity, &b->abort, (uint32_t)kDefaultWaitNs);
 }
 
-__device__ __forceinline__ bool warp_wait_ok(Bars *b, uint64_t *bar, uint32_t parity, unsigned int *status) {
-  return __all_sync(0xffffffffu, wait_ok(b, bar, parity, status));
+__device__ __forceinline__ bool warp_wait_ok(Bars *b, uint64_t *bar, uint32_t parity) {
+  return __all_sync(0xffffffffu, wait_ok(b, bar, parity));
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -303,56 +303,61 @@ __device__ __forceinline__ Work block_work(const PrefillParams &p, int block, in
   return w;
 }
 
-// The load warp.  One lane asks for the units in their order, each as soon as
-// its place in the ring is free (a lane for each unit of a step would make the
-// first ones wait for the last one's place: 8192 tokens 563 us).
+// The load warp asks for the units in their order, each as soon as its place in
+// the ring is free.  That decides how early keys are there, and so the time: places
+// are freed one by one (all keys, all values of a step at a time: 440 instead of
+// 421 us for 8192 tokens), and the whole warp waits while one elected lane asks (a
+// loop of one lane takes 500 cycles a unit: 421 instead of 409 us).
 __device__ __forceinline__ void load_rows(const CUtensorMap *q_map, const CUtensorMap *kn_map,
                                           const CUtensorMap *kp_map, const CUtensorMap *v_map, Bars *br,
-                                          uint32_t smem, unsigned int *status, int lane) {
+                                          uint32_t smem, int lane) {
   const uint64_t pol = policy_evict_normal(), once = policy_evict_first();
-  uint32_t u = 0, tiles0 = 0, tiles1 = 0;  // units, tiles so far
+  uint32_t u = 0, steps = 0, tiles0 = 0, tiles1 = 0;  // units, steps, tiles so far
   for (uint32_t count = 0;; count++) {
     const uint32_t slot = count & 1;
-    if (!warp_wait_ok(br, &br->work_full[slot], (count >> 1) & 1, status)) return;
+    if (!warp_wait_ok(br, &br->work_full[slot], (count >> 1) & 1)) return;
     const Work w = br->work[slot];
     const Steps st = br->steps[slot];
     __syncwarp();
     if (w.nq == 0) return;
     if (lane == 0) mbar_arrive(smem_u32(&br->work_empty[slot]));
-    bool ok = true;
-    if (lane == 0) {
 #pragma unroll 1
-      for (int t = 0; t < 2 && ok; t++) {
-        if ((t == 0 ? st.n[0] : st.n[1]) == 0) continue;
-        const uint32_t full = smem_u32(&br->q_full[t]);
-        ok = wait_ok(br, &br->q_empty[t], ((t == 0 ? tiles0++ : tiles1++) & 1) ^ 1, status);
-        if (!ok) break;
+    for (int t = 0; t < 2; t++) {
+      if ((t == 0 ? st.n[0] : st.n[1]) == 0) continue;
+      const uint32_t full = smem_u32(&br->q_full[t]);
+      if (!warp_wait_ok(br, &br->q_empty[t], ((t == 0 ? tiles0++ : tiles1++) & 1) ^ 1)) return;
+      if (elect_one()) {
         mbar_arrive_expect_tx(full, 3 * kUnit);
 #pragma unroll 1
         for (int c = 0; c < 3; c++)
-          tma_load_3d(smem + (3 * t + c) * kUnit, q_map, full, 64 * c, w.h, w.q0 + t * kRows, once);
+          tma_load_3d(smem + (3 * t + c) * kUnit, q_map, full, 64 * c, w.q0 + t * kRows, w.h, once);
       }
-      if (st.most == 0) mbar_arrive(smem_u32(&br->taken));
+      __syncwarp();
+    }
+    if (st.most == 0 && lane == 0) mbar_arrive(smem_u32(&br->taken));
 #pragma unroll 1
-      for (int j = 0; j < st.most && ok; j++) {
-        if (j == max(0, st.most - 3)) mbar_arrive(smem_u32(&br->taken));
-        const int key = w.k0 + j * kKeys;
-#pragma unroll 1
-        for (int c = 0; c < kUnitsPerStep; c++, u++) {
-          const uint32_t s = u % kUnits, full = smem_u32(&br->full[s]), dst = smem + OFF_RING + s * kUnit;
-          ok = wait_ok(br, &br->empty[s], ((u / kUnits) & 1) ^ 1, status);
-          if (!ok) break;
-          mbar_arrive_expect_tx(full, kUnit);
+    for (int j = 0; j < st.most; j++) {
+      if (j == max(0, st.most - 3) && lane == 0) mbar_arrive(smem_u32(&br->taken));
+      const int key = w.k0 + j * kKeys;
+      const uint32_t g = steps + j, k_full = smem_u32(&br->k_full[g & 1]), v_full = smem_u32(&br->v_full[g & 1]);
+#pragma unroll
+      for (int c = 0; c < kUnitsPerStep; c++, u++) {
+        const uint32_t s = u % kUnits, dst = smem + OFF_RING + s * kUnit;
+        if (!warp_wait_ok(br, &br->empty[s], ((u / kUnits) & 1) ^ 1)) return;
+        if (elect_one()) {
+          if (c == 0) mbar_arrive_expect_tx(k_full, 3 * kUnit);
+          if (c == 3) mbar_arrive_expect_tx(v_full, 2 * kUnit);
           if (c < 3) {
-            tma_load_3d(dst, c < 2 ? kn_map : kp_map, full, c < 2 ? 64 * c : 0, c < 2 ? w.h : 0, key, pol);
+            tma_load_3d(dst, c < 2 ? kn_map : kp_map, k_full, c < 2 ? 64 * c : 0, key, c < 2 ? w.h : 0, pol);
           } else {
-            tma_load_3d(dst, v_map, full, 0, w.h, key + 64 * (c - 3), pol);
-            tma_load_3d(dst + kUnit / 2, v_map, full, 64, w.h, key + 64 * (c - 3), pol);
+            tma_load_3d(dst, v_map, v_full, 0, key + 64 * (c - 3), w.h, pol);
+            tma_load_3d(dst + kUnit / 2, v_map, v_full, 64, key + 64 * (c - 3), w.h, pol);
           }
         }
+        __syncwarp();
       }
     }
-    if (!__all_sync(0xffffffffu, ok)) return;
+    steps += st.most;
   }
 }
 
@@ -365,31 +370,20 @@ __device__ __forceinline__ void load_rows(const CUtensorMap *q_map, const CUtens
 constexpr uint32_t kMmaBar = 1;
 
 template <bool kWaiter>
-__device__ __forceinline__ void mma_sequence(Bars *br, uint32_t smem, uint32_t tmem, unsigned int *status) {
+__device__ __forceinline__ void mma_sequence(Bars *br, uint32_t smem, uint32_t tmem) {
   const int lane = threadIdx.x & 31;
   const uint64_t q_desc = smem_desc_sw128(smem, 16, 1024), k_desc = smem_desc_sw128(smem + OFF_RING, 16, 1024);
   const uint64_t v_desc = smem_desc_sw128(smem + OFF_RING, kUnit / 2, 1024);
   bool ok = true;
   uint32_t base = 0, masked = 0, steps0 = 0, steps1 = 0, works0 = 0, works1 = 0;  // units, masked steps, steps, works so far
-  // up to `units` units from u on, and two barriers more, each waited for by a
-  // lane of its own (one after the other, the waits cost 60 cycles each)
-  auto wait_for = [&](uint32_t u, int units, uint64_t *bar, uint32_t parity, uint64_t *bar2, uint32_t parity2) {
-    if (!kWaiter) return;
-    uint64_t *mine = nullptr;
-    if (lane < units) {
-      mine = &br->full[(u + lane) % kUnits];
-      parity = ((u + lane) / kUnits) & 1;
-    } else if (lane == units) {
-      mine = bar;
-    } else if (lane == units + 1) {
-      mine = bar2;
-      parity = parity2;
-    }
-    ok = __all_sync(0xffffffffu, ok && (mine == nullptr || wait_ok(br, mine, parity, status)));
+  uint32_t steps = 0;  // of both tiles
+  // (one wait after the other, each by the whole warp: side by side, a lane for
+  // each, five waits took 400 cycles even where all were over)
+  auto wait = [&](uint64_t *bar, uint32_t parity) {
+    if (kWaiter) ok = ok && warp_wait_ok(br, bar, parity);
   };
   auto meet = [&](bool stop = false) { return !bar_red_or(kMmaBar, 64, !ok || stop); };
-  // Scores of tile t for step j (units 5j .. 5j + 2).  A unit goes back to the
-  // loads after the MMAs of the last tile that reads it, Q after the last step.
+  // Scores of tile t for step j (units 5j .. 5j + 2).
   auto qk = [&](int t, int j, bool last, bool last_q) {
     if (kWaiter) return;
     tc_fence_after();
@@ -409,7 +403,7 @@ __device__ __forceinline__ void mma_sequence(Bars *br, uint32_t smem, uint32_t t
     __syncwarp();
   };
   // Half c of P V of tile t for step j (unit 5j + 3 + c: 64 keys).
-  auto pv = [&](int t, int j, int c, bool last) {
+  auto pv = [&](int t, int j, int c, bool last, bool last_o) {
     if (kWaiter) return;
     tc_fence_after();
     if (elect_one()) {
@@ -419,14 +413,14 @@ __device__ __forceinline__ void mma_sequence(Bars *br, uint32_t smem, uint32_t t
       for (int k = 0; k < 4; k++)
         mma_ts(tmem + TM_O + t * 128, tmem + TM_S + t * 128 + c * 32 + k * 8, b + k * (2048 >> 4), IDESC_PV,
                (j | c | k) ? 1u : 0u);
-      if (c == 1) mma_commit(smem_u32(&br->o_done[t]));
+      if (c == 1 && last_o) mma_commit(smem_u32(&br->o_done[t]));
       if (last) mma_commit(smem_u32(&br->empty[s]));
     }
     __syncwarp();
   };
   for (uint32_t count = 0;; count++) {
     const uint32_t slot = count & 1;
-    wait_for(0, 0, &br->work_full[slot], (count >> 1) & 1, nullptr, 0);
+    wait(&br->work_full[slot], (count >> 1) & 1);
     const bool stop = kWaiter && ok && br->work[slot].nq == 0;
     if (!meet(stop)) return;
     const Steps st = br->steps[slot];
@@ -434,48 +428,46 @@ __device__ __forceinline__ void mma_sequence(Bars *br, uint32_t smem, uint32_t t
     if (lane == 0) mbar_arrive(smem_u32(&br->work_empty[slot]));
     const int n0 = st.n[0], n1 = st.n[1];
     // While a tile's softmax runs, the tensor cores work on the other tile:
-    // its P V, then its next scores (j = -1: the first ones).  The loops stay
-    // loops: the code of all roles has to stay in the instruction cache.
+    // its P V, then its next scores (j = -1: the first ones).  One loop for both
+    // tiles: the code of all roles has to stay in the instruction cache.
 #pragma unroll 1
-    for (int j = -1; j < st.most; j++) {
-      const uint32_t uv = base + (uint32_t)(j * kUnitsPerStep + 3);
-      if (j >= st.look) {
+    for (int i = -2; i < 2 * st.most; i++) {
+      const int j = i >> 1, t = i & 1;
+      const uint32_t g = steps + (uint32_t)j;
+      if (t == 0 && j >= st.look) {
         if (kWaiter) {
-          wait_for(uv, 2, nullptr, 0, nullptr, 0);
+          wait(&br->v_full[g & 1], (g >> 1) & 1);
           if (ok && elect_one()) mbar_arrive(smem_u32(&br->v_look));
-          wait_for(uv, 0, &br->v_ok, masked & 1, nullptr, 0);
+          wait(&br->v_ok, masked & 1);
         }
         masked++;
       }
-#pragma unroll 1
-      for (int t = 0; t < 2; t++) {
-        const int n = t == 0 ? n0 : n1, other = t == 0 ? n1 : n0;
-        if (j >= n) continue;
-        const uint32_t work_parity = (t == 0 ? works0 : works1) & 1, step = (t == 0 ? steps0 : steps1) + j;
-        if (j >= 0) {
+      const int n = t == 0 ? n0 : n1, other = t == 0 ? n1 : n0;
+      if (j >= n) continue;
+      const uint32_t work_parity = (t == 0 ? works0 : works1) & 1, step = (t == 0 ? steps0 : steps1) + j;
+      const bool first = t == 0 || j >= other, first_k = t == 0 || j + 1 >= other;
+      const bool last = t == 1 || j >= other, last_k = t == 1 || j + 1 >= other;
+      if (j >= 0) {
+        if (first) wait(&br->v_full[g & 1], (g >> 1) & 1);
+        if (j == 0) wait(&br->o_free[t], work_parity ^ 1);  // the output of the unit of work before has been read
 #pragma unroll
-          for (int c = 0; c < 2; c++) {
-            // first half: the values, and for the first P V of a unit of work the output of the one before; second
-            // half: the next keys, if this tile reads them first
-            if (c == 0) {
-              wait_for(uv, 2, &br->p_full[t][0], step & 1, j == 0 ? &br->o_free[t] : nullptr, work_parity ^ 1);
-            } else {
-              wait_for(uv + 2, j + 1 < n && (t == 0 || j + 1 >= other) ? 3 : 0, &br->p_full[t][1], step & 1, nullptr, 0);
-            }
-            if (!meet()) return;
-            pv(t, j, c, t == 1 || j >= other);
-          }
+        for (int c = 0; c < 2; c++) {
+          wait(&br->p_full[t][c], step & 1);
+          if (!meet()) return;
+          pv(t, j, c, last, j + 1 == n);
         }
-        if (j + 1 < n) {
-          if (j < 0) {
-            wait_for(uv + 2, 3, &br->q_full[t], work_parity, nullptr, 0);
-            if (!meet()) return;
-          }
-          qk(t, j + 1, t == 1 || j + 1 >= other, j + 2 == n);
+      }
+      if (j + 1 < n) {
+        if (first_k || j < 0) {
+          if (first_k) wait(&br->k_full[(g + 1) & 1], ((g + 1) >> 1) & 1);
+          if (j < 0) wait(&br->q_full[t], work_parity);
+          if (!meet()) return;
         }
+        qk(t, j + 1, last_k, j + 2 == n);
       }
     }
     base += (uint32_t)st.most * kUnitsPerStep;
+    steps += st.most;
     steps0 += n0;
     steps1 += n1;
     works0 += n0 > 0 ? 1 : 0;
@@ -486,13 +478,13 @@ __device__ __forceinline__ void mma_sequence(Bars *br, uint32_t smem, uint32_t t
 // The whole warp looks through the values of one unit of work, from step `look`
 // on; base: the unit of the ring that its first step begins with.
 __device__ __forceinline__ bool check_values(Bars *br, uint8_t *ring, const Steps &st, uint32_t slot, uint32_t base,
-                                             uint32_t &looks, int lane, unsigned int *status) {
+                                             uint32_t &looks, int lane) {
   for (int j = st.look; j < st.most; j++) {
-    if (!warp_wait_ok(br, &br->v_look, looks++ & 1, status)) return false;
+    if (!warp_wait_ok(br, &br->v_look, looks++ & 1)) return false;
     bool patched = false;
     for (int c = 0; c < 2; c++) {
-      const uint32_t u = base + (uint32_t)j * kUnitsPerStep + 3 + c, s = u % kUnits;
-      if (!warp_wait_ok(br, &br->full[s], (u / kUnits) & 1, status)) return false;
+      const uint32_t u = base + (uint32_t)j * kUnitsPerStep + 3 + c, s = u % kUnits, g = u / kUnitsPerStep;
+      if (!warp_wait_ok(br, &br->v_full[g & 1], (g >> 1) & 1)) return false;
       uint8_t *unit = ring + s * kUnit;
       // x * 0 summed up stays 0, unless some x is not finite: then it is nan
       uint32_t sum[4] = {0u, 0u, 0u, 0u};
@@ -553,7 +545,7 @@ __device__ __forceinline__ void schedule(const PrefillParams &p, Bars *br, uint8
   Place place = {0, 0};
   // the slot that unit of work number n gets is free
   auto slot_free = [&](uint32_t n) {
-    return warp_wait_ok(br, &br->work_empty[n & 1], ((n >> 1) & 1) ^ 1, p.status);
+    return warp_wait_ok(br, &br->work_empty[n & 1], ((n >> 1) & 1) ^ 1);
   };
   auto tell = [&](const Work &w, const Steps &st) {
     const uint32_t slot = count & 1;
@@ -588,17 +580,17 @@ __device__ __forceinline__ void schedule(const PrefillParams &p, Bars *br, uint8
       if (redo) st.look = st.masked;
       const uint32_t slot = count & 1;
       ok = tell(w, st);
-      if (ok && redo) ok = check_values(br, ring, st, slot, base, looks, lane, p.status);
+      if (ok && redo) ok = check_values(br, ring, st, slot, base, looks, lane);
       base += (uint32_t)st.most * kUnitsPerStep;
       // The next block is taken over when this one's last loads begin: taken
       // earlier, blocks are shared out unevenly (8192 tokens, two units ahead:
       // 545 us).
-      ok = ok && warp_wait_ok(br, &br->taken, (count - 1) & 1, p.status);
+      ok = ok && warp_wait_ok(br, &br->taken, (count - 1) & 1);
     }
     if (!redo && ok) {
       if (lane == 0) ask_next(br);
       // (also after a wait that gave up: the answer has to land before the CTA ends)
-      const bool told = warp_wait_ok(br, &br->next_full, asked++ & 1, p.status);
+      const bool told = warp_wait_ok(br, &br->next_full, asked++ & 1);
       ok = ok && told;
       block = told ? next_block(br) : -1;
       __syncwarp();
@@ -609,21 +601,22 @@ __device__ __forceinline__ void schedule(const PrefillParams &p, Bars *br, uint8
 }
 
 // One row a thread: the softmax of tile t over the steps of one unit of work,
-// then its output.  done: the tile's steps before this unit.
-__device__ __forceinline__ bool softmax_work(const PrefillParams &p, Bars *br, uint32_t tmem, const Work &w,
-                                             const Steps &st, int slot, int t, uint32_t done) {
+// then its output.  done, works: the tile's steps and its units of work with
+// steps before this one.
+__device__ __forceinline__ bool softmax_work(const PrefillParams &p, Bars *br, uint32_t tmem, int slot, int t,
+                                             uint32_t done, uint32_t works) {
   const int warp = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
   const int i = t * kRows + warp * 32 + lane;  // the CTA's row
-  const int seen = visible(w, i);
+  const int seen = visible(br->work[slot], i);
   const uint32_t lanes = (uint32_t)(warp * 32) << 16;
   const uint32_t ts = tmem + TM_S + t * 128 + lanes, to = tmem + TM_O + t * 128 + lanes;
-  const int n = t == 0 ? st.n[0] : st.n[1];
+  const int n = br->steps[slot].n[t];
   float m = -INFINITY;  // reference, in score units
   uint64_t l0 = 0, l1 = 0;
   const uint64_t c2 = pack2(p.scale_log2, p.scale_log2);
   const int low = __shfl_sync(0xffffffffu, seen, 0);  // the fewest keys of the warp's rows
   for (int j = 0; j < n; j++) {
-    if (!warp_wait_ok(br, &br->s_full[t], (done + j) & 1, p.status)) return false;
+    if (!warp_wait_ok(br, &br->s_full[t], (done + j) & 1)) return false;
     tc_fence_after();
     uint32_t s[4][32];
 #pragma unroll
@@ -654,9 +647,7 @@ __device__ __forceinline__ bool softmax_work(const PrefillParams &p, Bars *br, u
     if (__any_sync(0xffffffffu, move)) {
       const float alpha = move ? ex2((m - top) * p.scale_log2) : 1.f;
       if (move) m = top;
-      if (j > 0) {
-        if (!warp_wait_ok(br, &br->o_done[t], (done + j - 1) & 1, p.status)) return false;
-        tc_fence_after();
+      if (j > 0) {  // (the P V before has been added: its MMAs came before this step's scores)
         const uint64_t a2 = pack2(alpha, alpha);
         asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(l0) : "l"(a2));
         asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(l1) : "l"(a2));
@@ -711,9 +702,13 @@ __device__ __forceinline__ bool softmax_work(const PrefillParams &p, Bars *br, u
   unpack2(l0, la, lb);
   unpack2(l1, lc, ld);
   const float l = (la + lb) + (lc + ld);
+  // (the work is read again here, and above only what the steps need: with 28
+  // bytes spilled in the loop ragged prompts took 319 us instead of 303)
+  const Work w = br->work[slot];
+  const Steps st = br->steps[slot];
   const bool live = i < w.nq, none = seen == 0;
   if (n > 0) {
-    if (!warp_wait_ok(br, &br->o_done[t], (done + n - 1) & 1, p.status)) return false;
+    if (!warp_wait_ok(br, &br->o_done[t], works & 1)) return false;
     tc_fence_after();
   }
   // l = 0: every score of the row is -inf (0 / 0: nan, unless another part of its keys has weight)
@@ -723,7 +718,8 @@ __device__ __forceinline__ bool softmax_work(const PrefillParams &p, Bars *br, u
   bool bad = false;
   if (n > 0 && st.look < st.most)
     for (int k = 0; k < 16; k++) bad |= *(volatile const uint32_t *)&bad_keys[k] != 0;
-  float zero = 0.f;  // becomes nan if an output is not finite
+  uint64_t zero = 0;  // (two fp32) becomes nan if an output is not finite
+  const uint64_t inv2 = pack2(none ? 0.f : inv, none ? 0.f : inv);
   const size_t row = w.q0 + i;
   __nv_bfloat16 *dst = p.out + (row * p.H + w.h) * kDv;
   float *part = p.part_o + ((w.split * (size_t)p.Nq + row) * p.H + w.h) * kDv;
@@ -736,9 +732,15 @@ __device__ __forceinline__ bool softmax_work(const PrefillParams &p, Bars *br, u
     }
     if (!live) continue;
 #pragma unroll
-    for (int e = 0; e < 32; e++) {
-      zero = fmaf(__uint_as_float(o[e]), 0.f, zero);
-      o[e] = none ? 0u : __float_as_uint(__uint_as_float(o[e]) * inv);
+    for (int e = 0; e < 32; e += 2) {
+      const uint64_t x = pack2(__uint_as_float(o[e]), __uint_as_float(o[e + 1]));
+      zero = fma2(x, 0ull, zero);
+      uint64_t y;
+      asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(y) : "l"(x), "l"(inv2));
+      float a, b;
+      unpack2(y, a, b);
+      o[e] = none ? 0u : __float_as_uint(a);
+      o[e + 1] = none ? 0u : __float_as_uint(b);
     }
     if (p.splits > 1) {
 #pragma unroll
@@ -766,13 +768,15 @@ __device__ __forceinline__ bool softmax_work(const PrefillParams &p, Bars *br, u
         reinterpret_cast<uint4 *>(dst + 32 * c)[k] = make_uint4(r[4 * k], r[4 * k + 1], r[4 * k + 2], r[4 * k + 3]);
     }
   }
+  float zero0, zero1;
+  unpack2(zero, zero0, zero1);
   if (n > 0) {  // the MMA warp may start the next unit's output
     tc_fence_before();
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_u32(&br->o_free[t]));
   }
   // once more, with a look at the values
-  if (st.masked < st.most && st.look == kNever && __any_sync(0xffffffffu, n > 0 && live && !none && zero != 0.f)) {
+  if (st.masked < st.most && st.look == kNever && __any_sync(0xffffffffu, n > 0 && live && !none && (zero0 != 0.f || zero1 != 0.f))) {
     if (lane == 0 && atomicExch(&br->odd[slot], 1u) == 0) br->redo[atomicAdd(&br->redo_count, 1u) % kRedo] = w.block;
   }
   if (live && bad) {  // rare: add the non-finite values of the keys that this row sees
@@ -800,15 +804,15 @@ __device__ __forceinline__ bool softmax_work(const PrefillParams &p, Bars *br, u
 }
 
 __device__ __forceinline__ void softmax_rows(const PrefillParams &p, Bars *br, uint32_t tmem, int t) {
-  uint32_t done = 0;
+  uint32_t done = 0, works = 0;
   for (uint32_t count = 0;; count++) {
     const uint32_t slot = count & 1;
-    if (!warp_wait_ok(br, &br->work_full[slot], (count >> 1) & 1, p.status)) return;
-    const Work w = br->work[slot];
-    if (w.nq == 0) return;
-    const Steps st = br->steps[slot];
-    if (!softmax_work(p, br, tmem, w, st, (int)slot, t, done)) return;
-    done += t == 0 ? st.n[0] : st.n[1];
+    if (!warp_wait_ok(br, &br->work_full[slot], (count >> 1) & 1)) return;
+    if (br->work[slot].nq == 0) return;
+    if (!softmax_work(p, br, tmem, (int)slot, t, done, works)) return;
+    const int n = br->steps[slot].n[t];
+    done += n;
+    works += n > 0 ? 1 : 0;
     __syncwarp();
     if ((threadIdx.x & 31) == 0) mbar_arrive(smem_u32(&br->work_empty[slot]));
   }
@@ -898,15 +902,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_relinquish();
   }
   if (threadIdx.x == 32) {
-    for (int s = 0; s < kUnits; s++) {
-      mbar_init(smem_u32(&br->full[s]), 1);
-      mbar_init(smem_u32(&br->empty[s]), 1);
-    }
+    for (int s = 0; s < kUnits; s++) mbar_init(smem_u32(&br->empty[s]), 1);
     for (int t = 0; t < 2; t++) {
+      mbar_init(smem_u32(&br->k_full[t]), 1);
+      mbar_init(smem_u32(&br->v_full[t]), 1);
+      mbar_init(smem_u32(&br->q_empty[t]), 1);
       mbar_init(smem_u32(&br->work_full[t]), 1);
       mbar_init(smem_u32(&br->work_empty[t]), 11);  // softmax, MMA, waiting and load warps
       mbar_init(smem_u32(&br->q_full[t]), 1);
-      mbar_init(smem_u32(&br->q_empty[t]), 1);
       mbar_init(smem_u32(&br->s_full[t]), 1);
       mbar_init(smem_u32(&br->p_full[t][0]), 4);
       mbar_init(smem_u32(&br->p_full[t][1]), 4);
@@ -938,16 +941,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     if (warp == 8) {
-      mma_sequence<false>(br, smem, tmem, p.status);
+      mma_sequence<false>(br, smem, tmem);
     } else if (warp == 9) {
-      load_rows(&q_map, &kn_map, &kp_map, &v_map, br, smem, p.status, lane);
+      load_rows(&q_map, &kn_map, &kp_map, &v_map, br, smem, lane);
     } else if (warp == 10) {
       schedule(p, br, base + OFF_RING, lane);
     } else {
-      mma_sequence<true>(br, smem, tmem, p.status);
+      mma_sequence<true>(br, smem, tmem);
     }
   }
   __syncthreads();
+  if (threadIdx.x == 0 && *(volatile int *)&br->abort) atomicOr(p.status, MLA_STATUS_WAIT_TIMEOUT);
   if (*(volatile int *)&br->abort) {  // a wait gave up: let copies or MMAs still in flight land before the CTA exits
     const uint64_t t0 = globaltimer();
     while (globaltimer() - t0 < 2000000ull) {
@@ -1040,11 +1044,11 @@ int mla_prefill(const void *q, int64_t q_tok, int64_t q_head, const void *k_nope
   const int splits = splits_of(B, H, Nq, Nk);
   if (tiles * H * splits > 0x7FFFFFFFll) return fail(MLA_ERR_UNSUPPORTED, "too many query tiles");
   CUtensorMap q_map, kn_map, kp_map, v_map;
-  bool ok = make_map_3d(&q_map, q, kHead, H, Nq, q_head, q_tok, 1, kRows);
+  bool ok = make_map_3d(&q_map, q, kHead, Nq, H, q_tok, q_head, kRows, 1);
   if (Nk > 0) {
-    ok = ok && make_map_3d(&kn_map, k_nope, kNope, H, Nk, k_head, k_tok, 1, kKeys) &&
-         make_map_3d(&kp_map, k_pe, 64, 1, Nk, 64, pe_tok, 1, kKeys) &&
-         make_map_3d(&v_map, v, kDv, H, Nk, v_head, v_tok, 1, kKeys / 2);
+    ok = ok && make_map_3d(&kn_map, k_nope, kNope, Nk, H, k_tok, k_head, kKeys, 1) &&
+         make_map_3d(&kp_map, k_pe, 64, Nk, 1, pe_tok, 64, kKeys, 1) &&
+         make_map_3d(&v_map, v, kDv, Nk, H, v_tok, v_head, kKeys / 2, 1);
   } else {
     kn_map = kp_map = v_map = q_map;  // no step reads them
   }

@@ -134,6 +134,27 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity,
   }
 }
 
+// The same with little code, for kernels whose roles share the instruction cache
+// among many waits: true once the phase has completed; false, with *abort set,
+// after limit_ns (below 2^32) or when *abort is set already.
+template <bool kCluster>
+__device__ __forceinline__ bool mbar_wait_small(uint32_t bar, uint32_t parity, volatile int *abort,
+                                                uint32_t limit_ns) {
+  uint32_t t0 = 0, it = 0;
+  while (!(kCluster ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity))) {
+    if (++it & 15u) continue;
+    uint32_t t;
+    asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t));
+    if (t0 == 0) {
+      t0 = t & ~1u;  // (0: the next look starts)
+    } else if (*abort || t - t0 > limit_ns) {
+      *abort = 1;
+      return false;
+    }
+  }
+  return true;
+}
+
 // ---- cluster / DSMEM -----------------------------------------------------------
 
 __device__ __forceinline__ uint32_t cluster_ctarank() {
