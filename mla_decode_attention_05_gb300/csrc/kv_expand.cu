@@ -377,21 +377,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
   } else if (warp == kRowWarps) {
-    if (lane == 0) {
-      const uint64_t pol = policy_evict_normal();
-      const CUtensorMap *map = rank == 0 ? &uk_map : &uv_map;
-      uint32_t k = 0;
-      bool ok = true;
-      for (int i = 0; i < n && ok; i++) {
-        const int h = order.unit(i) % p.H;
-        for (int kb = 0; kb < kKBlocks; kb++, k++) {
-          const uint32_t s = k % kWStages, dst = sw + s * kWStage;
-          ok = wait_ok(br, &br->w_empty[s], ((k / kWStages) & 1) ^ 1, p.status);
-          if (!ok) break;
+    const uint64_t pol = policy_evict_normal();
+    const CUtensorMap *map = rank == 0 ? &uk_map : &uv_map;
+    uint32_t k = 0;
+    bool ok = true;
+    for (int i = 0; i < n && ok; i++) {
+      const int h = order.unit(i) % p.H;
+      for (int kb = 0; kb < kKBlocks; kb++, k++) {
+        const uint32_t s = k % kWStages, dst = sw + s * kWStage;
+        ok = __all_sync(0xffffffffu, wait_ok(br, &br->w_empty[s], ((k / kWStages) & 1) ^ 1, p.status));
+        if (!ok) break;
+        if (elect_one()) {
           if (rank == 0) mbar_arrive_expect_tx(smem_u32(&br->w_full[s]), 2 * kWStage);
-          const uint32_t full = mapa(smem_u32(&br->w_full[s]), 0);
-          tma_load_3d_pair(dst, map, full, 64 * kb, 0, h, pol);
+          tma_load_3d_pair(dst, map, mapa(smem_u32(&br->w_full[s]), 0), 64 * kb, 0, h, pol);
         }
+        __syncwarp();
       }
     }
   } else if (rank == 0) {

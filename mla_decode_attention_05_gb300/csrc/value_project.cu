@@ -93,27 +93,30 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t box = (uint32_t)ntile * 128;
 
   if (warp == 4) {
-    if (lane == 0) {
-      const uint64_t pol_w = policy_evict_normal(), pol_x = policy_evict_first();
-      uint32_t u = 0, heads = 0;
-      bool ok = true;
-      for (int i = i0; i < i1 && ok; i++) {
-        const int h = i / tiles, n0 = i % tiles * ntile;
-        const bool new_head = i == i0 || n0 == 0;
-        if (new_head) ok = wait_ok(br, &br->w_empty, (heads++ & 1) ^ 1, status);
-        for (int k = 0; k < kKBlocks / 2 && ok; k++, u++) {
-          if (new_head) {
-            mbar_arrive_expect_tx(smem_u32(&br->w_full[k]), 2 * kWBytes);
-            tma_load_3d(smem + 2 * k * kWBytes, &w_map, smem_u32(&br->w_full[k]), 128 * k, 0, h, pol_w);
-            tma_load_3d(smem + (2 * k + 1) * kWBytes, &w_map, smem_u32(&br->w_full[k]), 128 * k + 64, 0, h, pol_w);
-          }
-          const uint32_t s = u % kUnits, dst = smem + OFF_RING + s * kUnit;
-          ok = wait_ok(br, &br->empty[s], ((u / kUnits) & 1) ^ 1, status);
-          if (!ok) break;
+    // the whole warp waits, one elected lane asks
+    const uint64_t pol_w = policy_evict_normal(), pol_x = policy_evict_first();
+    uint32_t u = 0, heads = 0;
+    bool ok = true;
+    for (int i = i0; i < i1 && ok; i++) {
+      const int h = i / tiles, n0 = i % tiles * ntile;
+      const bool new_head = i == i0 || n0 == 0;
+      if (new_head) ok = __all_sync(0xffffffffu, wait_ok(br, &br->w_empty, (heads++ & 1) ^ 1, status));
+      for (int k = 0; k < kKBlocks / 2 && ok; k++, u++) {
+        const uint32_t s = u % kUnits, dst = smem + OFF_RING + s * kUnit;
+        if (new_head && elect_one()) {
+          mbar_arrive_expect_tx(smem_u32(&br->w_full[k]), 2 * kWBytes);
+          tma_load_3d(smem + 2 * k * kWBytes, &w_map, smem_u32(&br->w_full[k]), 128 * k, 0, h, pol_w);
+          tma_load_3d(smem + (2 * k + 1) * kWBytes, &w_map, smem_u32(&br->w_full[k]), 128 * k + 64, 0, h, pol_w);
+        }
+        __syncwarp();
+        ok = __all_sync(0xffffffffu, wait_ok(br, &br->empty[s], ((u / kUnits) & 1) ^ 1, status));
+        if (!ok) break;
+        if (elect_one()) {
           mbar_arrive_expect_tx(smem_u32(&br->full[s]), 2 * box);
           tma_load_3d(dst, &x_map, smem_u32(&br->full[s]), 128 * k, h, n0, pol_x);
           tma_load_3d(dst + box, &x_map, smem_u32(&br->full[s]), 128 * k + 64, h, n0, pol_x);
         }
+        __syncwarp();
       }
     }
   } else if (warp == 5) {
