@@ -156,6 +156,27 @@ def test_more_row_blocks_than_pairs():
     assert mla.device_status() == 0
 
 
+@pytest.mark.parametrize("H,n", [(2, 300), (4, 16000), (8, 16383), (8, 12000)])
+def test_few_heads_over_many_rows(H, n):
+    """Few heads: a block of rows for each pair of CTAs, or an equal share.  Each
+    head alone, which is shared out differently, has the same bits."""
+    import mla_decode_attention_05_gb300 as mla
+    w = _cache([n], "fp8", 16)
+    rng = np.random.default_rng(17)
+    w_uk, w_uv = bf16(rng, (H, 128, 512), 0.05).cuda(), bf16(rng, (H, 128, 512), 0.05).cuda()
+    cache, bt, sc = _dev(w, "fp8")
+    mla.device_status()
+    kv, pe = mla.kv_expand(cache, bt, cu([n]), w_uk, w_uv, total=n, kv_scales=sc)
+    for h in range(H):
+        k, e = mla.kv_expand(cache, bt, cu([n]), w_uk[h:h + 1], w_uv[h:h + 1], total=n, kv_scales=sc)
+        assert torch.equal(kv[:, h], k[:, 0]) and torch.equal(pe, e)
+    lat, _, _ = _rows(w, "fp8")
+    some = rng.integers(0, n, 100)
+    want, mag = O.expand(lat[some], f64(w_uk), f64(w_uv))
+    check_sum(kv[torch.from_numpy(some).cuda()], want, mag, 513)
+    assert mla.device_status() == 0
+
+
 def test_a_row_that_is_not_finite_stays_alone():
     import mla_decode_attention_05_gb300 as mla
     lens, H = [140], 3
