@@ -186,9 +186,12 @@ __device__ Work find_work(const PrefillParams &p, int t, int h, int lane, Place 
     w.k0 = min(max(ck, 0), p.Nk);
     w.nk = min(max(cke, w.k0), p.Nk) - w.k0;
     if (lane == 0 && (w.k0 != ck || w.k0 + w.nk != cke)) atomicOr(p.status, MLA_STATUS_BAD_SEQLEN);
-    w.q0 = s + part * kCtaRows;
-    w.nq = min(kCtaRows, e - w.q0);
-    w.diff = p.causal ? w.nk - (e - s) + part * kCtaRows : p.Nk;
+    // Of an odd number of tiles of 128 rows the first one is alone, not the last,
+    // which sees the most keys: a step of one tile takes as long as one of two.
+    const int odd = ceil_div(e - s, kRows) & 1, from = max(0, 2 * part - odd) * kRows;
+    w.q0 = s + from;
+    w.nq = min(part == 0 && odd ? kRows : kCtaRows, e - w.q0);
+    w.diff = p.causal ? w.nk - (e - s) + from : p.Nk;
     return w;
   }
 }
@@ -321,19 +324,6 @@ __device__ __forceinline__ void load_rows(const CUtensorMap *q_map, const CUtens
     __syncwarp();
     if (w.nq == 0) return;
     if (lane == 0) mbar_arrive(smem_u32(&br->work_empty[slot]));
-#pragma unroll 1
-    for (int t = 0; t < 2; t++) {
-      if ((t == 0 ? st.n[0] : st.n[1]) == 0) continue;
-      const uint32_t full = smem_u32(&br->q_full[t]);
-      if (!warp_wait_ok(br, &br->q_empty[t], ((t == 0 ? tiles0++ : tiles1++) & 1) ^ 1)) return;
-      if (elect_one()) {
-        mbar_arrive_expect_tx(full, 3 * kUnit);
-#pragma unroll 1
-        for (int c = 0; c < 3; c++)
-          tma_load_3d(smem + (3 * t + c) * kUnit, q_map, full, 64 * c, w.q0 + t * kRows, w.h, once);
-      }
-      __syncwarp();
-    }
     if (st.most == 0 && lane == 0) mbar_arrive(smem_u32(&br->taken));
 #pragma unroll 1
     for (int j = 0; j < st.most; j++) {
@@ -342,6 +332,21 @@ __device__ __forceinline__ void load_rows(const CUtensorMap *q_map, const CUtens
       const uint32_t g = steps + j, k_full = smem_u32(&br->k_full[g & 1]), v_full = smem_u32(&br->v_full[g & 1]);
 #pragma unroll
       for (int c = 0; c < kUnitsPerStep; c++, u++) {
+        if (c == 3 && j == 0) {  // Q, behind the first keys, whose places are free earlier
+#pragma unroll 1
+          for (int t = 0; t < 2; t++) {
+            if ((t == 0 ? st.n[0] : st.n[1]) == 0) continue;
+            const uint32_t full = smem_u32(&br->q_full[t]);
+            if (!warp_wait_ok(br, &br->q_empty[t], ((t == 0 ? tiles0++ : tiles1++) & 1) ^ 1)) return;
+            if (elect_one()) {
+              mbar_arrive_expect_tx(full, 3 * kUnit);
+#pragma unroll 1
+              for (int c = 0; c < 3; c++)
+                tma_load_3d(smem + (3 * t + c) * kUnit, q_map, full, 64 * c, w.q0 + t * kRows, w.h, once);
+            }
+            __syncwarp();
+          }
+        }
         const uint32_t s = u % kUnits, dst = smem + OFF_RING + s * kUnit;
         if (!warp_wait_ok(br, &br->empty[s], ((u / kUnits) & 1) ^ 1)) return;
         if (elect_one()) {
