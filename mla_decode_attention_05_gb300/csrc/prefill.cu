@@ -293,8 +293,8 @@ __device__ __forceinline__ int next_block(Bars *br) {
 }
 
 // Block -> work.  Heads go in groups of eight, so that several CTAs come by the
-// same keys and values together (groups of 4, 8, 16, 32: 443, 431, 439 and
-// 438 us for 8192 tokens and 32 heads); within a group the last tiles, which see
+// same keys and values together (groups of 4, 8, 16, 32: 425, 409, 412 and
+// 419 us for 8192 tokens and 32 heads); within a group the last tiles, which see
 // the most keys, go first, so that the small ones fill the end.
 constexpr int kHeadGroup = 8;
 __device__ __forceinline__ Work block_work(const PrefillParams &p, int block, int lane, Place &at) {
