@@ -42,7 +42,8 @@ def test_prefill(nq, nk, H, causal):
 
 @pytest.mark.parametrize("causal", [True, False])
 @pytest.mark.parametrize("nq,nk,H", [([200], [2200], 2), ([1], [5000], 1), ([3, 130], [40, 4100], 2), ([260], [4099], 1),
-                                     ([300, 5], [100, 6000], 3), ([9, 0, 2], [1, 2, 9000], 1)])
+                                     ([300, 5], [100, 6000], 3), ([9, 0, 2], [1, 2, 9000], 1),
+                                     ([2] * 8, [3000] * 8, 20)])
 def test_few_queries_over_long_keys(nq, nk, H, causal):
     """These are split over the keys; parts without keys of a row among them."""
     import mla_decode_attention_05_gb300 as mla

@@ -87,10 +87,12 @@ def test_prefill_arguments(L, args, code):
 def test_prefill_workspace(L):
     """Few query tiles over long keys are split over the keys, others not."""
     import mla_decode_attention_05_gb300 as m
-    assert m.prefill_workspace_bytes(1, 128, 256, 100000) == 0      # 128 tiles
+    assert m.prefill_workspace_bytes(1, 128, 256, 9000) == 0        # 128 tiles on 152 SMs
+    assert m.prefill_workspace_bytes(1, 128, 2000, 100000) == 0     # 1024
+    assert m.prefill_workspace_bytes(8, 20, 16, 24000) > 0          # 160: two rounds, the second one almost empty
     assert m.prefill_workspace_bytes(1, 8, 200, 500) == 0           # short keys
     n = m.prefill_workspace_bytes(1, 8, 200, 12200)
-    assert n == 19 * 200 * 8 * 129 * 4 + (-(19 * 200 * 8 * 4) % 256)
+    assert n == 16 * 200 * 8 * 129 * 4 + (-(16 * 200 * 8 * 4) % 256)
     assert m.prefill_workspace_bytes(1, 1, 1, 1 << 26) == 32 * 128 * 4 + 256
     assert m.prefill_workspace_bytes(0, 8, 0, 0) == 0 and m.prefill_workspace_bytes(1, 0, 5, 5) == 0
 
