@@ -432,6 +432,7 @@ __device__ __forceinline__ void mma_sequence(Bars *br, uint32_t smem, uint32_t t
     const Steps st = br->steps[slot];
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_u32(&br->work_empty[slot]));
+    __syncwarp();  // (the barrier below is the whole warp's)
     const int n0 = st.n[0], n1 = st.n[1];
     // While a tile's softmax runs, the tensor cores work on the other tile:
     // its P V, then its next scores (j = -1: the first ones).  One loop for both
@@ -654,6 +655,7 @@ __device__ __forceinline__ bool softmax_work(const PrefillParams &p, Bars *br, u
       const float alpha = move ? ex2((m - top) * p.scale_log2) : 1.f;
       if (move) m = top;
       if (j > 0) {  // (the P V before has been added: its MMAs came before this step's scores)
+        __syncwarp();  // (as below)
         const uint64_t a2 = pack2(alpha, alpha);
         asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(l0) : "l"(a2));
         asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(l1) : "l"(a2));
@@ -701,6 +703,7 @@ __device__ __forceinline__ bool softmax_work(const PrefillParams &p, Bars *br, u
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&br->p_full[t][half]));
+      __syncwarp();  // (as below)
     }
   }
 
@@ -731,6 +734,9 @@ __device__ __forceinline__ bool softmax_work(const PrefillParams &p, Bars *br, u
   float *part = p.part_o + ((w.split * (size_t)p.Nq + row) * p.H + w.h) * kDv;
 #pragma unroll 1
   for (int c = 0; c < 4; c++) {
+    // Loads from and stores to tensor memory are the whole warp's: its lanes
+    // have to meet again behind every branch that only some of them take.
+    __syncwarp();
     uint32_t o[32];
     if (n > 0) {
       tmem_ld32(to + 32 * c, o);

@@ -265,3 +265,19 @@ def test_empty_calls():
     assert not bool(o.any()) and bool(l.isneginf().all())
     o, l = mla.prefill(q[:0], kn[:0], kp[:0], v[:0], cu([]), cu([]), softmax_scale=SCALE)
     assert o.shape == (0, 2, 128)
+
+
+@pytest.mark.parametrize("causal", [True, False])
+def test_rows_that_end_inside_a_warp(causal):
+    """Tiles whose last row is at every place of a warp, one after the other in
+    the same CTAs: lanes without a row take no part in the output, but in every
+    load from tensor memory."""
+    import mla_decode_attention_05_gb300 as mla
+    nq = list(range(1, 34)) + [95, 97, 127, 129, 161, 191, 193, 225, 255, 257, 289]
+    nk = [n + 7 * (i % 3) for i, n in enumerate(nq)]
+    H = 6
+    ins = _inputs(nq, nk, H, 51)
+    mla.device_status()
+    out, lse = mla.prefill(*ins, cu(nq), cu(nk), softmax_scale=SCALE, causal=causal)
+    _check(out, lse, ins, nq, nk, causal)
+    assert mla.device_status() == 0
