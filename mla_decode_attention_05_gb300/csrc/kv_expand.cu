@@ -330,6 +330,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll 1
       for (int c = c0; c < c1; c++) {
         uint32_t v[2][32];
+        __syncwarp();  // the loads are the whole warp's, and its lanes may have stored apart from each other
         tmem_ld32(lane_base + buf * 256 + 64 * c, v[0]);
         tmem_ld32(lane_base + buf * 256 + 64 * c + 32, v[1]);
         uint8_t *out = base + OFF_OUT + (few ? warp : 2 * warp + (c & 1)) * kOutBytes;
@@ -337,6 +338,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           if (few) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
           else asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
         }
+        __syncwarp();
         tmem_wait_ld();
         __syncwarp();
 #pragma unroll

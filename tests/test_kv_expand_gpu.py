@@ -205,3 +205,27 @@ def test_empty_calls():
     assert bool((out == 2).all())
     with pytest.raises(ValueError, match="total"):
         mla.kv_expand(cache, bt, cu([5]), z, z)
+
+
+@pytest.mark.parametrize("lens,H", [([33], 2), ([290, 7], 40), ([2000, 61], 64)])
+def test_rows_of_no_sequence_inside_a_warp(lens, H):
+    """Rows of no sequence in front of the first and behind the last one, which
+    share warps with rows that are written, in few and in many units of work:
+    the written rows' bits are those of a call without them, the others stay."""
+    import mla_decode_attention_05_gb300 as mla
+    w = _cache(lens, "bf16", 90 + H)
+    rng = np.random.default_rng(5)
+    w_uk, w_uv = bf16(rng, (H, 128, 512), 0.05).cuda(), bf16(rng, (H, 128, 512), 0.05).cuda()
+    cache, bt, _ = _dev(w, "bf16")
+    n = sum(lens)
+    kv, pe = mla.kv_expand(cache, bt, cu(lens), w_uk, w_uv, total=n)
+    for front, back in ((5, 0), (45, 19), (0, 70)):
+        total = front + n + back
+        mla.device_status()
+        kv2 = torch.full((total, H, 256), 5.0, dtype=torch.bfloat16, device="cuda")
+        pe2 = torch.full((total, 64), 5.0, dtype=torch.bfloat16, device="cuda")
+        mla.kv_expand(cache, bt, cu(lens) + front, w_uk, w_uv, kv=kv2, k_pe=pe2)
+        assert torch.equal(kv2[front:front + n], kv) and torch.equal(pe2[front:front + n], pe)
+        rest = torch.cat([kv2[:front], kv2[front + n:]])
+        assert bool((rest == 5).all()) and bool((pe2[:front] == 5).all()) and bool((pe2[front + n:] == 5).all())
+        assert mla.device_status() == 0
