@@ -163,6 +163,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool ok = __all_sync(0xffffffffu, wait_ok(br, &br->d_full[buf], (j >> 1) & 1, status));
       tc_fence_after();
       if (threadIdx.x == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // the tile before is out
+      __syncwarp();  // (the barriers are the whole warp's)
       named_bar_sync(1, 128);
       if (ok) {
         // D (lane = value row, column = token) -> bf16 [token][128]
@@ -180,6 +181,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&br->d_empty[buf]));
+      __syncwarp();
       fence_proxy_async_smem();
       // all four warps stop together, at the barrier (abort alone may be set
       // by another role between their looks at it); nothing of this tile is stored then

@@ -63,3 +63,18 @@ def test_empty_call():
     import mla_decode_attention_05_gb300 as mla
     z = torch.zeros((2, 128, 512), dtype=torch.bfloat16, device="cuda")
     assert mla.value_project(z[:0, :2].reshape(0, 2, 512), z).shape == (0, 2, 128)
+
+
+@pytest.mark.parametrize("N,H", [(3000, 8), (10000, 1), (33, 128)])
+def test_many_tiles_in_one_block(N, H):
+    """More tiles than SMs, with and without a change of the head in a block's
+    share: a row's bits are those it has in a call of its own tile."""
+    import mla_decode_attention_05_gb300 as mla
+    rng = np.random.default_rng(N)
+    attn, w = bf16(rng, (N, H, 512), 0.5).cuda(), bf16(rng, (H, 128, 512), 0.05).cuda()
+    mla.device_status()
+    out = mla.value_project(attn, w)
+    for a in (0, 64 * (N // 128), 64 * (N // 64) - (64 if N % 64 == 0 else 0)):
+        assert torch.equal(out[a:a + 64], mla.value_project(attn[a:a + 64], w))
+    _check(out[-70:], attn[-70:], w)
+    assert mla.device_status() == 0
