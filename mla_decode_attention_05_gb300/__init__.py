@@ -30,7 +30,6 @@ import torch
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "_lib", "libmla_decode.so")
-FAST_PATH = os.path.join(_HERE, "_lib", "fastcall.so")
 
 KV_BF16 = 0
 KV_FP8_E4M3 = 1
@@ -104,18 +103,24 @@ def lib():
 
 
 def _load_fast(L) -> None:
-    """Loads fastcall.so, if it was built for this interpreter and PyTorch, and
-    gives it the library's functions."""
+    """Loads the short way, if it was built from these sources for this
+    interpreter and PyTorch (its file's name tells), and gives it the library's
+    functions."""
     global _fast
-    if _fast is not None or not os.path.exists(FAST_PATH):
+    if _fast is not None:
         return
     import importlib.machinery
     import importlib.util
+
+    from .build import fast_path
     try:
-        loader = importlib.machinery.ExtensionFileLoader("fastcall", FAST_PATH)
+        path = fast_path()
+        if not os.path.exists(path):
+            return
+        loader = importlib.machinery.ExtensionFileLoader("fastcall", path)
         m = importlib.util.module_from_spec(importlib.util.spec_from_loader("fastcall", loader))
         loader.exec_module(m)
-    except ImportError:
+    except (ImportError, OSError):  # (no sources to compare with, or a file that does not load)
         return
     m.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
         L.mla_kv_insert_rope, L.mla_kv_expand, L.mla_prefill, L.mla_prefill_workspace_bytes, L.mla_value_project)))

@@ -5,14 +5,16 @@
 Each translation unit of csrc/ is compiled by its own nvcc process (in
 parallel), then linked into _lib/libmla_decode.so with the CUDA runtime
 linked statically, so the library loads on a machine without a GPU driver.
-Beside it the host compiler makes _lib/fastcall.so, the binding's short way past
-the interpreter (csrc_host/), against the installed PyTorch.  The binding does
-without it where it cannot be built: it only saves a call's time on the host.
+Beside it the host compiler makes _lib/fastcall-<hash>.so, the binding's short
+way past the interpreter (csrc_host/), against the installed PyTorch.  The
+binding does without it where it cannot be built: it only saves a call's time
+on the host.
 """
 from __future__ import annotations
 
 import argparse
 import glob
+import hashlib
 import os
 import shutil
 import subprocess
@@ -26,7 +28,6 @@ LIB_DIR = os.path.join(HERE, "_lib")
 OBJ_DIR = os.path.join(LIB_DIR, "obj")
 SO = os.path.join(LIB_DIR, "libmla_decode.so")
 FAST_SRC = os.path.join(HERE, "csrc_host", "fastcall.cpp")
-FAST = os.path.join(LIB_DIR, "fastcall.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -51,25 +52,46 @@ def up_to_date() -> bool:
     return all(os.path.getmtime(d) <= t for d in deps) and os.path.getmtime(__file__) <= t
 
 
+def fast_path() -> str:
+    """Where the short way is that was built from these sources for this
+    interpreter and PyTorch.  The name holds what it depends on (it has
+    accessors of PyTorch's tensors inlined, and calls the library through bare
+    addresses), so one built for others is never found."""
+    import sysconfig
+
+    import torch
+    h = hashlib.sha256()
+    for part in (sysconfig.get_config_var("EXT_SUFFIX"), torch.__version__, torch.version.git_version):
+        h.update(f"{part}\n".encode())
+    for path in (FAST_SRC, os.path.join(INCLUDE, "mla_decode.h")):
+        with open(path, "rb") as f:
+            h.update(f.read())
+    return os.path.join(LIB_DIR, f"fastcall-{h.hexdigest()[:16]}.so")
+
+
 def _start_fast(force: bool):
     """Starts the host compiler on fastcall.cpp if it has to run -> (process,
-    its output file) or None."""
-    deps = [FAST_SRC, os.path.join(INCLUDE, "mla_decode.h"), __file__]
-    if not force and os.path.exists(FAST) and all(os.path.getmtime(d) <= os.path.getmtime(FAST) for d in deps):
+    its output file, the file's name to be) or None.  Files of other sources,
+    interpreters and PyTorches are removed first."""
+    path = fast_path()
+    for old in glob.glob(os.path.join(LIB_DIR, "fastcall*.so")):
+        if force or old != path:
+            os.remove(old)
+    if os.path.exists(path):
         return None
     import sysconfig
 
     import torch
     root = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(_nvcc()))
-    tmp = FAST + f".tmp{os.getpid()}"
+    tmp = path + f".tmp{os.getpid()}"
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE,
            "-I", os.path.join(root, "include"), "-I", os.path.join(root, "include", "torch", "csrc", "api", "include"),
            "-I", sysconfig.get_paths()["include"], "-I", os.path.join(cuda, "include"), FAST_SRC, "-o", tmp,
            "-L", os.path.join(root, "lib"), "-ltorch_python", "-ltorch_cpu", "-ltorch", "-lc10", "-lc10_cuda"]
     try:
-        return subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT), tmp
+        return subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT), tmp, path
     except OSError as e:
         sys.stderr.write(f"fastcall.so not built: {e}\n")
         return None
@@ -78,10 +100,10 @@ def _start_fast(force: bool):
 def _finish_fast(started) -> None:
     if started is None:
         return
-    pr, tmp = started
+    pr, tmp, path = started
     text = pr.communicate()[0].decode(errors="replace")
     if pr.returncode == 0:
-        os.replace(tmp, FAST)
+        os.replace(tmp, path)
     else:
         sys.stderr.write("fastcall.so not built (calls take longer on the host):\n" + text[-4000:])
 
