@@ -68,6 +68,15 @@ mla_stream_t stream_of(int dev) {
   return reinterpret_cast<mla_stream_t>(c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)dev).stream());
 }
 
+// Lets the interpreter's other threads run while this one allocates and
+// launches, as the Python way does: both can block (an allocation waits for
+// PyTorch's allocator, a launch for room in the stream's queue), and what they
+// wait for may need the interpreter.
+struct Unlocked {
+  PyThreadState *state = PyEval_SaveThread();
+  ~Unlocked() { PyEval_RestoreThread(state); }
+};
+
 PyObject *none() { Py_RETURN_NONE; }
 PyObject *code(int rc) { return PyLong_FromLong(rc); }
 
@@ -84,9 +93,14 @@ PyObject *value_project(PyObject *, PyObject *const *args, Py_ssize_t n) {
   const int64_t N = attn->size(0), H = attn->size(1);
   if (w->size(0) != H || w->size(1) != 128 || N > kMostInt) return none();
   if (given && (!whole(given, dev, at::kBFloat16, 3) || !sized(*given, {N, H, 128}))) return none();
-  at::Tensor out = given ? *given : at::empty({N, H, 128}, attn->options());
-  const int rc = value_fn(attn->data_ptr(), at_tok, at_head, w->data_ptr(), w_row, w_head, (int)N, (int)H,
-                          out.data_ptr(), stream_of(dev));
+  at::Tensor out;
+  int rc;
+  {
+    Unlocked others;
+    out = given ? *given : at::empty({N, H, 128}, attn->options());
+    rc = value_fn(attn->data_ptr(), at_tok, at_head, w->data_ptr(), w_row, w_head, (int)N, (int)H, out.data_ptr(),
+                  stream_of(dev));
+  }
   return rc < 0 ? code(rc) : THPVariable_Wrap(out);
 }
 
@@ -111,21 +125,26 @@ PyObject *prefill(PyObject *, PyObject *const *args, Py_ssize_t n) {
   if (out_given && (!whole(out_given, dev, at::kBFloat16, 3) || !sized(*out_given, {Nq, H, 128}))) return none();
   if (lse_given && (!whole(lse_given, dev, at::kFloat, 2) || !sized(*lse_given, {H, Nq}))) return none();
   if (space && !(on(space, dev) && space->is_contiguous())) return none();
-  at::Tensor out = out_given ? *out_given : at::empty({Nq, H, 128}, q->options());
-  at::Tensor lse = lse_given ? *lse_given : at::empty({H, Nq}, q->options().dtype(at::kFloat));
-  at::Tensor room;
-  size_t bytes = prefill_ws_fn((int)B, (int)H, (int)Nq, (int)Nk);
-  if (space) {
-    room = *space;
-    bytes = space->nbytes();
-  } else if (bytes) {
-    room = at::empty({(int64_t)bytes}, q->options().dtype(at::kByte));
+  const float scale = (float)PyFloat_AS_DOUBLE(args[6]);
+  const int causal = args[7] == Py_True ? 1 : 0;
+  at::Tensor out, lse, room;
+  int rc;
+  {
+    Unlocked others;
+    out = out_given ? *out_given : at::empty({Nq, H, 128}, q->options());
+    lse = lse_given ? *lse_given : at::empty({H, Nq}, q->options().dtype(at::kFloat));
+    size_t bytes = prefill_ws_fn((int)B, (int)H, (int)Nq, (int)Nk);
+    if (space) {
+      room = *space;
+      bytes = space->nbytes();
+    } else if (bytes) {
+      room = at::empty({(int64_t)bytes}, q->options().dtype(at::kByte));
+    }
+    rc = prefill_fn(q->data_ptr(), qt, qh, kn->data_ptr(), kt, kh, kp->data_ptr(), pt, v->data_ptr(), vt, vh,
+                    cq->data_ptr<int32_t>(), ck->data_ptr<int32_t>(), (int)B, (int)H, (int)Nq, (int)Nk, scale, causal,
+                    room.defined() ? room.data_ptr() : nullptr, bytes, out.data_ptr(), lse.data_ptr<float>(),
+                    stream_of(dev));
   }
-  const int rc = prefill_fn(q->data_ptr(), qt, qh, kn->data_ptr(), kt, kh, kp->data_ptr(), pt, v->data_ptr(), vt, vh,
-                            cq->data_ptr<int32_t>(), ck->data_ptr<int32_t>(), (int)B, (int)H, (int)Nq, (int)Nk,
-                            (float)PyFloat_AS_DOUBLE(args[6]), args[7] == Py_True ? 1 : 0,
-                            room.defined() ? room.data_ptr() : nullptr, bytes, out.data_ptr(), lse.data_ptr<float>(),
-                            stream_of(dev));
   if (rc < 0) return code(rc);
   PyObject *a = THPVariable_Wrap(out), *b = THPVariable_Wrap(lse);
   PyObject *r = a && b ? PyTuple_Pack(2, a, b) : nullptr;
@@ -160,12 +179,17 @@ PyObject *kv_expand(PyObject *, PyObject *const *args, Py_ssize_t n) {
     return none();
   if (kv_given && (!whole(kv_given, dev, at::kBFloat16, 3) || !sized(*kv_given, {total, H, 256}))) return none();
   if (pe_given && (!whole(pe_given, dev, at::kBFloat16, 2) || !sized(*pe_given, {total, 64}))) return none();
-  at::Tensor kv = kv_given ? *kv_given : at::empty({total, H, 256}, uk->options());
-  at::Tensor pe = pe_given ? *pe_given : at::empty({total, 64}, uk->options());
-  const int rc = expand_fn(c->data_ptr(), fmt, (int)c->size(0), (int)c->size(1), bt->data_ptr<int32_t>(),
-                           (int)bt->size(1), cu->data_ptr<int32_t>(), (int)B, (int)total,
-                           fmt != MLA_KV_BF16 ? sc->data_ptr<float>() : nullptr, uk->data_ptr(), uk_row, uk_head,
-                           uv->data_ptr(), uv_row, uv_head, (int)H, kv.data_ptr(), pe.data_ptr(), stream_of(dev));
+  at::Tensor kv, pe;
+  int rc;
+  {
+    Unlocked others;
+    kv = kv_given ? *kv_given : at::empty({total, H, 256}, uk->options());
+    pe = pe_given ? *pe_given : at::empty({total, 64}, uk->options());
+    rc = expand_fn(c->data_ptr(), fmt, (int)c->size(0), (int)c->size(1), bt->data_ptr<int32_t>(), (int)bt->size(1),
+                   cu->data_ptr<int32_t>(), (int)B, (int)total, fmt != MLA_KV_BF16 ? sc->data_ptr<float>() : nullptr,
+                   uk->data_ptr(), uk_row, uk_head, uv->data_ptr(), uv_row, uv_head, (int)H, kv.data_ptr(),
+                   pe.data_ptr(), stream_of(dev));
+  }
   if (rc < 0) return code(rc);
   PyObject *a = THPVariable_Wrap(kv), *b = THPVariable_Wrap(pe);
   PyObject *r = a && b ? PyTuple_Pack(2, a, b) : nullptr;
@@ -219,13 +243,19 @@ PyObject *kv_insert_rope(PyObject *, PyObject *const *args, Py_ssize_t n) {
   } else if (qo) {
     return none();
   }
-  const int rc = insert_rope_fn(
-      kc->data_ptr(), (int)ld_kv, kp->data_ptr(), (int)ld_pe, w->data_ptr(), (float)PyFloat_AS_DOUBLE(args[5]),
-      slots->data_ptr<int64_t>(), pos->data_ptr<int64_t>(), cs->data_ptr<float>(), (int)cs->size(0),
-      args[8] == Py_True ? 1 : 0, (int)N, c->data_ptr(), fmt, (int)c->size(0), (int)c->size(1),
-      fmt == MLA_KV_FP8_E4M3 ? sc->data_ptr<float>() : nullptr,
-      fmt == MLA_KV_FP8_E4M3_TENSOR ? ksi->data_ptr<float>() : nullptr, q ? q->data_ptr() : nullptr, qt, qh,
-      q ? qo->data_ptr() : nullptr, ot, oh, (int)H, stream_of(dev));
+  const float eps = (float)PyFloat_AS_DOUBLE(args[5]);
+  const int interleaved = args[8] == Py_True ? 1 : 0;
+  int rc;
+  {
+    Unlocked others;
+    rc = insert_rope_fn(kc->data_ptr(), (int)ld_kv, kp->data_ptr(), (int)ld_pe, w->data_ptr(), eps,
+                        slots->data_ptr<int64_t>(), pos->data_ptr<int64_t>(), cs->data_ptr<float>(), (int)cs->size(0),
+                        interleaved, (int)N, c->data_ptr(), fmt, (int)c->size(0), (int)c->size(1),
+                        fmt == MLA_KV_FP8_E4M3 ? sc->data_ptr<float>() : nullptr,
+                        fmt == MLA_KV_FP8_E4M3_TENSOR ? ksi->data_ptr<float>() : nullptr,
+                        q ? q->data_ptr() : nullptr, qt, qh, q ? qo->data_ptr() : nullptr, ot, oh, (int)H,
+                        stream_of(dev));
+  }
   if (rc < 0) return code(rc);
   Py_RETURN_TRUE;
 }

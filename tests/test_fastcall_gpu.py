@@ -200,3 +200,40 @@ def test_calls_that_follow_one_another():
     for _ in range(5):
         got = [one_prompt(*p, False) for p in prompts]
         assert all(torch.equal(a, b) for g, v in zip(got, want) for a, b in zip(g, v))
+
+
+def test_other_threads_run_meanwhile(tmp_path):
+    """The interpreter is free while a call allocates and launches: seen by a
+    function in the library's place."""
+    import ctypes
+    import shutil
+    import subprocess
+    import sysconfig
+
+    import mla_decode_attention_05_gb300 as mla
+    L = mla.lib()
+    cc = shutil.which("cc") or shutil.which("gcc")
+    if cc is None:
+        pytest.skip("no C compiler")
+    src, so = tmp_path / "held.c", tmp_path / "held.so"
+    src.write_text("#include <Python.h>\nint calls, held;\n"
+                   "int call(void) { calls++; held += PyGILState_Check(); return 0; }\n"
+                   "size_t room(void) { call(); return 0; }\n")
+    subprocess.check_call([cc, "-shared", "-fPIC", "-I", sysconfig.get_paths()["include"], str(src), "-o", str(so)])
+    stub = ctypes.CDLL(str(so))
+    at = lambda f: ctypes.cast(f, ctypes.c_void_p).value
+    s = _inputs(3)
+    cache = torch.zeros((3, 64, 576), dtype=torch.bfloat16, device="cuda")
+    kv = torch.zeros((70, 3, 256), dtype=torch.bfloat16, device="cuda")
+    pe = torch.zeros((70, 64), dtype=torch.bfloat16, device="cuda")
+    mla._fast.bind(at(stub.call), at(stub.call), at(stub.call), at(stub.room), at(stub.call))
+    try:
+        assert _taken(lambda: mla.kv_insert_rope(s["qkv"][:, 1536:2048], s["qkv"][:, 2048:], s["w"], s["slots"], cache,
+                                                 eps=1e-6, positions=s["pos"], cos_sin=s["cs"]))
+        assert _taken(lambda: mla.kv_expand(cache, s["bt"], s["cu"], s["w_kv"][:, :128], s["w_kv"][:, 128:], total=70))
+        assert _taken(lambda: mla.prefill(s["q"], kv[..., :128], pe, kv[..., 128:], s["cu"], s["cu"], softmax_scale=SCALE))
+        assert _taken(lambda: mla.value_project(s["qkv"][:, :1536].unflatten(1, (3, 512)), s["w_kv"][:, 128:]))
+    finally:
+        mla._fast.bind(*(at(f) for f in (L.mla_kv_insert_rope, L.mla_kv_expand, L.mla_prefill,
+                                         L.mla_prefill_workspace_bytes, L.mla_value_project)))
+    assert ctypes.c_int.in_dll(stub, "calls").value == 5 and ctypes.c_int.in_dll(stub, "held").value == 0
