@@ -237,8 +237,10 @@ PyObject *kv_insert_rope(PyObject *, PyObject *const *args, Py_ssize_t n) {
     if (!rows(q, dev, 3, 64, qt, qh) || !rows(qo, dev, 3, 64, ot, oh)) return none();
     H = q->size(1);
     if (q->size(0) != N || qo->size(0) != N || qo->size(1) != H || H > kMostInt) return none();
-    // tokens before heads or whole, without overlap; the same place only with the same strides
-    if (!(qo->is_contiguous() || (oh >= 64 && ot >= oh * (H - 1) + 64))) return none();
+    // tokens before heads or whole, without overlap (the stride of an axis of
+    // one entry does not matter); the same place only with the same strides
+    const bool apart = (H < 2 || oh >= 64) && (N < 2 || ot >= (H < 2 ? 0 : oh * (H - 1)) + 64);
+    if (!qo->is_contiguous() && !apart) return none();
     if (q->data_ptr() == qo->data_ptr() && (qt != ot || qh != oh)) return none();
   } else if (qo) {
     return none();

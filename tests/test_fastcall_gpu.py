@@ -237,3 +237,45 @@ def test_other_threads_run_meanwhile(tmp_path):
         mla._fast.bind(*(at(f) for f in (L.mla_kv_insert_rope, L.mla_kv_expand, L.mla_prefill,
                                          L.mla_prefill_workspace_bytes, L.mla_value_project)))
     assert ctypes.c_int.in_dll(stub, "calls").value == 5 and ctypes.c_int.in_dll(stub, "held").value == 0
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8", "fp8_tensor"])
+@pytest.mark.parametrize("n,H", [(1, 5), (1, 1), (2, 1), (2, 5)])
+def test_few_tokens_in_place(both, n, H, fmt):
+    """A decode step's queries, rotated in place as views of their absorbed rows:
+    taken for a single token and a single head too, with the Python way's bits."""
+    import mla_decode_attention_05_gb300 as mla
+    rng = np.random.default_rng(7)
+    qkv, q0, w = bf16(rng, (n, 2112)).cuda(), bf16(rng, (n, H, 576)).cuda(), bf16(rng, (512,)).cuda()
+    slots, pos = torch.arange(n, device="cuda") + 70, torch.arange(n, device="cuda") + 3
+    cs = torch.from_numpy(O.angle_table(8)).cuda()
+
+    def insert():
+        width = 640 if fmt == "fp8" else 576
+        cache = torch.zeros((2, 64, width), dtype=torch.bfloat16 if fmt == "bf16" else torch.uint8, device="cuda")
+        sc = torch.zeros((2, 64, 4), device="cuda") if fmt == "fp8" else None
+        q = q0.clone()
+        r = mla.kv_insert_rope(qkv[:, 1536:2048], qkv[:, 2048:], w, slots, cache, eps=1e-6, positions=pos, cos_sin=cs,
+                               q_pe=q[..., 512:], kv_scales=sc, fp8_per_tensor=fmt == "fp8_tensor",
+                               k_scale_inv=torch.full((1,), 0.5, device="cuda") if fmt == "fp8_tensor" else None)
+        assert r[1].data_ptr() == q[..., 512:].data_ptr()
+        return (cache, q) if sc is None else (cache, q, sc)
+    a, b = both(insert)
+    assert all(torch.equal(x, y) for x, y in zip(a, b)) and not torch.equal(a[1], q0)
+    assert torch.equal(a[1][..., :512], q0[..., :512])
+    assert _taken(insert)
+
+
+def test_rows_that_overlap_are_left_to_the_python_way():
+    import mla_decode_attention_05_gb300 as mla
+    rng = np.random.default_rng(8)
+    qkv, w = bf16(rng, (2, 2112)).cuda(), bf16(rng, (512,)).cuda()
+    cache = torch.zeros((2, 64, 576), dtype=torch.bfloat16, device="cuda")
+    z = torch.arange(2, device="cuda")
+    cs = torch.from_numpy(O.angle_table(8)).cuda()
+    flat = torch.zeros(4096, dtype=torch.bfloat16, device="cuda")
+    for n, H, strides in ((2, 3, (64, 64)), (2, 3, (128, 64)), (2, 3, (512, 32)), (1, 3, (0, 32)), (2, 1, (32, 0)), (2, 3, (64, 0))):
+        out = flat.as_strided((n, H, 64), strides + (1,))
+        with pytest.raises(ValueError, match="overlap"):
+            mla.kv_insert_rope(qkv[:n, 1536:2048], qkv[:n, 2048:], w, z[:n], cache, eps=1e-6, positions=z[:n], cos_sin=cs,
+                               q_pe=bf16(rng, (n, H, 64)).cuda(), q_out=out)
