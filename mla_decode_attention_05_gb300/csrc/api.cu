@@ -8,6 +8,7 @@
 #include <mutex>
 
 #include "common.cuh"
+#include "dependent.cuh"
 
 // Device status word (MLA_STATUS_* bits), one per device that loads the
 // library.  Kernels receive its address as a parameter.

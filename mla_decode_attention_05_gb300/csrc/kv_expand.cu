@@ -22,7 +22,9 @@
 #include <cuda_fp8.h>
 
 #include "common.cuh"
+#include "dependent.cuh"
 #include "ptx.cuh"
+#include "ptx_pair.cuh"
 #include "tma_map.cuh"
 
 namespace mla {

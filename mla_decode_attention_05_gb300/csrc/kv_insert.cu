@@ -37,6 +37,7 @@
 #include <cuda_fp8.h>
 
 #include "common.cuh"
+#include "dependent.cuh"
 #include "exact_sum.cuh"
 
 namespace mla {

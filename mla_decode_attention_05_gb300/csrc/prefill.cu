@@ -30,7 +30,9 @@
 #include <cstddef>
 
 #include "common.cuh"
+#include "dependent.cuh"
 #include "ptx.cuh"
+#include "ptx_pair.cuh"
 #include "tma_map.cuh"
 
 namespace mla {

@@ -8,6 +8,7 @@
 // flops a byte, a third of what the tensor cores can take (4095 tokens, 64 heads:
 // 57 us, 6.0 TB/s; 64 tokens, 128 heads: 4.6 us).
 #include "common.cuh"
+#include "dependent.cuh"
 #include "ptx.cuh"
 #include "tma_map.cuh"
 

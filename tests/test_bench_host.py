@@ -82,3 +82,22 @@ def test_reference_arm_reports_the_same_config(capsys, monkeypatch):
     want, flush = bench.decode_config(w, 1, 1, bench.device_parts(0), bench.device_l2_bytes(0))
     assert line["config"] == want and not flush
     assert line["steps"] == 1 and line["warmup"] == 3 and line["dtype"] == "f64"
+
+
+def test_the_traffic_record_is_of_the_decode_kernel_that_is_built():
+    """The committed DRAM traffic of the decode was taken on the sources that
+    its kernel is compiled from: that file and all headers it includes."""
+    import os
+    import re
+    csrc = os.path.join(bench.ROOT, "mla_decode_attention_05_gb300", "csrc")
+    seen, todo = set(), ["decode_tc.cu"]
+    while todo:
+        name = todo.pop()
+        if name in seen or not os.path.exists(os.path.join(csrc, name)):
+            continue
+        seen.add(name)
+        with open(os.path.join(csrc, name)) as f:
+            todo += re.findall(r'^#include "([^"]+)"', f.read(), re.M)
+    assert seen == set(bench.DECODE_KERNEL_SOURCES)
+    record = bench.traffic_record(bench.kernel_source_hash())
+    assert record is not None and record["dram_bytes_per_launch"] > bench.work_of(W.config(3))[0]
