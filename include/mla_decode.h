@@ -498,12 +498,13 @@ int mla_set_dual_gemm(int enable);
 
 /*
  * Test hook for the failure path: the time limit, in nanoseconds, of every
- * bounded wait inside the decode kernel of later mla_decode and
- * mla_decode_noalloc calls made on the calling thread (0 restores the
- * default of 2 s).  A wait that runs out sets MLA_STATUS_WAIT_TIMEOUT; every
+ * bounded wait inside the kernels of later mla_decode, mla_decode_noalloc,
+ * mla_kv_expand, mla_prefill (at most 4 s there) and mla_value_project calls
+ * made on the calling thread (0 restores the default of 2 s; mla_query_absorb's
+ * waits have limits of their own).  A wait that runs out sets MLA_STATUS_WAIT_TIMEOUT; every
  * role of the kernel then gives up at its next wait, the kernel waits for
  * its own copies and MMAs in flight, frees its tensor memory and returns, and
- * the context stays usable.  The out and lse of such a call are undefined.
+ * the context stays usable.  The outputs of such a call are undefined.
  * With a limit of a few microseconds, real waits of an ordinary call run
  * out, so a test can exercise this path without faulting or hanging the GPU.
  * Not meant for production calls.  Returns MLA_OK.

@@ -759,9 +759,9 @@ def set_dual_gemm(enable: bool):
 
 
 def set_wait_limit_ns(ns: int = 0):
-    """Test hook: the limit of the decode kernel's bounded waits for later
-    decode calls on this thread (0 = the default, 2 s); see
-    mla_set_wait_limit_ns in include/mla_decode.h."""
+    """Test hook: the limit of the bounded waits inside the kernels of later
+    decode, kv_expand, prefill and value_project calls on this thread (0 = the
+    default, 2 s); see mla_set_wait_limit_ns in include/mla_decode.h."""
     _check(lib().mla_set_wait_limit_ns(int(ns)))
 
 

@@ -104,6 +104,7 @@ void set_last_error(const char *msg) {
 // Address of the device status word on the current device (for the entry
 // points of other translation units).
 int status_word(unsigned int **out) { return status_ptr(out); }
+unsigned long long wait_limit_ns() { return g_wait_ns; }
 }  // namespace mla
 
 extern "C" {

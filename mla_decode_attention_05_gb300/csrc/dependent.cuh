@@ -1,5 +1,6 @@
 // What the operators around the decode share: their launches as programmatic
-// dependents, and the rotating insert's parameters.  (Apart from common.cuh and
+// dependents, the limit of their waits, and the rotating insert's parameters.
+// (Apart from common.cuh and
 // ptx.cuh, which the decode kernel is compiled from: a measurement of that
 // kernel holds as long as its sources stay as they are.)
 #pragma once
@@ -39,5 +40,8 @@ struct RopeParams {
   int H;
 };
 cudaError_t launch_kv_insert_rope(const KvInsertParams &p, const RopeParams &r, cudaStream_t stream);
+
+// The calling thread's limit of bounded waits (mla_set_wait_limit_ns).
+unsigned long long wait_limit_ns();
 
 }  // namespace mla

@@ -41,6 +41,7 @@ struct ExpandParams {
   __nv_bfloat16 *k_pe;  // [total][64]
   unsigned int *status;
   int format, num_pages, max_pages, B, H, total;
+  unsigned long long wait_ns;  // limit of every wait
 };
 
 // A cluster of two CTAs works as one: M = 256 rows, 128 gathered by each CTA;
@@ -81,9 +82,10 @@ struct Bars {
 constexpr uint32_t kSmem = OFF_BARS + sizeof(Bars) + 1024;
 static_assert(kSmem <= 232448, "shared memory budget");
 
-__device__ __forceinline__ bool wait_ok(Bars *b, uint64_t *bar, uint32_t parity, unsigned int *status) {
-  if (mbar_wait<true>(smem_u32(bar), parity, &b->abort, kDefaultWaitNs)) return true;
-  atomicOr(status, MLA_STATUS_WAIT_TIMEOUT);
+template <bool kPoll>
+__device__ __forceinline__ bool wait_ok(Bars *b, uint64_t *bar, uint32_t parity, const ExpandParams &p) {
+  if (mbar_wait_limited<true, kPoll>(smem_u32(bar), parity, &b->abort, p.wait_ns)) return true;
+  atomicOr(p.status, MLA_STATUS_WAIT_TIMEOUT);
   *(volatile int *)&b->abort = 1;
   return false;
 }
@@ -247,6 +249,7 @@ __device__ void gather_rows(const ExpandParams &p, uint8_t *a, int row0, int war
   }
 }
 
+template <bool kPoll>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     expand_kernel(const __grid_constant__ CUtensorMap uk_map, const __grid_constant__ CUtensorMap uv_map,
                   const __grid_constant__ CUtensorMap o_map, ExpandParams p) {
@@ -316,7 +319,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     int mine = -2;
     for (int i = 0; i < n; i++) {
       const int u = order.unit(i), buf = i & 1;
-      const bool ok = __all_sync(0xffffffffu, wait_ok(br, &br->d_full[buf], (i >> 1) & 1, p.status));
+      const bool ok = __all_sync(0xffffffffu, wait_ok<kPoll>(br, &br->d_full[buf], (i >> 1) & 1, p));
       if (!ok) break;
       tc_fence_after();
       if (order.new_rows(i)) mine = br->source[(blocks - 1) % 3][quarter * 32 + lane];
@@ -390,7 +393,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const int h = order.unit(i) % p.H;
       for (int kb = 0; kb < kKBlocks; kb++, k++) {
         const uint32_t s = k % kWStages, dst = sw + s * kWStage;
-        ok = __all_sync(0xffffffffu, wait_ok(br, &br->w_empty[s], ((k / kWStages) & 1) ^ 1, p.status));
+        ok = __all_sync(0xffffffffu, wait_ok<kPoll>(br, &br->w_empty[s], ((k / kWStages) & 1) ^ 1, p));
         if (!ok) break;
         if (elect_one()) {
           if (rank == 0) mbar_arrive_expect_tx(smem_u32(&br->w_full[s]), 2 * kWStage);
@@ -406,7 +409,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     uint32_t k = 0, na = 0;
     bool ok = true;
     auto wait = [&](uint64_t *bar, uint32_t parity) {
-      ok = ok && __all_sync(0xffffffffu, wait_ok(br, bar, parity, p.status));
+      ok = ok && __all_sync(0xffffffffu, wait_ok<kPoll>(br, bar, parity, p));
     };
     for (int i = 0; i < n && ok; i++) {
       const int buf = i & 1;
@@ -501,10 +504,12 @@ int mla_kv_expand(const void *kv_cache, int kv_format, int num_pages, int page_s
   p.B = B;
   p.H = H;
   p.total = total;
+  p.wait_ns = wait_limit_ns();
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  if (e == cudaSuccess) e = cudaFuncSetAttribute(expand_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+  auto *kernel = p.wait_ns < ptx::kShortWaitNs ? &expand_kernel<true> : &expand_kernel<false>;
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
   if (e != cudaSuccess) return fail(MLA_ERR_CUDA, cudaGetErrorString(e));
   const long long units = (long long)ceil_div(total, kPairRows) * H;
   // An equal share of the units for each pair; with few heads a block of rows for
@@ -515,7 +520,7 @@ int mla_kv_expand(const void *kv_cache, int kv_format, int num_pages, int page_s
   const int blocks = ceil_div(total, kPairRows);
   int pairs = (int)(units < sms / 2 ? units : sms / 2);
   if (blocks < pairs && H <= 8 && H - (int)((units + pairs - 1) / pairs) <= 1) pairs = blocks;
-  e = launch_dependent(expand_kernel, 2 * pairs, kThreads, kSmem, (cudaStream_t)stream, uk_map, uv_map, o_map, p);
+  e = launch_dependent(kernel, 2 * pairs, kThreads, kSmem, (cudaStream_t)stream, uk_map, uv_map, o_map, p);
   if (e != cudaSuccess) return fail(MLA_ERR_CUDA, cudaGetErrorString(e));
   set_last_error("");
   return MLA_OK;

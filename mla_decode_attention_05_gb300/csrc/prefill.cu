@@ -84,6 +84,12 @@ struct PrefillParams {
   int causal;
   int out_v8;
   float scale, scale_log2;
+  uint32_t wait_ns;  // limit of every wait
+};
+// The same for the kernel that is compiled for short limits (kPoll) or for others.
+template <bool kPoll>
+struct Limited : PrefillParams {
+  static constexpr bool poll = kPoll;
 };
 
 // A CTA's unit of work: up to 256 query rows of one sequence, one head, a
@@ -226,12 +232,9 @@ __device__ __forceinline__ void take_split(Work &w, int i, int splits) {
 
 // A bounded wait; the kernel tells of one that gave up at its end.  (With the
 // longer form of a wait in its twenty places: ragged prompts 304 us, not 296.)
-__device__ __forceinline__ bool wait_ok(Bars *b, uint64_t *bar, uint32_t parity) {
-  return mbar_wait_small<false>(smem_u32(bar), parity, &b->abort, (uint32_t)kDefaultWaitNs);
-}
-
-__device__ __forceinline__ bool warp_wait_ok(Bars *b, uint64_t *bar, uint32_t parity) {
-  return __all_sync(0xffffffffu, wait_ok(b, bar, parity));
+template <class P>
+__device__ __forceinline__ bool warp_wait_ok(const P &p, Bars *b, uint64_t *bar, uint32_t parity) {
+  return __all_sync(0xffffffffu, mbar_wait_small<false, P::poll>(smem_u32(bar), parity, &b->abort, p.wait_ns));
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -314,14 +317,15 @@ __device__ __forceinline__ Work block_work(const PrefillParams &p, int block, in
 // are freed one by one (all keys, all values of a step at a time: 440 instead of
 // 421 us for 8192 tokens), and the whole warp waits while one elected lane asks (a
 // loop of one lane takes 500 cycles a unit: 421 instead of 409 us).
-__device__ __forceinline__ void load_rows(const CUtensorMap *q_map, const CUtensorMap *kn_map,
+template <class P>
+__device__ __forceinline__ void load_rows(const P &p, const CUtensorMap *q_map, const CUtensorMap *kn_map,
                                           const CUtensorMap *kp_map, const CUtensorMap *v_map, Bars *br,
                                           uint32_t smem, int lane) {
   const uint64_t pol = policy_evict_normal(), once = policy_evict_first();
   uint32_t u = 0, steps = 0, tiles0 = 0, tiles1 = 0;  // units, steps, tiles so far
   for (uint32_t count = 0;; count++) {
     const uint32_t slot = count & 1;
-    if (!warp_wait_ok(br, &br->work_full[slot], (count >> 1) & 1)) return;
+    if (!warp_wait_ok(p, br, &br->work_full[slot], (count >> 1) & 1)) return;
     const Work w = br->work[slot];
     const Steps st = br->steps[slot];
     __syncwarp();
@@ -340,7 +344,7 @@ __device__ __forceinline__ void load_rows(const CUtensorMap *q_map, const CUtens
           for (int t = 0; t < 2; t++) {
             if ((t == 0 ? st.n[0] : st.n[1]) == 0) continue;
             const uint32_t full = smem_u32(&br->q_full[t]);
-            if (!warp_wait_ok(br, &br->q_empty[t], ((t == 0 ? tiles0++ : tiles1++) & 1) ^ 1)) return;
+            if (!warp_wait_ok(p, br, &br->q_empty[t], ((t == 0 ? tiles0++ : tiles1++) & 1) ^ 1)) return;
             if (elect_one()) {
               mbar_arrive_expect_tx(full, 3 * kUnit);
 #pragma unroll 1
@@ -351,7 +355,7 @@ __device__ __forceinline__ void load_rows(const CUtensorMap *q_map, const CUtens
           }
         }
         const uint32_t s = u % kUnits, dst = smem + OFF_RING + s * kUnit;
-        if (!warp_wait_ok(br, &br->empty[s], ((u / kUnits) & 1) ^ 1)) return;
+        if (!warp_wait_ok(p, br, &br->empty[s], ((u / kUnits) & 1) ^ 1)) return;
         if (elect_one()) {
           if (c == 0) mbar_arrive_expect_tx(k_full, 3 * kUnit);
           if (c == 3) mbar_arrive_expect_tx(v_full, 2 * kUnit);
@@ -377,8 +381,8 @@ __device__ __forceinline__ void load_rows(const CUtensorMap *q_map, const CUtens
 // before each group of MMAs; the barrier also tells of a wait that gave up.
 constexpr uint32_t kMmaBar = 1;
 
-template <bool kWaiter>
-__device__ __forceinline__ void mma_sequence(Bars *br, uint32_t smem, uint32_t tmem) {
+template <bool kWaiter, class P>
+__device__ __forceinline__ void mma_sequence(const P &p, Bars *br, uint32_t smem, uint32_t tmem) {
   const int lane = threadIdx.x & 31;
   const uint64_t q_desc = smem_desc_sw128(smem, 16, 1024), k_desc = smem_desc_sw128(smem + OFF_RING, 16, 1024);
   const uint64_t v_desc = smem_desc_sw128(smem + OFF_RING, kUnit / 2, 1024);
@@ -388,7 +392,7 @@ __device__ __forceinline__ void mma_sequence(Bars *br, uint32_t smem, uint32_t t
   // (one wait after the other, each by the whole warp: side by side, a lane for
   // each, five waits took 400 cycles even where all were over)
   auto wait = [&](uint64_t *bar, uint32_t parity) {
-    if (kWaiter) ok = ok && warp_wait_ok(br, bar, parity);
+    if (kWaiter) ok = ok && warp_wait_ok(p, br, bar, parity);
   };
   auto meet = [&](bool stop = false) { return !bar_red_or(kMmaBar, 64, !ok || stop); };
   // Scores of tile t for step j (units 5j .. 5j + 2).
@@ -486,14 +490,15 @@ __device__ __forceinline__ void mma_sequence(Bars *br, uint32_t smem, uint32_t t
 
 // The whole warp looks through the values of one unit of work, from step `look`
 // on; base: the unit of the ring that its first step begins with.
-__device__ __forceinline__ bool check_values(Bars *br, uint8_t *ring, const Steps &st, uint32_t slot, uint32_t base,
-                                             uint32_t &looks, int lane) {
+template <class P>
+__device__ __forceinline__ bool check_values(const P &p, Bars *br, uint8_t *ring, const Steps &st,
+                                             uint32_t slot, uint32_t base, uint32_t &looks, int lane) {
   for (int j = st.look; j < st.most; j++) {
-    if (!warp_wait_ok(br, &br->v_look, looks++ & 1)) return false;
+    if (!warp_wait_ok(p, br, &br->v_look, looks++ & 1)) return false;
     bool patched = false;
     for (int c = 0; c < 2; c++) {
       const uint32_t u = base + (uint32_t)j * kUnitsPerStep + 3 + c, s = u % kUnits, g = u / kUnitsPerStep;
-      if (!warp_wait_ok(br, &br->v_full[g & 1], (g >> 1) & 1)) return false;
+      if (!warp_wait_ok(p, br, &br->v_full[g & 1], (g >> 1) & 1)) return false;
       uint8_t *unit = ring + s * kUnit;
       // x * 0 summed up stays 0, unless some x is not finite: then it is nan
       uint32_t sum[4] = {0u, 0u, 0u, 0u};
@@ -549,12 +554,13 @@ __device__ __forceinline__ bool check_values(Bars *br, uint8_t *ring, const Step
 // (never more than their ring holds: two are under way beside this), all that
 // is under way is let finish, and they are, with this warp looking through their
 // values.
-__device__ __forceinline__ void schedule(const PrefillParams &p, Bars *br, uint8_t *ring, int lane) {
+template <class P>
+__device__ __forceinline__ void schedule(const P &p, Bars *br, uint8_t *ring, int lane) {
   uint32_t asked = 0, count = 0, redone = 0, base = 0, looks = 0;
   Place place = {0, 0};
   // the slot that unit of work number n gets is free
   auto slot_free = [&](uint32_t n) {
-    return warp_wait_ok(br, &br->work_empty[n & 1], ((n >> 1) & 1) ^ 1);
+    return warp_wait_ok(p, br, &br->work_empty[n & 1], ((n >> 1) & 1) ^ 1);
   };
   auto tell = [&](const Work &w, const Steps &st) {
     const uint32_t slot = count & 1;
@@ -589,17 +595,17 @@ __device__ __forceinline__ void schedule(const PrefillParams &p, Bars *br, uint8
       if (redo) st.look = st.masked;
       const uint32_t slot = count & 1;
       ok = tell(w, st);
-      if (ok && redo) ok = check_values(br, ring, st, slot, base, looks, lane);
+      if (ok && redo) ok = check_values(p, br, ring, st, slot, base, looks, lane);
       base += (uint32_t)st.most * kUnitsPerStep;
       // The next block is taken over when this one's last loads begin: taken
       // earlier, blocks are shared out unevenly (8192 tokens, two units ahead:
       // 545 us).
-      ok = ok && warp_wait_ok(br, &br->taken, (count - 1) & 1);
+      ok = ok && warp_wait_ok(p, br, &br->taken, (count - 1) & 1);
     }
     if (!redo && ok) {
       if (lane == 0) ask_next(br);
       // (also after a wait that gave up: the answer has to land before the CTA ends)
-      const bool told = warp_wait_ok(br, &br->next_full, asked++ & 1);
+      const bool told = warp_wait_ok(p, br, &br->next_full, asked++ & 1);
       ok = ok && told;
       block = told ? next_block(br) : -1;
       __syncwarp();
@@ -612,7 +618,8 @@ __device__ __forceinline__ void schedule(const PrefillParams &p, Bars *br, uint8
 // One row a thread: the softmax of tile t over the steps of one unit of work,
 // then its output.  done, works: the tile's steps and its units of work with
 // steps before this one.
-__device__ __forceinline__ bool softmax_work(const PrefillParams &p, Bars *br, uint32_t tmem, int slot, int t,
+template <class P>
+__device__ __forceinline__ bool softmax_work(const P &p, Bars *br, uint32_t tmem, int slot, int t,
                                              uint32_t done, uint32_t works) {
   const int warp = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
   const int i = t * kRows + warp * 32 + lane;  // the CTA's row
@@ -625,7 +632,7 @@ __device__ __forceinline__ bool softmax_work(const PrefillParams &p, Bars *br, u
   const uint64_t c2 = pack2(p.scale_log2, p.scale_log2);
   const int low = __shfl_sync(0xffffffffu, seen, 0);  // the fewest keys of the warp's rows
   for (int j = 0; j < n; j++) {
-    if (!warp_wait_ok(br, &br->s_full[t], (done + j) & 1)) return false;
+    if (!warp_wait_ok(p, br, &br->s_full[t], (done + j) & 1)) return false;
     tc_fence_after();
     uint32_t s[4][32];
 #pragma unroll
@@ -719,7 +726,7 @@ __device__ __forceinline__ bool softmax_work(const PrefillParams &p, Bars *br, u
   const Steps st = br->steps[slot];
   const bool live = i < w.nq, none = seen == 0;
   if (n > 0) {
-    if (!warp_wait_ok(br, &br->o_done[t], works & 1)) return false;
+    if (!warp_wait_ok(p, br, &br->o_done[t], works & 1)) return false;
     tc_fence_after();
   }
   // l = 0: every score of the row is -inf (0 / 0: nan, unless another part of its keys has weight)
@@ -817,11 +824,12 @@ __device__ __forceinline__ bool softmax_work(const PrefillParams &p, Bars *br, u
   return true;
 }
 
-__device__ __forceinline__ void softmax_rows(const PrefillParams &p, Bars *br, uint32_t tmem, int t) {
+template <class P>
+__device__ __forceinline__ void softmax_rows(const P &p, Bars *br, uint32_t tmem, int t) {
   uint32_t done = 0, works = 0;
   for (uint32_t count = 0;; count++) {
     const uint32_t slot = count & 1;
-    if (!warp_wait_ok(br, &br->work_full[slot], (count >> 1) & 1)) return;
+    if (!warp_wait_ok(p, br, &br->work_full[slot], (count >> 1) & 1)) return;
     if (br->work[slot].nq == 0) return;
     if (!softmax_work(p, br, tmem, (int)slot, t, done, works)) return;
     const int n = br->steps[slot].n[t];
@@ -902,10 +910,11 @@ __global__ void __launch_bounds__(32 * kJoinWarps) prefill_join_kernel(PrefillPa
   if (lane == 0) p.lse[(size_t)h * p.Nq + row] = none ? -INFINITY : m + logf(sum);
 }
 
+template <bool kPoll>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap kn_map,
                    const __grid_constant__ CUtensorMap kp_map, const __grid_constant__ CUtensorMap v_map,
-                   PrefillParams p) {
+                   Limited<kPoll> p) {
   grid_dep_trigger();
   extern __shared__ uint8_t smem_raw[];
   uint8_t *base = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -955,13 +964,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     if (warp == 8) {
-      mma_sequence<false>(br, smem, tmem);
+      mma_sequence<false>(p, br, smem, tmem);
     } else if (warp == 9) {
-      load_rows(&q_map, &kn_map, &kp_map, &v_map, br, smem, lane);
+      load_rows(p, &q_map, &kn_map, &kp_map, &v_map, br, smem, lane);
     } else if (warp == 10) {
       schedule(p, br, base + OFF_RING, lane);
     } else {
-      mma_sequence<true>(br, smem, tmem);
+      mma_sequence<true>(p, br, smem, tmem);
     }
   }
   __syncthreads();
@@ -1077,7 +1086,7 @@ int mla_prefill(const void *q, int64_t q_tok, int64_t q_head, const void *k_nope
     kn_map = kp_map = v_map = q_map;  // no step reads them
   }
   if (!ok) return fail(MLA_ERR_CUDA, "cuTensorMapEncodeTiled failed");
-  PrefillParams p;
+  Limited<false> p;
   p.cu_q = cu_seqlens_q;
   p.cu_k = cu_seqlens_k;
   p.v = static_cast<const __nv_bfloat16 *>(v);
@@ -1098,12 +1107,20 @@ int mla_prefill(const void *q, int64_t q_tok, int64_t q_head, const void *k_nope
   p.out_v8 = al(out, 32) ? 1 : 0;
   p.scale = softmax_scale;
   p.scale_log2 = softmax_scale * LOG2E;
-  cudaError_t e = cudaFuncSetAttribute(prefill_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
-  if (e != cudaSuccess) return fail(MLA_ERR_CUDA, cudaGetErrorString(e));
-  e = launch_dependent(prefill_kernel, (unsigned)(tiles * H * splits), kThreads, kSmem, (cudaStream_t)stream, q_map,
-                       kn_map, kp_map, v_map, p);
+  const unsigned long long limit = wait_limit_ns(), most = 4000000000ull;  // (a 32-bit clock)
+  p.wait_ns = (uint32_t)(limit < most ? limit : most);
+  auto launch = [&](auto *kernel, const auto &params) {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+    return e != cudaSuccess ? e
+                            : launch_dependent(kernel, (unsigned)(tiles * H * splits), kThreads, kSmem,
+                                               (cudaStream_t)stream, q_map, kn_map, kp_map, v_map, params);
+  };
+  const PrefillParams &common = p;
+  cudaError_t e = limit < ptx::kShortWaitNs ? launch(&prefill_kernel<true>, Limited<true>{common})
+                                            : launch(&prefill_kernel<false>, p);
   if (e == cudaSuccess && splits > 1)
-    e = launch_dependent(prefill_join_kernel, (unsigned)((long long)Nq * H), 32 * kJoinWarps, 0, (cudaStream_t)stream, p);
+    e = launch_dependent(prefill_join_kernel, (unsigned)((long long)Nq * H), 32 * kJoinWarps, 0, (cudaStream_t)stream,
+                         common);
   if (e != cudaSuccess) return fail(MLA_ERR_CUDA, cudaGetErrorString(e));
   set_last_error("");
   return MLA_OK;

@@ -7,15 +7,33 @@
 namespace mla {
 namespace ptx {
 
-// The same with little code, for kernels whose roles share the instruction cache
+// mbar_wait for kernels that are compiled for short limits (kPoll: below
+// kShortWaitNs) and for others apart, as a choice at each wait costs one or two
+// per cent of a call.  A short limit polls from the start (mbar_wait's first try
+// may sleep past a microsecond).
+template <bool kCluster, bool kPoll>
+__device__ __forceinline__ bool mbar_wait_limited(uint32_t bar, uint32_t parity, volatile int *abort,
+                                                  uint64_t limit_ns) {
+  if constexpr (kPoll) {
+    for (const uint64_t t0 = globaltimer();;) {
+      if (kCluster ? mbar_test_wait_cluster(bar, parity) : mbar_test_wait(bar, parity)) return true;
+      if (*abort || globaltimer() - t0 > limit_ns) return false;
+    }
+  } else {
+    return mbar_wait<kCluster>(bar, parity, abort, limit_ns < kShortWaitNs ? kShortWaitNs : limit_ns);
+  }
+}
+
+// mbar_wait with little code, for kernels whose roles share the instruction cache
 // among many waits: true once the phase has completed; false, with *abort set,
-// after limit_ns (below 2^32) or when *abort is set already.
-template <bool kCluster>
+// after limit_ns (at most 4e9) or when *abort is set already.
+template <bool kCluster, bool kPoll>
 __device__ __forceinline__ bool mbar_wait_small(uint32_t bar, uint32_t parity, volatile int *abort,
                                                 uint32_t limit_ns) {
   uint32_t t0 = 0, it = 0;
-  while (!(kCluster ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity))) {
-    if (++it & 15u) continue;
+  while (!(kPoll ? (kCluster ? mbar_test_wait_cluster(bar, parity) : mbar_test_wait(bar, parity))
+                 : (kCluster ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity)))) {
+    if (!kPoll && (++it & 15u)) continue;
     uint32_t t;
     asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t));
     if (t0 == 0) {

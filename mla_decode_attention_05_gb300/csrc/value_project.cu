@@ -10,6 +10,7 @@
 #include "common.cuh"
 #include "dependent.cuh"
 #include "ptx.cuh"
+#include "ptx_pair.cuh"
 #include "tma_map.cuh"
 
 namespace mla {
@@ -47,16 +48,20 @@ struct Bars {
 constexpr uint32_t kSmem = OFF_BARS + sizeof(Bars) + 1024;
 static_assert(kSmem <= 232448, "shared memory budget");
 
-__device__ __forceinline__ bool wait_ok(Bars *b, uint64_t *bar, uint32_t parity, unsigned int *status) {
-  if (mbar_wait<false>(smem_u32(bar), parity, &b->abort, kDefaultWaitNs)) return true;
+template <bool kPoll>
+__device__ __forceinline__ bool wait_ok(Bars *b, uint64_t *bar, uint32_t parity, unsigned int *status,
+                                        unsigned long long wait_ns) {
+  if (mbar_wait_limited<false, kPoll>(smem_u32(bar), parity, &b->abort, wait_ns)) return true;
   atomicOr(status, MLA_STATUS_WAIT_TIMEOUT);
   *(volatile int *)&b->abort = 1;
   return false;
 }
 
+template <bool kPoll>
 __global__ void __launch_bounds__(kThreads, 1)
     value_kernel(const __grid_constant__ CUtensorMap w_map, const __grid_constant__ CUtensorMap x_map,
-                 const __grid_constant__ CUtensorMap o_map, int tiles, int items, int ntile, unsigned int *status) {
+                 const __grid_constant__ CUtensorMap o_map, int tiles, int items, int ntile, unsigned int *status,
+                 unsigned long long wait_ns) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t *base = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   Bars *br = reinterpret_cast<Bars *>(base + OFF_BARS);
@@ -102,7 +107,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = i0; i < i1 && ok; i++) {
       const int h = i / tiles, n0 = i % tiles * ntile;
       const bool new_head = i == i0 || n0 == 0;
-      if (new_head) ok = __all_sync(0xffffffffu, wait_ok(br, &br->w_empty, (heads++ & 1) ^ 1, status));
+      if (new_head) ok = __all_sync(0xffffffffu, wait_ok<kPoll>(br, &br->w_empty, (heads++ & 1) ^ 1, status, wait_ns));
       for (int k = 0; k < kKBlocks / 2 && ok; k++, u++) {
         const uint32_t s = u % kUnits, dst = smem + OFF_RING + s * kUnit;
         if (new_head && elect_one()) {
@@ -111,7 +116,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tma_load_3d(smem + (2 * k + 1) * kWBytes, &w_map, smem_u32(&br->w_full[k]), 128 * k + 64, 0, h, pol_w);
         }
         __syncwarp();
-        ok = __all_sync(0xffffffffu, wait_ok(br, &br->empty[s], ((u / kUnits) & 1) ^ 1, status));
+        ok = __all_sync(0xffffffffu, wait_ok<kPoll>(br, &br->empty[s], ((u / kUnits) & 1) ^ 1, status, wait_ns));
         if (!ok) break;
         if (elect_one()) {
           mbar_arrive_expect_tx(smem_u32(&br->full[s]), 2 * box);
@@ -127,7 +132,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t u = 0, heads = 0;
     bool ok = true;
     auto wait = [&](uint64_t *bar, uint32_t parity) {
-      ok = ok && __all_sync(0xffffffffu, wait_ok(br, bar, parity, status));
+      ok = ok && __all_sync(0xffffffffu, wait_ok<kPoll>(br, bar, parity, status, wait_ns));
     };
     for (int i = i0; i < i1 && ok; i++) {
       const int j = i - i0, buf = j & 1;
@@ -161,7 +166,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = i0; i < i1; i++) {
       const int j = i - i0, buf = j & 1;
       // a wait that gives up lets all four warps go on to the barriers below, which they pass together
-      const bool ok = __all_sync(0xffffffffu, wait_ok(br, &br->d_full[buf], (j >> 1) & 1, status));
+      const bool ok = __all_sync(0xffffffffu, wait_ok<kPoll>(br, &br->d_full[buf], (j >> 1) & 1, status, wait_ns));
       tc_fence_after();
       if (threadIdx.x == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // the tile before is out
       __syncwarp();  // (the barriers are the whole warp's)
@@ -249,11 +254,13 @@ int mla_value_project(const void *attn, int64_t ld_token, int64_t ld_head, const
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  if (e == cudaSuccess) e = cudaFuncSetAttribute(value_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+  const unsigned long long limit = wait_limit_ns();
+  auto *kernel = limit < ptx::kShortWaitNs ? &value_kernel<true> : &value_kernel<false>;
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
   if (e != cudaSuccess) return fail(MLA_ERR_CUDA, cudaGetErrorString(e));
   const int items = tiles * H;
-  e = launch_dependent(value_kernel, items < sms ? items : sms, kThreads, kSmem, (cudaStream_t)stream, w_map, x_map,
-                       o_map, tiles, items, ntile, st);
+  e = launch_dependent(kernel, items < sms ? items : sms, kThreads, kSmem, (cudaStream_t)stream, w_map, x_map,
+                       o_map, tiles, items, ntile, st, limit);
   if (e != cudaSuccess) return fail(MLA_ERR_CUDA, cudaGetErrorString(e));
   set_last_error("");
   return MLA_OK;
