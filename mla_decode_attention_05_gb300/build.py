@@ -13,6 +13,7 @@ on the host.
 from __future__ import annotations
 
 import argparse
+import contextlib
 import glob
 import hashlib
 import os
@@ -76,7 +77,8 @@ def _start_fast(force: bool):
     path = fast_path()
     for old in glob.glob(os.path.join(LIB_DIR, "fastcall*.so")):
         if force or old != path:
-            os.remove(old)
+            with contextlib.suppress(FileNotFoundError):  # (another build removes them too)
+                os.remove(old)
     if os.path.exists(path):
         return None
     import sysconfig

@@ -72,3 +72,22 @@ def test_a_build_that_fails_leaves_none(monkeypatch, tmp_path, compiler):
     monkeypatch.setenv("CXX", compiler)
     build._finish_fast(build._start_fast(False))
     assert list(tmp_path.iterdir()) == []
+
+
+def test_two_builds_at_once(monkeypatch, tmp_path):
+    """A file of an earlier build that another build removes first."""
+    import os
+
+    from mla_decode_attention_05_gb300 import build
+    old = tmp_path / "fastcall.so"
+    old.write_bytes(b"of an earlier build")
+    monkeypatch.setattr(build, "LIB_DIR", str(tmp_path))
+    monkeypatch.setenv("CXX", "false")
+    remove = os.remove
+
+    def late(path):
+        remove(path)
+        remove(path)
+    monkeypatch.setattr(build.os, "remove", late)
+    build._finish_fast(build._start_fast(False))
+    assert not old.exists()
