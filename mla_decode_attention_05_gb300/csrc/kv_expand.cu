@@ -11,12 +11,15 @@
 // head: its W_UK rows, then its W_UV rows), K = 512.  2 * 512 flops per
 // 2-byte output value are above the ridge, so with many rows it is bound by
 // the tensor cores, with the output's write close behind; with few rows by
-// the read of the weights (16384 rows, 128 heads: 340 us, 1.6 PFLOP/s; 100 rows,
-// 64 heads: 10.5 us).
+// the read of the weights (16384 rows, 128 heads: 364 us in a long run of calls, 325
+// us, 1.7 PFLOP/s, over fifty from rest; 100 rows, 64 heads: 10.4 us with the
+// weights in L2, 11.9 us without).  Figures below that compare two forms were
+// taken side by side when the choice was made.
 //
 // Roundings: bf16 rows are used as they are.  A row with per-128 scales is
 // dequantised to bf16 (one rounding, the one the decode makes too: the MMA's
-// operands have one type, and the four scales of a row cannot leave its sum).
+// operands have one type, and four partial sums, which could take the row's four
+// scales, would need four times the tensor memory and drain).
 // The codes of a one-scale cache are exact in bf16, so there the scale
 // multiplies the fp32 sum.  Sums are fp32 in tensor memory, rounded once.
 #include <cuda_fp8.h>

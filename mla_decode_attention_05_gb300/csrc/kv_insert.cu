@@ -33,7 +33,8 @@
 // rotated by further blocks of the same launch: rows of 128 bytes, eight
 // lanes a row, so a warp moves four rows at a time; that part is bound by HBM
 // (256 bytes a row) and shares nothing with the insert but the launch (8191
-// tokens, 64 heads, FP8 rows: 27 us, 5.6 TB/s; 64 tokens, 128 heads: 3.0 us).
+// tokens, 64 heads, FP8 rows: 27 us, 5.6 TB/s where outputs cannot stay in L2;
+// 64 tokens, 128 heads: 3.1 us).
 #include <cuda_fp8.h>
 
 #include "common.cuh"

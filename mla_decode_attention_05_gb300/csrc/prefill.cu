@@ -7,9 +7,11 @@
 // A row without keys gets out = 0 and lse = -inf.
 //
 // 640 flops a pair and head against one exponential, so the tensor cores
-// bound it (8192 tokens, 32 heads, causal: 432 us, 1.6 PFLOP/s; eight prompts of
-// 136 to 1500 tokens, 128 heads: 286 us); softmax has to stay in their shadow.  One pass over the keys with
-// a running reference m and sum l per row:
+// bound it (8192 tokens, 32 heads, causal: 440 us in a long run of calls, 401 us,
+// 1.7 PFLOP/s, over fifty from rest; eight prompts of 136 to 1500 tokens, 128
+// heads: 302 and 282 us); softmax has to stay in their shadow.  (Figures below
+// that compare two forms were taken side by side when the choice was made.)  One
+// pass over the keys with a running reference m and sum l per row:
 //   p_j = 2^(s_j c - m c),  l += p_j,  O += p_j v_j        (c = scale log2 e)
 // m is the row's maximum when it was last moved.  It moves, and O and l are
 // scaled down, only when the maximum has grown by more than 8 in the exponent:

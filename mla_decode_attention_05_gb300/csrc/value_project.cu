@@ -6,7 +6,8 @@
 //
 // Bytes bound it: 2 * 128 * 512 flops per 1280 bytes of a row are about 100
 // flops a byte, a third of what the tensor cores can take (4095 tokens, 64 heads:
-// 57 us, 6.0 TB/s; 64 tokens, 128 heads: 4.6 us).
+// 60 us, 5.7 TB/s, where outputs cannot stay in L2; 64 tokens, 128 heads: 4.6 us
+// with the weights in L2, 7.4 us without).
 #include "common.cuh"
 #include "dependent.cuh"
 #include "ptx.cuh"
