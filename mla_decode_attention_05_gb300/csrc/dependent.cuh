@@ -1,8 +1,7 @@
 // What the operators around the decode share: their launches as programmatic
 // dependents, the limit of their waits, and the rotating insert's parameters.
-// (Apart from common.cuh and
-// ptx.cuh, which the decode kernel is compiled from: a measurement of that
-// kernel holds as long as its sources stay as they are.)
+// (Apart from common.cuh and ptx.cuh, which the decode kernel is compiled from: a
+// measurement of that kernel holds as long as its sources stay as they are.)
 #pragma once
 
 #include "common.cuh"
