@@ -28,8 +28,8 @@
  * synchronises the host, except mla_device_status().
  *
  * CUDA graphs: mla_decode_metadata, mla_decode, mla_kv_insert,
- * mla_kv_insert_rope, mla_query_absorb, mla_kv_expand, mla_prefill and
- * mla_value_project can be captured into a CUDA graph on `stream` once the
+ * mla_kv_insert_rope, mla_query_absorb, mla_kv_expand, mla_prefill,
+ * mla_value_project, mla_decode_shared, mla_attention_mass and mla_evict can be captured into a CUDA graph on `stream` once the
  * calling thread has made the same kind of call outside capture (the first
  * call does one-time host set-up).  A replay uses the buffers seen at
  * capture and reads their contents at replay time; the split-KV schedule is
@@ -458,6 +458,121 @@ int mla_prefill(const void *q, int64_t q_tok, int64_t q_head, const void *k_nope
  */
 int mla_value_project(const void *attn, int64_t ld_token, int64_t ld_head, const void *w_uv, int64_t w_row,
                       int64_t w_head, int N, int H, void *out, mla_stream_t stream);
+
+/*
+ * Decode of a batch whose sequences share prefixes (samples of one prompt, one
+ * system prompt for many users).  The prefix of a group of sequences lies in the
+ * cache once, and attention over it is computed for all of the group's query
+ * rows together; each sequence's own tokens follow it.  For query row (b, t, h) of
+ * a sequence of group g, with the formulas at the top of this file, over the keys
+ *   N(b, t) = {prefix tokens n < prefix_lens[g]} and
+ *             {own tokens n < s_k} (causal = 0) or {n < s_k - T + t + 1} (causal = 1)
+ * (with causal every query token sees the whole prefix: the query tokens are the
+ * last T of the own ones).  A row without any key gets out = 0 and lse = -inf.
+ *
+ *   q, kv_cache, kv_format, num_pages, page_size, kv_scales, softmax_scale, out,
+ *   lse, B, T, H   as for mla_decode
+ *   prefix_table   device int32 [G][max_prefix_pages]: pages of each group's prefix
+ *   prefix_lens    device int32 [G]: its tokens (0: none)
+ *   group_offsets  device int32 [G + 1]: group g has the sequences
+ *                  group_offsets[g] .. group_offsets[g + 1] - 1; sequences before
+ *                  the first and behind the last group have no prefix.  NULL
+ *                  (with G = 1): all sequences.  Values out of order or outside
+ *                  [0, B] are clamped and set MLA_STATUS_BAD_SEQLEN.
+ *   block_table, max_pages, cache_seqlens   as for mla_decode, the own tokens
+ *                  (lengths outside [0, max_pages * 64], here and for prefixes,
+ *                  are clamped and set MLA_STATUS_BAD_SEQLEN)
+ *   workspace      device, >= mla_decode_shared_workspace_bytes(...) bytes for the
+ *                  current device, 256-byte aligned; no initialisation; calls
+ *                  that overlap on the GPU need separate ones
+ * Parts of an output are joined in fp32, and rounded once.  At most 8192 tiles of
+ * 128 query rows (B * ceil(T * H / 128), and ceil(B * T * H / 128) + G;
+ * MLA_ERR_UNSUPPORTED above).  Cache rows behind the last token of a sequence or
+ * prefix, in its last page, must hold finite values.  A page outside the pool is
+ * skipped and sets MLA_STATUS_BAD_PAGE.  Asynchronous on `stream`; can be captured in a
+ * CUDA graph.  Returns MLA_OK or a negative code.
+ */
+size_t mla_decode_shared_workspace_bytes(int B, int T, int H, int G, int kv_format, int max_prefix_pages);
+int mla_decode_shared(const void *q, const void *kv_cache, int kv_format, int num_pages, int page_size,
+                      const int32_t *prefix_table, int max_prefix_pages, const int32_t *prefix_lens,
+                      const int32_t *group_offsets, int G, const int32_t *block_table, int max_pages,
+                      const int32_t *cache_seqlens, const float *kv_scales, float softmax_scale, int causal,
+                      void *workspace, size_t workspace_bytes, void *out, float *lse, int B, int T, int H,
+                      mla_stream_t stream);
+
+/*
+ * The attention weight of every cached token, added to a running sum:
+ *   mass[b][n] = decay * mass[b][n]
+ *                + sum over rows (t, h) that see n of exp(softmax_scale * q[b][t][h] . K_n - lse[b][h][t])
+ * for n < s_k; other entries are left as they were.  With decay = 0 the old
+ * entries are not read.  A row with lse = -inf (it saw no key) adds nothing.  The
+ * log-sum-exp is that of the attention in question: mla_decode's,
+ * mla_decode_shared's (its own part of the cache then gets its share of the
+ * whole), or of the last T queries of a prompt.
+ *
+ *   q              device bf16 [B][T][H][576], any T >= 1
+ *   kv_cache, kv_format, num_pages, page_size, block_table, max_pages, kv_scales,
+ *   softmax_scale, causal   as for mla_decode
+ *   cache_seqlens  device int32 [B]: outside [0, min(max_pages * 64, mass_cap)]
+ *                  clamped, sets MLA_STATUS_BAD_SEQLEN
+ *   lse            device fp32 [B][H][T] (natural log)
+ *   decay          finite, >= 0
+ *   mass           device fp32 [B][mass_cap], updated; mass_cap at most 2^24
+ *   workspace      device, >= mla_attention_mass_workspace_bytes(B, T, H, mass_cap)
+ *                  bytes, 256-byte aligned (NULL where that is 0, as it is for
+ *                  T * H <= 128); no initialisation; calls that overlap on the GPU
+ *                  need separate ones
+ * Scores and sums are fp32; FP8 rows with scales are rounded to bf16, as the
+ * decode does.  Sums are made in a fixed order: equal calls give equal bits.  A
+ * token whose page lies outside the pool gets no weight and sets
+ * MLA_STATUS_BAD_PAGE.  A wait that gives up sets MLA_STATUS_WAIT_TIMEOUT.
+ * Asynchronous on `stream`; can be captured in a CUDA graph.  Returns MLA_OK or a
+ * negative code.
+ */
+size_t mla_attention_mass_workspace_bytes(int B, int T, int H, int mass_cap);
+int mla_attention_mass(const void *q, const void *kv_cache, int kv_format, int num_pages, int page_size,
+                       const int32_t *block_table, int max_pages, const int32_t *cache_seqlens, const float *kv_scales,
+                       const float *lse, float softmax_scale, int causal, float decay, float *mass, int mass_cap,
+                       void *workspace, size_t workspace_bytes, int B, int T, int H, mla_stream_t stream);
+
+/*
+ * Eviction: cuts every sequence of n = cache_seqlens[b] > keep cached tokens down
+ * to keep of them, in place.  What stays, in this order until there are keep:
+ *   1. tokens with positions[b][i] < sinks or positions[b][i] > p - recent, p the
+ *      largest position among the n;
+ *   2. the others by mass[b][i], heaviest first (nan below everything);
+ * and of equals the lower slot i first.  A stayer in a slot below keep stays in
+ * it.  The stayers behind, in order of their slots, move into the slots below
+ * keep that have become free, in order: row, scales, mass and position.  The
+ * slots from keep to n - 1 then hold mass 0 and position -1, so a token
+ * appended there starts from nothing.  (The order of slots has no meaning to
+ * attention without `causal`, and with it none but for the last T, which are
+ * appended afterwards.)  Sequences of at most keep tokens are left as they are.
+ *
+ *   kv_cache, kv_format, num_pages, page_size, block_table, max_pages, kv_scales
+ *                  as for mla_decode; written.  No page may belong to two
+ *                  sequences (shared prefixes lie in a table of their own).
+ *   cache_seqlens  device int32 [B]: outside [0, min(max_pages * 64, mass_cap)]
+ *                  clamped, sets MLA_STATUS_BAD_SEQLEN
+ *   mass           device fp32 [B][mass_cap], positions device int32
+ *                  [B][mass_cap], updated; the positions of a sequence's tokens
+ *                  are distinct (they are what is rotated with, not the slots)
+ *   keep, sinks, recent   keep >= 1; sinks, recent >= 0; sinks + recent <= keep
+ *   out_seqlens    device int32 [B], min(n, keep) written; may be cache_seqlens
+ *                  (or not: the layers of a model share their lengths)
+ *   workspace      device, >= mla_evict_workspace_bytes(B, mass_cap, keep) bytes,
+ *                  256-byte aligned; no initialisation; calls that overlap on the
+ *                  GPU need separate ones
+ * A row whose page, or whose target's, lies outside the pool is not copied (its
+ * mass and position move) and sets MLA_STATUS_BAD_PAGE.  At most 8192 sequences.
+ * Asynchronous on `stream`; can be captured in a CUDA graph.  Returns MLA_OK or a
+ * negative code.
+ */
+size_t mla_evict_workspace_bytes(int B, int mass_cap, int keep);
+int mla_evict(void *kv_cache, int kv_format, int num_pages, int page_size, const int32_t *block_table, int max_pages,
+              const int32_t *cache_seqlens, float *kv_scales, float *mass, int32_t *positions, int mass_cap, int keep,
+              int sinks, int recent, int32_t *out_seqlens, void *workspace, size_t workspace_bytes, int B,
+              mla_stream_t stream);
 
 /* Text of the calling thread's last error ("" if none). */
 const char *mla_last_error_string(void);

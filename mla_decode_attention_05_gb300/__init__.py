@@ -89,6 +89,17 @@ def lib():
             L.mla_prefill_workspace_bytes.argtypes = [i, i, i, i]
             L.mla_prefill_workspace_bytes.restype = sz
             L.mla_value_project.argtypes = [P, i64, i64, P, i64, i64, i, i, P, P]
+            L.mla_decode_shared.argtypes = [P, P, i, i, i, P, i, P, P, i, P, i, P, P, ctypes.c_float, i, P, sz, P, P,
+                                            i, i, i, P]
+            L.mla_decode_shared_workspace_bytes.argtypes = [i, i, i, i, i, i]
+            L.mla_decode_shared_workspace_bytes.restype = sz
+            L.mla_attention_mass.argtypes = [P, P, i, i, i, P, i, P, P, P, ctypes.c_float, i, ctypes.c_float, P, i, P, sz,
+                                             i, i, i, P]
+            L.mla_attention_mass_workspace_bytes.argtypes = [i, i, i, i]
+            L.mla_attention_mass_workspace_bytes.restype = sz
+            L.mla_evict.argtypes = [P, i, i, i, P, i, P, P, P, P, i, i, i, i, P, P, sz, i, P]
+            L.mla_evict_workspace_bytes.argtypes = [i, i, i]
+            L.mla_evict_workspace_bytes.restype = sz
             L.mla_query_absorb_workspace_bytes.argtypes = [i, i]
             L.mla_query_absorb_workspace_bytes.restype = sz
             L.mla_query_absorb.argtypes = [P, i, P, ctypes.c_float, P, P, i, i, P, P, sz, P]
@@ -694,6 +705,170 @@ def value_project(attn: torch.Tensor, w_uv: torch.Tensor, *, out: Optional[torch
             raise ValueError(f"out must be [{N}, {H}, 128], got {list(out.shape)}")
     _call("mla_value_project", dev, attn.data_ptr(), *strides, w_uv.data_ptr(), w_row, w_head, N, H, out.data_ptr())
     return out
+
+
+def decode_shared(q: torch.Tensor, kv_cache: torch.Tensor, prefix_table: torch.Tensor, prefix_lens: torch.Tensor,
+                  block_table: torch.Tensor, cache_seqlens: torch.Tensor, *, softmax_scale: float,
+                  group_offsets: Optional[torch.Tensor] = None, causal: bool = False,
+                  kv_scales: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                  out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None):
+    """decode() of a batch whose sequences share prefixes, on the current stream
+    (mla_decode_shared) -> (out bf16 [B,T,H,512], lse fp32 [B,H,T]).
+
+    prefix_table int32 [G, max_prefix_pages] and prefix_lens int32 [G]: the
+    pages and tokens of each group's prefix; group_offsets int32 [G+1]: the
+    sequences of each group (None, with G = 1: all).  Sequences of no group
+    have no prefix.  block_table and cache_seqlens are of each sequence's own
+    tokens, which follow its prefix; causal applies to them.  The other
+    arguments are decode()'s.  workspace: at least
+    decode_shared_workspace_bytes() bytes (allocated here when not given)."""
+    dev, B, T, H, fmt, _ = _decode_args(q, kv_cache, block_table, cache_seqlens, None, kv_scales)
+    if fmt == KV_FP8_E4M3 and tuple(kv_scales.shape) != (kv_cache.shape[0], PAGE_SIZE, 4):
+        raise ValueError(f"kv_scales must be [{kv_cache.shape[0]}, {PAGE_SIZE}, 4], got {list(kv_scales.shape)}")
+    _need(prefix_table, "prefix_table", torch.int32, dev, 2)
+    _need(prefix_lens, "prefix_lens", torch.int32, dev, 1)
+    G, width = prefix_table.shape
+    if prefix_lens.shape[0] != G:
+        raise ValueError("prefix_lens must be [G] for a prefix_table of G rows")
+    if group_offsets is not None:
+        _need(group_offsets, "group_offsets", torch.int32, dev, 1)
+        if group_offsets.shape[0] != G + 1:
+            raise ValueError("group_offsets must be [G + 1]")
+    elif G != 1:
+        raise ValueError("group_offsets is needed for more than one group")
+    if out is None:
+        out = torch.empty((B, T, H, D_V), dtype=torch.bfloat16, device=dev)
+    if lse is None:
+        lse = torch.empty((B, H, T), dtype=torch.float32, device=dev)
+    _need(out, "out", torch.bfloat16, dev, 4)
+    _need(lse, "lse", torch.float32, dev, 3)
+    if tuple(out.shape) != (B, T, H, D_V) or tuple(lse.shape) != (B, H, T):
+        raise ValueError(f"out must be [{B}, {T}, {H}, {D_V}] and lse [{B}, {H}, {T}]")
+    if workspace is None:
+        workspace = torch.empty(decode_shared_workspace_bytes(B, T, H, G, fmt, width, dev), dtype=torch.uint8, device=dev)
+    _need(workspace, "workspace", workspace.dtype, dev)
+    _call("mla_decode_shared", dev, q.data_ptr(), kv_cache.data_ptr(), fmt, kv_cache.shape[0], kv_cache.shape[1],
+          prefix_table.data_ptr(), width, prefix_lens.data_ptr(), _at(group_offsets), G, block_table.data_ptr(),
+          block_table.shape[1], cache_seqlens.data_ptr(), _at(kv_scales) if fmt != KV_BF16 else None,
+          float(softmax_scale), int(bool(causal)), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+          out.data_ptr(), lse.data_ptr(), B, T, H)
+    return out, lse
+
+
+def decode_shared_workspace_bytes(B: int, T: int, H: int, G: int, kv_format: int, max_prefix_pages: int,
+                                  device=None) -> int:
+    """Workspace of decode_shared() for B sequences in G groups (kv_format:
+    KV_BF16, KV_FP8_E4M3 or KV_FP8_E4M3_TENSOR) on `device` (default: the
+    current one)."""
+    with torch.cuda.device(device if device is not None else torch.cuda.current_device()):
+        n = int(lib().mla_decode_shared_workspace_bytes(B, T, H, G, kv_format, max_prefix_pages))
+    if n == 0:
+        raise MlaError(-1, lib().mla_last_error_string().decode())
+    return n
+
+
+def _mass_args(mass, B, dev):
+    _need(mass, "mass", torch.float32, dev, 2)
+    if mass.shape[0] != B or mass.shape[1] < 1:
+        raise ValueError(f"mass must be [{B}, capacity], got {list(mass.shape)}")
+    return mass.shape[1]
+
+
+def attention_mass(q: torch.Tensor, kv_cache: torch.Tensor, block_table: torch.Tensor, cache_seqlens: torch.Tensor,
+                   lse: torch.Tensor, mass: torch.Tensor, *, softmax_scale: float, causal: bool = False,
+                   decay: float = 1.0, kv_scales: Optional[torch.Tensor] = None,
+                   workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The attention weight of every cached token, summed over query tokens and
+    heads and added to a running sum, on the current stream
+    (mla_attention_mass): mass[b, n] = decay * mass[b, n] + sum over (t, h) of
+    exp(softmax_scale * q[b, t, h] . K_n - lse[b, h, t]) for n <
+    cache_seqlens[b].  Returns mass.
+
+    lse fp32 [B,H,T] as decode() or decode_shared() has given it; mass fp32 [B,
+    capacity], updated in place (decay = 0: not read).  The other arguments are
+    decode()'s, but T may be any number of tokens.  workspace: at least
+    attention_mass_workspace_bytes() bytes (allocated here where it is needed
+    and not given)."""
+    dev, B, T, H, fmt, _ = _decode_args(q, kv_cache, block_table, cache_seqlens, None, kv_scales)
+    if fmt == KV_FP8_E4M3 and tuple(kv_scales.shape) != (kv_cache.shape[0], PAGE_SIZE, 4):
+        raise ValueError(f"kv_scales must be [{kv_cache.shape[0]}, {PAGE_SIZE}, 4], got {list(kv_scales.shape)}")
+    _need(lse, "lse", torch.float32, dev, 3)
+    if tuple(lse.shape) != (B, H, T):
+        raise ValueError(f"lse must be [{B}, {H}, {T}], got {list(lse.shape)}")
+    cap = _mass_args(mass, B, dev)
+    room = attention_mass_workspace_bytes(B, T, H, cap)
+    if workspace is None:
+        if room:
+            workspace = torch.empty(room, dtype=torch.uint8, device=dev)
+    else:
+        _need(workspace, "workspace", workspace.dtype, dev)
+        room = workspace.numel() * workspace.element_size()
+    _call("mla_attention_mass", dev, q.data_ptr(), kv_cache.data_ptr(), fmt, kv_cache.shape[0], kv_cache.shape[1],
+          block_table.data_ptr(), block_table.shape[1], cache_seqlens.data_ptr(),
+          _at(kv_scales) if fmt != KV_BF16 else None, lse.data_ptr(), float(softmax_scale), int(bool(causal)),
+          float(decay), mass.data_ptr(), cap, _at(workspace), room, B, T, H)
+    return mass
+
+
+def attention_mass_workspace_bytes(B: int, T: int, H: int, capacity: int) -> int:
+    """Workspace of attention_mass() (0: none)."""
+    return int(lib().mla_attention_mass_workspace_bytes(B, T, H, capacity))
+
+
+def evict(kv_cache: torch.Tensor, block_table: torch.Tensor, cache_seqlens: torch.Tensor, mass: torch.Tensor,
+          positions: torch.Tensor, *, keep: int, sinks: int = 0, recent: int = 0,
+          kv_scales: Optional[torch.Tensor] = None, out_seqlens: Optional[torch.Tensor] = None,
+          workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Cuts each sequence of more than `keep` cached tokens down to `keep`, in
+    place, on the current stream (mla_evict) -> the new lengths int32 [B].
+
+    Tokens at positions below `sinks`, the `recent` latest positions, and of the
+    others those with the largest mass stay (of equals the lower slot).  The
+    rows (and scales, mass and positions) of stayers in slots from `keep` on
+    move into the slots below that have become free; the slots from `keep` on
+    then hold mass 0 and position -1.  mass fp32 and positions int32 [B,
+    capacity]; kv_cache, block_table and kv_scales as in decode(); no page of
+    two sequences.  out_seqlens: where the lengths go (default: a new tensor;
+    cache_seqlens itself will do).  workspace: at least evict_workspace_bytes()
+    bytes (allocated here when not given)."""
+    if not isinstance(kv_cache, torch.Tensor):
+        raise TypeError("kv_cache must be a torch.Tensor")
+    fmt = _cache_format(kv_cache, kv_scales)
+    dev = kv_cache.device
+    _need(kv_cache, "kv_cache", kv_cache.dtype, dev, 3)
+    _need(block_table, "block_table", torch.int32, dev, 2)
+    _need(cache_seqlens, "cache_seqlens", torch.int32, dev, 1)
+    B = block_table.shape[0]
+    if cache_seqlens.shape[0] != B:
+        raise ValueError("block_table / cache_seqlens batch mismatch")
+    if fmt == KV_FP8_E4M3 and tuple(kv_scales.shape) != (kv_cache.shape[0], PAGE_SIZE, 4):
+        raise ValueError(f"kv_scales must be [{kv_cache.shape[0]}, {PAGE_SIZE}, 4], got {list(kv_scales.shape)}")
+    cap = _mass_args(mass, B, dev)
+    _need(positions, "positions", torch.int32, dev, 2)
+    if tuple(positions.shape) != (B, cap):
+        raise ValueError(f"positions must be [{B}, {cap}] as mass is, got {list(positions.shape)}")
+    if out_seqlens is None:
+        out_seqlens = torch.empty((B,), dtype=torch.int32, device=dev)
+    else:
+        _need(out_seqlens, "out_seqlens", torch.int32, dev, 1)
+        if out_seqlens.shape[0] != B:
+            raise ValueError("out_seqlens must be [B]")
+    if workspace is None:
+        workspace = torch.empty(evict_workspace_bytes(B, cap, keep), dtype=torch.uint8, device=dev)
+    _need(workspace, "workspace", workspace.dtype, dev)
+    _call("mla_evict", dev, kv_cache.data_ptr(), fmt, kv_cache.shape[0], kv_cache.shape[1], block_table.data_ptr(),
+          block_table.shape[1], cache_seqlens.data_ptr(), _at(kv_scales) if fmt == KV_FP8_E4M3 else None,
+          mass.data_ptr(), positions.data_ptr(), cap, int(keep), int(sinks), int(recent), out_seqlens.data_ptr(),
+          workspace.data_ptr(), workspace.numel() * workspace.element_size(), B)
+    return out_seqlens
+
+
+def evict_workspace_bytes(B: int, capacity: int, keep: int) -> int:
+    """Workspace of evict() for B sequences with room for `capacity` tokens."""
+    n = int(lib().mla_evict_workspace_bytes(B, capacity, keep))
+    if n == 0:
+        raise MlaError(-1, lib().mla_last_error_string().decode())
+    return n
 
 
 D_QA = 1536
