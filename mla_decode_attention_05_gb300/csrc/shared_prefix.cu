@@ -1,11 +1,17 @@
-// Decode of a batch whose sequences share long prefixes: attention over a
-// group's prefix for the query rows of all its sequences together, over each
-// sequence's own cache, and the join of the two.
+// Decode of a batch whose sequences share long prefixes: the schedule, the
+// widening of FP8 prefixes, the join of prefix and own parts, and the C entry.
+//
+// For a query row with parts s over disjoint keys (its group's prefix and its own
+// tokens, each perhaps split over several workers), L_s = log2 sum 2^score and
+// O_s = sum 2^(score - L_s) v:
+//   L = log2 sum_s 2^L_s,  O = sum_s 2^(L_s - L) O_s
+// and a part without keys has L_s = -inf and weight 0.
 #include <cmath>
 #include <cstdio>
 
-#include "common.cuh"
 #include "dependent.cuh"
+#include "fp8.cuh"
+#include "shared_prefix.cuh"
 
 namespace mla {
 namespace {
@@ -13,34 +19,8 @@ namespace {
 constexpr int kSchedThreads = 1024;
 constexpr int kMaxItems = MLA_MAX_ITEMS;
 
-struct SharedParams {
-  const __nv_bfloat16 *q;
-  const uint8_t *cache;
-  const float *kv_scales;
-  const int32_t *prefix_table, *prefix_lens, *offsets;  // offsets null: one group of all sequences
-  const int32_t *block_table, *seqlens;
-  unsigned int *status;
-  int format, num_pages, max_prefix, max_pages, G, B, T, H, causal;
-  int n_pt;   // room for prefix tiles
-  int n_mt;   // own M tiles of a sequence
-  int parts;
-  // workspace
-  int32_t *md_p, *ns_p, *md_o, *ns_o;  // the two schedules
-  int32_t *cnt_p, *cnt_o;              // pieces of each item (0: no keys)
-  int32_t *lens_p;                     // [n_pt] keys of a prefix tile
-  int4 *tile_p;                        // [n_pt] {group, first query row, rows, 0}
-  int32_t *table_p;                    // [n_pt][max_prefix]
-  int32_t *lens_o;                     // [B] clamped
-  int2 *seq;                           // [B] {first prefix tile of its group or -1, its first row among the group's}
-  uint8_t *q_p;                        // [n_pt * 128][576] bf16
-  uint8_t *scratch;                    // FP8: [G * max_prefix][64][576] bf16
-  float *lse_p, *o_p, *lse_o, *o_o;    // partials
-  __nv_bfloat16 *out;
-  float *lse;
-};
-
 template <class Op>
-__device__ inline int block_scan(int v, int *warp_sums, int identity, Op op) {
+__device__ inline int block_scan(int v, int *warp_sums, Op op) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -64,196 +44,213 @@ __device__ inline int block_scan(int v, int *warp_sums, int identity, Op op) {
   return v;
 }
 
-__device__ inline int last_le(const int *C, int n, int x) {
-  int lo = 0, hi = n;
+struct Add {
+  __device__ int operator()(int a, int b) const { return a + b; }
+};
+struct Max {
+  __device__ int operator()(int a, int b) const { return max(a, b); }
+};
+
+// The largest i in [0, n) with at(i) <= x (at(0) <= x, nondecreasing).
+template <class At>
+__device__ inline int last_le(int n, int x, At at) {
+  int lo = 0, hi = n - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
-    if (C[mid] <= x) lo = mid; else hi = mid - 1;
+    if (at(mid) <= x) lo = mid; else hi = mid - 1;
   }
   return lo;
 }
 
-// The decode kernel's schedule (mla_decode_metadata's rule) of n items with
-// tiles(i) key tiles each, but with room for two pieces at least of every item:
-// it then writes all its results as fp32 partials.
-template <class Tiles>
-__device__ void schedule(int n, int parts, int32_t *md_out, int32_t *ns_out, int32_t *cnt, int *C, int *warp_sums,
-                         int *carry, Tiles tiles) {
+struct SchedShared {
+  int C[kMaxItems + 1];
+  int warp_sums[32];
+  int carry, top;
+};
+
+// mla_decode_metadata's rule over n items of tiles(i) key tiles: an item costs
+// tiles(i) + 4 on a line, which is cut into `parts` equal segments.  Writes the
+// segments, the pieces of each item and its first slot of results; `least`: slots
+// that every item has at least.
+template <class Tiles, class Slot>
+__device__ void schedule(SchedShared &sh, int n, int parts, int least, int32_t *md_out, int32_t *pieces, Tiles tiles, Slot slot) {
   const int tid = threadIdx.x;
-  auto add = [](int a, int b) { return a + b; };
-  if (tid == 0) { *carry = 0; C[0] = 0; }
+  if (tid == 0) { sh.carry = 0; sh.C[0] = 0; }
   __syncthreads();
   for (int base = 0; base < n; base += kSchedThreads) {
     const int i = base + tid;
-    const int incl = block_scan(i < n ? FIXED_COST + tiles(i) : 0, warp_sums, 0, add);
-    if (i < n) C[i + 1] = *carry + incl;
+    const int incl = block_scan(i < n ? FIXED_COST + tiles(i) : 0, sh.warp_sums, Add());
+    if (i < n) sh.C[i + 1] = sh.carry + incl;
     __syncthreads();
-    if (tid == kSchedThreads - 1) *carry += incl;
+    if (tid == kSchedThreads - 1) sh.carry += incl;
     __syncthreads();
   }
-  const int W = C[n], L = max(ceil_div(W, parts), 1);
+  const int W = sh.C[n], L = max(ceil_div(W, parts), 1);
   for (int p = tid; p < parts; p += kSchedThreads) {
-    int32_t *md = md_out + (size_t)p * MD_STRIDE;
     const long long at = (long long)p * L;
-    if (at >= W) {
-      md[0] = n; md[1] = 0; md[2] = n - 1; md[3] = 0; md[4] = 0; md[5] = 0; md[6] = 0; md[7] = 0;
-      continue;
+    int4 lo4 = make_int4(n, 0, n - 1, 0), hi4 = make_int4(0, 0, 0, 0);
+    if (at < W) {
+      const int lo = (int)at, hi = min(lo + L, W);
+      auto C = [&](int i) { return sh.C[i]; };
+      const int a = last_le(n, lo, C), z = last_le(n, hi - 1, C);
+      const int na = sh.C[a + 1] - sh.C[a] - FIXED_COST, nz = sh.C[z + 1] - sh.C[z] - FIXED_COST;
+      lo4 = make_int4(a, min(max(lo - sh.C[a] - FIXED_COST, 0), na), z, min(max(hi - sh.C[z] - FIXED_COST, 0), nz));
+      hi4 = make_int4(na > 0 ? max(p - (sh.C[a] + FIXED_COST) / L, 0) : 0, sh.C[a] == lo ? 1 : 0, 0, 0);
     }
-    const int lo = (int)at, hi = min(lo + L, W);
-    const int a = last_le(C, n, lo), z = last_le(C, n, hi - 1);
-    const int na = C[a + 1] - C[a] - FIXED_COST, nz = C[z + 1] - C[z] - FIXED_COST;
-    md[0] = a;
-    md[1] = min(max(lo - C[a] - FIXED_COST, 0), na);
-    md[2] = z;
-    md[3] = min(max(hi - C[z] - FIXED_COST, 0), nz);
-    md[4] = na > 0 ? max(p - (C[a] + FIXED_COST) / L, 0) : 0;
-    md[5] = C[a] == lo ? 1 : 0;
-    md[6] = 0; md[7] = 0;
+    reinterpret_cast<int4 *>(md_out)[2 * p] = lo4;
+    reinterpret_cast<int4 *>(md_out)[2 * p + 1] = hi4;
   }
-  if (tid == 0) *carry = 0;
+  if (tid == 0) sh.carry = 0;
   __syncthreads();
   for (int base = 0; base < n; base += kSchedThreads) {
     const int i = base + tid;
     int room = 0;
     if (i < n) {
-      const int k = C[i + 1] - C[i] - FIXED_COST, first = C[i] + FIXED_COST;
-      const int pieces = k == 0 ? 0 : (first + k - 1) / L - first / L + 1;
-      cnt[i] = pieces;
-      room = max(pieces, 2);
+      const int k = sh.C[i + 1] - sh.C[i] - FIXED_COST, first = sh.C[i] + FIXED_COST;
+      const int got = k == 0 ? 0 : (first + k - 1) / L - first / L + 1;
+      pieces[i] = got;
+      room = max(got, least);
     }
-    const int incl = block_scan(room, warp_sums, 0, add);
-    if (i < n) ns_out[i + 1] = *carry + incl;
+    const int incl = block_scan(room, sh.warp_sums, Add());
+    if (i < n) slot(i, sh.carry + incl - room, sh.carry + incl);
     __syncthreads();
-    if (tid == kSchedThreads - 1) *carry += incl;
+    if (tid == kSchedThreads - 1) sh.carry += incl;
     __syncthreads();
   }
-  if (tid == 0) ns_out[0] = 0;
 }
 
-// Block 0: the groups' tiles of 128 query rows and their schedule; block 1: the own caches'.
+// Keys of the last row of own tile mt of a sequence of n tokens.
+__device__ __forceinline__ int own_keys(const SharedParams &p, int n, int mt) {
+  const int last = min((mt + 1) * M_TILE, p.T * p.H) - 1;
+  return row_kv_len(n, p.T, last / p.H, p.causal);
+}
+
+// Block 0: the items of shared_attention_kernel, prefixes first, and their
+// schedule.  Block 1 (FP8): the decode kernel's schedule of the own tokens, with room for two pieces
+// of every item, so that it writes all its results as partials.
 __global__ void __launch_bounds__(kSchedThreads) shared_schedule_kernel(SharedParams p) {
-  __shared__ int C[kMaxItems + 1];
-  __shared__ int warp_sums[32];
-  __shared__ int carry, top;
+  __shared__ SchedShared sh;
   const int tid = threadIdx.x, TH = p.T * p.H;
   grid_dep_trigger();
   grid_dep_wait();
+  const bool wide = p.format != MLA_KV_BF16;
+  auto length = [&](int n, int pages) {
+    const int most = pages > 0x7fffffff / PAGE ? 0x7fffffff : pages * PAGE;
+    if (n < 0 || n > most) atomicOr(p.status, MLA_STATUS_BAD_SEQLEN);
+    return min(max(n, 0), most);
+  };
   if (blockIdx.x == 1) {
-    const int most = p.max_pages > 0x7fffffff / PAGE ? 0x7fffffff : p.max_pages * PAGE;
-    for (int b = tid; b < p.B; b += kSchedThreads) {
-      const int n = p.seqlens[b];
-      if (n < 0 || n > most) atomicOr(p.status, MLA_STATUS_BAD_SEQLEN);
-      p.lens_o[b] = min(max(n, 0), most);
-    }
+    for (int b = tid; b < p.B; b += kSchedThreads) p.lens_o[b] = length(p.seqlens[b], p.max_pages);
     __syncthreads();
-    schedule(p.B * p.n_mt, p.parts, p.md_o, p.ns_o, p.cnt_o, C, warp_sums, &carry, [&](int i) {
-      return item_at(i, p.lens_o, p.B, p.H, p.T, 0, p.causal, p.status).ntiles;
-    });
+    schedule(sh, p.B * p.n_mt, p.parts, 2, p.md_o, p.cnt_o,
+             [&](int i) { return ceil_div(own_keys(p, p.lens_o[i % p.B], i / p.B), PAGE); },
+             [&](int i, int at, int end) {
+               if (i == 0) p.ns_o[0] = 0;
+               p.ns_o[i + 1] = end;
+             });
     return;
   }
-  for (int b = tid; b < p.B; b += kSchedThreads) p.seq[b] = make_int2(-1, 0);
-  if (tid == 0) { carry = 0; top = 0; }
+  // groups: {first sequence, end, first item, keys}; items are numbered among the
+  // groups that have keys and sequences
+  int4 *groups = p.groups;
+  if (tid == 0) { sh.carry = 0; sh.top = 0; }
   __syncthreads();
-  const int most = p.max_prefix > 0x7fffffff / PAGE ? 0x7fffffff : p.max_prefix * PAGE;
-  // (tiles are numbered among the groups that have any keys)
   for (int base = 0; base < p.G; base += kSchedThreads) {
     const int g = base + tid;
     int b0 = 0, b1 = 0, n = 0;
-    bool bad = false;
     if (g < p.G) {
       b0 = p.offsets ? p.offsets[g] : 0;
       b1 = p.offsets ? p.offsets[g + 1] : p.B;
-      bad = b0 < 0 || b0 > b1 || b1 > p.B;
-      n = p.prefix_lens[g];
-      bad = bad || n < 0 || n > most;
-      n = min(max(n, 0), most);
-      if (bad) atomicOr(p.status, MLA_STATUS_BAD_SEQLEN);
+      if (b0 < 0 || b0 > b1 || b1 > p.B) atomicOr(p.status, MLA_STATUS_BAD_SEQLEN);
+      n = length(p.prefix_lens[g], p.max_prefix);
     }
-    // offsets out of order are pulled up to the largest before them
-    const int ceil1 = max(block_scan(min(max(max(b0, b1), 0), p.B), warp_sums, 0, [](int a, int b) { return max(a, b); }), top);
-    int before = __shfl_up_sync(0xffffffffu, ceil1, 1);
-    if ((tid & 31) == 31) warp_sums[tid >> 5] = ceil1;
+    // a group that begins before the end of an earlier one begins there
+    const int reach = max(block_scan(min(max(max(b0, b1), 0), p.B), sh.warp_sums, Max()), sh.top);
+    int before = __shfl_up_sync(0xffffffffu, reach, 1);
+    if ((tid & 31) == 31) sh.warp_sums[tid >> 5] = reach;
     __syncthreads();
-    if ((tid & 31) == 0) before = tid == 0 ? top : warp_sums[(tid >> 5) - 1];
+    if ((tid & 31) == 0) before = tid == 0 ? sh.top : sh.warp_sums[(tid >> 5) - 1];
     __syncthreads();
-    b0 = min(max(max(b0, before), 0), p.B);
-    b1 = max(min(max(b1, b0), p.B), b0);
-    const int rows = (b1 - b0) * TH;
-    const int tiles = g < p.G && n > 0 ? ceil_div(rows, M_TILE) : 0;
-    const int incl = block_scan(tiles, warp_sums, 0, [](int a, int b) { return a + b; });
-    const int first = carry + incl - tiles;
-    for (int t = 0; t < tiles; t++) {
-      p.tile_p[first + t] = make_int4(g, b0 * TH + t * M_TILE, min(M_TILE, rows - t * M_TILE), 0);
-      p.lens_p[first + t] = n;
+    b0 = min(max(b0, before), p.B);
+    b1 = max(min(b1, p.B), b0);
+    const int tiles = g < p.G && n > 0 ? ceil_div((b1 - b0) * TH, M_TILE) : 0;
+    const int incl = block_scan(tiles, sh.warp_sums, Add());
+    if (g < p.G) groups[g] = make_int4(b0, b1, sh.carry + incl - tiles, n);
+    __syncthreads();
+    if (tid == kSchedThreads - 1) {
+      sh.carry += incl;
+      sh.top = reach;
     }
-    if (tiles > 0)
-      for (int b = b0; b < b1; b++) p.seq[b] = make_int2(first, (b - b0) * TH);
-    __syncthreads();
-    if (tid == kSchedThreads - 1) { carry += incl; top = max(top, ceil1); }
     __syncthreads();
   }
-  const int n_tiles = carry;
+  const int n_prefix = sh.carry, n_items = n_prefix + (wide ? 0 : p.B * p.n_mt);
+  if (tid == 0) *p.n_prefix = n_prefix;
   __syncthreads();
-  for (int t = n_tiles + tid; t < p.n_pt; t += kSchedThreads) {
-    p.lens_p[t] = 0;
-    p.tile_p[t] = make_int4(-1, 0, 0, 0);
+  for (int b = tid; b < p.B; b += kSchedThreads) {
+    const int4 g = groups[last_le(p.G, b, [&](int i) { return i == 0 ? 0 : groups[i].x; })];
+    p.seq[b] = g.w > 0 && b >= g.x && b < g.y ? make_int2(g.z, (b - g.x) * TH) : make_int2(-1, 0);
   }
-  schedule(n_tiles, p.parts, p.md_p, p.ns_p, p.cnt_p, C, warp_sums, &carry,
-           [&](int i) { return ceil_div(p.lens_p[i], PAGE); });
-}
-
-// Block t: the query rows of prefix tile t side by side, and its group's pages.
-__global__ void __launch_bounds__(256) shared_pack_kernel(SharedParams p) {
-  grid_dep_trigger();
-  grid_dep_wait();
-  const int t = blockIdx.x;
-  const int4 tile = p.tile_p[t];
-  if (tile.x < 0) return;
-  const uint4 *src = reinterpret_cast<const uint4 *>(p.q) + (size_t)tile.y * (D_QK / 8);
-  uint4 *dst = reinterpret_cast<uint4 *>(p.q_p) + (size_t)t * M_TILE * (D_QK / 8);
-  for (int i = threadIdx.x; i < tile.z * (D_QK / 8); i += blockDim.x) dst[i] = src[i];
-  for (int j = threadIdx.x; j < p.max_prefix; j += blockDim.x) {
-    int page = p.prefix_table[(size_t)tile.x * p.max_prefix + j];
-    if (p.format != MLA_KV_BF16) {
-      if (page >= 0 && page < p.num_pages) page = tile.x * p.max_prefix + j;
-      else page = -1;
+  for (int i = tid; i < n_items; i += kSchedThreads) {
+    SharedItem it;
+    if (i < n_prefix) {
+      const int g = last_le(p.G, i, [&](int k) { return groups[k].z; });
+      const int4 at = groups[g];
+      const int row = (i - at.z) * M_TILE;
+      it = SharedItem{at.x * TH + row, min(M_TILE, (at.y - at.x) * TH - row), at.w, ceil_div(at.w, PAGE), g, 0, 0, 0};
+    } else {
+      const int b = (i - n_prefix) % p.B, mt = (i - n_prefix) / p.B, n = length(p.seqlens[b], p.max_pages);
+      it = SharedItem{b * TH + mt * M_TILE, min(M_TILE, TH - mt * M_TILE), n, ceil_div(own_keys(p, n, mt), PAGE), b, 1,
+                      mt * M_TILE, 0};
     }
-    p.table_p[(size_t)t * p.max_prefix + j] = page;
+    p.items[i] = it;
   }
+  __syncthreads();
+  schedule(sh, n_items, p.parts, 0, p.md, p.pieces, [&](int i) { return p.items[i].tiles; },
+           [&](int i, int at, int) { p.items[i].slot = at; });
 }
 
-// FP8 prefixes: page j of group g as bf16 rows, once for all its tiles.
+// FP8 prefixes: page j of group g as bf16 rows (zeros behind the last token), once for all the
+// group's tiles.  A warp a row: lane l widens 16 of its values, and lanes 0-3 or
+// 0-7 the rotated part.
 __global__ void __launch_bounds__(256) shared_widen_kernel(SharedParams p) {
   grid_dep_trigger();
   grid_dep_wait();
-  const int g = blockIdx.y;
-  const int n = min(p.prefix_lens[g], p.max_prefix * PAGE);
-  for (int j = blockIdx.x; j * PAGE < n; j += gridDim.x) {
+  const int g = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int n = (int)min((long long)max(p.prefix_lens[g], 0), (long long)p.max_prefix * PAGE);
+  const bool tensor = p.format == MLA_KV_FP8_E4M3_TENSOR;
+  const int row_bytes = tensor ? D_QK : FP8_ROW;
+  for (int j = blockIdx.x; (long long)j * PAGE < n; j += gridDim.x) {
     const int page = p.prefix_table[(size_t)g * p.max_prefix + j];
     if (page < 0 || page >= p.num_pages) continue;
-    __nv_bfloat16 *dst = reinterpret_cast<__nv_bfloat16 *>(p.scratch) + ((size_t)g * p.max_prefix + j) * PAGE * D_QK;
-    const bool tensor = p.format == MLA_KV_FP8_E4M3_TENSOR;
-    const int row_bytes = tensor ? D_QK : FP8_ROW;
-    for (int i = threadIdx.x; i < PAGE * D_QK; i += blockDim.x) {
-      const int r = i / D_QK, d = i % D_QK;
-      const uint8_t *src = p.cache + ((size_t)page * PAGE + r) * row_bytes;
-      float v = 0.f;
+    uint8_t *to = p.scratch + ((size_t)g * p.max_prefix + j) * PAGE * D_QK * 2;
+#pragma unroll 4
+    for (int r = warp; r < PAGE; r += 8) {
+      const size_t at = (size_t)page * PAGE + r;
+      const uint4 *src = reinterpret_cast<const uint4 *>(p.cache + at * row_bytes);
+      uint4 *dst = reinterpret_cast<uint4 *>(to + (size_t)r * D_QK * 2);
+      const uint4 zero = make_uint4(0, 0, 0, 0);
+      uint4 lo = zero, hi = zero;
       if (j * PAGE + r < n) {
-        if (d < D_V || tensor) {
-          const float s = tensor ? p.kv_scales[0] : p.kv_scales[((size_t)page * PAGE + r) * 4 + d / 128];
-          v = e4m3_to_float(src[d]) * s;
-        } else {
-          v = bf16_bits_to_float(reinterpret_cast<const uint16_t *>(src + D_V)[d - D_V]);
-        }
+        const float s = tensor ? p.kv_scales[0] : p.kv_scales[at * 4 + lane / 8];
+        widen16(__ldg(src + lane), s, lo, hi);
       }
-      dst[i] = __float2bfloat16_rn(v);
+      dst[2 * lane] = lo;
+      dst[2 * lane + 1] = hi;
+      if (tensor && lane < 4) {
+        lo = hi = zero;
+        if (j * PAGE + r < n) widen16(__ldg(src + 32 + lane), p.kv_scales[0], lo, hi);
+        dst[64 + 2 * lane] = lo;
+        dst[65 + 2 * lane] = hi;
+      } else if (!tensor && lane < 8) {
+        dst[64 + lane] = j * PAGE + r < n ? __ldg(src + 32 + lane) : zero;
+      }
     }
   }
 }
 
 // ---- join ------------------------------------------------------------------------
 
-constexpr int kWarps = 8, kChunks = 4;
+constexpr int kJoinWarps = 8;
 
 __device__ __forceinline__ void ld_cg_v8(float (&v)[8], const float *ptr) {
   uint32_t u[8];
@@ -264,101 +261,110 @@ __device__ __forceinline__ void ld_cg_v8(float (&v)[8], const float *ptr) {
   for (int j = 0; j < 8; j++) v[j] = __uint_as_float(u[j]);
 }
 
-// Lane: one query row; warp: 32 of its columns; block: 32 rows x 256 columns.
-__global__ void __launch_bounds__(kWarps * 32) shared_join_kernel(SharedParams p) {
-  grid_dep_wait();
+// Lane: a query row; warp: 8 of its columns (one chunk of the partials); block: 32
+// rows x 64 columns.  Rows side by side lie side by side in the partials, so a
+// warp reads 1 KB at once; four parts are on their way together.
+__global__ void __launch_bounds__(kJoinWarps * 32) shared_join_kernel(SharedParams p) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, TH = p.T * p.H;
-  const long long R = (long long)blockIdx.x * 32 + lane;
-  if (R >= (long long)p.B * TH) return;
-  const int b = (int)(R / TH), r = (int)(R % TH);
-  const int chunk0 = blockIdx.y * 32 + warp * kChunks;
-  const float *lse_part[2] = {nullptr, nullptr};
-  const float *o_part[2] = {nullptr, nullptr};
+  const int R = blockIdx.x * 32 + lane, chunk = blockIdx.y * kJoinWarps + warp;
+  const bool live = R < p.B * TH;
+  const int b = live ? R / TH : 0, r = live ? R % TH : 0;
+  const float *lse[2], *o[2];
   int n[2] = {0, 0};
-  const int2 s = p.seq[b];
-  if (s.x >= 0) {
-    const int row = s.y + r, i = s.x + row / M_TILE, at = row % M_TILE;
-    n[0] = p.cnt_p[i];
-    lse_part[0] = p.lse_p + (size_t)p.ns_p[i] * M_TILE + at;
-    o_part[0] = p.o_p + (((size_t)p.ns_p[i] * 64 + chunk0) * M_TILE + at) * 8;
+  // (the schedule was complete before the kernel before this one began its work)
+  if (live) {
+    const int2 s = p.seq[b];
+    if (s.x >= 0) {
+      const int row = s.y + r, i = s.x + row / M_TILE, slot = p.items[i].slot, at = row % M_TILE;
+      n[0] = p.pieces[i];
+      lse[0] = p.lse_p + (size_t)slot * M_TILE + at;
+      o[0] = p.o_p + (((size_t)slot * 64 + chunk) * M_TILE + at) * 8;
+    }
+    const int k = (r / M_TILE) * p.B + b, at = r % M_TILE;
+    const bool wide = p.format != MLA_KV_BF16;
+    const int i = wide ? k : *p.n_prefix + k, slot = wide ? p.ns_o[i] : p.items[i].slot;
+    n[1] = wide ? p.cnt_o[i] : p.pieces[i];
+    lse[1] = (wide ? p.lse_o : p.lse_p) + (size_t)slot * M_TILE + at;
+    o[1] = (wide ? p.o_o : p.o_p) + (((size_t)slot * 64 + chunk) * M_TILE + at) * 8;
   }
-  {
-    const int i = (r / M_TILE) * p.B + b, at = r % M_TILE;
-    n[1] = p.cnt_o[i];
-    lse_part[1] = p.lse_o + (size_t)p.ns_o[i] * M_TILE + at;
-    o_part[1] = p.o_o + (((size_t)p.ns_o[i] * 64 + chunk0) * M_TILE + at) * 8;
-  }
+  grid_dep_wait();
+  if (!live) return;
+  constexpr size_t kNext = (size_t)64 * M_TILE * 8;
   float m = -INFINITY;
+#pragma unroll
   for (int k = 0; k < 2; k++)
-    for (int j = 0; j < n[k]; j++) m = fmaxf(m, __ldcg(lse_part[k] + (size_t)j * M_TILE));
-  float acc[kChunks * 8], sum = 0.f;
+#pragma unroll 4
+    for (int j = 0; j < n[k]; j++) m = fmaxf(m, __ldcg(lse[k] + (size_t)j * M_TILE));
+  float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, sum = 0.f;
+  if (m != -INFINITY) {
 #pragma unroll
-  for (int k = 0; k < kChunks * 8; k++) acc[k] = 0.f;
-  if (m != -INFINITY)
     for (int k = 0; k < 2; k++)
-      for (int j = 0; j < n[k]; j++) {
-        const float l = __ldcg(lse_part[k] + (size_t)j * M_TILE);
-        const float w = l == -INFINITY ? 0.f : exp2f(l - m);
-        sum += w;
+      for (int j0 = 0; j0 < n[k]; j0 += 4) {
+        float v[4][8], l[4];
 #pragma unroll
-        for (int c = 0; c < kChunks; c++) {
-          float v[8];
-          ld_cg_v8(v, o_part[k] + ((size_t)j * 64 + c) * M_TILE * 8);
+        for (int j = 0; j < 4; j++) {
+          l[j] = -INFINITY;
+          if (j0 + j < n[k]) {
+            l[j] = __ldcg(lse[k] + (size_t)(j0 + j) * M_TILE);
+            ld_cg_v8(v[j], o[k] + (j0 + j) * kNext);
+          }
+        }
 #pragma unroll
-          for (int e = 0; e < 8; e++) acc[8 * c + e] = fmaf(w, v[e], acc[8 * c + e]);
+        for (int j = 0; j < 4; j++) {
+          if (l[j] == -INFINITY) continue;
+          const float w = exp2f(l[j] - m);
+          sum += w;
+#pragma unroll
+          for (int e = 0; e < 8; e++) acc[e] = fmaf(w, v[j][e], acc[e]);
         }
       }
-  const float inv = sum > 0.f ? 1.f / sum : 0.f;
-  uint4 *dst = reinterpret_cast<uint4 *>(p.out + R * D_V + chunk0 * 8);
-#pragma unroll
-  for (int c = 0; c < kChunks; c++) {
-    uint32_t w[4];
-#pragma unroll
-    for (int e = 0; e < 4; e++) {
-      __nv_bfloat162 v = __floats2bfloat162_rn(acc[8 * c + 2 * e] * inv, acc[8 * c + 2 * e + 1] * inv);
-      w[e] = *reinterpret_cast<uint32_t *>(&v);
-    }
-    dst[c] = make_uint4(w[0], w[1], w[2], w[3]);
   }
-  if (warp == 0 && blockIdx.y == 0)
+  const float inv = sum > 0.f ? 1.f / sum : 0.f;
+  uint32_t w[4];
+#pragma unroll
+  for (int e = 0; e < 4; e++) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+    w[e] = *reinterpret_cast<const uint32_t *>(&v);
+  }
+  reinterpret_cast<uint4 *>(p.out + (size_t)R * D_V)[chunk] = make_uint4(w[0], w[1], w[2], w[3]);
+  if (chunk == 0)
     p.lse[((size_t)b * p.H + r % p.H) * p.T + r / p.H] = sum > 0.f ? (m + log2f(sum)) * LN2 : -INFINITY;
 }
 
 // ---- host ------------------------------------------------------------------------
 
 struct Layout {
-  size_t md_p, ns_p, md_o, ns_o, cnt_p, cnt_o, lens_p, tile_p, table_p, lens_o, seq, q_p, scratch, lse_p, o_p, lse_o, o_o,
-      ring, total;
-  int n_pt, n_mt;
+  size_t items, md, pieces, n_prefix, groups, lens_o, seq, md_o, ns_o, cnt_o, scratch, lse_p, o_p, lse_o, o_o, ring, total;
+  int room, n_mt;
 };
 
 Layout layout(int B, int T, int H, int G, int format, int max_prefix, int parts) {
+  const bool wide = format != MLA_KV_BF16;
   Layout l;
-  l.n_pt = (int)(((long long)B * T * H + M_TILE - 1) / M_TILE) + G;
   l.n_mt = ceil_div(T * H, M_TILE);
-  const size_t n_ot = (size_t)B * l.n_mt;
+  const size_t own = (size_t)B * l.n_mt, prefix = ((size_t)B * T * H + M_TILE - 1) / M_TILE + G;
+  l.room = (int)(prefix + (wide ? 0 : own));
   size_t at = 0;
   auto take = [&](size_t bytes) {
     const size_t here = at;
     at = (at + bytes + 255) / 256 * 256;
     return here;
   };
-  const size_t slots_p = 2 * (size_t)l.n_pt + parts, slots_o = 2 * n_ot + parts, row = M_TILE * sizeof(float);
-  l.md_p = take((size_t)parts * MD_STRIDE * 4);
-  l.ns_p = take(((size_t)l.n_pt + 1) * 4);
-  l.md_o = take((size_t)parts * MD_STRIDE * 4);
-  l.ns_o = take((n_ot + 1) * 4);
-  l.cnt_p = take((size_t)l.n_pt * 4);
-  l.cnt_o = take(n_ot * 4);
-  l.lens_p = take((size_t)l.n_pt * 4);
-  l.tile_p = take((size_t)l.n_pt * sizeof(int4));
-  l.table_p = take((size_t)l.n_pt * max_prefix * 4);
+  // slots of results: one for each item, and one for each cut
+  const size_t slots = (size_t)l.room + parts, slots_o = wide ? 2 * own + parts : 0, row = M_TILE * sizeof(float);
+  l.items = take((size_t)l.room * sizeof(SharedItem));
+  l.md = take((size_t)parts * MD_STRIDE * 4);
+  l.pieces = take((size_t)l.room * 4);
+  l.n_prefix = take(4);
+  l.groups = take((size_t)G * sizeof(int4));
   l.lens_o = take((size_t)B * 4);
   l.seq = take((size_t)B * sizeof(int2));
-  l.q_p = take((size_t)l.n_pt * M_TILE * D_QK * 2);
-  l.scratch = take(format == MLA_KV_BF16 ? 0 : (size_t)G * max_prefix * PAGE * D_QK * 2);
-  l.lse_p = take(slots_p * row);
-  l.o_p = take(slots_p * row * D_V);
+  l.md_o = take(wide ? (size_t)parts * MD_STRIDE * 4 : 0);
+  l.ns_o = take(wide ? (own + 1) * 4 : 0);
+  l.cnt_o = take(wide ? own * 4 : 0);
+  l.scratch = take(wide ? (size_t)G * max_prefix * PAGE * D_QK * 2 : 0);
+  l.lse_p = take(slots * row);
+  l.o_p = take(slots * row * D_V);
   l.lse_o = take(slots_o * row);
   l.o_o = take(slots_o * row * D_V);
   l.ring = take((size_t)parts * P_RING * P_SLOT_BYTES);
@@ -383,9 +389,9 @@ int check_sizes(int B, int T, int H, int G, int format, int max_prefix) {
   }
   if (format != MLA_KV_BF16 && format != MLA_KV_FP8_E4M3 && format != MLA_KV_FP8_E4M3_TENSOR)
     return fail(MLA_ERR_INVALID_ARG, "kv_format unknown");
-  const long long own = (long long)B * ceil_div(T * H, M_TILE), shared = ((long long)B * T * H + M_TILE - 1) / M_TILE + G;
-  if (own > kMaxItems || shared > kMaxItems) {
-    snprintf(msg, sizeof msg, "%lld work items exceed the limit %d", own > shared ? own : shared, kMaxItems);
+  const long long items = (long long)B * ceil_div(T * H, M_TILE) + ((long long)B * T * H + M_TILE - 1) / M_TILE + G;
+  if (items > kMaxItems) {
+    snprintf(msg, sizeof msg, "%lld work items exceed the limit %d", items, kMaxItems);
     return fail(MLA_ERR_UNSUPPORTED, msg);
   }
   if ((long long)G * max_prefix > 0x7fffffffLL) return fail(MLA_ERR_UNSUPPORTED, "G * max_prefix_pages exceeds 2^31 - 1");
@@ -468,106 +474,79 @@ extern "C" int mla_decode_shared(const void *q, const void *kv_cache, int kv_for
   p.T = T;
   p.H = H;
   p.causal = causal;
-  p.n_pt = l.n_pt;
+  p.room = l.room;
   p.n_mt = l.n_mt;
   p.parts = parts;
-  p.md_p = reinterpret_cast<int32_t *>(at(l.md_p));
-  p.ns_p = reinterpret_cast<int32_t *>(at(l.ns_p));
-  p.md_o = reinterpret_cast<int32_t *>(at(l.md_o));
-  p.ns_o = reinterpret_cast<int32_t *>(at(l.ns_o));
-  p.cnt_p = reinterpret_cast<int32_t *>(at(l.cnt_p));
-  p.cnt_o = reinterpret_cast<int32_t *>(at(l.cnt_o));
-  p.lens_p = reinterpret_cast<int32_t *>(at(l.lens_p));
-  p.tile_p = reinterpret_cast<int4 *>(at(l.tile_p));
-  p.table_p = reinterpret_cast<int32_t *>(at(l.table_p));
+  p.scale_log2 = softmax_scale * LOG2E;
+  p.wait_ns = wait_limit_ns();
+  p.items = reinterpret_cast<SharedItem *>(at(l.items));
+  p.md = reinterpret_cast<int32_t *>(at(l.md));
+  p.pieces = reinterpret_cast<int32_t *>(at(l.pieces));
+  p.n_prefix = reinterpret_cast<int32_t *>(at(l.n_prefix));
+  p.groups = reinterpret_cast<int4 *>(at(l.groups));
   p.lens_o = reinterpret_cast<int32_t *>(at(l.lens_o));
   p.seq = reinterpret_cast<int2 *>(at(l.seq));
-  p.q_p = at(l.q_p);
+  p.md_o = reinterpret_cast<int32_t *>(at(l.md_o));
+  p.ns_o = reinterpret_cast<int32_t *>(at(l.ns_o));
+  p.cnt_o = reinterpret_cast<int32_t *>(at(l.cnt_o));
   p.scratch = at(l.scratch);
   p.lse_p = reinterpret_cast<float *>(at(l.lse_p));
   p.o_p = reinterpret_cast<float *>(at(l.o_p));
   p.lse_o = reinterpret_cast<float *>(at(l.lse_o));
   p.o_o = reinterpret_cast<float *>(at(l.o_o));
+  p.ring = at(l.ring);
   p.out = static_cast<__nv_bfloat16 *>(out);
   p.lse = lse;
-
-  DecodeParams own{};
-  own.q = p.q;
-  own.kv = p.cache;
-  own.kv_scales = kv_scales;
-  own.block_table = block_table;
-  own.seqlens = p.lens_o;
-  own.tile_md = p.md_o;
-  own.num_splits = p.ns_o;
-  own.ws_lse = p.lse_o;
-  own.ws_o = p.o_o;
-  own.ws_p = at(l.ring);
-  own.out = p.out;
-  own.lse = p.lse;
-  own.status = st;
-  own.kv_format = kv_format;
-  own.num_pages = num_pages;
-  own.max_pages = max_pages;
-  own.causal = causal;
-  own.B = B;
-  own.T = T;
-  own.H = H;
-  own.n_mt = l.n_mt;
-  own.n_items = B * l.n_mt;
-  own.num_parts = parts;
-  own.out_v8 = 0;
-  own.scale_log2 = softmax_scale * LOG2E;
-  own.wait_ns = wait_limit_ns();
-  own.help = kv_format != MLA_KV_BF16 && T * H <= 64 ? 1 : 0;
-
-  // (a tile of prefix rows is a sequence of one token and 128 heads)
-  DecodeParams pre = own;
-  pre.q = reinterpret_cast<const __nv_bfloat16 *>(p.q_p);
-  pre.kv = kv_format == MLA_KV_BF16 ? p.cache : p.scratch;
-  pre.block_table = p.table_p;
-  pre.seqlens = p.lens_p;
-  pre.tile_md = p.md_p;
-  pre.num_splits = p.ns_p;
-  pre.ws_lse = p.lse_p;
-  pre.ws_o = p.o_p;
-  pre.kv_format = MLA_KV_BF16;
-  pre.num_pages = kv_format == MLA_KV_BF16 ? num_pages : G * max_prefix_pages;
-  pre.max_pages = max_prefix_pages;
-  pre.causal = 0;
-  pre.B = l.n_pt;
-  pre.T = 1;
-  pre.H = M_TILE;
-  pre.n_mt = 1;
-  pre.n_items = l.n_pt;
-  pre.help = 0;
+  const bool wide = kv_format != MLA_KV_BF16;
 
   cudaStream_t s = (cudaStream_t)stream;
-  cudaError_t e = launch_dependent(shared_schedule_kernel, 2, kSchedThreads, 0, s, p);
-  if (e == cudaSuccess && kv_format != MLA_KV_BF16) {
-    cudaLaunchAttribute pdl[1];
-    pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    pdl[0].val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute pdl[1];
+  pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  pdl[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.blockDim = dim3(256);
+  cfg.stream = s;
+  cfg.attrs = pdl;
+  cfg.numAttrs = 1;
+  cudaError_t e = launch_dependent(shared_schedule_kernel, wide ? 2 : 1, kSchedThreads, 0, s, p);
+  if (e == cudaSuccess && wide) {
     cfg.gridDim = dim3(max_prefix_pages < 1024 ? max_prefix_pages : 1024, G);
-    cfg.blockDim = dim3(256);
-    cfg.stream = s;
-    cfg.attrs = pdl;
-    cfg.numAttrs = 1;
     e = cudaLaunchKernelEx(&cfg, shared_widen_kernel, p);
   }
-  if (e == cudaSuccess) e = launch_dependent(shared_pack_kernel, l.n_pt, 256, 0, s, p);
-  if (e == cudaSuccess) e = launch_decode(pre, s, nullptr, nullptr);
-  if (e == cudaSuccess) e = launch_decode(own, s, nullptr, nullptr);
+  if (e == cudaSuccess) e = launch_shared_attention(p, s);
+  if (e == cudaSuccess && wide) {
+    // own FP8 rows go through the decode kernel, which gathers and widens them
+    DecodeParams d{};
+    d.q = p.q;
+    d.kv = p.cache;
+    d.kv_scales = kv_scales;
+    d.block_table = block_table;
+    d.seqlens = p.lens_o;
+    d.tile_md = p.md_o;
+    d.num_splits = p.ns_o;
+    d.ws_lse = p.lse_o;
+    d.ws_o = p.o_o;
+    d.ws_p = p.ring;
+    d.out = p.out;  // (it writes the zeros of empty sequences; the join writes every row after it)
+    d.lse = p.lse;
+    d.status = st;
+    d.kv_format = kv_format;
+    d.num_pages = num_pages;
+    d.max_pages = max_pages;
+    d.causal = causal;
+    d.B = B;
+    d.T = T;
+    d.H = H;
+    d.n_mt = l.n_mt;
+    d.n_items = B * l.n_mt;
+    d.num_parts = parts;
+    d.scale_log2 = p.scale_log2;
+    d.wait_ns = p.wait_ns;
+    d.help = T * H <= 64 ? 1 : 0;
+    e = launch_decode(d, s, nullptr, nullptr);
+  }
   if (e == cudaSuccess) {
-    cudaLaunchAttribute pdl[1];
-    pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    pdl[0].val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(((long long)B * T * H + 31) / 32), 2);
-    cfg.blockDim = dim3(kWarps * 32);
-    cfg.stream = s;
-    cfg.attrs = pdl;
-    cfg.numAttrs = 1;
+    cfg.gridDim = dim3((unsigned)(((long long)B * T * H + 31) / 32), 64 / kJoinWarps);
     e = cudaLaunchKernelEx(&cfg, shared_join_kernel, p);
   }
   if (e != cudaSuccess) {
