@@ -134,7 +134,9 @@ def _load_fast(L) -> None:
     except (ImportError, OSError):  # (no sources to compare with, or a file that does not load)
         return
     m.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
-        L.mla_kv_insert_rope, L.mla_kv_expand, L.mla_prefill, L.mla_prefill_workspace_bytes, L.mla_value_project)))
+        L.mla_kv_insert_rope, L.mla_kv_expand, L.mla_prefill, L.mla_prefill_workspace_bytes, L.mla_value_project,
+        L.mla_decode_shared, L.mla_decode_shared_workspace_bytes, L.mla_attention_mass, L.mla_attention_mass_workspace_bytes,
+        L.mla_evict, L.mla_evict_workspace_bytes)))
     _fast = m
 
 
@@ -722,6 +724,11 @@ def decode_shared(q: torch.Tensor, kv_cache: torch.Tensor, prefix_table: torch.T
     tokens, which follow its prefix; causal applies to them.  The other
     arguments are decode()'s.  workspace: at least
     decode_shared_workspace_bytes() bytes (allocated here when not given)."""
+    if _fast is not None:
+        r = _fast.decode_shared(q, kv_cache, prefix_table, prefix_lens, block_table, cache_seqlens, softmax_scale,
+                                group_offsets, causal, kv_scales, workspace, out, lse)
+        if r is not None:
+            return r if type(r) is tuple else _check(r)
     dev, B, T, H, fmt, _ = _decode_args(q, kv_cache, block_table, cache_seqlens, None, kv_scales)
     if fmt == KV_FP8_E4M3 and tuple(kv_scales.shape) != (kv_cache.shape[0], PAGE_SIZE, 4):
         raise ValueError(f"kv_scales must be [{kv_cache.shape[0]}, {PAGE_SIZE}, 4], got {list(kv_scales.shape)}")
@@ -789,6 +796,13 @@ def attention_mass(q: torch.Tensor, kv_cache: torch.Tensor, block_table: torch.T
     decode()'s, but T may be any number of tokens.  workspace: at least
     attention_mass_workspace_bytes() bytes (allocated here where it is needed
     and not given)."""
+    if _fast is not None:
+        r = _fast.attention_mass(q, kv_cache, block_table, cache_seqlens, lse, mass, softmax_scale, causal, decay,
+                                 kv_scales, workspace)
+        if r is not None:
+            if r is not True:
+                _check(r)
+            return mass
     dev, B, T, H, fmt, _ = _decode_args(q, kv_cache, block_table, cache_seqlens, None, kv_scales)
     if fmt == KV_FP8_E4M3 and tuple(kv_scales.shape) != (kv_cache.shape[0], PAGE_SIZE, 4):
         raise ValueError(f"kv_scales must be [{kv_cache.shape[0]}, {PAGE_SIZE}, 4], got {list(kv_scales.shape)}")
@@ -831,6 +845,11 @@ def evict(kv_cache: torch.Tensor, block_table: torch.Tensor, cache_seqlens: torc
     two sequences.  out_seqlens: where the lengths go (default: a new tensor;
     cache_seqlens itself will do).  workspace: at least evict_workspace_bytes()
     bytes (allocated here when not given)."""
+    if _fast is not None:
+        r = _fast.evict(kv_cache, block_table, cache_seqlens, mass, positions, keep, sinks, recent, kv_scales,
+                        out_seqlens, workspace)
+        if r is not None:
+            return _check(r) if type(r) is int else r
     if not isinstance(kv_cache, torch.Tensor):
         raise TypeError("kv_cache must be a torch.Tensor")
     fmt = _cache_format(kv_cache, kv_scales)

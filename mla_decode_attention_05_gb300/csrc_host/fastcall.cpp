@@ -25,6 +25,12 @@ decltype(&mla_kv_expand) expand_fn;
 decltype(&mla_prefill) prefill_fn;
 decltype(&mla_prefill_workspace_bytes) prefill_ws_fn;
 decltype(&mla_value_project) value_fn;
+decltype(&mla_decode_shared) shared_fn;
+decltype(&mla_decode_shared_workspace_bytes) shared_ws_fn;
+decltype(&mla_attention_mass) mass_fn;
+decltype(&mla_attention_mass_workspace_bytes) mass_ws_fn;
+decltype(&mla_evict) evict_fn;
+decltype(&mla_evict_workspace_bytes) evict_ws_fn;
 
 // A plain tensor, or null.
 const at::Tensor *tensor(PyObject *o) { return THPVariable_CheckExact(o) ? &THPVariable_Unpack(o) : nullptr; }
@@ -79,6 +85,14 @@ struct Unlocked {
 
 PyObject *none() { Py_RETURN_NONE; }
 PyObject *code(int rc) { return PyLong_FromLong(rc); }
+
+PyObject *pair(const at::Tensor &x, const at::Tensor &y) {
+  PyObject *a = THPVariable_Wrap(x), *b = THPVariable_Wrap(y);
+  PyObject *r = a && b ? PyTuple_Pack(2, a, b) : nullptr;
+  Py_XDECREF(a);
+  Py_XDECREF(b);
+  return r;
+}
 
 // value_project(attn, w_uv, out | None) -> out
 PyObject *value_project(PyObject *, PyObject *const *args, Py_ssize_t n) {
@@ -145,12 +159,7 @@ PyObject *prefill(PyObject *, PyObject *const *args, Py_ssize_t n) {
                     room.defined() ? room.data_ptr() : nullptr, bytes, out.data_ptr(), lse.data_ptr<float>(),
                     stream_of(dev));
   }
-  if (rc < 0) return code(rc);
-  PyObject *a = THPVariable_Wrap(out), *b = THPVariable_Wrap(lse);
-  PyObject *r = a && b ? PyTuple_Pack(2, a, b) : nullptr;
-  Py_XDECREF(a);
-  Py_XDECREF(b);
-  return r;
+  return rc < 0 ? code(rc) : pair(out, lse);
 }
 
 // kv_expand(cache, block_table, cu, w_uk, w_uv, total, scales | None, kv | None, k_pe | None) -> (kv, k_pe)
@@ -190,12 +199,7 @@ PyObject *kv_expand(PyObject *, PyObject *const *args, Py_ssize_t n) {
                    uk->data_ptr(), uk_row, uk_head, uv->data_ptr(), uv_row, uv_head, (int)H, kv.data_ptr(),
                    pe.data_ptr(), stream_of(dev));
   }
-  if (rc < 0) return code(rc);
-  PyObject *a = THPVariable_Wrap(kv), *b = THPVariable_Wrap(pe);
-  PyObject *r = a && b ? PyTuple_Pack(2, a, b) : nullptr;
-  Py_XDECREF(a);
-  Py_XDECREF(b);
-  return r;
+  return rc < 0 ? code(rc) : pair(kv, pe);
 }
 
 // kv_insert_rope(kv_c, k_pe, w_kva, slots, cache, eps, positions, cos_sin, interleaved, q_pe | None, q_out | None,
@@ -262,6 +266,154 @@ PyObject *kv_insert_rope(PyObject *, PyObject *const *args, Py_ssize_t n) {
   Py_RETURN_TRUE;
 }
 
+// A paged cache with its scales, page table and lengths, as the decode takes them.
+struct Paged {
+  const at::Tensor *cache, *table, *lens, *scales;
+  int dev, format, pages, page, width;
+  int64_t B;
+};
+
+bool paged(PyObject *cache, PyObject *table, PyObject *lens, PyObject *scales, Paged &c) {
+  c.cache = tensor(cache), c.table = tensor(table), c.lens = tensor(lens);
+  if (!c.cache || !c.cache->is_cuda() || !optional(scales, c.scales)) return false;
+  c.dev = c.cache->get_device();
+  c.format = format_of(*c.cache);
+  if (c.dev != c10::cuda::current_device() || c.format < 0 || !c.cache->is_contiguous() ||
+      !whole(c.table, c.dev, at::kInt, 2) || !whole(c.lens, c.dev, at::kInt, 1))
+    return false;
+  c.B = c.table->size(0);
+  if (c.lens->size(0) != c.B || c.B > kMostInt || c.table->size(1) > kMostInt || c.cache->size(0) > kMostInt ||
+      c.cache->size(1) > kMostInt)
+    return false;
+  c.pages = (int)c.cache->size(0), c.page = (int)c.cache->size(1), c.width = (int)c.table->size(1);
+  if (c.format == MLA_KV_FP8_E4M3)
+    return whole(c.scales, c.dev, at::kFloat, 3) && sized(*c.scales, {c.cache->size(0), 64, 4});
+  if (c.format == MLA_KV_FP8_E4M3_TENSOR)
+    return on(c.scales, c.dev) && c.scales->scalar_type() == at::kFloat && c.scales->is_contiguous() && c.scales->numel() == 1;
+  c.scales = nullptr;
+  return true;
+}
+
+bool queries(const at::Tensor *q, const Paged &c, int64_t &T, int64_t &H) {
+  if (!whole(q, c.dev, at::kBFloat16, 4) || q->size(0) != c.B || q->size(3) != 576) return false;
+  T = q->size(1), H = q->size(2);
+  return T <= kMostInt && H <= kMostInt;
+}
+
+float *scales_of(const Paged &c) { return c.scales ? c.scales->data_ptr<float>() : nullptr; }
+
+bool whole_number(PyObject *o, int &v) {
+  if (!PyLong_CheckExact(o)) return false;
+  int overflow = 0;
+  const long n = PyLong_AsLongAndOverflow(o, &overflow);
+  v = (int)n;
+  return !overflow && n >= -kMostInt && n <= kMostInt;
+}
+
+// A given workspace, or a new one of `bytes` (none for 0).
+bool given_space(const at::Tensor *space, int dev) { return !space || (on(space, dev) && space->is_contiguous()); }
+
+void *make_space(const at::Tensor *space, const at::Tensor &like, size_t &bytes, at::Tensor &room) {
+  if (space) {
+    room = *space;
+    bytes = space->nbytes();
+  } else if (bytes) {
+    room = at::empty({(int64_t)bytes}, like.options().dtype(at::kByte));
+  }
+  return room.defined() ? room.data_ptr() : nullptr;
+}
+
+// decode_shared(q, cache, prefix_table, prefix_lens, table, lens, scale, offsets | None, causal, scales | None,
+//               workspace | None, out | None, lse | None) -> (out, lse)
+PyObject *decode_shared(PyObject *, PyObject *const *args, Py_ssize_t n) {
+  if (n != 13 || !shared_fn || !PyFloat_CheckExact(args[6]) || !PyBool_Check(args[8])) return none();
+  const at::Tensor *q = tensor(args[0]), *pt = tensor(args[2]), *pl = tensor(args[3]), *off, *space, *out_given, *lse_given;
+  Paged c;
+  int64_t T, H;
+  if (!q || !optional(args[7], off) || !optional(args[10], space) || !optional(args[11], out_given) ||
+      !optional(args[12], lse_given) || !paged(args[1], args[4], args[5], args[9], c) || !queries(q, c, T, H))
+    return none();
+  if (!whole(pt, c.dev, at::kInt, 2) || !whole(pl, c.dev, at::kInt, 1) || pl->size(0) != pt->size(0) ||
+      pt->size(0) > kMostInt || pt->size(1) > kMostInt || !given_space(space, c.dev))
+    return none();
+  const int64_t G = pt->size(0);
+  if (off ? !whole(off, c.dev, at::kInt, 1) || off->size(0) != G + 1 : G != 1) return none();
+  if (out_given && (!whole(out_given, c.dev, at::kBFloat16, 4) || !sized(*out_given, {c.B, T, H, 512}))) return none();
+  if (lse_given && (!whole(lse_given, c.dev, at::kFloat, 3) || !sized(*lse_given, {c.B, H, T}))) return none();
+  const float scale = (float)PyFloat_AS_DOUBLE(args[6]);
+  const int causal = args[8] == Py_True ? 1 : 0;
+  at::Tensor out, lse, room;
+  int rc;
+  {
+    Unlocked others;
+    size_t bytes = shared_ws_fn((int)c.B, (int)T, (int)H, (int)G, c.format, (int)pt->size(1));  // (0: refused below)
+    out = out_given ? *out_given : at::empty({c.B, T, H, 512}, q->options());
+    lse = lse_given ? *lse_given : at::empty({c.B, H, T}, q->options().dtype(at::kFloat));
+    void *at = make_space(space, *q, bytes, room);
+    rc = shared_fn(q->data_ptr(), c.cache->data_ptr(), c.format, c.pages, c.page, pt->data_ptr<int32_t>(), (int)pt->size(1),
+                   pl->data_ptr<int32_t>(), off ? off->data_ptr<int32_t>() : nullptr, (int)G, c.table->data_ptr<int32_t>(),
+                   c.width, c.lens->data_ptr<int32_t>(), scales_of(c), scale, causal, at, bytes, out.data_ptr(),
+                   lse.data_ptr<float>(), (int)c.B, (int)T, (int)H, stream_of(c.dev));
+  }
+  return rc < 0 ? code(rc) : pair(out, lse);
+}
+
+// attention_mass(q, cache, table, lens, lse, mass, scale, causal, decay, scales | None, workspace | None) -> True
+PyObject *attention_mass(PyObject *, PyObject *const *args, Py_ssize_t n) {
+  if (n != 11 || !mass_fn || !PyFloat_CheckExact(args[6]) || !PyBool_Check(args[7]) || !PyFloat_CheckExact(args[8]))
+    return none();
+  const at::Tensor *q = tensor(args[0]), *lse = tensor(args[4]), *mass = tensor(args[5]), *space;
+  Paged c;
+  int64_t T, H;
+  if (!q || !optional(args[10], space) || !paged(args[1], args[2], args[3], args[9], c) || !queries(q, c, T, H) ||
+      !whole(lse, c.dev, at::kFloat, 3) || !sized(*lse, {c.B, H, T}) || !whole(mass, c.dev, at::kFloat, 2) ||
+      mass->size(0) != c.B || mass->size(1) > kMostInt || !given_space(space, c.dev))
+    return none();
+  const int cap = (int)mass->size(1);
+  at::Tensor room;
+  int rc;
+  {
+    Unlocked others;
+    size_t bytes = mass_ws_fn((int)c.B, (int)T, (int)H, cap);
+    void *at = make_space(space, *q, bytes, room);
+    rc = mass_fn(q->data_ptr(), c.cache->data_ptr(), c.format, c.pages, c.page, c.table->data_ptr<int32_t>(), c.width,
+                 c.lens->data_ptr<int32_t>(), scales_of(c), lse->data_ptr<float>(), (float)PyFloat_AS_DOUBLE(args[6]),
+                 args[7] == Py_True ? 1 : 0, (float)PyFloat_AS_DOUBLE(args[8]), mass->data_ptr<float>(), cap, at, bytes,
+                 (int)c.B, (int)T, (int)H, stream_of(c.dev));
+  }
+  if (rc < 0) return code(rc);
+  Py_RETURN_TRUE;
+}
+
+// evict(cache, table, lens, mass, positions, keep, sinks, recent, scales | None, out_lens | None, workspace | None)
+//   -> new lengths
+PyObject *evict(PyObject *, PyObject *const *args, Py_ssize_t n) {
+  if (n != 11 || !evict_fn) return none();
+  const at::Tensor *mass = tensor(args[3]), *pos = tensor(args[4]), *given, *space;
+  Paged c;
+  int keep, sinks, recent;
+  if (!optional(args[9], given) || !optional(args[10], space) || !paged(args[0], args[1], args[2], args[8], c) ||
+      !whole(mass, c.dev, at::kFloat, 2) || mass->size(0) != c.B || mass->size(1) > kMostInt ||
+      !whole(pos, c.dev, at::kInt, 2) || pos->sizes() != mass->sizes() || !whole_number(args[5], keep) ||
+      !whole_number(args[6], sinks) || !whole_number(args[7], recent) || !given_space(space, c.dev))
+    return none();
+  if (given && (!whole(given, c.dev, at::kInt, 1) || given->size(0) != c.B)) return none();
+  const int cap = (int)mass->size(1);
+  at::Tensor lens, room;
+  int rc;
+  {
+    Unlocked others;
+    size_t bytes = evict_ws_fn((int)c.B, cap, keep);  // (0: refused below)
+    lens = given ? *given : at::empty({c.B}, c.lens->options());
+    void *at = make_space(space, *c.cache, bytes, room);
+    rc = evict_fn(c.cache->data_ptr(), c.format, c.pages, c.page, c.table->data_ptr<int32_t>(), c.width,
+                  c.lens->data_ptr<int32_t>(), c.format == MLA_KV_FP8_E4M3 ? scales_of(c) : nullptr, mass->data_ptr<float>(),
+                  pos->data_ptr<int32_t>(), cap, keep, sinks, recent, lens.data_ptr<int32_t>(), at, bytes, (int)c.B,
+                  stream_of(c.dev));
+  }
+  return rc < 0 ? code(rc) : THPVariable_Wrap(lens);
+}
+
 // C++ exceptions (an allocation that failed, say) become Python's.
 template <PyObject *(*F)(PyObject *, PyObject *const *, Py_ssize_t)>
 PyObject *guarded(PyObject *self, PyObject *const *args, Py_ssize_t n) {
@@ -276,14 +428,15 @@ PyObject *guarded(PyObject *self, PyObject *const *args, Py_ssize_t n) {
   }
 }
 
-// bind(addresses of the library's functions, in this order)
+// bind(addresses of the library's functions, in this order): the first five, or all.
 PyObject *bind(PyObject *, PyObject *const *args, Py_ssize_t n) {
-  void *at[5];
-  if (n != 5) {
-    PyErr_SetString(PyExc_TypeError, "bind takes five addresses");
+  constexpr int kAll = 11;
+  void *at[kAll];
+  if (n != 5 && n != kAll) {
+    PyErr_SetString(PyExc_TypeError, "bind takes five or eleven addresses");
     return nullptr;
   }
-  for (int i = 0; i < 5; i++) {
+  for (int i = 0; i < n; i++) {
     at[i] = PyLong_AsVoidPtr(args[i]);
     if (!at[i]) {
       if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "null address");
@@ -295,12 +448,21 @@ PyObject *bind(PyObject *, PyObject *const *args, Py_ssize_t n) {
   prefill_fn = reinterpret_cast<decltype(prefill_fn)>(at[2]);
   prefill_ws_fn = reinterpret_cast<decltype(prefill_ws_fn)>(at[3]);
   value_fn = reinterpret_cast<decltype(value_fn)>(at[4]);
+  if (n == kAll) {
+    shared_fn = reinterpret_cast<decltype(shared_fn)>(at[5]);
+    shared_ws_fn = reinterpret_cast<decltype(shared_ws_fn)>(at[6]);
+    mass_fn = reinterpret_cast<decltype(mass_fn)>(at[7]);
+    mass_ws_fn = reinterpret_cast<decltype(mass_ws_fn)>(at[8]);
+    evict_fn = reinterpret_cast<decltype(evict_fn)>(at[9]);
+    evict_ws_fn = reinterpret_cast<decltype(evict_ws_fn)>(at[10]);
+  }
   Py_RETURN_NONE;
 }
 
 #define FAST(f) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(guarded<f>)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {
-    FAST(value_project), FAST(prefill), FAST(kv_expand), FAST(kv_insert_rope),
+    FAST(value_project), FAST(prefill), FAST(kv_expand), FAST(kv_insert_rope), FAST(decode_shared), FAST(attention_mass),
+    FAST(evict),
     {"bind", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(bind)), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "fastcall", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
