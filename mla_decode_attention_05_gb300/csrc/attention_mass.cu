@@ -27,11 +27,21 @@ constexpr int kRows = 128;                     // query rows of a tile
 constexpr int kBlocks = D_QK / 64;             // blocks of 64 of the 576 dims
 constexpr uint32_t kBlock = kKeys * 128;       // 128 rows x 64 dims, 128-byte swizzle
 constexpr uint32_t kHalf = kBlock / 2;
-constexpr int kSlots = 4;
 constexpr int kD = 4;                          // score tiles in tensor memory
 constexpr int kWideWarps = 8;                  // FP8: warps that widen cached rows
+constexpr int kWideGroups = 2;
+constexpr int kRaw = 5;                        // FP8: blocks as they lie in the cache, on their way or being widened
+constexpr uint32_t kRawBlock = kKeys * 64;     // 128 rows x 64 bytes
+constexpr uint32_t kRawHalf = kRawBlock / 2;
+// The streaming operand's ring; FP8 gives half of it to the raw blocks.
+__host__ __device__ constexpr int slots_of(bool fp8) { return fp8 ? 2 : 4; }
+constexpr int kMostSlots = 4;
 constexpr uint32_t OFF_SLOTS = kBlocks * kBlock;
-constexpr uint32_t OFF_BARS = OFF_SLOTS + kSlots * kBlock;
+constexpr uint32_t OFF_RAW = OFF_SLOTS + 2 * kBlock;
+constexpr uint32_t OFF_SCALES = OFF_RAW + kRaw * kRawBlock;  // two tiles' scales, [128][4]
+constexpr uint32_t kScaleBytes = kKeys * 16;
+constexpr uint32_t OFF_BARS = OFF_SLOTS + 5 * kBlock;
+static_assert(OFF_SCALES + 2 * kScaleBytes <= OFF_BARS, "shared memory map");
 __host__ __device__ constexpr int threads_of(bool fp8) { return fp8 ? 256 + 32 * kWideWarps : 256; }
 
 struct MassParams {
@@ -52,7 +62,8 @@ struct MassParams {
 
 struct Bars {
   uint64_t res_full[kBlocks], res_empty[kBlocks];
-  uint64_t slot_full[kSlots], slot_empty[kSlots];
+  uint64_t slot_full[kMostSlots], slot_empty[kMostSlots];
+  uint64_t raw_full[kRaw], raw_empty[kRaw];
   uint64_t d_full[kD], d_empty[kD];
   float nl2[2][kRows];  // -lse * log2(e) of a tile's query rows
   int lim[2][kRows];    // keys that a row sees; 0 for one that is no row, or has no weight to give
@@ -63,6 +74,13 @@ struct Bars {
 };
 constexpr uint32_t kSmem = OFF_BARS + sizeof(Bars);
 static_assert(kSmem <= 232448, "shared memory budget");
+
+// `bytes` (a multiple of 16) side by side into shared memory.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bar)
+               : "memory");
+}
 
 __device__ __forceinline__ int seq_len(const MassParams &p, int b) {
   const int most = (int)min((long long)p.max_pages * PAGE, (long long)p.cap);
@@ -187,21 +205,26 @@ __device__ __forceinline__ int page_of(const MassParams &p, int b, int j, int le
 
 // ---- loads -------------------------------------------------------------------------
 
-// Warp 0: query rows, and the pages of a bf16 cache.  The whole warp waits and
-// looks pages up, one elected lane asks for the copies.
+// Warp 0: query rows, the pages of a bf16 cache, and the raw blocks of an FP8 one
+// (64 bytes of each row; ten of them where the rotated part is bf16).  The whole
+// warp waits and looks pages up, one elected lane asks for the copies.
 template <bool kStreamKeys, bool kFp8, bool kPoll>
 __device__ void load_role(const MassParams &p, uint8_t *base, Bars &br, const CUtensorMap *k_map, const CUtensorMap *q_map,
                           const Work &w) {
+  constexpr int kSlots = slots_of(kFp8);
   const uint32_t res = smem_u32(base), slots = smem_u32(base + OFF_SLOTS);
+  const uint32_t raws = smem_u32(base + OFF_RAW), scales = smem_u32(base + OFF_SCALES);
   const uint64_t keep = policy_evict_normal(), pass = policy_evict_first();
-  uint32_t s = 0, ph = 1, rph = 1;
+  const uint64_t key_pol = kStreamKeys ? pass : keep;
+  const bool scaled = p.format == MLA_KV_FP8_E4M3;
+  const int n_raw = scaled ? 10 : 9;
+  uint32_t s = 0, ph = 1, rph = 1, rs = 0, rawph = 1, tile = 0;
   auto keys = [&](uint32_t dst, uint64_t *full, int pg0, int pg1, int kb) {
     if (!elect_one()) return;
     const uint32_t bar = smem_u32(full);
     mbar_arrive_expect_tx(bar, (pg0 >= 0 ? kHalf : 0) + (pg1 >= 0 ? kHalf : 0));
-    const uint64_t pol = kStreamKeys ? pass : keep;
-    if (pg0 >= 0) tma_load_4d(dst, k_map, bar, 0, 0, kb, pg0, pol);
-    if (pg1 >= 0) tma_load_4d(dst + kHalf, k_map, bar, 0, 0, kb, pg1, pol);
+    if (pg0 >= 0) tma_load_4d(dst, k_map, bar, 0, 0, kb, pg0, key_pol);
+    if (pg1 >= 0) tma_load_4d(dst + kHalf, k_map, bar, 0, 0, kb, pg1, key_pol);
   };
   auto rows = [&](uint32_t dst, uint64_t *full, int b, int qt, int kb) {
     if (!elect_one()) return;
@@ -209,10 +232,38 @@ __device__ void load_role(const MassParams &p, uint8_t *base, Bars &br, const CU
     mbar_arrive_expect_tx(bar, p.box * 128);
     tma_load_3d(dst, q_map, bar, 0, b * p.rows + qt * kRows, kb, keep);
   };
+  // an FP8 tile's raw blocks and, with the first, its scales
+  auto raw_tile = [&](int pg0, int pg1) {
+    const uint32_t n = (pg0 >= 0) + (pg1 >= 0);
+    for (int k = 0; k < n_raw; k++) {
+      if (!warp_wait<kPoll>(&br, &br.raw_empty[rs], rawph, p)) return false;
+      if (elect_one()) {
+        const uint32_t bar = smem_u32(&br.raw_full[rs]), dst = raws + rs * kRawBlock;
+        const bool with = scaled && k == 0;
+        mbar_arrive_expect_tx(bar, n * (kRawHalf + (with ? kScaleBytes / 2 : 0)));
+#pragma unroll
+        for (int h = 0; h < 2; h++) {
+          const int pg = h ? pg1 : pg0;
+          if (pg < 0) continue;
+          tma_load_3d(dst + h * kRawHalf, k_map, bar, k * 64, 0, pg, key_pol);
+          if (with)
+            bulk_load(scales + (tile & 1) * kScaleBytes + h * (kScaleBytes / 2), p.kv_scales + (size_t)pg * PAGE * 4,
+                      kScaleBytes / 2, bar);
+        }
+      }
+      __syncwarp();
+      if (++rs == kRaw) {
+        rs = 0;
+        rawph ^= 1;
+      }
+    }
+    tile++;
+    return true;
+  };
   for_each_phase<kStreamKeys>(p, w, [&](const Phase &f) {
     if (f.i0 >= f.i1) return true;
     int pg0 = -1, pg1 = -1;
-    if (!kStreamKeys && !kFp8) {
+    if (!kStreamKeys) {
       pg0 = page_of(p, f.b, 2 * f.t, f.len);
       pg1 = page_of(p, f.b, 2 * f.t + 1, f.len);
     }
@@ -224,21 +275,26 @@ __device__ void load_role(const MassParams &p, uint8_t *base, Bars &br, const CU
         __syncwarp();
       }
       rph ^= 1;
+    } else if (!raw_tile(pg0, pg1)) {
+      return false;
     }
-    if (kStreamKeys && kFp8) return true;
     for (int i = f.i0; i < f.i1; i++) {
       if (kStreamKeys) {
         pg0 = page_of(p, f.b, 2 * i, f.len);
         pg1 = page_of(p, f.b, 2 * i + 1, f.len);
       }
-      for (int kb = 0; kb < kBlocks; kb++) {
-        if (!warp_wait<kPoll>(&br, &br.slot_empty[s], ph, p)) return false;
-        if (kStreamKeys) keys(slots + s * kBlock, &br.slot_full[s], pg0, pg1, kb);
-        else rows(slots + s * kBlock, &br.slot_full[s], f.b, i, kb);
-        __syncwarp();
-        if (++s == kSlots) {
-          s = 0;
-          ph ^= 1;
+      if constexpr (kStreamKeys && kFp8) {
+        if (!raw_tile(pg0, pg1)) return false;
+      } else {
+        for (int kb = 0; kb < kBlocks; kb++) {
+          if (!warp_wait<kPoll>(&br, &br.slot_empty[s], ph, p)) return false;
+          if (kStreamKeys) keys(slots + s * kBlock, &br.slot_full[s], pg0, pg1, kb);
+          else rows(slots + s * kBlock, &br.slot_full[s], f.b, i, kb);
+          __syncwarp();
+          if (++s == kSlots) {
+            s = 0;
+            ph ^= 1;
+          }
         }
       }
     }
@@ -246,111 +302,83 @@ __device__ void load_role(const MassParams &p, uint8_t *base, Bars &br, const CU
   });
 }
 
-// FP8 rows: thread i of 256 widens 16 bytes of rows i / 4 and i / 4 + 64 (the
-// tile's two pages) of each block; the raw bytes of the next tile's block are
-// asked for when the current one's have been used.
-struct RawTile {
-  uint4 v[2][kBlocks + 1];
-  float4 sc[2];
-  const uint8_t *row[2];
-};
+__device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+  return v;
+}
 
+__device__ __forceinline__ void st_shared_v4(uint32_t addr, const uint4 &v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
+// Warps 8-15 widen FP8 rows, in two groups that take the blocks in turn: thread i of
+// a group has 16 bytes of rows i / 4 + 32 k.  (The raw blocks come by TMA: a load of its own in flight
+// would hold up the thread's proxy fences.)
 template <bool kStreamKeys, bool kPoll>
-__device__ void widen_role(const MassParams &p, uint8_t *base, Bars &br, const Work &w, int i) {
-  const uint32_t res = smem_u32(base), slots = smem_u32(base + OFF_SLOTS);
-  const int r = i >> 2, c = i & 3;
-  const bool tensor = p.format == MLA_KV_FP8_E4M3_TENSOR;
-  const int row_bytes = tensor ? D_QK : FP8_ROW;
-  RawTile raw;
-  auto point = [&](int b, int t, int len) {
+__device__ void widen_role(const MassParams &p, uint8_t *base, Bars &br, const Work &w, int thread) {
+  constexpr int kSlots = slots_of(true);
+  static_assert(kSlots == kWideGroups, "a group has a slot of its own");
+  const uint32_t res = smem_u32(base), slots = smem_u32(base + OFF_SLOTS), raws = smem_u32(base + OFF_RAW);
+  const int group = thread / (32 * kWideWarps / kWideGroups), i = thread % (32 * kWideWarps / kWideGroups);
+  const int r = i >> 2, c = i & 3, x = r & 7;
+  const bool first = (threadIdx.x & 31) == 0, scaled = p.format == MLA_KV_FP8_E4M3;
+  const float one = scaled ? 0.f : __ldg(p.kv_scales);
+  uint32_t raw = 0, block = 0, phase = 0, tile = 0;  // raw blocks, blocks, phases and tiles so far
+  uint4 v[4];
+  // this thread's bytes of raw block `raw`, which is then free
+  auto take = [&](uint32_t k) {
+    if (!warp_wait<kPoll>(&br, &br.raw_full[k % kRaw], (k / kRaw) & 1, p)) return false;
 #pragma unroll
-    for (int h = 0; h < 2; h++) {
-      raw.row[h] = nullptr;
-      raw.sc[h] = make_float4(0, 0, 0, 0);
-      if (b >= 0 && t * kKeys + h * PAGE + r < len) {
-        const int page = page_of(p, b, 2 * t + h, len);
-        if (page >= 0) {
-          const size_t at = (size_t)page * PAGE + r;
-          raw.row[h] = p.cache + at * row_bytes;
-          if (tensor) {
-            const float k = __ldg(p.kv_scales);
-            raw.sc[h] = make_float4(k, k, k, k);
-          } else {
-            raw.sc[h] = __ldg(reinterpret_cast<const float4 *>(p.kv_scales) + at);
-          }
-        }
-      }
-    }
+    for (int j = 0; j < 4; j++) v[j] = ld_shared_v4(raws + (k % kRaw) * kRawBlock + (r + 32 * j) * 64 + c * 16);
+    return true;
   };
-  auto ask = [&](int kb) {
+  auto taken = [&](uint32_t k) {
+    __syncwarp();
+    if (first) mbar_arrive(smem_u32(&br.raw_empty[k % kRaw]));
+  };
+  auto widen_tile = [&] {
+    const float *sc = reinterpret_cast<const float *>(base + OFF_SCALES + (tile & 1) * kScaleBytes) + r * 4;
+    for (int kb = 0; kb < kBlocks; kb++, block++, raw++) {
+      const bool two = kb == 8 && scaled;  // the rotated part, bf16: two raw blocks, chunks 0-3 and 4-7 of a row
+      if ((int)(block % kWideGroups) != group) {
+        raw += two;
+        continue;
+      }
+      const uint32_t s = block % kSlots;
+      if (!take(raw)) return false;
+      if (!warp_wait<kPoll>(&br, kStreamKeys ? &br.slot_empty[s] : &br.res_empty[kb],
+                            ((kStreamKeys ? block / kSlots : phase) & 1) ^ 1, p))
+        return false;
+      const uint32_t at = (kStreamKeys ? slots + s * kBlock : res + kb * kBlock) + r * 128;
+      if (two) {
 #pragma unroll
-    for (int h = 0; h < 2; h++) {
-      const uint4 *src = reinterpret_cast<const uint4 *>(raw.row[h]);
-      const uint4 none = make_uint4(0, 0, 0, 0);
-      if (kb < 8 || tensor) {
-        raw.v[h][kb] = src ? __ldg(src + kb * 4 + c) : none;
+        for (int j = 0; j < 4; j++) st_shared_v4(at + 32 * j * 128 + ((c ^ x) << 4), v[j]);
+        taken(raw);
+        if (!take(++raw)) return false;
+#pragma unroll
+        for (int j = 0; j < 4; j++) st_shared_v4(at + 32 * j * 128 + (((4 + c) ^ x) << 4), v[j]);
       } else {
-        raw.v[h][8] = src ? __ldg(src + 32 + 2 * c) : none;
-        raw.v[h][9] = src ? __ldg(src + 33 + 2 * c) : none;
-      }
-    }
-  };
-  uint32_t s = 0, ph = 1, rph = 1;
-  bool asked = false;
-  // (tile, next tile): writes the tile's blocks and asks for the next one's
-  auto tile = [&](int b, int t, int len, int nb, int nt, int nlen) {
-    if (!asked) {
-      point(b, t, len);
 #pragma unroll
-      for (int kb = 0; kb < kBlocks; kb++) ask(kb);
-    }
-    float4 sc[2] = {raw.sc[0], raw.sc[1]};
-    point(nb, nt, nlen);
-    asked = nb >= 0;
-#pragma unroll
-    for (int kb = 0; kb < kBlocks; kb++) {
-      uint64_t *empty = kStreamKeys ? &br.slot_empty[s] : &br.res_empty[kb];
-      if (!warp_wait<kPoll>(&br, empty, kStreamKeys ? ph : rph, p)) return false;
-      const uint32_t dst = kStreamKeys ? slots + s * kBlock : res + kb * kBlock;
-#pragma unroll
-      for (int h = 0; h < 2; h++) {
-        uint4 lo, hi;
-        const int t4 = kb >> 1;
-        const float scl = t4 == 0 ? sc[h].x : t4 == 1 ? sc[h].y : t4 == 2 ? sc[h].z : sc[h].w;
-        if (kb < 8) {
-          widen16(raw.v[h][kb], scl, lo, hi);
-        } else if (tensor) {
-          widen16(raw.v[h][8], sc[h].x, lo, hi);
-        } else {
-          lo = raw.v[h][8];
-          hi = raw.v[h][9];
+        for (int j = 0; j < 4; j++) {
+          uint4 lo, hi;
+          widen16(v[j], scaled ? sc[32 * j * 4 + (kb >> 1)] : one, lo, hi);
+          st_shared_v4(at + 32 * j * 128 + (((2 * c) ^ x) << 4), lo);
+          st_shared_v4(at + 32 * j * 128 + (((2 * c + 1) ^ x) << 4), hi);
         }
-        const uint32_t at = dst + h * kHalf + r * 128;
-        const int x = r & 7;
-        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at + (((2 * c) ^ x) << 4)), "r"(lo.x), "r"(lo.y),
-                     "r"(lo.z), "r"(lo.w)
-                     : "memory");
-        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at + (((2 * c + 1) ^ x) << 4)), "r"(hi.x), "r"(hi.y),
-                     "r"(hi.z), "r"(hi.w)
-                     : "memory");
       }
+      taken(raw);
       fence_proxy_async_smem();
       __syncwarp();
-      if ((threadIdx.x & 31) == 0) mbar_arrive(smem_u32(kStreamKeys ? &br.slot_full[s] : &br.res_full[kb]));
-      if (asked) ask(kb);
-      if (kStreamKeys && ++s == kSlots) {
-        s = 0;
-        ph ^= 1;
-      }
+      if (first) mbar_arrive(smem_u32(kStreamKeys ? &br.slot_full[s] : &br.res_full[kb]));
     }
-    rph ^= 1;
+    phase++;
+    tile++;
     return true;
   };
   for_each_phase<kStreamKeys>(p, w, [&](const Phase &f) {
-    if (f.i0 >= f.i1) return true;
-    if (!kStreamKeys) return tile(f.b, f.t, f.len, -1, 0, 0);
-    for (int t = f.i0; t < f.i1; t++)
-      if (!tile(f.b, t, f.len, t + 1 < f.i1 ? f.b : -1, t + 1, f.len)) return false;
+    for (int t = f.i0; t < (kStreamKeys ? f.i1 : min(f.i0 + 1, f.i1)); t++)
+      if (!widen_tile()) return false;
     return true;
   });
 }
@@ -361,8 +389,9 @@ constexpr uint32_t kMmaBar = 1, kSumBar = 2;
 
 // Warp 2 waits for what the MMAs of warp 1 need and meets it at a named barrier (a
 // wait in the issuing warp would hold up its MMAs in flight).
-template <bool kStreamKeys, bool kPoll>
+template <bool kStreamKeys, bool kFp8, bool kPoll>
 __device__ void wait_role(const MassParams &p, Bars &br, const Work &w) {
+  constexpr int kSlots = slots_of(kFp8);
   uint32_t s = 0, ph = 0, rph = 0, g = 0;
   for_each_phase<kStreamKeys>(p, w, [&](const Phase &f) {
     if (f.i0 >= f.i1) return true;
@@ -383,8 +412,9 @@ __device__ void wait_role(const MassParams &p, Bars &br, const Work &w) {
   });
 }
 
-template <bool kStreamKeys>
+template <bool kStreamKeys, bool kFp8>
 __device__ void mma_role(const MassParams &p, uint8_t *base, Bars &br, const Work &w, uint32_t tmem) {
+  constexpr int kSlots = slots_of(kFp8);
   const uint32_t res = smem_u32(base), slots = smem_u32(base + OFF_SLOTS);
   const uint32_t idesc = idesc_bf16_f32(kKeys, p.box, false, false);
   uint32_t s = 0, g = 0;
@@ -506,12 +536,16 @@ __global__ void __launch_bounds__(threads_of(kFp8), 1)
   const int warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) {
     for (int i = 0; i < kBlocks; i++) {
-      mbar_init(smem_u32(&br.res_full[i]), kFp8 && !kStreamKeys ? kWideWarps : 1);
+      mbar_init(smem_u32(&br.res_full[i]), kFp8 && !kStreamKeys ? kWideWarps / kWideGroups : 1);
       mbar_init(smem_u32(&br.res_empty[i]), 1);
     }
-    for (int i = 0; i < kSlots; i++) {
-      mbar_init(smem_u32(&br.slot_full[i]), kFp8 && kStreamKeys ? kWideWarps : 1);
+    for (int i = 0; i < kMostSlots; i++) {
+      mbar_init(smem_u32(&br.slot_full[i]), kFp8 && kStreamKeys ? kWideWarps / kWideGroups : 1);
       mbar_init(smem_u32(&br.slot_empty[i]), 1);
+    }
+    for (int i = 0; i < kRaw; i++) {
+      mbar_init(smem_u32(&br.raw_full[i]), 1);
+      mbar_init(smem_u32(&br.raw_empty[i]), kWideWarps / kWideGroups);
     }
     for (int i = 0; i < kD; i++) {
       mbar_init(smem_u32(&br.d_full[i]), 1);
@@ -521,7 +555,7 @@ __global__ void __launch_bounds__(threads_of(kFp8), 1)
     br.start_b = br.start_t = 0;
     fence_mbar_init_cluster();
     prefetch_tensormap(&q_map);
-    if (!kFp8) prefetch_tensormap(&k_map);
+    prefetch_tensormap(&k_map);
   }
   if (warp == 1) {
     tmem_alloc(smem_u32(&br.tmem_base), kD * kRows);
@@ -535,10 +569,12 @@ __global__ void __launch_bounds__(threads_of(kFp8), 1)
   grid_dep_wait();
   const Work w = find_work<kStreamKeys>(p, br);
   if (warp == 0) load_role<kStreamKeys, kFp8, kPoll>(p, smem, br, &k_map, &q_map, w);
-  else if (warp == 1) mma_role<kStreamKeys>(p, smem, br, w, tmem);
-  else if (warp == 2) wait_role<kStreamKeys, kPoll>(p, br, w);
+  else if (warp == 1) mma_role<kStreamKeys, kFp8>(p, smem, br, w, tmem);
+  else if (warp == 2) wait_role<kStreamKeys, kFp8, kPoll>(p, br, w);
   else if (warp >= 4 && warp < 8) sum_role<kStreamKeys, kPoll>(p, br, w, tmem);
-  else if (kFp8 && warp >= 8) widen_role<kStreamKeys, kPoll>(p, smem, br, w, threadIdx.x - 256);
+  else if constexpr (kFp8) {
+    if (warp >= 8) widen_role<kStreamKeys, kPoll>(p, smem, br, w, threadIdx.x - 256);
+  }
   __syncwarp();
   tc_fence_before();
   __syncthreads();
@@ -671,6 +707,14 @@ extern "C" int mla_attention_mass(const void *q, const void *kv_cache, int kv_fo
     cuuint32_t box[4] = {64, (cuuint32_t)PAGE, 1, 1}, estr[4] = {1, 1, 1, 1};
     ok = fn(&k_map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(kv_cache), dims, strides, box, estr,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  } else if (ok) {
+    // bytes, 64 of each row of a page at a time
+    const cuuint64_t row = kv_format == MLA_KV_FP8_E4M3 ? FP8_ROW : D_QK;
+    cuuint64_t dims[3] = {row, (cuuint64_t)PAGE, (cuuint64_t)num_pages}, strides[2] = {row, row * PAGE};
+    cuuint32_t box[3] = {64, (cuuint32_t)PAGE, 1}, estr[3] = {1, 1, 1};
+    ok = fn(&k_map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(kv_cache), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
   }
   if (!ok) return fail(MLA_ERR_CUDA, "a tensor map could not be made");
