@@ -520,7 +520,7 @@ int mla_decode_shared(const void *q, const void *kv_cache, int kv_format, int nu
  *   mass           device fp32 [B][mass_cap], updated; mass_cap at most 2^24
  *   workspace      device, >= mla_attention_mass_workspace_bytes(B, T, H, mass_cap)
  *                  bytes, 256-byte aligned (NULL where that is 0, as it is for
- *                  T * H <= 128); no initialisation; calls that overlap on the GPU
+ *                  T * H <= 256); no initialisation; calls that overlap on the GPU
  *                  need separate ones
  * Scores and sums are fp32; FP8 rows with scales are rounded to bf16, as the
  * decode does.  Sums are made in a fixed order: equal calls give equal bits.  A

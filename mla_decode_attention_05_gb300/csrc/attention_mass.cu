@@ -4,9 +4,13 @@
 // decode (or a prompt's attention) has made, from its log-sum-exp, without its
 // product with the values.
 //
-// One MMA tile has 128 keys as its M rows and up to 128 query rows as its N
-// columns, so a key's scores lie in one lane of tensor memory and its sum is
-// one thread's own: nothing crosses lanes, no atomics.
+// A pair of CTAs works as one: an MMA tile has 256 keys as its M rows, 128 of each
+// CTA, and up to 256 query rows as its N columns, half of them from the shared
+// memory of each.  A key's scores lie in one lane of tensor memory, so its sum is
+// one thread's own: nothing crosses lanes, no atomics.  (Pairs halve what each SM
+// holds and reads of the query rows: alone, an SM has room for 128 rows and 64 KB
+// of keys on their way, and with many rows its shared memory is the limit: 8192
+// rows on 12001 keys 101 us.)
 #include <cmath>
 #include <cstdio>
 
@@ -22,27 +26,22 @@ namespace {
 
 using namespace ptx;
 
-constexpr int kKeys = 128;                     // keys of a tile: two pages
-constexpr int kRows = 128;                     // query rows of a tile
+constexpr int kKeys = 128;                     // keys of a CTA's half of a tile: two pages
+constexpr int kTileKeys = 2 * kKeys;
+constexpr int kRows = 256;                     // query rows of a tile
 constexpr int kBlocks = D_QK / 64;             // blocks of 64 of the 576 dims
 constexpr uint32_t kBlock = kKeys * 128;       // 128 rows x 64 dims, 128-byte swizzle
 constexpr uint32_t kHalf = kBlock / 2;
-constexpr int kD = 4;                          // score tiles in tensor memory
-constexpr int kWideWarps = 8;                  // FP8: warps that widen cached rows
-constexpr int kWideGroups = 2;
-constexpr int kRaw = 5;                        // FP8: blocks as they lie in the cache, on their way or being widened
-constexpr uint32_t kRawBlock = kKeys * 64;     // 128 rows x 64 bytes
-constexpr uint32_t kRawHalf = kRawBlock / 2;
-// The streaming operand's ring; FP8 gives half of it to the raw blocks.
-__host__ __device__ constexpr int slots_of(bool fp8) { return fp8 ? 2 : 4; }
-constexpr int kMostSlots = 4;
-constexpr uint32_t OFF_SLOTS = kBlocks * kBlock;
-constexpr uint32_t OFF_RAW = OFF_SLOTS + 2 * kBlock;
-constexpr uint32_t OFF_SCALES = OFF_RAW + kRaw * kRawBlock;  // two tiles' scales, [128][4]
-constexpr uint32_t kScaleBytes = kKeys * 16;
-constexpr uint32_t OFF_BARS = OFF_SLOTS + 5 * kBlock;
-static_assert(OFF_SCALES + 2 * kScaleBytes <= OFF_BARS, "shared memory map");
+constexpr int kMostSlots = 9;                  // blocks of the streaming operand
+constexpr int kD = 2;                          // score tiles in tensor memory
+constexpr int kWideWarps = 16;                 // FP8: warps that widen cached rows
+constexpr int kWideGroups = 4;                 // groups of them, which take the blocks in turn
+constexpr int kGroupWarps = kWideWarps / kWideGroups;
+constexpr int kWideThreads = 32 * kGroupWarps;
+constexpr int kWideRows = kKeys * 4 / kWideThreads;  // rows of which a thread has 16 bytes
+constexpr int kSumThreads = 128;
 __host__ __device__ constexpr int threads_of(bool fp8) { return fp8 ? 256 + 32 * kWideWarps : 256; }
+constexpr uint32_t IDESC = idesc_bf16_f32(kTileKeys, 16, false, false) - (2u << 17);  // N is added
 
 struct MassParams {
   const uint8_t *cache;
@@ -50,36 +49,54 @@ struct MassParams {
   const int32_t *block_table, *seqlens;
   const float *lse;  // [B][H][T]
   float *mass;       // [B][cap]
-  float *partial;    // [splits][B][cap], and before it the number of splits in use
-  int32_t *splits;
+  float *partial;    // [pairs][2][256]: sums of tiles that a pair has in part, its first and its last
   unsigned int *status;
   int format, num_pages, max_pages, B, T, H, cap, causal;
-  int rows, n_qt, box;  // query rows of a sequence, their tiles, rows of a tile's box
-  int max_splits;
+  int rows, n_qt, box;  // query rows of a sequence, their tiles, the columns of a tile (half of each CTA)
+  int slots;
   float scale_log2, decay;
   unsigned long long wait_ns;
 };
 
 struct Bars {
-  uint64_t res_full[kBlocks], res_empty[kBlocks];
+  uint64_t res_full[kBlocks], res_empty[kBlocks];        // full: rank 0, for both CTAs
   uint64_t slot_full[kMostSlots], slot_empty[kMostSlots];
-  uint64_t raw_full[kRaw], raw_empty[kRaw];
-  uint64_t d_full[kD], d_empty[kD];
-  float nl2[2][kRows];  // -lse * log2(e) of a tile's query rows
-  int lim[2][kRows];    // keys that a row sees; 0 for one that is no row, or has no weight to give
+  uint64_t raw_full[kMostSlots];  // FP8: a block's codes are in place (of the resident blocks, or of the slots)
+  uint64_t d_full[kD], d_empty[kD];                      // empty: rank 0
+  alignas(16) float nl2[2][kRows];  // -lse * log2(e) of a tile's query rows
+  alignas(16) int lim[2][kRows];    // keys that a row sees; 0 for one that is no row, or has no weight to give
+  int least[2][kRows / 32];         // the smallest of each 32 rows
   int warp_sums[32];
-  int start_b, start_t, n_tiles;
+  int start_b, start_t;
   uint32_t tmem_base;
   int abort;
 };
-constexpr uint32_t kSmem = OFF_BARS + sizeof(Bars);
-static_assert(kSmem <= 232448, "shared memory budget");
+// Shared memory: barriers, the resident operand's blocks, slots, FP8 scales of two tiles ([128][4]).
+constexpr uint32_t OFF_RES = 6 * 1024;
+constexpr uint32_t kScaleBytes = kKeys * 16;
+constexpr uint32_t kSmem = 232448 / 1024 * 1024;
+constexpr uint32_t OFF_SCALES = kSmem - 2 * kScaleBytes;
+static_assert(sizeof(Bars) <= OFF_RES, "shared memory map");
+static_assert(OFF_RES + kBlocks * kBlock + 4 * kBlock <= OFF_SCALES, "shared memory map");
+
+// The most bytes that may come between the barriers and the scales.
+constexpr uint32_t kRoom = OFF_SCALES - OFF_RES;
 
 // `bytes` (a multiple of 16) side by side into shared memory.
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
                "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bar)
                : "memory");
+}
+
+// Tile loads into this CTA whose bytes a barrier of either CTA of the pair counts.
+__device__ __forceinline__ void tma_load_4d_pair(uint32_t dst, const void *map, uint32_t cluster_bar, int c0, int c1, int c2,
+                                                 int c3, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes.cta_group::2.L2::cache_hint"
+      " [%0], [%1, {%2, %3, %4, %5}], [%6], %7;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(cluster_bar), "l"(policy)
+      : "memory");
 }
 
 __device__ __forceinline__ int seq_len(const MassParams &p, int b) {
@@ -89,7 +106,7 @@ __device__ __forceinline__ int seq_len(const MassParams &p, int b) {
 
 template <bool kPoll>
 __device__ __forceinline__ bool wait_ok(Bars *b, uint64_t *bar, uint32_t parity, const MassParams &p) {
-  if (mbar_wait_limited<false, kPoll>(smem_u32(bar), parity, &b->abort, p.wait_ns)) return true;
+  if (mbar_wait_limited<true, kPoll>(smem_u32(bar), parity, &b->abort, p.wait_ns)) return true;
   atomicOr(p.status, MLA_STATUS_WAIT_TIMEOUT);
   *(volatile int *)&b->abort = 1;
   return false;
@@ -101,92 +118,108 @@ __device__ __forceinline__ bool warp_wait(Bars *b, uint64_t *bar, uint32_t parit
   return __all_sync(0xffffffffu, wait_ok<kPoll>(b, bar, parity, p));
 }
 
-// A phase: a resident operand and what streams past it.  kStreamKeys: the query
-// rows of sequence b stay and its key tiles [i0, i1) pass by, each one a sum of its
-// own.  Otherwise key tile t stays, query tiles [i0, i1) pass by, and their sum
-// is part `split` of the tile's.
+// The work is a line of units (key tile, query tile), query tiles innermost, of
+// which each pair has an equal part.  A phase: a resident operand and what
+// streams past it.  kStreamKeys (one query tile): the query rows of sequence b stay
+// and its key tiles [i0, i1) pass by, each one a sum of its own.  Otherwise key tile
+// t stays and query tiles [i0, i1) pass by; whole: they are all of its query tiles,
+// else their sum is one of several, kept in place `part` of the pair's two.
 struct Phase {
-  int b, t, i0, i1, split, len;
+  int b, t, i0, i1, len, part;
+  bool whole;
 };
 
 struct Work {
-  int b, t;              // sequence and key tile of the first unit
-  long long u0, u1;      // units
-  int splits;
+  int b, t;          // sequence and key tile of the first unit
+  long long u0, u1;  // units of this pair
 };
 
 template <bool kStreamKeys, class F>
 __device__ __forceinline__ bool for_each_phase(const MassParams &p, const Work &w, F &&f) {
   int b = w.b, t = w.t, len = w.u0 < w.u1 ? seq_len(p, b) : 0;
   for (long long u = w.u0; u < w.u1;) {
-    while (t * kKeys >= len) {
+    while (t * kTileKeys >= len) {
       if (++b >= p.B) return true;
       t = 0;
       len = seq_len(p, b);
     }
     if (kStreamKeys) {
-      const int n = (int)min(w.u1 - u, (long long)(ceil_div(len, kKeys) - t));
-      if (!f(Phase{b, t, t, t + n, 0, len})) return false;
+      const int n = (int)min(w.u1 - u, (long long)(ceil_div(len, kTileKeys) - t));
+      if (!f(Phase{b, t, t, t + n, len, 0, true})) return false;
       t += n;
       u += n;
     } else {
-      const int s = (int)(u % w.splits);
-      int i0 = (int)((long long)p.n_qt * s / w.splits), i1 = (int)((long long)p.n_qt * (s + 1) / w.splits);
+      const int i0 = (int)(u % p.n_qt), i1 = (int)min((long long)p.n_qt, i0 + (w.u1 - u));
+      Phase ph{b, t, i0, i1, len, i0 == 0 ? 1 : 0, i0 == 0 && i1 == p.n_qt};
       if (p.causal) {  // query rows before the first that sees any of these keys
-        const int t_min = max(0, t * kKeys - len + p.T);
-        i0 = (int)min((long long)i1, max((long long)i0, (long long)t_min * p.H / kRows));
+        const int t_min = max(0, t * kTileKeys - len + p.T);
+        ph.i0 = (int)min((long long)i1, max((long long)i0, (long long)t_min * p.H / kRows));
       }
-      if (!f(Phase{b, t, i0, i1, s, len})) return false;
-      u++;
-      if (s == w.splits - 1) t++;
+      if (!f(ph)) return false;
+      u += i1 - i0;
+      t++;
     }
   }
   return true;
 }
 
-// This CTA's units, found by all threads together.
-template <bool kStreamKeys>
-__device__ Work find_work(const MassParams &p, Bars &br) {
+// The number of key tiles; with `b` and `at`, those of the sequences before this thread's.
+struct Tiles {
+  int mine, before, total, b0, b1;
+};
+
+__device__ Tiles count_tiles(const MassParams &p, int *warp_sums) {
   const int n = blockDim.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int per = ceil_div(p.B, n), b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
-  int mine = 0;
-  for (int b = b0; b < b1; b++) {
-    const int raw = __ldg(p.seqlens + b), len = seq_len(p, b);
-    if (raw != len && blockIdx.x == 0) atomicOr(p.status, MLA_STATUS_BAD_SEQLEN);
-    mine += ceil_div(len, kKeys);
-  }
-  int incl = mine;
+  const int per = ceil_div(p.B, n);
+  Tiles t;
+  t.b0 = min(p.B, tid * per);
+  t.b1 = min(p.B, t.b0 + per);
+  t.mine = 0;
+  for (int b = t.b0; b < t.b1; b++) t.mine += ceil_div(seq_len(p, b), kTileKeys);
+  int incl = t.mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int v = __shfl_up_sync(0xffffffffu, incl, o);
     if (lane >= o) incl += v;
   }
-  if (lane == 31) br.warp_sums[warp] = incl;
+  if (lane == 31) warp_sums[warp] = incl;
   __syncthreads();
-  int before = 0, total = 0;
+  t.before = incl - t.mine;
+  t.total = 0;
   for (int i = 0; i < n / 32; i++) {
-    if (i < warp) before += br.warp_sums[i];
-    total += br.warp_sums[i];
+    if (i < warp) t.before += warp_sums[i];
+    t.total += warp_sums[i];
   }
-  Work w;
-  w.splits = 1;
-  if (!kStreamKeys) w.splits = max(1, min(p.max_splits, ceil_div(2 * (int)gridDim.x, max(total, 1))));
-  const long long units = (long long)total * w.splits;
-  w.u0 = units * blockIdx.x / gridDim.x;
-  w.u1 = units * (blockIdx.x + 1) / gridDim.x;
-  const int first = (int)(w.u0 / w.splits);
-  int at = before + incl - mine;
-  if (first >= at && first < at + mine)
-    for (int b = b0; b < b1; b++) {
-      const int c = ceil_div(seq_len(p, b), kKeys);
-      if (first < at + c) {
-        br.start_b = b;
-        br.start_t = first - at;
-        break;
-      }
-      at += c;
+  return t;
+}
+
+// Sequence and tile within it of tile `x` of all, told by the thread that has it.
+__device__ __forceinline__ void find_tile(const MassParams &p, const Tiles &t, int x, int *b_out, int *t_out) {
+  if (x < t.before || x >= t.before + t.mine) return;
+  int at = t.before;
+  for (int b = t.b0; b < t.b1; b++) {
+    const int c = ceil_div(seq_len(p, b), kTileKeys);
+    if (x < at + c) {
+      *b_out = b;
+      *t_out = x - at;
+      return;
     }
-  if (blockIdx.x == 0 && tid == 0 && p.splits) *p.splits = w.splits;
+    at += c;
+  }
+}
+
+__device__ __forceinline__ long long first_unit(long long units, int pair, int pairs) { return units * pair / pairs; }
+
+__device__ Work find_work(const MassParams &p, Bars &br, int pair, int pairs) {
+  const Tiles t = count_tiles(p, br.warp_sums);
+  if (blockIdx.x == 0)
+    for (int b = t.b0; b < t.b1; b++)
+      if (__ldg(p.seqlens + b) != seq_len(p, b)) atomicOr(p.status, MLA_STATUS_BAD_SEQLEN);
+  const long long units = (long long)t.total * p.n_qt;
+  Work w;
+  w.u0 = first_unit(units, pair, pairs);
+  w.u1 = first_unit(units, pair + 1, pairs);
+  find_tile(p, t, (int)(w.u0 / p.n_qt), &br.start_b, &br.start_t);
   __syncthreads();
   w.b = br.start_b;
   w.t = br.start_t;
@@ -203,100 +236,87 @@ __device__ __forceinline__ int page_of(const MassParams &p, int b, int j, int le
   return page;
 }
 
+// Where this CTA's operands lie.
+struct Place {
+  uint32_t res, res_block, slots, rank;
+};
+
 // ---- loads -------------------------------------------------------------------------
 
-// Warp 0: query rows, the pages of a bf16 cache, and the raw blocks of an FP8 one
-// (64 bytes of each row; ten of them where the rotated part is bf16).  The whole
-// warp waits and looks pages up, one elected lane asks for the copies.
+// Warp 0: query rows and cached ones.  The whole warp waits and looks pages up, one
+// elected lane asks for the copies.  rank 0's barriers count the bytes of both
+// CTAs.  A block of FP8 rows lands as codes (64 bytes of each row) in the upper half
+// of the block that it will fill, on a barrier of this CTA; the rotated part of rows
+// with scales is bf16 and lands as it is used.
 template <bool kStreamKeys, bool kFp8, bool kPoll>
-__device__ void load_role(const MassParams &p, uint8_t *base, Bars &br, const CUtensorMap *k_map, const CUtensorMap *q_map,
-                          const Work &w) {
-  constexpr int kSlots = slots_of(kFp8);
-  const uint32_t res = smem_u32(base), slots = smem_u32(base + OFF_SLOTS);
-  const uint32_t raws = smem_u32(base + OFF_RAW), scales = smem_u32(base + OFF_SCALES);
-  const uint64_t keep = policy_evict_normal(), pass = policy_evict_first();
-  const uint64_t key_pol = kStreamKeys ? pass : keep;
+__device__ void load_role(const MassParams &p, uint8_t *base, Bars &br, const CUtensorMap *k_map, const CUtensorMap *pe_map,
+                          const CUtensorMap *q_map, const Work &w, const Place &at) {
+  const uint32_t scales = smem_u32(base + OFF_SCALES);
+  const uint64_t keep = policy_evict_normal(), key_pol = kStreamKeys ? policy_evict_first() : keep;
   const bool scaled = p.format == MLA_KV_FP8_E4M3;
-  const int n_raw = scaled ? 10 : 9;
-  uint32_t s = 0, ph = 1, rph = 1, rs = 0, rawph = 1, tile = 0;
-  auto keys = [&](uint32_t dst, uint64_t *full, int pg0, int pg1, int kb) {
-    if (!elect_one()) return;
-    const uint32_t bar = smem_u32(full);
-    mbar_arrive_expect_tx(bar, (pg0 >= 0 ? kHalf : 0) + (pg1 >= 0 ? kHalf : 0));
-    if (pg0 >= 0) tma_load_4d(dst, k_map, bar, 0, 0, kb, pg0, key_pol);
-    if (pg1 >= 0) tma_load_4d(dst + kHalf, k_map, bar, 0, 0, kb, pg1, key_pol);
+  int s = 0;
+  uint32_t ph = 1, rph = 1, tile = 0;
+  int pg[2] = {-1, -1}, pages = 0;  // this CTA's pages of a tile, and how many both have
+  auto look = [&](int b, int t, int len) {
+    const int lane = threadIdx.x & 31;
+    const int page = lane < 4 ? page_of(p, b, 4 * t + lane, len) : -1;
+    pages = __popc(__ballot_sync(0xffffffffu, page >= 0));
+    pg[0] = __shfl_sync(0xffffffffu, page, 2 * at.rank);
+    pg[1] = __shfl_sync(0xffffffffu, page, 2 * at.rank + 1);
   };
+  auto keys = [&](uint32_t dst, uint64_t *full, uint64_t *raw, int kb) {
+    if (!elect_one()) return;
+    if (!kFp8) {
+      const uint32_t bar = mapa(smem_u32(full), 0);
+      if (at.rank == 0) mbar_arrive_expect_tx(smem_u32(full), pages * kHalf);
+#pragma unroll
+      for (int h = 0; h < 2; h++)
+        if (pg[h] >= 0) tma_load_4d_pair(dst + h * kHalf, k_map, bar, 0, 0, kb, pg[h], key_pol);
+      return;
+    }
+    const uint32_t bar = smem_u32(raw), n = (pg[0] >= 0) + (pg[1] >= 0);
+    const bool codes = !(scaled && kb == 8), with = scaled && kb == 0;
+    mbar_arrive_expect_tx(bar, n * ((codes ? kHalf / 2 : kHalf) + (with ? kScaleBytes / 2 : 0)));
+#pragma unroll
+    for (int h = 0; h < 2; h++) {
+      if (pg[h] < 0) continue;
+      if (codes) tma_load_3d(dst + kHalf + h * (kHalf / 2), k_map, bar, kb * 64, 0, pg[h], key_pol);
+      else tma_load_3d(dst + h * kHalf, pe_map, bar, 0, 0, pg[h], key_pol);
+      if (with)
+        bulk_load(scales + (tile & 1) * kScaleBytes + h * (kScaleBytes / 2), p.kv_scales + (size_t)pg[h] * PAGE * 4,
+                  kScaleBytes / 2, bar);
+    }
+  };
+  const int half = p.box / 2;  // query rows of each CTA
   auto rows = [&](uint32_t dst, uint64_t *full, int b, int qt, int kb) {
     if (!elect_one()) return;
-    const uint32_t bar = smem_u32(full);
-    mbar_arrive_expect_tx(bar, p.box * 128);
-    tma_load_3d(dst, q_map, bar, 0, b * p.rows + qt * kRows, kb, keep);
-  };
-  // an FP8 tile's raw blocks and, with the first, its scales
-  auto raw_tile = [&](int pg0, int pg1) {
-    const uint32_t n = (pg0 >= 0) + (pg1 >= 0);
-    for (int k = 0; k < n_raw; k++) {
-      if (!warp_wait<kPoll>(&br, &br.raw_empty[rs], rawph, p)) return false;
-      if (elect_one()) {
-        const uint32_t bar = smem_u32(&br.raw_full[rs]), dst = raws + rs * kRawBlock;
-        const bool with = scaled && k == 0;
-        mbar_arrive_expect_tx(bar, n * (kRawHalf + (with ? kScaleBytes / 2 : 0)));
-#pragma unroll
-        for (int h = 0; h < 2; h++) {
-          const int pg = h ? pg1 : pg0;
-          if (pg < 0) continue;
-          tma_load_3d(dst + h * kRawHalf, k_map, bar, k * 64, 0, pg, key_pol);
-          if (with)
-            bulk_load(scales + (tile & 1) * kScaleBytes + h * (kScaleBytes / 2), p.kv_scales + (size_t)pg * PAGE * 4,
-                      kScaleBytes / 2, bar);
-        }
-      }
-      __syncwarp();
-      if (++rs == kRaw) {
-        rs = 0;
-        rawph ^= 1;
-      }
-    }
-    tile++;
-    return true;
+    if (at.rank == 0) mbar_arrive_expect_tx(smem_u32(full), p.box * 128);
+    tma_load_3d_pair(dst, q_map, mapa(smem_u32(full), 0), 0, b * p.rows + qt * kRows + (int)at.rank * half, kb, keep);
   };
   for_each_phase<kStreamKeys>(p, w, [&](const Phase &f) {
     if (f.i0 >= f.i1) return true;
-    int pg0 = -1, pg1 = -1;
-    if (!kStreamKeys) {
-      pg0 = page_of(p, f.b, 2 * f.t, f.len);
-      pg1 = page_of(p, f.b, 2 * f.t + 1, f.len);
+    if (!kStreamKeys) look(f.b, f.t, f.len);
+    for (int kb = 0; kb < kBlocks; kb++) {
+      if (!warp_wait<kPoll>(&br, &br.res_empty[kb], rph, p)) return false;
+      if (kStreamKeys) rows(at.res + kb * at.res_block, &br.res_full[kb], f.b, 0, kb);
+      else keys(at.res + kb * at.res_block, &br.res_full[kb], &br.raw_full[kb], kb);
+      __syncwarp();
     }
-    if (kStreamKeys || !kFp8) {
-      for (int kb = 0; kb < kBlocks; kb++) {
-        if (!warp_wait<kPoll>(&br, &br.res_empty[kb], rph, p)) return false;
-        if (kStreamKeys) rows(res + kb * kBlock, &br.res_full[kb], f.b, 0, kb);
-        else keys(res + kb * kBlock, &br.res_full[kb], pg0, pg1, kb);
-        __syncwarp();
-      }
-      rph ^= 1;
-    } else if (!raw_tile(pg0, pg1)) {
-      return false;
-    }
+    rph ^= 1;
+    if (!kStreamKeys) tile++;
     for (int i = f.i0; i < f.i1; i++) {
-      if (kStreamKeys) {
-        pg0 = page_of(p, f.b, 2 * i, f.len);
-        pg1 = page_of(p, f.b, 2 * i + 1, f.len);
-      }
-      if constexpr (kStreamKeys && kFp8) {
-        if (!raw_tile(pg0, pg1)) return false;
-      } else {
-        for (int kb = 0; kb < kBlocks; kb++) {
-          if (!warp_wait<kPoll>(&br, &br.slot_empty[s], ph, p)) return false;
-          if (kStreamKeys) keys(slots + s * kBlock, &br.slot_full[s], pg0, pg1, kb);
-          else rows(slots + s * kBlock, &br.slot_full[s], f.b, i, kb);
-          __syncwarp();
-          if (++s == kSlots) {
-            s = 0;
-            ph ^= 1;
-          }
+      if (kStreamKeys) look(f.b, i, f.len);
+      for (int kb = 0; kb < kBlocks; kb++) {
+        if (!warp_wait<kPoll>(&br, &br.slot_empty[s], ph, p)) return false;
+        if (kStreamKeys) keys(at.slots + s * kBlock, &br.slot_full[s], &br.raw_full[s], kb);
+        else rows(at.slots + s * kBlock, &br.slot_full[s], f.b, i, kb);
+        __syncwarp();
+        if (++s == p.slots) {
+          s = 0;
+          ph ^= 1;
         }
       }
+      if (kStreamKeys) tile++;
     }
     return true;
   });
@@ -312,67 +332,53 @@ __device__ __forceinline__ void st_shared_v4(uint32_t addr, const uint4 &v) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
 
-// Warps 8-15 widen FP8 rows, in two groups that take the blocks in turn: thread i of
-// a group has 16 bytes of rows i / 4 + 32 k.  (The raw blocks come by TMA: a load of its own in flight
-// would hold up the thread's proxy fences.)
+// Warps 8-23 widen FP8 rows in place, in groups that take the blocks in turn: thread
+// i of a group has 16 codes of rows i / 4 + 32 k.  All of a group read their codes
+// before any writes bf16 values over them.  (The codes come by TMA: a load of its
+// own in flight would hold up the thread's proxy fences.)
+constexpr uint32_t kWideBar = 3;
+
 template <bool kStreamKeys, bool kPoll>
-__device__ void widen_role(const MassParams &p, uint8_t *base, Bars &br, const Work &w, int thread) {
-  constexpr int kSlots = slots_of(true);
-  static_assert(kSlots == kWideGroups, "a group has a slot of its own");
-  const uint32_t res = smem_u32(base), slots = smem_u32(base + OFF_SLOTS), raws = smem_u32(base + OFF_RAW);
-  const int group = thread / (32 * kWideWarps / kWideGroups), i = thread % (32 * kWideWarps / kWideGroups);
+__device__ void widen_role(const MassParams &p, uint8_t *base, Bars &br, const Work &w, const Place &at, int thread) {
+  const int group = thread / kWideThreads, i = thread % kWideThreads;
   const int r = i >> 2, c = i & 3, x = r & 7;
+  constexpr int kStep = kWideThreads / 4;  // rows between a thread's
+  static_assert(kStep % 8 == 0, "a thread's rows have one swizzle");
   const bool first = (threadIdx.x & 31) == 0, scaled = p.format == MLA_KV_FP8_E4M3;
   const float one = scaled ? 0.f : __ldg(p.kv_scales);
-  uint32_t raw = 0, block = 0, phase = 0, tile = 0;  // raw blocks, blocks, phases and tiles so far
-  uint4 v[4];
-  // this thread's bytes of raw block `raw`, which is then free
-  auto take = [&](uint32_t k) {
-    if (!warp_wait<kPoll>(&br, &br.raw_full[k % kRaw], (k / kRaw) & 1, p)) return false;
-#pragma unroll
-    for (int j = 0; j < 4; j++) v[j] = ld_shared_v4(raws + (k % kRaw) * kRawBlock + (r + 32 * j) * 64 + c * 16);
-    return true;
-  };
-  auto taken = [&](uint32_t k) {
-    __syncwarp();
-    if (first) mbar_arrive(smem_u32(&br.raw_empty[k % kRaw]));
-  };
+  int s = 0, turn = 0;
+  uint32_t ph = 0, tile = 0;
   auto widen_tile = [&] {
     const float *sc = reinterpret_cast<const float *>(base + OFF_SCALES + (tile & 1) * kScaleBytes) + r * 4;
-    for (int kb = 0; kb < kBlocks; kb++, block++, raw++) {
-      const bool two = kb == 8 && scaled;  // the rotated part, bf16: two raw blocks, chunks 0-3 and 4-7 of a row
-      if ((int)(block % kWideGroups) != group) {
-        raw += two;
-        continue;
-      }
-      const uint32_t s = block % kSlots;
-      if (!take(raw)) return false;
-      if (!warp_wait<kPoll>(&br, kStreamKeys ? &br.slot_empty[s] : &br.res_empty[kb],
-                            ((kStreamKeys ? block / kSlots : phase) & 1) ^ 1, p))
-        return false;
-      const uint32_t at = (kStreamKeys ? slots + s * kBlock : res + kb * kBlock) + r * 128;
-      if (two) {
+    for (int kb = 0; kb < kBlocks; kb++) {
+      if (turn == group) {
+        const int k = kStreamKeys ? s : kb;
+        const uint32_t dst = kStreamKeys ? at.slots + s * kBlock : at.res + kb * kBlock;
+        const bool ok = warp_wait<kPoll>(&br, &br.raw_full[k], kStreamKeys ? ph : tile & 1, p);
+        uint4 v[kWideRows];
 #pragma unroll
-        for (int j = 0; j < 4; j++) st_shared_v4(at + 32 * j * 128 + ((c ^ x) << 4), v[j]);
-        taken(raw);
-        if (!take(++raw)) return false;
+        for (int j = 0; j < kWideRows; j++) v[j] = ld_shared_v4(dst + kHalf + (r + kStep * j) * 64 + c * 16);
+        if (bar_red_or(kWideBar + group, kWideThreads, !ok)) return false;
+        if (!(scaled && kb == 8)) {
 #pragma unroll
-        for (int j = 0; j < 4; j++) st_shared_v4(at + 32 * j * 128 + (((4 + c) ^ x) << 4), v[j]);
-      } else {
-#pragma unroll
-        for (int j = 0; j < 4; j++) {
-          uint4 lo, hi;
-          widen16(v[j], scaled ? sc[32 * j * 4 + (kb >> 1)] : one, lo, hi);
-          st_shared_v4(at + 32 * j * 128 + (((2 * c) ^ x) << 4), lo);
-          st_shared_v4(at + 32 * j * 128 + (((2 * c + 1) ^ x) << 4), hi);
+          for (int j = 0; j < kWideRows; j++) {
+            uint4 lo, hi;
+            widen16(v[j], scaled ? sc[kStep * j * 4 + (kb >> 1)] : one, lo, hi);
+            const uint32_t row = dst + (r + kStep * j) * 128;
+            st_shared_v4(row + (((2 * c) ^ x) << 4), lo);
+            st_shared_v4(row + (((2 * c + 1) ^ x) << 4), hi);
+          }
         }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (first) mbar_arrive_remote(mapa(smem_u32(kStreamKeys ? &br.slot_full[k] : &br.res_full[k]), 0));
       }
-      taken(raw);
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (first) mbar_arrive(smem_u32(kStreamKeys ? &br.slot_full[s] : &br.res_full[kb]));
+      if (++turn == kWideGroups) turn = 0;
+      if (++s == p.slots) {
+        s = 0;
+        ph ^= 1;
+      }
     }
-    phase++;
     tile++;
     return true;
   };
@@ -387,12 +393,12 @@ __device__ void widen_role(const MassParams &p, uint8_t *base, Bars &br, const W
 
 constexpr uint32_t kMmaBar = 1, kSumBar = 2;
 
-// Warp 2 waits for what the MMAs of warp 1 need and meets it at a named barrier (a
-// wait in the issuing warp would hold up its MMAs in flight).
-template <bool kStreamKeys, bool kFp8, bool kPoll>
+// rank 0, warp 2 waits for what the MMAs of warp 1 need and meets it at a named
+// barrier (a wait in the issuing warp would hold up its MMAs in flight).
+template <bool kStreamKeys, bool kPoll>
 __device__ void wait_role(const MassParams &p, Bars &br, const Work &w) {
-  constexpr int kSlots = slots_of(kFp8);
-  uint32_t s = 0, ph = 0, rph = 0, g = 0;
+  int s = 0;
+  uint32_t ph = 0, rph = 0, g = 0;
   for_each_phase<kStreamKeys>(p, w, [&](const Phase &f) {
     if (f.i0 >= f.i1) return true;
     for (int i = f.i0; i < f.i1; i++, g++) {
@@ -401,7 +407,7 @@ __device__ void wait_role(const MassParams &p, Bars &br, const Work &w) {
         if (ok && i == f.i0) ok = warp_wait<kPoll>(&br, &br.res_full[kb], rph, p);
         if (ok) ok = warp_wait<kPoll>(&br, &br.slot_full[s], ph, p);
         if (bar_red_or(kMmaBar, 64, !ok)) return false;
-        if (++s == kSlots) {
+        if (++s == p.slots) {
           s = 0;
           ph ^= 1;
         }
@@ -412,12 +418,11 @@ __device__ void wait_role(const MassParams &p, Bars &br, const Work &w) {
   });
 }
 
-template <bool kStreamKeys, bool kFp8>
-__device__ void mma_role(const MassParams &p, uint8_t *base, Bars &br, const Work &w, uint32_t tmem) {
-  constexpr int kSlots = slots_of(kFp8);
-  const uint32_t res = smem_u32(base), slots = smem_u32(base + OFF_SLOTS);
-  const uint32_t idesc = idesc_bf16_f32(kKeys, p.box, false, false);
-  uint32_t s = 0, g = 0;
+template <bool kStreamKeys>
+__device__ void mma_role(const MassParams &p, Bars &br, const Work &w, const Place &at, uint32_t tmem) {
+  const uint32_t idesc = IDESC + ((uint32_t)(p.box >> 3) << 17);
+  int s = 0;
+  uint32_t g = 0;
   for_each_phase<kStreamKeys>(p, w, [&](const Phase &f) {
     if (f.i0 >= f.i1) return true;
     for (int i = f.i0; i < f.i1; i++, g++) {
@@ -425,18 +430,18 @@ __device__ void mma_role(const MassParams &p, uint8_t *base, Bars &br, const Wor
         if (bar_red_or(kMmaBar, 64, false)) return false;
         tc_fence_after();
         if (elect_one()) {
-          const uint64_t stay = smem_desc_sw128(res + kb * kBlock, 16, 1024);
-          const uint64_t pass = smem_desc_sw128(slots + s * kBlock, 16, 1024);
+          const uint64_t stay = smem_desc_sw128(at.res + kb * at.res_block, 16, 1024);
+          const uint64_t pass = smem_desc_sw128(at.slots + s * kBlock, 16, 1024);
           const uint64_t a = kStreamKeys ? pass : stay, b = kStreamKeys ? stay : pass;
 #pragma unroll
           for (int kk = 0; kk < 4; kk++)
-            mma_ss(tmem + (g % kD) * kRows, a + kk * 2, b + kk * 2, idesc, kb || kk ? 1u : 0u);
-          mma_commit(smem_u32(&br.slot_empty[s]));
-          if (i == f.i1 - 1) mma_commit(smem_u32(&br.res_empty[kb]));
-          if (kb == kBlocks - 1) mma_commit(smem_u32(&br.d_full[g % kD]));
+            mma_pair_ss(tmem + (g % kD) * kRows, a + kk * 2, b + kk * 2, idesc, kb || kk ? 1u : 0u);
+          mma_commit_pair(smem_u32(&br.slot_empty[s]));
+          if (i == f.i1 - 1) mma_commit_pair(smem_u32(&br.res_empty[kb]));
+          if (kb == kBlocks - 1) mma_commit_pair(smem_u32(&br.d_full[g % kD]));
         }
         __syncwarp();
-        if (++s == kSlots) s = 0;
+        if (++s == p.slots) s = 0;
       }
     }
     return true;
@@ -449,36 +454,64 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+      "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+
+__device__ __forceinline__ float2 pair(uint32_t a, uint32_t b) { return make_float2(__uint_as_float(a), __uint_as_float(b)); }
+
 // Warps 4-7: thread = key of the tile = lane of tensor memory.
 template <bool kStreamKeys, bool kPoll>
-__device__ void sum_role(const MassParams &p, Bars &br, const Work &w, uint32_t tmem) {
+__device__ void sum_role(const MassParams &p, Bars &br, const Work &w, uint32_t tmem, uint32_t rank, int pair_index) {
   const int i = threadIdx.x - 128, lane = threadIdx.x & 31;
   const uint32_t lt = tmem + ((uint32_t)(i & 96) << 16);
   uint32_t g = 0, buf = 0;
+  const float2 cs = make_float2(p.scale_log2, p.scale_log2);
+  const uint32_t d_empty = mapa(smem_u32(&br.d_empty[0]), 0);
   auto set_rows = [&](const Phase &f, int qt) {
     buf ^= 1;
-    const int R = qt * kRows + i;
-    int lim = 0;
-    float nl = 0.f;
-    if (R < p.rows) {
-      const int t = R / p.H, h = R % p.H;
-      const float l = __ldg(p.lse + ((size_t)f.b * p.H + h) * p.T + t);
-      lim = l == -INFINITY ? 0 : row_kv_len(f.len, p.T, t, p.causal);
-      nl = -l * LOG2E;
+#pragma unroll
+    for (int k = 0; k < kRows; k += kSumThreads) {
+      const int R = qt * kRows + k + i;
+      int lim = 0;
+      float nl = 0.f;
+      if (R < p.rows) {
+        const int t = R / p.H, h = R % p.H;
+        const float l = __ldg(p.lse + ((size_t)f.b * p.H + h) * p.T + t);
+        lim = l == -INFINITY ? 0 : row_kv_len(f.len, p.T, t, p.causal);
+        nl = -l * LOG2E;
+      }
+      br.nl2[buf][k + i] = nl;
+      br.lim[buf][k + i] = lim;
+      const int least = __reduce_min_sync(0xffffffffu, lim);
+      if (lane == 0) br.least[buf][(k + i) / 32] = least;
     }
-    br.nl2[buf][i] = nl;
-    br.lim[buf][i] = lim;
   };
   for_each_phase<kStreamKeys>(p, w, [&](const Phase &f) {
     if (kStreamKeys) set_rows(f, 0);
     float sum = 0.f;
-    auto key_of = [&](int t) { return t * kKeys + i; };
+    auto key_of = [&](int t) { return t * kTileKeys + (int)rank * kKeys + i; };
     auto store = [&](int t, float v) {
       const int n = key_of(t);
       if (n >= f.len) return;
       if (page_of(p, f.b, n / PAGE, f.len) < 0) v = 0.f;
-      if (!kStreamKeys && w.splits > 1) {
-        p.partial[((size_t)f.split * p.B + f.b) * p.cap + n] = v;
+      if (!kStreamKeys && !f.whole) {
+        p.partial[((size_t)pair_index * 2 + f.part) * kTileKeys + rank * kKeys + i] = v;
       } else {
         float *m = p.mass + (size_t)f.b * p.cap + n;
         *m = p.decay != 0.f ? fmaf(p.decay, *m, v) : v;
@@ -491,30 +524,41 @@ __device__ void sum_role(const MassParams &p, Bars &br, const Work &w, uint32_t 
       tc_fence_after();
       const int key = key_of(kStreamKeys ? k : f.t);
       const int cols = min(kRows, p.rows - (kStreamKeys ? 0 : k * kRows));
-      float acc[4] = {0.f, 0.f, 0.f, 0.f};
+      const int end = min((kStreamKeys ? k + 1 : f.t + 1) * kTileKeys, f.len);
+      float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
       for (int c0 = 0; c0 < cols; c0 += 32) {
         uint32_t v[32];
         __syncwarp();
         tmem_ld32(lt + (g % kD) * kRows + c0, v);
+        const float4 *nl = reinterpret_cast<const float4 *>(&br.nl2[buf][c0]);
+        const bool all = end <= br.least[buf][c0 / 32];  // these rows see all the tile's keys
         tmem_wait_ld();
+        if (all) {
 #pragma unroll
-        for (int j = 0; j < 32; j += 4) {
-          const float4 nl = *reinterpret_cast<const float4 *>(&br.nl2[buf][c0 + j]);
-          const int4 lim = *reinterpret_cast<const int4 *>(&br.lim[buf][c0 + j]);
-          const float e0 = ex2(fmaf(__uint_as_float(v[j]), p.scale_log2, nl.x));
-          const float e1 = ex2(fmaf(__uint_as_float(v[j + 1]), p.scale_log2, nl.y));
-          const float e2 = ex2(fmaf(__uint_as_float(v[j + 2]), p.scale_log2, nl.z));
-          const float e3 = ex2(fmaf(__uint_as_float(v[j + 3]), p.scale_log2, nl.w));
-          if (key < lim.x) acc[0] += e0;
-          if (key < lim.y) acc[1] += e1;
-          if (key < lim.z) acc[2] += e2;
-          if (key < lim.w) acc[3] += e3;
+          for (int j = 0; j < 8; j++) {
+            const float4 n = nl[j];
+            const float2 a = fma2(pair(v[4 * j], v[4 * j + 1]), cs, make_float2(n.x, n.y));
+            const float2 b = fma2(pair(v[4 * j + 2], v[4 * j + 3]), cs, make_float2(n.z, n.w));
+            acc[0] = add2(acc[0], make_float2(ex2(a.x), ex2(a.y)));
+            acc[1] = add2(acc[1], make_float2(ex2(b.x), ex2(b.y)));
+          }
+        } else {
+          const int4 *lims = reinterpret_cast<const int4 *>(&br.lim[buf][c0]);
+#pragma unroll
+          for (int j = 0; j < 8; j++) {
+            const float4 n = nl[j];
+            const int4 lim = lims[j];
+            const float2 a = fma2(pair(v[4 * j], v[4 * j + 1]), cs, make_float2(n.x, n.y));
+            const float2 b = fma2(pair(v[4 * j + 2], v[4 * j + 3]), cs, make_float2(n.z, n.w));
+            acc[0] = add2(acc[0], make_float2(key < lim.x ? ex2(a.x) : 0.f, key < lim.y ? ex2(a.y) : 0.f));
+            acc[1] = add2(acc[1], make_float2(key < lim.z ? ex2(b.x) : 0.f, key < lim.w ? ex2(b.y) : 0.f));
+          }
         }
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&br.d_empty[g % kD]));
-      const float got = (acc[0] + acc[1]) + (acc[2] + acc[3]);
+      if (lane == 0) mbar_arrive_remote_relaxed(d_empty + (g % kD) * 8);
+      const float got = (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
       if (kStreamKeys) store(k, got);
       else sum += got;
     }
@@ -524,32 +568,35 @@ __device__ void sum_role(const MassParams &p, Bars &br, const Work &w, uint32_t 
 }
 
 template <bool kStreamKeys, bool kFp8, bool kPoll>
-__global__ void __launch_bounds__(threads_of(kFp8), 1)
-    attention_mass_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap q_map,
-                          const MassParams p) {
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(kFp8), 1)
+    attention_mass_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap pe_map,
+                          const __grid_constant__ CUtensorMap q_map, const MassParams p) {
   extern __shared__ __align__(1024) uint8_t smem[];
   if (smem_u32(smem) & 1023u) {
     if (threadIdx.x == 0) atomicOr(p.status, MLA_STATUS_SMEM_ALIGN);
     return;
   }
-  Bars &br = *reinterpret_cast<Bars *>(smem + OFF_BARS);
+  Bars &br = *reinterpret_cast<Bars *>(smem);
   const int warp = threadIdx.x >> 5;
+  const int pair_index = (int)cluster_id_x(), pairs = (int)gridDim.x / 2;
+  Place at;
+  at.rank = cluster_ctarank();
+  at.res = smem_u32(smem + OFF_RES);
+  at.res_block = kStreamKeys ? p.box / 2 * 128 : kBlock;
+  at.slots = at.res + kBlocks * at.res_block;
   if (threadIdx.x == 0) {
     for (int i = 0; i < kBlocks; i++) {
-      mbar_init(smem_u32(&br.res_full[i]), kFp8 && !kStreamKeys ? kWideWarps / kWideGroups : 1);
+      mbar_init(smem_u32(&br.res_full[i]), kFp8 && !kStreamKeys ? 2 * kGroupWarps : 1);
       mbar_init(smem_u32(&br.res_empty[i]), 1);
     }
     for (int i = 0; i < kMostSlots; i++) {
-      mbar_init(smem_u32(&br.slot_full[i]), kFp8 && kStreamKeys ? kWideWarps / kWideGroups : 1);
+      mbar_init(smem_u32(&br.slot_full[i]), kFp8 && kStreamKeys ? 2 * kGroupWarps : 1);
       mbar_init(smem_u32(&br.slot_empty[i]), 1);
-    }
-    for (int i = 0; i < kRaw; i++) {
       mbar_init(smem_u32(&br.raw_full[i]), 1);
-      mbar_init(smem_u32(&br.raw_empty[i]), kWideWarps / kWideGroups);
     }
     for (int i = 0; i < kD; i++) {
       mbar_init(smem_u32(&br.d_full[i]), 1);
-      mbar_init(smem_u32(&br.d_empty[i]), 4);
+      mbar_init(smem_u32(&br.d_empty[i]), 2 * kSumThreads / 32);
     }
     br.abort = 0;
     br.start_b = br.start_t = 0;
@@ -558,22 +605,27 @@ __global__ void __launch_bounds__(threads_of(kFp8), 1)
     prefetch_tensormap(&k_map);
   }
   if (warp == 1) {
-    tmem_alloc(smem_u32(&br.tmem_base), kD * kRows);
-    tmem_relinquish();
+    tmem_alloc_pair(smem_u32(&br.tmem_base), kD * kRows);
+    tmem_relinquish_pair();
   }
   grid_dep_trigger();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  cluster_sync();  // the peer's barriers exist before anything arrives on them
   const uint32_t tmem = br.tmem_base;
   grid_dep_wait();
-  const Work w = find_work<kStreamKeys>(p, br);
-  if (warp == 0) load_role<kStreamKeys, kFp8, kPoll>(p, smem, br, &k_map, &q_map, w);
-  else if (warp == 1) mma_role<kStreamKeys, kFp8>(p, smem, br, w, tmem);
-  else if (warp == 2) wait_role<kStreamKeys, kFp8, kPoll>(p, br, w);
-  else if (warp >= 4 && warp < 8) sum_role<kStreamKeys, kPoll>(p, br, w, tmem);
-  else if constexpr (kFp8) {
-    if (warp >= 8) widen_role<kStreamKeys, kPoll>(p, smem, br, w, threadIdx.x - 256);
+  const Work w = find_work(p, br, pair_index, pairs);
+  if (warp == 0) {
+    load_role<kStreamKeys, kFp8, kPoll>(p, smem, br, &k_map, &pe_map, &q_map, w, at);
+  } else if (warp == 1) {
+    if (at.rank == 0) mma_role<kStreamKeys>(p, br, w, at, tmem);
+  } else if (warp == 2) {
+    if (at.rank == 0) wait_role<kStreamKeys, kPoll>(p, br, w);
+  } else if (warp >= 4 && warp < 8) {
+    sum_role<kStreamKeys, kPoll>(p, br, w, tmem, at.rank, pair_index);
+  } else if constexpr (kFp8) {
+    if (warp >= 8) widen_role<kStreamKeys, kPoll>(p, smem, br, w, at, threadIdx.x - 256);
   }
   __syncwarp();
   tc_fence_before();
@@ -583,24 +635,35 @@ __global__ void __launch_bounds__(threads_of(kFp8), 1)
     while (globaltimer() - t0 < 2000000ull) {
     }
   }
+  __syncwarp();
+  cluster_sync();  // nothing of the peer's reads or arrives here any more
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, kD * kRows);
+    tmem_dealloc_pair(tmem, kD * kRows);
   }
 }
 
-// The parts of each key's sum, in their order.
-__global__ void __launch_bounds__(256) mass_reduce_kernel(MassParams p) {
+// Sums of tiles that several pairs have a part of, in the order of the pairs.  Block
+// p: the tile that begins in pair p and ends in another.
+__global__ void __launch_bounds__(kTileKeys) mass_reduce_kernel(MassParams p, int pairs) {
+  __shared__ int warp_sums[32], found[2];
   grid_dep_wait();
-  const int splits = *p.splits;
-  if (splits <= 1) return;
-  const int b = blockIdx.y, len = seq_len(p, b);
-  for (int n = blockIdx.x * 256 + threadIdx.x; n < len; n += gridDim.x * 256) {
-    float v = 0.f;
-    for (int s = 0; s < splits; s++) v += p.partial[((size_t)s * p.B + b) * p.cap + n];
-    float *m = p.mass + (size_t)b * p.cap + n;
-    *m = p.decay != 0.f ? fmaf(p.decay, *m, v) : v;
-  }
+  const Tiles t = count_tiles(p, warp_sums);
+  const long long units = (long long)t.total * p.n_qt;
+  const int pair = blockIdx.x;
+  const long long u0 = first_unit(units, pair, pairs), u1 = first_unit(units, pair + 1, pairs);
+  if (u0 >= u1) return;
+  const long long tile = (u1 - 1) / p.n_qt, first = tile * p.n_qt, end = first + p.n_qt;
+  if (first < u0 || end <= u1) return;  // begins before this pair, or is whole
+  find_tile(p, t, (int)tile, &found[0], &found[1]);
+  __syncthreads();
+  const int b = found[0], n = found[1] * kTileKeys + threadIdx.x;
+  if (n >= seq_len(p, b)) return;
+  float v = p.partial[((size_t)pair * 2 + 1) * kTileKeys + threadIdx.x];
+  for (int q = pair + 1; q < pairs && first_unit(units, q, pairs) < end; q++)
+    if (first_unit(units, q, pairs) < first_unit(units, q + 1, pairs)) v += p.partial[(size_t)q * 2 * kTileKeys + threadIdx.x];
+  float *m = p.mass + (size_t)b * p.cap + n;
+  *m = p.decay != 0.f ? fmaf(p.decay, *m, v) : v;
 }
 
 int fail(int code, const char *msg) {
@@ -622,11 +685,17 @@ int check_sizes(int B, int T, int H, int cap) {
   return MLA_OK;
 }
 
-// Parts of a key's sum, at most: none where a sequence's query rows are one tile.
-int most_splits(int B, int T, int H) {
-  const int n_qt = ceil_div(T * H, kRows), want = ceil_div(304, B);
-  return n_qt < want ? n_qt : want;
+int sm_pairs(int *pairs) {
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return fail(MLA_ERR_CUDA, cudaGetErrorString(e));
+  *pairs = sms / 2 > 0 ? sms / 2 : 1;
+  return MLA_OK;
 }
+
+// Room for the partial sums of twice as many pairs as any GPU of this kind has.
+constexpr size_t kMostPairs = 160;
 
 }  // namespace
 }  // namespace mla
@@ -635,8 +704,7 @@ using namespace mla;
 
 extern "C" size_t mla_attention_mass_workspace_bytes(int B, int T, int H, int mass_cap) {
   if (check_sizes(B, T, H, mass_cap) != MLA_OK) return 0;
-  const int s = most_splits(B, T, H);
-  return s <= 1 ? 0 : 256 + ((size_t)s * B * mass_cap * sizeof(float) + 255) / 256 * 256;
+  return T * H <= kRows ? 0 : kMostPairs * 2 * kTileKeys * sizeof(float);
 }
 
 extern "C" int mla_attention_mass(const void *q, const void *kv_cache, int kv_format, int num_pages, int page_size,
@@ -670,17 +738,16 @@ extern "C" int mla_attention_mass(const void *q, const void *kv_cache, int kv_fo
   if (need && !aligned(workspace, 256)) return fail(MLA_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
   MassParams p{};
   if ((rc = status_word(&p.status)) != MLA_OK) return rc;
-  int dev = 0, sms = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  int pairs = 0;
+  if ((rc = sm_pairs(&pairs)) != MLA_OK) return rc;
+  if (need && (size_t)pairs > kMostPairs) return fail(MLA_ERR_UNSUPPORTED, "more SMs than the workspace has room for");
   p.cache = static_cast<const uint8_t *>(kv_cache);
   p.kv_scales = kv_scales;
   p.block_table = block_table;
   p.seqlens = cache_seqlens;
   p.lse = lse;
   p.mass = mass;
-  p.splits = need ? static_cast<int32_t *>(workspace) : nullptr;
-  p.partial = need ? reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + 256) : nullptr;
+  p.partial = need ? static_cast<float *>(workspace) : nullptr;
   p.format = kv_format;
   p.num_pages = num_pages;
   p.max_pages = max_pages;
@@ -692,15 +759,14 @@ extern "C" int mla_attention_mass(const void *q, const void *kv_cache, int kv_fo
   p.rows = T * H;
   p.n_qt = ceil_div(p.rows, kRows);
   p.box = p.rows < kRows ? ceil_div(p.rows, 16) * 16 : kRows;
-  p.max_splits = most_splits(B, T, H);
   p.scale_log2 = softmax_scale * LOG2E;
   p.decay = decay;
   p.wait_ns = wait_limit_ns();
 
-  CUtensorMap k_map{}, q_map{};
+  CUtensorMap k_map{}, pe_map{}, q_map{};
   auto fn = tensor_map_encoder();
   if (!fn) return fail(MLA_ERR_CUDA, "cuTensorMapEncodeTiled not found");
-  bool ok = make_map_3d(&q_map, q, 64, (uint64_t)B * p.rows, kBlocks, D_QK, 64, p.box, 1);
+  bool ok = make_map_3d(&q_map, q, 64, (uint64_t)B * p.rows, kBlocks, D_QK, 64, p.box / 2, 1);
   if (ok && kv_format == MLA_KV_BF16) {
     cuuint64_t dims[4] = {64, (cuuint64_t)PAGE, kBlocks, (cuuint64_t)num_pages};
     cuuint64_t strides[3] = {(cuuint64_t)D_QK * 2, 128, (cuuint64_t)D_QK * 2 * PAGE};
@@ -716,10 +782,17 @@ extern "C" int mla_attention_mass(const void *q, const void *kv_cache, int kv_fo
     ok = fn(&k_map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(kv_cache), dims, strides, box, estr,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    if (ok && kv_format == MLA_KV_FP8_E4M3)  // the rotated part: 64 bf16 behind the codes
+      ok = make_map_3d(&pe_map, static_cast<const uint8_t *>(kv_cache) + D_V, 64, PAGE, (uint64_t)num_pages, FP8_ROW / 2,
+                       PAGE * FP8_ROW / 2, PAGE, 1);
   }
   if (!ok) return fail(MLA_ERR_CUDA, "a tensor map could not be made");
+  const uint32_t resident = kBlocks * (p.n_qt == 1 ? p.box / 2 * 128 : kBlock);
+  p.slots = (int)((kRoom - resident) / kBlock);
+  if (p.slots > kMostSlots) p.slots = kMostSlots;
+  cudaError_t e = cudaSuccess;
   const bool keys = p.n_qt == 1, fp8 = kv_format != MLA_KV_BF16, poll = p.wait_ns < kShortWaitNs;
-  using Kernel = void (*)(CUtensorMap, CUtensorMap, MassParams);
+  using Kernel = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, MassParams);
   Kernel k = nullptr;
 #define PICK(a, b, c) \
   if (keys == a && fp8 == b && poll == c) k = attention_mass_kernel<a, b, c>
@@ -728,20 +801,8 @@ extern "C" int mla_attention_mass(const void *q, const void *kv_cache, int kv_fo
 #undef PICK
   cudaStream_t s = (cudaStream_t)stream;
   if (e == cudaSuccess) e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
-  if (e == cudaSuccess) e = launch_dependent(k, sms, threads_of(fp8), kSmem, s, k_map, q_map, p);
-  if (e == cudaSuccess && need) {
-    cudaLaunchAttribute pdl[1];
-    pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    pdl[0].val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    const int blocks = ceil_div(mass_cap, 256);
-    cfg.gridDim = dim3(blocks < 64 ? blocks : 64, B);
-    cfg.blockDim = dim3(256);
-    cfg.stream = s;
-    cfg.attrs = pdl;
-    cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, mass_reduce_kernel, p);
-  }
+  if (e == cudaSuccess) e = launch_dependent(k, 2 * pairs, threads_of(fp8), kSmem, s, k_map, pe_map, q_map, p);
+  if (e == cudaSuccess && need) e = launch_dependent(mass_reduce_kernel, pairs, kTileKeys, 0, s, p, pairs);
   if (e != cudaSuccess) {
     char msg[128];
     snprintf(msg, sizeof msg, "attention mass: %s", cudaGetErrorString(e));

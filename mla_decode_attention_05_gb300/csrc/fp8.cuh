@@ -18,7 +18,12 @@ __device__ __forceinline__ void widen16(const uint4 &codes, float scale, uint4 &
     uint32_t half2;
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(half2) : "h"(pair));
     const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&half2));
-    const __nv_bfloat162 v = __floats2bfloat162_rn(f.x * scale, f.y * scale);
+    float x, y;  // both products in one instruction
+    asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %4};\n\t"
+        "mul.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(x), "=f"(y)
+        : "f"(f.x), "f"(f.y), "f"(scale));
+    const __nv_bfloat162 v = __floats2bfloat162_rn(x, y);
     o[i] = *reinterpret_cast<const uint32_t *>(&v);
   }
   lo = make_uint4(o[0], o[1], o[2], o[3]);
