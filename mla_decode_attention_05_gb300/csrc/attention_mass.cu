@@ -89,6 +89,14 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_
                : "memory");
 }
 
+// Arrives on a barrier of the pair's other CTA behind this thread's own writes to
+// shared memory.  (Release at the scope of the CTA: what it publishes is read on this
+// SM, by its half of the pair's MMA.  At cluster scope the arrive waits for all the
+// thread's writes and costs a thousand cycles.)
+__device__ __forceinline__ void mbar_arrive_pair(uint32_t cluster_bar) {
+  asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+}
+
 // Tile loads into this CTA whose bytes a barrier of either CTA of the pair counts.
 __device__ __forceinline__ void tma_load_4d_pair(uint32_t dst, const void *map, uint32_t cluster_bar, int c0, int c1, int c2,
                                                  int c3, uint64_t policy) {
@@ -295,18 +303,18 @@ __device__ void load_role(const MassParams &p, uint8_t *base, Bars &br, const CU
   };
   for_each_phase<kStreamKeys>(p, w, [&](const Phase &f) {
     if (f.i0 >= f.i1) return true;
+    // (the first of what streams is asked for along with the resident blocks, so that
+    // both follow the last phase's MMAs block by block)
     if (!kStreamKeys) look(f.b, f.t, f.len);
-    for (int kb = 0; kb < kBlocks; kb++) {
-      if (!warp_wait<kPoll>(&br, &br.res_empty[kb], rph, p)) return false;
-      if (kStreamKeys) rows(at.res + kb * at.res_block, &br.res_full[kb], f.b, 0, kb);
-      else keys(at.res + kb * at.res_block, &br.res_full[kb], &br.raw_full[kb], kb);
-      __syncwarp();
-    }
-    rph ^= 1;
-    if (!kStreamKeys) tile++;
     for (int i = f.i0; i < f.i1; i++) {
       if (kStreamKeys) look(f.b, i, f.len);
       for (int kb = 0; kb < kBlocks; kb++) {
+        if (i == f.i0) {
+          if (!warp_wait<kPoll>(&br, &br.res_empty[kb], rph, p)) return false;
+          if (kStreamKeys) rows(at.res + kb * at.res_block, &br.res_full[kb], f.b, 0, kb);
+          else keys(at.res + kb * at.res_block, &br.res_full[kb], &br.raw_full[kb], kb);
+          __syncwarp();
+        }
         if (!warp_wait<kPoll>(&br, &br.slot_empty[s], ph, p)) return false;
         if (kStreamKeys) keys(at.slots + s * kBlock, &br.slot_full[s], &br.raw_full[s], kb);
         else rows(at.slots + s * kBlock, &br.slot_full[s], f.b, i, kb);
@@ -318,6 +326,8 @@ __device__ void load_role(const MassParams &p, uint8_t *base, Bars &br, const CU
       }
       if (kStreamKeys) tile++;
     }
+    rph ^= 1;
+    if (!kStreamKeys) tile++;
     return true;
   });
 }
@@ -371,7 +381,7 @@ __device__ void widen_role(const MassParams &p, uint8_t *base, Bars &br, const W
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (first) mbar_arrive_remote(mapa(smem_u32(kStreamKeys ? &br.slot_full[k] : &br.res_full[k]), 0));
+        if (first) mbar_arrive_pair(mapa(smem_u32(kStreamKeys ? &br.slot_full[k] : &br.res_full[k]), 0));
       }
       if (++turn == kWideGroups) turn = 0;
       if (++s == p.slots) {
@@ -506,19 +516,25 @@ __device__ void sum_role(const MassParams &p, Bars &br, const Work &w, uint32_t 
     if (kStreamKeys) set_rows(f, 0);
     float sum = 0.f;
     auto key_of = [&](int t) { return t * kTileKeys + (int)rank * kKeys + i; };
+    // what a key had before is fetched while its scores are made
+    float before = 0.f;
+    bool placed = false;
+    auto prepare = [&](int t) {
+      const int n = key_of(t);
+      placed = n < f.len && page_of(p, f.b, n / PAGE, f.len) >= 0;
+      if (f.whole && p.decay != 0.f && n < f.len) before = p.mass[(size_t)f.b * p.cap + n];
+    };
     auto store = [&](int t, float v) {
       const int n = key_of(t);
       if (n >= f.len) return;
-      if (page_of(p, f.b, n / PAGE, f.len) < 0) v = 0.f;
-      if (!kStreamKeys && !f.whole) {
-        p.partial[((size_t)pair_index * 2 + f.part) * kTileKeys + rank * kKeys + i] = v;
-      } else {
-        float *m = p.mass + (size_t)f.b * p.cap + n;
-        *m = p.decay != 0.f ? fmaf(p.decay, *m, v) : v;
-      }
+      if (!placed) v = 0.f;
+      if (f.whole) p.mass[(size_t)f.b * p.cap + n] = p.decay != 0.f ? fmaf(p.decay, before, v) : v;
+      else p.partial[((size_t)pair_index * 2 + f.part) * kTileKeys + rank * kKeys + i] = v;
     };
+    if (!kStreamKeys) prepare(f.t);
     for (int k = f.i0; k < f.i1; k++, g++) {
-      if (!kStreamKeys) set_rows(f, k);
+      if (kStreamKeys) prepare(k);
+      else set_rows(f, k);
       const bool ok = warp_wait<kPoll>(&br, &br.d_full[g % kD], (g / kD) & 1, p);
       if (bar_red_or(kSumBar, 128, !ok)) return false;
       tc_fence_after();
