@@ -112,9 +112,12 @@ __device__ __forceinline__ int seq_len(const MassParams &p, int b) {
   return min(max(__ldg(p.seqlens + b), 0), most);
 }
 
+// (Acquire at the scope of the CTA also for what the peer or its MMA arrives on: what
+// is read behind these waits lies in this SM's shared or tensor memory, and at cluster
+// scope every wait would cost some 500 cycles.)
 template <bool kPoll>
 __device__ __forceinline__ bool wait_ok(Bars *b, uint64_t *bar, uint32_t parity, const MassParams &p) {
-  if (mbar_wait_limited<true, kPoll>(smem_u32(bar), parity, &b->abort, p.wait_ns)) return true;
+  if (mbar_wait_limited<false, kPoll>(smem_u32(bar), parity, &b->abort, p.wait_ns)) return true;
   atomicOr(p.status, MLA_STATUS_WAIT_TIMEOUT);
   *(volatile int *)&b->abort = 1;
   return false;
@@ -264,13 +267,25 @@ __device__ void load_role(const MassParams &p, uint8_t *base, Bars &br, const CU
   const bool scaled = p.format == MLA_KV_FP8_E4M3;
   int s = 0;
   uint32_t ph = 1, rph = 1, tile = 0;
-  int pg[2] = {-1, -1}, pages = 0;  // this CTA's pages of a tile, and how many both have
-  auto look = [&](int b, int t, int len) {
-    const int lane = threadIdx.x & 31;
-    const int page = lane < 4 ? page_of(p, b, 4 * t + lane, len) : -1;
-    pages = __popc(__ballot_sync(0xffffffffu, page >= 0));
-    pg[0] = __shfl_sync(0xffffffffu, page, 2 * at.rank);
-    pg[1] = __shfl_sync(0xffffffffu, page, 2 * at.rank + 1);
+  // This CTA's pages of a tile, and how many both CTAs have.  Lanes 0-3 look up the
+  // tile's four pages; those of the next tile while this one is asked for.
+  int pg[2] = {-1, -1}, pages = 0, entry = -1;
+  const int lane = threadIdx.x & 31;
+  auto fetch = [&](int b, int t, int len) {
+    entry = -1;
+    if (lane < 4 && (4ll * t + lane) * PAGE < len) {
+      entry = __ldg(p.block_table + (size_t)b * p.max_pages + 4 * t + lane);
+      if (entry < 0) entry = INT32_MAX;  // no page, as any outside the pool
+    }
+  };
+  auto look = [&] {
+    if (entry >= p.num_pages) {
+      atomicOr(p.status, MLA_STATUS_BAD_PAGE);
+      entry = -1;
+    }
+    pages = __popc(__ballot_sync(0xffffffffu, entry >= 0));
+    pg[0] = __shfl_sync(0xffffffffu, entry, 2 * at.rank);
+    pg[1] = __shfl_sync(0xffffffffu, entry, 2 * at.rank + 1);
   };
   auto keys = [&](uint32_t dst, uint64_t *full, uint64_t *raw, int kb) {
     if (!elect_one()) return;
@@ -305,9 +320,13 @@ __device__ void load_role(const MassParams &p, uint8_t *base, Bars &br, const CU
     if (f.i0 >= f.i1) return true;
     // (the first of what streams is asked for along with the resident blocks, so that
     // both follow the last phase's MMAs block by block)
-    if (!kStreamKeys) look(f.b, f.t, f.len);
+    fetch(f.b, f.t, f.len);
+    if (!kStreamKeys) look();
     for (int i = f.i0; i < f.i1; i++) {
-      if (kStreamKeys) look(f.b, i, f.len);
+      if (kStreamKeys) {
+        look();
+        if (i + 1 < f.i1) fetch(f.b, i + 1, f.len);
+      }
       for (int kb = 0; kb < kBlocks; kb++) {
         if (i == f.i0) {
           if (!warp_wait<kPoll>(&br, &br.res_empty[kb], rph, p)) return false;
