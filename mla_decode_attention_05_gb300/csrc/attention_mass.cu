@@ -254,14 +254,16 @@ struct Place {
 
 // ---- loads -------------------------------------------------------------------------
 
-// Warp 0: query rows and cached ones.  The whole warp waits and looks pages up, one
-// elected lane asks for the copies.  rank 0's barriers count the bytes of both
-// CTAs.  A block of FP8 rows lands as codes (64 bytes of each row) in the upper half
-// of the block that it will fill, on a barrier of this CTA; the rotated part of rows
-// with scales is bf16 and lands as it is used.
+// Warps 0 and 3: cached rows, each one page of this CTA's two; warp 0 query rows too.
+// (A warp's wait, arrival and copy take some 350 cycles together, whatever the copy's
+// size: one warp alone would take longer over a block's two pages than HBM.)  The
+// whole warp waits and looks pages up, one elected lane asks for the copies.  rank 0's
+// barriers count the bytes of both CTAs.  A block of FP8 rows lands as codes (64 bytes of each row) in
+// the upper half of the block that it will fill, on a barrier of this CTA; the
+// rotated part of rows with scales is bf16 and lands as it is used.
 template <bool kStreamKeys, bool kFp8, bool kPoll>
 __device__ void load_role(const MassParams &p, uint8_t *base, Bars &br, const CUtensorMap *k_map, const CUtensorMap *pe_map,
-                          const CUtensorMap *q_map, const Work &w, const Place &at) {
+                          const CUtensorMap *q_map, const Work &w, const Place &at, int which) {
   const uint32_t scales = smem_u32(base + OFF_SCALES);
   const uint64_t keep = policy_evict_normal(), key_pol = kStreamKeys ? policy_evict_first() : keep;
   const bool scaled = p.format == MLA_KV_FP8_E4M3;
@@ -289,26 +291,21 @@ __device__ void load_role(const MassParams &p, uint8_t *base, Bars &br, const CU
   };
   auto keys = [&](uint32_t dst, uint64_t *full, uint64_t *raw, int kb) {
     if (!elect_one()) return;
+    const int page = pg[which];
     if (!kFp8) {
-      const uint32_t bar = mapa(smem_u32(full), 0);
-      if (at.rank == 0) mbar_arrive_expect_tx(smem_u32(full), pages * kHalf);
-#pragma unroll
-      for (int h = 0; h < 2; h++)
-        if (pg[h] >= 0) tma_load_4d_pair(dst + h * kHalf, k_map, bar, 0, 0, kb, pg[h], key_pol);
+      if (which == 0 && at.rank == 0) mbar_arrive_expect_tx(smem_u32(full), pages * kHalf);
+      if (page >= 0) tma_load_4d_pair(dst + which * kHalf, k_map, mapa(smem_u32(full), 0), 0, 0, kb, page, key_pol);
       return;
     }
     const uint32_t bar = smem_u32(raw), n = (pg[0] >= 0) + (pg[1] >= 0);
     const bool codes = !(scaled && kb == 8), with = scaled && kb == 0;
-    mbar_arrive_expect_tx(bar, n * ((codes ? kHalf / 2 : kHalf) + (with ? kScaleBytes / 2 : 0)));
-#pragma unroll
-    for (int h = 0; h < 2; h++) {
-      if (pg[h] < 0) continue;
-      if (codes) tma_load_3d(dst + kHalf + h * (kHalf / 2), k_map, bar, kb * 64, 0, pg[h], key_pol);
-      else tma_load_3d(dst + h * kHalf, pe_map, bar, 0, 0, pg[h], key_pol);
-      if (with)
-        bulk_load(scales + (tile & 1) * kScaleBytes + h * (kScaleBytes / 2), p.kv_scales + (size_t)pg[h] * PAGE * 4,
-                  kScaleBytes / 2, bar);
-    }
+    if (which == 0) mbar_arrive_expect_tx(bar, n * ((codes ? kHalf / 2 : kHalf) + (with ? kScaleBytes / 2 : 0)));
+    if (page < 0) return;
+    if (codes) tma_load_3d(dst + kHalf + which * (kHalf / 2), k_map, bar, kb * 64, 0, page, key_pol);
+    else tma_load_3d(dst + which * kHalf, pe_map, bar, 0, 0, page, key_pol);
+    if (with)
+      bulk_load(scales + (tile & 1) * kScaleBytes + which * (kScaleBytes / 2), p.kv_scales + (size_t)page * PAGE * 4,
+                kScaleBytes / 2, bar);
   };
   const int half = p.box / 2;  // query rows of each CTA
   auto rows = [&](uint32_t dst, uint64_t *full, int b, int qt, int kb) {
@@ -322,18 +319,19 @@ __device__ void load_role(const MassParams &p, uint8_t *base, Bars &br, const CU
     // both follow the last phase's MMAs block by block)
     fetch(f.b, f.t, f.len);
     if (!kStreamKeys) look();
-    for (int i = f.i0; i < f.i1; i++) {
+    for (int i = f.i0; i < (kStreamKeys || which == 0 ? f.i1 : f.i0 + 1); i++) {
       if (kStreamKeys) {
         look();
         if (i + 1 < f.i1) fetch(f.b, i + 1, f.len);
       }
       for (int kb = 0; kb < kBlocks; kb++) {
-        if (i == f.i0) {
+        if (i == f.i0 && (!kStreamKeys || which == 0)) {
           if (!warp_wait<kPoll>(&br, &br.res_empty[kb], rph, p)) return false;
           if (kStreamKeys) rows(at.res + kb * at.res_block, &br.res_full[kb], f.b, 0, kb);
           else keys(at.res + kb * at.res_block, &br.res_full[kb], &br.raw_full[kb], kb);
           __syncwarp();
         }
+        if (!kStreamKeys && which == 1) continue;
         if (!warp_wait<kPoll>(&br, &br.slot_empty[s], ph, p)) return false;
         if (kStreamKeys) keys(at.slots + s * kBlock, &br.slot_full[s], &br.raw_full[s], kb);
         else rows(at.slots + s * kBlock, &br.slot_full[s], f.b, i, kb);
@@ -651,8 +649,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(kFp8), 1)
   const uint32_t tmem = br.tmem_base;
   grid_dep_wait();
   const Work w = find_work(p, br, pair_index, pairs);
-  if (warp == 0) {
-    load_role<kStreamKeys, kFp8, kPoll>(p, smem, br, &k_map, &pe_map, &q_map, w, at);
+  if (warp == 0 || warp == 3) {
+    load_role<kStreamKeys, kFp8, kPoll>(p, smem, br, &k_map, &pe_map, &q_map, w, at, warp == 3);
   } else if (warp == 1) {
     if (at.rank == 0) mma_role<kStreamKeys>(p, br, w, at, tmem);
   } else if (warp == 2) {
