@@ -272,22 +272,22 @@ __device__ void load_role(const MassParams &p, uint8_t *base, Bars &br, const CU
   // This CTA's pages of a tile, and how many both CTAs have.  Lanes 0-3 look up the
   // tile's four pages; those of the next tile while this one is asked for.
   int pg[2] = {-1, -1}, pages = 0, entry = -1;
+  bool listed = false;
   const int lane = threadIdx.x & 31;
   auto fetch = [&](int b, int t, int len) {
-    entry = -1;
-    if (lane < 4 && (4ll * t + lane) * PAGE < len) {
-      entry = __ldg(p.block_table + (size_t)b * p.max_pages + 4 * t + lane);
-      if (entry < 0) entry = INT32_MAX;  // no page, as any outside the pool
-    }
+    listed = lane < 4 && (4ll * t + lane) * PAGE < len;
+    if (listed) entry = __ldg(p.block_table + (size_t)b * p.max_pages + 4 * t + lane);
   };
   auto look = [&] {
-    if (entry >= p.num_pages) {
-      atomicOr(p.status, MLA_STATUS_BAD_PAGE);
-      entry = -1;
+    const bool good = listed && entry >= 0 && entry < p.num_pages;
+    if (listed && !good) atomicOr(p.status, MLA_STATUS_BAD_PAGE);
+    const uint32_t have = __ballot_sync(0xffffffffu, good);
+    pages = __popc(have);
+#pragma unroll
+    for (int h = 0; h < 2; h++) {
+      const int at_lane = 2 * at.rank + h, page = __shfl_sync(0xffffffffu, entry, at_lane);
+      pg[h] = (have >> at_lane) & 1 ? page : -1;
     }
-    pages = __popc(__ballot_sync(0xffffffffu, entry >= 0));
-    pg[0] = __shfl_sync(0xffffffffu, entry, 2 * at.rank);
-    pg[1] = __shfl_sync(0xffffffffu, entry, 2 * at.rank + 1);
   };
   auto keys = [&](uint32_t dst, uint64_t *full, uint64_t *raw, int kb) {
     if (!elect_one()) return;
