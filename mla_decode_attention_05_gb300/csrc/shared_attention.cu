@@ -51,13 +51,12 @@ struct Bars {
   uint64_t kv_full[kStages], kv_empty[kStages];      // rank 0: blocks 0-4 of a stage; rank 1: whole stages
   uint64_t kv_full_b[kStages], kv_empty_b[kStages];  // rank 0: blocks 5-8
   uint64_t s_full[2], s_free[2];
-  uint64_t vfull[kValidRing];
   uint64_t gfree[P_RING], pwritten[P_RING];          // rank 0: ring slot copied out by rank 1; written
   uint64_t q_ready;
   uint64_t p_full[P_RING];                           // rank 1: ring slot published
   uint64_t p_land[2], p_empty[2], o_done[2], o_ready[2];
   uint64_t lsum[4][2];
-  int valid[kValidRing];                             // keys of a tile that count
+  int valid[kValidRing];                             // rank 0: keys of a tile that count (seen through the tile's scores)
   uint32_t tmem_base;
   int abort;
 };
@@ -69,7 +68,8 @@ static_assert(kStages * kStage0 <= OFF_BARS && kSmem <= 232448, "shared memory b
 struct Meta {
   float alpha[M_TILE];
   float ell[M_TILE];
-  uint32_t flags[kSoftWarps];  // a warp has rescaled a row in this tile
+  uint32_t flags[kSoftWarps];  // of each warp: it has rescaled a row in this tile (else alpha is not written)
+  int valid;                   // keys of the tile that count
 };
 static_assert(kPBytes + sizeof(Meta) <= P_SLOT_BYTES, "P ring slot");
 
@@ -173,8 +173,7 @@ __device__ void load_role(const Ctx &c, const CUtensorMap *map, const CUtensorMa
         const int page = __shfl_sync(0xffffffffu, pg, i);
         bool ok = true;
         if (lane == 0) {
-          br.valid[g % kValidRing] = page < 0 ? 0 : min(PAGE, it.len - (base + i) * PAGE);
-          mbar_arrive(smem_u32(&br.vfull[g % kValidRing]));
+          if (c.rank == 0) br.valid[g % kValidRing] = page < 0 ? 0 : min(PAGE, it.len - (base + i) * PAGE);
           ok = wait_ok(c, &br.kv_empty[s], ph);
           if (ok) {
             const uint32_t bar = smem_u32(&br.kv_full[s]);
@@ -400,10 +399,9 @@ __device__ void softmax_role(const Ctx &c, uint32_t tmem, int w, int lane) {
     const int len = it.own ? row_kv_len(it.len, p.T, min(it.row0 + r, p.T * p.H - 1) / p.H, p.causal) : it.len;
     float m_ref = -INFINITY, l = 0.f, l_all = 0.f;
     for (int t = t0; t < t1; t++, g++) {
-      const uint32_t b = g & 1, u = g >> 1, vi = g % kValidRing;
-      if (!warp_wait(c, &br.vfull[vi], (g / kValidRing) & 1)) return false;
-      const int lim = min(br.valid[vi], len - t * PAGE);
+      const uint32_t b = g & 1, u = g >> 1;
       if (!warp_wait(c, &br.s_full[b], u & 1)) return false;
+      const int valid = br.valid[g % kValidRing], lim = min(valid, len - t * PAGE);
       tc_fence_after();
       float own[32], oth[32];
       tmem_ld32(lt + TM_S + b * 64 + hf * 32, *reinterpret_cast<uint32_t(*)[32]>(&own[0]));
@@ -427,7 +425,7 @@ __device__ void softmax_role(const Ctx &c, uint32_t tmem, int w, int lane) {
       }
       const float nb = m_ref == -INFINITY ? 0.f : -m_ref * cs;
       const uint32_t gs = g % P_RING;
-      if (!warp_wait<true>(c, &br.gfree[gs], ((g / P_RING) & 1) ^ 1)) return false;
+      if (!warp_wait(c, &br.gfree[gs], ((g / P_RING) & 1) ^ 1)) return false;
       uint8_t *slot = p.ring + ((size_t)c.part * P_RING + gs) * P_SLOT_BYTES;
       float psum = 0.f;
 #pragma unroll
@@ -443,9 +441,10 @@ __device__ void softmax_role(const Ctx &c, uint32_t tmem, int w, int lane) {
       }
       l += psum;
       Meta *mo = reinterpret_cast<Meta *>(slot + kPBytes);
-      if (hf == 0) mo->alpha[r] = alpha;
       const bool any = __any_sync(0xffffffffu, resc);
+      if (any && hf == 0) mo->alpha[r] = alpha;
       if (lane == 0) mo->flags[w - 4] = any ? 1u : 0u;
+      if (w == 4 && lane == 0) mo->valid = valid;
       if (t == t1 - 1) {  // the row's two halves meet
         float *lp = lpart + (pc & 1) * 2 * M_TILE;
         lp[hf * M_TILE + r] = l;
@@ -502,7 +501,7 @@ __device__ void output_role(const Ctx &c, uint32_t tmem, int w, int lane) {
   for_each_piece(p, c.part, [&](const SharedItem &it, int t0, int t1, int slot_out) {
     float ell = 0.f;
     for (int t = t0; t < t1; t++, g++) {
-      const uint32_t b = g & 1, u = g >> 1, gs = g % P_RING, vi = g % kValidRing;
+      const uint32_t b = g & 1, u = g >> 1, gs = g % P_RING;
       if (!warp_wait<true>(c, &br.p_full[gs], (g / P_RING) & 1)) return false;
       const uint8_t *slot = p.ring + ((size_t)c.part * P_RING + gs) * P_SLOT_BYTES;
       const uint4 *src = reinterpret_cast<const uint4 *>(slot);
@@ -512,10 +511,8 @@ __device__ void output_role(const Ctx &c, uint32_t tmem, int w, int lane) {
       const Meta *m = reinterpret_cast<const Meta *>(slot + kPBytes);
       const uint4 f0 = __ldcg(reinterpret_cast<const uint4 *>(m->flags));
       const uint4 f1 = __ldcg(reinterpret_cast<const uint4 *>(m->flags) + 1);
-      const float alpha = __ldcg(&m->alpha[r]);
+      const int valid = __ldcg(&m->valid);
       if (t == t1 - 1) ell = __ldcg(&m->ell[r]);
-      if (!warp_wait(c, &br.vfull[vi], (g / kValidRing) & 1)) return false;
-      const int valid = br.valid[vi];
       if (!warp_wait(c, &br.p_empty[b], (u & 1) ^ 1)) return false;
 #pragma unroll
       for (int k = 0; k < 4; k++) st_shared_v4(pbuf + b * kPBytes + (e + 256 * k) * 16, v[k]);
@@ -525,12 +522,17 @@ __device__ void output_role(const Ctx &c, uint32_t tmem, int w, int lane) {
         for (int i = valid * 64 + e; i < PAGE * 64; i += 256)
           st_shared_v4(stage + ((i >> 3) & 7) * kBlk + (i >> 6) * 128 + (i & 7) * 16, make_uint4(0, 0, 0, 0));
       }
+      // (the rescales' factors are read from the slot only where there are any)
+      const bool rescale = (f0.x | f0.y | f0.z | f0.w | f1.x | f1.y | f1.z | f1.w) != 0u;
+      const bool mine = (q == 0 ? f0.x : q == 1 ? f0.y : q == 2 ? f0.z : f0.w) != 0u;  // this row group's
+      float alpha = 1.f;
+      if (mine) alpha = __ldcg(&m->alpha[r]);
       // the slot goes back once this warp's loads are done: the chunks are consumed
       // by the stores above, the rest by this (a release would wait for the stores too)
       {
         uint32_t dep;
         asm volatile("add.u32 %0, %1, %2;" : "=r"(dep) : "r"(__float_as_uint(alpha)), "r"(__float_as_uint(ell)));
-        asm volatile("" ::"r"(dep), "r"(f0.x), "r"(f1.w));
+        asm volatile("" ::"r"(dep), "r"(f0.x), "r"(f1.w), "r"(valid));
       }
       fence_proxy_async_smem();
       __syncwarp();
@@ -538,7 +540,7 @@ __device__ void output_role(const Ctx &c, uint32_t tmem, int w, int lane) {
         mbar_arrive(smem_u32(&br.p_land[b]));
         mbar_arrive_remote_relaxed(gfree + gs * 8);
       }
-      if ((f0.x | f0.y | f0.z | f0.w | f1.x | f1.y | f1.z | f1.w) != 0u) {  // rare: O *= alpha between two products
+      if (rescale) {  // rare: O *= alpha between two products
         if (!warp_wait(c, &br.o_done[(g - 1) & 1], ((g - 1) >> 1) & 1)) return false;
         tc_fence_after();
         for (int cc = 0; cc < 8; cc++) {
@@ -600,7 +602,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       mbar_init(smem_u32(&br.kv_full_b[s]), 1);
       mbar_init(smem_u32(&br.kv_empty_b[s]), 1);
     }
-    for (int i = 0; i < kValidRing; i++) mbar_init(smem_u32(&br.vfull[i]), 1);
     for (int i = 0; i < P_RING; i++) {
       mbar_init(smem_u32(&br.gfree[i]), kSoftWarps);
       mbar_init(smem_u32(&br.pwritten[i]), kSoftWarps);
