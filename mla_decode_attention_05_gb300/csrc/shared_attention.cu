@@ -20,6 +20,7 @@
 #include <cudaTypedefs.h>
 
 #include "dependent.cuh"
+#include "pairs_f32.cuh"
 #include "ptx.cuh"
 #include "shared_prefix.cuh"
 #include "tma_map.cuh"
@@ -38,6 +39,7 @@ constexpr uint32_t kStage1 = 8 * kBlk;      // rank 1: one page of values
 constexpr uint32_t kPBytes = M_TILE * 128;  // P tile: 128 rows x 64 tokens bf16
 constexpr int kValidRing = 8;
 constexpr int kPublishBatch = 4;
+constexpr uint32_t kFreeBatch = 4;          // P slots that rank 0 waits for at once
 constexpr int kSplit = 5;                   // rank 0: blocks of a page's first box
 constexpr float kRescale = 8.0f;            // log2 units
 
@@ -358,11 +360,22 @@ __device__ __noinline__ void load_q(uint32_t lane_tmem, uint32_t stage, int row,
   tmem_wait_st();
 }
 
+// The largest of three (one instruction).
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
 __device__ __forceinline__ float max32(const float (&v)[32]) {
-  float m[8];
+  float m[4];
 #pragma unroll
-  for (int k = 0; k < 8; k++) m[k] = fmaxf(fmaxf(v[k], v[k + 8]), fmaxf(v[k + 16], v[k + 24]));
-  return fmaxf(fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])), fmaxf(fmaxf(m[4], m[5]), fmaxf(m[6], m[7])));
+  for (int k = 0; k < 4; k++) {
+    m[k] = max3(v[8 * k], v[8 * k + 1], v[8 * k + 2]);
+    m[k] = max3(m[k], v[8 * k + 3], v[8 * k + 4]);
+    m[k] = max3(m[k], v[8 * k + 5], v[8 * k + 6]);
+  }
+  return max3(max3(max3(m[0], v[7], v[15]), m[1], m[2]), max3(m[3], v[23], v[31]), m[0]);
 }
 
 // Scores from `lim` on become -inf.
@@ -425,21 +438,26 @@ __device__ void softmax_role(const Ctx &c, uint32_t tmem, int w, int lane) {
       }
       const float nb = m_ref == -INFINITY ? 0.f : -m_ref * cs;
       const uint32_t gs = g % P_RING;
-      if (!warp_wait(c, &br.gfree[gs], ((g / P_RING) & 1) ^ 1)) return false;
+      // (slots come back in order: one wait for the last of four)
+      if (g % kFreeBatch == 0) {
+        const uint32_t ahead = g | (kFreeBatch - 1);
+        if (!warp_wait(c, &br.gfree[ahead % P_RING], ((ahead / P_RING) & 1) ^ 1)) return false;
+      }
       uint8_t *slot = p.ring + ((size_t)c.part * P_RING + gs) * P_SLOT_BYTES;
-      float psum = 0.f;
+      float2 psum = make_float2(0.f, 0.f);
 #pragma unroll
       for (int cc = 0; cc < 4; cc++) {  // chunk-major: chunk ch of row r at ch * 2048 + r * 16
         uint32_t wv[4];
 #pragma unroll
         for (int e = 0; e < 4; e++) {
-          const float p0 = ex2(fmaf(own[cc * 8 + 2 * e], cs, nb)), p1 = ex2(fmaf(own[cc * 8 + 2 * e + 1], cs, nb));
-          psum += p0 + p1;
-          wv[e] = pack_bf16(p0, p1);
+          const float2 x = fma2(make_float2(own[cc * 8 + 2 * e], own[cc * 8 + 2 * e + 1]), make_float2(cs, cs), make_float2(nb, nb));
+          const float2 pr = make_float2(ex2(x.x), ex2(x.y));
+          psum = add2(psum, pr);
+          wv[e] = pack_bf16(pr.x, pr.y);
         }
         *reinterpret_cast<uint4 *>(slot + (hf * 4 + cc) * 2048 + r * 16) = make_uint4(wv[0], wv[1], wv[2], wv[3]);
       }
-      l += psum;
+      l += psum.x + psum.y;
       Meta *mo = reinterpret_cast<Meta *>(slot + kPBytes);
       const bool any = __any_sync(0xffffffffu, resc);
       if (any && hf == 0) mo->alpha[r] = alpha;
