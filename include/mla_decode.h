@@ -492,7 +492,8 @@ int mla_value_project(const void *attn, int64_t ld_token, int64_t ld_head, const
  * skipped and sets MLA_STATUS_BAD_PAGE.  Asynchronous on `stream`; can be captured in a
  * CUDA graph.  Returns MLA_OK or a negative code.
  */
-size_t mla_decode_shared_workspace_bytes(int B, int T, int H, int G, int kv_format, int max_prefix_pages);
+size_t mla_decode_shared_workspace_bytes(int B, int T, int H, int G, int kv_format, int max_prefix_pages,
+                                         int max_pages);
 int mla_decode_shared(const void *q, const void *kv_cache, int kv_format, int num_pages, int page_size,
                       const int32_t *prefix_table, int max_prefix_pages, const int32_t *prefix_lens,
                       const int32_t *group_offsets, int G, const int32_t *block_table, int max_pages,

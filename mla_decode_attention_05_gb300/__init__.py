@@ -91,7 +91,7 @@ def lib():
             L.mla_value_project.argtypes = [P, i64, i64, P, i64, i64, i, i, P, P]
             L.mla_decode_shared.argtypes = [P, P, i, i, i, P, i, P, P, i, P, i, P, P, ctypes.c_float, i, P, sz, P, P,
                                             i, i, i, P]
-            L.mla_decode_shared_workspace_bytes.argtypes = [i, i, i, i, i, i]
+            L.mla_decode_shared_workspace_bytes.argtypes = [i, i, i, i, i, i, i]
             L.mla_decode_shared_workspace_bytes.restype = sz
             L.mla_attention_mass.argtypes = [P, P, i, i, i, P, i, P, P, P, ctypes.c_float, i, ctypes.c_float, P, i, P, sz,
                                              i, i, i, P]
@@ -752,7 +752,7 @@ def decode_shared(q: torch.Tensor, kv_cache: torch.Tensor, prefix_table: torch.T
     if tuple(out.shape) != (B, T, H, D_V) or tuple(lse.shape) != (B, H, T):
         raise ValueError(f"out must be [{B}, {T}, {H}, {D_V}] and lse [{B}, {H}, {T}]")
     if workspace is None:
-        workspace = torch.empty(decode_shared_workspace_bytes(B, T, H, G, fmt, width, dev), dtype=torch.uint8, device=dev)
+        workspace = torch.empty(decode_shared_workspace_bytes(B, T, H, G, fmt, width, block_table.shape[1], dev), dtype=torch.uint8, device=dev)
     _need(workspace, "workspace", workspace.dtype, dev)
     _call("mla_decode_shared", dev, q.data_ptr(), kv_cache.data_ptr(), fmt, kv_cache.shape[0], kv_cache.shape[1],
           prefix_table.data_ptr(), width, prefix_lens.data_ptr(), _at(group_offsets), G, block_table.data_ptr(),
@@ -763,12 +763,13 @@ def decode_shared(q: torch.Tensor, kv_cache: torch.Tensor, prefix_table: torch.T
 
 
 def decode_shared_workspace_bytes(B: int, T: int, H: int, G: int, kv_format: int, max_prefix_pages: int,
-                                  device=None) -> int:
+                                  max_pages: int, device=None) -> int:
     """Workspace of decode_shared() for B sequences in G groups (kv_format:
-    KV_BF16, KV_FP8_E4M3 or KV_FP8_E4M3_TENSOR) on `device` (default: the
-    current one)."""
+    KV_BF16, KV_FP8_E4M3 or KV_FP8_E4M3_TENSOR) whose page tables have
+    max_prefix_pages and max_pages columns, on `device` (default: the current
+    one)."""
     with torch.cuda.device(device if device is not None else torch.cuda.current_device()):
-        n = int(lib().mla_decode_shared_workspace_bytes(B, T, H, G, kv_format, max_prefix_pages))
+        n = int(lib().mla_decode_shared_workspace_bytes(B, T, H, G, kv_format, max_prefix_pages, max_pages))
     if n == 0:
         raise MlaError(-1, lib().mla_last_error_string().decode())
     return n

@@ -120,18 +120,15 @@ __device__ __forceinline__ bool for_each_piece(const SharedParams &p, int part, 
 // rank 0's ring carries, per piece, the query rows (one stage for 64 rows) before the keys.
 __device__ __forceinline__ int q_stages(const SharedItem &it) { return it.rows > 64 ? 2 : 1; }
 
+// (A widened page lies at its entry's place among the tables' entries.)
 __device__ __forceinline__ int page_of(const SharedParams &p, const SharedItem &it, int tile) {
-  int page, most = p.num_pages;
-  if (it.own) {
-    page = __ldg(p.block_table + (size_t)it.src * p.max_pages + tile);
-  } else {
-    page = __ldg(p.prefix_table + (size_t)it.src * p.max_prefix + tile);
-    // (a page of a widened prefix lies at its place in the table)
-    if (p.format != MLA_KV_BF16 && page >= 0 && page < most) page = it.src * p.max_prefix + tile, most = page + 1;
+  const int width = it.own ? p.max_pages : p.max_prefix;
+  const int page = __ldg((it.own ? p.block_table : p.prefix_table) + (size_t)it.src * width + tile);
+  if (page < 0 || page >= p.num_pages) {
+    atomicOr(p.status, MLA_STATUS_BAD_PAGE);
+    return -1;
   }
-  if (page >= 0 && page < most) return page;
-  atomicOr(p.status, MLA_STATUS_BAD_PAGE);
-  return -1;
+  return p.format == MLA_KV_BF16 ? page : (it.own ? p.G * p.max_prefix : 0) + it.src * width + tile;
 }
 
 // ---- warp 0: loads --------------------------------------------------------------------
@@ -689,7 +686,7 @@ cudaError_t launch_shared_attention(const SharedParams &p, cudaStream_t stream) 
   if (!fn) return cudaErrorNotSupported;
   const bool wide = p.format != MLA_KV_BF16;
   const uint8_t *pool = wide ? p.scratch : p.cache;
-  const cuuint64_t pages = wide ? (cuuint64_t)p.G * p.max_prefix : (cuuint64_t)p.num_pages;
+  const cuuint64_t pages = wide ? (cuuint64_t)p.scratch_pages : (cuuint64_t)p.num_pages;
   cuuint64_t dims[4] = {64, (cuuint64_t)PAGE, 9, pages};
   cuuint64_t strides[3] = {(cuuint64_t)D_QK * 2, 128, (cuuint64_t)D_QK * 2 * PAGE};
   cuuint32_t estr[4] = {1, 1, 1, 1};

@@ -62,28 +62,40 @@ __device__ inline int last_le(int n, int x, At at) {
   return lo;
 }
 
+constexpr int kGroupCache = 256;  // groups that are kept in shared memory
+
 struct SchedShared {
   int C[kMaxItems + 1];
+  uint8_t head[kMaxItems];
+  int4 groups[kGroupCache];
   int warp_sums[32];
   int carry, top;
 };
 
-// mla_decode_metadata's rule over n items of tiles(i) key tiles: an item costs
-// head(i) + tiles(i) on a line, which is cut into `parts` equal segments.  Writes the
-// segments, the pieces of each item and its first slot of results; `least`: slots
-// that every item has at least.
-template <class Head, class Tiles, class Slot>
-__device__ void schedule(SchedShared &sh, int n, int parts, int least, int32_t *md_out, int32_t *pieces, Head head, Tiles tiles,
-                         Slot slot) {
+struct Cost {
+  int head, tiles;
+};
+
+// mla_decode_metadata's rule over n items: item i costs head + tiles, as item(i) says, on a
+// line that is cut into `parts` equal segments.  Writes the segments, the pieces
+// of each item and its first slot of results; `least`: slots that every item has
+// at least.
+template <class Item, class Slot>
+__device__ void schedule(SchedShared &sh, int n, int parts, int least, int32_t *md_out, int32_t *pieces, Item item, Slot slot) {
   const int tid = threadIdx.x;
   if (tid == 0) { sh.carry = 0; sh.C[0] = 0; }
   __syncthreads();
   for (int base = 0; base < n; base += kSchedThreads) {
     const int i = base + tid;
-    const int incl = block_scan(i < n ? head(i) + tiles(i) : 0, sh.warp_sums, Add());
-    if (i < n) sh.C[i + 1] = sh.carry + incl;
+    Cost cost = {0, 0};
+    if (i < n) {
+      cost = item(i);
+      sh.head[i] = (uint8_t)cost.head;
+    }
+    const int incl = block_scan(cost.head + cost.tiles, sh.warp_sums, Add()) + sh.carry;
+    if (i < n) sh.C[i + 1] = incl;
     __syncthreads();
-    if (tid == kSchedThreads - 1) sh.carry += incl;
+    if (tid == kSchedThreads - 1) sh.carry = incl;
     __syncthreads();
   }
   const int W = sh.C[n], L = max(ceil_div(W, parts), 1);
@@ -94,7 +106,7 @@ __device__ void schedule(SchedShared &sh, int n, int parts, int least, int32_t *
       const int lo = (int)at, hi = min(lo + L, W);
       auto C = [&](int i) { return sh.C[i]; };
       const int a = last_le(n, lo, C), z = last_le(n, hi - 1, C);
-      const int fa = sh.C[a] + head(a), fz = sh.C[z] + head(z);  // where their first tiles lie
+      const int fa = sh.C[a] + sh.head[a], fz = sh.C[z] + sh.head[z];  // where their first tiles lie
       const int na = sh.C[a + 1] - fa, nz = sh.C[z + 1] - fz;
       lo4 = make_int4(a, min(max(lo - fa, 0), na), z, min(max(hi - fz, 0), nz));
       hi4 = make_int4(na > 0 ? max(p - fa / L, 0) : 0, sh.C[a] == lo ? 1 : 0, 0, 0);
@@ -108,15 +120,15 @@ __device__ void schedule(SchedShared &sh, int n, int parts, int least, int32_t *
     const int i = base + tid;
     int room = 0;
     if (i < n) {
-      const int first = sh.C[i] + head(i), k = sh.C[i + 1] - first;
+      const int first = sh.C[i] + sh.head[i], k = sh.C[i + 1] - first;
       const int got = k == 0 ? 0 : (first + k - 1) / L - first / L + 1;
       pieces[i] = got;
       room = max(got, least);
     }
-    const int incl = block_scan(room, sh.warp_sums, Add());
-    if (i < n) slot(i, sh.carry + incl - room, sh.carry + incl);
+    const int incl = block_scan(room, sh.warp_sums, Add()) + sh.carry;
+    if (i < n) slot(i, incl - room, incl);
     __syncthreads();
-    if (tid == kSchedThreads - 1) sh.carry += incl;
+    if (tid == kSchedThreads - 1) sh.carry = incl;
     __syncthreads();
   }
 }
@@ -135,7 +147,7 @@ __global__ void __launch_bounds__(kSchedThreads) shared_schedule_kernel(SharedPa
   const int tid = threadIdx.x, TH = p.T * p.H;
   grid_dep_trigger();
   grid_dep_wait();
-  const bool wide = p.format != MLA_KV_BF16;
+  const bool apart = p.md_o != nullptr;  // own tokens go another way
   auto length = [&](int n, int pages) {
     const int most = pages > 0x7fffffff / PAGE ? 0x7fffffff : pages * PAGE;
     if (n < 0 || n > most) atomicOr(p.status, MLA_STATUS_BAD_SEQLEN);
@@ -144,8 +156,8 @@ __global__ void __launch_bounds__(kSchedThreads) shared_schedule_kernel(SharedPa
   if (blockIdx.x == 1) {
     for (int b = tid; b < p.B; b += kSchedThreads) p.lens_o[b] = length(p.seqlens[b], p.max_pages);
     __syncthreads();
-    schedule(sh, p.B * p.n_mt, p.parts, 2, p.md_o, p.cnt_o, [](int) { return FIXED_COST; },
-             [&](int i) { return ceil_div(own_keys(p, p.lens_o[i % p.B], i / p.B), PAGE); },
+    schedule(sh, p.B * p.n_mt, p.parts, 2, p.md_o, p.cnt_o,
+             [&](int i) { return Cost{FIXED_COST, ceil_div(own_keys(p, p.lens_o[i % p.B], i / p.B), PAGE)}; },
              [&](int i, int at, int end) {
                if (i == 0) p.ns_o[0] = 0;
                p.ns_o[i + 1] = end;
@@ -154,7 +166,7 @@ __global__ void __launch_bounds__(kSchedThreads) shared_schedule_kernel(SharedPa
   }
   // groups: {first sequence, end, first item, keys}; items are numbered among the
   // groups that have keys and sequences
-  int4 *groups = p.groups;
+  int4 *groups = p.G <= kGroupCache ? sh.groups : p.groups;
   if (tid == 0) { sh.carry = 0; sh.top = 0; }
   __syncthreads();
   for (int base = 0; base < p.G; base += kSchedThreads) {
@@ -185,49 +197,52 @@ __global__ void __launch_bounds__(kSchedThreads) shared_schedule_kernel(SharedPa
     }
     __syncthreads();
   }
-  const int n_prefix = sh.carry, n_items = n_prefix + (wide ? 0 : p.B * p.n_mt);
+  const int n_prefix = sh.carry, n_items = n_prefix + (apart ? 0 : p.B * p.n_mt);
   if (tid == 0) *p.n_prefix = n_prefix;
   __syncthreads();
   for (int b = tid; b < p.B; b += kSchedThreads) {
     const int4 g = groups[last_le(p.G, b, [&](int i) { return i == 0 ? 0 : groups[i].x; })];
     p.seq[b] = g.w > 0 && b >= g.x && b < g.y ? make_int2(g.z, (b - g.x) * TH) : make_int2(-1, 0);
   }
-  for (int i = tid; i < n_items; i += kSchedThreads) {
-    SharedItem it;
-    if (i < n_prefix) {
-      const int g = last_le(p.G, i, [&](int k) { return groups[k].z; });
-      const int4 at = groups[g];
-      const int row = (i - at.z) * M_TILE;
-      it = SharedItem{at.x * TH + row, min(M_TILE, (at.y - at.x) * TH - row), at.w, ceil_div(at.w, PAGE), g, 0, 0, 0};
-    } else {
-      const int b = (i - n_prefix) % p.B, mt = (i - n_prefix) / p.B, n = length(p.seqlens[b], p.max_pages);
-      it = SharedItem{b * TH + mt * M_TILE, min(M_TILE, TH - mt * M_TILE), n, ceil_div(own_keys(p, n, mt), PAGE), b, 1,
-                      mt * M_TILE, 0};
-    }
-    p.items[i] = it;
-  }
-  __syncthreads();
   // An item's head: its queries' way into tensor memory and its results' way out,
   // in tiles of 1 us (items of one tile each: 5.6 us beside the tile with 128 rows, 2.8 with 16).
-  schedule(sh, n_items, p.parts, 0, p.md, p.pieces, [&](int i) { return 2 + ceil_div(p.items[i].rows, 32); },
-           [&](int i) { return p.items[i].tiles; },
+  schedule(sh, n_items, p.parts, 0, p.md, p.pieces,
+           [&](int i) {
+             SharedItem it;
+             if (i < n_prefix) {
+               const int g = last_le(p.G, i, [&](int k) { return groups[k].z; });
+               const int4 at = groups[g];
+               const int row = (i - at.z) * M_TILE;
+               it = SharedItem{at.x * TH + row, min(M_TILE, (at.y - at.x) * TH - row), at.w, ceil_div(at.w, PAGE), g, 0, 0, 0};
+             } else {
+               const int b = (i - n_prefix) % p.B, mt = (i - n_prefix) / p.B, n = length(p.seqlens[b], p.max_pages);
+               it = SharedItem{b * TH + mt * M_TILE, min(M_TILE, TH - mt * M_TILE), n, ceil_div(own_keys(p, n, mt), PAGE), b,
+                               1, mt * M_TILE, 0};
+             }
+             p.items[i] = it;
+             return Cost{2 + ceil_div(it.rows, 32), it.tiles};
+           },
            [&](int i, int at, int) { p.items[i].slot = at; });
 }
 
-// FP8 prefixes: page j of group g as bf16 rows (zeros behind the last token), once for all the
-// group's tiles.  A warp a row: lane l widens 16 of its values, and lanes 0-3 or
-// 0-7 the rotated part.
+// FP8: page j of table row y as bf16 rows (zeros behind the last token), once for all the
+// tiles that read it: prefixes first, then own pages where there is room for them.  A warp a
+// row: lane l widens 16 of its values, and lanes 0-3 or 0-7 the rotated part.
 __global__ void __launch_bounds__(256) shared_widen_kernel(SharedParams p) {
   grid_dep_trigger();
   grid_dep_wait();
-  const int g = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int n = (int)min((long long)max(p.prefix_lens[g], 0), (long long)p.max_prefix * PAGE);
+  const bool own = (int)blockIdx.y >= p.G;
+  const int row = own ? blockIdx.y - p.G : blockIdx.y, width = own ? p.max_pages : p.max_prefix;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int n = (int)min((long long)max((own ? p.seqlens : p.prefix_lens)[row], 0), (long long)width * PAGE);
+  const int32_t *table = (own ? p.block_table : p.prefix_table) + (size_t)row * width;
+  uint8_t *first = p.scratch + ((own ? (size_t)p.G * p.max_prefix : 0) + (size_t)row * width) * PAGE * D_QK * 2;
   const bool tensor = p.format == MLA_KV_FP8_E4M3_TENSOR;
   const int row_bytes = tensor ? D_QK : FP8_ROW;
   for (int j = blockIdx.x; (long long)j * PAGE < n; j += gridDim.x) {
-    const int page = p.prefix_table[(size_t)g * p.max_prefix + j];
+    const int page = table[j];
     if (page < 0 || page >= p.num_pages) continue;
-    uint8_t *to = p.scratch + ((size_t)g * p.max_prefix + j) * PAGE * D_QK * 2;
+    uint8_t *to = first + (size_t)j * PAGE * D_QK * 2;
 #pragma unroll 4
     for (int r = warp; r < PAGE; r += 8) {
       const size_t at = (size_t)page * PAGE + r;
@@ -266,15 +281,17 @@ __device__ __forceinline__ void ld_cg_v8(float (&v)[8], const float *ptr) {
   for (int j = 0; j < 8; j++) v[j] = __uint_as_float(u[j]);
 }
 
-// Lane: a query row; warp: 8 of its columns (one chunk of the partials); block: 32
-// rows x 64 columns.  Rows side by side lie side by side in the partials, so a
-// warp reads 1 KB at once; four parts are on their way together.
+// Lane: a query row; warp: kChunks * 8 of its columns; block: 32 rows and the columns
+// of its eight warps.  Rows side by side lie side by side in the partials, so a warp
+// reads 1 KB at once.  The first part of each side is asked for with the first
+// log-sum-exps, before its weight is known.
+template <int kChunks>
 __global__ void __launch_bounds__(kJoinWarps * 32) shared_join_kernel(SharedParams p) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, TH = p.T * p.H;
-  const int R = blockIdx.x * 32 + lane, chunk = blockIdx.y * kJoinWarps + warp;
-  const bool live = R < p.B * TH;
+  const int R = blockIdx.x * 32 + lane, chunk = (blockIdx.y * kJoinWarps + warp) * kChunks;
+  const bool live = R < p.B * TH, apart = p.md_o != nullptr;
   const int b = live ? R / TH : 0, r = live ? R % TH : 0;
-  const float *lse[2], *o[2];
+  const float *lse[2] = {p.lse_p, p.lse_p}, *o[2] = {p.o_p, p.o_p};
   int n[2] = {0, 0};
   // (the schedule was complete before the kernel before this one began its work)
   if (live) {
@@ -282,56 +299,77 @@ __global__ void __launch_bounds__(kJoinWarps * 32) shared_join_kernel(SharedPara
     if (s.x >= 0) {
       const int row = s.y + r, i = s.x + row / M_TILE, slot = p.items[i].slot, at = row % M_TILE;
       n[0] = p.pieces[i];
-      lse[0] = p.lse_p + (size_t)slot * M_TILE + at;
-      o[0] = p.o_p + (((size_t)slot * 64 + chunk) * M_TILE + at) * 8;
+      lse[0] += (size_t)slot * M_TILE + at;
+      o[0] += (((size_t)slot * 64 + chunk) * M_TILE + at) * 8;
     }
     const int k = (r / M_TILE) * p.B + b, at = r % M_TILE;
-    const bool wide = p.format != MLA_KV_BF16;
-    const int i = wide ? k : *p.n_prefix + k, slot = wide ? p.ns_o[i] : p.items[i].slot;
-    n[1] = wide ? p.cnt_o[i] : p.pieces[i];
-    lse[1] = (wide ? p.lse_o : p.lse_p) + (size_t)slot * M_TILE + at;
-    o[1] = (wide ? p.o_o : p.o_p) + (((size_t)slot * 64 + chunk) * M_TILE + at) * 8;
+    const int i = apart ? k : *p.n_prefix + k, slot = apart ? p.ns_o[i] : p.items[i].slot;
+    n[1] = apart ? p.cnt_o[i] : p.pieces[i];
+    lse[1] = (apart ? p.lse_o : p.lse_p) + (size_t)slot * M_TILE + at;
+    o[1] = (apart ? p.o_o : p.o_p) + (((size_t)slot * 64 + chunk) * M_TILE + at) * 8;
   }
   grid_dep_wait();
   if (!live) return;
-  constexpr size_t kNext = (size_t)64 * M_TILE * 8;
-  float m = -INFINITY;
+  constexpr size_t kNext = (size_t)64 * M_TILE * 8, kChunk = (size_t)M_TILE * 8;
+  float v[2][kChunks][8], first[2];
+#pragma unroll
+  for (int k = 0; k < 2; k++) {
+    first[k] = -INFINITY;
+    if (n[k] > 0) {
+      first[k] = __ldcg(lse[k]);
+#pragma unroll
+      for (int c = 0; c < kChunks; c++) ld_cg_v8(v[k][c], o[k] + c * kChunk);
+    }
+  }
+  float m = fmaxf(first[0], first[1]);
 #pragma unroll
   for (int k = 0; k < 2; k++)
 #pragma unroll 4
-    for (int j = 0; j < n[k]; j++) m = fmaxf(m, __ldcg(lse[k] + (size_t)j * M_TILE));
-  float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, sum = 0.f;
-  if (m != -INFINITY) {
+    for (int j = 1; j < n[k]; j++) m = fmaxf(m, __ldcg(lse[k] + (size_t)j * M_TILE));
+  float acc[kChunks][8], sum = 0.f;
 #pragma unroll
-    for (int k = 0; k < 2; k++)
-      for (int j0 = 0; j0 < n[k]; j0 += 4) {
-        float v[4][8], l[4];
+  for (int c = 0; c < kChunks; c++)
 #pragma unroll
-        for (int j = 0; j < 4; j++) {
-          l[j] = -INFINITY;
-          if (j0 + j < n[k]) {
-            l[j] = __ldcg(lse[k] + (size_t)(j0 + j) * M_TILE);
-            ld_cg_v8(v[j], o[k] + (j0 + j) * kNext);
-          }
-        }
+    for (int e = 0; e < 8; e++) acc[c][e] = 0.f;
+  auto add = [&](float l, const float(&part)[kChunks][8]) {
+    if (l == -INFINITY) return;
+    const float w = exp2f(l - m);
+    sum += w;
 #pragma unroll
-        for (int j = 0; j < 4; j++) {
-          if (l[j] == -INFINITY) continue;
-          const float w = exp2f(l[j] - m);
-          sum += w;
+    for (int c = 0; c < kChunks; c++)
 #pragma unroll
-          for (int e = 0; e < 8; e++) acc[e] = fmaf(w, v[j][e], acc[e]);
+      for (int e = 0; e < 8; e++) acc[c][e] = fmaf(w, part[c][e], acc[c][e]);
+  };
+#pragma unroll
+  for (int k = 0; k < 2; k++) {
+    add(first[k], v[k]);
+    constexpr int kDeep = kChunks == 1 ? 4 : 1;  // parts on their way together
+    for (int j0 = 1; j0 < n[k]; j0 += kDeep) {
+      float w[kDeep][kChunks][8], l[kDeep];
+#pragma unroll
+      for (int j = 0; j < kDeep; j++) {
+        l[j] = -INFINITY;
+        if (j0 + j < n[k]) {
+          l[j] = __ldcg(lse[k] + (size_t)(j0 + j) * M_TILE);
+#pragma unroll
+          for (int c = 0; c < kChunks; c++) ld_cg_v8(w[j][c], o[k] + (j0 + j) * kNext + c * kChunk);
         }
       }
+#pragma unroll
+      for (int j = 0; j < kDeep; j++) add(l[j], w[j]);
+    }
   }
   const float inv = sum > 0.f ? 1.f / sum : 0.f;
-  uint32_t w[4];
 #pragma unroll
-  for (int e = 0; e < 4; e++) {
-    const __nv_bfloat162 v = __floats2bfloat162_rn(acc[2 * e] * inv, acc[2 * e + 1] * inv);
-    w[e] = *reinterpret_cast<const uint32_t *>(&v);
+  for (int c = 0; c < kChunks; c++) {
+    uint32_t w[4];
+#pragma unroll
+    for (int e = 0; e < 4; e++) {
+      const __nv_bfloat162 x = __floats2bfloat162_rn(acc[c][2 * e] * inv, acc[c][2 * e + 1] * inv);
+      w[e] = *reinterpret_cast<const uint32_t *>(&x);
+    }
+    reinterpret_cast<uint4 *>(p.out + (size_t)R * D_V)[chunk + c] = make_uint4(w[0], w[1], w[2], w[3]);
   }
-  reinterpret_cast<uint4 *>(p.out + (size_t)R * D_V)[chunk] = make_uint4(w[0], w[1], w[2], w[3]);
   if (chunk == 0)
     p.lse[((size_t)b * p.H + r % p.H) * p.T + r / p.H] = sum > 0.f ? (m + log2f(sum)) * LN2 : -INFINITY;
 }
@@ -340,15 +378,24 @@ __global__ void __launch_bounds__(kJoinWarps * 32) shared_join_kernel(SharedPara
 
 struct Layout {
   size_t items, md, pieces, n_prefix, groups, lens_o, seq, md_o, ns_o, cnt_o, scratch, lse_p, o_p, lse_o, o_o, ring, total;
+  size_t pages;
   int room, n_mt;
+  bool apart;  // own FP8 tokens go through the decode kernel
 };
 
-Layout layout(int B, int T, int H, int G, int format, int max_prefix, int parts) {
-  const bool wide = format != MLA_KV_BF16;
+// Own FP8 pages are widened along with the prefixes' where the page table has at
+// most this many entries (302 MB of workspace): 48 sequences of up to 300 tokens,
+// four query tokens, 64 heads 120 us against 155 us through the decode kernel's gather.
+constexpr long long kMostOwnPages = 4096;
+
+Layout layout(int B, int T, int H, int G, int format, int max_prefix, int max_pages, int parts) {
+  const bool wide = format != MLA_KV_BF16, apart = wide && (long long)B * max_pages > kMostOwnPages;
   Layout l;
   l.n_mt = ceil_div(T * H, M_TILE);
+  l.apart = apart;
   const size_t own = (size_t)B * l.n_mt, prefix = ((size_t)B * T * H + M_TILE - 1) / M_TILE + G;
-  l.room = (int)(prefix + (wide ? 0 : own));
+  l.room = (int)(prefix + (apart ? 0 : own));
+  l.pages = wide ? (size_t)G * max_prefix + (apart ? 0 : (size_t)B * max_pages) : 0;
   size_t at = 0;
   auto take = [&](size_t bytes) {
     const size_t here = at;
@@ -356,18 +403,18 @@ Layout layout(int B, int T, int H, int G, int format, int max_prefix, int parts)
     return here;
   };
   // slots of results: one for each item, and one for each cut
-  const size_t slots = (size_t)l.room + parts, slots_o = wide ? 2 * own + parts : 0, row = M_TILE * sizeof(float);
+  const size_t slots = (size_t)l.room + parts, slots_o = apart ? 2 * own + parts : 0, row = M_TILE * sizeof(float);
   l.items = take((size_t)l.room * sizeof(SharedItem));
   l.md = take((size_t)parts * MD_STRIDE * 4);
   l.pieces = take((size_t)l.room * 4);
   l.n_prefix = take(4);
   l.groups = take((size_t)G * sizeof(int4));
-  l.lens_o = take((size_t)B * 4);
   l.seq = take((size_t)B * sizeof(int2));
-  l.md_o = take(wide ? (size_t)parts * MD_STRIDE * 4 : 0);
-  l.ns_o = take(wide ? (own + 1) * 4 : 0);
-  l.cnt_o = take(wide ? own * 4 : 0);
-  l.scratch = take(wide ? (size_t)G * max_prefix * PAGE * D_QK * 2 : 0);
+  l.lens_o = take(apart ? (size_t)B * 4 : 0);
+  l.md_o = take(apart ? (size_t)parts * MD_STRIDE * 4 : 0);
+  l.ns_o = take(apart ? (own + 1) * 4 : 0);
+  l.cnt_o = take(apart ? own * 4 : 0);
+  l.scratch = take(l.pages * PAGE * D_QK * 2);
   l.lse_p = take(slots * row);
   l.o_p = take(slots * row * D_V);
   l.lse_o = take(slots_o * row);
@@ -382,10 +429,10 @@ int fail(int code, const char *msg) {
   return code;
 }
 
-int check_sizes(int B, int T, int H, int G, int format, int max_prefix) {
+int check_sizes(int B, int T, int H, int G, int format, int max_prefix, int max_pages) {
   char msg[160];
-  if (B < 1 || G < 1 || max_prefix < 1) {
-    snprintf(msg, sizeof msg, "B = %d, G = %d and max_prefix_pages = %d must be >= 1", B, G, max_prefix);
+  if (B < 1 || G < 1 || max_prefix < 1 || max_pages < 1) {
+    snprintf(msg, sizeof msg, "B = %d, G = %d, max_prefix_pages = %d and max_pages = %d must be >= 1", B, G, max_prefix, max_pages);
     return fail(MLA_ERR_INVALID_ARG, msg);
   }
   if (H < 1 || H > MLA_MAX_HEADS || T < 1 || T > MLA_MAX_QUERY_TOKENS) {
@@ -417,10 +464,11 @@ bool aligned(const void *p, size_t a) { return reinterpret_cast<uintptr_t>(p) % 
 
 using namespace mla;
 
-extern "C" size_t mla_decode_shared_workspace_bytes(int B, int T, int H, int G, int kv_format, int max_prefix_pages) {
+extern "C" size_t mla_decode_shared_workspace_bytes(int B, int T, int H, int G, int kv_format, int max_prefix_pages,
+                                                    int max_pages) {
   int parts = 0;
-  if (check_sizes(B, T, H, G, kv_format, max_prefix_pages) != MLA_OK || device_parts(&parts) != MLA_OK) return 0;
-  return layout(B, T, H, G, kv_format, max_prefix_pages, parts).total;
+  if (check_sizes(B, T, H, G, kv_format, max_prefix_pages, max_pages) != MLA_OK || device_parts(&parts) != MLA_OK) return 0;
+  return layout(B, T, H, G, kv_format, max_prefix_pages, max_pages, parts).total;
 }
 
 extern "C" int mla_decode_shared(const void *q, const void *kv_cache, int kv_format, int num_pages, int page_size,
@@ -429,7 +477,7 @@ extern "C" int mla_decode_shared(const void *q, const void *kv_cache, int kv_for
                                  const int32_t *cache_seqlens, const float *kv_scales, float softmax_scale, int causal,
                                  void *workspace, size_t workspace_bytes, void *out, float *lse, int B, int T, int H,
                                  mla_stream_t stream) {
-  int rc = check_sizes(B, T, H, G, kv_format, max_prefix_pages);
+  int rc = check_sizes(B, T, H, G, kv_format, max_prefix_pages, max_pages);
   if (rc != MLA_OK) return rc;
   if (!q || !kv_cache || !prefix_table || !prefix_lens || !block_table || !cache_seqlens || !out || !lse)
     return fail(MLA_ERR_INVALID_ARG, "null pointer argument");
@@ -442,13 +490,13 @@ extern "C" int mla_decode_shared(const void *q, const void *kv_cache, int kv_for
   if (kv_format != MLA_KV_BF16 && (!kv_scales || !aligned(kv_scales, kv_format == MLA_KV_FP8_E4M3 ? 16 : 4)))
     return fail(MLA_ERR_INVALID_ARG, "an FP8 cache needs aligned kv_scales");
   if (page_size != MLA_PAGE_SIZE) return fail(MLA_ERR_UNSUPPORTED, "page_size must be 64");
-  if (num_pages < 1 || max_pages < 1) return fail(MLA_ERR_INVALID_ARG, "num_pages/max_pages < 1");
+  if (num_pages < 1) return fail(MLA_ERR_INVALID_ARG, "num_pages must be >= 1");
   if (causal != 0 && causal != 1) return fail(MLA_ERR_INVALID_ARG, "causal must be 0 or 1");
   if (!(softmax_scale > 0.f) || !std::isfinite(softmax_scale))
     return fail(MLA_ERR_INVALID_ARG, "softmax_scale must be finite and > 0");
   int parts = 0;
   if ((rc = device_parts(&parts)) != MLA_OK) return rc;
-  const Layout l = layout(B, T, H, G, kv_format, max_prefix_pages, parts);
+  const Layout l = layout(B, T, H, G, kv_format, max_prefix_pages, max_pages, parts);
   if (!workspace || workspace_bytes < l.total) {
     char msg[96];
     snprintf(msg, sizeof msg, "workspace needs %zu bytes, got %zu", l.total, workspace_bytes);
@@ -491,9 +539,9 @@ extern "C" int mla_decode_shared(const void *q, const void *kv_cache, int kv_for
   p.groups = reinterpret_cast<int4 *>(at(l.groups));
   p.lens_o = reinterpret_cast<int32_t *>(at(l.lens_o));
   p.seq = reinterpret_cast<int2 *>(at(l.seq));
-  p.md_o = reinterpret_cast<int32_t *>(at(l.md_o));
-  p.ns_o = reinterpret_cast<int32_t *>(at(l.ns_o));
-  p.cnt_o = reinterpret_cast<int32_t *>(at(l.cnt_o));
+  p.md_o = l.apart ? reinterpret_cast<int32_t *>(at(l.md_o)) : nullptr;
+  p.ns_o = l.apart ? reinterpret_cast<int32_t *>(at(l.ns_o)) : nullptr;
+  p.cnt_o = l.apart ? reinterpret_cast<int32_t *>(at(l.cnt_o)) : nullptr;
   p.scratch = at(l.scratch);
   p.lse_p = reinterpret_cast<float *>(at(l.lse_p));
   p.o_p = reinterpret_cast<float *>(at(l.o_p));
@@ -502,6 +550,7 @@ extern "C" int mla_decode_shared(const void *q, const void *kv_cache, int kv_for
   p.ring = at(l.ring);
   p.out = static_cast<__nv_bfloat16 *>(out);
   p.lse = lse;
+  p.scratch_pages = l.pages;
   const bool wide = kv_format != MLA_KV_BF16;
 
   cudaStream_t s = (cudaStream_t)stream;
@@ -513,13 +562,14 @@ extern "C" int mla_decode_shared(const void *q, const void *kv_cache, int kv_for
   cfg.stream = s;
   cfg.attrs = pdl;
   cfg.numAttrs = 1;
-  cudaError_t e = launch_dependent(shared_schedule_kernel, wide ? 2 : 1, kSchedThreads, 0, s, p);
+  cudaError_t e = launch_dependent(shared_schedule_kernel, l.apart ? 2 : 1, kSchedThreads, 0, s, p);
   if (e == cudaSuccess && wide) {
-    cfg.gridDim = dim3(max_prefix_pages < 1024 ? max_prefix_pages : 1024, G);
+    const int longest = l.apart || max_prefix_pages > max_pages ? max_prefix_pages : max_pages;
+    cfg.gridDim = dim3(longest < 1024 ? longest : 1024, l.apart ? G : G + B);
     e = cudaLaunchKernelEx(&cfg, shared_widen_kernel, p);
   }
   if (e == cudaSuccess) e = launch_shared_attention(p, s);
-  if (e == cudaSuccess && wide) {
+  if (e == cudaSuccess && l.apart) {
     // own FP8 rows go through the decode kernel, which gathers and widens them
     DecodeParams d{};
     d.q = p.q;
@@ -551,8 +601,12 @@ extern "C" int mla_decode_shared(const void *q, const void *kv_cache, int kv_for
     e = launch_decode(d, s, nullptr, nullptr);
   }
   if (e == cudaSuccess) {
-    cfg.gridDim = dim3((unsigned)(((long long)B * T * H + 31) / 32), 64 / kJoinWarps);
-    e = cudaLaunchKernelEx(&cfg, shared_join_kernel, p);
+    // Few rows: a warp has 8 columns, so that there are warps enough; many: 32, as finding a row's
+    // parts takes longer than reading 8 columns of them.
+    const unsigned blocks = (unsigned)(((long long)B * T * H + 31) / 32);
+    const bool few = blocks < 128;
+    cfg.gridDim = dim3(blocks, 64 / kJoinWarps / (few ? 1 : 4));
+    e = cudaLaunchKernelEx(&cfg, few ? shared_join_kernel<1> : shared_join_kernel<4>, p);
   }
   if (e != cudaSuccess) {
     char msg[128];

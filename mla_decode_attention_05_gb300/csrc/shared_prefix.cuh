@@ -39,12 +39,13 @@ struct SharedParams {
   int32_t *pieces;     // [room] slots of an item that hold results
   int32_t *n_prefix;   // items that are prefixes: they come first
   int4 *groups;        // [G] {first sequence, end, first item, keys}
-  int32_t *lens_o;     // [B] own tokens, clamped
   int2 *seq;           // [B] {first prefix item of its group or -1, its first row among the group's}
-  int32_t *md_o, *ns_o, *cnt_o;  // FP8: the decode kernel's schedule of the own tokens
-  uint8_t *scratch;    // FP8: prefix pages as bf16, [G * max_prefix][64][576]
+  int32_t *lens_o;     // [B] own tokens, clamped, where they
+  int32_t *md_o, *ns_o, *cnt_o;  // go through the decode kernel: its schedule (else null)
+  uint8_t *scratch;    // FP8: pages as bf16, [64][576] each: G * max_prefix, and B * max_pages
+  size_t scratch_pages;
   float *lse_p, *o_p;  // partial results: base-2 log-sum-exp [slots][128] and output [slots][64][128][8]
-  float *lse_o, *o_o;  // FP8: those of the decode kernel
+  float *lse_o, *o_o;  // those of the decode kernel
   uint8_t *ring;       // [parts][P_RING][P_SLOT_BYTES]
   __nv_bfloat16 *out;
   float *lse;

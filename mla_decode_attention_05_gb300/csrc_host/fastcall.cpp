@@ -346,7 +346,7 @@ PyObject *decode_shared(PyObject *, PyObject *const *args, Py_ssize_t n) {
   int rc;
   {
     Unlocked others;
-    size_t bytes = shared_ws_fn((int)c.B, (int)T, (int)H, (int)G, c.format, (int)pt->size(1));  // (0: refused below)
+    size_t bytes = shared_ws_fn((int)c.B, (int)T, (int)H, (int)G, c.format, (int)pt->size(1), c.width);  // (0: refused below)
     out = out_given ? *out_given : at::empty({c.B, T, H, 512}, q->options());
     lse = lse_given ? *lse_given : at::empty({c.B, H, T}, q->options().dtype(at::kFloat));
     void *at = make_space(space, *q, bytes, room);

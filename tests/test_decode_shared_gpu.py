@@ -73,6 +73,18 @@ def test_matches_the_oracle(case):
     assert mla.device_status() == 0
 
 
+@pytest.mark.parametrize("fmt", ["fp8", "fp8_tensor"])
+def test_fp8_own_tokens_behind_a_wide_page_table(fmt):
+    """A page table too wide for its pages to be widened ahead."""
+    import mla_decode_attention_05_gb300 as mla
+    prefixes, offsets, own = [130, 64], [0, 1, 3], [9, 0, 70]
+    c, pre, mine, q = _make(335, fmt, 4, 48, prefixes, offsets, own)
+    data, scales = c.cuda()
+    out, lse = mla.decode_shared(q.cuda(), data, table(pre), i32(prefixes), table(mine, 1400), i32(own), softmax_scale=SCALE,
+                                 group_offsets=i32(offsets), causal=True, kv_scales=scales)
+    _check(c, pre, mine, q, prefixes, offsets, own, True, out, lse)
+
+
 def test_many_sequences_and_a_long_prefix():
     """Prefix tiles split over many workers, and own caches of all lengths."""
     rng = np.random.default_rng(330)
@@ -135,7 +147,7 @@ def test_given_buffers_another_stream_and_a_graph():
     data, _ = c.cuda()
     q, pt, pl, bt, sk = q.cuda(), table(pre), i32(prefixes), table(mine), i32(own)
     want = mla.decode_shared(q, data, pt, pl, bt, sk, softmax_scale=SCALE, causal=True)
-    ws = torch.full((mla.decode_shared_workspace_bytes(3, 2, 16, 1, mla.KV_BF16, pt.shape[1]),), 0xFF, dtype=torch.uint8, device="cuda")
+    ws = torch.full((mla.decode_shared_workspace_bytes(3, 2, 16, 1, mla.KV_BF16, pt.shape[1], bt.shape[1]),), 0xFF, dtype=torch.uint8, device="cuda")
     out = torch.full((3, 2, 16, 512), float("nan"), dtype=torch.bfloat16, device="cuda")
     lse = torch.full((3, 16, 2), float("nan"), device="cuda")
     s = torch.cuda.Stream()
