@@ -485,12 +485,16 @@ int mla_value_project(const void *attn, int64_t ld_token, int64_t ld_head, const
  *   workspace      device, >= mla_decode_shared_workspace_bytes(...) bytes for the
  *                  current device, 256-byte aligned; no initialisation; calls
  *                  that overlap on the GPU need separate ones
- * Parts of an output are joined in fp32, and rounded once.  At most 8192 tiles of
- * 128 query rows (B * ceil(T * H / 128), and ceil(B * T * H / 128) + G;
- * MLA_ERR_UNSUPPORTED above).  Cache rows behind the last token of a sequence or
- * prefix, in its last page, must hold finite values.  A page outside the pool is
- * skipped and sets MLA_STATUS_BAD_PAGE.  Asynchronous on `stream`; can be captured in a
- * CUDA graph.  Returns MLA_OK or a negative code.
+ * Probabilities are rounded to bf16 before they multiply the values, FP8 rows with
+ * scales to bf16 before both products; parts of an output are joined in fp32 and
+ * rounded once.  What the cache holds behind the last token of a sequence or prefix
+ * does not matter (inf and nan included); the tokens' own rows must be finite.  A
+ * page outside the pool is skipped and sets MLA_STATUS_BAD_PAGE.  Of an FP8 cache,
+ * prefix pages are widened to bf16 in the workspace (73728 bytes an entry of
+ * prefix_table), and own pages too where B * max_pages <= 4096.  At most 8192 work
+ * items: B * ceil(T * H / 128) + ceil(B * T * H / 128) + G (MLA_ERR_UNSUPPORTED above).
+ * A wait that gives up sets MLA_STATUS_WAIT_TIMEOUT.  Asynchronous on `stream`; can
+ * be captured in a CUDA graph.  Returns MLA_OK or a negative code.
  */
 size_t mla_decode_shared_workspace_bytes(int B, int T, int H, int G, int kv_format, int max_prefix_pages,
                                          int max_pages);
