@@ -29,19 +29,32 @@ using namespace ptx;
 
 constexpr int kKeys = 128;                     // keys of a CTA's half of a tile: two pages
 constexpr int kTileKeys = 2 * kKeys;
-constexpr int kRows = 256;                     // query rows of a tile
 constexpr int kBlocks = D_QK / 64;             // blocks of 64 of the 576 dims
 constexpr uint32_t kBlock = kKeys * 128;       // 128 rows x 64 dims, 128-byte swizzle
 constexpr uint32_t kHalf = kBlock / 2;
 constexpr int kMostSlots = 9;                  // blocks of the streaming operand
-constexpr int kD = 2;                          // score tiles in tensor memory
-constexpr int kWideWarps = 16;                 // FP8: warps that widen cached rows
-constexpr int kWideGroups = 4;                 // groups of them, which take the blocks in turn
-constexpr int kGroupWarps = kWideWarps / kWideGroups;
-constexpr int kWideThreads = 32 * kGroupWarps;
-constexpr int kWideRows = kKeys * 4 / kWideThreads;  // rows of which a thread has 16 bytes
-constexpr int kSumThreads = 128;
-__host__ __device__ constexpr int threads_of(bool fp8) { return fp8 ? 256 + 32 * kWideWarps : 256; }
+constexpr int kMostRows = 256;                 // query rows of a tile
+
+// What depends on the cache's format.  No rounding is made on the way to the scores:
+// FP8 codes are exact in bf16, so a per-tensor scale multiplies the scores, and
+// with a scale for each 128 latent values the product is made in five parts (four
+// times 128 values, and the rotated 64), which the summing threads scale and add.
+// Those hold a tile's scores in registers, so its tiles have half the query rows and
+// two threads a key.  (Rows dequantised to bf16 would put the scores off by 3e-3.)
+template <int kFormat>
+struct Of {
+  static constexpr bool fp8 = kFormat != MLA_KV_BF16, scaled = kFormat == MLA_KV_FP8_E4M3;
+  static constexpr int rows = scaled ? 128 : kMostRows;        // query rows of a tile
+  static constexpr int parts = scaled ? 5 : 1;                 // score tiles in tensor memory for one tile
+  static constexpr int kd = 512 / rows;                        // score tiles that there is room for
+  static constexpr int halves = scaled ? 2 : 1;                // threads of a key
+  static constexpr int cols = rows / halves;                   // columns of a thread
+  static constexpr int sum_warps = 4 * halves;
+  static constexpr int wide_warps = !fp8 ? 0 : scaled ? 8 : 16;  // warps that widen cached rows,
+  static constexpr int group_warps = wide_warps / 4;           // in four groups that take the blocks in turn
+  static constexpr int threads = 32 * (4 + sum_warps + wide_warps);
+};
+constexpr int kWideGroups = 4;
 constexpr uint32_t IDESC = idesc_bf16_f32(kTileKeys, 16, false, false) - (2u << 17);  // N is added
 
 struct MassParams {
@@ -55,7 +68,7 @@ struct MassParams {
   int format, num_pages, max_pages, B, T, H, cap, causal;
   int rows, n_qt, box;  // query rows of a sequence, their tiles, the columns of a tile (half of each CTA)
   int slots;
-  float scale_log2, decay;
+  float scale, decay;
   unsigned long long wait_ns;
 };
 
@@ -63,17 +76,19 @@ struct Bars {
   uint64_t res_full[kBlocks], res_empty[kBlocks];        // full: rank 0, for both CTAs
   uint64_t slot_full[kMostSlots], slot_empty[kMostSlots];
   uint64_t raw_full[kMostSlots];  // FP8: a block's codes are in place (of the resident blocks, or of the slots)
-  uint64_t d_full[kD], d_empty[kD];                      // empty: rank 0
-  alignas(16) float nl2[2][kRows];  // -lse * log2(e) of a tile's query rows
-  alignas(16) int lim[2][kRows];    // keys that a row sees; 0 for one that is no row, or has no weight to give
-  int least[2][kRows / 32];         // the smallest of each 32 rows
+  uint64_t d_full[4], d_empty[4];                        // empty: rank 0
+  uint64_t sc_full[2], sc_empty[2];                      // a tile's scales
+  alignas(16) float nl[2][kMostRows];  // -lse of a tile's query rows
+  alignas(16) int lim[2][kMostRows];   // keys that a row sees; 0 for one that is no row, or has no weight to give
+  int least[2][kMostRows / 32];        // the smallest of each 32 rows
+  float half[2][kKeys];                // sums of the columns' upper half
   int warp_sums[32];
   int start_b, start_t;
   uint32_t tmem_base;
   int abort;
 };
 // Shared memory: barriers, the resident operand's blocks, slots, FP8 scales of two tiles ([128][4]).
-constexpr uint32_t OFF_RES = 6 * 1024;
+constexpr uint32_t OFF_RES = 7 * 1024;
 constexpr uint32_t kScaleBytes = kKeys * 16;
 constexpr uint32_t kSmem = 232448 / 1024 * 1024;
 constexpr uint32_t OFF_SCALES = kSmem - 2 * kScaleBytes;
@@ -146,7 +161,7 @@ struct Work {
   long long u0, u1;  // units of this pair
 };
 
-template <bool kStreamKeys, class F>
+template <bool kStreamKeys, int kRows, class F>
 __device__ __forceinline__ bool for_each_phase(const MassParams &p, const Work &w, F &&f) {
   int b = w.b, t = w.t, len = w.u0 < w.u1 ? seq_len(p, b) : 0;
   for (long long u = w.u0; u < w.u1;) {
@@ -259,15 +274,16 @@ struct Place {
 // (A warp's wait, arrival and copy take some 350 cycles together, whatever the copy's
 // size: one warp alone would take longer over a block's two pages than HBM.)  The
 // whole warp waits and looks pages up, one elected lane asks for the copies.  rank 0's
-// barriers count the bytes of both CTAs.  A block of FP8 rows lands as codes (64 bytes of each row) in
-// the upper half of the block that it will fill, on a barrier of this CTA; the
-// rotated part of rows with scales is bf16 and lands as it is used.
-template <bool kStreamKeys, bool kFp8, bool kPoll>
+// barriers count the bytes of both CTAs.  A block of FP8 rows lands as codes (64
+// bytes of each row) in the upper half of the block that it will fill, on a barrier
+// of this CTA; the rotated part of rows with scales is bf16 and lands as it is used.
+template <bool kStreamKeys, int kFormat, bool kPoll>
 __device__ void load_role(const MassParams &p, uint8_t *base, Bars &br, const CUtensorMap *k_map, const CUtensorMap *pe_map,
                           const CUtensorMap *q_map, const Work &w, const Place &at, int which) {
+  using C = Of<kFormat>;
+  constexpr int kRows = C::rows;
   const uint32_t scales = smem_u32(base + OFF_SCALES);
   const uint64_t keep = policy_evict_normal(), key_pol = kStreamKeys ? policy_evict_first() : keep;
-  const bool scaled = p.format == MLA_KV_FP8_E4M3;
   int s = 0;
   uint32_t ph = 1, rph = 1, tile = 0;
   // This CTA's pages of a tile, and how many both CTAs have.  Lanes 0-3 look up the
@@ -293,20 +309,33 @@ __device__ void load_role(const MassParams &p, uint8_t *base, Bars &br, const CU
   auto keys = [&](uint32_t dst, uint64_t *full, uint64_t *raw, int kb) {
     if (!elect_one()) return;
     const int page = pg[which];
-    if (!kFp8) {
+    if (!C::fp8) {
       if (which == 0 && at.rank == 0) mbar_arrive_expect_tx(smem_u32(full), pages * kHalf);
       if (page >= 0) tma_load_4d_pair(dst + which * kHalf, k_map, mapa(smem_u32(full), 0), 0, 0, kb, page, key_pol);
       return;
     }
     const uint32_t bar = smem_u32(raw), n = (pg[0] >= 0) + (pg[1] >= 0);
-    const bool codes = !(scaled && kb == 8), with = scaled && kb == 0;
-    if (which == 0) mbar_arrive_expect_tx(bar, n * ((codes ? kHalf / 2 : kHalf) + (with ? kScaleBytes / 2 : 0)));
+    const bool codes = !(C::scaled && kb == 8);
+    if (which == 0) mbar_arrive_expect_tx(bar, n * (codes ? kHalf / 2 : kHalf));
     if (page < 0) return;
     if (codes) tma_load_3d(dst + kHalf + which * (kHalf / 2), k_map, bar, kb * 64, 0, page, key_pol);
     else tma_load_3d(dst + which * kHalf, pe_map, bar, 0, 0, page, key_pol);
-    if (with)
-      bulk_load(scales + (tile & 1) * kScaleBytes + which * (kScaleBytes / 2), p.kv_scales + (size_t)page * PAGE * 4,
-                kScaleBytes / 2, bar);
+  };
+  // a tile's scales, both pages' by warp 3
+  auto scales_of_tile = [&] {
+    if (!C::scaled || which == 0) return true;
+    const uint32_t b = tile & 1;
+    if (!warp_wait<kPoll>(&br, &br.sc_empty[b], ((tile >> 1) & 1) ^ 1, p)) return false;
+    if (elect_one()) {
+      const uint32_t bar = smem_u32(&br.sc_full[b]);
+      mbar_arrive_expect_tx(bar, ((pg[0] >= 0) + (pg[1] >= 0)) * (kScaleBytes / 2));
+#pragma unroll
+      for (int h = 0; h < 2; h++)
+        if (pg[h] >= 0)
+          bulk_load(scales + b * kScaleBytes + h * (kScaleBytes / 2), p.kv_scales + (size_t)pg[h] * PAGE * 4, kScaleBytes / 2, bar);
+    }
+    __syncwarp();
+    return true;
   };
   const int half = p.box / 2;  // query rows of each CTA
   auto rows = [&](uint32_t dst, uint64_t *full, int b, int qt, int kb) {
@@ -314,16 +343,20 @@ __device__ void load_role(const MassParams &p, uint8_t *base, Bars &br, const CU
     if (at.rank == 0) mbar_arrive_expect_tx(smem_u32(full), p.box * 128);
     tma_load_3d_pair(dst, q_map, mapa(smem_u32(full), 0), 0, b * p.rows + qt * kRows + (int)at.rank * half, kb, keep);
   };
-  for_each_phase<kStreamKeys>(p, w, [&](const Phase &f) {
+  for_each_phase<kStreamKeys, kRows>(p, w, [&](const Phase &f) {
     if (f.i0 >= f.i1) return true;
     // (the first of what streams is asked for along with the resident blocks, so that
     // both follow the last phase's MMAs block by block)
     fetch(f.b, f.t, f.len);
-    if (!kStreamKeys) look();
+    if (!kStreamKeys) {
+      look();
+      if (!scales_of_tile()) return false;
+    }
     for (int i = f.i0; i < (kStreamKeys || which == 0 ? f.i1 : f.i0 + 1); i++) {
       if (kStreamKeys) {
         look();
         if (i + 1 < f.i1) fetch(f.b, i + 1, f.len);
+        if (!scales_of_tile()) return false;
       }
       for (int kb = 0; kb < kBlocks; kb++) {
         if (i == f.i0 && (!kStreamKeys || which == 0)) {
@@ -360,38 +393,37 @@ __device__ __forceinline__ void st_shared_v4(uint32_t addr, const uint4 &v) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
 
-// Warps 8-23 widen FP8 rows in place, in groups that take the blocks in turn: thread
-// i of a group has 16 codes of rows i / 4 + 32 k.  All of a group read their codes
-// before any writes bf16 values over them.  (The codes come by TMA: a load of its
-// own in flight would hold up the thread's proxy fences.)
+// The last warps widen FP8 codes in place, in groups that take the blocks in turn:
+// thread i of a group has 16 codes of rows i / 4 + a multiple of its group's.  All of a
+// group read their codes before any writes bf16 values over them.  (The codes come
+// by TMA: a load of its own in flight would hold up the thread's proxy fences.)
 constexpr uint32_t kWideBar = 3;
 
-template <bool kStreamKeys, bool kPoll>
-__device__ void widen_role(const MassParams &p, uint8_t *base, Bars &br, const Work &w, const Place &at, int thread) {
-  const int group = thread / kWideThreads, i = thread % kWideThreads;
-  const int r = i >> 2, c = i & 3, x = r & 7;
-  constexpr int kStep = kWideThreads / 4;  // rows between a thread's
+template <bool kStreamKeys, int kFormat, bool kPoll>
+__device__ void widen_role(const MassParams &p, Bars &br, const Work &w, const Place &at, int thread) {
+  using C = Of<kFormat>;
+  constexpr int kThreads = 32 * C::group_warps, kStep = kThreads / 4, kMine = kKeys / kStep;  // rows between a thread's; its rows
   static_assert(kStep % 8 == 0, "a thread's rows have one swizzle");
-  const bool first = (threadIdx.x & 31) == 0, scaled = p.format == MLA_KV_FP8_E4M3;
-  const float one = scaled ? 0.f : __ldg(p.kv_scales);
+  const int group = thread / kThreads, i = thread % kThreads;
+  const int r = i >> 2, c = i & 3, x = r & 7;
+  const bool first = (threadIdx.x & 31) == 0;
   int s = 0, turn = 0;
   uint32_t ph = 0, tile = 0;
   auto widen_tile = [&] {
-    const float *sc = reinterpret_cast<const float *>(base + OFF_SCALES + (tile & 1) * kScaleBytes) + r * 4;
     for (int kb = 0; kb < kBlocks; kb++) {
       if (turn == group) {
         const int k = kStreamKeys ? s : kb;
         const uint32_t dst = kStreamKeys ? at.slots + s * kBlock : at.res + kb * kBlock;
         const bool ok = warp_wait<kPoll>(&br, &br.raw_full[k], kStreamKeys ? ph : tile & 1, p);
-        uint4 v[kWideRows];
+        uint4 v[kMine];
 #pragma unroll
-        for (int j = 0; j < kWideRows; j++) v[j] = ld_shared_v4(dst + kHalf + (r + kStep * j) * 64 + c * 16);
-        if (bar_red_or(kWideBar + group, kWideThreads, !ok)) return false;
-        if (!(scaled && kb == 8)) {
+        for (int j = 0; j < kMine; j++) v[j] = ld_shared_v4(dst + kHalf + (r + kStep * j) * 64 + c * 16);
+        if (bar_red_or(kWideBar + group, kThreads, !ok)) return false;
+        if (!(C::scaled && kb == 8)) {
 #pragma unroll
-          for (int j = 0; j < kWideRows; j++) {
+          for (int j = 0; j < kMine; j++) {
             uint4 lo, hi;
-            widen16(v[j], scaled ? sc[kStep * j * 4 + (kb >> 1)] : one, lo, hi);
+            codes16(v[j], lo, hi);
             const uint32_t row = dst + (r + kStep * j) * 128;
             st_shared_v4(row + (((2 * c) ^ x) << 4), lo);
             st_shared_v4(row + (((2 * c + 1) ^ x) << 4), hi);
@@ -410,7 +442,7 @@ __device__ void widen_role(const MassParams &p, uint8_t *base, Bars &br, const W
     tile++;
     return true;
   };
-  for_each_phase<kStreamKeys>(p, w, [&](const Phase &f) {
+  for_each_phase<kStreamKeys, C::rows>(p, w, [&](const Phase &f) {
     for (int t = f.i0; t < (kStreamKeys ? f.i1 : min(f.i0 + 1, f.i1)); t++)
       if (!widen_tile()) return false;
     return true;
@@ -421,17 +453,28 @@ __device__ void widen_role(const MassParams &p, uint8_t *base, Bars &br, const W
 
 constexpr uint32_t kMmaBar = 1, kSumBar = 2;
 
+// The score tile that block kb belongs to begins, or ends, with it.
+template <int kFormat>
+__device__ __forceinline__ bool begins(int kb) { return Of<kFormat>::parts == 1 ? kb == 0 : (kb & 1) == 0; }
+template <int kFormat>
+__device__ __forceinline__ bool ends(int kb) { return kb == kBlocks - 1 || (Of<kFormat>::parts > 1 && (kb & 1)); }
+
 // rank 0, warp 2 waits for what the MMAs of warp 1 need and meets it at a named
 // barrier (a wait in the issuing warp would hold up its MMAs in flight).
-template <bool kStreamKeys, bool kPoll>
+template <bool kStreamKeys, int kFormat, bool kPoll>
 __device__ void wait_role(const MassParams &p, Bars &br, const Work &w) {
+  constexpr int kD = Of<kFormat>::kd;
   int s = 0;
   uint32_t ph = 0, rph = 0, g = 0;
-  for_each_phase<kStreamKeys>(p, w, [&](const Phase &f) {
+  for_each_phase<kStreamKeys, Of<kFormat>::rows>(p, w, [&](const Phase &f) {
     if (f.i0 >= f.i1) return true;
-    for (int i = f.i0; i < f.i1; i++, g++) {
-      bool ok = warp_wait<kPoll>(&br, &br.d_empty[g % kD], ((g / kD) & 1) ^ 1, p);
+    for (int i = f.i0; i < f.i1; i++) {
       for (int kb = 0; kb < kBlocks; kb++) {
+        bool ok = true;
+        if (begins<kFormat>(kb)) {
+          ok = warp_wait<kPoll>(&br, &br.d_empty[g % kD], ((g / kD) & 1) ^ 1, p);
+          g++;
+        }
         if (ok && i == f.i0) ok = warp_wait<kPoll>(&br, &br.res_full[kb], rph, p);
         if (ok) ok = warp_wait<kPoll>(&br, &br.slot_full[s], ph, p);
         if (bar_red_or(kMmaBar, 64, !ok)) return false;
@@ -446,14 +489,15 @@ __device__ void wait_role(const MassParams &p, Bars &br, const Work &w) {
   });
 }
 
-template <bool kStreamKeys>
+template <bool kStreamKeys, int kFormat>
 __device__ void mma_role(const MassParams &p, Bars &br, const Work &w, const Place &at, uint32_t tmem) {
+  constexpr int kD = Of<kFormat>::kd, kRows = Of<kFormat>::rows;
   const uint32_t idesc = IDESC + ((uint32_t)(p.box >> 3) << 17);
   int s = 0;
   uint32_t g = 0;
-  for_each_phase<kStreamKeys>(p, w, [&](const Phase &f) {
+  for_each_phase<kStreamKeys, kRows>(p, w, [&](const Phase &f) {
     if (f.i0 >= f.i1) return true;
-    for (int i = f.i0; i < f.i1; i++, g++) {
+    for (int i = f.i0; i < f.i1; i++) {
       for (int kb = 0; kb < kBlocks; kb++) {
         if (bar_red_or(kMmaBar, 64, false)) return false;
         tc_fence_after();
@@ -463,12 +507,13 @@ __device__ void mma_role(const MassParams &p, Bars &br, const Work &w, const Pla
           const uint64_t a = kStreamKeys ? pass : stay, b = kStreamKeys ? stay : pass;
 #pragma unroll
           for (int kk = 0; kk < 4; kk++)
-            mma_pair_ss(tmem + (g % kD) * kRows, a + kk * 2, b + kk * 2, idesc, kb || kk ? 1u : 0u);
+            mma_pair_ss(tmem + (g % kD) * kRows, a + kk * 2, b + kk * 2, idesc, !begins<kFormat>(kb) || kk ? 1u : 0u);
           mma_commit_pair(smem_u32(&br.slot_empty[s]));
           if (i == f.i1 - 1) mma_commit_pair(smem_u32(&br.res_empty[kb]));
-          if (kb == kBlocks - 1) mma_commit_pair(smem_u32(&br.d_full[g % kD]));
+          if (ends<kFormat>(kb)) mma_commit_pair(smem_u32(&br.d_full[g % kD]));
         }
         __syncwarp();
+        if (ends<kFormat>(kb)) g++;
         if (++s == p.slots) s = 0;
       }
     }
@@ -482,36 +527,78 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-__device__ __forceinline__ float2 pair(uint32_t a, uint32_t b) { return make_float2(__uint_as_float(a), __uint_as_float(b)); }
+// 32 lanes x 16 columns (see tmem_ld32).
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
+        "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
 
-// Warps 4-7: thread = key of the tile = lane of tensor memory.
-template <bool kStreamKeys, bool kPoll>
-__device__ void sum_role(const MassParams &p, Bars &br, const Work &w, uint32_t tmem, uint32_t rank, int pair_index) {
-  const int i = threadIdx.x - 128, lane = threadIdx.x & 31;
-  const uint32_t lt = tmem + ((uint32_t)(i & 96) << 16);
-  uint32_t g = 0, buf = 0;
-  const float2 cs = make_float2(p.scale_log2, p.scale_log2);
+// The warps from 4 on that sum: thread = key of the tile = lane of tensor memory (and,
+// with scales, half of the columns).
+template <bool kStreamKeys, int kFormat, bool kPoll>
+__device__ void sum_role(const MassParams &p, uint8_t *base, Bars &br, const Work &w, uint32_t tmem, uint32_t rank, int pair_index) {
+  using C = Of<kFormat>;
+  constexpr int kD = C::kd, kRows = C::rows, kThreads = 32 * C::sum_warps;
+  const int me = threadIdx.x - 128, lane = threadIdx.x & 31, i = me % kKeys, first = me / kKeys * C::cols;
+  const uint32_t lt = tmem + ((uint32_t)(i & 96) << 16) + first;
   const uint32_t d_empty = mapa(smem_u32(&br.d_empty[0]), 0);
+  uint32_t g = 0, buf = 0, tile = 0;
+  const float scale = kFormat == MLA_KV_FP8_E4M3_TENSOR ? p.scale * __ldg(p.kv_scales) : p.scale;
+  const float2 cs = make_float2(scale, scale), log2e = make_float2(LOG2E, LOG2E);
   auto set_rows = [&](const Phase &f, int qt) {
     buf ^= 1;
 #pragma unroll
-    for (int k = 0; k < kRows; k += kSumThreads) {
-      const int R = qt * kRows + k + i;
+    for (int k = 0; k < kRows; k += kThreads) {
+      if (k + me >= kRows) break;  // (whole warps)
+      const int R = qt * kRows + k + me;
       int lim = 0;
       float nl = 0.f;
       if (R < p.rows) {
         const int t = R / p.H, h = R % p.H;
         const float l = __ldg(p.lse + ((size_t)f.b * p.H + h) * p.T + t);
         lim = l == -INFINITY ? 0 : row_kv_len(f.len, p.T, t, p.causal);
-        nl = -l * LOG2E;
+        nl = -l;
       }
-      br.nl2[buf][k + i] = nl;
-      br.lim[buf][k + i] = lim;
+      br.nl[buf][k + me] = nl;
+      br.lim[buf][k + me] = lim;
       const int least = __reduce_min_sync(0xffffffffu, lim);
-      if (lane == 0) br.least[buf][(k + i) / 32] = least;
+      if (lane == 0) br.least[buf][(k + me) / 32] = least;
     }
   };
-  for_each_phase<kStreamKeys>(p, w, [&](const Phase &f) {
+  // exp(score - lse), the difference made before it is taken to base 2: its rounding then goes with
+  // the difference, which is small where the weight is not
+  auto weights = [&](float2 x, float2 nl) {
+    const float2 y = mul2(fma2(x, cs, nl), log2e);
+    return make_float2(ex2(y.x), ex2(y.y));
+  };
+  // the weights of 32 rows, from column c0 of the thread's on
+  float2 acc[2];
+  auto add32 = [&](const float2 (&v)[16], int c0, int key, int end) {
+    const float4 *nl = reinterpret_cast<const float4 *>(&br.nl[buf][first + c0]);
+    if (end <= br.least[buf][(first + c0) / 32]) {  // these rows see all the tile's keys
+#pragma unroll
+      for (int j = 0; j < 8; j++) {
+        const float4 n = nl[j];
+        acc[0] = add2(acc[0], weights(v[2 * j], make_float2(n.x, n.y)));
+        acc[1] = add2(acc[1], weights(v[2 * j + 1], make_float2(n.z, n.w)));
+      }
+    } else {
+      const int4 *lims = reinterpret_cast<const int4 *>(&br.lim[buf][first + c0]);
+#pragma unroll
+      for (int j = 0; j < 8; j++) {
+        const float4 n = nl[j];
+        const int4 lim = lims[j];
+        const float2 a = weights(v[2 * j], make_float2(n.x, n.y)), b = weights(v[2 * j + 1], make_float2(n.z, n.w));
+        acc[0] = add2(acc[0], make_float2(key < lim.x ? a.x : 0.f, key < lim.y ? a.y : 0.f));
+        acc[1] = add2(acc[1], make_float2(key < lim.z ? b.x : 0.f, key < lim.w ? b.y : 0.f));
+      }
+    }
+  };
+  for_each_phase<kStreamKeys, kRows>(p, w, [&](const Phase &f) {
     if (kStreamKeys) set_rows(f, 0);
     float sum = 0.f;
     auto key_of = [&](int t) { return t * kTileKeys + (int)rank * kKeys + i; };
@@ -520,72 +607,109 @@ __device__ void sum_role(const MassParams &p, Bars &br, const Work &w, uint32_t 
     bool placed = false;
     auto prepare = [&](int t) {
       const int n = key_of(t);
+      if (first > 0) return;
       placed = n < f.len && page_of(p, f.b, n / PAGE, f.len) >= 0;
       if (f.whole && p.decay != 0.f && n < f.len) before = p.mass[(size_t)f.b * p.cap + n];
     };
     auto store = [&](int t, float v) {
       const int n = key_of(t);
-      if (n >= f.len) return;
+      if (first > 0 || n >= f.len) return;
       if (!placed) v = 0.f;
       if (f.whole) p.mass[(size_t)f.b * p.cap + n] = p.decay != 0.f ? fmaf(p.decay, before, v) : v;
       else p.partial[((size_t)pair_index * 2 + f.part) * kTileKeys + rank * kKeys + i] = v;
     };
+    // the halves of a key's sum meet
+    auto finish = [&](int t, float v, bool ok) {
+      if (C::halves > 1) {
+        if (first > 0) br.half[tile & 1][i] = v;
+        if (bar_red_or(kSumBar, kThreads, !ok)) return false;
+        v += br.half[tile & 1][i];
+      }
+      store(t, v);
+      tile++;
+      return true;
+    };
     if (!kStreamKeys) prepare(f.t);
-    for (int k = f.i0; k < f.i1; k++, g++) {
+    float4 sc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k = f.i0; k < f.i1; k++) {
       if (kStreamKeys) prepare(k);
       else set_rows(f, k);
-      const bool ok = warp_wait<kPoll>(&br, &br.d_full[g % kD], (g / kD) & 1, p);
-      if (bar_red_or(kSumBar, 128, !ok)) return false;
+      bool ok = warp_wait<kPoll>(&br, &br.d_full[g % kD], (g / kD) & 1, p);
+      if (C::scaled && (kStreamKeys || k == f.i0)) {
+        if (ok) ok = warp_wait<kPoll>(&br, &br.sc_full[tile & 1], (tile >> 1) & 1, p);
+        sc = *reinterpret_cast<const float4 *>(base + OFF_SCALES + (tile & 1) * kScaleBytes + i * 16);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&br.sc_empty[tile & 1]));
+      }
+      if (bar_red_or(kSumBar, kThreads, !ok)) return false;
       tc_fence_after();
       const int key = key_of(kStreamKeys ? k : f.t);
-      const int cols = min(kRows, p.rows - (kStreamKeys ? 0 : k * kRows));
+      const int cols = p.rows - (kStreamKeys ? 0 : k * kRows) - first;  // of the thread's columns (may be more, or none)
       const int end = min((kStreamKeys ? k + 1 : f.t + 1) * kTileKeys, f.len);
-      float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-      for (int c0 = 0; c0 < cols; c0 += 32) {
-        uint32_t v[32];
-        __syncwarp();
-        tmem_ld32(lt + (g % kD) * kRows + c0, v);
-        const float4 *nl = reinterpret_cast<const float4 *>(&br.nl2[buf][c0]);
-        const bool all = end <= br.least[buf][c0 / 32];  // these rows see all the tile's keys
-        tmem_wait_ld();
-        if (all) {
-#pragma unroll
-          for (int j = 0; j < 8; j++) {
-            const float4 n = nl[j];
-            const float2 a = fma2(pair(v[4 * j], v[4 * j + 1]), cs, make_float2(n.x, n.y));
-            const float2 b = fma2(pair(v[4 * j + 2], v[4 * j + 3]), cs, make_float2(n.z, n.w));
-            acc[0] = add2(acc[0], make_float2(ex2(a.x), ex2(a.y)));
-            acc[1] = add2(acc[1], make_float2(ex2(b.x), ex2(b.y)));
-          }
-        } else {
-          const int4 *lims = reinterpret_cast<const int4 *>(&br.lim[buf][c0]);
-#pragma unroll
-          for (int j = 0; j < 8; j++) {
-            const float4 n = nl[j];
-            const int4 lim = lims[j];
-            const float2 a = fma2(pair(v[4 * j], v[4 * j + 1]), cs, make_float2(n.x, n.y));
-            const float2 b = fma2(pair(v[4 * j + 2], v[4 * j + 3]), cs, make_float2(n.z, n.w));
-            acc[0] = add2(acc[0], make_float2(key < lim.x ? ex2(a.x) : 0.f, key < lim.y ? ex2(a.y) : 0.f));
-            acc[1] = add2(acc[1], make_float2(key < lim.z ? ex2(b.x) : 0.f, key < lim.w ? ex2(b.y) : 0.f));
-          }
+      acc[0] = acc[1] = make_float2(0.f, 0.f);
+      if constexpr (!C::scaled) {
+        for (int c0 = 0; c0 < min(C::cols, cols); c0 += 32) {
+          float2 v[16];
+          __syncwarp();
+          tmem_ld32(lt + (g % kD) * kRows + c0, *reinterpret_cast<uint32_t(*)[32]>(&v[0]));
+          tmem_wait_ld();
+          add32(v, c0, key, end);
         }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_remote_relaxed(d_empty + (g % kD) * 8);
+        g++;
+      } else {
+        float2 x[2][16];
+#pragma unroll
+        for (int part = 0; part < C::parts; part++) {
+          if (part > 0 && ok) ok = warp_wait<kPoll>(&br, &br.d_full[g % kD], (g / kD) & 1, p);
+          tc_fence_after();
+          const float factor = part == 0 ? sc.x : part == 1 ? sc.y : part == 2 ? sc.z : part == 3 ? sc.w : 1.f;
+          const float2 f2 = make_float2(factor, factor);
+#pragma unroll
+          for (int q = 0; q < 4; q++) {
+            if (q * 16 < cols) {
+              float2 v[8];
+              __syncwarp();
+              tmem_ld16(lt + (g % kD) * kRows + q * 16, *reinterpret_cast<uint32_t(*)[16]>(&v[0]));
+              tmem_wait_ld();
+#pragma unroll
+              for (int j = 0; j < 8; j++) {
+                float2 &to = x[q >> 1][(q & 1) * 8 + j];
+                to = part == 0 ? mul2(v[j], f2) : fma2(v[j], f2, to);
+              }
+            }
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_remote_relaxed(d_empty + (g % kD) * 8);
+          g++;
+        }
+#pragma unroll
+        for (int c = 0; c < 2; c++)
+          if (c * 32 < cols) add32(x[c], c * 32, key, end);
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_remote_relaxed(d_empty + (g % kD) * 8);
       const float got = (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
-      if (kStreamKeys) store(k, got);
-      else sum += got;
+      if (kStreamKeys) {
+        if (!finish(k, got, ok)) return false;
+      } else {
+        sum += got;
+        if (bar_red_or(kSumBar, kThreads, !ok)) return false;
+      }
     }
-    if (!kStreamKeys) store(f.t, sum);
+    if (kStreamKeys) return true;
+    if (f.i0 < f.i1) return finish(f.t, sum, true);
+    store(f.t, 0.f);  // no row sees these keys
     return true;
   });
 }
 
-template <bool kStreamKeys, bool kFp8, bool kPoll>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(kFp8), 1)
+template <bool kStreamKeys, int kFormat, bool kPoll>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Of<kFormat>::threads, 1)
     attention_mass_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap pe_map,
                           const __grid_constant__ CUtensorMap q_map, const MassParams p) {
+  using C = Of<kFormat>;
   extern __shared__ __align__(1024) uint8_t smem[];
   if (smem_u32(smem) & 1023u) {
     if (threadIdx.x == 0) atomicOr(p.status, MLA_STATUS_SMEM_ALIGN);
@@ -601,17 +725,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(kFp8), 1)
   at.slots = at.res + kBlocks * at.res_block;
   if (threadIdx.x == 0) {
     for (int i = 0; i < kBlocks; i++) {
-      mbar_init(smem_u32(&br.res_full[i]), kFp8 && !kStreamKeys ? 2 * kGroupWarps : 1);
+      mbar_init(smem_u32(&br.res_full[i]), C::fp8 && !kStreamKeys ? 2 * C::group_warps : 1);
       mbar_init(smem_u32(&br.res_empty[i]), 1);
     }
     for (int i = 0; i < kMostSlots; i++) {
-      mbar_init(smem_u32(&br.slot_full[i]), kFp8 && kStreamKeys ? 2 * kGroupWarps : 1);
+      mbar_init(smem_u32(&br.slot_full[i]), C::fp8 && kStreamKeys ? 2 * C::group_warps : 1);
       mbar_init(smem_u32(&br.slot_empty[i]), 1);
       mbar_init(smem_u32(&br.raw_full[i]), 1);
     }
-    for (int i = 0; i < kD; i++) {
+    for (int i = 0; i < C::kd; i++) {
       mbar_init(smem_u32(&br.d_full[i]), 1);
-      mbar_init(smem_u32(&br.d_empty[i]), 2 * kSumThreads / 32);
+      mbar_init(smem_u32(&br.d_empty[i]), 2 * C::sum_warps);
+    }
+    for (int i = 0; i < 2; i++) {
+      mbar_init(smem_u32(&br.sc_full[i]), 1);
+      mbar_init(smem_u32(&br.sc_empty[i]), C::sum_warps);
     }
     br.abort = 0;
     br.start_b = br.start_t = 0;
@@ -620,7 +748,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(kFp8), 1)
     prefetch_tensormap(&k_map);
   }
   if (warp == 1) {
-    tmem_alloc_pair(smem_u32(&br.tmem_base), kD * kRows);
+    tmem_alloc_pair(smem_u32(&br.tmem_base), 512);
     tmem_relinquish_pair();
   }
   grid_dep_trigger();
@@ -632,15 +760,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(kFp8), 1)
   grid_dep_wait();
   const Work w = find_work(p, br, pair_index, pairs);
   if (warp == 0 || warp == 3) {
-    load_role<kStreamKeys, kFp8, kPoll>(p, smem, br, &k_map, &pe_map, &q_map, w, at, warp == 3);
+    load_role<kStreamKeys, kFormat, kPoll>(p, smem, br, &k_map, &pe_map, &q_map, w, at, warp == 3);
   } else if (warp == 1) {
-    if (at.rank == 0) mma_role<kStreamKeys>(p, br, w, at, tmem);
+    if (at.rank == 0) mma_role<kStreamKeys, kFormat>(p, br, w, at, tmem);
   } else if (warp == 2) {
-    if (at.rank == 0) wait_role<kStreamKeys, kPoll>(p, br, w);
-  } else if (warp >= 4 && warp < 8) {
-    sum_role<kStreamKeys, kPoll>(p, br, w, tmem, at.rank, pair_index);
-  } else if constexpr (kFp8) {
-    if (warp >= 8) widen_role<kStreamKeys, kPoll>(p, smem, br, w, at, threadIdx.x - 256);
+    if (at.rank == 0) wait_role<kStreamKeys, kFormat, kPoll>(p, br, w);
+  } else if (warp < 4 + C::sum_warps) {
+    sum_role<kStreamKeys, kFormat, kPoll>(p, smem, br, w, tmem, at.rank, pair_index);
+  } else if constexpr (C::fp8) {
+    widen_role<kStreamKeys, kFormat, kPoll>(p, br, w, at, threadIdx.x - 32 * (4 + C::sum_warps));
   }
   __syncwarp();
   tc_fence_before();
@@ -654,7 +782,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(kFp8), 1)
   cluster_sync();  // nothing of the peer's reads or arrives here any more
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc_pair(tmem, kD * kRows);
+    tmem_dealloc_pair(tmem, 512);
   }
 }
 
@@ -719,7 +847,8 @@ using namespace mla;
 
 extern "C" size_t mla_attention_mass_workspace_bytes(int B, int T, int H, int mass_cap) {
   if (check_sizes(B, T, H, mass_cap) != MLA_OK) return 0;
-  return T * H <= kRows ? 0 : kMostPairs * 2 * kTileKeys * sizeof(float);
+  // (a tile of query rows of the format with most tiles)
+  return T * H <= Of<MLA_KV_FP8_E4M3>::rows ? 0 : kMostPairs * 2 * kTileKeys * sizeof(float);
 }
 
 extern "C" int mla_attention_mass(const void *q, const void *kv_cache, int kv_format, int num_pages, int page_size,
@@ -772,9 +901,10 @@ extern "C" int mla_attention_mass(const void *q, const void *kv_cache, int kv_fo
   p.cap = mass_cap;
   p.causal = causal;
   p.rows = T * H;
-  p.n_qt = ceil_div(p.rows, kRows);
-  p.box = p.rows < kRows ? ceil_div(p.rows, 16) * 16 : kRows;
-  p.scale_log2 = softmax_scale * LOG2E;
+  const int tile_rows = kv_format == MLA_KV_FP8_E4M3 ? Of<MLA_KV_FP8_E4M3>::rows : kMostRows;
+  p.n_qt = ceil_div(p.rows, tile_rows);
+  p.box = p.rows < tile_rows ? ceil_div(p.rows, 16) * 16 : tile_rows;
+  p.scale = softmax_scale;
   p.decay = decay;
   p.wait_ns = wait_limit_ns();
 
@@ -806,18 +936,26 @@ extern "C" int mla_attention_mass(const void *q, const void *kv_cache, int kv_fo
   p.slots = (int)((kRoom - resident) / kBlock);
   if (p.slots > kMostSlots) p.slots = kMostSlots;
   cudaError_t e = cudaSuccess;
-  const bool keys = p.n_qt == 1, fp8 = kv_format != MLA_KV_BF16, poll = p.wait_ns < kShortWaitNs;
+  const bool keys = p.n_qt == 1, poll = p.wait_ns < kShortWaitNs;
   using Kernel = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, MassParams);
   Kernel k = nullptr;
-#define PICK(a, b, c) \
-  if (keys == a && fp8 == b && poll == c) k = attention_mass_kernel<a, b, c>
-  PICK(false, false, false); PICK(false, false, true); PICK(false, true, false); PICK(false, true, true);
-  PICK(true, false, false); PICK(true, false, true); PICK(true, true, false); PICK(true, true, true);
+  int threads = 0;
+#define PICK(format)                                                                                              \
+  case format:                                                                                                    \
+    k = keys ? (poll ? attention_mass_kernel<true, format, true> : attention_mass_kernel<true, format, false>)    \
+             : (poll ? attention_mass_kernel<false, format, true> : attention_mass_kernel<false, format, false>); \
+    threads = Of<format>::threads;                                                                                \
+    break
+  switch (kv_format) {
+    PICK(MLA_KV_BF16);
+    PICK(MLA_KV_FP8_E4M3);
+    PICK(MLA_KV_FP8_E4M3_TENSOR);
+  }
 #undef PICK
   cudaStream_t s = (cudaStream_t)stream;
   if (e == cudaSuccess) e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
-  if (e == cudaSuccess) e = launch_dependent(k, 2 * pairs, threads_of(fp8), kSmem, s, k_map, pe_map, q_map, p);
-  if (e == cudaSuccess && need) e = launch_dependent(mass_reduce_kernel, pairs, kTileKeys, 0, s, p, pairs);
+  if (e == cudaSuccess) e = launch_dependent(k, 2 * pairs, threads, kSmem, s, k_map, pe_map, q_map, p);
+  if (e == cudaSuccess && p.n_qt > 1) e = launch_dependent(mass_reduce_kernel, pairs, kTileKeys, 0, s, p, pairs);
   if (e != cudaSuccess) {
     char msg[128];
     snprintf(msg, sizeof msg, "attention mass: %s", cudaGetErrorString(e));

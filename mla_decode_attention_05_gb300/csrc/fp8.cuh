@@ -30,4 +30,21 @@ __device__ __forceinline__ void widen16(const uint4 &codes, float scale, uint4 &
   hi = make_uint4(o[4], o[5], o[6], o[7]);
 }
 
+// 16 e4m3 codes -> 16 bf16 values, exactly.
+__device__ __forceinline__ void codes16(const uint4 &codes, uint4 &lo, uint4 &hi) {
+  const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
+  uint32_t o[8];
+#pragma unroll
+  for (int i = 0; i < 8; i++) {
+    const uint16_t pair = (uint16_t)(w[i >> 1] >> (16 * (i & 1)));
+    uint32_t half2;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(half2) : "h"(pair));
+    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&half2));
+    const __nv_bfloat162 v = __floats2bfloat162_rn(f.x, f.y);
+    o[i] = *reinterpret_cast<const uint32_t *>(&v);
+  }
+  lo = make_uint4(o[0], o[1], o[2], o[3]);
+  hi = make_uint4(o[4], o[5], o[6], o[7]);
+}
+
 }  // namespace mla

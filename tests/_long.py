@@ -9,7 +9,7 @@ from _ops import HALF_BF16, STEP_F32, f64
 class Cache:
     """A pool of pages.  Unused rows hold `fill` (NaN codes in FP8 where it is
     nan); `rows(pages, n)` gives the first n tokens behind a page list as the
-    kernels see them (FP8 rows with scales rounded to bf16)."""
+    kernels see them (FP8 rows with scales rounded to bf16), `exact_rows` unrounded."""
 
     def __init__(self, rng, pages, fmt, std=1.0):
         self.fmt, self.pages = fmt, pages
@@ -17,12 +17,13 @@ class Cache:
         self.scales = None
         if fmt == "bf16":
             self.data = x.to(torch.bfloat16)
-            self.seen = self.data.double()
+            self.seen = self.exact = self.data.double()
         elif fmt == "fp8_tensor":
             self.scales = torch.tensor([2.0 ** -6 * 1.25])
             codes = (x / self.scales).clamp(-448, 448).to(torch.float8_e4m3fn)
             self.data = codes.view(torch.uint8)
             self.seen = (codes.float() * self.scales).to(torch.bfloat16).double()
+            self.exact = codes.double() * self.scales.double()
         else:
             tiles = x[..., :512].reshape(pages, 64, 4, 128)
             self.scales = (tiles.abs().amax(-1) / 448).contiguous()
@@ -31,6 +32,8 @@ class Cache:
             self.data = torch.cat([codes.view(torch.uint8).reshape(pages, 64, 512), pe.view(torch.uint8)], -1).contiguous()
             latent = (codes.float() * self.scales[..., None]).to(torch.bfloat16).reshape(pages, 64, 512)
             self.seen = torch.cat([latent, pe], -1).double()
+            latent = (codes.double() * self.scales[..., None].double()).reshape(pages, 64, 512)
+            self.exact = torch.cat([latent, pe.double()], -1)
         self.order = [int(i) for i in rng.permutation(pages)]
 
     def take(self, n):
@@ -59,6 +62,11 @@ class Cache:
         if n == 0:
             return np.zeros((0, 576))
         return self.seen[pages].reshape(-1, 576)[:n].numpy()
+
+    def exact_rows(self, pages, n):
+        if n == 0:
+            return np.zeros((0, 576))
+        return self.exact[pages].reshape(-1, 576)[:n].numpy()
 
     def cuda(self):
         return self.data.cuda(), None if self.scales is None else self.scales.cuda()

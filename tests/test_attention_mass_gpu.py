@@ -20,7 +20,7 @@ def _make(seed, fmt, T, H, lens, causal, spoil=True):
     q = bf16(rng, (len(lens), T, H, 576), 1.3)
     lse = torch.empty(len(lens), H, T)
     for b, n in enumerate(lens):
-        ref = O.attention(q[b].double().numpy(), np.zeros((0, 576)), c.rows(pages[b], n), SCALE, causal)
+        ref = O.attention(q[b].double().numpy(), np.zeros((0, 576)), c.exact_rows(pages[b], n), SCALE, causal)
         lse[b] = torch.from_numpy(ref["lse"]).t()
     return c, pages, q, lse
 
@@ -28,7 +28,7 @@ def _make(seed, fmt, T, H, lens, causal, spoil=True):
 def _check(c, pages, q, lse, lens, causal, before, decay, got):
     T, H = q.shape[1], q.shape[2]
     for b, n in enumerate(lens):
-        want, bound = O.mass(q[b].double().numpy(), c.rows(pages[b], n), lse[b].t().double().numpy(), SCALE, causal)
+        want, bound = O.mass(q[b].double().numpy(), c.exact_rows(pages[b], n), lse[b].t().double().numpy(), SCALE, causal)
         old = decay * f64(before[b, :n]) if decay else np.zeros(n)
         err = np.abs(f64(got[b, :n]) - (want + old))
         # the weights' own bounds, a step for each addition of the T * H, and the two roundings of the update
@@ -52,6 +52,12 @@ CASES = [
     ("fp8", 2, 100, [129, 70], True, 0.0),
     ("fp8_tensor", 1, 40, [200, 0, 65], False, 0.9),
     ("fp8_tensor", 5, 64, [190], True, 1.0),
+    ("fp8", 1, 8, [20000, 4097], False, 0.5),           # many key tiles one after the other
+    ("fp8", 2, 128, [5000, 64 * 39 + 1], True, 1.0),    # and two tiles of query rows
+    ("fp8", 3, 100, [5000], True, 1.0),
+    ("fp8_tensor", 1, 8, [20000, 4097], False, 0.5),
+    ("fp8_tensor", 64, 10, [2500], True, 1.0),
+    ("fp8", 64, 10, [2500, 20], True, 1.0),
 ]
 
 
@@ -108,7 +114,7 @@ def test_rows_without_weight_and_bad_pages():
     data, _ = c.cuda()
     mla.device_status()
     got = mla_mass(q, data, pages, lens, lse, before.cuda())
-    want, _ = O.mass(q[0].double().numpy(), c.rows(pages[0], 100), lse[0].t().double().numpy(), SCALE, False)
+    want, _ = O.mass(q[0].double().numpy(), c.exact_rows(pages[0], 100), lse[0].t().double().numpy(), SCALE, False)
     assert np.allclose(f64(got[0, :100]), want, rtol=1e-4, atol=1e-7)
     assert got[1, :70].isnan().all() and (got[1, 70:] == 0).all()  # a row of nan reaches what it sees, and nothing else
     bt = table(pages)
