@@ -485,13 +485,16 @@ int mla_value_project(const void *attn, int64_t ld_token, int64_t ld_head, const
  *   workspace      device, >= mla_decode_shared_workspace_bytes(...) bytes for the
  *                  current device, 256-byte aligned; no initialisation; calls
  *                  that overlap on the GPU need separate ones
- * Probabilities are rounded to bf16 before they multiply the values, FP8 rows with
- * scales to bf16 before both products; parts of an output are joined in fp32 and
- * rounded once.  What the cache holds behind the last token of a sequence or prefix
+ * Probabilities are rounded to bf16 before they multiply the values, and so are the
+ * values of FP8 rows with a scale for each 128; their keys are not rounded to fewer
+ * than 22 bits.  Codes with one scale are exact.  Parts of an output are joined in
+ * fp32 and rounded once.  Scales are finite, and >= 0 for one scale.  What the cache holds behind the last token of a sequence or prefix
  * does not matter (inf and nan included); the tokens' own rows must be finite.  A
  * page outside the pool is skipped and sets MLA_STATUS_BAD_PAGE.  Of an FP8 cache,
- * prefix pages are widened to bf16 in the workspace (73728 bytes an entry of
- * prefix_table), and own pages too where B * max_pages <= 4096.  At most 8192 work
+ * prefix pages are widened in the workspace (73728 bytes an entry of
+ * prefix_table, with a scale for each 128 values 204804), and own pages too where
+ * B * max_pages <= 2048; where it is more, own FP8 rows are rounded to bf16 as
+ * mla_decode's.  At most 8192 work
  * items: B * ceil(T * H / 128) + ceil(B * T * H / 128) + G (MLA_ERR_UNSUPPORTED above).
  * A wait that gives up sets MLA_STATUS_WAIT_TIMEOUT.  Asynchronous on `stream`; can
  * be captured in a CUDA graph.  Returns MLA_OK or a negative code.
@@ -525,10 +528,10 @@ int mla_decode_shared(const void *q, const void *kv_cache, int kv_format, int nu
  *   mass           device fp32 [B][mass_cap], updated; mass_cap at most 2^24
  *   workspace      device, >= mla_attention_mass_workspace_bytes(B, T, H, mass_cap)
  *                  bytes, 256-byte aligned (NULL where that is 0, as it is for
- *                  T * H <= 256); no initialisation; calls that overlap on the GPU
+ *                  T * H <= 128); no initialisation; calls that overlap on the GPU
  *                  need separate ones
- * Scores and sums are fp32; FP8 rows with scales are rounded to bf16, as the
- * decode does.  Sums are made in a fixed order: equal calls give equal bits.  A
+ * Scores and sums are fp32 and FP8 rows exact (their scales multiply partial
+ * scores).  Sums are made in a fixed order: equal calls give equal bits.  A
  * token whose page lies outside the pool gets no weight and sets
  * MLA_STATUS_BAD_PAGE.  A wait that gives up sets MLA_STATUS_WAIT_TIMEOUT.
  * Asynchronous on `stream`; can be captured in a CUDA graph.  Returns MLA_OK or a

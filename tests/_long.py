@@ -7,9 +7,9 @@ from _ops import HALF_BF16, STEP_F32, f64
 
 
 class Cache:
-    """A pool of pages.  Unused rows hold `fill` (NaN codes in FP8 where it is
-    nan); `rows(pages, n)` gives the first n tokens behind a page list as the
-    kernels see them (FP8 rows with scales rounded to bf16), `exact_rows` unrounded."""
+    """A pool of pages.  `exact_rows(pages, n)` gives the first n tokens behind a
+    page list, FP8 rows as code times scale; `rows` has these rounded to bf16, as
+    the decode kernel sees them."""
 
     def __init__(self, rng, pages, fmt, std=1.0):
         self.fmt, self.pages = fmt, pages
@@ -85,15 +85,25 @@ def i32(values):
     return torch.tensor(values, dtype=torch.int32, device="cuda")
 
 
-def check_rows(got, lse, ref, n_keys):
+def check_rows(got, lse, ref, n_keys, fmt="bf16"):
     """One sequence's out [T, H, 512] and lse [T, H] against oracle.long_context's.
 
     Score error d: 576 products in fp32, and the rounding of score and reference
     in the exponent.  p: relative error d + 2^-21 (the exponential), then half a
     bf16 step.  The sum: the same without that step, and n additions.  out: the
     weighted sum of |v| times these, n additions, the join's weights (d again),
-    and half a bf16 step of the result."""
+    and half a bf16 step of the result.
+
+    FP8 with one scale: codes are exact, two more roundings of scores and output in
+    fp32.  With a scale for each 128 values: each product of code and scale is the
+    sum of two fp16 values as a key (half a step of half a step: 2^-22; 2^-39 of the
+    page's largest is the smallest part) and rounded to bf16 as a value (half a step)."""
     d = 576 * STEP_F32 * ref["mag"] + 4 * STEP_F32 * ref["top"] + 2.0 ** -20
+    v = 0.0
+    if fmt == "fp8_tensor":
+        d, v = d + 2 * STEP_F32 * ref["top"], 2 * STEP_F32
+    elif fmt == "fp8":
+        d, v = d + 512 * STEP_F32 * ref["mag"] + (2.0 ** -22 + 2.0 ** -28) * ref["mag"], HALF_BF16 + STEP_F32
     n = max(1, n_keys) * STEP_F32
     got, lse = f64(got), f64(lse)
     empty = np.isneginf(ref["lse"])
@@ -103,7 +113,7 @@ def check_rows(got, lse, ref, n_keys):
     err = np.abs(lse[live] - ref["lse"][live])
     tol = (d + n)[live] + 4 * STEP_F32 * np.abs(ref["lse"][live]) + 4 * STEP_F32 * ref["top"][live]
     assert np.all(err <= tol), f"lse off by {err.max()}, bound {tol[err.argmax()]}"
-    rel = (HALF_BF16 + 3 * d + 2 * n)[..., None]
+    rel = (HALF_BF16 + v + 3 * d + 2 * n)[..., None]
     tol = ref["spread"] * rel + HALF_BF16 * (np.abs(ref["out"]) + ref["spread"] * rel) + 1e-38
     err = np.abs(got - ref["out"])[live]
     assert np.all(err <= tol[live]), f"out off by {err.max()}"

@@ -31,16 +31,18 @@ def _run(c, pre, mine, q, prefixes, offsets, own, causal, **kw):
                              group_offsets=None if offsets is None else i32(offsets), causal=causal, kv_scales=scales, **kw)
 
 
-def _check(c, pre, mine, q, prefixes, offsets, own, causal, out, lse, seqs=None):
+def _check(c, pre, mine, q, prefixes, offsets, own, causal, out, lse, seqs=None, rounded=False):
+    """rounded: own tokens go through the decode kernel."""
     group = {}
     for g in range(len(prefixes)):
         for b in range(offsets[g] if offsets else 0, offsets[g + 1] if offsets else len(own)):
             group[b] = g
     for b in seqs if seqs is not None else range(len(own)):
         g = group.get(b)
-        prefix = np.zeros((0, 576)) if g is None else c.rows(pre[g], prefixes[g])
-        ref = O.attention(q[b].double().numpy(), prefix, c.rows(mine[b], own[b]), SCALE, causal)
-        check_rows(out[b], lse[b].t(), ref, len(prefix) + own[b])
+        prefix = np.zeros((0, 576)) if g is None else c.exact_rows(pre[g], prefixes[g])
+        rows = (c.rows if rounded else c.exact_rows)(mine[b], own[b])
+        ref = O.attention(q[b].double().numpy(), prefix, rows, SCALE, causal)
+        check_rows(out[b], lse[b].t(), ref, len(prefix) + own[b], c.fmt)
 
 
 CASES = [
@@ -73,6 +75,50 @@ def test_matches_the_oracle(case):
     assert mla.device_status() == 0
 
 
+def _log2_sizes(rng, n, spread):
+    return torch.from_numpy(2.0 ** rng.integers(-spread, spread + 1, n).astype(np.float32))
+
+
+@pytest.mark.parametrize("fmt", ["fp8", "fp8_tensor"])
+@pytest.mark.parametrize("size", [2.0 ** -90, 2.0 ** 60])
+def test_fp8_rows_and_queries_of_any_size(fmt, size):
+    """Keys far outside fp16's range, and queries that undo it; rows of other sizes
+    side by side; a page whose latent or whose rotated part is all zeros."""
+    T, H, prefixes, own = 1, 40, [150], [70, 64, 3]
+    c, pre, mine, q = _make(336, fmt, T, H, prefixes, None, own)
+    rng = np.random.default_rng(337)
+    c.scales *= size
+    if fmt == "fp8":
+        tiles = _log2_sizes(rng, (c.pages, 64, 4), 6)
+        c.scales *= tiles
+        pe = c.data[..., 512:].contiguous().view(torch.bfloat16)
+        pe *= size
+        c.data[pre[0][0], :, :512] = 0
+        pe[pre[0][1]] = 0
+        c.data[..., 512:] = pe.view(torch.uint8)
+        codes = c.data[..., :512].contiguous().view(torch.float8_e4m3fn).double().reshape(c.pages, 64, 4, 128)
+        c.exact = torch.cat([(codes * c.scales[..., None].double()).reshape(c.pages, 64, 512), pe.double()], -1)
+    else:
+        c.exact = c.data.view(torch.float8_e4m3fn).double() * c.scales.double()
+    q = (q.float() * _log2_sizes(rng, (3, T, H, 1), 5) / 64 / size).to(torch.bfloat16)
+    out, lse = _run(c, pre, mine, q, prefixes, None, own, False)
+    if size < 1:  # the test's bounds hold relative to the output's size: bf16 has its smallest numbers at 2^-126
+        assert (out != 0).any()
+    _check(c, pre, mine, q, prefixes, None, own, False, out, lse)
+
+
+@pytest.mark.parametrize("fmt", ["fp8", "fp8_tensor"])
+def test_fp8_scales_of_zero(fmt):
+    """Cached rows that are all zeros, as an empty model's: every key counts alike."""
+    c, pre, mine, q = _make(338, fmt, 1, 16, [70], None, [5, 0])
+    c.scales[...] = 0
+    if fmt == "fp8":
+        c.data[..., 512:] = 0
+    out, lse = _run(c, pre, mine, q, [70], None, [5, 0], False)
+    assert (out == 0).all()
+    assert torch.allclose(lse[:, :, 0].cpu(), torch.log(torch.tensor([[75.0], [70.0]])), atol=1e-6)
+
+
 @pytest.mark.parametrize("fmt", ["fp8", "fp8_tensor"])
 def test_fp8_own_tokens_behind_a_wide_page_table(fmt):
     """A page table too wide for its pages to be widened ahead."""
@@ -82,7 +128,7 @@ def test_fp8_own_tokens_behind_a_wide_page_table(fmt):
     data, scales = c.cuda()
     out, lse = mla.decode_shared(q.cuda(), data, table(pre), i32(prefixes), table(mine, 1400), i32(own), softmax_scale=SCALE,
                                  group_offsets=i32(offsets), causal=True, kv_scales=scales)
-    _check(c, pre, mine, q, prefixes, offsets, own, True, out, lse)
+    _check(c, pre, mine, q, prefixes, offsets, own, True, out, lse, rounded=True)
 
 
 def test_many_sequences_and_a_long_prefix():

@@ -33,8 +33,9 @@ def test_what_lies_behind_the_last_token_does_not_count(fmt, width):
     out, lse = mla.decode_shared(q.cuda(), data, table(pre), i32(prefixes), table(mine, width), i32(own), softmax_scale=SCALE,
                                  group_offsets=i32(offsets), causal=True, kv_scales=scales)
     for b, g in enumerate([0, 0, 1, 1]):
-        ref = O.attention(q[b].double().numpy(), c.rows(pre[g], prefixes[g]), c.rows(mine[b], own[b]), SCALE, True)
-        check_rows(out[b], lse[b].t(), ref, prefixes[g] + own[b])
+        rows = (c.rows if width else c.exact_rows)(mine[b], own[b])  # (a wide table's own rows go through the decode kernel)
+        ref = O.attention(q[b].double().numpy(), c.exact_rows(pre[g], prefixes[g]), rows, SCALE, True)
+        check_rows(out[b], lse[b].t(), ref, prefixes[g] + own[b], fmt)
 
 
 def test_scores_that_grow_a_lot():
@@ -48,12 +49,12 @@ def test_scores_that_grow_a_lot():
     pages = c.take(n)
     for i, j in enumerate((3, 5, 9)):   # three pages ever larger
         c.data[pages[j]] *= 4 * 3 ** i
-    c.seen = c.data.double()
+    c.exact = c.data.double()
     q = bf16(rng, (3, 1, 16, 576), 2.0)
     out, lse = mla.decode_shared(q.cuda(), c.data.cuda(), table([pages]), i32([n]), table([[]] * 3, 1), i32([0, 0, 0]),
                                  softmax_scale=SCALE)
     for b in range(3):
-        ref = O.attention(q[b].double().numpy(), c.rows(pages, n), np.zeros((0, 576)), SCALE, False)
+        ref = O.attention(q[b].double().numpy(), c.exact_rows(pages, n), np.zeros((0, 576)), SCALE, False)
         assert (ref["top"] > 60).any()
         check_rows(out[b], lse[b].t(), ref, n)
 
@@ -160,7 +161,7 @@ def test_a_cache_that_stays_small():
             sums[b].append(0.0)
             where[b].append(P + step)
             own, qb = np.array(rows[b]), q[b].double().cpu().numpy()
-            ref = O.attention(qb, c.rows(pre, P), own, SCALE, False)
+            ref = O.attention(qb, c.exact_rows(pre, P), own, SCALE, False)
             check_rows(out[b], lse[b].t(), ref, P + len(own))
             weights, _ = O.mass(qb, own, lse[b].t().double().cpu().numpy(), SCALE, False)
             sums[b] = list(np.array(sums[b]) + weights)
