@@ -11,6 +11,7 @@
 // holds and reads of the query rows: alone, an SM has room for 128 rows and 64 KB
 // of keys on their way, and with many rows its shared memory is the limit: 8192
 // rows on 12001 keys 101 us.)
+#include <atomic>
 #include <cmath>
 #include <cstdio>
 
@@ -55,6 +56,10 @@ struct Of {
   static constexpr int threads = 32 * (4 + sum_warps + wide_warps);
 };
 constexpr int kWideGroups = 4;
+// With scales: registers of the threads that load, sum and widen (96 each would spill where
+// scores are summed, 48.5 us instead of 44.6 for 32 sequences of up to 8192 tokens, two query
+// tokens, 64 heads).
+constexpr int kLoadRegs = 72, kSumRegs = 120, kWideRegs = 80;
 constexpr uint32_t IDESC = idesc_bf16_f32(kTileKeys, 16, false, false) - (2u << 17);  // N is added
 
 struct MassParams {
@@ -527,16 +532,6 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// 32 lanes x 16 columns (see tmem_ld32).
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
-        "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr)
-      : "memory");
-}
-
 // The warps from 4 on that sum: thread = key of the tile = lane of tensor memory (and,
 // with scales, half of the columns).
 template <bool kStreamKeys, int kFormat, bool kPoll>
@@ -668,15 +663,15 @@ __device__ void sum_role(const MassParams &p, uint8_t *base, Bars &br, const Wor
           const float factor = part == 0 ? sc.x : part == 1 ? sc.y : part == 2 ? sc.z : part == 3 ? sc.w : 1.f;
           const float2 f2 = make_float2(factor, factor);
 #pragma unroll
-          for (int q = 0; q < 4; q++) {
-            if (q * 16 < cols) {
-              float2 v[8];
+          for (int q = 0; q < 2; q++) {
+            if (q * 32 < cols) {
+              float2 v[16];
               __syncwarp();
-              tmem_ld16(lt + (g % kD) * kRows + q * 16, *reinterpret_cast<uint32_t(*)[16]>(&v[0]));
+              tmem_ld32(lt + (g % kD) * kRows + q * 32, *reinterpret_cast<uint32_t(*)[32]>(&v[0]));
               tmem_wait_ld();
 #pragma unroll
-              for (int j = 0; j < 8; j++) {
-                float2 &to = x[q >> 1][(q & 1) * 8 + j];
+              for (int j = 0; j < 16; j++) {
+                float2 &to = x[q][j];
                 to = part == 0 ? mul2(v[j], f2) : fma2(v[j], f2, to);
               }
             }
@@ -759,15 +754,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Of<kFormat>::threads
   const uint32_t tmem = br.tmem_base;
   grid_dep_wait();
   const Work w = find_work(p, br, pair_index, pairs);
-  if (warp == 0 || warp == 3) {
-    load_role<kStreamKeys, kFormat, kPoll>(p, smem, br, &k_map, &pe_map, &q_map, w, at, warp == 3);
-  } else if (warp == 1) {
-    if (at.rank == 0) mma_role<kStreamKeys, kFormat>(p, br, w, at, tmem);
-  } else if (warp == 2) {
-    if (at.rank == 0) wait_role<kStreamKeys, kFormat, kPoll>(p, br, w);
+  if (warp < 4) {
+    if constexpr (C::scaled) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLoadRegs));
+    if (warp == 0 || warp == 3) load_role<kStreamKeys, kFormat, kPoll>(p, smem, br, &k_map, &pe_map, &q_map, w, at, warp == 3);
+    else if (at.rank == 0 && warp == 1) mma_role<kStreamKeys, kFormat>(p, br, w, at, tmem);
+    else if (at.rank == 0 && warp == 2) wait_role<kStreamKeys, kFormat, kPoll>(p, br, w);
   } else if (warp < 4 + C::sum_warps) {
+    if constexpr (C::scaled) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSumRegs));
     sum_role<kStreamKeys, kFormat, kPoll>(p, smem, br, w, tmem, at.rank, pair_index);
   } else if constexpr (C::fp8) {
+    if constexpr (C::scaled) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kWideRegs));
     widen_role<kStreamKeys, kFormat, kPoll>(p, br, w, at, threadIdx.x - 32 * (4 + C::sum_warps));
   }
   __syncwarp();
@@ -839,6 +835,21 @@ int sm_pairs(int *pairs) {
 
 // Room for the partial sums of twice as many pairs as any GPU of this kind has.
 constexpr size_t kMostPairs = 160;
+
+// Warpgroups that ask for more registers than the block was launched with wait for ever.
+// Looked at once for each of the four kernels.
+cudaError_t registers_suffice(const void *kernel, int threads, bool keys, bool poll) {
+  static std::atomic<int> seen[4];
+  std::atomic<int> &s = seen[2 * keys + poll];
+  if (s.load(std::memory_order_relaxed)) return cudaSuccess;
+  cudaFuncAttributes a;
+  const cudaError_t e = cudaFuncGetAttributes(&a, kernel);
+  if (e != cudaSuccess) return e;
+  using C = Of<MLA_KV_FP8_E4M3>;
+  if (a.numRegs * threads < 32 * (4 * kLoadRegs + C::sum_warps * kSumRegs + C::wide_warps * kWideRegs)) return cudaErrorLaunchOutOfResources;
+  s.store(1, std::memory_order_relaxed);
+  return cudaSuccess;
+}
 
 }  // namespace
 }  // namespace mla
@@ -953,6 +964,7 @@ extern "C" int mla_attention_mass(const void *q, const void *kv_cache, int kv_fo
   }
 #undef PICK
   cudaStream_t s = (cudaStream_t)stream;
+  if (e == cudaSuccess && kv_format == MLA_KV_FP8_E4M3) e = registers_suffice(reinterpret_cast<const void *>(k), threads, keys, poll);
   if (e == cudaSuccess) e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
   if (e == cudaSuccess) e = launch_dependent(k, 2 * pairs, threads, kSmem, s, k_map, pe_map, q_map, p);
   if (e == cudaSuccess && p.n_qt > 1) e = launch_dependent(mass_reduce_kernel, pairs, kTileKeys, 0, s, p, pairs);
