@@ -33,7 +33,7 @@ constexpr int kTileKeys = 2 * kKeys;
 constexpr int kBlocks = D_QK / 64;             // blocks of 64 of the 576 dims
 constexpr uint32_t kBlock = kKeys * 128;       // 128 rows x 64 dims, 128-byte swizzle
 constexpr uint32_t kHalf = kBlock / 2;
-constexpr int kMostSlots = 9;                  // blocks of the streaming operand
+constexpr int kMostSlots = 9;                  // units of the streaming operand
 constexpr int kMostRows = 256;                 // query rows of a tile
 
 // What depends on the cache's format.  No rounding is made on the way to the scores:
@@ -52,10 +52,17 @@ struct Of {
   static constexpr int cols = rows / halves;                   // columns of a thread
   static constexpr int sum_warps = 4 * halves;
   static constexpr int wide_warps = !fp8 ? 0 : scaled ? 8 : 16;  // warps that widen cached rows,
-  static constexpr int group_warps = wide_warps / 4;           // in four groups that take the blocks in turn
   static constexpr int threads = 32 * (4 + sum_warps + wide_warps);
+  // Operands come in units: a block, or with FP8 two (a last one alone), so that a row of a
+  // copy is 128 bytes (rows of 64 codes: 44.5 us instead of 38.8 for 32 sequences of up to 8192
+  // tokens, two query tokens, 64 heads)
+  static constexpr int unit = fp8 ? 2 : 1, units = fp8 ? 5 : kBlocks;
+  __device__ static constexpr int blocks(int u) { return u < kBlocks / unit ? unit : kBlocks % unit; }
+  // The score tile that unit u belongs to begins, or ends, with it.
+  __device__ static constexpr bool begins(int u) { return parts > 1 || u == 0; }
+  __device__ static constexpr bool ends(int u) { return parts > 1 || u == units - 1; }
 };
-constexpr int kWideGroups = 4;
+constexpr int kGroupWarps = 4;  // warps that widen a unit together
 // With scales: registers of the threads that load, sum and widen (96 each would spill where
 // scores are summed, 48.5 us instead of 44.6 for 32 sequences of up to 8192 tokens, two query
 // tokens, 64 heads).
@@ -80,7 +87,7 @@ struct MassParams {
 struct Bars {
   uint64_t res_full[kBlocks], res_empty[kBlocks];        // full: rank 0, for both CTAs
   uint64_t slot_full[kMostSlots], slot_empty[kMostSlots];
-  uint64_t raw_full[kMostSlots];  // FP8: a block's codes are in place (of the resident blocks, or of the slots)
+  uint64_t raw_full[kMostSlots];  // FP8: a unit's codes are in place (of the resident ones, or of the slots)
   uint64_t d_full[4], d_empty[4];                        // empty: rank 0
   uint64_t sc_full[2], sc_empty[2];                      // a tile's scales
   alignas(16) float nl[2][kMostRows];  // -lse of a tile's query rows
@@ -258,19 +265,9 @@ __device__ Work find_work(const MassParams &p, Bars &br, int pair, int pairs) {
   return w;
 }
 
-__device__ __forceinline__ int page_of(const MassParams &p, int b, int j, int len) {
-  if ((long long)j * PAGE >= len) return -1;
-  const int page = __ldg(p.block_table + (size_t)b * p.max_pages + j);
-  if (page < 0 || page >= p.num_pages) {
-    atomicOr(p.status, MLA_STATUS_BAD_PAGE);
-    return -1;
-  }
-  return page;
-}
-
 // Where this CTA's operands lie.
 struct Place {
-  uint32_t res, res_block, slots, rank;
+  uint32_t res, res_block, slots, slot_block, slot, rank;  // slot: bytes of a unit
 };
 
 // ---- loads -------------------------------------------------------------------------
@@ -279,9 +276,9 @@ struct Place {
 // (A warp's wait, arrival and copy take some 350 cycles together, whatever the copy's
 // size: one warp alone would take longer over a block's two pages than HBM.)  The
 // whole warp waits and looks pages up, one elected lane asks for the copies.  rank 0's
-// barriers count the bytes of both CTAs.  A block of FP8 rows lands as codes (64
-// bytes of each row) in the upper half of the block that it will fill, on a barrier
-// of this CTA; the rotated part of rows with scales is bf16 and lands as it is used.
+// barriers count the bytes of both CTAs.  A unit of FP8 rows lands as codes in the
+// upper half of what it will fill, on a barrier of this CTA; the rotated part of rows
+// with scales is bf16 and lands as it is used.
 template <bool kStreamKeys, int kFormat, bool kPoll>
 __device__ void load_role(const MassParams &p, uint8_t *base, Bars &br, const CUtensorMap *k_map, const CUtensorMap *pe_map,
                           const CUtensorMap *q_map, const Work &w, const Place &at, int which) {
@@ -311,20 +308,21 @@ __device__ void load_role(const MassParams &p, uint8_t *base, Bars &br, const CU
       pg[h] = (have >> at_lane) & 1 ? page : -1;
     }
   };
-  auto keys = [&](uint32_t dst, uint64_t *full, uint64_t *raw, int kb) {
+  auto keys = [&](uint32_t dst, uint64_t *full, uint64_t *raw, int u) {
     if (!elect_one()) return;
     const int page = pg[which];
     if (!C::fp8) {
       if (which == 0 && at.rank == 0) mbar_arrive_expect_tx(smem_u32(full), pages * kHalf);
-      if (page >= 0) tma_load_4d_pair(dst + which * kHalf, k_map, mapa(smem_u32(full), 0), 0, 0, kb, page, key_pol);
+      if (page >= 0) tma_load_4d_pair(dst + which * kHalf, k_map, mapa(smem_u32(full), 0), 0, 0, u, page, key_pol);
       return;
     }
     const uint32_t bar = smem_u32(raw), n = (pg[0] >= 0) + (pg[1] >= 0);
-    const bool codes = !(C::scaled && kb == 8);
-    if (which == 0) mbar_arrive_expect_tx(bar, n * (codes ? kHalf / 2 : kHalf));
+    const bool last = u == C::units - 1;
+    if (which == 0) mbar_arrive_expect_tx(bar, n * (last && !C::scaled ? kHalf / 2 : kHalf));
     if (page < 0) return;
-    if (codes) tma_load_3d(dst + kHalf + which * (kHalf / 2), k_map, bar, kb * 64, 0, page, key_pol);
-    else tma_load_3d(dst + which * kHalf, pe_map, bar, 0, 0, page, key_pol);
+    if (!last) tma_load_3d(dst + kBlock + which * kHalf, k_map, bar, u * 128, 0, page, key_pol);
+    else if (C::scaled) tma_load_3d(dst + which * kHalf, pe_map, bar, 0, 0, page, key_pol);
+    else tma_load_3d(dst + kHalf + which * (kHalf / 2), pe_map, bar, D_V, 0, page, key_pol);
   };
   // a tile's scales, both pages' by warp 3
   auto scales_of_tile = [&] {
@@ -343,15 +341,18 @@ __device__ void load_role(const MassParams &p, uint8_t *base, Bars &br, const CU
     return true;
   };
   const int half = p.box / 2;  // query rows of each CTA
-  auto rows = [&](uint32_t dst, uint64_t *full, int b, int qt, int kb) {
+  auto rows = [&](uint32_t dst, uint32_t block, uint64_t *full, int b, int qt, int u) {
     if (!elect_one()) return;
-    if (at.rank == 0) mbar_arrive_expect_tx(smem_u32(full), p.box * 128);
-    tma_load_3d_pair(dst, q_map, mapa(smem_u32(full), 0), 0, b * p.rows + qt * kRows + (int)at.rank * half, kb, keep);
+    const int n = C::blocks(u);
+    if (at.rank == 0) mbar_arrive_expect_tx(smem_u32(full), n * p.box * 128);
+    for (int j = 0; j < n; j++)
+      tma_load_3d_pair(dst + j * block, q_map, mapa(smem_u32(full), 0), 0, b * p.rows + qt * kRows + (int)at.rank * half,
+                       u * C::unit + j, keep);
   };
   for_each_phase<kStreamKeys, kRows>(p, w, [&](const Phase &f) {
     if (f.i0 >= f.i1) return true;
-    // (the first of what streams is asked for along with the resident blocks, so that
-    // both follow the last phase's MMAs block by block)
+    // (the first of what streams is asked for along with the resident units, so that
+    // both follow the last phase's MMAs unit by unit)
     fetch(f.b, f.t, f.len);
     if (!kStreamKeys) {
       look();
@@ -363,17 +364,19 @@ __device__ void load_role(const MassParams &p, uint8_t *base, Bars &br, const CU
         if (i + 1 < f.i1) fetch(f.b, i + 1, f.len);
         if (!scales_of_tile()) return false;
       }
-      for (int kb = 0; kb < kBlocks; kb++) {
+      for (int u = 0; u < C::units; u++) {
         if (i == f.i0 && (!kStreamKeys || which == 0)) {
-          if (!warp_wait<kPoll>(&br, &br.res_empty[kb], rph, p)) return false;
-          if (kStreamKeys) rows(at.res + kb * at.res_block, &br.res_full[kb], f.b, 0, kb);
-          else keys(at.res + kb * at.res_block, &br.res_full[kb], &br.raw_full[kb], kb);
+          if (!warp_wait<kPoll>(&br, &br.res_empty[u], rph, p)) return false;
+          const uint32_t dst = at.res + u * C::unit * at.res_block;
+          if (kStreamKeys) rows(dst, at.res_block, &br.res_full[u], f.b, 0, u);
+          else keys(dst, &br.res_full[u], &br.raw_full[u], u);
           __syncwarp();
         }
         if (!kStreamKeys && which == 1) continue;
         if (!warp_wait<kPoll>(&br, &br.slot_empty[s], ph, p)) return false;
-        if (kStreamKeys) keys(at.slots + s * kBlock, &br.slot_full[s], &br.raw_full[s], kb);
-        else rows(at.slots + s * kBlock, &br.slot_full[s], f.b, i, kb);
+        const uint32_t dst = at.slots + s * at.slot;
+        if (kStreamKeys) keys(dst, &br.slot_full[s], &br.raw_full[s], u);
+        else rows(dst, at.slot_block, &br.slot_full[s], f.b, i, u);
         __syncwarp();
         if (++s == p.slots) {
           s = 0;
@@ -398,47 +401,58 @@ __device__ __forceinline__ void st_shared_v4(uint32_t addr, const uint4 &v) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
 
-// The last warps widen FP8 codes in place, in groups that take the blocks in turn:
-// thread i of a group has 16 codes of rows i / 4 + a multiple of its group's.  All of a
-// group read their codes before any writes bf16 values over them.  (The codes come
+// The last warps widen FP8 codes in place, in groups that take the units in turn.  All
+// of a group read their codes before any writes bf16 values over them.  (The codes come
 // by TMA: a load of its own in flight would hold up the thread's proxy fences.)
-constexpr uint32_t kWideBar = 3;
+constexpr uint32_t kWideBar = 3, kGroupThreads = 32 * kGroupWarps;
+
+// Rows of kChunks * 16 codes at `raw` to blocks from `dst` on: thread i has 16 codes of
+// kChunks rows.
+template <int kChunks>
+__device__ __forceinline__ bool widen_unit(uint32_t dst, uint32_t raw, int i, int group, bool ok) {
+  constexpr int kStep = kGroupThreads / kChunks, kMine = kKeys / kStep;
+  static_assert(kStep % 8 == 0, "a thread's rows have one swizzle");
+  const int r = i / kChunks, c = i % kChunks, x = r & 7;
+  uint4 v[kMine];
+#pragma unroll
+  for (int j = 0; j < kMine; j++) v[j] = ld_shared_v4(raw + (r + kStep * j) * (kChunks * 16) + c * 16);
+  if (bar_red_or(kWideBar + group, kGroupThreads, !ok)) return false;
+#pragma unroll
+  for (int j = 0; j < kMine; j++) {
+    uint4 lo, hi;
+    codes16(v[j], lo, hi);
+    const uint32_t row = dst + (c >> 2) * kBlock + (r + kStep * j) * 128;
+    st_shared_v4(row + (((2 * (c & 3)) ^ x) << 4), lo);
+    st_shared_v4(row + (((2 * (c & 3) + 1) ^ x) << 4), hi);
+  }
+  fence_proxy_async_smem();
+  return true;
+}
 
 template <bool kStreamKeys, int kFormat, bool kPoll>
 __device__ void widen_role(const MassParams &p, Bars &br, const Work &w, const Place &at, int thread) {
   using C = Of<kFormat>;
-  constexpr int kThreads = 32 * C::group_warps, kStep = kThreads / 4, kMine = kKeys / kStep;  // rows between a thread's; its rows
-  static_assert(kStep % 8 == 0, "a thread's rows have one swizzle");
-  const int group = thread / kThreads, i = thread % kThreads;
-  const int r = i >> 2, c = i & 3, x = r & 7;
+  const int group = thread / kGroupThreads, i = thread % kGroupThreads;
   const bool first = (threadIdx.x & 31) == 0;
   int s = 0, turn = 0;
   uint32_t ph = 0, tile = 0;
   auto widen_tile = [&] {
-    for (int kb = 0; kb < kBlocks; kb++) {
+    for (int u = 0; u < C::units; u++) {
       if (turn == group) {
-        const int k = kStreamKeys ? s : kb;
-        const uint32_t dst = kStreamKeys ? at.slots + s * kBlock : at.res + kb * kBlock;
+        const int k = kStreamKeys ? s : u;
+        const uint32_t dst = kStreamKeys ? at.slots + s * at.slot : at.res + u * C::unit * kBlock;
         const bool ok = warp_wait<kPoll>(&br, &br.raw_full[k], kStreamKeys ? ph : tile & 1, p);
-        uint4 v[kMine];
-#pragma unroll
-        for (int j = 0; j < kMine; j++) v[j] = ld_shared_v4(dst + kHalf + (r + kStep * j) * 64 + c * 16);
-        if (bar_red_or(kWideBar + group, kThreads, !ok)) return false;
-        if (!(C::scaled && kb == 8)) {
-#pragma unroll
-          for (int j = 0; j < kMine; j++) {
-            uint4 lo, hi;
-            codes16(v[j], lo, hi);
-            const uint32_t row = dst + (r + kStep * j) * 128;
-            st_shared_v4(row + (((2 * c) ^ x) << 4), lo);
-            st_shared_v4(row + (((2 * c + 1) ^ x) << 4), hi);
-          }
+        if (u < C::units - 1) {
+          if (!widen_unit<8>(dst, dst + kBlock, i, group, ok)) return false;
+        } else if (!C::scaled) {
+          if (!widen_unit<4>(dst, dst + kHalf, i, group, ok)) return false;
+        } else if (bar_red_or(kWideBar + group, kGroupThreads, !ok)) {
+          return false;
         }
-        fence_proxy_async_smem();
         __syncwarp();
         if (first) mbar_arrive_pair(mapa(smem_u32(kStreamKeys ? &br.slot_full[k] : &br.res_full[k]), 0));
       }
-      if (++turn == kWideGroups) turn = 0;
+      if (++turn == C::wide_warps / kGroupWarps) turn = 0;
       if (++s == p.slots) {
         s = 0;
         ph ^= 1;
@@ -458,29 +472,23 @@ __device__ void widen_role(const MassParams &p, Bars &br, const Work &w, const P
 
 constexpr uint32_t kMmaBar = 1, kSumBar = 2;
 
-// The score tile that block kb belongs to begins, or ends, with it.
-template <int kFormat>
-__device__ __forceinline__ bool begins(int kb) { return Of<kFormat>::parts == 1 ? kb == 0 : (kb & 1) == 0; }
-template <int kFormat>
-__device__ __forceinline__ bool ends(int kb) { return kb == kBlocks - 1 || (Of<kFormat>::parts > 1 && (kb & 1)); }
-
 // rank 0, warp 2 waits for what the MMAs of warp 1 need and meets it at a named
 // barrier (a wait in the issuing warp would hold up its MMAs in flight).
 template <bool kStreamKeys, int kFormat, bool kPoll>
 __device__ void wait_role(const MassParams &p, Bars &br, const Work &w) {
-  constexpr int kD = Of<kFormat>::kd;
+  using C = Of<kFormat>;
   int s = 0;
   uint32_t ph = 0, rph = 0, g = 0;
-  for_each_phase<kStreamKeys, Of<kFormat>::rows>(p, w, [&](const Phase &f) {
+  for_each_phase<kStreamKeys, C::rows>(p, w, [&](const Phase &f) {
     if (f.i0 >= f.i1) return true;
     for (int i = f.i0; i < f.i1; i++) {
-      for (int kb = 0; kb < kBlocks; kb++) {
+      for (int u = 0; u < C::units; u++) {
         bool ok = true;
-        if (begins<kFormat>(kb)) {
-          ok = warp_wait<kPoll>(&br, &br.d_empty[g % kD], ((g / kD) & 1) ^ 1, p);
+        if (C::begins(u)) {
+          ok = warp_wait<kPoll>(&br, &br.d_empty[g % C::kd], ((g / C::kd) & 1) ^ 1, p);
           g++;
         }
-        if (ok && i == f.i0) ok = warp_wait<kPoll>(&br, &br.res_full[kb], rph, p);
+        if (ok && i == f.i0) ok = warp_wait<kPoll>(&br, &br.res_full[u], rph, p);
         if (ok) ok = warp_wait<kPoll>(&br, &br.slot_full[s], ph, p);
         if (bar_red_or(kMmaBar, 64, !ok)) return false;
         if (++s == p.slots) {
@@ -496,29 +504,33 @@ __device__ void wait_role(const MassParams &p, Bars &br, const Work &w) {
 
 template <bool kStreamKeys, int kFormat>
 __device__ void mma_role(const MassParams &p, Bars &br, const Work &w, const Place &at, uint32_t tmem) {
-  constexpr int kD = Of<kFormat>::kd, kRows = Of<kFormat>::rows;
+  using C = Of<kFormat>;
   const uint32_t idesc = IDESC + ((uint32_t)(p.box >> 3) << 17);
   int s = 0;
   uint32_t g = 0;
-  for_each_phase<kStreamKeys, kRows>(p, w, [&](const Phase &f) {
+  for_each_phase<kStreamKeys, C::rows>(p, w, [&](const Phase &f) {
     if (f.i0 >= f.i1) return true;
     for (int i = f.i0; i < f.i1; i++) {
-      for (int kb = 0; kb < kBlocks; kb++) {
+      for (int u = 0; u < C::units; u++) {
         if (bar_red_or(kMmaBar, 64, false)) return false;
         tc_fence_after();
         if (elect_one()) {
-          const uint64_t stay = smem_desc_sw128(at.res + kb * at.res_block, 16, 1024);
-          const uint64_t pass = smem_desc_sw128(at.slots + s * kBlock, 16, 1024);
-          const uint64_t a = kStreamKeys ? pass : stay, b = kStreamKeys ? stay : pass;
 #pragma unroll
-          for (int kk = 0; kk < 4; kk++)
-            mma_pair_ss(tmem + (g % kD) * kRows, a + kk * 2, b + kk * 2, idesc, !begins<kFormat>(kb) || kk ? 1u : 0u);
+          for (int j = 0; j < C::unit; j++) {
+            if (j >= C::blocks(u)) break;
+            const uint64_t stay = smem_desc_sw128(at.res + (u * C::unit + j) * at.res_block, 16, 1024);
+            const uint64_t pass = smem_desc_sw128(at.slots + s * at.slot + j * at.slot_block, 16, 1024);
+            const uint64_t a = kStreamKeys ? pass : stay, b = kStreamKeys ? stay : pass;
+#pragma unroll
+            for (int kk = 0; kk < 4; kk++)
+              mma_pair_ss(tmem + (g % C::kd) * C::rows, a + kk * 2, b + kk * 2, idesc, !C::begins(u) || j || kk ? 1u : 0u);
+          }
           mma_commit_pair(smem_u32(&br.slot_empty[s]));
-          if (i == f.i1 - 1) mma_commit_pair(smem_u32(&br.res_empty[kb]));
-          if (ends<kFormat>(kb)) mma_commit_pair(smem_u32(&br.d_full[g % kD]));
+          if (i == f.i1 - 1) mma_commit_pair(smem_u32(&br.res_empty[u]));
+          if (C::ends(u)) mma_commit_pair(smem_u32(&br.d_full[g % C::kd]));
         }
         __syncwarp();
-        if (ends<kFormat>(kb)) g++;
+        if (C::ends(u)) g++;
         if (++s == p.slots) s = 0;
       }
     }
@@ -599,17 +611,17 @@ __device__ void sum_role(const MassParams &p, uint8_t *base, Bars &br, const Wor
     auto key_of = [&](int t) { return t * kTileKeys + (int)rank * kKeys + i; };
     // what a key had before is fetched while its scores are made
     float before = 0.f;
-    bool placed = false;
+    int page = -1;
     auto prepare = [&](int t) {
       const int n = key_of(t);
       if (first > 0) return;
-      placed = n < f.len && page_of(p, f.b, n / PAGE, f.len) >= 0;
+      page = n < f.len ? __ldg(p.block_table + (size_t)f.b * p.max_pages + n / PAGE) : -1;
       if (f.whole && p.decay != 0.f && n < f.len) before = p.mass[(size_t)f.b * p.cap + n];
     };
     auto store = [&](int t, float v) {
       const int n = key_of(t);
       if (first > 0 || n >= f.len) return;
-      if (!placed) v = 0.f;
+      if (page < 0 || page >= p.num_pages) v = 0.f;  // (told by the warps that load)
       if (f.whole) p.mass[(size_t)f.b * p.cap + n] = p.decay != 0.f ? fmaf(p.decay, before, v) : v;
       else p.partial[((size_t)pair_index * 2 + f.part) * kTileKeys + rank * kKeys + i] = v;
     };
@@ -718,13 +730,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Of<kFormat>::threads
   at.res = smem_u32(smem + OFF_RES);
   at.res_block = kStreamKeys ? p.box / 2 * 128 : kBlock;
   at.slots = at.res + kBlocks * at.res_block;
+  at.slot_block = kStreamKeys ? kBlock : p.box / 2 * 128;
+  at.slot = C::unit * at.slot_block;
   if (threadIdx.x == 0) {
     for (int i = 0; i < kBlocks; i++) {
-      mbar_init(smem_u32(&br.res_full[i]), C::fp8 && !kStreamKeys ? 2 * C::group_warps : 1);
+      mbar_init(smem_u32(&br.res_full[i]), C::fp8 && !kStreamKeys ? 2 * kGroupWarps : 1);
       mbar_init(smem_u32(&br.res_empty[i]), 1);
     }
     for (int i = 0; i < kMostSlots; i++) {
-      mbar_init(smem_u32(&br.slot_full[i]), C::fp8 && kStreamKeys ? 2 * C::group_warps : 1);
+      mbar_init(smem_u32(&br.slot_full[i]), C::fp8 && kStreamKeys ? 2 * kGroupWarps : 1);
       mbar_init(smem_u32(&br.slot_empty[i]), 1);
       mbar_init(smem_u32(&br.raw_full[i]), 1);
     }
@@ -931,20 +945,27 @@ extern "C" int mla_attention_mass(const void *q, const void *kv_cache, int kv_fo
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
   } else if (ok) {
-    // bytes, 64 of each row of a page at a time
+    // codes, 128 of each row of a page at a time
     const cuuint64_t row = kv_format == MLA_KV_FP8_E4M3 ? FP8_ROW : D_QK;
     cuuint64_t dims[3] = {row, (cuuint64_t)PAGE, (cuuint64_t)num_pages}, strides[2] = {row, row * PAGE};
-    cuuint32_t box[3] = {64, (cuuint32_t)PAGE, 1}, estr[3] = {1, 1, 1};
-    ok = fn(&k_map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(kv_cache), dims, strides, box, estr,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-    if (ok && kv_format == MLA_KV_FP8_E4M3)  // the rotated part: 64 bf16 behind the codes
+    cuuint32_t box[3] = {128, (cuuint32_t)PAGE, 1}, estr[3] = {1, 1, 1};
+    auto codes = [&](CUtensorMap *map) {
+      return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(kv_cache), dims, strides, box, estr,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    };
+    ok = codes(&k_map);
+    // the rotated part: 64 codes, or 64 bf16 behind the codes
+    box[0] = 64;
+    if (ok && kv_format == MLA_KV_FP8_E4M3_TENSOR) ok = codes(&pe_map);
+    if (ok && kv_format == MLA_KV_FP8_E4M3)
       ok = make_map_3d(&pe_map, static_cast<const uint8_t *>(kv_cache) + D_V, 64, PAGE, (uint64_t)num_pages, FP8_ROW / 2,
                        PAGE * FP8_ROW / 2, PAGE, 1);
   }
   if (!ok) return fail(MLA_ERR_CUDA, "a tensor map could not be made");
-  const uint32_t resident = kBlocks * (p.n_qt == 1 ? p.box / 2 * 128 : kBlock);
-  p.slots = (int)((kRoom - resident) / kBlock);
+  const uint32_t q_block = p.box / 2 * 128, unit = kv_format == MLA_KV_BF16 ? 1 : 2;
+  const uint32_t resident = kBlocks * (p.n_qt == 1 ? q_block : kBlock);
+  p.slots = (int)((kRoom - resident) / (unit * (p.n_qt == 1 ? kBlock : q_block)));
   if (p.slots > kMostSlots) p.slots = kMostSlots;
   cudaError_t e = cudaSuccess;
   const bool keys = p.n_qt == 1, poll = p.wait_ns < kShortWaitNs;
