@@ -51,7 +51,7 @@ struct Of {
   static constexpr int halves = scaled ? 2 : 1;                // threads of a key
   static constexpr int cols = rows / halves;                   // columns of a thread
   static constexpr int sum_warps = 4 * halves;
-  static constexpr int wide_warps = !fp8 ? 0 : scaled ? 8 : 16;  // warps that widen cached rows,
+  static constexpr int wide_warps = fp8 ? 8 : 0;               // warps that widen cached rows
   static constexpr int threads = 32 * (4 + sum_warps + wide_warps);
   // Operands come in units: a block, or with FP8 two (a last one alone), so that a row of a
   // copy is 128 bytes (rows of 64 codes: 44.5 us instead of 38.8 for 32 sequences of up to 8192
@@ -62,7 +62,10 @@ struct Of {
   __device__ static constexpr bool begins(int u) { return parts > 1 || u == 0; }
   __device__ static constexpr bool ends(int u) { return parts > 1 || u == units - 1; }
 };
-constexpr int kGroupWarps = 4;  // warps that widen a unit together
+// Two groups of four warps widen units in turn.  A barrier is always waited for by the same
+// group (of an even number of slots, and of the units that stay): one that comes to it while
+// the phase before is still open would take the one before that for its own.
+constexpr int kGroups = 2, kGroupWarps = 4;
 // With scales: registers of the threads that load, sum and widen (96 each would spill where
 // scores are summed, 48.5 us instead of 44.6 for 32 sequences of up to 8192 tokens, two query
 // tokens, 64 heads).
@@ -434,12 +437,13 @@ __device__ void widen_role(const MassParams &p, Bars &br, const Work &w, const P
   using C = Of<kFormat>;
   const int group = thread / kGroupThreads, i = thread % kGroupThreads;
   const bool first = (threadIdx.x & 31) == 0;
-  int s = 0, turn = 0;
+  static_assert(C::wide_warps == kGroups * kGroupWarps, "");
+  int s = 0;
   uint32_t ph = 0, tile = 0;
   auto widen_tile = [&] {
     for (int u = 0; u < C::units; u++) {
-      if (turn == group) {
-        const int k = kStreamKeys ? s : u;
+      const int k = kStreamKeys ? s : u;
+      if (k % kGroups == group) {
         const uint32_t dst = kStreamKeys ? at.slots + s * at.slot : at.res + u * C::unit * kBlock;
         const bool ok = warp_wait<kPoll>(&br, &br.raw_full[k], kStreamKeys ? ph : tile & 1, p);
         if (u < C::units - 1) {
@@ -452,7 +456,6 @@ __device__ void widen_role(const MassParams &p, Bars &br, const Work &w, const P
         __syncwarp();
         if (first) mbar_arrive_pair(mapa(smem_u32(kStreamKeys ? &br.slot_full[k] : &br.res_full[k]), 0));
       }
-      if (++turn == C::wide_warps / kGroupWarps) turn = 0;
       if (++s == p.slots) {
         s = 0;
         ph ^= 1;
@@ -967,6 +970,7 @@ extern "C" int mla_attention_mass(const void *q, const void *kv_cache, int kv_fo
   const uint32_t resident = kBlocks * (p.n_qt == 1 ? q_block : kBlock);
   p.slots = (int)((kRoom - resident) / (unit * (p.n_qt == 1 ? kBlock : q_block)));
   if (p.slots > kMostSlots) p.slots = kMostSlots;
+  if (kv_format != MLA_KV_BF16) p.slots -= p.slots % kGroups;
   cudaError_t e = cudaSuccess;
   const bool keys = p.n_qt == 1, poll = p.wait_ns < kShortWaitNs;
   using Kernel = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, MassParams);

@@ -58,6 +58,10 @@ CASES = [
     ("fp8_tensor", 1, 8, [20000, 4097], False, 0.5),
     ("fp8_tensor", 64, 10, [2500], True, 1.0),
     ("fp8", 64, 10, [2500, 20], True, 1.0),
+    ("fp8", 1, 1, [30000], False, 0.0),                 # few query rows: more codes on their way
+    ("fp8_tensor", 1, 24, [30000, 64, 0, 200], False, 1.0),
+    ("fp8_tensor", 1, 128, [20000, 100], False, 1.0),
+    ("fp8_tensor", 2, 128, [9000], True, 1.0),
 ]
 
 
