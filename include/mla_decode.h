@@ -487,12 +487,12 @@ int mla_value_project(const void *attn, int64_t ld_token, int64_t ld_head, const
  *                  that overlap on the GPU need separate ones
  * Probabilities are rounded to bf16 before they multiply the values, and so are the
  * values of FP8 rows with a scale for each 128; their keys are not rounded to fewer
- * than 22 bits.  Codes with one scale are exact.  Parts of an output are joined in
+ * than 16 bits.  Codes with one scale are exact.  Parts of an output are joined in
  * fp32 and rounded once.  Scales are finite, and >= 0 for one scale.  What the cache holds behind the last token of a sequence or prefix
  * does not matter (inf and nan included); the tokens' own rows must be finite.  A
  * page outside the pool is skipped and sets MLA_STATUS_BAD_PAGE.  Of an FP8 cache,
  * prefix pages are widened in the workspace (73728 bytes an entry of
- * prefix_table, with a scale for each 128 values 204804), and own pages too where
+ * prefix_table, with a scale for each 128 values 139264), and own pages too where
  * B * max_pages <= 2048; where it is more, own FP8 rows are rounded to bf16 as
  * mla_decode's.  At most 8192 work
  * items: B * ceil(T * H / 128) + ceil(B * T * H / 128) + G (MLA_ERR_UNSUPPORTED above).

@@ -13,15 +13,14 @@
 // other through a small ring in L2.  All results are fp32 partials, normalised,
 // with a base-2 log-sum-exp: another kernel joins prefix and own parts.
 //
-// FP8 rows are multiplied as 16-bit values that the widening kernel has made.  With one
-// scale the codes themselves (exact in bf16; the scale multiplies scores and results).  With a scale
+// FP8 rows are multiplied as bf16 values that the widening kernel has made.  With one
+// scale the codes themselves (exact; the scale multiplies scores and results).  With a scale
 // for each 128 values a product of code and scale does not fit 8 bits, and a log-sum-exp over few
-// keys shows it: keys are sums of two fp16 values (22 bits), each page of keys and each
-// query row (fp16 too then) first brought into fp16's range by a power of two that goes
-// back into the scores.  So rank 0 makes twice the products of a latent, from a second stage
-// a tile.  (One fp16 value: 129 us instead of 173 for 48 sequences of four tokens and 64 heads on
-// three prefixes of up to 5000, and log-sum-exps off by 1.3e-5 of themselves.)  Values are bf16:
-// P is, and their rounding is of the size of P's.
+// keys shows it: keys are sums of two bf16 values (16 bits), so rank 0 makes twice the products
+// of a latent, from a second stage a tile.  (One: 117 us instead of 163 for 48 sequences of four
+// tokens and 64 heads on three prefixes of up to 5000, and log-sum-exps off by 1e-4 of
+// themselves instead of 1e-6.)  Values are the first of the two: P is bf16 too, and its
+// rounding of the same size.
 //
 // Rows behind an item's last key, in its last page, and pages outside the pool never
 // reach a result: their scores are replaced by -inf, and rank 1 clears their
@@ -30,7 +29,6 @@
 #include <cudaTypedefs.h>
 
 #include "dependent.cuh"
-#include "fp8.cuh"
 #include "pairs_f32.cuh"
 #include "ptx.cuh"
 #include "shared_prefix.cuh"
@@ -62,7 +60,6 @@ constexpr uint32_t OFF_RCV_P = kStages * kStage1;        // rank 1: two P tiles
 constexpr uint32_t OFF_BARS = OFF_RCV_P + 2 * kPBytes;
 constexpr uint32_t TM_Q = 0, TM_S = 320, TM_O = 0, TM_COLS = 512;
 constexpr uint32_t IDESC_QK = idesc_bf16_f32(128, 64, false, false);
-constexpr uint32_t IDESC_QK_F16 = IDESC_QK & ~(1u << 7 | 1u << 10);  // fp16 operands
 constexpr uint32_t IDESC_PV = idesc_bf16_f32(128, 256, false, true);
 
 struct Bars {
@@ -75,14 +72,12 @@ struct Bars {
   uint64_t p_land[2], p_empty[2], o_done[2], o_ready[2];
   uint64_t lsum[4][2];
   int valid[kValidRing];                             // rank 0: keys of a tile that count (seen through the tile's scores)
-  float factor[kValidRing];                          // with scales: what its keys were divided by
   uint32_t tmem_base;
   int abort;
 };
 constexpr uint32_t OFF_LPART = OFF_BARS + (sizeof(Bars) + 15) / 16 * 16;  // rank 0: float[2][2][128]
 constexpr uint32_t kSmem = OFF_LPART + 4 * M_TILE * 4;
-constexpr uint32_t OFF_QMAX = kStages * kStage0;  // rank 0, with scales: the largest |q| of each half of a row, bf16 bits
-static_assert(OFF_QMAX + 2 * M_TILE * 4 <= OFF_BARS && kSmem <= 232448, "shared memory budget");
+static_assert(kStages * kStage0 <= OFF_BARS && kSmem <= 232448, "shared memory budget");
 
 // A message from rank 0 to rank 1 behind its P tile.
 struct Meta {
@@ -190,17 +185,12 @@ __device__ void load_role(const Ctx &c, const CUtensorMap *map, const CUtensorMa
       }
     for (int base = t0; base < t1; base += 32) {
       const int pg = base + lane < t1 ? page_of(p, it, base + lane) : -1;
-      const float factor = kScaled && pg >= 0 ? __ldg(p.factors + pg) : 1.f;
       const int cnt = min(32, t1 - base);
       for (int i = 0; i < cnt; i++, g++) {
         const int page = __shfl_sync(0xffffffffu, pg, i);
-        const float fac = kScaled ? __shfl_sync(0xffffffffu, factor, i) : 1.f;
         bool ok = true;
         if (lane == 0) {
-          if (c.rank == 0) {
-            br.valid[g % kValidRing] = page < 0 ? 0 : min(PAGE, it.len - (base + i) * PAGE);
-            if (kScaled) br.factor[g % kValidRing] = fac;
-          }
+          if (c.rank == 0) br.valid[g % kValidRing] = page < 0 ? 0 : min(PAGE, it.len - (base + i) * PAGE);
           ok = wait_ok(c, &br.kv_empty[s], ph);
           if (ok) {
             const uint32_t bar = smem_u32(&br.kv_full[s]);
@@ -274,7 +264,6 @@ __device__ void qk_waiter(const Ctx &c, int lane) {
 template <bool kScaled>
 __device__ void mma_qk(const Ctx &c, uint32_t tmem) {
   Bars &br = *c.bars;
-  constexpr uint32_t idesc = kScaled ? IDESC_QK_F16 : IDESC_QK;
   const uint32_t kv0 = smem_u32(c.base);
   uint32_t g = 0, sq = 0;
   for_each_piece(*c.p, c.part, [&](const SharedItem &it, int t0, int t1, int) {
@@ -298,7 +287,7 @@ __device__ void mma_qk(const Ctx &c, uint32_t tmem) {
         if (elect_one()) {
 #pragma unroll
           for (int i = 0; i < 4 * kSplit; i++)
-            mma_ts(d, tmem + TM_Q + i * 8, kd + (uint64_t)((i >> 2) * 512 + (i & 3) * 2), idesc, k || i ? 1u : 0u);
+            mma_ts(d, tmem + TM_Q + i * 8, kd + (uint64_t)((i >> 2) * 512 + (i & 3) * 2), IDESC_QK, k || i ? 1u : 0u);
           mma_commit(smem_u32(&br.kv_empty[s]));
         }
         __syncwarp();
@@ -307,7 +296,7 @@ __device__ void mma_qk(const Ctx &c, uint32_t tmem) {
         if (elect_one()) {
 #pragma unroll
           for (int i = 4 * kSplit; i < (k ? 32 : 36); i++)
-            mma_ts(d, tmem + TM_Q + i * 8, kd + (uint64_t)((i >> 2) * 512 + (i & 3) * 2), idesc, 1u);
+            mma_ts(d, tmem + TM_Q + i * 8, kd + (uint64_t)((i >> 2) * 512 + (i & 3) * 2), IDESC_QK, 1u);
           mma_commit(smem_u32(&br.kv_empty_b[s]));
           if (k + 1 == kTileStages<kScaled>) mma_commit(smem_u32(&br.s_full[b]));
         }
@@ -378,47 +367,28 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   return *reinterpret_cast<const uint32_t *>(&v);
 }
 
-__device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
-  uint4 v;
-  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
-  return v;
-}
-
 // Query row `row` of a stage of 64, blocks [kb0, kb1), into tensor memory; zeros
-// for a row that the item has not.  With scales as fp16, times `factor`, a power of two.  (Not
-// inlined: it runs once a piece, and its registers would crowd the softmax loop.)
-template <bool kScaled>
-__device__ __noinline__ void load_q(uint32_t lane_tmem, uint32_t stage, int row, bool ok, int kb0, int kb1, float factor) {
+// for a row that the item has not.  (Not inlined: it runs once a piece, and its
+// registers would crowd the softmax loop.)
+__device__ __noinline__ void load_q(uint32_t lane_tmem, uint32_t stage, int row, bool ok, int kb0, int kb1) {
   for (int kb = kb0; kb < kb1; kb++) {
     uint32_t v[32];
 #pragma unroll
     for (int j = 0; j < 8; j++) {
       uint4 x = make_uint4(0, 0, 0, 0);
-      if (ok) x = ld_shared_v4(stage + kb * kBlk + row * 128 + ((j ^ (row & 7)) << 4));
+      if (ok)
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
+                     : "r"(stage + kb * kBlk + row * 128 + ((j ^ (row & 7)) << 4)));
       v[4 * j] = x.x;
       v[4 * j + 1] = x.y;
       v[4 * j + 2] = x.z;
       v[4 * j + 3] = x.w;
     }
-    if (kScaled)
-#pragma unroll
-      for (int j = 0; j < 32; j++) v[j] = f16_of_bf16(v[j], factor);
     __syncwarp();
     tmem_st32(lane_tmem + TM_Q + kb * 32, v);
   }
   tmem_wait_st();
-}
-
-// The largest finite |q| of those (bf16 bits; only its exponent is used).
-__device__ __noinline__ uint32_t largest_q(uint32_t stage, int row, int kb0, int kb1) {
-  uint32_t m = 0;
-  for (int kb = kb0; kb < kb1; kb++)
-#pragma unroll
-    for (int j = 0; j < 8; j++) {
-      const uint4 x = ld_shared_v4(stage + kb * kBlk + row * 128 + ((j ^ (row & 7)) << 4));
-      m = max(m, max(max(largest_bf16(x.x), largest_bf16(x.y)), max(largest_bf16(x.z), largest_bf16(x.w))));
-    }
-  return m;
 }
 
 // The largest of three (one instruction).
@@ -447,8 +417,6 @@ __device__ __forceinline__ void cut32(float (&v)[32], int lim) {
   }
 }
 
-constexpr uint32_t kRowBar = 2;  // and three more
-
 // Warps 4-11: thread (q, hf) has row 32 q + lane and keys [32 hf, 32 hf + 32) of
 // each tile.  Both threads of a row read all 64 scores, so they agree on the
 // running maximum without talking; the reference moves only when it grows by kRescale.
@@ -459,26 +427,15 @@ __device__ void softmax_role(const Ctx &c, uint32_t tmem, int w, int lane) {
   const int q = w & 3, hf = (w - 4) >> 2, r = q * 32 + lane;
   const uint32_t lt = tmem + ((uint32_t)(q * 32) << 16), kv0 = smem_u32(c.base);
   float *lpart = reinterpret_cast<float *>(c.base + OFF_LPART);
-  uint32_t *q_max = reinterpret_cast<uint32_t *>(c.base + OFF_QMAX);
   // (not 0, so that -inf stays -inf: a scale of 0 is one of codes of 0)
-  const float scale = p.format == MLA_KV_FP8_E4M3_TENSOR ? fmaxf(p.scale_log2 * __ldg(p.kv_scales), 1e-37f) : p.scale_log2;
+  const float cs = p.format == MLA_KV_FP8_E4M3_TENSOR ? fmaxf(p.scale_log2 * __ldg(p.kv_scales), 1e-37f) : p.scale_log2;
   uint32_t g = 0, pc = 0, sq = 0;
   for_each_piece(p, c.part, [&](const SharedItem &it, int t0, int t1, int slot_out) {
     const bool live = r < it.rows;
-    float cs = scale;
     {
-      const uint32_t qs = sq + (r >> 6), stage = kv0 + (qs % kStages) * kStage0;
-      const bool ok = warp_wait(c, &br.kv_full[qs % kStages], (qs / kStages) & 1, live);
-      float factor = 1.f;
-      if (kScaled) {  // the row's two threads agree on its factor
-        if (ok) q_max[hf * M_TILE + r] = live ? largest_q(stage, r & 63, hf ? 5 : 0, hf ? 9 : 5) : 0u;
-        if (bar_red_or(kRowBar + q, 64, !ok)) return false;
-        const uint32_t most = max(q_max[r], q_max[M_TILE + r]) << 16;
-        factor = to_f16_range(most);
-        cs *= from_f16_range(most);
-      }
-      if (!ok) return false;
-      load_q<kScaled>(lt, stage, r & 63, live, hf ? 5 : 0, hf ? 9 : 5, factor);
+      const uint32_t qs = sq + (r >> 6);
+      if (!warp_wait(c, &br.kv_full[qs % kStages], (qs / kStages) & 1, live)) return false;
+      load_q(lt, kv0 + (qs % kStages) * kStage0, r & 63, live, hf ? 5 : 0, hf ? 9 : 5);
       sq += q_stages(it) + (t1 - t0) * kTileStages<kScaled>;
       tc_fence_before();
       __syncwarp();
@@ -501,9 +458,7 @@ __device__ void softmax_role(const Ctx &c, uint32_t tmem, int w, int lane) {
       if (lane == 0) mbar_arrive(smem_u32(&br.s_free[b]));
       cut32(own, lim - 32 * hf);
       cut32(oth, lim - 32 * (hf ^ 1));
-      // a tile's scores are in units of its keys' factor, a row's reference is not
-      const float unit = kScaled ? br.factor[g % kValidRing] : 1.f, ct = kScaled ? cs * unit : cs;
-      const float mt = fmaxf(max32(own), max32(oth)) * unit;
+      const float mt = fmaxf(max32(own), max32(oth));
       float alpha = 1.f;
       bool resc = false;
       if ((mt - m_ref) * cs > kRescale) {
@@ -528,7 +483,7 @@ __device__ void softmax_role(const Ctx &c, uint32_t tmem, int w, int lane) {
         uint32_t wv[4];
 #pragma unroll
         for (int e = 0; e < 4; e++) {
-          const float2 x = fma2(make_float2(own[cc * 8 + 2 * e], own[cc * 8 + 2 * e + 1]), make_float2(ct, ct), make_float2(nb, nb));
+          const float2 x = fma2(make_float2(own[cc * 8 + 2 * e], own[cc * 8 + 2 * e + 1]), make_float2(cs, cs), make_float2(nb, nb));
           const float2 pr = make_float2(ex2(x.x), ex2(x.y));
           psum = add2(psum, pr);
           wv[e] = pack_bf16(pr.x, pr.y);
@@ -766,20 +721,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 cudaError_t launch_shared_attention(const SharedParams &p, cudaStream_t stream) {
   const auto fn = tensor_map_encoder();
   if (!fn) return cudaErrorNotSupported;
-  // keys as pages of 9 blocks, 8 of which are the values too; with scales 17 blocks, and
-  // values as pages of their own
+  // pages of 9 blocks, with scales 17; the first 8 are the values too
   const bool wide = p.format != MLA_KV_BF16, scaled = p.format == MLA_KV_FP8_E4M3;
   const uint8_t *pool = wide ? p.scratch : p.cache;
   const cuuint64_t pages = wide ? (cuuint64_t)p.scratch_pages : (cuuint64_t)p.num_pages;
+  const cuuint64_t row = (scaled ? D_QK + D_V : D_QK) * 2;
+  cuuint64_t dims[4] = {64, (cuuint64_t)PAGE, scaled ? 17u : 9u, pages}, strides[3] = {row, 128, row * PAGE};
   cuuint32_t estr[4] = {1, 1, 1, 1};
   CUtensorMap maps[4];
   const cuuint32_t blocks[3] = {kSplit, 9 - kSplit, 8};
   for (int m = 0; m < 3; m++) {
-    const bool apart = scaled && m == 2;
-    const cuuint64_t row = (apart ? D_V : scaled ? D_QK + D_V : D_QK) * 2;
-    cuuint64_t dims[4] = {64, (cuuint64_t)PAGE, apart ? 8u : scaled ? 17u : 9u, pages}, strides[3] = {row, 128, row * PAGE};
     cuuint32_t box[4] = {64, (cuuint32_t)PAGE, blocks[m], 1};
-    if (fn(&maps[m], CU_TENSOR_MAP_DATA_TYPE_UINT16, 4, const_cast<uint8_t *>(apart ? p.values : pool), dims, strides, box, estr,
+    if (fn(&maps[m], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<uint8_t *>(pool), dims, strides, box, estr,
            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
       return cudaErrorInvalidValue;

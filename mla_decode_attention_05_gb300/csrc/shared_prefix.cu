@@ -225,100 +225,63 @@ __global__ void __launch_bounds__(kSchedThreads) shared_schedule_kernel(SharedPa
            [&](int i, int at, int) { p.items[i].slot = at; });
 }
 
-// FP8: page j of table row y as 16-bit rows (zeros behind the last token), once for all the
-// tiles that read it: prefixes first, then own pages where there is room for them.  Block z has
-// one of kWidenParts parts of a page's rows (48 sequences and three prefixes, 477 pages on 152 SMs: 174 us
-// of the whole with whole pages, 170 with halves).  A warp a row: lane l widens 16 of its values, and lanes 0-3 or 0-7 the rotated part.  With one scale
-// the codes as they are; with a scale for each 128 values, keys as two fp16 values, the
-// second ones behind the row's first, and bf16 values.
-__host__ __device__ constexpr size_t key_page_bytes(int format) {
+// Bytes of a page as bf16 rows.
+__host__ __device__ constexpr size_t wide_page_bytes(int format) {
   return (size_t)PAGE * 2 * (format == MLA_KV_FP8_E4M3 ? D_QK + D_V : D_QK);
 }
 
 constexpr int kWidenParts = 2;
 
+// FP8: page j of table row y as bf16 rows (zeros behind the last token), once for all the
+// tiles that read it: prefixes first, then own pages where there is room for them.  Block z has
+// one of kWidenParts parts of a page's rows (FP8 groups of 48 sequences, 477 pages on 152 SMs:
+// 170.4 us with halves, 174.5 with whole pages, 172.1 with quarters).  A warp a row: lane l widens 16 of its
+// values, and lanes 0-3 or 0-7 the rotated part.  With one scale the codes as they are; with a
+// scale for each 128 values as sums of two values, the second ones behind the row's first.
 template <bool kScaled>
 __global__ void __launch_bounds__(256) shared_widen_kernel(SharedParams p) {
-  __shared__ uint32_t most[2][8];
   grid_dep_trigger();
   grid_dep_wait();
   const bool own = (int)blockIdx.y >= p.G;
   const int row = own ? blockIdx.y - p.G : blockIdx.y, width = own ? p.max_pages : p.max_prefix;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int n = (int)min((long long)max((own ? p.seqlens : p.prefix_lens)[row], 0), (long long)width * PAGE);
   const int32_t *table = (own ? p.block_table : p.prefix_table) + (size_t)row * width;
   const size_t first = (own ? (size_t)p.G * p.max_prefix : 0) + (size_t)row * width;
   constexpr int kRowBytes = kScaled ? FP8_ROW : D_QK, kRows = PAGE / 8 / kWidenParts;
-  const int row0 = blockIdx.z * (PAGE / kWidenParts);
+  constexpr int kPieces = (kScaled ? D_QK + D_V : D_QK) / 8;  // 16-byte pieces of a widened row
   const uint4 zero = make_uint4(0, 0, 0, 0);
-  int turn = 0;
-  for (int j = blockIdx.x; (long long)j * PAGE < n; j += gridDim.x, turn ^= 1) {
+  for (int j = blockIdx.x; (long long)j * PAGE < n; j += gridDim.x) {
     const int page = table[j];
     if (page < 0 || page >= p.num_pages) continue;
     const int tokens = min(PAGE, n - j * PAGE);
-    auto from = [&](int r) { return reinterpret_cast<const uint4 *>(p.cache + ((size_t)page * PAGE + r) * kRowBytes); };
-    uint4 *keys = reinterpret_cast<uint4 *>(p.scratch + (first + j) * key_page_bytes(p.format));
-    constexpr int kKey = (kScaled ? D_QK + D_V : D_QK) / 8, kValue = D_V / 8;  // 16-byte pieces of a row
-    uint4 c[kRows];
+    uint4 *to = reinterpret_cast<uint4 *>(p.scratch + (first + j) * wide_page_bytes(p.format));
 #pragma unroll
     for (int i = 0; i < kRows; i++) {
-      const int r = row0 + warp + 8 * i;
-      c[i] = r < tokens ? __ldg(from(r) + lane) : zero;
-    }
-    if constexpr (!kScaled) {
+      const int r = blockIdx.z * (PAGE / kWidenParts) + warp + 8 * i;
+      const size_t at = (size_t)page * PAGE + r;
+      const uint4 *src = reinterpret_cast<const uint4 *>(p.cache + at * kRowBytes);
+      uint4 *dst = to + r * kPieces;
+      const bool live = r < tokens;
+      const uint4 codes = live ? __ldg(src + lane) : zero;
+      if constexpr (kScaled) {
+        uint4 v[2] = {zero, zero}, rest[2] = {zero, zero};
+        if (live) widen16_twice(codes, __ldg(p.kv_scales + at * 4 + lane / 8), v, rest);
 #pragma unroll
-      for (int i = 0; i < kRows; i++) {
-        const int r = row0 + warp + 8 * i;
-        uint4 *dst = keys + r * kKey, lo, hi;
-        codes16(c[i], lo, hi);
+        for (int e = 0; e < 2; e++) {
+          dst[2 * lane + e] = v[e];
+          dst[D_QK / 8 + 2 * lane + e] = rest[e];
+        }
+        if (lane < 8) dst[64 + lane] = live ? __ldg(src + 32 + lane) : zero;
+      } else {
+        uint4 lo, hi;
+        codes16(codes, lo, hi);
         dst[2 * lane] = lo;
         dst[2 * lane + 1] = hi;
         if (lane < 4) {
-          codes16(r < tokens ? __ldg(from(r) + 32 + lane) : zero, lo, hi);
+          codes16(live ? __ldg(src + 32 + lane) : zero, lo, hi);
           dst[64 + 2 * lane] = lo;
           dst[65 + 2 * lane] = hi;
-        }
-      }
-    } else {
-      // no value of the page is larger than the largest code times its largest scale, or its largest rotated value
-      const float4 *scales = reinterpret_cast<const float4 *>(p.kv_scales) + (size_t)page * PAGE;
-      uint4 pe[2];
-      uint32_t big = 0;
-#pragma unroll
-      for (int i = 0; i < 2; i++) {
-        const int r = warp * 8 + i * 4 + lane / 8;
-        pe[i] = r < tokens ? __ldg(from(r) + 32 + lane % 8) : zero;
-        big = max(big, max(max(largest_bf16(pe[i].x), largest_bf16(pe[i].y)), max(largest_bf16(pe[i].z), largest_bf16(pe[i].w))) << 16);
-      }
-      if (tid / 4 < tokens) {
-        const uint32_t v = __float_as_uint(448.f * fabsf(__ldg(p.kv_scales + ((size_t)page * PAGE) * 4 + tid)));
-        big = max(big, v < 0x7f800000u ? v : 0u);
-      }
-      big = __reduce_max_sync(0xffffffffu, big);
-      if (lane == 0) most[turn][warp] = big;
-      __syncthreads();
-#pragma unroll
-      for (int i = 0; i < 8; i++) big = max(big, most[turn][i]);
-      const float factor = to_f16_range(big);
-      if (tid == 0 && row0 == 0) p.factors[first + j] = from_f16_range(big);
-      uint4 *values = reinterpret_cast<uint4 *>(p.values + (first + j) * (PAGE * D_V * 2));
-#pragma unroll
-      for (int i = 0; i < 2; i++) {
-        const int r = warp * 8 + i * 4 + lane / 8;
-        if (r / (PAGE / kWidenParts) != blockIdx.z) continue;
-        keys[r * kKey + 64 + lane % 8] = make_uint4(f16_of_bf16(pe[i].x, factor), f16_of_bf16(pe[i].y, factor),
-                                                    f16_of_bf16(pe[i].z, factor), f16_of_bf16(pe[i].w, factor));
-      }
-#pragma unroll
-      for (int i = 0; i < kRows; i++) {
-        const int r = row0 + warp + 8 * i;
-        uint4 k[2] = {zero, zero}, rest[2] = {zero, zero}, v[2] = {zero, zero};
-        if (r < tokens) widen16_twice(c[i], __ldg(reinterpret_cast<const float *>(scales + r) + lane / 8), factor, k, rest, v);
-#pragma unroll
-        for (int e = 0; e < 2; e++) {
-          keys[r * kKey + 2 * lane + e] = k[e];
-          keys[r * kKey + D_QK / 8 + 2 * lane + e] = rest[e];
-          values[r * kValue + 2 * lane + e] = v[e];
         }
       }
     }
@@ -434,14 +397,14 @@ __global__ void __launch_bounds__(kJoinWarps * 32) shared_join_kernel(SharedPara
 // ---- host ------------------------------------------------------------------------
 
 struct Layout {
-  size_t items, md, pieces, n_prefix, groups, lens_o, seq, md_o, ns_o, cnt_o, scratch, values, factors, lse_p, o_p, lse_o, o_o, ring, total;
+  size_t items, md, pieces, n_prefix, groups, lens_o, seq, md_o, ns_o, cnt_o, scratch, lse_p, o_p, lse_o, o_o, ring, total;
   size_t pages;
   int room, n_mt;
   bool apart;  // own FP8 tokens go through the decode kernel
 };
 
 // Own FP8 pages are widened along with the prefixes' where the page table has at
-// most this many entries (151 MB of workspace, 420 MB with scales).  Otherwise they go through
+// most this many entries (151 MB of workspace, 285 MB with scales).  Otherwise they go through
 // the decode kernel's gather, which needs no such room but rounds rows to bf16; with one scale, 48
 // sequences of up to 300 tokens, four query tokens, 64 heads take 155 us that way, 120 us this way.
 constexpr long long kMostOwnPages = 2048;
@@ -472,10 +435,7 @@ Layout layout(int B, int T, int H, int G, int format, int max_prefix, int max_pa
   l.md_o = take(apart ? (size_t)parts * MD_STRIDE * 4 : 0);
   l.ns_o = take(apart ? (own + 1) * 4 : 0);
   l.cnt_o = take(apart ? own * 4 : 0);
-  const size_t scaled = format == MLA_KV_FP8_E4M3 ? l.pages : 0;
-  l.scratch = take(l.pages * key_page_bytes(format));
-  l.values = take(scaled * PAGE * D_V * 2);
-  l.factors = take(scaled * sizeof(float));
+  l.scratch = take(l.pages * wide_page_bytes(format));
   l.lse_p = take(slots * row);
   l.o_p = take(slots * row * D_V);
   l.lse_o = take(slots_o * row);
@@ -604,8 +564,6 @@ extern "C" int mla_decode_shared(const void *q, const void *kv_cache, int kv_for
   p.ns_o = l.apart ? reinterpret_cast<int32_t *>(at(l.ns_o)) : nullptr;
   p.cnt_o = l.apart ? reinterpret_cast<int32_t *>(at(l.cnt_o)) : nullptr;
   p.scratch = at(l.scratch);
-  p.values = at(l.values);
-  p.factors = reinterpret_cast<float *>(at(l.factors));
   p.lse_p = reinterpret_cast<float *>(at(l.lse_p));
   p.o_p = reinterpret_cast<float *>(at(l.o_p));
   p.lse_o = reinterpret_cast<float *>(at(l.lse_o));

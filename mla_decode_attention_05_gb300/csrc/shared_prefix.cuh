@@ -42,9 +42,7 @@ struct SharedParams {
   int2 *seq;           // [B] {first prefix item of its group or -1, its first row among the group's}
   int32_t *lens_o;     // [B] own tokens, clamped, where they
   int32_t *md_o, *ns_o, *cnt_o;  // go through the decode kernel: its schedule (else null)
-  uint8_t *scratch;    // FP8: pages of 16-bit keys, G * max_prefix and B * max_pages: [64][576], with scales [64][1088]
-  uint8_t *values;     // with scales: pages of bf16 values, [64][512] each (else the keys are the values too)
-  float *factors;      // with scales: what a page's keys were divided by
+  uint8_t *scratch;    // FP8: pages as bf16, G * max_prefix and B * max_pages: [64][576], with scales [64][1088]
   size_t scratch_pages;
   float *lse_p, *o_p;  // partial results: base-2 log-sum-exp [slots][128] and output [slots][64][128][8]
   float *lse_o, *o_o;  // those of the decode kernel

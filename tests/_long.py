@@ -96,14 +96,14 @@ def check_rows(got, lse, ref, n_keys, fmt="bf16"):
 
     FP8 with one scale: codes are exact, two more roundings of scores and output in
     fp32.  With a scale for each 128 values: each product of code and scale is the
-    sum of two fp16 values as a key (half a step of half a step: 2^-22; 2^-39 of the
-    page's largest is the smallest part) and rounded to bf16 as a value (half a step)."""
+    sum of two bf16 values as a key (half a step of half a step, 512 products more),
+    and rounded to bf16 as a value (half a step)."""
     d = 576 * STEP_F32 * ref["mag"] + 4 * STEP_F32 * ref["top"] + 2.0 ** -20
     v = 0.0
     if fmt == "fp8_tensor":
         d, v = d + 2 * STEP_F32 * ref["top"], 2 * STEP_F32
     elif fmt == "fp8":
-        d, v = d + 512 * STEP_F32 * ref["mag"] + (2.0 ** -22 + 2.0 ** -28) * ref["mag"], HALF_BF16 + STEP_F32
+        d, v = d + (512 * STEP_F32 + HALF_BF16 ** 2) * ref["mag"], HALF_BF16 + STEP_F32
     n = max(1, n_keys) * STEP_F32
     got, lse = f64(got), f64(lse)
     empty = np.isneginf(ref["lse"])

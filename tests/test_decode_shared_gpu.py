@@ -82,7 +82,7 @@ def _log2_sizes(rng, n, spread):
 @pytest.mark.parametrize("fmt", ["fp8", "fp8_tensor"])
 @pytest.mark.parametrize("size", [2.0 ** -90, 2.0 ** 60])
 def test_fp8_rows_and_queries_of_any_size(fmt, size):
-    """Keys far outside fp16's range, and queries that undo it; rows of other sizes
+    """Very small and very large keys, and queries that undo it; rows of other sizes
     side by side; a page whose latent or whose rotated part is all zeros."""
     T, H, prefixes, own = 1, 40, [150], [70, 64, 3]
     c, pre, mine, q = _make(336, fmt, T, H, prefixes, None, own)
