@@ -29,9 +29,9 @@
  *
  * CUDA graphs: mla_decode_metadata, mla_decode, mla_kv_insert,
  * mla_kv_insert_rope, mla_query_absorb, mla_kv_expand, mla_prefill,
- * mla_value_project, mla_decode_shared, mla_attention_mass and mla_evict can be captured into a CUDA graph on `stream` once the
- * calling thread has made the same kind of call outside capture (the first
- * call does one-time host set-up).  A replay uses the buffers seen at
+ * mla_value_project, mla_decode_shared, mla_attention_mass and mla_evict can be
+ * captured into a CUDA graph on `stream` once the calling thread has made the same
+ * kind of call outside capture (the first call does one-time host set-up).  A replay uses the buffers seen at
  * capture and reads their contents at replay time; the split-KV schedule is
  * a device kernel, so it follows the sequence lengths of each replay.
  *
@@ -488,16 +488,16 @@ int mla_value_project(const void *attn, int64_t ld_token, int64_t ld_head, const
  * Probabilities are rounded to bf16 before they multiply the values, and so are the
  * values of FP8 rows with a scale for each 128; their keys are not rounded to fewer
  * than 16 bits.  Codes with one scale are exact.  Parts of an output are joined in
- * fp32 and rounded once.  Scales are finite, and >= 0 for one scale.  What the cache holds behind the last token of a sequence or prefix
- * does not matter (inf and nan included); the tokens' own rows must be finite.  A
- * page outside the pool is skipped and sets MLA_STATUS_BAD_PAGE.  Of an FP8 cache,
- * prefix pages are widened in the workspace (73728 bytes an entry of
- * prefix_table, with a scale for each 128 values 139264), and own pages too where
- * B * max_pages <= 2048; where it is more, own FP8 rows are rounded to bf16 as
- * mla_decode's.  At most 8192 work
- * items: B * ceil(T * H / 128) + ceil(B * T * H / 128) + G (MLA_ERR_UNSUPPORTED above).
- * A wait that gives up sets MLA_STATUS_WAIT_TIMEOUT.  Asynchronous on `stream`; can
- * be captured in a CUDA graph.  Returns MLA_OK or a negative code.
+ * fp32 and rounded once.  What the cache holds behind the last token of a sequence
+ * or prefix does not matter (inf and nan included); the tokens' own rows must be
+ * finite, a single scale >= 0.  A page outside the pool is skipped and sets
+ * MLA_STATUS_BAD_PAGE.  Of an FP8 cache, prefix pages are widened in the workspace
+ * (73728 bytes an entry of prefix_table, with a scale for each 128 values 139264),
+ * and own pages too where B * max_pages <= 2048; where it is more, own FP8 rows are
+ * rounded to bf16, as mla_decode does.  At most 8192 work items: B * ceil(T * H / 128) +
+ * ceil(B * T * H / 128) + G (MLA_ERR_UNSUPPORTED above).  A wait that gives up sets
+ * MLA_STATUS_WAIT_TIMEOUT.  Asynchronous on `stream`; can be captured in a CUDA
+ * graph.  Returns MLA_OK or a negative code.
  */
 size_t mla_decode_shared_workspace_bytes(int B, int T, int H, int G, int kv_format, int max_prefix_pages,
                                          int max_pages);
@@ -622,8 +622,8 @@ int mla_set_dual_gemm(int enable);
 /*
  * Test hook for the failure path: the time limit, in nanoseconds, of every
  * bounded wait inside the kernels of later mla_decode, mla_decode_noalloc,
- * mla_kv_expand, mla_prefill (at most 4 s there) and mla_value_project calls
- * made on the calling thread (0 restores the default of 2 s; mla_query_absorb's
+ * mla_kv_expand, mla_prefill (at most 4 s there), mla_value_project,
+ * mla_decode_shared and mla_attention_mass calls made on the calling thread (0 restores the default of 2 s; mla_query_absorb's
  * waits have limits of their own).  A wait that runs out sets MLA_STATUS_WAIT_TIMEOUT; every
  * role of the kernel then gives up at its next wait, the kernel waits for
  * its own copies and MMAs in flight, frees its tensor memory and returns, and

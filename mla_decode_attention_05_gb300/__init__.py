@@ -18,6 +18,11 @@ every call raises.
 A decode step from the projections' output: query_absorb, kv_insert_rope
 (rotates the queries in place and appends the rotated keys), metadata, decode,
 value_project.  A prompt or a chunk of one: kv_insert_rope, kv_expand, prefill.
+
+Long contexts: decode_shared in metadata's and decode's place where sequences
+share prefixes; attention_mass behind either (or behind a prompt) sums the weight
+that each cached token has had, and evict cuts the caches down to the tokens with
+the most of it, the first and the latest.
 """
 from __future__ import annotations
 
@@ -955,8 +960,8 @@ def set_dual_gemm(enable: bool):
 
 def set_wait_limit_ns(ns: int = 0):
     """Test hook: the limit of the bounded waits inside the kernels of later
-    decode, kv_expand, prefill and value_project calls on this thread (0 = the
-    default, 2 s); see mla_set_wait_limit_ns in include/mla_decode.h."""
+    decode, kv_expand, prefill, value_project, decode_shared and attention_mass
+    calls on this thread (0 = the default, 2 s); see mla_set_wait_limit_ns in include/mla_decode.h."""
     _check(lib().mla_set_wait_limit_ns(int(ns)))
 
 
