@@ -13,6 +13,10 @@
 // other through a small ring in L2.  All results are fp32 partials, normalised,
 // with a base-2 log-sum-exp: another kernel joins prefix and own parts.
 //
+// 64 sequences of 128 heads on 16384 shared tokens: 228 us in all for 301 GFLOP (154 us at the
+// measured bf16 rate); a tile takes about 1750 cycles, in which rank 0's softmax (1500), rank 1's message loop
+// (1500) and the QK MMAs (1364) each are nearly back to back.
+//
 // FP8 rows are multiplied as bf16 values that the widening kernel has made.  With one
 // scale the codes themselves (exact; the scale multiplies scores and results).  With a scale
 // for each 128 values a product of code and scale does not fit 8 bits, and a log-sum-exp over few

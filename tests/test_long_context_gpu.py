@@ -249,3 +249,91 @@ def test_two_graphs_with_a_workspace_each():
                 g.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(o, want[0]) and torch.equal(l, want[1]) for o, l in outs)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8"])
+def test_many_small_groups_and_sequences(fmt):
+    """More groups than the schedule keeps at hand, more sequences than it has
+    threads, groups without sequences and prefixes of no tokens among them."""
+    import mla_decode_attention_05_gb300 as mla
+    rng = np.random.default_rng(620)
+    G, B = 700, 1300
+    prefixes = [int(x) for x in rng.integers(0, 3, G)]
+    own = [int(x) for x in rng.integers(0, 3, B)]
+    cuts = np.sort(rng.integers(0, B + 1, G + 1))
+    prefixes[5], own[7], own[B - 1] = 130, 70, 66
+    c = Cache(rng, sum(-(-n // 64) for n in prefixes + own), fmt)
+    pre, mine = [c.take(n) for n in prefixes], [c.take(n) for n in own]
+    q = bf16(rng, (B, 1, 2, 576), 1.3)
+    data, scales = c.cuda()
+    mla.device_status()
+    out, lse = mla.decode_shared(q.cuda(), data, table(pre), i32(prefixes), table(mine), i32(own), softmax_scale=SCALE,
+                                 group_offsets=i32([int(x) for x in cuts]), kv_scales=scales)
+    assert mla.device_status() == 0
+    group = {}
+    for g in range(G):
+        for b in range(cuts[g], cuts[g + 1]):
+            group[b] = g
+    out, lse = out.cpu(), lse.cpu()
+    for b in list(range(0, B, 13)) + [7, B - 1, cuts[5], min(B - 1, cuts[6])]:
+        prefix = c.exact_rows(pre[group[b]], prefixes[group[b]]) if b in group else np.zeros((0, 576))
+        rounded = B * table(mine).shape[1] > 2048 and fmt != "bf16"
+        ref = O.attention(q[b].double().numpy(), prefix, (c.rows if rounded else c.exact_rows)(mine[b], own[b]), SCALE, False)
+        check_rows(out[b], lse[b].t(), ref, len(prefix) + own[b], fmt)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8", "fp8_tensor"])
+def test_weights_and_eviction_of_many_sequences(fmt):
+    import mla_decode_attention_05_gb300 as mla
+    rng = np.random.default_rng(621)
+    B, cap = 3001, 64
+    own = [int(x) for x in rng.integers(0, 4, B)]
+    own[0] = own[B - 1] = 64
+    c = Cache(rng, sum(-(-n // 64) for n in own), fmt)
+    mine = [c.take(n) for n in own]
+    q = bf16(rng, (B, 1, 2, 576), 1.0)
+    data, scales = c.cuda()
+    bt, sk = table(mine), i32(own)
+    lse = torch.full((B, 2, 1), 3.0, device="cuda")
+    mass = mla.attention_mass(q.cuda(), data, bt, sk, lse, torch.zeros(B, cap, device="cuda"), softmax_scale=SCALE, kv_scales=scales)
+    got = mass.cpu()
+    for b in list(range(0, B, 29)) + [B - 1]:
+        want, bound = O.mass(q[b].double().numpy(), c.exact_rows(mine[b], own[b]), lse[b].t().double().cpu().numpy(), SCALE, False)
+        # a step for each of the two additions beside the weights' own bounds
+        assert np.all(np.abs(got[b, :own[b]].double().numpy() - want) <= bound + 4 * 2.0 ** -24 * (want + bound))
+        assert (got[b, own[b]:] == 0).all()
+    pos = torch.arange(cap, dtype=torch.int32, device="cuda").repeat(B, 1)
+    before, plain = data.clone(), mass.clone()
+    n = mla.evict(data, bt, sk, mass, pos, keep=2, recent=1, kv_scales=scales)
+    assert n.tolist() == [min(x, 2) for x in own] and mla.device_status() == 0
+    for b in list(range(0, B, 31)) + [B - 1]:
+        holes, movers = O.evict(plain[b].cpu().numpy(), np.arange(cap), own[b], 2, 0, 1)
+        for h, m in zip(holes, movers):
+            assert torch.equal(data[mine[b][0], h], before[mine[b][0], m]) and int(pos[b, h]) == m
+            assert mass[b, h] == plain[b, m]
+
+
+def test_two_calls_at_once():
+    """On two streams, with workspaces of their own."""
+    import mla_decode_attention_05_gb300 as mla
+    own, prefixes = [300, 700, 90, 5], [3000]
+    c, pre, mine, q = _batch(622, "fp8", 2, 64, prefixes, own)
+    data, scales = c.cuda()
+    q, pt, pl, bt, sk = q.cuda(), table(pre), i32(prefixes), table(mine), i32(own)
+    shared = lambda: mla.decode_shared(q, data, pt, pl, bt, sk, softmax_scale=SCALE, causal=True, kv_scales=scales)
+    want = shared()
+    weigh = lambda: mla.attention_mass(q, data, bt, sk, want[1], torch.zeros(4, 704, device="cuda"), softmax_scale=SCALE, causal=True,
+                                       kv_scales=scales)
+    sums = weigh()
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream() for _ in range(4)], []
+    for k in range(12):
+        with torch.cuda.stream(streams[k % 4]):
+            got.append(shared() if k % 2 else weigh())
+    torch.cuda.synchronize()
+    for k, r in enumerate(got):
+        if k % 2:
+            assert torch.equal(r[0], want[0]) and torch.equal(r[1], want[1])
+        else:
+            assert torch.equal(r[:, :90], sums[:, :90])
+    assert mla.device_status() == 0
