@@ -13,7 +13,7 @@
 // other through a small ring in L2.  All results are fp32 partials, normalised,
 // with a base-2 log-sum-exp: another kernel joins prefix and own parts.
 //
-// 64 sequences of 128 heads on 16384 shared tokens: 228 us in all for 301 GFLOP (154 us at the
+// 64 sequences of 128 heads on 16384 shared tokens: 221 us in all for 301 GFLOP (154 us at the
 // measured bf16 rate); a tile takes about 1750 cycles, in which rank 0's softmax (1500), rank 1's message loop
 // (1500) and the QK MMAs (1364) each are nearly back to back.
 //
@@ -21,7 +21,7 @@
 // scale the codes themselves (exact; the scale multiplies scores and results).  With a scale
 // for each 128 values a product of code and scale does not fit 8 bits, and a log-sum-exp over few
 // keys shows it: keys are sums of two bf16 values (16 bits), so rank 0 makes twice the products
-// of a latent, from a second stage a tile.  (One: 117 us instead of 163 for 48 sequences of four
+// of a latent, from a second stage a tile.  (One: 117 us instead of 155 for 48 sequences of four
 // tokens and 64 heads on three prefixes of up to 5000, and log-sum-exps off by 1e-4 of
 // themselves instead of 1e-6.)  Values are the first of the two: P is bf16 too, and its
 // rounding of the same size.

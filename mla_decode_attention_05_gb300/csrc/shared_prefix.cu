@@ -16,10 +16,9 @@
 namespace mla {
 namespace {
 
-constexpr int kSchedThreads = 1024;
 constexpr int kMaxItems = MLA_MAX_ITEMS;
 
-template <class Op>
+template <int kSchedThreads, class Op>
 __device__ inline int block_scan(int v, int *warp_sums, Op op) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
@@ -30,13 +29,13 @@ __device__ inline int block_scan(int v, int *warp_sums, Op op) {
   if (lane == 31) warp_sums[warp] = v;
   __syncthreads();
   if (warp == 0) {
-    int s = warp_sums[lane];
+    int s = lane < kSchedThreads / 32 ? warp_sums[lane] : 0;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int u = __shfl_up_sync(0xffffffffu, s, o);
       if (lane >= o) s = op(s, u);
     }
-    warp_sums[lane] = s;
+    if (lane < kSchedThreads / 32) warp_sums[lane] = s;
   }
   __syncthreads();
   if (warp > 0) v = op(v, warp_sums[warp - 1]);
@@ -63,9 +62,12 @@ __device__ inline int last_le(int n, int x, At at) {
 }
 
 constexpr int kGroupCache = 256;  // groups that are kept in shared memory
+constexpr int kMostParts = 511;
+constexpr int kFewThreads = 256;  // of the schedule's block where that is enough for items, sequences, groups and workers
 
 struct SchedShared {
   int C[kMaxItems + 1];
+  int cuts[kMostParts + 1];  // where each worker's segment of the line begins, and the end
   uint8_t head[kMaxItems];
   int4 groups[kGroupCache];
   int warp_sums[32];
@@ -76,12 +78,30 @@ struct Cost {
   int head, tiles;
 };
 
-// mla_decode_metadata's rule over n items: item i costs head + tiles, as item(i) says, on a
-// line that is cut into `parts` equal segments.  Writes the segments, the pieces
+// Two kinds of items lie on one line, those from `from` on of the second kind.  A worker that
+// begins within an item has that item's head to do again, which is not on the line.
+struct Kinds {
+  int from, head1, head2;  // heads of a usual item of each
+};
+
+// How much of the line a worker gets of each kind, c1 and c2, so that all have the same to do:
+//   c1 + head1 = c2 + head2 = L,  W1 / c1 + W2 / c2 = parts
+// which is a quadratic equation for L (its larger root).
+__device__ __forceinline__ float2 shares(const Kinds &k, int W1, int W2, int parts) {
+  const float n = (float)parts, w1 = (float)W1, w2 = (float)W2;
+  const float h1 = W1 > 0 ? (float)k.head1 : 0.f, h2 = W2 > 0 ? (float)k.head2 : 0.f;
+  const float b = n * (h1 + h2) + w1 + w2, c = n * h1 * h2 + w1 * h2 + w2 * h1;
+  const float L = (b + sqrtf(fmaxf(b * b - 4.f * n * c, 0.f))) / (2.f * n);
+  return make_float2(fmaxf(L - h1, 1.f), fmaxf(L - h2, 1.f));
+}
+
+// The schedule of n items: item i costs head + tiles, as item(i) says, on a
+// line that is cut into `parts` segments (mla_decode_metadata's form).  Writes the segments, the pieces
 // of each item and its first slot of results; `least`: slots that every item has
 // at least.
-template <class Item, class Slot>
-__device__ void schedule(SchedShared &sh, int n, int parts, int least, int32_t *md_out, int32_t *pieces, Item item, Slot slot) {
+template <int kSchedThreads, class Item, class Slot>
+__device__ void schedule(SchedShared &sh, int n, int parts, int least, int32_t *md_out, int32_t *pieces, const Kinds &kinds,
+                         Item item, Slot slot) {
   const int tid = threadIdx.x;
   if (tid == 0) { sh.carry = 0; sh.C[0] = 0; }
   __syncthreads();
@@ -92,24 +112,32 @@ __device__ void schedule(SchedShared &sh, int n, int parts, int least, int32_t *
       cost = item(i);
       sh.head[i] = (uint8_t)cost.head;
     }
-    const int incl = block_scan(cost.head + cost.tiles, sh.warp_sums, Add()) + sh.carry;
+    const int incl = block_scan<kSchedThreads>(cost.head + cost.tiles, sh.warp_sums, Add()) + sh.carry;
     if (i < n) sh.C[i + 1] = incl;
     __syncthreads();
     if (tid == kSchedThreads - 1) sh.carry = incl;
     __syncthreads();
   }
-  const int W = sh.C[n], L = max(ceil_div(W, parts), 1);
+  const int W = sh.C[n], W1 = sh.C[min(kinds.from, n)];
+  {
+    // no two cuts at one place before the end: every segment has a tile or a head
+    const float2 c = shares(kinds, W1, W - W1, parts);
+    const float border = (float)W1 / c.x, at = (float)tid <= border ? tid * c.x : W1 + (tid - border) * c.y;
+    const int cut = block_scan<kSchedThreads>(tid < parts ? (int)fminf(at, (float)W) - tid : INT32_MIN, sh.warp_sums, Max());
+    if (tid <= parts) sh.cuts[tid] = tid < parts ? min(cut + tid, W) : W;
+    __syncthreads();
+  }
+  auto worker = [&](int x) { return last_le(parts, x, [&](int p) { return sh.cuts[p]; }); };
   for (int p = tid; p < parts; p += kSchedThreads) {
-    const long long at = (long long)p * L;
+    const int lo = sh.cuts[p], hi = sh.cuts[p + 1];
     int4 lo4 = make_int4(n, 0, n - 1, 0), hi4 = make_int4(0, 0, 0, 0);
-    if (at < W) {
-      const int lo = (int)at, hi = min(lo + L, W);
+    if (lo < W) {
       auto C = [&](int i) { return sh.C[i]; };
       const int a = last_le(n, lo, C), z = last_le(n, hi - 1, C);
       const int fa = sh.C[a] + sh.head[a], fz = sh.C[z] + sh.head[z];  // where their first tiles lie
       const int na = sh.C[a + 1] - fa, nz = sh.C[z + 1] - fz;
       lo4 = make_int4(a, min(max(lo - fa, 0), na), z, min(max(hi - fz, 0), nz));
-      hi4 = make_int4(na > 0 ? max(p - fa / L, 0) : 0, sh.C[a] == lo ? 1 : 0, 0, 0);
+      hi4 = make_int4(na > 0 ? max(p - worker(fa), 0) : 0, sh.C[a] == lo ? 1 : 0, 0, 0);
     }
     reinterpret_cast<int4 *>(md_out)[2 * p] = lo4;
     reinterpret_cast<int4 *>(md_out)[2 * p + 1] = hi4;
@@ -121,16 +149,26 @@ __device__ void schedule(SchedShared &sh, int n, int parts, int least, int32_t *
     int room = 0;
     if (i < n) {
       const int first = sh.C[i] + sh.head[i], k = sh.C[i + 1] - first;
-      const int got = k == 0 ? 0 : (first + k - 1) / L - first / L + 1;
+      const int got = k == 0 ? 0 : worker(first + k - 1) - worker(first) + 1;
       pieces[i] = got;
       room = max(got, least);
     }
-    const int incl = block_scan(room, sh.warp_sums, Add()) + sh.carry;
+    const int incl = block_scan<kSchedThreads>(room, sh.warp_sums, Add()) + sh.carry;
     if (i < n) slot(i, incl - room, incl);
     __syncthreads();
     if (tid == kSchedThreads - 1) sh.carry = incl;
     __syncthreads();
   }
+}
+
+// An item's head, in tiles: its queries' way into tensor memory and its results' way out.  On 80
+// workers' times over eight batches (bf16, one scale): 6.7 us + 0.78 a tile of a prefix + 0.85 of own
+// tokens + 1.1 an item + 1.2 for each 32 of its rows; with a scale for each 128 values a tile takes 1.4 us and an item
+// of 128 rows 4.2.  (Heads of 2 + rows / 32 for all, and equal parts of the line: 228 instead of 221 us for 64
+// sequences of 128 heads on 16384 shared tokens, FP8 groups 163 instead of 155.)
+__device__ __forceinline__ int head_of(const SharedParams &p, int rows) {
+  const int r = ceil_div(rows, 32);
+  return p.format == MLA_KV_FP8_E4M3 ? 1 + (r + 1) / 2 : (3 + 3 * r) / 2;
 }
 
 // Keys of the last row of own tile mt of a sequence of n tokens.
@@ -142,6 +180,7 @@ __device__ __forceinline__ int own_keys(const SharedParams &p, int n, int mt) {
 // Block 0: the items of shared_attention_kernel, prefixes first, and their
 // schedule.  Block 1 (FP8): the decode kernel's schedule of the own tokens, with room for two pieces
 // of every item, so that it writes all its results as partials.
+template <int kSchedThreads>
 __global__ void __launch_bounds__(kSchedThreads) shared_schedule_kernel(SharedParams p) {
   __shared__ SchedShared sh;
   const int tid = threadIdx.x, TH = p.T * p.H;
@@ -156,7 +195,7 @@ __global__ void __launch_bounds__(kSchedThreads) shared_schedule_kernel(SharedPa
   if (blockIdx.x == 1) {
     for (int b = tid; b < p.B; b += kSchedThreads) p.lens_o[b] = length(p.seqlens[b], p.max_pages);
     __syncthreads();
-    schedule(sh, p.B * p.n_mt, p.parts, 2, p.md_o, p.cnt_o,
+    schedule<kSchedThreads>(sh, p.B * p.n_mt, p.parts, 2, p.md_o, p.cnt_o, Kinds{0, 0, 0},
              [&](int i) { return Cost{FIXED_COST, ceil_div(own_keys(p, p.lens_o[i % p.B], i / p.B), PAGE)}; },
              [&](int i, int at, int end) {
                if (i == 0) p.ns_o[0] = 0;
@@ -179,7 +218,7 @@ __global__ void __launch_bounds__(kSchedThreads) shared_schedule_kernel(SharedPa
       n = length(p.prefix_lens[g], p.max_prefix);
     }
     // a group that begins before the end of an earlier one begins there
-    const int reach = max(block_scan(min(max(max(b0, b1), 0), p.B), sh.warp_sums, Max()), sh.top);
+    const int reach = max(block_scan<kSchedThreads>(min(max(max(b0, b1), 0), p.B), sh.warp_sums, Max()), sh.top);
     int before = __shfl_up_sync(0xffffffffu, reach, 1);
     if ((tid & 31) == 31) sh.warp_sums[tid >> 5] = reach;
     __syncthreads();
@@ -188,7 +227,7 @@ __global__ void __launch_bounds__(kSchedThreads) shared_schedule_kernel(SharedPa
     b0 = min(max(b0, before), p.B);
     b1 = max(min(b1, p.B), b0);
     const int tiles = g < p.G && n > 0 ? ceil_div((b1 - b0) * TH, M_TILE) : 0;
-    const int incl = block_scan(tiles, sh.warp_sums, Add());
+    const int incl = block_scan<kSchedThreads>(tiles, sh.warp_sums, Add());
     if (g < p.G) groups[g] = make_int4(b0, b1, sh.carry + incl - tiles, n);
     __syncthreads();
     if (tid == kSchedThreads - 1) {
@@ -204,9 +243,8 @@ __global__ void __launch_bounds__(kSchedThreads) shared_schedule_kernel(SharedPa
     const int4 g = groups[last_le(p.G, b, [&](int i) { return i == 0 ? 0 : groups[i].x; })];
     p.seq[b] = g.w > 0 && b >= g.x && b < g.y ? make_int2(g.z, (b - g.x) * TH) : make_int2(-1, 0);
   }
-  // An item's head: its queries' way into tensor memory and its results' way out,
-  // in tiles of 1 us (items of one tile each: 5.6 us beside the tile with 128 rows, 2.8 with 16).
-  schedule(sh, n_items, p.parts, 0, p.md, p.pieces,
+  const Kinds kinds{n_prefix, head_of(p, min(M_TILE, p.B * TH)), head_of(p, min(M_TILE, TH))};
+  schedule<kSchedThreads>(sh, n_items, p.parts, 0, p.md, p.pieces, kinds,
            [&](int i) {
              SharedItem it;
              if (i < n_prefix) {
@@ -220,7 +258,7 @@ __global__ void __launch_bounds__(kSchedThreads) shared_schedule_kernel(SharedPa
                                1, mt * M_TILE, 0};
              }
              p.items[i] = it;
-             return Cost{2 + ceil_div(it.rows, 32), it.tiles};
+             return Cost{head_of(p, it.rows), it.tiles};
            },
            [&](int i, int at, int) { p.items[i].slot = at; });
 }
@@ -517,6 +555,7 @@ extern "C" int mla_decode_shared(const void *q, const void *kv_cache, int kv_for
     return fail(MLA_ERR_INVALID_ARG, "softmax_scale must be finite and > 0");
   int parts = 0;
   if ((rc = device_parts(&parts)) != MLA_OK) return rc;
+  if (parts > kMostParts) return fail(MLA_ERR_UNSUPPORTED, "more SMs than the schedule has room for");
   const Layout l = layout(B, T, H, G, kv_format, max_prefix_pages, max_pages, parts);
   if (!workspace || workspace_bytes < l.total) {
     char msg[96];
@@ -583,7 +622,10 @@ extern "C" int mla_decode_shared(const void *q, const void *kv_cache, int kv_for
   cfg.stream = s;
   cfg.attrs = pdl;
   cfg.numAttrs = 1;
-  cudaError_t e = launch_dependent(shared_schedule_kernel, l.apart ? 2 : 1, kSchedThreads, 0, s, p);
+  // (few threads meet sooner)
+  const bool small = l.room <= kFewThreads && B <= kFewThreads && G <= kFewThreads && parts < kFewThreads;
+  cudaError_t e = small ? launch_dependent(shared_schedule_kernel<kFewThreads>, l.apart ? 2 : 1, kFewThreads, 0, s, p)
+                        : launch_dependent(shared_schedule_kernel<1024>, l.apart ? 2 : 1, 1024, 0, s, p);
   if (e == cudaSuccess && wide) {
     const int longest = l.apart || max_prefix_pages > max_pages ? max_prefix_pages : max_pages;
     cfg.gridDim = dim3(longest < 1024 ? longest : 1024, l.apart ? G : G + B, kWidenParts);
