@@ -97,7 +97,6 @@ struct Bars {
   uint64_t slot_full[kMostSlots], slot_empty[kMostSlots];
   uint64_t raw_full[kMostSlots];  // FP8: a unit's codes are in place (of the resident ones, or of the slots)
   uint64_t d_full[4], d_empty[4];                        // empty: rank 0
-  uint64_t sc_full[2], sc_empty[2];                      // a tile's scales
   alignas(16) float nl[2][kMostRows];  // -lse of a tile's query rows
   alignas(16) int lim[2][kMostRows];   // keys that a row sees; 0 for one that is no row, or has no weight to give
   int least[2][kMostRows / 32];        // the smallest of each 32 rows
@@ -107,23 +106,13 @@ struct Bars {
   uint32_t tmem_base;
   int abort;
 };
-// Shared memory: barriers, the resident operand's blocks, slots, FP8 scales of two tiles ([128][4]).
+// Shared memory: barriers, the resident operand's blocks, what streams.
 constexpr uint32_t OFF_RES = 7 * 1024;
-constexpr uint32_t kScaleBytes = kKeys * 16;
 constexpr uint32_t kSmem = 232448 / 1024 * 1024;
-constexpr uint32_t OFF_SCALES = kSmem - 2 * kScaleBytes;
 static_assert(sizeof(Bars) <= OFF_RES, "shared memory map");
-static_assert(OFF_RES + kBlocks * kBlock + 4 * kBlock <= OFF_SCALES, "shared memory map");
+static_assert(OFF_RES + kBlocks * kBlock + 4 * kBlock <= kSmem, "shared memory map");
 
-// The most bytes that may come between the barriers and the scales.
-constexpr uint32_t kRoom = OFF_SCALES - OFF_RES;
-
-// `bytes` (a multiple of 16) side by side into shared memory.
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-               "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bar)
-               : "memory");
-}
+constexpr uint32_t kRoom = kSmem - OFF_RES;
 
 // Arrives on a barrier of the pair's other CTA behind this thread's own writes to
 // shared memory.  (Release at the scope of the CTA: what it publishes is read on this
@@ -288,14 +277,13 @@ struct Place {
 // upper half of what it will fill, on a barrier of this CTA; the rotated part of rows
 // with scales is bf16 and lands as it is used.
 template <bool kStreamKeys, int kFormat, bool kPoll>
-__device__ void load_role(const MassParams &p, uint8_t *base, Bars &br, const CUtensorMap *k_map, const CUtensorMap *pe_map,
+__device__ void load_role(const MassParams &p, Bars &br, const CUtensorMap *k_map, const CUtensorMap *pe_map,
                           const CUtensorMap *q_map, const Work &w, const Place &at, int which) {
   using C = Of<kFormat>;
   constexpr int kRows = C::rows;
-  const uint32_t scales = smem_u32(base + OFF_SCALES);
   const uint64_t keep = policy_evict_normal(), key_pol = kStreamKeys ? policy_evict_first() : keep;
   int s = 0;
-  uint32_t ph = 1, rph = 1, tile = 0;
+  uint32_t ph = 1, rph = 1;
   // This CTA's pages of a tile, and how many both CTAs have.  Lanes 0-3 look up the
   // tile's four pages; those of the next tile while this one is asked for.
   int pg[2] = {-1, -1}, pages = 0, entry = -1;
@@ -332,22 +320,6 @@ __device__ void load_role(const MassParams &p, uint8_t *base, Bars &br, const CU
     else if (C::scaled) tma_load_3d(dst + which * kHalf, pe_map, bar, 0, 0, page, key_pol);
     else tma_load_3d(dst + kHalf + which * (kHalf / 2), pe_map, bar, D_V, 0, page, key_pol);
   };
-  // a tile's scales, both pages' by warp 3
-  auto scales_of_tile = [&] {
-    if (!C::scaled || which == 0) return true;
-    const uint32_t b = tile & 1;
-    if (!warp_wait<kPoll>(&br, &br.sc_empty[b], ((tile >> 1) & 1) ^ 1, p)) return false;
-    if (elect_one()) {
-      const uint32_t bar = smem_u32(&br.sc_full[b]);
-      mbar_arrive_expect_tx(bar, ((pg[0] >= 0) + (pg[1] >= 0)) * (kScaleBytes / 2));
-#pragma unroll
-      for (int h = 0; h < 2; h++)
-        if (pg[h] >= 0)
-          bulk_load(scales + b * kScaleBytes + h * (kScaleBytes / 2), p.kv_scales + (size_t)pg[h] * PAGE * 4, kScaleBytes / 2, bar);
-    }
-    __syncwarp();
-    return true;
-  };
   const int half = p.box / 2;  // query rows of each CTA
   auto rows = [&](uint32_t dst, uint32_t block, uint64_t *full, int b, int qt, int u) {
     if (!elect_one()) return;
@@ -362,15 +334,11 @@ __device__ void load_role(const MassParams &p, uint8_t *base, Bars &br, const CU
     // (the first of what streams is asked for along with the resident units, so that
     // both follow the last phase's MMAs unit by unit)
     fetch(f.b, f.t, f.len);
-    if (!kStreamKeys) {
-      look();
-      if (!scales_of_tile()) return false;
-    }
+    if (!kStreamKeys) look();
     for (int i = f.i0; i < (kStreamKeys || which == 0 ? f.i1 : f.i0 + 1); i++) {
       if (kStreamKeys) {
         look();
         if (i + 1 < f.i1) fetch(f.b, i + 1, f.len);
-        if (!scales_of_tile()) return false;
       }
       for (int u = 0; u < C::units; u++) {
         if (i == f.i0 && (!kStreamKeys || which == 0)) {
@@ -391,10 +359,8 @@ __device__ void load_role(const MassParams &p, uint8_t *base, Bars &br, const CU
           ph ^= 1;
         }
       }
-      if (kStreamKeys) tile++;
     }
     rph ^= 1;
-    if (!kStreamKeys) tile++;
     return true;
   });
 }
@@ -555,7 +521,7 @@ __device__ __forceinline__ float ex2(float x) {
 // The warps from 4 on that sum: thread = key of the tile = lane of tensor memory (and,
 // with scales, half of the columns).
 template <bool kStreamKeys, int kFormat, bool kPoll>
-__device__ void sum_role(const MassParams &p, uint8_t *base, Bars &br, const Work &w, uint32_t tmem, uint32_t rank, int pair_index) {
+__device__ void sum_role(const MassParams &p, Bars &br, const Work &w, uint32_t tmem, uint32_t rank, int pair_index) {
   using C = Of<kFormat>;
   constexpr int kD = C::kd, kRows = C::rows, kThreads = 32 * C::sum_warps;
   const int me = threadIdx.x - 128, lane = threadIdx.x & 31, i = me % kKeys, first = me / kKeys * C::cols;
@@ -619,11 +585,24 @@ __device__ void sum_role(const MassParams &p, uint8_t *base, Bars &br, const Wor
     auto key_of = [&](int t) { return t * kTileKeys + (int)rank * kKeys + i; };
     // what a key had before is fetched while its scores are made
     float before = 0.f;
-    int page = -1;
+    // A key's page is looked up two tiles ahead, its scales are fetched one ahead.  (By TMA along
+    // with the keys they came 2400 cycles after the first scores: 35 instead of 33 us for 32 sequences of 4400
+    // tokens, 64 heads.)
+    const int end_t = kStreamKeys ? f.i1 : f.t + 1;
+    auto page_at = [&](int t) {
+      const int n = key_of(t), page = t < end_t && n < f.len ? __ldg(p.block_table + (size_t)f.b * p.max_pages + n / PAGE) : -1;
+      return page;
+    };
+    auto scales_at = [&](int t, int page) {
+      return C::scaled && page >= 0 && page < p.num_pages
+                 ? __ldg(reinterpret_cast<const float4 *>(p.kv_scales) + (size_t)page * PAGE + key_of(t) % PAGE)
+                 : make_float4(0.f, 0.f, 0.f, 0.f);
+    };
+    int page = page_at(kStreamKeys ? f.i0 : f.t), next_page = page_at(kStreamKeys ? f.i0 + 1 : f.t + 1);
+    float4 sc = scales_at(kStreamKeys ? f.i0 : f.t, page);
     auto prepare = [&](int t) {
       const int n = key_of(t);
       if (first > 0) return;
-      page = n < f.len ? __ldg(p.block_table + (size_t)f.b * p.max_pages + n / PAGE) : -1;
       if (f.whole && p.decay != 0.f && n < f.len) before = p.mass[(size_t)f.b * p.cap + n];
     };
     auto store = [&](int t, float v) {
@@ -645,17 +624,12 @@ __device__ void sum_role(const MassParams &p, uint8_t *base, Bars &br, const Wor
       return true;
     };
     if (!kStreamKeys) prepare(f.t);
-    float4 sc = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int k = f.i0; k < f.i1; k++) {
       if (kStreamKeys) prepare(k);
       else set_rows(f, k);
+      const float4 next_sc = scales_at(k + 1, kStreamKeys ? next_page : -1);
+      const int after = kStreamKeys ? page_at(k + 2) : -1;
       bool ok = warp_wait<kPoll>(&br, &br.d_full[g % kD], (g / kD) & 1, p);
-      if (C::scaled && (kStreamKeys || k == f.i0)) {
-        if (ok) ok = warp_wait<kPoll>(&br, &br.sc_full[tile & 1], (tile >> 1) & 1, p);
-        sc = *reinterpret_cast<const float4 *>(base + OFF_SCALES + (tile & 1) * kScaleBytes + i * 16);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&br.sc_empty[tile & 1]));
-      }
       if (bar_red_or(kSumBar, kThreads, !ok)) return false;
       tc_fence_after();
       const int key = key_of(kStreamKeys ? k : f.t);
@@ -708,6 +682,7 @@ __device__ void sum_role(const MassParams &p, uint8_t *base, Bars &br, const Wor
       const float got = (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
       if (kStreamKeys) {
         if (!finish(k, got, ok)) return false;
+        page = next_page, next_page = after, sc = next_sc;
       } else {
         sum += got;
         if (bar_red_or(kSumBar, kThreads, !ok)) return false;
@@ -754,10 +729,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Of<kFormat>::threads
       mbar_init(smem_u32(&br.d_full[i]), 1);
       mbar_init(smem_u32(&br.d_empty[i]), 2 * C::sum_warps);
     }
-    for (int i = 0; i < 2; i++) {
-      mbar_init(smem_u32(&br.sc_full[i]), 1);
-      mbar_init(smem_u32(&br.sc_empty[i]), C::sum_warps);
-    }
     br.abort = 0;
     br.start_b = br.start_t = 0;
     fence_mbar_init_cluster();
@@ -778,12 +749,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Of<kFormat>::threads
   const Work w = find_work(p, br, pair_index, pairs);
   if (warp < 4) {
     if constexpr (C::scaled) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLoadRegs));
-    if (warp == 0 || warp == 3) load_role<kStreamKeys, kFormat, kPoll>(p, smem, br, &k_map, &pe_map, &q_map, w, at, warp == 3);
+    if (warp == 0 || warp == 3) load_role<kStreamKeys, kFormat, kPoll>(p, br, &k_map, &pe_map, &q_map, w, at, warp == 3);
     else if (at.rank == 0 && warp == 1) mma_role<kStreamKeys, kFormat>(p, br, w, at, tmem);
     else if (at.rank == 0 && warp == 2) wait_role<kStreamKeys, kFormat, kPoll>(p, br, w);
   } else if (warp < 4 + C::sum_warps) {
     if constexpr (C::scaled) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSumRegs));
-    sum_role<kStreamKeys, kFormat, kPoll>(p, smem, br, w, tmem, at.rank, pair_index);
+    sum_role<kStreamKeys, kFormat, kPoll>(p, br, w, tmem, at.rank, pair_index);
   } else if constexpr (C::fp8) {
     if constexpr (C::scaled) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kWideRegs));
     widen_role<kStreamKeys, kFormat, kPoll>(p, br, w, at, threadIdx.x - 32 * (4 + C::sum_warps));
