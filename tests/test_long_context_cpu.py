@@ -79,7 +79,8 @@ def test_evict_arguments(L, args, code):
 
 def test_workspace_sizes(L):
     import mla_decode_attention_05_gb300 as m
-    assert m.attention_mass_workspace_bytes(4, 2, 128, 1000) == 0     # one tile of query rows
+    assert m.attention_mass_workspace_bytes(4, 1, 128, 1000) == 0     # one tile of query rows, whatever the format
+    assert m.attention_mass_workspace_bytes(4, 2, 128, 1000) > 0      # (FP8 rows with scales: two)
     assert m.attention_mass_workspace_bytes(4, 3, 128, 1000) > 0
     assert L.mla_attention_mass_workspace_bytes(0, 1, 1, 1) == 0
     assert m.evict_workspace_bytes(3, 1000, 400) >= 3 * 4 + 2 * 3 * 400 * 4
