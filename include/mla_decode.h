@@ -495,7 +495,8 @@ int mla_value_project(const void *attn, int64_t ld_token, int64_t ld_head, const
  * (73728 bytes an entry of prefix_table, with a scale for each 128 values 139264),
  * and own pages too where B * max_pages <= 2048; where it is more, own FP8 rows are
  * rounded to bf16, as mla_decode does.  At most 8192 work items: B * ceil(T * H / 128) +
- * ceil(B * T * H / 128) + G (MLA_ERR_UNSUPPORTED above).  A wait that gives up sets
+ * ceil(B * T * H / 128) + G, and 2^30 tiles of 64 keys in the tables' width
+ * (MLA_ERR_UNSUPPORTED above).  A wait that gives up sets
  * MLA_STATUS_WAIT_TIMEOUT.  Asynchronous on `stream`; can be captured in a CUDA
  * graph.  Returns MLA_OK or a negative code.
  */

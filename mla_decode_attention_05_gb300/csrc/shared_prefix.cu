@@ -505,6 +505,9 @@ int check_sizes(int B, int T, int H, int G, int format, int max_prefix, int max_
     snprintf(msg, sizeof msg, "%lld work items exceed the limit %d", items, kMaxItems);
     return fail(MLA_ERR_UNSUPPORTED, msg);
   }
+  // (the schedule counts tiles in 32 bits)
+  const long long tiles = (long long)B * ceil_div(T * H, M_TILE) * max_pages + (((long long)B * T * H + M_TILE - 1) / M_TILE + G) * max_prefix;
+  if (tiles > 0x3fffffffLL) return fail(MLA_ERR_UNSUPPORTED, "more than 2^30 tiles of 64 keys in max_pages and max_prefix_pages");
   if ((long long)G * max_prefix > 0x7fffffffLL) return fail(MLA_ERR_UNSUPPORTED, "G * max_prefix_pages exceeds 2^31 - 1");
   return MLA_OK;
 }

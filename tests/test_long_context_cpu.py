@@ -24,7 +24,7 @@ def v(x):
 @pytest.mark.parametrize("args,code", [
     (dict(B=0), -1), (dict(T=0), -1), (dict(T=17), -1), (dict(H=0), -1), (dict(H=129), -1), (dict(G=0), -1), (dict(width=0), -1),
     (dict(own=0), -1), (dict(fmt=3), -1), (dict(fmt=-1), -1), (dict(B=9000), -2), (dict(G=8192), -2),
-    (dict(G=1 << 12, width=1 << 20), -2), (dict(q=None), -1), (dict(cache=None), -1), (dict(pt=None), -1), (dict(pl=None), -1),
+    (dict(G=1 << 12, width=1 << 20), -2), (dict(own=1 << 30), -2), (dict(B=64, T=16, H=128, own=1 << 20), -2), (dict(q=None), -1), (dict(cache=None), -1), (dict(pt=None), -1), (dict(pl=None), -1),
     (dict(bt=None), -1), (dict(sk=None), -1), (dict(out=None), -1), (dict(lse=None), -1), (dict(off=None, G=2), -1), (dict(q=8), -1),
     (dict(cache=264), -1), (dict(out=264), -1), (dict(pt=258), -1), (dict(off=258), -1), (dict(lse=258), -1), (dict(fmt=1, sc=None), -1),
     (dict(fmt=1, sc=264), -1), (dict(fmt=2, sc=258), -1), (dict(page=32), -2), (dict(pages=0), -1), (dict(causal=2), -1),
