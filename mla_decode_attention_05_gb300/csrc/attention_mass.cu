@@ -13,7 +13,7 @@
 // rows on 12001 keys 101 us.)
 //
 // 64 sequences of up to 32768 tokens, 128 heads: 184 us, bound by HBM (6.6 TB/s of 6.7).
-// The last 64 tokens of 12001, 128 heads: 65 us for 113 GFLOP, bound by the tensor cores (82 % of the
+// The last 64 tokens of 12001, 128 heads: 67 us for 113 GFLOP, bound by the tensor cores (82 % of the
 // cycles).  32 FP8 sequences of up to 8192 tokens, 2 x 64 rows: 38 us for 95 MB, bound by the
 // hand-overs between loads, widening, products and sums.
 #include <atomic>
