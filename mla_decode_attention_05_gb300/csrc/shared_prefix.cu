@@ -63,6 +63,7 @@ __device__ inline int last_le(int n, int x, At at) {
 
 constexpr int kGroupCache = 256;  // groups that are kept in shared memory
 constexpr int kMostParts = 511;
+
 constexpr int kFewThreads = 256;  // of the schedule's block where that is enough for items, sequences, groups and workers
 
 struct SchedShared {
@@ -70,6 +71,7 @@ struct SchedShared {
   int cuts[kMostParts + 1];  // where each worker's segment of the line begins, and the end
   uint8_t head[kMaxItems];
   int4 groups[kGroupCache];
+  int lens[kFewThreads];  // own tokens, where there are no more sequences
   int warp_sums[32];
   int carry, top;
 };
@@ -119,15 +121,22 @@ __device__ void schedule(SchedShared &sh, int n, int parts, int least, int32_t *
     __syncthreads();
   }
   const int W = sh.C[n], W1 = sh.C[min(kinds.from, n)];
+  const float2 c = shares(kinds, W1, W - W1, parts);
+  const float border = (float)W1 / c.x;
   {
     // no two cuts at one place before the end: every segment has a tile or a head
-    const float2 c = shares(kinds, W1, W - W1, parts);
-    const float border = (float)W1 / c.x, at = (float)tid <= border ? tid * c.x : W1 + (tid - border) * c.y;
+    const float at = (float)tid <= border ? tid * c.x : W1 + (tid - border) * c.y;
     const int cut = block_scan<kSchedThreads>(tid < parts ? (int)fminf(at, (float)W) - tid : INT32_MIN, sh.warp_sums, Max());
     if (tid <= parts) sh.cuts[tid] = tid < parts ? min(cut + tid, W) : W;
     __syncthreads();
   }
-  auto worker = [&](int x) { return last_le(parts, x, [&](int p) { return sh.cuts[p]; }); };
+  const float per1 = 1.f / c.x, per2 = 1.f / c.y;
+  auto worker = [&](int x) {  // the last whose segment begins at x or before: near where the shares put it
+    int p = min(max((int)(x < W1 ? x * per1 : border + (x - W1) * per2), 0), parts - 1);
+    while (p > 0 && sh.cuts[p] > x) p--;
+    while (p + 1 < parts && sh.cuts[p + 1] <= x) p++;
+    return p;
+  };
   for (int p = tid; p < parts; p += kSchedThreads) {
     const int lo = sh.cuts[p], hi = sh.cuts[p + 1];
     int4 lo4 = make_int4(n, 0, n - 1, 0), hi4 = make_int4(0, 0, 0, 0);
@@ -192,6 +201,8 @@ __global__ void __launch_bounds__(kSchedThreads) shared_schedule_kernel(SharedPa
     if (n < 0 || n > most) atomicOr(p.status, MLA_STATUS_BAD_SEQLEN);
     return min(max(n, 0), most);
   };
+  const bool near_by = p.B <= kFewThreads;
+  if (near_by && tid < p.B) sh.lens[tid] = p.seqlens[tid];  // (seen behind the groups' barriers)
   if (blockIdx.x == 1) {
     for (int b = tid; b < p.B; b += kSchedThreads) p.lens_o[b] = length(p.seqlens[b], p.max_pages);
     __syncthreads();
@@ -253,7 +264,8 @@ __global__ void __launch_bounds__(kSchedThreads) shared_schedule_kernel(SharedPa
                const int row = (i - at.z) * M_TILE;
                it = SharedItem{at.x * TH + row, min(M_TILE, (at.y - at.x) * TH - row), at.w, ceil_div(at.w, PAGE), g, 0, 0, 0};
              } else {
-               const int b = (i - n_prefix) % p.B, mt = (i - n_prefix) / p.B, n = length(p.seqlens[b], p.max_pages);
+               const int k = i - n_prefix, mt = p.n_mt == 1 ? 0 : k / p.B, b = k - mt * p.B;
+               const int n = length(near_by ? sh.lens[b] : p.seqlens[b], p.max_pages);
                it = SharedItem{b * TH + mt * M_TILE, min(M_TILE, TH - mt * M_TILE), n, ceil_div(own_keys(p, n, mt), PAGE), b,
                                1, mt * M_TILE, 0};
              }
