@@ -468,7 +468,9 @@ int mla_value_project(const void *attn, int64_t ld_token, int64_t ld_head, const
  *   N(b, t) = {prefix tokens n < prefix_lens[g]} and
  *             {own tokens n < s_k} (causal = 0) or {n < s_k - T + t + 1} (causal = 1)
  * (with causal every query token sees the whole prefix: the query tokens are the
- * last T of the own ones).  A row without any key gets out = 0 and lse = -inf.
+ * last T of the own ones).  A row without any key gets out = 0 and lse = -inf; one
+ * whose scores are all -inf gets out = nan (0 / 0) and lse = -inf; one with a score of
+ * nan or +inf (a query of nan or inf, products that overflow) gets nan in both.
  *
  *   q, kv_cache, kv_format, num_pages, page_size, kv_scales, softmax_scale, out,
  *   lse, B, T, H   as for mla_decode

@@ -28,7 +28,8 @@
 //
 // Rows behind an item's last key, in its last page, and pages outside the pool never
 // reach a result: their scores are replaced by -inf, and rank 1 clears their
-// values in shared memory before the MMA reads them (0 * nan is nan).
+// values in shared memory before the MMA reads them (0 * nan is nan).  A query of nan or a score of
+// +inf makes its row's sum nan, which no comparison may take for the 0 of a row without keys.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -448,10 +449,12 @@ __device__ void softmax_role(const Ctx &c, uint32_t tmem, int w, int lane) {
     // keys that this row sees
     const int len = it.own ? row_kv_len(it.len, p.T, min(it.row0 + r, p.T * p.H - 1) / p.H, p.causal) : it.len;
     float m_ref = -INFINITY, l = 0.f, l_all = 0.f;
+    int most = 0;  // keys of a tile that it has seen, at most
     for (int t = t0; t < t1; t++, g++) {
       const uint32_t b = g & 1, u = g >> 1;
       if (!warp_wait(c, &br.s_full[b], u & 1)) return false;
       const int valid = br.valid[g % kValidRing], lim = min(valid, len - t * PAGE);
+      most = max(most, lim);
       tc_fence_after();
       float own[32], oth[32];
       tmem_ld32(lt + TM_S + b * 64 + hf * 32, *reinterpret_cast<uint32_t(*)[32]>(&own[0]));
@@ -513,7 +516,9 @@ __device__ void softmax_role(const Ctx &c, uint32_t tmem, int w, int lane) {
       if (lane == 0) mbar_arrive(smem_u32(&br.pwritten[gs]));
     }
     pc++;
-    if (live && hf == 0) p.lse_p[(size_t)slot_out * M_TILE + r] = l_all > 0.f ? m_ref * cs + __log2f(l_all) : -INFINITY;
+    // (the sum is 0 without keys and where all scores are -inf: the largest score's weight is 1 otherwise)
+    if (live && hf == 0)
+      p.lse_p[(size_t)slot_out * M_TILE + r] = l_all != 0.f ? m_ref * cs + __log2f(l_all) : most > 0 ? kAllLow : -INFINITY;
     return true;
   });
 }
@@ -614,7 +619,7 @@ __device__ void output_role(const Ctx &c, uint32_t tmem, int w, int lane) {
     }
     if (!warp_wait(c, &br.o_done[(g - 1) & 1], ((g - 1) >> 1) & 1)) return false;
     tc_fence_after();
-    const float inv = (ell > 0.f ? 1.f / ell : 0.f) * (p.format == MLA_KV_FP8_E4M3_TENSOR ? __ldg(p.kv_scales) : 1.f);
+    const float inv = (ell != 0.f ? 1.f / ell : 0.f) * (p.format == MLA_KV_FP8_E4M3_TENSOR ? __ldg(p.kv_scales) : 1.f);
     // chunk-major: the 32 rows of a warp store 8 columns as 1 KB side by side; the
     // next columns are on their way meanwhile
     float *dst = p.o_p + ((size_t)slot_out * 64 + hf * 32) * (M_TILE * 8) + (size_t)r * 8;

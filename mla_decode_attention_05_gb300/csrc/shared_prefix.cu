@@ -5,7 +5,7 @@
 // tokens, each perhaps split over several workers), L_s = log2 sum 2^score and
 // O_s = sum 2^(score - L_s) v:
 //   L = log2 sum_s 2^L_s,  O = sum_s 2^(L_s - L) O_s
-// and a part without keys has L_s = -inf and weight 0.
+// and a part without keys has L_s = -inf and weight 0 (see also kAllLow).
 #include <cmath>
 #include <cstdio>
 
@@ -429,7 +429,9 @@ __global__ void __launch_bounds__(kJoinWarps * 32) shared_join_kernel(SharedPara
       for (int j = 0; j < kDeep; j++) add(l[j], w[j]);
     }
   }
-  const float inv = sum > 0.f ? 1.f / sum : 0.f;
+  // nan in any part is nan here (m leaves it out, the sum does not)
+  const bool low = m == kAllLow && sum == sum;
+  const float inv = low ? NAN : sum != 0.f ? 1.f / sum : 0.f;
 #pragma unroll
   for (int c = 0; c < kChunks; c++) {
     uint32_t w[4];
@@ -441,7 +443,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) shared_join_kernel(SharedPara
     reinterpret_cast<uint4 *>(p.out + (size_t)R * D_V)[chunk + c] = make_uint4(w[0], w[1], w[2], w[3]);
   }
   if (chunk == 0)
-    p.lse[((size_t)b * p.H + r % p.H) * p.T + r / p.H] = sum > 0.f ? (m + log2f(sum)) * LN2 : -INFINITY;
+    p.lse[((size_t)b * p.H + r % p.H) * p.T + r / p.H] = sum != 0.f && !low ? (m + log2f(sum)) * LN2 : -INFINITY;
 }
 
 // ---- host ------------------------------------------------------------------------
