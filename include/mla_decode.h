@@ -12,7 +12,7 @@
  *
  *   s_n = softmax_scale * sum_{d<576} q[b,t,h,d] * K_n[d]      n in N(b,t)
  *   lse = ln sum_n exp(s_n)                  (natural log; -inf if N empty)
- *   out = sum_n exp(s_n - lse) * K_n[0:512]  (0 if N empty)
+ *   out = sum_n exp(s_n - lse) * K_n[0:512]  (0 if N empty; nan, 0 / 0, if all s_n are -inf)
  *
  * where N(b,t) = {n < s_k}                       dense
  *               {n < s_k - T + t + 1}           causal (query token t of T)

@@ -2,7 +2,7 @@
 // several workers.  With partial results (O_s, L_s) over disjoint key sets,
 // L = log2 sum_s 2^{L_s} and O = sum_s 2^{L_s - L} O_s (partials are stored
 // normalised and in base 2); a partial over no key has L_s = -inf and
-// weight 0.  One lane per query row, one warp per 32 output columns.
+// weight 0 (see also kAllLow).  One lane per query row, one warp per 32 output columns.
 #include "common.cuh"
 
 namespace mla {
@@ -82,12 +82,17 @@ combine_kernel(DecodeParams p) {
 #pragma unroll
   for (int s = 0; s < 4; s++) l4[s] = s < ns ? __ldcg(lse_r + (size_t)s * M_TILE) : -INFINITY;
   float m = fmaxf(fmaxf(l4[0], l4[1]), fmaxf(l4[2], l4[3]));
-  for (int s = 4; s < ns; s++) m = fmaxf(m, __ldcg(lse_r + (size_t)s * M_TILE));
+  bool any = l4[0] != -INFINITY || l4[1] != -INFINITY || l4[2] != -INFINITY || l4[3] != -INFINITY;
+  for (int s = 4; s < ns; s++) {
+    const float l = __ldcg(lse_r + (size_t)s * M_TILE);
+    any |= l != -INFINITY;
+    m = fmaxf(m, l);  // (leaves nan out; the sum does not)
+  }
   float acc[kChunks * 8];
 #pragma unroll
   for (int k = 0; k < kChunks * 8; k++) acc[k] = 0.f;
   float sum = 0.f;
-  if (m != -INFINITY) {
+  if (any) {
     for (int s = 0; s < ns; s += 2) {
       if (s > 0) {
         load_chunks(va, p, base + s, chunk0, r);
@@ -108,7 +113,8 @@ combine_kernel(DecodeParams p) {
   if (r >= rows) return;
   const int R = row0 + r;
   const int t = R / p.H, h = R % p.H;
-  const float inv = sum > 0.f ? 1.f / sum : 0.f;
+  const bool low = m == kAllLow && sum == sum;
+  const float inv = low ? __uint_as_float(0x7FC00000u) : sum != 0.f ? 1.f / sum : 0.f;
   __nv_bfloat16 *dst = p.out + (((size_t)b * p.T + t) * p.H + h) * D_V + chunk0 * 8;
   uint32_t wv[kChunks * 4];
 #pragma unroll
@@ -125,7 +131,7 @@ combine_kernel(DecodeParams p) {
       reinterpret_cast<uint4 *>(dst)[k] = make_uint4(wv[4 * k], wv[4 * k + 1], wv[4 * k + 2], wv[4 * k + 3]);
   }
   if (warp == 0 && blockIdx.z == 0)
-    p.lse[((size_t)b * p.H + h) * p.T + t] = sum > 0.f ? (m + log2f(sum)) * LN2 : -INFINITY;
+    p.lse[((size_t)b * p.H + h) * p.T + t] = sum != 0.f && !low ? (m + log2f(sum)) * LN2 : -INFINITY;
 }
 
 }  // namespace

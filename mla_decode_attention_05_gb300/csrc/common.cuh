@@ -23,6 +23,10 @@ constexpr int P_RING = 8;
 constexpr int P_SLOT_BYTES = 17920;
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float LN2 = 0.6931471805599453f;
+// A partial result's base-2 log-sum-exp: -inf says that a row has no keys there, this that all of its
+// keys' scores are -inf, so that the part weighs nothing beside others and a row of nothing
+// else is 0 / 0.  (A sum of nan is the part's log-sum-exp too, and goes on into the result.)
+constexpr float kAllLow = -3.402823466e38f;
 
 // Everything a decode / combine kernel needs, by value.
 struct DecodeParams {

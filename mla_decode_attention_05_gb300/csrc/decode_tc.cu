@@ -1063,6 +1063,7 @@ __device__ void softmax_role(const Ctx &c, uint32_t tmem, int w, int lane) {
     float m_ref = -INFINITY;  // reference max, raw score units
     float l = 0.f;            // this half's part of the row sum
     float l_all = 0.f;
+    uint32_t seen = 0;        // not 0: the row has a key here
     for (int tile = t0; tile < t1; tile++, g++) {
       const uint32_t b = g & 1, u = g >> 1, mi = g % kMaskRing;
       // 1. tile validity and this row's 64 scores
@@ -1074,6 +1075,7 @@ __device__ void softmax_role(const Ctx &c, uint32_t tmem, int w, int lane) {
         mlo &= (uint32_t)keep;
         mhi &= (uint32_t)(keep >> 32);
       }
+      seen |= mlo | mhi;
       if (!warp_wait(c, &br.s_full[b], u & 1)) return false;
       tc_fence_after();
       float own[32], oth[32];  // this half's 32 scores and the partner half's
@@ -1139,19 +1141,21 @@ __device__ void softmax_role(const Ctx &c, uint32_t tmem, int w, int lane) {
         if (lane == 0) mbar_arrive(smem_u32(&br.lsum[q][pc & 1]));
         if (!warp_wait(c, &br.lsum[q][pc & 1], (pc >> 1) & 1)) return false;
         l_all = lp[r] + lp[M_TILE + r];
-        if (hf == 0) mo->ell[r] = l_all;
+        // (0 / 0 in the final output of a row whose scores are all -inf)
+        if (hf == 0) mo->ell[r] = l_all == 0.f && seen && ri.nsplit <= 1 ? __uint_as_float(0x7FC00000u) : l_all;
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&br.pwritten[gs]));
     }
     pc++;
-    // LSE of this piece (final, natural log; or the split partial, base 2)
+    // LSE of this piece (final, natural log; or the split partial, base 2).  A sum of nan is one;
+    // 0 is that of a row without keys, or whose scores are all -inf.
     if (ri.ok && hf == 0) {
-      const float lse2 = l_all > 0.f ? m_ref * cs + __log2f(l_all) : -INFINITY;
+      const float lse2 = l_all != 0.f ? m_ref * cs + __log2f(l_all) : -INFINITY;
       if (ri.nsplit <= 1)
         *lse_dst = lse2 * LN2;
       else
-        p.ws_lse[ri.slot * M_TILE + r] = lse2;
+        p.ws_lse[ri.slot * M_TILE + r] = l_all == 0.f && seen ? kAllLow : lse2;
     }
     return true;
   });
@@ -1277,7 +1281,7 @@ __device__ void epilogue_role(const Ctx &c, uint32_t tmem, int w, int lane) {
     // commit after the last PV covers every earlier MMA)
     if (!warp_wait(c, &br.o_done[(g - 1) & 1], ((g - 1) >> 1) & 1)) return false;
     tc_fence_after();
-    const float inv = ell > 0.f ? 1.f / ell : 0.f;
+    const float inv = ell != 0.f ? 1.f / ell : 0.f;
     // Split partials are stored chunk-major, [slot][64 chunks of 8 columns]
     // [128 rows][8 floats]: the 32 lanes of a warp (32 consecutive rows)
     // store one chunk as 1 KB of contiguous memory.  The TMEM load of the

@@ -431,7 +431,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) shared_join_kernel(SharedPara
   }
   // nan in any part is nan here (m leaves it out, the sum does not)
   const bool low = m == kAllLow && sum == sum;
-  const float inv = low ? NAN : sum != 0.f ? 1.f / sum : 0.f;
+  const float inv = low ? __uint_as_float(0x7FC00000u) : sum != 0.f ? 1.f / sum : 0.f;
 #pragma unroll
   for (int c = 0; c < kChunks; c++) {
     uint32_t w[4];

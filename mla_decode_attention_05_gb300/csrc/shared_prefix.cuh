@@ -5,11 +5,6 @@
 
 namespace mla {
 
-// A part's base-2 log-sum-exp: -inf says that a row has no keys there, this that all of its keys'
-// scores are -inf, so that the part weighs nothing beside others and a row of nothing
-// else is 0 / 0.  (A sum of nan is the part's log-sum-exp too, and goes on into the result.)
-constexpr float kAllLow = -3.402823466e38f;
-
 // One item of work: up to 128 query rows that lie side by side, and the keys that
 // all of them attend to: a group's rows and its prefix, or the rows of one sequence
 // and its own tokens.

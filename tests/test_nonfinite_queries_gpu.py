@@ -145,3 +145,79 @@ def test_a_row_that_sees_no_key_stays_empty_whatever_its_query(fmt):
     out, lse, mass = x.run(q, causal=True)
     assert not out[0, 0].any() and (lse[0, :, 0] == -INF).all()
     assert torch.isfinite(out[0, 1].float()).all() and torch.isfinite(mass).all()
+
+
+@pytest.mark.parametrize("bad", [NAN, INF])
+@pytest.mark.parametrize("fmt", ["fp8", "fp8_tensor"])
+def test_behind_a_wide_page_table(fmt, bad):
+    x = Batch(704, fmt, [130, 0], [70, 1500], width=1500)
+    base = x.run()
+    for row in ((0, 1, 7), (1, 0, 39)):
+        q = x.q.clone()
+        q[row][17] = bad
+        out, lse = _only_this_row(base, x.run(q), row)
+        assert out.isnan().all() and lse.isnan()
+    if fmt == "fp8":
+        for pages, n in list(zip(x.pre, x.prefixes)) + list(zip(x.mine, x.own)):
+            x.set_dim(pages, n, -HUGE)
+        base, q = x.run(), x.q.clone()
+        q[1, 0, 39, DIM] = HUGE
+        out, lse = _only_this_row(base, x.run(q), (1, 0, 39))
+        assert out.isnan().all() and lse == -INF
+
+
+def _decode(x, q, parts, causal=False, topk=None):
+    import mla_decode_attention_05_gb300 as mla
+    data, scales = x.c.cuda()
+    sk, T, H = i32(x.own), q.shape[1], q.shape[2]
+    md, ns = mla.metadata(sk, H, T, topk=0 if topk is None else topk.shape[2], causal=causal, num_parts=parts)
+    out, lse = mla.decode(q.cuda(), data, table(x.mine), sk, softmax_scale=SCALE, causal=causal, kv_scales=scales,
+                          topk_indices=topk, tile_md=md, num_splits=ns)
+    assert mla.device_status() == 0
+    return out.cpu(), lse.cpu(), ns.cpu()
+
+
+@pytest.mark.parametrize("bad", [NAN, INF])
+@pytest.mark.parametrize("parts", [1, 3, 76])
+@pytest.mark.parametrize("fmt,way", [("bf16", "dense"), ("bf16", "causal"), ("bf16", "topk"), ("bf16", "dual"), ("fp8", "dense"),
+                                     ("fp8", "topk"), ("fp8_tensor", "causal")])
+def test_decode_whole_and_in_parts(fmt, way, parts, bad):
+    import mla_decode_attention_05_gb300 as mla
+    x = Batch(705, fmt, [0, 0], [3000, 90], T=2, H=32 if way == "dual" else 40)
+    topk = None
+    if way == "topk":
+        rng = np.random.default_rng(706)
+        topk = i32([[rng.permutation(n)[:64].tolist() for _ in range(2)] for n in x.own])
+    call = lambda q: _decode(x, q, parts, way == "causal", topk)
+    mla.set_dual_gemm(way == "dual")
+    try:
+        base = call(x.q)
+        if parts == 3 and topk is None:
+            assert (base[2].diff() > 1).any()
+        for row in ((0, 1, 7), (1, 0, 31)):
+            q = x.q.clone()
+            q[row][17] = bad
+            out, lse = _only_this_row(base, call(q), row)
+            assert out.isnan().all() and lse.isnan()
+        if fmt == "fp8_tensor":
+            return
+        for sign in (-1, 1):
+            for pages, n in zip(x.mine, x.own):
+                x.set_dim(pages, n, sign * HUGE)
+            base = call(x.q)
+            for row in ((0, 1, 7), (1, 0, 31)):
+                q = x.q.clone()
+                q[row][DIM] = HUGE
+                out, lse = _only_this_row(base, call(q), row)
+                assert out.isnan().all() and (lse.isnan() if sign > 0 else lse == -INF)
+    finally:
+        mla.set_dual_gemm(False)
+
+
+@pytest.mark.parametrize("parts", [1, 4])
+def test_decode_of_rows_without_keys_whatever_their_queries(parts):
+    x = Batch(707, "bf16", [0, 0], [1, 400], T=2)
+    q = x.q.clone()
+    q[0, 0, 5] = NAN
+    out, lse, _ = _decode(x, q, parts, causal=True)
+    assert not out[0, 0].any() and (lse[0, :, 0] == -INF).all() and torch.isfinite(out[0, 1].float()).all()
