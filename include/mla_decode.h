@@ -29,7 +29,7 @@
  *
  * CUDA graphs: mla_decode_metadata, mla_decode, mla_kv_insert,
  * mla_kv_insert_rope, mla_query_absorb, mla_kv_expand, mla_prefill,
- * mla_value_project, mla_decode_shared, mla_attention_mass and mla_evict can be
+ * mla_value_project, mla_decode_shared (and _bounded), mla_attention_mass and mla_evict can be
  * captured into a CUDA graph on `stream` once the calling thread has made the same
  * kind of call outside capture (the first call does one-time host set-up).  A replay uses the buffers seen at
  * capture and reads their contents at replay time; the split-KV schedule is
@@ -495,8 +495,11 @@ int mla_value_project(const void *attn, int64_t ld_token, int64_t ld_head, const
  * finite, a single scale >= 0.  A page outside the pool is skipped and sets
  * MLA_STATUS_BAD_PAGE.  Of an FP8 cache, prefix pages are widened in the workspace
  * (73728 bytes an entry of prefix_table, with a scale for each 128 values 139264),
- * and own pages too where B * max_pages <= 2048; where it is more, own FP8 rows are
- * rounded to bf16, as mla_decode does.  At most 8192 work items: B * ceil(T * H / 128) +
+ * and own pages too where there is room; where there is none, own FP8 rows are
+ * rounded to bf16, as mla_decode does.  There is room for B * max_pages <= 2048; of
+ * more, with one scale, for the first 2048 pages in use (of cache_seqlens, whatever
+ * max_pages is), and with a scale for each 128 values for none:
+ * mla_decode_shared_bounded makes it.  At most 8192 work items: B * ceil(T * H / 128) +
  * ceil(B * T * H / 128) + G, and 2^30 tiles of 64 keys in the tables' width
  * (MLA_ERR_UNSUPPORTED above).  A wait that gives up sets
  * MLA_STATUS_WAIT_TIMEOUT.  Asynchronous on `stream`; can be captured in a CUDA
@@ -510,6 +513,25 @@ int mla_decode_shared(const void *q, const void *kv_cache, int kv_format, int nu
                       const int32_t *cache_seqlens, const float *kv_scales, float softmax_scale, int causal,
                       void *workspace, size_t workspace_bytes, void *out, float *lse, int B, int T, int H,
                       mla_stream_t stream);
+
+/*
+ * mla_decode_shared with room in the workspace for own_pages widened own pages, so
+ * that what becomes of own FP8 rows goes by the tokens there are and not by the
+ * page table's width: as long as all sequences' own tokens together are in at most
+ * own_pages pages (the sum of ceil(cache_seqlens[b] / 64)), no row is rounded, and
+ * results are the same, bit by bit, for any max_pages and any such own_pages.
+ * Where they are in more, own rows are rounded to bf16.  own_pages >= 0, of
+ * which at most B * max_pages are used (73728 bytes each, with a scale for each 128
+ * values 139264); -1: as mla_decode_shared.  It does not matter for a bf16 cache.
+ */
+size_t mla_decode_shared_bounded_workspace_bytes(int B, int T, int H, int G, int kv_format, int max_prefix_pages,
+                                                 int max_pages, int own_pages);
+int mla_decode_shared_bounded(const void *q, const void *kv_cache, int kv_format, int num_pages, int page_size,
+                              const int32_t *prefix_table, int max_prefix_pages, const int32_t *prefix_lens,
+                              const int32_t *group_offsets, int G, const int32_t *block_table, int max_pages,
+                              const int32_t *cache_seqlens, int own_pages, const float *kv_scales,
+                              float softmax_scale, int causal, void *workspace, size_t workspace_bytes, void *out,
+                              float *lse, int B, int T, int H, mla_stream_t stream);
 
 /*
  * The attention weight of every cached token, added to a running sum:

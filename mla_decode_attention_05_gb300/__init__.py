@@ -27,6 +27,7 @@ the most of it, the first and the latest.
 from __future__ import annotations
 
 import ctypes
+import operator
 import os
 import threading
 from typing import Optional
@@ -98,6 +99,10 @@ def lib():
                                             i, i, i, P]
             L.mla_decode_shared_workspace_bytes.argtypes = [i, i, i, i, i, i, i]
             L.mla_decode_shared_workspace_bytes.restype = sz
+            L.mla_decode_shared_bounded.argtypes = [P, P, i, i, i, P, i, P, P, i, P, i, P, i, P, ctypes.c_float, i, P, sz, P, P,
+                                                    i, i, i, P]
+            L.mla_decode_shared_bounded_workspace_bytes.argtypes = [i, i, i, i, i, i, i, i]
+            L.mla_decode_shared_bounded_workspace_bytes.restype = sz
             L.mla_attention_mass.argtypes = [P, P, i, i, i, P, i, P, P, P, ctypes.c_float, i, ctypes.c_float, P, i, P, sz,
                                              i, i, i, P]
             L.mla_attention_mass_workspace_bytes.argtypes = [i, i, i, i]
@@ -140,7 +145,7 @@ def _load_fast(L) -> None:
         return
     m.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
         L.mla_kv_insert_rope, L.mla_kv_expand, L.mla_prefill, L.mla_prefill_workspace_bytes, L.mla_value_project,
-        L.mla_decode_shared, L.mla_decode_shared_workspace_bytes, L.mla_attention_mass, L.mla_attention_mass_workspace_bytes,
+        L.mla_decode_shared_bounded, L.mla_decode_shared_bounded_workspace_bytes, L.mla_attention_mass, L.mla_attention_mass_workspace_bytes,
         L.mla_evict, L.mla_evict_workspace_bytes)))
     _fast = m
 
@@ -718,7 +723,8 @@ def decode_shared(q: torch.Tensor, kv_cache: torch.Tensor, prefix_table: torch.T
                   block_table: torch.Tensor, cache_seqlens: torch.Tensor, *, softmax_scale: float,
                   group_offsets: Optional[torch.Tensor] = None, causal: bool = False,
                   kv_scales: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
-                  out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None):
+                  out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                  own_pages: Optional[int] = None):
     """decode() of a batch whose sequences share prefixes, on the current stream
     (mla_decode_shared) -> (out bf16 [B,T,H,512], lse fp32 [B,H,T]).
 
@@ -728,10 +734,16 @@ def decode_shared(q: torch.Tensor, kv_cache: torch.Tensor, prefix_table: torch.T
     have no prefix.  block_table and cache_seqlens are of each sequence's own
     tokens, which follow its prefix; causal applies to them.  The other
     arguments are decode()'s.  workspace: at least
-    decode_shared_workspace_bytes() bytes (allocated here when not given)."""
+    decode_shared_workspace_bytes() bytes (allocated here when not given).
+
+    own_pages: how many pages the sequences' own tokens are in, at most (the sum
+    of ceil(cache_seqlens / 64)).  Of an FP8 cache with a block_table of more
+    than 2048 entries, own rows are rounded to bf16 without it, and only where
+    they are in more pages with it (mla_decode_shared_bounded)."""
+    own_pages = -1 if own_pages is None else _bound(own_pages)
     if _fast is not None:
         r = _fast.decode_shared(q, kv_cache, prefix_table, prefix_lens, block_table, cache_seqlens, softmax_scale,
-                                group_offsets, causal, kv_scales, workspace, out, lse)
+                                group_offsets, causal, kv_scales, workspace, out, lse, own_pages)
         if r is not None:
             return r if type(r) is tuple else _check(r)
     dev, B, T, H, fmt, _ = _decode_args(q, kv_cache, block_table, cache_seqlens, None, kv_scales)
@@ -757,24 +769,34 @@ def decode_shared(q: torch.Tensor, kv_cache: torch.Tensor, prefix_table: torch.T
     if tuple(out.shape) != (B, T, H, D_V) or tuple(lse.shape) != (B, H, T):
         raise ValueError(f"out must be [{B}, {T}, {H}, {D_V}] and lse [{B}, {H}, {T}]")
     if workspace is None:
-        workspace = torch.empty(decode_shared_workspace_bytes(B, T, H, G, fmt, width, block_table.shape[1], dev), dtype=torch.uint8, device=dev)
+        workspace = torch.empty(decode_shared_workspace_bytes(B, T, H, G, fmt, width, block_table.shape[1], dev,
+                                                              None if own_pages < 0 else own_pages),
+                                dtype=torch.uint8, device=dev)
     _need(workspace, "workspace", workspace.dtype, dev)
-    _call("mla_decode_shared", dev, q.data_ptr(), kv_cache.data_ptr(), fmt, kv_cache.shape[0], kv_cache.shape[1],
+    _call("mla_decode_shared_bounded", dev, q.data_ptr(), kv_cache.data_ptr(), fmt, kv_cache.shape[0], kv_cache.shape[1],
           prefix_table.data_ptr(), width, prefix_lens.data_ptr(), _at(group_offsets), G, block_table.data_ptr(),
-          block_table.shape[1], cache_seqlens.data_ptr(), _at(kv_scales) if fmt != KV_BF16 else None,
+          block_table.shape[1], cache_seqlens.data_ptr(), own_pages, _at(kv_scales) if fmt != KV_BF16 else None,
           float(softmax_scale), int(bool(causal)), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
           out.data_ptr(), lse.data_ptr(), B, T, H)
     return out, lse
 
 
+def _bound(own_pages) -> int:
+    n = operator.index(own_pages)
+    if n < 0:
+        raise ValueError("own_pages must be >= 0 (None: no bound)")
+    return min(n, 0x7FFFFFFF)
+
+
 def decode_shared_workspace_bytes(B: int, T: int, H: int, G: int, kv_format: int, max_prefix_pages: int,
-                                  max_pages: int, device=None) -> int:
+                                  max_pages: int, device=None, own_pages: Optional[int] = None) -> int:
     """Workspace of decode_shared() for B sequences in G groups (kv_format:
     KV_BF16, KV_FP8_E4M3 or KV_FP8_E4M3_TENSOR) whose page tables have
     max_prefix_pages and max_pages columns, on `device` (default: the current
-    one)."""
+    one), with the same own_pages."""
     with torch.cuda.device(device if device is not None else torch.cuda.current_device()):
-        n = int(lib().mla_decode_shared_workspace_bytes(B, T, H, G, kv_format, max_prefix_pages, max_pages))
+        n = int(lib().mla_decode_shared_bounded_workspace_bytes(B, T, H, G, kv_format, max_prefix_pages, max_pages,
+                                                                -1 if own_pages is None else _bound(own_pages)))
     if n == 0:
         raise MlaError(-1, lib().mla_last_error_string().decode())
     return n

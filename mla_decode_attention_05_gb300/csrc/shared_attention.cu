@@ -142,7 +142,7 @@ constexpr uint32_t kTileStages = kScaled ? 2 : 1;
 // rank 0's ring carries, per piece, the query rows (one stage for 64 rows) before the keys.
 __device__ __forceinline__ int q_stages(const SharedItem &it) { return it.rows > 64 ? 2 : 1; }
 
-// (A widened page lies at its entry's place among the tables' entries.)
+// (Widened pages lie side by side, a table row's behind those of the rows before it.)
 __device__ __forceinline__ int page_of(const SharedParams &p, const SharedItem &it, int tile) {
   const int width = it.own ? p.max_pages : p.max_prefix;
   const int page = __ldg((it.own ? p.block_table : p.prefix_table) + (size_t)it.src * width + tile);
@@ -150,7 +150,7 @@ __device__ __forceinline__ int page_of(const SharedParams &p, const SharedItem &
     atomicOr(p.status, MLA_STATUS_BAD_PAGE);
     return -1;
   }
-  return p.format == MLA_KV_BF16 ? page : (it.own ? p.G * p.max_prefix : 0) + it.src * width + tile;
+  return p.format == MLA_KV_BF16 ? page : __ldg(p.first + (it.own ? p.G : 0) + it.src) + tile;
 }
 
 // ---- warp 0: loads --------------------------------------------------------------------

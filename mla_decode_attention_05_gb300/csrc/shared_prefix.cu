@@ -187,15 +187,15 @@ __device__ __forceinline__ int own_keys(const SharedParams &p, int n, int mt) {
 }
 
 // Block 0: the items of shared_attention_kernel, prefixes first, and their
-// schedule.  Block 1 (FP8): the decode kernel's schedule of the own tokens, with room for two pieces
-// of every item, so that it writes all its results as partials.
+// schedule.  Block 1 (FP8): where widened pages lie.  Block 2 (FP8, where own pages in use may be more
+// than there is room for): the decode kernel's schedule of the own tokens, with room for two pieces
+// of every item, so that it writes all its results as partials; an empty one where there is room.
 template <int kSchedThreads>
 __global__ void __launch_bounds__(kSchedThreads) shared_schedule_kernel(SharedParams p) {
   __shared__ SchedShared sh;
   const int tid = threadIdx.x, TH = p.T * p.H;
   grid_dep_trigger();
   grid_dep_wait();
-  const bool apart = p.md_o != nullptr;  // own tokens go another way
   auto length = [&](int n, int pages) {
     const int most = pages > 0x7fffffff / PAGE ? 0x7fffffff : pages * PAGE;
     if (n < 0 || n > most) atomicOr(p.status, MLA_STATUS_BAD_SEQLEN);
@@ -203,7 +203,43 @@ __global__ void __launch_bounds__(kSchedThreads) shared_schedule_kernel(SharedPa
   };
   const bool near_by = p.B <= kFewThreads;
   if (near_by && tid < p.B) sh.lens[tid] = p.seqlens[tid];  // (seen behind the groups' barriers)
+  bool apart = false;  // own tokens go another way: their pages in use are more than there is room for
+  if (p.md_o) {
+    int pages = 0;
+    for (int b = tid; b < p.B; b += kSchedThreads) pages += ceil_div(length(p.seqlens[b], p.max_pages), PAGE);
+    pages = block_scan<kSchedThreads>(pages, sh.warp_sums, Add());
+    if (tid == kSchedThreads - 1) sh.top = pages;
+    __syncthreads();
+    apart = sh.top > p.own_room;
+    __syncthreads();
+  }
   if (blockIdx.x == 1) {
+    if (tid == 0) {
+      sh.carry = 0;
+      p.first[0] = 0;
+    }
+    __syncthreads();
+    for (int base = 0; base < p.G + p.B; base += kSchedThreads) {
+      const int y = base + tid;
+      int pages = 0;
+      if (y < p.G) pages = ceil_div(length(p.prefix_lens[y], p.max_prefix), PAGE);
+      else if (y < p.G + p.B && !apart) pages = ceil_div(length(p.seqlens[y - p.G], p.max_pages), PAGE);
+      const int incl = block_scan<kSchedThreads>(pages, sh.warp_sums, Add()) + sh.carry;
+      if (y < p.G + p.B) p.first[y + 1] = incl;
+      __syncthreads();
+      if (tid == kSchedThreads - 1) sh.carry = incl;
+      __syncthreads();
+    }
+    return;
+  }
+  if (blockIdx.x == 2) {
+    if (!apart) {
+      for (int w = tid; w < p.parts; w += kSchedThreads) {
+        reinterpret_cast<int4 *>(p.md_o)[2 * w] = make_int4(p.B * p.n_mt, 0, p.B * p.n_mt - 1, 0);
+        reinterpret_cast<int4 *>(p.md_o)[2 * w + 1] = make_int4(0, 0, 0, 0);
+      }
+      return;
+    }
     for (int b = tid; b < p.B; b += kSchedThreads) p.lens_o[b] = length(p.seqlens[b], p.max_pages);
     __syncthreads();
     schedule<kSchedThreads>(sh, p.B * p.n_mt, p.parts, 2, p.md_o, p.cnt_o, Kinds{0, 0, 0},
@@ -248,7 +284,10 @@ __global__ void __launch_bounds__(kSchedThreads) shared_schedule_kernel(SharedPa
     __syncthreads();
   }
   const int n_prefix = sh.carry, n_items = n_prefix + (apart ? 0 : p.B * p.n_mt);
-  if (tid == 0) *p.n_prefix = n_prefix;
+  if (tid == 0) {
+    *p.n_prefix = n_prefix;
+    if (p.md_o) *p.apart = apart;
+  }
   __syncthreads();
   for (int b = tid; b < p.B; b += kSchedThreads) {
     const int4 g = groups[last_le(p.G, b, [&](int i) { return i == 0 ? 0 : groups[i].x; })];
@@ -282,9 +321,28 @@ __host__ __device__ constexpr size_t wide_page_bytes(int format) {
 
 constexpr int kWidenParts = 2;
 
-// FP8: page j of table row y as bf16 rows (zeros behind the last token), once for all the
-// tiles that read it: prefixes first, then own pages where there is room for them.  Block z has
-// one of kWidenParts parts of a page's rows (FP8 groups of 48 sequences, 477 pages on 152 SMs:
+// The last i in [0, n) with first[i] <= x (first[0] <= x, nondecreasing), found by a whole warp,
+// 256 entries at once.
+__device__ __forceinline__ int warp_last_le(const int32_t *first, int n, int x) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0;
+  while (n > 1) {
+    const int step = ceil_div(n, 256);
+    int count = 0;
+#pragma unroll
+    for (int k = 0; k < 8; k++) {
+      const int i = (32 * k + lane) * step;
+      count += __popc(__ballot_sync(0xffffffffu, i < n && first[lo + i] <= x));
+    }
+    lo += (count - 1) * step;
+    n = min(step, n - (count - 1) * step);
+  }
+  return lo;
+}
+
+// FP8: the pages in use as bf16 rows (zeros behind the last token), once for all the
+// tiles that read them: prefixes first, then own pages where there is room for them.  A block takes
+// one of kWidenParts parts of a page's rows at a time (FP8 groups of 48 sequences, 477 pages on 152 SMs:
 // 170.4 us with halves, 174.5 with whole pages, 172.1 with quarters).  A warp a row: lane l widens 16 of its
 // values, and lanes 0-3 or 0-7 the rotated part.  With one scale the codes as they are; with a
 // scale for each 128 values as sums of two values, the second ones behind the row's first.
@@ -292,23 +350,22 @@ template <bool kScaled>
 __global__ void __launch_bounds__(256) shared_widen_kernel(SharedParams p) {
   grid_dep_trigger();
   grid_dep_wait();
-  const bool own = (int)blockIdx.y >= p.G;
-  const int row = own ? blockIdx.y - p.G : blockIdx.y, width = own ? p.max_pages : p.max_prefix;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int n = (int)min((long long)max((own ? p.seqlens : p.prefix_lens)[row], 0), (long long)width * PAGE);
-  const int32_t *table = (own ? p.block_table : p.prefix_table) + (size_t)row * width;
-  const size_t first = (own ? (size_t)p.G * p.max_prefix : 0) + (size_t)row * width;
+  const long long units = (long long)p.first[p.G + p.B] * kWidenParts;
   constexpr int kRowBytes = kScaled ? FP8_ROW : D_QK, kRows = PAGE / 8 / kWidenParts;
   constexpr int kPieces = (kScaled ? D_QK + D_V : D_QK) / 8;  // 16-byte pieces of a widened row
   const uint4 zero = make_uint4(0, 0, 0, 0);
-  for (int j = blockIdx.x; (long long)j * PAGE < n; j += gridDim.x) {
-    const int page = table[j];
+  for (long long u = blockIdx.x; u < units; u += gridDim.x) {
+    const int at_page = (int)(u / kWidenParts), y = warp_last_le(p.first, p.G + p.B, at_page), j = at_page - p.first[y];
+    const bool own = y >= p.G;
+    const int row = own ? y - p.G : y, width = own ? p.max_pages : p.max_prefix;
+    const int page = (own ? p.block_table : p.prefix_table)[(size_t)row * width + j];
     if (page < 0 || page >= p.num_pages) continue;
-    const int tokens = min(PAGE, n - j * PAGE);
-    uint4 *to = reinterpret_cast<uint4 *>(p.scratch + (first + j) * wide_page_bytes(p.format));
+    const int tokens = (int)min((long long)PAGE, (long long)(own ? p.seqlens : p.prefix_lens)[row] - (long long)j * PAGE);
+    uint4 *to = reinterpret_cast<uint4 *>(p.scratch + (size_t)at_page * wide_page_bytes(p.format));
 #pragma unroll
     for (int i = 0; i < kRows; i++) {
-      const int r = blockIdx.z * (PAGE / kWidenParts) + warp + 8 * i;
+      const int r = (int)(u % kWidenParts) * (PAGE / kWidenParts) + warp + 8 * i;
       const size_t at = (size_t)page * PAGE + r;
       const uint4 *src = reinterpret_cast<const uint4 *>(p.cache + at * kRowBytes);
       uint4 *dst = to + r * kPieces;
@@ -359,7 +416,7 @@ template <int kChunks>
 __global__ void __launch_bounds__(kJoinWarps * 32) shared_join_kernel(SharedParams p) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, TH = p.T * p.H;
   const int R = blockIdx.x * 32 + lane, chunk = (blockIdx.y * kJoinWarps + warp) * kChunks;
-  const bool live = R < p.B * TH, apart = p.md_o != nullptr;
+  const bool live = R < p.B * TH, apart = p.md_o && *p.apart;
   const int b = live ? R / TH : 0, r = live ? R % TH : 0;
   const float *lse[2] = {p.lse_p, p.lse_p}, *o[2] = {p.o_p, p.o_p};
   int n[2] = {0, 0};
@@ -449,34 +506,48 @@ __global__ void __launch_bounds__(kJoinWarps * 32) shared_join_kernel(SharedPara
 // ---- host ------------------------------------------------------------------------
 
 struct Layout {
-  size_t items, md, pieces, n_prefix, groups, lens_o, seq, md_o, ns_o, cnt_o, scratch, lse_p, o_p, lse_o, o_o, ring, total;
+  size_t items, md, pieces, n_prefix, groups, lens_o, seq, md_o, ns_o, cnt_o, apart, first, scratch, lse_p, o_p, lse_o, o_o, ring, total;
   size_t pages;
-  int room, n_mt;
-  bool apart;  // own FP8 tokens go through the decode kernel
+  int room, own_room, n_mt;
+  bool maybe_apart;  // own FP8 tokens go through the decode kernel where their pages in use exceed own_room
 };
 
-// Own FP8 pages are widened along with the prefixes' where the page table has at
-// most this many entries (151 MB of workspace, 285 MB with scales).  Otherwise they go through
-// the decode kernel's gather, which needs no such room but rounds rows to bf16; with one scale, 48
-// sequences of up to 300 tokens, four query tokens, 64 heads take 155 us that way, 120 us this way.
+// Room for widened own FP8 pages where the caller gives no bound (151 MB of workspace, 285 MB with
+// scales).  Own tokens of more pages go through the decode kernel's gather, which needs no room but
+// rounds rows to bf16 and takes longer: 48 sequences of up to 300 tokens, four query tokens, 64 heads
+// 135 us that way and 105 this way with one scale, 175 and 147 with a scale for each 128 values; 16 of up to
+// 8000 tokens, one query token, 128 heads 142 and 81, 152 and 121.  (Where a table is wider than the room, the decode
+// kernel is launched with nothing to do, which takes 6 to 8 us.)
 constexpr long long kMostOwnPages = 2048;
 
-Layout layout(int B, int T, int H, int G, int format, int max_prefix, int max_pages, int parts) {
-  const bool wide = format != MLA_KV_BF16, apart = wide && (long long)B * max_pages > kMostOwnPages;
+// Room for B * max_pages = `entries` own pages at most.  Without a bound (-1) rows with a scale for each 128
+// values have room for a whole table or none: their results with a wide table are those of rounded rows.
+int own_room_of(int format, long long entries, int bound) {
+  if (format == MLA_KV_BF16) return 0;
+  if (bound >= 0) return (int)(bound < entries ? bound : entries);
+  if (entries <= kMostOwnPages) return (int)entries;
+  return format == MLA_KV_FP8_E4M3_TENSOR ? (int)kMostOwnPages : 0;
+}
+
+Layout layout(int B, int T, int H, int G, int format, int max_prefix, int max_pages, int bound, int parts) {
+  const bool wide = format != MLA_KV_BF16;
+  const long long entries = (long long)B * max_pages;
   Layout l;
   l.n_mt = ceil_div(T * H, M_TILE);
-  l.apart = apart;
+  l.own_room = own_room_of(format, entries, bound);
+  const bool apart = l.maybe_apart = wide && l.own_room < entries;
   const size_t own = (size_t)B * l.n_mt, prefix = ((size_t)B * T * H + M_TILE - 1) / M_TILE + G;
-  l.room = (int)(prefix + (apart ? 0 : own));
-  l.pages = wide ? (size_t)G * max_prefix + (apart ? 0 : (size_t)B * max_pages) : 0;
+  l.room = (int)(prefix + own);
+  l.pages = wide ? (size_t)G * max_prefix + l.own_room : 0;
   size_t at = 0;
   auto take = [&](size_t bytes) {
     const size_t here = at;
     at = (at + bytes + 255) / 256 * 256;
     return here;
   };
-  // slots of results: one for each item, and one for each cut
-  const size_t slots = (size_t)l.room + parts, slots_o = apart ? 2 * own + parts : 0, row = M_TILE * sizeof(float);
+  // slots of results: one for each item, and one for each cut.  Those of the decode kernel lie behind the
+  // prefixes', where the own tokens' are otherwise.
+  const size_t slots_p = prefix + parts, slots = slots_p + (apart ? 2 * own + parts : own), row = M_TILE * sizeof(float);
   l.items = take((size_t)l.room * sizeof(SharedItem));
   l.md = take((size_t)parts * MD_STRIDE * 4);
   l.pieces = take((size_t)l.room * 4);
@@ -487,11 +558,13 @@ Layout layout(int B, int T, int H, int G, int format, int max_prefix, int max_pa
   l.md_o = take(apart ? (size_t)parts * MD_STRIDE * 4 : 0);
   l.ns_o = take(apart ? (own + 1) * 4 : 0);
   l.cnt_o = take(apart ? own * 4 : 0);
+  l.apart = take(apart ? 4 : 0);
+  l.first = take(wide ? ((size_t)G + B + 1) * 4 : 0);
   l.scratch = take(l.pages * wide_page_bytes(format));
   l.lse_p = take(slots * row);
   l.o_p = take(slots * row * D_V);
-  l.lse_o = take(slots_o * row);
-  l.o_o = take(slots_o * row * D_V);
+  l.lse_o = l.lse_p + slots_p * row;
+  l.o_o = l.o_p + slots_p * row * D_V;
   l.ring = take((size_t)parts * P_RING * P_SLOT_BYTES);
   l.total = at;
   return l;
@@ -502,7 +575,7 @@ int fail(int code, const char *msg) {
   return code;
 }
 
-int check_sizes(int B, int T, int H, int G, int format, int max_prefix, int max_pages) {
+int check_sizes(int B, int T, int H, int G, int format, int max_prefix, int max_pages, int bound) {
   char msg[160];
   if (B < 1 || G < 1 || max_prefix < 1 || max_pages < 1) {
     snprintf(msg, sizeof msg, "B = %d, G = %d, max_prefix_pages = %d and max_pages = %d must be >= 1", B, G, max_prefix, max_pages);
@@ -514,15 +587,15 @@ int check_sizes(int B, int T, int H, int G, int format, int max_prefix, int max_
   }
   if (format != MLA_KV_BF16 && format != MLA_KV_FP8_E4M3 && format != MLA_KV_FP8_E4M3_TENSOR)
     return fail(MLA_ERR_INVALID_ARG, "kv_format unknown");
+  if (bound < -1) return fail(MLA_ERR_INVALID_ARG, "own_pages must be >= 0, or -1 for no bound");
   const long long items = (long long)B * ceil_div(T * H, M_TILE) + ((long long)B * T * H + M_TILE - 1) / M_TILE + G;
   if (items > kMaxItems) {
     snprintf(msg, sizeof msg, "%lld work items exceed the limit %d", items, kMaxItems);
     return fail(MLA_ERR_UNSUPPORTED, msg);
   }
-  // (the schedule counts tiles in 32 bits)
+  // (the schedule counts tiles in 32 bits, and so are widened pages, of which there are no more)
   const long long tiles = (long long)B * ceil_div(T * H, M_TILE) * max_pages + (((long long)B * T * H + M_TILE - 1) / M_TILE + G) * max_prefix;
   if (tiles > 0x3fffffffLL) return fail(MLA_ERR_UNSUPPORTED, "more than 2^30 tiles of 64 keys in max_pages and max_prefix_pages");
-  if ((long long)G * max_prefix > 0x7fffffffLL) return fail(MLA_ERR_UNSUPPORTED, "G * max_prefix_pages exceeds 2^31 - 1");
   return MLA_OK;
 }
 
@@ -542,9 +615,7 @@ using namespace mla;
 
 extern "C" size_t mla_decode_shared_workspace_bytes(int B, int T, int H, int G, int kv_format, int max_prefix_pages,
                                                     int max_pages) {
-  int parts = 0;
-  if (check_sizes(B, T, H, G, kv_format, max_prefix_pages, max_pages) != MLA_OK || device_parts(&parts) != MLA_OK) return 0;
-  return layout(B, T, H, G, kv_format, max_prefix_pages, max_pages, parts).total;
+  return mla_decode_shared_bounded_workspace_bytes(B, T, H, G, kv_format, max_prefix_pages, max_pages, -1);
 }
 
 extern "C" int mla_decode_shared(const void *q, const void *kv_cache, int kv_format, int num_pages, int page_size,
@@ -553,7 +624,26 @@ extern "C" int mla_decode_shared(const void *q, const void *kv_cache, int kv_for
                                  const int32_t *cache_seqlens, const float *kv_scales, float softmax_scale, int causal,
                                  void *workspace, size_t workspace_bytes, void *out, float *lse, int B, int T, int H,
                                  mla_stream_t stream) {
-  int rc = check_sizes(B, T, H, G, kv_format, max_prefix_pages, max_pages);
+  return mla_decode_shared_bounded(q, kv_cache, kv_format, num_pages, page_size, prefix_table, max_prefix_pages, prefix_lens,
+                                   group_offsets, G, block_table, max_pages, cache_seqlens, -1, kv_scales, softmax_scale,
+                                   causal, workspace, workspace_bytes, out, lse, B, T, H, stream);
+}
+
+extern "C" size_t mla_decode_shared_bounded_workspace_bytes(int B, int T, int H, int G, int kv_format, int max_prefix_pages,
+                                                            int max_pages, int own_pages) {
+  int parts = 0;
+  if (check_sizes(B, T, H, G, kv_format, max_prefix_pages, max_pages, own_pages) != MLA_OK || device_parts(&parts) != MLA_OK)
+    return 0;
+  return layout(B, T, H, G, kv_format, max_prefix_pages, max_pages, own_pages, parts).total;
+}
+
+extern "C" int mla_decode_shared_bounded(const void *q, const void *kv_cache, int kv_format, int num_pages, int page_size,
+                                         const int32_t *prefix_table, int max_prefix_pages, const int32_t *prefix_lens,
+                                         const int32_t *group_offsets, int G, const int32_t *block_table, int max_pages,
+                                         const int32_t *cache_seqlens, int own_pages, const float *kv_scales,
+                                         float softmax_scale, int causal, void *workspace, size_t workspace_bytes, void *out,
+                                         float *lse, int B, int T, int H, mla_stream_t stream) {
+  int rc = check_sizes(B, T, H, G, kv_format, max_prefix_pages, max_pages, own_pages);
   if (rc != MLA_OK) return rc;
   if (!q || !kv_cache || !prefix_table || !prefix_lens || !block_table || !cache_seqlens || !out || !lse)
     return fail(MLA_ERR_INVALID_ARG, "null pointer argument");
@@ -573,7 +663,7 @@ extern "C" int mla_decode_shared(const void *q, const void *kv_cache, int kv_for
   int parts = 0;
   if ((rc = device_parts(&parts)) != MLA_OK) return rc;
   if (parts > kMostParts) return fail(MLA_ERR_UNSUPPORTED, "more SMs than the schedule has room for");
-  const Layout l = layout(B, T, H, G, kv_format, max_prefix_pages, max_pages, parts);
+  const Layout l = layout(B, T, H, G, kv_format, max_prefix_pages, max_pages, own_pages, parts);
   if (!workspace || workspace_bytes < l.total) {
     char msg[96];
     snprintf(msg, sizeof msg, "workspace needs %zu bytes, got %zu", l.total, workspace_bytes);
@@ -605,6 +695,7 @@ extern "C" int mla_decode_shared(const void *q, const void *kv_cache, int kv_for
   p.H = H;
   p.causal = causal;
   p.room = l.room;
+  p.own_room = l.own_room;
   p.n_mt = l.n_mt;
   p.parts = parts;
   p.scale_log2 = softmax_scale * LOG2E;
@@ -616,9 +707,11 @@ extern "C" int mla_decode_shared(const void *q, const void *kv_cache, int kv_for
   p.groups = reinterpret_cast<int4 *>(at(l.groups));
   p.lens_o = reinterpret_cast<int32_t *>(at(l.lens_o));
   p.seq = reinterpret_cast<int2 *>(at(l.seq));
-  p.md_o = l.apart ? reinterpret_cast<int32_t *>(at(l.md_o)) : nullptr;
-  p.ns_o = l.apart ? reinterpret_cast<int32_t *>(at(l.ns_o)) : nullptr;
-  p.cnt_o = l.apart ? reinterpret_cast<int32_t *>(at(l.cnt_o)) : nullptr;
+  p.md_o = l.maybe_apart ? reinterpret_cast<int32_t *>(at(l.md_o)) : nullptr;
+  p.ns_o = reinterpret_cast<int32_t *>(at(l.ns_o));
+  p.cnt_o = reinterpret_cast<int32_t *>(at(l.cnt_o));
+  p.apart = reinterpret_cast<int32_t *>(at(l.apart));
+  p.first = reinterpret_cast<int32_t *>(at(l.first));
   p.scratch = at(l.scratch);
   p.lse_p = reinterpret_cast<float *>(at(l.lse_p));
   p.o_p = reinterpret_cast<float *>(at(l.o_p));
@@ -641,16 +734,18 @@ extern "C" int mla_decode_shared(const void *q, const void *kv_cache, int kv_for
   cfg.numAttrs = 1;
   // (few threads meet sooner)
   const bool small = l.room <= kFewThreads && B <= kFewThreads && G <= kFewThreads && parts < kFewThreads;
-  cudaError_t e = small ? launch_dependent(shared_schedule_kernel<kFewThreads>, l.apart ? 2 : 1, kFewThreads, 0, s, p)
-                        : launch_dependent(shared_schedule_kernel<1024>, l.apart ? 2 : 1, 1024, 0, s, p);
+  const unsigned blocks_s = !wide ? 1 : l.maybe_apart ? 3 : 2;
+  cudaError_t e = small ? launch_dependent(shared_schedule_kernel<kFewThreads>, blocks_s, kFewThreads, 0, s, p)
+                        : launch_dependent(shared_schedule_kernel<1024>, blocks_s, 1024, 0, s, p);
   if (e == cudaSuccess && wide) {
-    const int longest = l.apart || max_prefix_pages > max_pages ? max_prefix_pages : max_pages;
-    cfg.gridDim = dim3(longest < 1024 ? longest : 1024, l.apart ? G : G + B, kWidenParts);
+    // as many blocks as an SM holds (44 registers a thread), or as there can be parts of pages
+    const long long most = (long long)l.pages * kWidenParts, held = 2ll * parts * 5;
+    cfg.gridDim = dim3((unsigned)(most < held ? most : held));
     e = cudaLaunchKernelEx(&cfg, kv_format == MLA_KV_FP8_E4M3 ? shared_widen_kernel<true> : shared_widen_kernel<false>, p);
   }
   if (e == cudaSuccess) e = launch_shared_attention(p, s);
-  if (e == cudaSuccess && l.apart) {
-    // own FP8 rows go through the decode kernel, which gathers and widens them
+  if (e == cudaSuccess && l.maybe_apart) {
+    // own FP8 rows that there is no room for go through the decode kernel, which gathers and widens them
     DecodeParams d{};
     d.q = p.q;
     d.kv = p.cache;

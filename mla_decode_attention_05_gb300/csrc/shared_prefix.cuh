@@ -29,6 +29,7 @@ struct SharedParams {
   unsigned int *status;
   int format, num_pages, max_prefix, max_pages, G, B, T, H, causal;
   int room;       // room for items
+  int own_room;   // FP8: room for widened own pages
   int n_mt;       // own tiles of query rows of a sequence
   int parts;
   float scale_log2;
@@ -41,8 +42,10 @@ struct SharedParams {
   int4 *groups;        // [G] {first sequence, end, first item, keys}
   int2 *seq;           // [B] {first prefix item of its group or -1, its first row among the group's}
   int32_t *lens_o;     // [B] own tokens, clamped, where they
-  int32_t *md_o, *ns_o, *cnt_o;  // go through the decode kernel: its schedule (else null)
-  uint8_t *scratch;    // FP8: pages as bf16, G * max_prefix and B * max_pages: [64][576], with scales [64][1088]
+  int32_t *md_o, *ns_o, *cnt_o;  // may go through the decode kernel: its schedule (else null)
+  int32_t *apart;      // with md_o: whether they do
+  int32_t *first;      // FP8: [G + B + 1] widened pages of the prefixes and sequences before each
+  uint8_t *scratch;    // FP8: pages as bf16, those in use side by side: [64][576], with scales [64][1088]
   size_t scratch_pages;
   float *lse_p, *o_p;  // partial results: base-2 log-sum-exp [slots][128] and output [slots][64][128][8]
   float *lse_o, *o_o;  // those of the decode kernel

@@ -25,8 +25,8 @@ decltype(&mla_kv_expand) expand_fn;
 decltype(&mla_prefill) prefill_fn;
 decltype(&mla_prefill_workspace_bytes) prefill_ws_fn;
 decltype(&mla_value_project) value_fn;
-decltype(&mla_decode_shared) shared_fn;
-decltype(&mla_decode_shared_workspace_bytes) shared_ws_fn;
+decltype(&mla_decode_shared_bounded) shared_fn;
+decltype(&mla_decode_shared_bounded_workspace_bytes) shared_ws_fn;
 decltype(&mla_attention_mass) mass_fn;
 decltype(&mla_attention_mass_workspace_bytes) mass_ws_fn;
 decltype(&mla_evict) evict_fn;
@@ -324,12 +324,14 @@ void *make_space(const at::Tensor *space, const at::Tensor &like, size_t &bytes,
 }
 
 // decode_shared(q, cache, prefix_table, prefix_lens, table, lens, scale, offsets | None, causal, scales | None,
-//               workspace | None, out | None, lse | None) -> (out, lse)
+//               workspace | None, out | None, lse | None, own_pages) -> (out, lse)
 PyObject *decode_shared(PyObject *, PyObject *const *args, Py_ssize_t n) {
-  if (n != 13 || !shared_fn || !PyFloat_CheckExact(args[6]) || !PyBool_Check(args[8])) return none();
+  if (n != 14 || !shared_fn || !PyFloat_CheckExact(args[6]) || !PyBool_Check(args[8])) return none();
   const at::Tensor *q = tensor(args[0]), *pt = tensor(args[2]), *pl = tensor(args[3]), *off, *space, *out_given, *lse_given;
   Paged c;
   int64_t T, H;
+  int bound;
+  if (!whole_number(args[13], bound)) return none();
   if (!q || !optional(args[7], off) || !optional(args[10], space) || !optional(args[11], out_given) ||
       !optional(args[12], lse_given) || !paged(args[1], args[4], args[5], args[9], c) || !queries(q, c, T, H))
     return none();
@@ -346,13 +348,13 @@ PyObject *decode_shared(PyObject *, PyObject *const *args, Py_ssize_t n) {
   int rc;
   {
     Unlocked others;
-    size_t bytes = shared_ws_fn((int)c.B, (int)T, (int)H, (int)G, c.format, (int)pt->size(1), c.width);  // (0: refused below)
+    size_t bytes = shared_ws_fn((int)c.B, (int)T, (int)H, (int)G, c.format, (int)pt->size(1), c.width, bound);  // (0: refused below)
     out = out_given ? *out_given : at::empty({c.B, T, H, 512}, q->options());
     lse = lse_given ? *lse_given : at::empty({c.B, H, T}, q->options().dtype(at::kFloat));
     void *at = make_space(space, *q, bytes, room);
     rc = shared_fn(q->data_ptr(), c.cache->data_ptr(), c.format, c.pages, c.page, pt->data_ptr<int32_t>(), (int)pt->size(1),
                    pl->data_ptr<int32_t>(), off ? off->data_ptr<int32_t>() : nullptr, (int)G, c.table->data_ptr<int32_t>(),
-                   c.width, c.lens->data_ptr<int32_t>(), scales_of(c), scale, causal, at, bytes, out.data_ptr(),
+                   c.width, c.lens->data_ptr<int32_t>(), bound, scales_of(c), scale, causal, at, bytes, out.data_ptr(),
                    lse.data_ptr<float>(), (int)c.B, (int)T, (int)H, stream_of(c.dev));
   }
   return rc < 0 ? code(rc) : pair(out, lse);
