@@ -5,6 +5,7 @@ import pytest
 import torch
 
 from _long import Cache, check_rows, i32, table
+from _odd_scale import odd_scale
 from _ops import bf16
 from oracle import long_context as O
 
@@ -17,10 +18,7 @@ class Batch:
         rng = np.random.default_rng(seed)
         self.c = Cache(rng, sum(-(-n // 64) for n in prefixes + own) + 1, fmt)
         if fmt == "fp8_tensor":   # a product of a code and this scale takes more than bf16's bits
-            self.c.scales = torch.tensor([0.0213])
-            self.c.exact = self.c.data.view(torch.float8_e4m3fn).double() * self.c.scales.double()
-            self.c.seen = self.c.exact.to(torch.float32).to(torch.bfloat16).double()
-            assert (self.c.seen != self.c.exact).double().mean() > 0.9
+            odd_scale(self.c)
         self.prefixes, self.offsets, self.own = prefixes, offsets, own
         self.pre, self.mine = [self.c.take(n) for n in prefixes], [self.c.take(n) for n in own]
         self.pages = sum(len(p) for p in self.mine)
