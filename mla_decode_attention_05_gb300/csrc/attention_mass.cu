@@ -96,6 +96,7 @@ struct Bars {
   uint64_t res_full[kBlocks], res_empty[kBlocks];        // full: rank 0, for both CTAs
   uint64_t slot_full[kMostSlots], slot_empty[kMostSlots];
   uint64_t raw_full[kMostSlots];  // FP8: a unit's codes are in place (of the resident ones, or of the slots)
+  uint64_t wide_full[kMostSlots]; // FP8, rank 1: a unit is widened
   uint64_t d_full[4], d_empty[4];                        // empty: rank 0
   alignas(16) float nl[2][kMostRows];  // -lse of a tile's query rows
   alignas(16) int lim[2][kMostRows];   // keys that a row sees; 0 for one that is no row, or has no weight to give
@@ -114,14 +115,6 @@ static_assert(OFF_RES + kBlocks * kBlock + 4 * kBlock <= kSmem, "shared memory m
 
 constexpr uint32_t kRoom = kSmem - OFF_RES;
 
-// Arrives on a barrier of the pair's other CTA behind this thread's own writes to
-// shared memory.  (Release at the scope of the CTA: what it publishes is read on this
-// SM, by its half of the pair's MMA.  At cluster scope the arrive waits for all the
-// thread's writes and costs a thousand cycles.)
-__device__ __forceinline__ void mbar_arrive_pair(uint32_t cluster_bar) {
-  asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
-}
-
 // Tile loads into this CTA whose bytes a barrier of either CTA of the pair counts.
 __device__ __forceinline__ void tma_load_4d_pair(uint32_t dst, const void *map, uint32_t cluster_bar, int c0, int c1, int c2,
                                                  int c3, uint64_t policy) {
@@ -137,21 +130,20 @@ __device__ __forceinline__ int seq_len(const MassParams &p, int b) {
   return min(max(__ldg(p.seqlens + b), 0), most);
 }
 
-// (Acquire at the scope of the CTA also for what the peer or its MMA arrives on: what
-// is read behind these waits lies in this SM's shared or tensor memory, and at cluster
-// scope every wait would cost some 500 cycles.)
-template <bool kPoll>
+// kCluster: acquire at the scope of the cluster, for what threads of the other CTA have written
+// (some 500 cycles more).  The other waits are for copies and MMAs, or for writes of this CTA.
+template <bool kPoll, bool kCluster = false>
 __device__ __forceinline__ bool wait_ok(Bars *b, uint64_t *bar, uint32_t parity, const MassParams &p) {
-  if (mbar_wait_limited<false, kPoll>(smem_u32(bar), parity, &b->abort, p.wait_ns)) return true;
+  if (mbar_wait_limited<kCluster, kPoll>(smem_u32(bar), parity, &b->abort, p.wait_ns)) return true;
   atomicOr(p.status, MLA_STATUS_WAIT_TIMEOUT);
   *(volatile int *)&b->abort = 1;
   return false;
 }
 
 // The same for a whole warp: its lanes go on, or give up, together.
-template <bool kPoll>
+template <bool kPoll, bool kCluster = false>
 __device__ __forceinline__ bool warp_wait(Bars *b, uint64_t *bar, uint32_t parity, const MassParams &p) {
-  return __all_sync(0xffffffffu, wait_ok<kPoll>(b, bar, parity, p));
+  return __all_sync(0xffffffffu, wait_ok<kPoll, kCluster>(b, bar, parity, p));
 }
 
 // The work is a line of units (key tile, query tile), query tiles innermost, of
@@ -425,7 +417,7 @@ __device__ void widen_role(const MassParams &p, Bars &br, const Work &w, const P
           return false;
         }
         __syncwarp();
-        if (first) mbar_arrive_pair(mapa(smem_u32(kStreamKeys ? &br.slot_full[k] : &br.res_full[k]), 0));
+        if (first) mbar_arrive(smem_u32(at.rank == 1 ? &br.wide_full[k] : kStreamKeys ? &br.slot_full[k] : &br.res_full[k]));
       }
       if (++s == p.slots) {
         s = 0;
@@ -438,6 +430,36 @@ __device__ void widen_role(const MassParams &p, Bars &br, const Work &w, const P
   for_each_phase<kStreamKeys, C::rows>(p, w, [&](const Phase &f) {
     for (int t = f.i0; t < (kStreamKeys ? f.i1 : min(f.i0 + 1, f.i1)); t++)
       if (!widen_tile()) return false;
+    return true;
+  });
+}
+
+// rank 1, two warps in turn that write nothing themselves: they pass on to rank 0 that units are widened.  What the
+// widening warps have written is ordered before them by a barrier of this CTA, and before rank 0's MMA, which reads
+// it, by their release at cluster scope, which takes some thousand cycles whatever there is to wait for.  (32 sequences
+// of up to 8192 tokens, two query tokens, 64 heads, one scale: 38.3 us, with one such warp 40.8, with the
+// release in the four widening warps 44.4; 33.2 with a release at the scope of the CTA, which orders
+// nothing for rank 0.  With a scale for each 128 values 41.4 and 37.3.)
+template <bool kStreamKeys, int kFormat, bool kPoll>
+__device__ void forward_role(const MassParams &p, Bars &br, const Work &w, int which) {
+  using C = Of<kFormat>;
+  const uint32_t full = mapa(smem_u32(kStreamKeys ? &br.slot_full[0] : &br.res_full[0]), 0);
+  const bool first = (threadIdx.x & 31) == 0;
+  int s = 0;
+  uint32_t ph = 0, tile = 0;
+  for_each_phase<kStreamKeys, C::rows>(p, w, [&](const Phase &f) {
+    for (int t = f.i0; t < (kStreamKeys ? f.i1 : min(f.i0 + 1, f.i1)); t++, tile++)
+      for (int u = 0; u < C::units; u++) {
+        const int k = kStreamKeys ? s : u;
+        if (k % 2 == which) {
+          if (!warp_wait<kPoll>(&br, &br.wide_full[k], kStreamKeys ? ph : tile & 1, p)) return false;
+          if (first) mbar_arrive_remote(full + k * 8);
+        }
+        if (++s == p.slots) {
+          s = 0;
+          ph ^= 1;
+        }
+      }
     return true;
   });
 }
@@ -462,8 +484,9 @@ __device__ void wait_role(const MassParams &p, Bars &br, const Work &w) {
           ok = warp_wait<kPoll>(&br, &br.d_empty[g % C::kd], ((g / C::kd) & 1) ^ 1, p);
           g++;
         }
-        if (ok && i == f.i0) ok = warp_wait<kPoll>(&br, &br.res_full[u], rph, p);
-        if (ok) ok = warp_wait<kPoll>(&br, &br.slot_full[s], ph, p);
+        // (keys widened by threads of both CTAs)
+        if (ok && i == f.i0) ok = warp_wait<kPoll, C::fp8 && !kStreamKeys>(&br, &br.res_full[u], rph, p);
+        if (ok) ok = warp_wait<kPoll, C::fp8 && kStreamKeys>(&br, &br.slot_full[s], ph, p);
         if (bar_red_or(kMmaBar, 64, !ok)) return false;
         if (++s == p.slots) {
           s = 0;
@@ -717,13 +740,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Of<kFormat>::threads
   at.slot = C::unit * at.slot_block;
   if (threadIdx.x == 0) {
     for (int i = 0; i < kBlocks; i++) {
-      mbar_init(smem_u32(&br.res_full[i]), C::fp8 && !kStreamKeys ? 2 * kGroupWarps : 1);
+      mbar_init(smem_u32(&br.res_full[i]), C::fp8 && !kStreamKeys ? kGroupWarps + 1 : 1);
       mbar_init(smem_u32(&br.res_empty[i]), 1);
     }
     for (int i = 0; i < kMostSlots; i++) {
-      mbar_init(smem_u32(&br.slot_full[i]), C::fp8 && kStreamKeys ? 2 * kGroupWarps : 1);
+      mbar_init(smem_u32(&br.slot_full[i]), C::fp8 && kStreamKeys ? kGroupWarps + 1 : 1);
       mbar_init(smem_u32(&br.slot_empty[i]), 1);
       mbar_init(smem_u32(&br.raw_full[i]), 1);
+      mbar_init(smem_u32(&br.wide_full[i]), kGroupWarps);
     }
     for (int i = 0; i < C::kd; i++) {
       mbar_init(smem_u32(&br.d_full[i]), 1);
@@ -752,6 +776,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Of<kFormat>::threads
     if (warp == 0 || warp == 3) load_role<kStreamKeys, kFormat, kPoll>(p, br, &k_map, &pe_map, &q_map, w, at, warp == 3);
     else if (at.rank == 0 && warp == 1) mma_role<kStreamKeys, kFormat>(p, br, w, at, tmem);
     else if (at.rank == 0 && warp == 2) wait_role<kStreamKeys, kFormat, kPoll>(p, br, w);
+    else if (C::fp8 && (warp == 1 || warp == 2)) forward_role<kStreamKeys, kFormat, kPoll>(p, br, w, warp - 1);
   } else if (warp < 4 + C::sum_warps) {
     if constexpr (C::scaled) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSumRegs));
     sum_role<kStreamKeys, kFormat, kPoll>(p, br, w, tmem, at.rank, pair_index);
