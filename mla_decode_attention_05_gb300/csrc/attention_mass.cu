@@ -78,14 +78,13 @@ constexpr int kLoadRegs = 72, kSumRegs = 120, kWideRegs = 80;
 constexpr uint32_t IDESC = idesc_bf16_f32(kTileKeys, 16, false, false) - (2u << 17);  // N is added
 
 struct MassParams {
-  const uint8_t *cache;
   const float *kv_scales;
   const int32_t *block_table, *seqlens;
   const float *lse;  // [B][H][T]
   float *mass;       // [B][cap]
   float *partial;    // [pairs][2][256]: sums of tiles that a pair has in part, its first and its last
   unsigned int *status;
-  int format, num_pages, max_pages, B, T, H, cap, causal;
+  int num_pages, max_pages, B, T, H, cap, causal;
   int rows, n_qt, box;  // query rows of a sequence, their tiles, the columns of a tile (half of each CTA)
   int slots;
   float scale, decay;
@@ -914,14 +913,12 @@ extern "C" int mla_attention_mass(const void *q, const void *kv_cache, int kv_fo
   int pairs = 0;
   if ((rc = sm_pairs(&pairs)) != MLA_OK) return rc;
   if (need && (size_t)pairs > kMostPairs) return fail(MLA_ERR_UNSUPPORTED, "more SMs than the workspace has room for");
-  p.cache = static_cast<const uint8_t *>(kv_cache);
   p.kv_scales = kv_scales;
   p.block_table = block_table;
   p.seqlens = cache_seqlens;
   p.lse = lse;
   p.mass = mass;
   p.partial = need ? static_cast<float *>(workspace) : nullptr;
-  p.format = kv_format;
   p.num_pages = num_pages;
   p.max_pages = max_pages;
   p.B = B;

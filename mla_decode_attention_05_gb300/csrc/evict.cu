@@ -39,7 +39,7 @@ struct EvictParams {
   int32_t *positions, *out_seqlens;
   int32_t *counts, *holes, *movers;  // workspace: [B], [B][room], [B][room]
   unsigned int *status;
-  int format, num_pages, max_pages, B, cap, keep, sinks, recent, room;
+  int format, num_pages, max_pages, cap, keep, sinks, recent, room;
 };
 
 struct SelectShared {
@@ -406,7 +406,6 @@ extern "C" int mla_evict(void *kv_cache, int kv_format, int num_pages, int page_
   p.format = kv_format;
   p.num_pages = num_pages;
   p.max_pages = max_pages;
-  p.B = B;
   p.cap = mass_cap;
   p.keep = keep;
   p.sinks = sinks;

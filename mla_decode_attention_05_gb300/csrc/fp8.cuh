@@ -1,4 +1,4 @@
-// Decoding of FP8 cache rows to bf16.
+// FP8 cache rows as bf16 values: codes exactly, and products of codes and scales as sums of two.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -6,29 +6,6 @@
 #include <stdint.h>
 
 namespace mla {
-
-// 16 e4m3 codes times a scale -> 16 bf16 values, each rounded once (every code is
-// exact in f16, and the product is made in fp32).
-__device__ __forceinline__ void widen16(const uint4 &codes, float scale, uint4 &lo, uint4 &hi) {
-  const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
-  uint32_t o[8];
-#pragma unroll
-  for (int i = 0; i < 8; i++) {
-    const uint16_t pair = (uint16_t)(w[i >> 1] >> (16 * (i & 1)));
-    uint32_t half2;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(half2) : "h"(pair));
-    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&half2));
-    float x, y;  // both products in one instruction
-    asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %4};\n\t"
-        "mul.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
-        : "=f"(x), "=f"(y)
-        : "f"(f.x), "f"(f.y), "f"(scale));
-    const __nv_bfloat162 v = __floats2bfloat162_rn(x, y);
-    o[i] = *reinterpret_cast<const uint32_t *>(&v);
-  }
-  lo = make_uint4(o[0], o[1], o[2], o[3]);
-  hi = make_uint4(o[4], o[5], o[6], o[7]);
-}
 
 // 16 e4m3 codes -> 16 bf16 values, exactly.
 __device__ __forceinline__ void codes16(const uint4 &codes, uint4 &lo, uint4 &hi) {

@@ -694,7 +694,6 @@ extern "C" int mla_decode_shared_bounded(const void *q, const void *kv_cache, in
   p.T = T;
   p.H = H;
   p.causal = causal;
-  p.room = l.room;
   p.own_room = l.own_room;
   p.n_mt = l.n_mt;
   p.parts = parts;

@@ -28,7 +28,6 @@ struct SharedParams {
   const int32_t *block_table, *seqlens;
   unsigned int *status;
   int format, num_pages, max_prefix, max_pages, G, B, T, H, causal;
-  int room;       // room for items
   int own_room;   // FP8: room for widened own pages
   int n_mt;       // own tiles of query rows of a sequence
   int parts;
