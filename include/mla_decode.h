@@ -578,7 +578,8 @@ int mla_attention_mass(const void *q, const void *kv_cache, int kv_format, int n
  * it.  The stayers behind, in order of their slots, move into the slots below
  * keep that have become free, in order: row, scales, mass and position.  The
  * slots from keep to n - 1 then hold mass 0 and position -1, so a token
- * appended there starts from nothing.  (The order of slots has no meaning to
+ * appended there starts from nothing, and its position is written by whoever appends it
+ * (-1 is below sinks, even where that is 0: a token without one would stay for ever).  (The order of slots has no meaning to
  * attention without `causal`, and with it none but for the last T, which are
  * appended afterwards.)  Sequences of at most keep tokens are left as they are.
  *
