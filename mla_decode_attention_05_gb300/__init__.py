@@ -870,8 +870,9 @@ def evict(kv_cache: torch.Tensor, block_table: torch.Tensor, cache_seqlens: torc
     move into the slots below that have become free; the slots from `keep` on
     then hold mass 0 and position -1: whoever appends a token there writes its
     position (-1 is below `sinks`, even where that is 0, so a token without one
-    would stay for ever).  mass fp32 and positions int32 [B, capacity]; kv_cache, block_table and kv_scales as in decode(); no page of
-    two sequences.  out_seqlens: where the lengths go (default: a new tensor;
+    would stay for ever).  mass fp32 and positions int32 [B, capacity];
+    kv_cache, block_table and kv_scales as in decode(); no page of two
+    sequences.  out_seqlens: where the lengths go (default: a new tensor;
     cache_seqlens itself will do).  workspace: at least evict_workspace_bytes()
     bytes (allocated here when not given)."""
     if _fast is not None:

@@ -14,7 +14,7 @@
 //
 // 64 sequences of up to 32768 tokens, 128 heads: 184 us, bound by HBM (6.6 TB/s of 6.7).
 // The last 64 tokens of 12001, 128 heads: 67 us for 113 GFLOP, bound by the tensor cores (82 % of the
-// cycles).  32 FP8 sequences of up to 8192 tokens, 2 x 64 rows: 38 us for 95 MB, bound by the
+// cycles).  32 FP8 sequences of up to 8192 tokens, 2 x 64 rows: 41 us for 95 MB (one scale: 36 for 84), bound by the
 // hand-overs between loads, widening, products and sums.
 #include <atomic>
 #include <cmath>
@@ -129,8 +129,8 @@ __device__ __forceinline__ int seq_len(const MassParams &p, int b) {
   return min(max(__ldg(p.seqlens + b), 0), most);
 }
 
-// kCluster: acquire at the scope of the cluster, for what threads of the other CTA have written
-// (some 500 cycles more).  The other waits are for copies and MMAs, or for writes of this CTA.
+// kCluster: acquire at the scope of the cluster, for what threads of the other CTA have written.
+// The other waits are for copies and MMAs, or for writes of this CTA.
 template <bool kPoll, bool kCluster = false>
 __device__ __forceinline__ bool wait_ok(Bars *b, uint64_t *bar, uint32_t parity, const MassParams &p) {
   if (mbar_wait_limited<kCluster, kPoll>(smem_u32(bar), parity, &b->abort, p.wait_ns)) return true;
@@ -438,7 +438,7 @@ __device__ void widen_role(const MassParams &p, Bars &br, const Work &w, const P
 // it, by their release at cluster scope, which takes some thousand cycles whatever there is to wait for.  (32 sequences
 // of up to 8192 tokens, two query tokens, 64 heads, one scale: 38.3 us, with one such warp 40.8, with the
 // release in the four widening warps 44.4; 33.2 with a release at the scope of the CTA, which orders
-// nothing for rank 0.  With a scale for each 128 values 41.4 and 37.3.)
+// nothing for rank 0.  With a scale for each 128 values 41.4 and 37.3; both with the copy of the sums, 1.5.)
 template <bool kStreamKeys, int kFormat, bool kPoll>
 __device__ void forward_role(const MassParams &p, Bars &br, const Work &w, int which) {
   using C = Of<kFormat>;

@@ -13,7 +13,7 @@
 // other through a small ring in L2.  All results are fp32 partials, normalised,
 // with a base-2 log-sum-exp: another kernel joins prefix and own parts.
 //
-// 64 sequences of 128 heads on 16384 shared tokens: 221 us in all for 301 GFLOP (154 us at the
+// 64 sequences of 128 heads on 16384 shared tokens: 220 us in all for 301 GFLOP (154 us at the
 // measured bf16 rate, which would keep both SMs' tensor cores busy).  A tile takes 0.78 us, bound by rank 0's MMAs
 // (36 of 38 cycles, 0.7 us); the start and the end of an item of 128 rows take 5.8 us.
 //
@@ -21,8 +21,8 @@
 // scale the codes themselves (exact; the scale multiplies scores and results).  With a scale
 // for each 128 values a product of code and scale does not fit 8 bits, and a log-sum-exp over few
 // keys shows it: keys are sums of two bf16 values (16 bits), so rank 0 makes twice the products
-// of a latent, from a second stage a tile.  (One: 117 us instead of 155 for 48 sequences of four
-// tokens and 64 heads on three prefixes of up to 5000, and log-sum-exps off by 1e-4 of
+// of a latent, from a second stage a tile: 117 us of 146 for 48 sequences of four tokens and 64 heads on three
+// prefixes of up to 5000, where codes with one scale take 80 of 104.  (One bf16 value: log-sum-exps off by 1e-4 of
 // themselves instead of 1e-6.)  Values are the first of the two: P is bf16 too, and its
 // rounding of the same size.
 //

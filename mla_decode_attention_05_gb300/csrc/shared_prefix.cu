@@ -737,8 +737,8 @@ extern "C" int mla_decode_shared_bounded(const void *q, const void *kv_cache, in
   cudaError_t e = small ? launch_dependent(shared_schedule_kernel<kFewThreads>, blocks_s, kFewThreads, 0, s, p)
                         : launch_dependent(shared_schedule_kernel<1024>, blocks_s, 1024, 0, s, p);
   if (e == cudaSuccess && wide) {
-    // as many blocks as an SM holds (44 registers a thread), or as there can be parts of pages
-    const long long most = (long long)l.pages * kWidenParts, held = 2ll * parts * 5;
+    // as many blocks as the SMs hold (six each, of 40 registers a thread), or as there can be parts of pages
+    const long long most = (long long)l.pages * kWidenParts, held = 2ll * parts * 6;
     cfg.gridDim = dim3((unsigned)(most < held ? most : held));
     e = cudaLaunchKernelEx(&cfg, kv_format == MLA_KV_FP8_E4M3 ? shared_widen_kernel<true> : shared_widen_kernel<false>, p);
   }
