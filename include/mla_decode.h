@@ -496,9 +496,10 @@ int mla_value_project(const void *attn, int64_t ld_token, int64_t ld_head, const
  * MLA_STATUS_BAD_PAGE.  Of an FP8 cache, prefix pages are widened in the workspace
  * (73728 bytes an entry of prefix_table, with a scale for each 128 values 139264),
  * and own pages too where there is room; where there is none, own FP8 rows are
- * rounded to bf16, as mla_decode does.  There is room for B * max_pages <= 2048; of
- * more, with one scale, for the first 2048 pages in use (of cache_seqlens, whatever
- * max_pages is), and with a scale for each 128 values for none:
+ * rounded to bf16, as mla_decode does.  There is room where B * max_pages <= 2048.
+ * Where it is more there is, with one scale, for 2048 pages (the sum of
+ * ceil(cache_seqlens[b] / 64), whatever max_pages is; none of the own rows is rounded,
+ * or all are), and with a scale for each 128 values for none:
  * mla_decode_shared_bounded makes it.  At most 8192 work items: B * ceil(T * H / 128) +
  * ceil(B * T * H / 128) + G, and 2^30 tiles of 64 keys in the tables' width
  * (MLA_ERR_UNSUPPORTED above).  A wait that gives up sets
@@ -518,7 +519,7 @@ int mla_decode_shared(const void *q, const void *kv_cache, int kv_format, int nu
  * mla_decode_shared with room in the workspace for own_pages widened own pages, so
  * that what becomes of own FP8 rows goes by the tokens there are and not by the
  * page table's width: as long as all sequences' own tokens together are in at most
- * own_pages pages (the sum of ceil(cache_seqlens[b] / 64)), no row is rounded, and
+ * own_pages pages (the sum of ceil(cache_seqlens[b] / 64)), own rows are as exact as prefixes are, and
  * results are the same, bit by bit, for any max_pages and any such own_pages.
  * Where they are in more, own rows are rounded to bf16.  own_pages >= 0, of
  * which at most B * max_pages are used (73728 bytes each, with a scale for each 128
